@@ -29,6 +29,8 @@ KDA_FLAG_SAVE_FOR_BWD = 8
 KDA_FLAG_BWD_REUSE_FWD = 16
 KDA_FLAG_BWD_UMMA = 32
 KDA_FLAG_FWD_TOKEN_EXACT = 64
+KDA_FLAG_FP16 = 128
+KDA_FLAG_CAUSAL = 256
 
 KDA_DEBUG_WAIT_LIMIT = 1
 KDA_DEBUG_DROP_SCAN_LOAD = 2
@@ -37,6 +39,7 @@ _STATUS = {
     0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error",
     4: "invalid cu_seqlens", 5: "device wait timed out", 6: "too large for the no-alloc scratch",
     7: "state slot index or accepted-token count out of range",
+    8: "page, slot or length out of range, or too few free pages",
 }
 
 RECURRENT_WORKSPACE_BYTES = 256
@@ -83,6 +86,21 @@ def load_library(path: Optional[str] = None):
                             i, i, i, i, i, i, u, vp, sz, vp]
     lib.kda_bwd_timed.restype = ctypes.c_int
     lib.kda_bwd_timed.argtypes = lib.kda_bwd.argtypes + [vp]
+    ll = ctypes.c_longlong
+    lib.kda_latent_fwd.restype = ctypes.c_int
+    lib.kda_latent_fwd.argtypes = [vp, vp, vp, ll, f, vp, vp, vp, vp, i, i, i, i, i, u, vp, vp]
+    lib.kda_latent_bwd_workspace_bytes.restype = sz
+    lib.kda_latent_bwd_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.kda_latent_bwd.restype = ctypes.c_int
+    lib.kda_latent_bwd.argtypes = [vp, vp, vp, ll, vp, vp, vp, f, vp, vp, vp, vp, vp, i, i, i, i, i, u, vp, sz, vp]
+    lib.kda_latent_decode_workspace_bytes.restype = sz
+    lib.kda_latent_decode_workspace_bytes.argtypes = [i, i, i]
+    lib.kda_latent_decode.restype = ctypes.c_int
+    lib.kda_latent_decode.argtypes = [vp, vp, i, i, vp, i, vp, f, vp, vp, i, i, i, u, vp, sz, vp]
+    lib.kda_latent_append.restype = ctypes.c_int
+    lib.kda_latent_append.argtypes = [vp, ll, vp, vp, f, vp, ll, i, u, vp, vp]
+    lib.kda_block_tables.restype = ctypes.c_int
+    lib.kda_block_tables.argtypes = [vp, vp, vp, i, vp, i, vp, i, vp, i, vp, vp, vp, i, vp, vp]
     lib.kda_debug_set.restype = ctypes.c_int
     lib.kda_debug_set.argtypes = [i, u]
     lib.kda_status_str.restype = ctypes.c_char_p

@@ -1,0 +1,111 @@
+// Shared definitions of the latent-attention kernels: sizes, parameters, the
+// map from 128-row tile slots to sequences, and the 16-bit float types.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+constexpr int LAT_C = 512;                  // latent channels of a cached row
+constexpr int LAT_P = 64;                   // positional channels, shared by the heads
+constexpr int LAT_ROW = LAT_C + LAT_P;      // a cached row, an absorbed query
+constexpr int LAT_N = 128;                  // per-head key channels (expanded)
+constexpr int LAT_V = 128;                  // value channels (expanded)
+constexpr int LAT_QK = LAT_N + LAT_P;       // expanded query
+constexpr int LAT_KV = LAT_N + LAT_V;       // expanded key and value of one token and head
+constexpr int LAT_TILE = 128;               // rows of a query or key tile
+
+struct LatentParams {
+    const void* q;          // [B*Tq, H, 192]
+    const void* kv;         // [B*Tk, H, 256]
+    const void* k_pe;       // [B*Tk, 64], k_pe_stride elements apart
+    long long k_pe_stride;
+    const void* o;          // backward: [B*Tq, H, 128]
+    const float* lse;       // backward: [B*Tq, H]
+    const void* dout;       // backward: [B*Tq, H, 128]
+    void* o_out;            // forward
+    float* lse_out;         // forward, or null
+    void* dq;
+    void* dkv;
+    void* dk_pe;
+    float* delta;           // backward workspace: [B*Tq, H] dout . o
+    float* dpe_part;        // backward workspace: [H][B*Tk][64] per-head gradients of k_pe
+    const int32_t* cu_q;    // int32 [N+1] or null
+    const int32_t* cu_k;
+    uint32_t* status;       // or null
+    float scale;
+    int Tq, Tk;             // per sequence (fixed) or packed (varlen)
+    int H, N;
+    int causal;
+    uint32_t wait_limit;
+};
+
+// A sequence's queries [q0, q0 + lq) and keys [k0, k0 + lk) as packed rows.
+struct LatentSeq {
+    long long q0, k0;
+    int lq, lk;
+};
+
+__device__ __forceinline__ void set_status(uint32_t* status, uint32_t bit) {
+    if (status != nullptr) atomicOr(status, bit);
+}
+
+// False (and the status word flagged) where the offsets are not a valid
+// non-decreasing list into [0, T].
+__device__ __forceinline__ bool latent_seq(const LatentParams& p, int n, LatentSeq& s) {
+    if (p.cu_q == nullptr) {
+        s.q0 = (long long)n * p.Tq;
+        s.k0 = (long long)n * p.Tk;
+        s.lq = p.Tq;
+        s.lk = p.Tk;
+        return true;
+    }
+    const int a = p.cu_q[n], b = p.cu_q[n + 1], c = p.cu_k[n], d = p.cu_k[n + 1];
+    if (a < 0 || b < a || b > p.Tq || (n == 0 && a != 0) || (n == p.N - 1 && b != p.Tq) || c < 0 || d < c ||
+        d > p.Tk || (n == 0 && c != 0) || (n == p.N - 1 && d != p.Tk)) {
+        set_status(p.status, STATUS_BAD_CU);
+        return false;
+    }
+    s.q0 = a;
+    s.k0 = c;
+    s.lq = b - a;
+    s.lk = d - c;
+    return true;
+}
+
+// Tile slots over packed rows with offsets cu (null: N sequences of T rows):
+// slot floor(cu[n] / 128) + n + j holds tile j of sequence n, so
+// floor(T / 128) + N slots hold every tile and some hold none.
+__host__ __device__ __forceinline__ int latent_slots(bool varlen, int T, int N) {
+    return varlen ? T / LAT_TILE + N : N * ((T + LAT_TILE - 1) / LAT_TILE);
+}
+
+__device__ __forceinline__ void latent_slot(const int32_t* cu, int T, int N, int slot, int& n, int& j) {
+    if (cu == nullptr) {
+        const int per = (T + LAT_TILE - 1) / LAT_TILE;
+        n = slot / per;
+        j = slot % per;
+        return;
+    }
+    int lo = 0, hi = N - 1;   // the last n with floor(cu[n] / 128) + n <= slot
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] / LAT_TILE + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    n = lo;
+    j = slot - (cu[lo] / LAT_TILE + lo);
+}
+
+// ---- 16-bit floats ----
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+
+}  // namespace kda

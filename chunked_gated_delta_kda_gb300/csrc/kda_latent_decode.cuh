@@ -1,0 +1,23 @@
+// Parameters of the absorbed (decode) form.
+#pragma once
+
+#include "kda_latent.cuh"
+
+namespace kda {
+
+struct DecodeParams {
+    const void* q;              // [N, S, H, 576]
+    const void* cache;          // [num_pages * page_size, 576]
+    const int32_t* table;       // [N, table_width]
+    const int32_t* lens;        // [N]
+    void* o;                    // [N, S, H, 512]
+    float* lse;                 // [N, S, H] or null
+    uint8_t* workspace;
+    uint32_t* status;
+    float scale;
+    int num_pages, page_size, table_width;
+    int N, S, H;
+    uint32_t wait_limit;
+};
+
+}  // namespace kda

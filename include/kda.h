@@ -48,8 +48,11 @@ typedef enum {
     KDA_ERR_TIMEOUT = 5,         /* a bounded device wait ran out (via kda_get_status) */
     KDA_ERR_TOO_LARGE = 6,       /* kda_fwd_noalloc: the problem needs more workspace than
                                     the library's static scratch holds */
-    KDA_ERR_BAD_STATE_INDEX = 7  /* kda_fused_recurrent: device found a state slot index or an
+    KDA_ERR_BAD_STATE_INDEX = 7, /* kda_fused_recurrent: device found a state slot index or an
                                     accepted-token count out of range (via kda_get_status) */
+    KDA_ERR_BAD_PAGE = 8         /* kda_latent_decode, kda_latent_append, kda_block_tables: device found
+                                    a page, slot or length out of range, or too few free pages (via
+                                    kda_get_status) */
 } kda_status;
 
 /* Apply the per-token L2 normalisation x / sqrt(sum(x^2) + 1e-6) to q and k
@@ -163,9 +166,10 @@ kda_status kda_fwd_timed(const void* q, const void* k, const void* v, const floa
 
 /*
  * Synchronise `stream`, then read the device status word that the last
- * kda_fwd, kda_bwd or kda_fused_recurrent on this workspace wrote.  Returns KDA_OK,
- * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_TIMEOUT, KDA_ERR_BAD_STATE_INDEX (in that
- * order of precedence), or KDA_ERR_CUDA if synchronising or reading failed.
+ * kda_fwd, kda_bwd, kda_fused_recurrent, kda_latent_* or kda_block_tables on
+ * this workspace wrote.  Returns KDA_OK, KDA_ERR_BAD_CU_SEQLENS,
+ * KDA_ERR_TIMEOUT, KDA_ERR_BAD_STATE_INDEX, KDA_ERR_BAD_PAGE (in that order of
+ * precedence), or KDA_ERR_CUDA if synchronising or reading failed.
  */
 kda_status kda_get_status(const void* workspace, cudaStream_t stream);
 
@@ -372,6 +376,162 @@ kda_status kda_bwd_timed(const void* q, const void* k, const void* v, const floa
                          float* dk, float* dv, float* dg, float* dbeta, float* dh0, int B, int T, int H, int K, int V,
                          int N, unsigned flags, void* workspace, size_t workspace_bytes, cudaStream_t stream,
                          cudaEvent_t* stage_events);
+
+/* ------------------------------------------------------------------------
+ * Latent attention and its paged cache: softmax attention whose keys and
+ * values come from one shared row a token, 512 latent channels c and 64
+ * positional channels p (whatever position encoding the model applies is
+ * already in them).  No counterpart on the method's pages: the full-attention
+ * layers that stand between KDA layers in a hybrid decoder need it.
+ *
+ * Head sizes are fixed: queries and keys have 128 + 64 channels in the
+ * expanded form (128 made from c for each head, 64 the shared p) and 512 + 64
+ * in the absorbed form (the head's key projection multiplied into the
+ * query); values have 128, and 512.  Tensors are bf16, or all fp16 with
+ * KDA_FLAG_FP16.  scale <= 0 or NaN means 192^-0.5, the expanded head size's,
+ * in both forms (absorbing does not change the scores).
+ *
+ * For the entry points below `workspace` may be NULL where no
+ * *_workspace_bytes function is given: device-detected faults are then
+ * handled as described but not recorded.
+ * ------------------------------------------------------------------------ */
+
+/* kda_latent_*, tensors of 16-bit floats are fp16 instead of bf16. */
+#define KDA_FLAG_FP16 128u
+
+/* kda_latent_fwd and kda_latent_bwd: query i of a sequence of Lq queries and
+ * Lk keys sees the keys j <= i + Lk - Lq (the last query sees all of them). */
+#define KDA_FLAG_CAUSAL 256u
+
+/*
+ * Expanded form, forward.  Per sequence and head, over the keys j that query
+ * i sees, x_ij = scale (q_i . [k_j | p_j]), lse_i = log sum_j exp(x_ij),
+ * o_i = sum_j exp(x_ij - lse_i) v_j.  A query that sees no key (Lq > Lk with
+ * KDA_FLAG_CAUSAL, or Lk = 0) gets o = 0 and lse = -infinity.
+ *
+ *   q           [B, Tq, H, 192]  queries, the 64 positional channels last
+ *   kv          [B, Tk, H, 256]  expanded keys (128 channels, without the
+ *               positional ones) and values (128), as one up-projection of c
+ *               gives them
+ *   k_pe        [B, Tk, 64] with `k_pe_stride` elements from token to token
+ *               (a multiple of 8, at least 64: p may be read in place from
+ *               the rows of the latent projection)
+ *   cu_seqlens_q, cu_seqlens_k  int32 [N+1] device offsets of N packed
+ *               sequences (varlen: B == 1), or both NULL (N == B sequences of
+ *               Tq queries and Tk keys).  Never read by the host.
+ *   o           [B, Tq, H, 128]
+ *   lse         fp32 [B, Tq, H], natural logarithm, or NULL to skip it
+ *   flags       KDA_FLAG_FP16, KDA_FLAG_CAUSAL
+ *   workspace   NULL, or the 256-byte status header (256-byte aligned)
+ *
+ * Precision: products on the tensor cores with 32-bit sums; the softmax's
+ * running maximum, sum and exponentials in 32 bits; the exponentials are
+ * rounded to the tensors' type as the second product's operand.
+ * Rows of other sequences never reach a result, whatever they hold.  Inside
+ * a sequence the product of a masked (zero) weight with an infinite or NaN
+ * value is not suppressed.
+ */
+kda_status kda_latent_fwd(const void* q, const void* kv, const void* k_pe, long long k_pe_stride, float scale,
+                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, void* o, float* lse, int B,
+                          int Tq, int Tk, int H, int N, unsigned flags, void* workspace, cudaStream_t stream);
+
+/* Bytes of device workspace kda_latent_bwd needs (0 on invalid sizes). */
+size_t kda_latent_bwd_workspace_bytes(int B, int Tq, int Tk, int H, int N);
+
+/*
+ * Expanded form, backward: the gradients of L = sum <dout, o>.  With
+ * p = exp(x - lse), D_i = dout_i . o_i:  dv_j = sum_i p_ij dout_i,
+ * dx_ij = scale p_ij (dout_i . v_j - D_i), dq_i = sum_j dx_ij [k_j | p_j],
+ * dk_j = sum_i dx_ij q_i; the shared positional key's gradient is the sum
+ * over the heads.  Arguments as for kda_latent_fwd; o and lse are its
+ * results, dout has o's shape.
+ *   dq          [B, Tq, H, 192]
+ *   dkv         [B, Tk, H, 256]
+ *   dk_pe       [B, Tk, 64], contiguous
+ *   workspace   kda_latent_bwd_workspace_bytes(...) bytes, 256-byte aligned,
+ *               contents need not be initialised
+ * Every gradient row is written (zero where nothing reaches it).  Sums are
+ * in 32 bits and in a fixed order: equal inputs give equal bits.
+ */
+kda_status kda_latent_bwd(const void* q, const void* kv, const void* k_pe, long long k_pe_stride, const void* o,
+                          const float* lse, const void* dout, float scale, const int32_t* cu_seqlens_q,
+                          const int32_t* cu_seqlens_k, void* dq, void* dkv, void* dk_pe, int B, int Tq, int Tk,
+                          int H, int N, unsigned flags, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* Bytes of device workspace kda_latent_decode needs (0 on invalid sizes). */
+size_t kda_latent_decode_workspace_bytes(int N, int S, int H);
+
+/*
+ * Absorbed form over the paged cache, for S tokens a sequence (1 in plain
+ * decoding, more to verify drafted ones).  Token s of sequence n sees the
+ * first seq_lens[n] - S + 1 + s cached rows r: x = scale (q . r), and
+ * o = softmax(x) r[0:512].  A token that sees no row gets o = 0 and
+ * lse = -infinity.
+ *   q           [N, S, H, 576]
+ *   cache       [num_pages, page_size, 576]; rows that no token sees are not
+ *               used, whatever they hold
+ *   page_size   16, 32, or a multiple of 64
+ *   block_table int32 [N, table_width], device: the pages of each sequence in
+ *               order; entries past its last page are not read
+ *   seq_lens    int32 [N], device: cached rows of each sequence, its S own
+ *               tokens included.  Never read by the host.
+ *   o           [N, S, H, 512];   lse  fp32 [N, S, H] or NULL
+ *   flags       KDA_FLAG_FP16
+ *   workspace   kda_latent_decode_workspace_bytes(...) bytes, 256-byte
+ *               aligned, contents need not be initialised
+ * A negative length, or one past table_width pages, is clipped to that range,
+ * and rows on a page outside [0, num_pages) count as masked; both set
+ * KDA_ERR_BAD_PAGE in the status word.
+ */
+kda_status kda_latent_decode(const void* q, const void* cache, int num_pages, int page_size,
+                             const int32_t* block_table, int table_width, const int32_t* seq_lens, float scale,
+                             void* o, float* lse, int N, int S, int H, unsigned flags, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Write new tokens' rows into the paged cache.
+ *   rows        [T, 576] with `row_stride` elements from row to row (a
+ *               multiple of 8)
+ *   slots       int64 [T], device: row t goes to cache row slots[t]; a
+ *               negative slot is a padding entry and is skipped.  Slots are
+ *               distinct.  A slot >= num_slots is skipped and sets
+ *               KDA_ERR_BAD_PAGE.
+ *   norm_weight [512] or NULL.  With it the latent channels are written as
+ *               c / sqrt(mean(c^2) + eps) * norm_weight, computed in fp32 and
+ *               rounded once; without it rows are copied.
+ *   cache       [num_slots, 576]
+ *   workspace   NULL, or the 256-byte status header
+ */
+kda_status kda_latent_append(const void* rows, long long row_stride, const int64_t* slots, const void* norm_weight,
+                             float eps, void* cache, long long num_slots, int T, unsigned flags, void* workspace,
+                             cudaStream_t stream);
+
+/*
+ * Block tables and slot map of one step, on the device: sequence n holds
+ * seq_lens[n] cached rows on its pages and gets new_lens[n] more.  The pages
+ * it lacks are taken from the free list in the order of the sequences.
+ *   seq_lens, new_lens  int32 [N]
+ *   block_table int32 [N, table_width]: cells of pages already held are read,
+ *               cells of pages taken now are written, others left alone
+ *   free_pages  int32 [num_free];  free_head  int32 [1]: the next entry to take
+ *   slot_mapping  int64 [num_tokens]: slot (page * page_size + row) of every
+ *               new token, sequence after sequence; -1 past the last one
+ *   cu_seqlens  int32 [N+1]: where each sequence's new tokens start
+ *   seq_lens_out  int32 [N]: seq_lens + new_lens
+ *   free_head_out int32 [1]: free_head + the pages taken (at most num_free)
+ *   page_size   a power of two
+ * Nothing but block_table, and the four outputs, is written; the inputs may
+ * not overlap them.  A token without a page (free list too short, table too
+ * narrow, negative page in a held cell) gets slot -1, a cell without one -1;
+ * a negative length counts as 0, tokens past num_tokens are not mapped; each
+ * sets KDA_ERR_BAD_PAGE.
+ *   workspace   NULL, or the 256-byte status header
+ */
+kda_status kda_block_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table, int table_width,
+                            const int32_t* free_pages, int num_free, const int32_t* free_head, int page_size,
+                            int64_t* slot_mapping, int num_tokens, int32_t* cu_seqlens, int32_t* seq_lens_out,
+                            int32_t* free_head_out, int N, void* workspace, cudaStream_t stream);
 
 /* Static English description of a status code. */
 const char* kda_status_str(kda_status status);
