@@ -77,28 +77,28 @@ __device__ __forceinline__ bool latent_seq(const LatentParams& p, int n, LatentS
     return true;
 }
 
-// Tile slots over packed rows with offsets cu (null: N sequences of T rows):
-// slot floor(cu[n] / 128) + n + j holds tile j of sequence n, so
-// floor(T / 128) + N slots hold every tile and some hold none.
-__host__ __device__ __forceinline__ int latent_slots(bool varlen, int T, int N) {
-    return varlen ? T / LAT_TILE + N : N * ((T + LAT_TILE - 1) / LAT_TILE);
+// Tile slots over packed rows with offsets cu (null: N sequences of T rows),
+// `tile` rows each: slot floor(cu[n] / tile) + n + j holds tile j of sequence
+// n, so floor(T / tile) + N slots hold every tile and some hold none.
+__host__ __device__ __forceinline__ int latent_slots(bool varlen, int T, int N, int tile) {
+    return varlen ? T / tile + N : N * ((T + tile - 1) / tile);
 }
 
-__device__ __forceinline__ void latent_slot(const int32_t* cu, int T, int N, int slot, int& n, int& j) {
+__device__ __forceinline__ void latent_slot(const int32_t* cu, int T, int N, int slot, int tile, int& n, int& j) {
     if (cu == nullptr) {
-        const int per = (T + LAT_TILE - 1) / LAT_TILE;
+        const int per = (T + tile - 1) / tile;
         n = slot / per;
         j = slot % per;
         return;
     }
-    int lo = 0, hi = N - 1;   // the last n with floor(cu[n] / 128) + n <= slot
+    int lo = 0, hi = N - 1;   // the last n with floor(cu[n] / tile) + n <= slot
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] / LAT_TILE + mid <= slot) lo = mid;
+        if (cu[mid] / tile + mid <= slot) lo = mid;
         else hi = mid - 1;
     }
     n = lo;
-    j = slot - (cu[lo] / LAT_TILE + lo);
+    j = slot - (cu[lo] / tile + lo);
 }
 
 // ---- 16-bit floats ----

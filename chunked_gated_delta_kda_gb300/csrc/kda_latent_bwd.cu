@@ -11,7 +11,7 @@ template <typename T>
 __global__ void latent_dq_kernel(LatentParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n, j;
-    latent_slot(p.cu_q, p.Tq, p.N, blockIdx.x, n, j);
+    latent_slot(p.cu_q, p.Tq, p.N, blockIdx.x, LAT_TILE, n, j);
     LatentSeq s;
     if (!latent_seq(p, n, s)) return;
     const int h = blockIdx.y;
@@ -53,7 +53,7 @@ template <typename T>
 __global__ void latent_dkv_kernel(LatentParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n, j;
-    latent_slot(p.cu_k, p.Tk, p.N, blockIdx.x, n, j);
+    latent_slot(p.cu_k, p.Tk, p.N, blockIdx.x, LAT_TILE, n, j);
     LatentSeq s;
     if (!latent_seq(p, n, s)) return;
     const int h = blockIdx.y;
@@ -109,9 +109,9 @@ template <typename T>
 cudaError_t launch(const LatentParams& p, cudaStream_t stream) {
     const bool varlen = p.cu_q != nullptr;
     const long long rows = varlen ? p.Tk : (long long)p.N * p.Tk;
-    if (const int slots = latent_slots(varlen, p.Tq, p.N))
+    if (const int slots = latent_slots(varlen, p.Tq, p.N, LAT_TILE))
         latent_dq_kernel<T><<<dim3(slots, p.H), 256, 0, stream>>>(p);
-    if (const int slots = latent_slots(varlen, p.Tk, p.N))
+    if (const int slots = latent_slots(varlen, p.Tk, p.N, LAT_TILE))
         latent_dkv_kernel<T><<<dim3(slots, p.H), 256, 0, stream>>>(p);
     if (rows) latent_dpe_kernel<T><<<(unsigned)((rows * LAT_P + 255) / 256), 256, 0, stream>>>(p, rows);
     return cudaGetLastError();

@@ -1,54 +1,354 @@
-// Expanded latent attention, forward: one warp per (query, head), the keys in
-// order, with the running maximum and sum of the softmax.
-#include "kda_latent.cuh"
+// Expanded latent attention, forward.
+//
+// One pass over the keys with the softmax's running maximum m and sum l:
+//   S = Q K^T (tcgen05, 192 channels: 128 of the head, 64 shared), P = exp2(c S - c m), O = O + P V,
+// with c = scale log2(e).  m is a reference, not the exact maximum: it follows
+// the row maximum only when that has grown by more than 2^8 in P's terms, so
+// that O is rarely rescaled; P stays below 2^8 and the result is the same in
+// exact arithmetic.
+//
+// A CTA owns 256 queries of one head as two tiles of 128 rows, so that one
+// tile's softmax runs while the tensor cores work on the other:
+//   warps 0-3, 4-7  softmax of tile 0 / 1, one thread a row, and its output
+//   warp 8          issues the products
+//   warp 9          loads: Q once, then K and V tiles of 128 keys through a
+//                   ring of eight 16 KiB slabs (64 columns x 128 rows, as
+//                   the tensor map's 128-byte swizzle stores them)
+// Tensor memory: S (128 columns) and O (128) of both tiles; P, as 16-bit
+// operand of the second product, takes the first half of its S columns.  The
+// products of one tile are issued in the order P V (j), Q K^T (j + 1); the
+// tensor pipe keeps that order, so S may overwrite P, and a full S means that
+// the P V before it is done.
+#include "kda_latent_mma.cuh"
+
+#include <cudaTypedefs.h>
 
 namespace kda {
 
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder();
+
+bool latent_row_map(CUtensorMap* m, const void* base, int width, int heads, long long tokens, long long row_stride,
+                    int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2u, (cuuint64_t)row_stride * 2u};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
-template <typename T>
-__global__ void latent_fwd_kernel(LatentParams p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int n, j;
-    latent_slot(p.cu_q, p.Tq, p.N, blockIdx.x, n, j);
+constexpr int FWD_ROWS = 2 * LAT_TILE;
+constexpr int FWD_THREADS = 384;                        // warps 10 and 11 only hold registers for the softmax
+constexpr uint32_t SLAB = 64 * LAT_TILE * 2;            // 16 KiB
+constexpr uint32_t RING = 8;
+constexpr uint32_t F_Q = 0;                             // [tile][3 slabs]
+constexpr uint32_t F_RING = 6 * SLAB;
+constexpr uint32_t F_BAR = F_RING + RING * SLAB;
+constexpr uint32_t F_FULL = F_BAR;                      // [RING]
+constexpr uint32_t F_EMPTY = F_FULL + 8 * RING;         // [RING]
+constexpr uint32_t F_QFULL = F_EMPTY + 8 * RING;        // [2]
+constexpr uint32_t F_SFULL = F_QFULL + 16;              // [2]
+constexpr uint32_t F_PFULL = F_SFULL + 16;              // [2]
+constexpr uint32_t F_ODONE = F_PFULL + 16;              // [2]
+constexpr uint32_t F_DRAIN = F_ODONE + 16;
+constexpr uint32_t F_TMEM = F_DRAIN + 8;
+constexpr uint32_t F_FAILED = F_TMEM + 4;
+constexpr uint32_t F_BYTES = F_FAILED + 4;
+constexpr uint32_t F_SMEM = F_BYTES + 1024;             // room to align the base
+static_assert(F_SMEM <= 232448, "shared memory of one CTA");
+
+constexpr float RESCALE_LOG2 = 8.f;
+
+struct FwdMaps {
+    CUtensorMap q, kv, pe;
+};
+
+template <bool FP16>
+__global__ void __launch_bounds__(FWD_THREADS, 1)
+    latent_fwd_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ FwdMaps maps, int slots) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    volatile uint32_t* failed = reinterpret_cast<volatile uint32_t*>(smem + F_FAILED);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
+
+    // the last rows of a sequence see the most keys: largest work first
+    int n, j0;
     LatentSeq s;
+    latent_slot(p.cu_q, p.Tq, p.N, slots - 1 - (int)blockIdx.x, FWD_ROWS, n, j0);
     if (!latent_seq(p, n, s)) return;
-    const int h = blockIdx.y;
-    for (int r = warp; r < LAT_TILE; r += blockDim.x >> 5) {
-        const int i = j * LAT_TILE + r;
-        if (i >= s.lq) return;
-        const T* q = static_cast<const T*>(p.q) + ((s.q0 + i) * p.H + h) * LAT_QK;
-        float qv[6], acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int e = 0; e < 6; ++e) qv[e] = to_f(q[lane + 32 * e]) * p.scale;
-        const int last = p.causal ? min(s.lk, i + s.lk - s.lq + 1) : s.lk;
-        float m = -INFINITY, l = 0.f;
-        for (int k = 0; k < last; ++k) {
-            const T* kv = static_cast<const T*>(p.kv) + ((s.k0 + k) * p.H + h) * LAT_KV;
-            const T* pe = static_cast<const T*>(p.k_pe) + (s.k0 + k) * p.k_pe_stride;
-            float x = 0.f;
-            for (int e = 0; e < 4; ++e) x += qv[e] * to_f(kv[lane + 32 * e]);
-            for (int e = 0; e < 2; ++e) x += qv[4 + e] * to_f(pe[lane + 32 * e]);
-            x = warp_sum(x);
-            const float mn = fmaxf(m, x), c = mn == -INFINITY ? 1.f : expf(m - mn), w = mn == -INFINITY ? 0.f : expf(x - mn);
-            l = l * c + w;
-            for (int e = 0; e < 4; ++e) acc[e] = acc[e] * c + w * to_f(kv[LAT_N + lane + 32 * e]);
-            m = mn;
-        }
-        T* o = static_cast<T*>(p.o_out) + ((s.q0 + i) * p.H + h) * LAT_V;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        for (int e = 0; e < 4; ++e) o[lane + 32 * e] = from_f<T>(l > 0.f ? acc[e] * inv : 0.f);
-        if (lane == 0 && p.lse_out) p.lse_out[(s.q0 + i) * p.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    const int row0 = j0 * FWD_ROWS, h = blockIdx.y;
+    if (row0 >= s.lq) return;
+    const int shift = s.lk - s.lq;
+    int nt[2];   // key tiles that each query tile needs
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = row0 + t * LAT_TILE, last = min(first + LAT_TILE, s.lq) - 1;
+        const int kmax = first >= s.lq ? 0 : p.causal ? min(s.lk, last + shift + 1) : s.lk;
+        nt[t] = kmax > 0 ? (kmax + LAT_TILE - 1) / LAT_TILE : 0;
     }
+    const int steps = max(nt[0], nt[1]);
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < RING; ++i) {
+            mbar_init(base + F_FULL + 8 * i, 1);
+            mbar_init(base + F_EMPTY + 8 * i, 1);
+        }
+        for (uint32_t t = 0; t < 2; ++t) {
+            mbar_init(base + F_QFULL + 8 * t, 1);
+            mbar_init(base + F_SFULL + 8 * t, 1);
+            mbar_init(base + F_PFULL + 8 * t, 4);
+            mbar_init(base + F_ODONE + 8 * t, 1);
+        }
+        mbar_init(base + F_DRAIN, 1);
+        *failed = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(base + F_TMEM, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + F_TMEM);
+    // slab sequence: K of step j at 5 j .. 5 j + 2, its V at 5 j + 3, 5 j + 4
+    auto slab = [&](uint32_t i) { return base + F_RING + (i % RING) * SLAB; };
+
+    if (warp >= 8) {
+        // 168 registers a thread at launch: the softmax's 256 threads take 208, these 88 (2 x 208 + 88 = 3 x 168)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 9 && lane == 0 && steps > 0) {
+            for (int t = 0; t < 2; ++t) {
+                if (nt[t] == 0) continue;
+                mbar_arrive_expect_tx(base + F_QFULL + 8 * t, 3 * SLAB);
+                for (uint32_t c = 0; c < 3; ++c)
+                    tma_load_3d(base + F_Q + (3 * t + c) * SLAB, &maps.q, 64 * c, h, (int)s.q0 + row0 + t * LAT_TILE,
+                                base + F_QFULL + 8 * t);
+            }
+            uint32_t i = 0;
+            bool ok = true;
+            for (int j = 0; j < steps && ok; ++j) {
+                const int tok = (int)s.k0 + j * LAT_TILE;
+                for (uint32_t c = 0; c < 5; ++c, ++i) {
+                    if (i >= RING) ok = wait_phase(base + F_EMPTY + 8 * (i % RING), (i / RING - 1) & 1, limit, failed);
+                    if (!ok) break;
+                    const uint32_t bar = base + F_FULL + 8 * (i % RING);
+                    mbar_arrive_expect_tx(bar, SLAB);
+                    if (c == 2) tma_load_3d(slab(i), &maps.pe, 0, 0, tok, bar);
+                    else tma_load_3d(slab(i), &maps.kv, c < 2 ? 64 * c : 64 * (c - 1), h, tok, bar);
+                }
+            }
+            // every copy issued here has landed before the CTA ends
+            for (int t = 0; t < 2; ++t)
+                if (nt[t] > 0) mbar_wait(base + F_QFULL + 8 * t, 0, DRAIN_LIMIT);
+            for (uint32_t k = i > RING ? i - RING : 0; k < i; ++k)
+                mbar_wait(base + F_FULL + 8 * (k % RING), (k / RING) & 1, DRAIN_LIMIT);
+        } else if (warp == 8) {
+            const uint32_t id = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 128, false, false);
+            const uint32_t idv = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 128, false, true);
+            const uint32_t idv64 = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 64, false, true);
+            bool ok = true;
+            auto full = [&](uint32_t i) {
+                ok = __all_sync(0xffffffffu,
+                                ok && wait_phase(base + F_FULL + 8 * (i % RING), (i / RING) & 1, limit, failed));
+            };
+            auto qk = [&](int t, int j) {   // S_t = Q_t K_j^T
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    if (t == 0 || nt[0] <= j) full(5 * j + c);
+                    if (!ok) return;
+                    const uint32_t a = base + F_Q + (3 * t + c) * SLAB, b = slab(5 * j + c);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16_warp(tmem + 256 * t, desc_k(a, LAT_TILE, ks), desc_k(b, LAT_TILE, ks), id, c + ks > 0);
+                }
+                mma_commit_warp(base + F_SFULL + 8 * t);
+            };
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (nt[t] == 0) continue;
+                ok = __all_sync(0xffffffffu, wait_phase(base + F_QFULL + 8 * t, 0, limit, failed));
+                if (ok) qk(t, 0);
+            }
+            if (steps > 0 && ok)
+                for (uint32_t c = 0; c < 3; ++c) mma_commit_warp(base + F_EMPTY + 8 * c);
+            for (int j = 0; j < steps && ok; ++j) {
+                const uint32_t v = 5 * j + 3;
+                full(v);
+                full(v + 1);
+                if (!ok) break;
+                if ((j + 1) * LAT_TILE > s.lk) {
+                    // rows past the sequence's end hold whatever follows: zero weights must meet zeros
+                    for (int r = s.lk - j * LAT_TILE; r < LAT_TILE; ++r)
+                        if (lane < 16)
+                            *reinterpret_cast<uint4*>(smem + (slab(v + (lane >> 3)) - base) + r * 128 + (lane & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j < nt[t] && ok) {
+                        ok = __all_sync(0xffffffffu, wait_phase(base + F_PFULL + 8 * t, j & 1, limit, failed));
+                        if (!ok) break;
+                        tc_fence_after();
+                        // O_t += P_t V_j; where the ring wraps between V's two slabs, one product for each
+                        const uint32_t d = tmem + 256 * t + 128, a = tmem + 256 * t;
+                        if ((v + 1) % RING != 0) {
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)
+                                mma_f16_ts_warp(d, a + 8 * ks, desc_mn(slab(v), LAT_TILE, ks), idv, j + ks > 0);
+                        } else {
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks) {
+                                mma_f16_ts_warp(d, a + 8 * ks, desc_mn(slab(v), LAT_TILE, ks), idv64, j + ks > 0);
+                                mma_f16_ts_warp(d + 64, a + 8 * ks, desc_mn(slab(v + 1), LAT_TILE, ks), idv64,
+                                                j + ks > 0);
+                            }
+                        }
+                        if (j == nt[t] - 1) mma_commit_warp(base + F_ODONE + 8 * t);
+                    }
+                    if (t == 1) {
+                        mma_commit_warp(base + F_EMPTY + 8 * (v % RING));
+                        mma_commit_warp(base + F_EMPTY + 8 * ((v + 1) % RING));
+                    }
+                    if (j + 1 < nt[t] && ok) qk(t, j + 1);
+                }
+                if (j + 1 < steps && ok)
+                    for (uint32_t c = 0; c < 3; ++c) mma_commit_warp(base + F_EMPTY + 8 * ((5 * (j + 1) + c) % RING));
+            }
+            // every product issued here is done before the tensor memory is freed
+            mma_commit_warp(base + F_DRAIN);
+            mbar_wait(base + F_DRAIN, 0, DRAIN_LIMIT);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2;
+        const int row = row0 + t * LAT_TILE + (warp & 3) * 32 + lane;
+        const uint32_t ts = tmem + 256 * t + ((uint32_t)(warp & 3) << 21);   // this warp's lanes
+        const float c = p.scale * 1.4426950408889634f;
+        const int kmax = p.causal ? min(s.lk, row + shift + 1) : s.lk;      // keys [0, kmax) count
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nt[t]; ++j) {
+            ok = __all_sync(0xffffffffu, wait_phase(base + F_SFULL + 8 * t, j & 1, limit, failed));
+            if (!ok) break;
+            tc_fence_after();
+            float x[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, x[b]);
+            tmem_ld_wait();
+            const int lim = kmax - j * LAT_TILE;
+            if (__any_sync(0xffffffffu, lim < LAT_TILE)) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[b][e] = 32 * b + e < lim ? x[b][e] : -INFINITY;
+            }
+            float top = x[0][0];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top = fmaxf(top, x[b][e]);
+            const bool grown = top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, grown)) {
+                const float mn = grown ? top : m;
+                const float f = grown ? ex2((m - mn) * c) : 1.f;   // 0 from -inf
+                l *= f;
+                if (j > 0) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float o[32];
+                        tmem_ld32(ts + 128 + 32 * b, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tmem_st32(ts + 128 + 32 * b, o);
+                    }
+                }
+                m = mn;
+            }
+            const float mc = m == -INFINITY ? 0.f : m * c;
+#pragma unroll
+            for (int b = 0; b < 4; b += 2) {
+                float w[32];
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    const float u = ex2(fmaf(x[b + (e >> 5)][e & 31], c, -mc));
+                    const float v = ex2(fmaf(x[b + (e >> 5)][(e & 31) + 1], c, -mc));
+                    l += u + v;
+                    w[e >> 1] = __uint_as_float(pack2<FP16>(u, v));
+                }
+                tmem_st32(ts + 16 * b, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + F_PFULL + 8 * t);
+        }
+        if (nt[t] > 0 && ok) ok = wait_phase(base + F_ODONE + 8 * t, 0, limit, failed);
+        if (__all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const long long at = (s.q0 + row) * p.H + h;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o_out) + at * LAT_V);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float o[32];
+                if (nt[t] > 0) {
+                    tmem_ld32(ts + 128 + 32 * b, o);
+                    tmem_ld_wait();
+                }
+                if (row < s.lq) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            r[k] = l == 0.f ? 0u : pack2<FP16>(o[e + 2 * k] * inv, o[e + 2 * k + 1] * inv);
+                        out[4 * b + (e >> 3)] = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
+                }
+            }
+            if (row < s.lq && p.lse_out) p.lse_out[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
+}
+
+template <bool FP16>
+cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, cudaStream_t stream) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(latent_fwd_kernel<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
+    if (e != cudaSuccess) return e;
+    latent_fwd_kernel<FP16><<<dim3(slots, p.H), FWD_THREADS, F_SMEM, stream>>>(p, maps, slots);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t stream) {
-    const int slots = latent_slots(p.cu_q != nullptr, p.Tq, p.N);
-    const dim3 grid(slots, p.H);
-    if (fp16) latent_fwd_kernel<__half><<<grid, 256, 0, stream>>>(p);
-    else latent_fwd_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    const bool varlen = p.cu_q != nullptr;
+    const long long rows_q = varlen ? p.Tq : (long long)p.N * p.Tq, rows_k = varlen ? p.Tk : (long long)p.N * p.Tk;
+    FwdMaps maps;
+    // without keys nothing is loaded: any valid tensor does
+    const void* kv = rows_k > 0 ? p.kv : p.q;
+    const void* pe = rows_k > 0 ? p.k_pe : p.q;
+    if (!latent_row_map(&maps.q, p.q, LAT_QK, p.H, rows_q, (long long)p.H * LAT_QK, LAT_TILE) ||
+        !latent_row_map(&maps.kv, kv, LAT_KV, p.H, rows_k > 0 ? rows_k : 1, (long long)p.H * LAT_KV, LAT_TILE) ||
+        !latent_row_map(&maps.pe, pe, LAT_P, 1, rows_k > 0 ? rows_k : 1, p.k_pe_stride, LAT_TILE))
+        return cudaErrorInvalidValue;
+    const int slots = latent_slots(varlen, p.Tq, p.N, FWD_ROWS);
+    return fp16 ? launch<true>(p, maps, slots, stream) : launch<false>(p, maps, slots, stream);
 }
 
 }  // namespace kda

@@ -1299,8 +1299,6 @@ __global__ void __launch_bounds__(PREP_THREADS, 1)
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-namespace {
-
 // The driver's tensor-map encoder, found once through the runtime (no link
 // against the driver library).
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
@@ -1315,6 +1313,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     });
     return fn;
 }
+
+namespace {
 
 // q, k or v ([tokens][H][128] bf16) as a 3-D tensor (dimension, head, token):
 // one load brings 64 dimensions of one head for 128 consecutive tokens, in
