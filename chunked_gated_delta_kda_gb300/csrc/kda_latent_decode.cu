@@ -1,57 +1,629 @@
-// Absorbed latent attention over the paged cache: one warp per (token, head).
+// Absorbed latent attention over the paged cache (kda_latent_decode).
+//
+// The cached rows serve all rows (token, head) of a sequence, as keys with
+// their 576 channels and as values with the first 512, so each is read once
+// and used from shared memory by both products:
+//   S = Q R^T            [rows, 64 keys]       M = 64, K = 576
+//   O^T += R_v^T P^T     [512 channels, rows]  four M = 128 blocks, K = 64 keys
+// O is kept transposed: its channels fill the lanes of tensor memory whatever
+// the number of rows, so 64 rows take half of it, and the second product costs
+// what the rows need (16, 32 or 64) instead of a padded 128.
+//
+// Bound by the cache's bytes: 64 rows of the cache are 72 KiB, about 3100
+// cycles of an SM's share of the HBM, beside about 1800 of products (both
+// limited by what the tensor core reads from shared memory) and 800 of
+// softmax, which overlap.  The lengths are on the device, so the work is
+// split there: the 64-key tiles of all (sequence, 64-row block) units form
+// one line that is cut into equal ranges, one a CTA, wherever the cuts fall.
+// A unit inside one range is finished by its CTA; the parts of a cut one go
+// to the workspace with their log-sum-exp and are joined by a second kernel,
+// which also writes the empty sequences.
+//   warps 0-3  softmax (row 16 w + l in lane l < 16 of warp w, as an M = 64
+//              product lays its rows out), rescaling and output of O
+//   warp 4     issues the products;  warp 5  loads
 #include "kda_latent_decode.cuh"
+#include "kda_latent_mma.cuh"
 
 namespace kda {
 
 namespace {
 
-template <typename T>
-__global__ void latent_decode_kernel(DecodeParams p) {
-    const int lane = threadIdx.x, h = blockIdx.x, t = blockIdx.y, n = blockIdx.z;
-    const long long row = ((long long)n * p.S + t) * p.H + h;
-    const T* q = static_cast<const T*>(p.q) + row * LAT_ROW;
-    float qv[18], acc[16] = {}, m = -INFINITY, l = 0.f;
-    for (int e = 0; e < 18; ++e) qv[e] = to_f(q[lane + 32 * e]) * p.scale;
+constexpr int DEC_THREADS = 192;
+constexpr int KEYS = 64;                                 // keys of a tile
+constexpr uint32_t PAIR = 2 * KEYS * 128;                // 128 channels of a tile: two 64-channel slabs
+constexpr uint32_t PE = KEYS * 128;                      // its 64 positional channels
+constexpr float RESCALE_LOG2 = 8.f;
+
+// Shared-memory layout for R rows of a unit: Q, P, then the two rings.
+template <int R>
+struct Lay {
+    static constexpr uint32_t NP = R == 64 ? 8 : 10, NE = R == 64 ? 2 : 3;   // 2 or 2.5 tiles in flight
+    static constexpr uint32_t Q = 0;                     // 9 slabs of R rows
+    static constexpr uint32_t P = Q + 9 * R * 128;
+    static constexpr uint32_t RP = P + R * 128;
+    static constexpr uint32_t RE = RP + NP * PAIR;
+    static constexpr uint32_t BAR = RE + NE * PE;
+    static constexpr uint32_t PFULL = BAR;               // ring: [NP] full, [NP] empty, [NE] full, [NE] empty
+    static constexpr uint32_t PEMPTY = PFULL + 8 * NP;
+    static constexpr uint32_t EFULL = PEMPTY + 8 * NP;
+    static constexpr uint32_t EEMPTY = EFULL + 8 * NE;
+    static constexpr uint32_t QFULL = EEMPTY + 8 * NE;
+    static constexpr uint32_t QEMPTY = QFULL + 8;
+    static constexpr uint32_t SFULL = QEMPTY + 8;        // [2]
+    static constexpr uint32_t WFULL = SFULL + 16;        // P written
+    static constexpr uint32_t VDONE = WFULL + 8;         // second product of a tile done
+    static constexpr uint32_t OFREE = VDONE + 8;         // O read out
+    static constexpr uint32_t DRAIN = OFREE + 8;
+    static constexpr uint32_t FACT = DRAIN + 8;          // [64] floats
+    static constexpr uint32_t PLAN = FACT + 256;
+    static constexpr uint32_t BYTES = PLAN + 256;
+    static constexpr uint32_t SMEM = BYTES + 1024;
+    static_assert(SMEM <= 232448, "shared memory of one CTA");
+};
+
+struct Plan {
+    long long scan[DEC_THREADS / 32];
+    long long first, count;     // this CTA's range
+    int n, mt, k0;              // where it starts
+    uint32_t tmem, failed, err;
+};
+
+struct DecMaps {
+    CUtensorMap q, cache;
+};
+
+__device__ __forceinline__ int clipped_len(const DecodeParams& p, int n) {
     const long long most = (long long)p.table_width * p.page_size;
-    int len = p.lens[n];
-    if (len < 0 || len > most) {
-        if (lane == 0) set_status(p.status, STATUS_BAD_PAGE);
-        len = len < 0 ? 0 : (int)most;
+    return (int)max(0ll, min((long long)p.lens[n], most));
+}
+
+// A role's walk over the segments of its CTA's range.
+struct Walk {
+    int n, mt, k0, tiles, cnt, len;
+    long long left;             // tiles of the range from this segment on
+    bool first;
+    __device__ __forceinline__ void set(const DecodeParams& p) {
+        len = clipped_len(p, n);
+        tiles = (len + KEYS - 1) / KEYS;
+        cnt = (int)min((long long)(tiles - k0), left);
     }
-    const int last = len - p.S + 1 + t;
-    for (int k = 0; k < last; ++k) {
-        const int page = p.table[(long long)n * p.table_width + k / p.page_size];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) set_status(p.status, STATUS_BAD_PAGE);
-            continue;
-        }
-        const T* r = static_cast<const T*>(p.cache) + ((long long)page * p.page_size + k % p.page_size) * LAT_ROW;
-        float x = 0.f, rv[18];
-        for (int e = 0; e < 18; ++e) {
-            rv[e] = to_f(r[lane + 32 * e]);
-            x += qv[e] * rv[e];
-        }
-        x = warp_sum(x);
-        const float mn = fmaxf(m, x), c = mn == -INFINITY ? 1.f : expf(m - mn), w = mn == -INFINITY ? 0.f : expf(x - mn);
-        l = l * c + w;
-        for (int e = 0; e < 16; ++e) acc[e] = acc[e] * c + w * rv[e];
-        m = mn;
+    __device__ __forceinline__ Walk(const DecodeParams& p, const Plan& pl)
+        : n(pl.n), mt(pl.mt), k0(pl.k0), left(pl.count), first(true) {
+        if (left > 0) set(p);
     }
-    T* o = static_cast<T*>(p.o) + row * LAT_C;
-    for (int e = 0; e < 16; ++e) o[lane + 32 * e] = from_f<T>(l > 0.f ? acc[e] / l : 0.f);
-    if (lane == 0 && p.lse) p.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+    __device__ __forceinline__ void next(const DecodeParams& p, int mts) {
+        left -= cnt;
+        first = false;
+        if (left <= 0) return;
+        k0 = 0;
+        if (++mt == mts) {
+            mt = 0;
+            do ++n;
+            while (n < p.N - 1 && clipped_len(p, n) == 0);
+        }
+        set(p);
+    }
+};
+
+// The page of the 64-key tile's box b (`rows` keys), or -1 where its keys are
+// past the sequence's end or the page does not exist.
+__device__ __forceinline__ int box_page(const DecodeParams& p, const Walk& w, int tile, int b, int rows, int& row) {
+    const int key = tile * KEYS + b * rows;
+    row = 0;
+    if (key >= w.len) return -1;
+    const int page = p.table[(long long)w.n * p.table_width + key / p.page_size];
+    row = key % p.page_size;
+    return page >= 0 && page < p.num_pages ? page : -1;
+}
+
+// Whether a page of the segment does not exist (whole warp).
+__device__ __forceinline__ bool bad_pages(const DecodeParams& p, const Walk& w, int lane) {
+    const int a = w.k0 * KEYS / p.page_size, last = min((w.k0 + w.cnt) * KEYS, w.len) - 1;
+    bool bad = false;
+    for (int i = a + lane; i <= last / p.page_size; i += 32) {
+        const int page = p.table[(long long)w.n * p.table_width + i];
+        bad |= page < 0 || page >= p.num_pages;
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+
+// Keys of a tile that exist, as bits.
+__device__ __forceinline__ unsigned long long tile_keys(const DecodeParams& p, const Walk& w, int tile, int box) {
+    unsigned long long m = 0;
+    for (int b = 0; b < KEYS / box; ++b) {
+        int row;
+        const int have = min(box, w.len - tile * KEYS - b * box);
+        if (have > 0 && box_page(p, w, tile, b, box, row) >= 0)
+            m |= (have == 64 ? ~0ull : (1ull << have) - 1) << (b * box);
+    }
+    return m;
+}
+
+template <int R, bool FP16>
+__global__ void __launch_bounds__(DEC_THREADS, 1)
+    latent_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ DecMaps maps,
+                         const __grid_constant__ DecodeScratch sc) {
+    using L = Lay<R>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    Plan& plan = *reinterpret_cast<Plan*>(smem + L::PLAN);
+    static_assert(sizeof(Plan) <= 256, "plan");
+    volatile uint32_t* failed = &plan.failed;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
+    const int rows = p.S * p.H, mts = (rows + R - 1) / R;
+    const int box = min(p.page_size, KEYS);
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < L::NP; ++i) {
+            mbar_init(base + L::PFULL + 8 * i, 1);
+            mbar_init(base + L::PEMPTY + 8 * i, 1);
+        }
+        for (uint32_t i = 0; i < L::NE; ++i) {
+            mbar_init(base + L::EFULL + 8 * i, 1);
+            mbar_init(base + L::EEMPTY + 8 * i, 1);
+        }
+        mbar_init(base + L::QFULL, 1);
+        mbar_init(base + L::QEMPTY, 1);
+        mbar_init(base + L::SFULL, 1);
+        mbar_init(base + L::SFULL + 8, 1);
+        mbar_init(base + L::WFULL, 4);
+        mbar_init(base + L::VDONE, 1);
+        mbar_init(base + L::OFREE, 4);
+        mbar_init(base + L::DRAIN, 1);
+        plan.failed = 0u;
+        plan.err = 0u;
+        plan.count = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(base + L::PLAN + (uint32_t)offsetof(Plan, tmem), 512);
+        tmem_relinquish();
+    }
+    // ---- the line of tiles, and this CTA's part of it ----
+    {
+        const int per = (p.N + DEC_THREADS - 1) / DEC_THREADS;
+        const int a = min(p.N, tid * per), b = min(p.N, a + per);
+        long long sum = 0;
+        bool bad = false;
+        for (int n = a; n < b; ++n) {
+            const int len = clipped_len(p, n);
+            bad |= len != p.lens[n];
+            sum += (long long)((len + KEYS - 1) / KEYS) * mts;
+        }
+        long long x = sum;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) plan.scan[warp] = x;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        long long before = 0, total = 0;
+        for (int w = 0; w < DEC_THREADS / 32; ++w) {
+            if (w < warp) before += plan.scan[w];
+            total += plan.scan[w];
+        }
+        const long long g = min((long long)gridDim.x, total);
+        long long at = before + x - sum;               // tiles before sequence a
+        if (cta == 0) {
+            if (bad) atomicOr(&plan.err, STATUS_BAD_PAGE);
+            long long pos = at;
+            for (int n = a; n < b; ++n) {
+                sc.prefix[n] = pos;
+                pos += (long long)((clipped_len(p, n) + KEYS - 1) / KEYS) * mts;
+            }
+            if (tid == 0) sc.prefix[p.N] = total;
+        }
+        if (cta < g) {
+            const long long lo = cta * total / g, hi = (cta + 1) * total / g;
+            if (lo >= at && lo < at + sum) {           // one thread: the range starts in its sequences
+                int n = a;
+                for (;; ++n) {
+                    const int t = (clipped_len(p, n) + KEYS - 1) / KEYS;
+                    if (lo < at + (long long)t * mts) {
+                        plan.n = n;
+                        plan.mt = (int)((lo - at) / t);
+                        plan.k0 = (int)((lo - at) % t);
+                        break;
+                    }
+                    at += (long long)t * mts;
+                }
+                plan.first = lo;
+                plan.count = hi - lo;
+            }
+        }
+        __syncthreads();
+    }
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&plan.tmem);
+    const uint32_t t_s = tmem + 256;                   // S: two buffers of 64 columns; O: columns [0, 4 R)
+
+    if (warp == 5) {
+        // ---- loads ----
+        uint32_t ip = 0, ie = 0, seg = 0;              // pairs, positional slabs and queries asked for
+        bool ok = true;
+        for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts)) {
+            if (seg > 0) ok = __all_sync(0xffffffffu, wait_phase(base + L::QEMPTY, (seg - 1) & 1, limit, failed));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(base + L::QFULL, 9 * R * 128);
+            __syncwarp();
+            if (lane < 9)
+                tma_load_3d(base + L::Q + lane * R * 128, &maps.q, 64 * lane, 0, w.n * rows + w.mt * R, base + L::QFULL);
+            ++seg;
+            const int nbox = KEYS / box;
+            bool bad = false;
+            for (int k = 0; k < w.cnt && ok; ++k) {
+                const int tile = w.k0 + k;
+                int row;
+                const int page = lane < 2 * nbox ? box_page(p, w, tile, lane >> 1, box, row) : -1;
+                const bool have = page >= 0;
+                bad |= lane < 2 * nbox && !have && tile * KEYS + (lane >> 1) * box < w.len;
+                const int at = page * p.page_size + row;
+                const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) / 2u;
+                for (int c = 0; c < 5 && ok; ++c) {
+                    const uint32_t i = c < 4 ? ip : ie, depth = c < 4 ? L::NP : L::NE;
+                    const uint32_t full = base + (c < 4 ? L::PFULL : L::EFULL) + 8 * (i % depth);
+                    if (i >= depth)
+                        ok = __all_sync(0xffffffffu,
+                                        wait_phase(base + (c < 4 ? L::PEMPTY : L::EEMPTY) + 8 * (i % depth),
+                                                   (i / depth - 1) & 1, limit, failed));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)box * (c < 4 ? 256u : 128u));
+                    __syncwarp();
+                    const uint32_t dst = base + (c < 4 ? L::RP + (i % depth) * PAIR : L::RE + (i % depth) * PE) +
+                                         (uint32_t)(lane >> 1) * (uint32_t)box * 128u;
+                    if (have && (c < 4 || (lane & 1) == 0))
+                        tma_load_3d(dst + (uint32_t)(lane & 1) * (PAIR / 2), &maps.cache, 128 * c + 64 * (lane & 1), 0, at,
+                                    full);
+                    if (c < 4) ++ip;
+                    else ++ie;
+                }
+            }
+            if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&plan.err, STATUS_BAD_PAGE);
+        }
+        // every copy issued here has landed before the CTA ends
+        for (uint32_t k = ip > L::NP ? ip - L::NP : 0; k < ip; ++k)
+            mbar_wait(base + L::PFULL + 8 * (k % L::NP), (k / L::NP) & 1, DRAIN_LIMIT);
+        for (uint32_t k = ie > L::NE ? ie - L::NE : 0; k < ie; ++k)
+            mbar_wait(base + L::EFULL + 8 * (k % L::NE), (k / L::NE) & 1, DRAIN_LIMIT);
+        if (seg > 0) mbar_wait(base + L::QFULL, (seg - 1) & 1, DRAIN_LIMIT);
+    } else if (warp == 4) {
+        // ---- products ----
+        const MmaType ty = FP16 ? T_F16 : T_BF16;
+        const uint32_t id_s = idesc_f16(ty, 64, KEYS, false, false), id_o = idesc_f16(ty, 128, R, true, false);
+        uint32_t g = 0, seg = 0;                       // tiles and segments so far
+        bool ok = true;
+        auto score = [&](uint32_t t) {                 // S of tile t of the line
+#pragma unroll
+            for (int c = 0; c < 5; ++c) {
+                const uint32_t i = c < 4 ? 4 * t + c : t, depth = c < 4 ? L::NP : L::NE;
+                ok = __all_sync(0xffffffffu, ok && wait_phase(base + (c < 4 ? L::PFULL : L::EFULL) + 8 * (i % depth),
+                                                              (i / depth) & 1, limit, failed));
+                if (!ok) return;
+                const uint32_t b = base + (c < 4 ? L::RP + (i % depth) * PAIR : L::RE + (i % depth) * PE);
+#pragma unroll
+                for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks)
+                    mma_f16_warp(t_s + 64 * (t & 1), desc_k(base + L::Q + 2 * c * R * 128, R, ks), desc_k(b, KEYS, ks), id_s,
+                                 c + ks > 0);
+            }
+            mma_commit_warp(base + L::SFULL + 8 * (t & 1));
+            mma_commit_warp(base + L::EEMPTY + 8 * (t % L::NE));
+        };
+        for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts), ++seg) {
+            const bool gaps = bad_pages(p, w, lane);
+            ok = __all_sync(0xffffffffu, wait_phase(base + L::QFULL, seg & 1, limit, failed));
+            if (ok) score(g);
+            if (ok && w.cnt == 1) mma_commit_warp(base + L::QEMPTY);
+            for (int k = 0; k < w.cnt && ok; ++k, ++g) {
+                if (k + 1 < w.cnt) {
+                    score(g + 1);
+                    if (ok && k + 2 == w.cnt) mma_commit_warp(base + L::QEMPTY);
+                }
+                ok = __all_sync(0xffffffffu, ok && wait_phase(base + L::WFULL, g & 1, limit, failed));
+                if (ok && k == 0 && seg > 0)
+                    ok = __all_sync(0xffffffffu, wait_phase(base + L::OFREE, (seg - 1) & 1, limit, failed));
+                if (!ok) break;
+                tc_fence_after();
+                const int tile = w.k0 + k;
+                if (gaps || (tile + 1) * KEYS > w.len) {
+                    // rows that do not exist hold whatever was there: zero weights must meet zeros
+                    const unsigned long long keys = tile_keys(p, w, tile, box);
+                    for (int r = 0; r < KEYS; ++r)
+                        if (!(keys >> r & 1))
+                            for (uint32_t c = lane; c < 64; c += 32)
+                                *reinterpret_cast<uint4*>(smem + L::RP + ((4 * g + (c >> 4)) % L::NP) * PAIR +
+                                                          (c >> 3 & 1) * (PAIR / 2) + r * 128 + (c & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {          // O^T: channels 128 c ..
+                    const uint32_t i = (4 * g + c) % L::NP;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16_warp(tmem + c * R, desc_mn(base + L::RP + i * PAIR, KEYS, ks),
+                                     desc_k(base + L::P, R, ks), id_o, k + ks > 0);
+                    mma_commit_warp(base + L::PEMPTY + 8 * i);
+                }
+                mma_commit_warp(base + L::VDONE);
+            }
+        }
+        // every product issued here is done before the tensor memory is freed
+        mma_commit_warp(base + L::DRAIN);
+        mbar_wait(base + L::DRAIN, 0, DRAIN_LIMIT);
+    } else {
+        // ---- softmax and output ----
+        const float c = p.scale * 1.4426950408889634f;
+        const uint32_t quad = (uint32_t)warp << 21;    // this warp's lanes
+        const int r = 16 * warp + (lane & 15);         // its row; lanes 16-31 repeat it and store nothing
+        float* fact = reinterpret_cast<float*>(smem + L::FACT);
+        uint32_t g = 0;
+        bool ok = true;
+        for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts)) {
+            const bool gaps = bad_pages(p, w, lane);
+            const int gr = w.mt * R + r;
+            const int lim = w.len - p.S + 1 + min(gr, rows - 1) / p.H;   // keys [0, lim) are seen
+            float m = -INFINITY, l = 0.f;
+            for (int k = 0; k < w.cnt && ok; ++k, ++g) {
+                ok = bar_and_named(1, 128, wait_phase(base + L::SFULL + 8 * (g & 1), g >> 1 & 1, limit, failed));
+                if (!ok) break;
+                tc_fence_after();
+                const int tile = w.k0 + k;
+                float x[2][32];
+                tmem_ld32(t_s + 64 * (g & 1) + quad, x[0]);
+                tmem_ld32(t_s + 64 * (g & 1) + 32 + quad, x[1]);
+                tmem_ld_wait();
+                const int have = lim - tile * KEYS;
+                if (gaps || __any_sync(0xffffffffu, have < KEYS)) {
+                    unsigned long long keys = gaps ? tile_keys(p, w, tile, box) : ~0ull;
+                    keys &= have >= KEYS ? ~0ull : have > 0 ? (1ull << have) - 1 : 0ull;
+#pragma unroll
+                    for (int e = 0; e < KEYS; ++e)
+                        if (!(keys >> e & 1)) x[e >> 5][e & 31] = -INFINITY;
+                }
+                float top = x[0][0];
+#pragma unroll
+                for (int e = 1; e < KEYS; ++e) top = fmaxf(top, x[e >> 5][e & 31]);
+                bool grown = top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m);
+                grown = grown && r < R && lane < 16;
+                // P's buffer is free, and O stands still, once the tile before is done
+                if (k > 0) ok = wait_phase(base + L::VDONE, (g - 1) & 1, limit, failed);
+                if (!bar_and_named(1, 128, ok && !grown)) {
+                    ok = bar_and_named(1, 128, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float mn = grown ? top : m;
+                    const float f = grown ? ex2((m - mn) * c) : 1.f;
+                    l *= f;
+                    m = mn;
+                    if (k > 0) {
+                        if (lane < 16) fact[r] = f;
+                        bar_and_named(1, 128, true);
+#pragma unroll 1
+                        for (int b = 0; b < 4 * R; b += 16) {
+                            float o[16];
+                            tmem_ld16(tmem + quad + b, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= fact[(b + e) % R];
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                tmem_st4(tmem + quad + b + e, __float_as_uint(o[e]), __float_as_uint(o[e + 1]),
+                                         __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                if (r < R) {
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = 8 * q + 2 * e;
+                            const float u = ex2(fmaf(x[at >> 5][at & 31], c, -mc));
+                            const float v = ex2(fmaf(x[at >> 5][(at & 31) + 1], c, -mc));
+                            l += u + v;
+                            o[e] = pack2<FP16>(u, v);
+                        }
+                        if (lane < 16)
+                            *reinterpret_cast<uint4*>(smem + L::P + r * 128 + ((q ^ (r & 7)) * 16)) =
+                                make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(base + L::WFULL);
+            }
+            if (ok) ok = wait_phase(base + L::VDONE, (g - 1) & 1, limit, failed);
+            ok = bar_and_named(1, 128, ok);
+            if (!ok) break;
+            tc_fence_after();
+            // ---- the segment's rows ----
+            const bool whole = w.cnt == w.tiles;
+            const int slot = 2 * cta + (w.first ? 0 : 1);
+            if (r < R && lane < 16) {
+                fact[r] = l == 0.f ? 0.f : 1.f / l;
+                const float lse = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+                if (whole) {
+                    if (gr < rows && p.lse) p.lse[(long long)w.n * rows + gr] = lse;
+                } else {
+                    sc.lse[slot * R + r] = lse;
+                }
+            }
+            bar_and_named(1, 128, true);
+            const int have = min(R, rows - w.mt * R);
+#pragma unroll 1
+            for (int b = 0; b < 4 * R; b += 16) {
+                float o[16];
+                tmem_ld16(tmem + quad + b, o);
+                tmem_ld_wait();
+                const int ch = b / R * 128 + 32 * warp + lane;
+                if (whole) {
+                    uint16_t* out = static_cast<uint16_t*>(p.o) + ((long long)w.n * rows + w.mt * R) * LAT_C + ch;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int rr = b % R + e;
+                        const float f = fact[rr];
+                        if (rr < have) out[(long long)rr * LAT_C] = (uint16_t)pack2<FP16>(f == 0.f ? 0.f : o[e] * f, 0.f);
+                    }
+                } else {
+                    float* out = sc.o + (long long)slot * R * LAT_C + ch;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int rr = b % R + e;
+                        const float f = fact[rr];
+                        if (rr < have) out[rr * LAT_C] = f == 0.f ? 0.f : o[e] * f;
+                    }
+                }
+            }
+            tc_fence_before();
+            bar_and_named(1, 128, true);               // fact is reused by the next segment
+            if (lane == 0) mbar_arrive(base + L::OFREE);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) tmem_dealloc(tmem, 512);
+    if (tid == 0) sc.err[cta] = plan.err | (plan.failed ? STATUS_TIMEOUT : 0u);
+}
+
+// Joins the parts of the units that were cut, one row a group of warps:
+// lse = log sum exp(lse_i), o = sum exp(lse_i - lse) o_i, in the order of the
+// parts; writes zeros for empty sequences.
+template <bool FP16>
+__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ DecodeParams p,
+                                                          const __grid_constant__ DecodeScratch sc, int R, int mts,
+                                                          int rows_cta, int ctas) {
+    __shared__ float acc[8][LAT_C];
+    __shared__ float stat[8][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = p.S * p.H;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+        uint32_t err = 0;
+        for (int c = lane; c < ctas; c += 32) err |= sc.err[c];
+        err = __reduce_or_sync(0xffffffffu, err);
+        if (lane == 0) *p.status = err;
+    }
+    const int n = blockIdx.x / mts, mt = blockIdx.x % mts;
+    const long long total = sc.prefix[p.N], tiles = (sc.prefix[n + 1] - sc.prefix[n]) / mts;
+    const long long w0 = sc.prefix[n] + mt * tiles, g = min((long long)ctas, total);
+    int c0 = 0, c1 = -1;
+    if (tiles > 0) {
+        c0 = (int)(((w0 + 1) * g - 1) / total);
+        c1 = (int)(((w0 + tiles) * g - 1) / total);
+        if (c0 == c1) return;
+    }
+    const int group = 8 / rows_cta;                    // warps of a row
+    const int r = blockIdx.y * rows_cta + warp / group, part = warp % group;
+    const bool there = r < R && mt * R + r < rows;
+    float m = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+    if (there) {
+        auto slot_of = [&](int c) { return 2 * c + (c > c0 || c * total / g == w0 ? 0 : 1); };
+        for (int c = c0 + part; c <= c1; c += group) m = fmaxf(m, sc.lse[slot_of(c) * R + r]);
+        for (int c = c0 + part; c <= c1; c += group) {
+            const int s = slot_of(c);
+            const float lse = sc.lse[s * R + r];
+            const float w = lse == -INFINITY ? 0.f : expf(lse - m);
+            const float4* src = reinterpret_cast<const float4*>(sc.o + ((long long)s * R + r) * LAT_C);
+            l += w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 v = src[lane + 32 * e];
+                o[4 * e] += w * v.x;
+                o[4 * e + 1] += w * v.y;
+                o[4 * e + 2] += w * v.z;
+                o[4 * e + 3] += w * v.w;
+            }
+        }
+    }
+    if (group > 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<float4*>(&acc[warp][4 * (lane + 32 * e)]) =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        if (lane == 0) stat[warp][0] = m, stat[warp][1] = l;
+        __syncthreads();
+        if (part != 0) return;
+        float top = m;
+        for (int k = 1; k < group; ++k) top = fmaxf(top, stat[warp + k][0]);
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = 0.f;
+        for (int k = 0; k < group; ++k) {
+            const float mk = stat[warp + k][0], f = mk == -INFINITY ? 0.f : expf(mk - top);
+            l += f * stat[warp + k][1];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] += f * acc[warp + k][4 * (lane + 32 * (e >> 2)) + (e & 3)];
+        }
+        m = top;
+    }
+    if (!there) return;
+    const long long at = (long long)n * rows + mt * R + r;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at * LAT_C);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        out[lane + 32 * e] = make_uint2(pack2<FP16>(o[4 * e] * inv, o[4 * e + 1] * inv),
+                                        pack2<FP16>(o[4 * e + 2] * inv, o[4 * e + 3] * inv));
+    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+int unit_rows(int S, int H) { return (long long)S * H <= 16 ? 16 : (long long)S * H <= 32 ? 32 : 64; }
+
+unsigned long long up256(unsigned long long b) { return (b + 255ull) / 256ull * 256ull; }
+
+template <int R, bool FP16>
+cudaError_t launch(const DecodeParams& p, const DecMaps& maps, const DecodeScratch& sc, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<R, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Lay<R>::SMEM);
+    if (e != cudaSuccess) return e;
+    latent_decode_kernel<R, FP16><<<DEC_CTAS, DEC_THREADS, Lay<R>::SMEM, stream>>>(p, maps, sc);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int mts = (p.S * p.H + R - 1) / R;
+    // few units: a CTA for each row, its warps sharing the parts; many: a warp a row
+    const int rows_cta = (long long)p.N * mts * R <= 1024 ? 1 : 8;
+    latent_join_kernel<FP16><<<dim3(p.N * mts, (R + rows_cta - 1) / rows_cta), 256, 0, stream>>>(p, sc, R, mts, rows_cta,
+                                                                                                DEC_CTAS);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-unsigned long long latent_decode_scratch(int N, int S, int H) { return WS_HEADER; }
+// Workspace: header, error words of the CTAs, tiles before each sequence, two
+// parts a CTA (log-sum-exp and output of each row).
+unsigned long long latent_decode_scratch(int N, int S, int H) {
+    const unsigned long long r = (unsigned long long)unit_rows(S, H);
+    return WS_HEADER + up256(DEC_CTAS * 4ull) + up256((N + 1ull) * 8ull) + up256(2ull * DEC_CTAS * r * 4ull) +
+           2ull * DEC_CTAS * r * LAT_C * 4ull;
+}
 
 cudaError_t launch_latent_decode(const DecodeParams& p, bool fp16, cudaStream_t stream) {
-    if (cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return cudaGetLastError();
-    const dim3 grid(p.H, p.S, p.N);
-    if (fp16) latent_decode_kernel<__half><<<grid, 32, 0, stream>>>(p);
-    else latent_decode_kernel<__nv_bfloat16><<<grid, 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int r = unit_rows(p.S, p.H);
+    DecodeScratch sc;
+    uint8_t* ws = p.workspace + WS_HEADER;
+    sc.err = reinterpret_cast<uint32_t*>(ws);
+    ws += up256(DEC_CTAS * 4ull);
+    sc.prefix = reinterpret_cast<long long*>(ws);
+    ws += up256((p.N + 1ull) * 8ull);
+    sc.lse = reinterpret_cast<float*>(ws);
+    ws += up256(2ull * DEC_CTAS * r * 4ull);
+    sc.o = reinterpret_cast<float*>(ws);
+    DecMaps maps;
+    const int box = p.page_size < KEYS ? p.page_size : KEYS;
+    if (!latent_row_map(&maps.q, p.q, LAT_ROW, 1, (long long)p.N * p.S * p.H, LAT_ROW, r) ||
+        !latent_row_map(&maps.cache, p.cache, LAT_ROW, 1, (long long)p.num_pages * p.page_size, LAT_ROW, box))
+        return cudaErrorInvalidValue;
+    if (r == 16) return fp16 ? launch<16, true>(p, maps, sc, stream) : launch<16, false>(p, maps, sc, stream);
+    if (r == 32) return fp16 ? launch<32, true>(p, maps, sc, stream) : launch<32, false>(p, maps, sc, stream);
+    return fp16 ? launch<64, true>(p, maps, sc, stream) : launch<64, false>(p, maps, sc, stream);
 }
 
 }  // namespace kda

@@ -20,4 +20,13 @@ struct DecodeParams {
     uint32_t wait_limit;
 };
 
+constexpr int DEC_CTAS = 152;   // one a SM
+
+struct DecodeScratch {
+    uint32_t* err;              // [DEC_CTAS] status bits
+    long long* prefix;          // [N + 1] 64-key tiles before each sequence
+    float* lse;                 // [2 DEC_CTAS][rows of a unit]
+    float* o;                   // [2 DEC_CTAS][rows of a unit][512]
+};
+
 }  // namespace kda
