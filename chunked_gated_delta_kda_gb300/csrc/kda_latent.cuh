@@ -32,7 +32,7 @@ struct LatentParams {
     void* dq;
     void* dkv;
     void* dk_pe;
-    float* delta;           // backward workspace: [B*Tq, H] dout . o
+    float* aux;             // backward workspace: per (64-query tile slot, head) 64 log2 lse, 64 dout . o
     float* dpe_part;        // backward workspace: [H][B*Tk][64] per-head gradients of k_pe
     const int32_t* cu_q;    // int32 [N+1] or null
     const int32_t* cu_k;

@@ -13,6 +13,7 @@ cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t str
 cudaError_t launch_latent_bwd(const LatentParams& p, bool fp16, cudaStream_t stream);
 cudaError_t launch_latent_decode(const DecodeParams& p, bool fp16, cudaStream_t stream);
 unsigned long long latent_decode_scratch(int N, int S, int H);
+unsigned long long latent_aux_floats(int B, int Tq, int H, int N);
 }  // namespace kda
 
 namespace {
@@ -75,11 +76,11 @@ kda_status kda_latent_fwd(const void* q, const void* kv, const void* k_pe, long 
     return kda::launch_latent_fwd(p, (flags & KDA_FLAG_FP16) != 0u, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-// Header, dout . o of every query and head, the per-head gradients of k_pe.
+// Header, the queries' tables (latent_aux_kernel), the per-head gradients of k_pe.
 size_t kda_latent_bwd_workspace_bytes(int B, int Tq, int Tk, int H, int N) {
     if (!sizes_ok(B, Tq, Tk, H, N)) return 0;
-    const unsigned long long q = (unsigned long long)B * Tq * H, k = (unsigned long long)B * Tk * H;
-    return (size_t)(kda::WS_HEADER + round256(q * 4ull) + k * kda::LAT_P * 4ull);
+    return (size_t)(kda::WS_HEADER + round256(kda::latent_aux_floats(B, Tq, H, N) * 4ull) +
+                    (unsigned long long)B * Tk * H * kda::LAT_P * 4ull);
 }
 
 kda_status kda_latent_bwd(const void* q, const void* kv, const void* k_pe, long long k_pe_stride, const void* o,
@@ -108,8 +109,8 @@ kda_status kda_latent_bwd(const void* q, const void* kv, const void* k_pe, long 
     p.cu_k = cu_seqlens_k;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.status = reinterpret_cast<uint32_t*>(ws);
-    p.delta = reinterpret_cast<float*>(ws + kda::WS_HEADER);
-    p.dpe_part = reinterpret_cast<float*>(ws + kda::WS_HEADER + round256((unsigned long long)B * Tq * H * 4ull));
+    p.aux = reinterpret_cast<float*>(ws + kda::WS_HEADER);
+    p.dpe_part = reinterpret_cast<float*>(ws + kda::WS_HEADER + round256(kda::latent_aux_floats(B, Tq, H, N) * 4ull));
     p.scale = scale_of(scale);
     p.Tq = Tq;
     p.Tk = Tk;

@@ -1,126 +1,682 @@
-// Expanded latent attention, backward.  One warp per (query, head) for dq and
-// dout . o, one per (key, head) for dk and dv; the shared positional key's
-// per-head gradients go to the workspace and are summed in head order.
-#include "kda_latent.cuh"
+// Expanded latent attention, backward, in four launches:
+//   aux   D_i = dout_i . o_i and log2(e) lse_i of every query and head, laid
+//         out as the key kernel reads them
+//   dq    one CTA for 128 queries of a head, over the keys:
+//           S = Q K^T, dP = dO V^T, dS = P (dP - D), dQ += dS K
+//   dkv   one CTA for 128 keys of a head, over the queries:
+//           S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
+//   dpe   the shared positional key's gradient: the heads' parts, in order
+// with P = exp(scale S - lse), recomputed in both middle kernels: that is
+// 1152 instead of 832 multiply-adds a pair, but no gradient is summed through
+// memory by more than one CTA, so nothing is atomic and equal inputs give
+// equal bits.  All products are tcgen05 with 32-bit accumulators in tensor
+// memory.  S and dP are read to registers as soon as they are complete, so
+// that the next tile's can be issued; P and dS go back to tensor memory in
+// 16 bits as first operands.  dS is kept without the factor `scale`, which
+// the final dq and dk get in 32 bits.
+#include "kda_latent_mma.cuh"
 
 namespace kda {
 
 namespace {
 
-template <typename T>
-__global__ void latent_dq_kernel(LatentParams p) {
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr uint32_t SLAB = 64 * LAT_TILE * 2;            // 128 rows x 64 columns
+constexpr int BWD_THREADS = 320;                        // warps 0-7 elementwise, 8 products, 9 loads
+constexpr int QT = 64;                                  // queries of a dkv step
+constexpr uint32_t HSLAB = 64 * QT * 2;                 // 64 rows x 64 columns
+
+struct BwdMaps {
+    CUtensorMap q, dout, kv, pe;                        // boxes of 128 rows
+    CUtensorMap q64, dout64;                            // of 64 rows
+};
+
+// fp16 P of the key kernel carries a factor 2^8: at long lengths the weights
+// themselves would fall into fp16's subnormal range (below 6e-5).
+template <bool FP16> constexpr float P_SHIFT = FP16 ? 8.f : 0.f;
+
+// Per 64-query tile slot and head: 64 of log2(e) lse - P_SHIFT (+infinity for
+// rows past the end and rows without keys: their weights become 0), 64 of D.
+template <bool FP16>
+__global__ void __launch_bounds__(256) latent_aux_kernel(const __grid_constant__ LatentParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n, j;
-    latent_slot(p.cu_q, p.Tq, p.N, blockIdx.x, LAT_TILE, n, j);
+    latent_slot(p.cu_q, p.Tq, p.N, blockIdx.x, QT, n, j);
     LatentSeq s;
-    if (!latent_seq(p, n, s)) return;
+    if (!latent_seq(p, n, s) || j * QT >= s.lq) return;
     const int h = blockIdx.y;
-    for (int r = warp; r < LAT_TILE; r += blockDim.x >> 5) {
-        const int i = j * LAT_TILE + r;
-        if (i >= s.lq) return;
+    float* aux = p.aux + ((long long)blockIdx.x * p.H + h) * 2 * QT;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {                       // two rows a warp at a time, 16 bytes a lane
+        const int r = 2 * (8 * k + warp) + (lane >> 4);
+        const int i = j * QT + r;
         const long long row = (s.q0 + i) * p.H + h;
-        const T* q = static_cast<const T*>(p.q) + row * LAT_QK;
-        const T* dob = static_cast<const T*>(p.dout) + row * LAT_V;
-        const T* ob = static_cast<const T*>(p.o) + row * LAT_V;
-        float qv[6], dv[4], acc[6] = {}, delta = 0.f;
-        for (int e = 0; e < 6; ++e) qv[e] = to_f(q[lane + 32 * e]) * p.scale;
-        for (int e = 0; e < 4; ++e) {
-            dv[e] = to_f(dob[lane + 32 * e]);
-            delta += dv[e] * to_f(ob[lane + 32 * e]);
-        }
-        delta = warp_sum(delta);
-        if (lane == 0) p.delta[row] = delta;
-        const float lse = p.lse[row];
-        const int last = p.causal ? min(s.lk, i + s.lk - s.lq + 1) : s.lk;
-        for (int k = 0; k < last; ++k) {
-            const T* kv = static_cast<const T*>(p.kv) + ((s.k0 + k) * p.H + h) * LAT_KV;
-            const T* pe = static_cast<const T*>(p.k_pe) + (s.k0 + k) * p.k_pe_stride;
-            float x = 0.f, d = 0.f, kk[6];
-            for (int e = 0; e < 6; ++e) kk[e] = to_f(e < 4 ? kv[lane + 32 * e] : pe[lane + 32 * (e - 4)]);
-            for (int e = 0; e < 6; ++e) x += qv[e] * kk[e];
-            for (int e = 0; e < 4; ++e) d += dv[e] * to_f(kv[LAT_N + lane + 32 * e]);
-            x = warp_sum(x);
-            d = warp_sum(d);
-            const float dx = expf(x - lse) * (d - delta) * p.scale;
-            for (int e = 0; e < 6; ++e) acc[e] += dx * kk[e];
-        }
-        T* out = static_cast<T*>(p.dq) + row * LAT_QK;
-        for (int e = 0; e < 6; ++e) out[lane + 32 * e] = from_f<T>(acc[e]);
-    }
-}
-
-template <typename T>
-__global__ void latent_dkv_kernel(LatentParams p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int n, j;
-    latent_slot(p.cu_k, p.Tk, p.N, blockIdx.x, LAT_TILE, n, j);
-    LatentSeq s;
-    if (!latent_seq(p, n, s)) return;
-    const int h = blockIdx.y;
-    const long long rows = p.cu_k ? p.Tk : (long long)p.N * p.Tk;
-    for (int r = warp; r < LAT_TILE; r += blockDim.x >> 5) {
-        const int k = j * LAT_TILE + r;
-        if (k >= s.lk) return;
-        const T* kv = static_cast<const T*>(p.kv) + ((s.k0 + k) * p.H + h) * LAT_KV;
-        const T* pe = static_cast<const T*>(p.k_pe) + (s.k0 + k) * p.k_pe_stride;
-        float kk[6], vv[4], dk[6] = {}, dv[4] = {};
-        for (int e = 0; e < 6; ++e) kk[e] = to_f(e < 4 ? kv[lane + 32 * e] : pe[lane + 32 * (e - 4)]) * p.scale;
-        for (int e = 0; e < 4; ++e) vv[e] = to_f(kv[LAT_N + lane + 32 * e]);
-        const int first = p.causal ? max(0, k - (s.lk - s.lq)) : 0;
-        for (int i = first; i < s.lq; ++i) {
-            const long long row = (s.q0 + i) * p.H + h;
-            const T* q = static_cast<const T*>(p.q) + row * LAT_QK;
-            const T* dob = static_cast<const T*>(p.dout) + row * LAT_V;
-            float x = 0.f, d = 0.f, qv[6], dd[4];
-            for (int e = 0; e < 6; ++e) {
-                qv[e] = to_f(q[lane + 32 * e]);
-                x += qv[e] * kk[e];
-            }
+        float d = 0.f;
+        if (i < s.lq) {
+            const uint4 a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + row * LAT_V)[lane & 15];
+            const uint4 b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.o) + row * LAT_V)[lane & 15];
+            const uint32_t *x = &a.x, *y = &b.x;
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
-                dd[e] = to_f(dob[lane + 32 * e]);
-                d += dd[e] * vv[e];
+                const float2 u = unpack2<FP16>(x[e]), v = unpack2<FP16>(y[e]);
+                d += u.x * v.x + u.y * v.y;
             }
-            x = warp_sum(x);
-            d = warp_sum(d);
-            const float w = expf(x - p.lse[row]), dx = w * (d - p.delta[row]) * p.scale;
-            for (int e = 0; e < 4; ++e) dv[e] += w * dd[e];
-            for (int e = 0; e < 6; ++e) dk[e] += dx * qv[e];
         }
-        T* out = static_cast<T*>(p.dkv) + ((s.k0 + k) * p.H + h) * LAT_KV;
-        for (int e = 0; e < 4; ++e) {
-            out[lane + 32 * e] = from_f<T>(dk[e]);
-            out[LAT_N + lane + 32 * e] = from_f<T>(dv[e]);
+#pragma unroll
+        for (int m = 8; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+        if ((lane & 15) == 0) {
+            const float lse = i < s.lq ? p.lse[row] : -INFINITY;
+            aux[r] = lse == -INFINITY ? INFINITY : lse * LOG2E - P_SHIFT<FP16>;
+            aux[QT + r] = d;
         }
-        float* part = p.dpe_part + ((long long)h * rows + s.k0 + k) * LAT_P;
-        for (int e = 0; e < 2; ++e) part[lane + 32 * e] = dk[4 + e];
     }
 }
 
-template <typename T>
-__global__ void latent_dpe_kernel(LatentParams p, long long rows) {
-    const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= rows * LAT_P) return;
-    float sum = 0.f;
-    for (int h = 0; h < p.H; ++h) sum += p.dpe_part[h * rows * LAT_P + e];
-    static_cast<T*>(p.dk_pe)[e] = from_f<T>(sum);
+// Sixteen registers -> columns col .. col + 15 of this thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) tmem_st4(taddr + i, r[i], r[i + 1], r[i + 2], r[i + 3]);
 }
 
-template <typename T>
-cudaError_t launch(const LatentParams& p, cudaStream_t stream) {
+// ---------------------------------------------------------------------------
+// dq.  Shared memory: Q and dO (five slabs), K through a ring of seven slabs,
+// V through one of two.  K of step j is needed by S (j) and dQ (j); with the
+// order S (j + 1), dQ (j), dP (j + 1) the first slab of K (j + 2) loads while
+// S (j + 1) runs and the other two behind dP (j + 1).
+// Tensor memory: S 128 columns, dP 128, dS 64 (16-bit), dQ 192: all 512.
+// ---------------------------------------------------------------------------
+constexpr uint32_t KRING = 7, VRING = 2;
+constexpr uint32_t D_Q = 0, D_DO = 3 * SLAB, D_K = 5 * SLAB, D_V = D_K + KRING * SLAB, D_BAR = D_V + VRING * SLAB;
+constexpr uint32_t D_QFULL = D_BAR, D_DOFULL = D_QFULL + 8, D_KFULL = D_DOFULL + 8, D_KEMPTY = D_KFULL + 8 * KRING,
+                   D_VFULL = D_KEMPTY + 8 * KRING, D_VEMPTY = D_VFULL + 8 * VRING, D_SFULL = D_VEMPTY + 8 * VRING,
+                   D_PFULL = D_SFULL + 8, D_SREAD = D_PFULL + 8, D_PREAD = D_SREAD + 8, D_DSFULL = D_PREAD + 8,
+                   D_DONE = D_DSFULL + 8, D_DRAIN = D_DONE + 8, D_TMEM = D_DRAIN + 8, D_FAILED = D_TMEM + 4;
+constexpr uint32_t D_SMEM = D_FAILED + 4 + 1024;
+static_assert(D_SMEM <= 232448, "shared memory of one CTA");
+
+template <bool FP16>
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+    latent_dq_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ BwdMaps maps, int slots) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    volatile uint32_t* failed = reinterpret_cast<volatile uint32_t*>(smem + D_FAILED);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
+
+    int n, j0;
+    LatentSeq s;
+    latent_slot(p.cu_q, p.Tq, p.N, slots - 1 - (int)blockIdx.x, LAT_TILE, n, j0);
+    if (!latent_seq(p, n, s)) return;
+    const int row0 = j0 * LAT_TILE, h = blockIdx.y;
+    if (row0 >= s.lq) return;
+    const int shift = s.lk - s.lq;
+    const int most = p.causal ? min(s.lk, min(row0 + LAT_TILE, s.lq) + shift) : s.lk;
+    const int steps = most > 0 ? (most + LAT_TILE - 1) / LAT_TILE : 0;
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < KRING; ++i) mbar_init(base + D_KFULL + 8 * i, 1), mbar_init(base + D_KEMPTY + 8 * i, 1);
+        for (uint32_t i = 0; i < VRING; ++i) mbar_init(base + D_VFULL + 8 * i, 1), mbar_init(base + D_VEMPTY + 8 * i, 1);
+        mbar_init(base + D_QFULL, 1);
+        mbar_init(base + D_DOFULL, 1);
+        mbar_init(base + D_SFULL, 1);
+        mbar_init(base + D_PFULL, 1);
+        mbar_init(base + D_SREAD, 8);
+        mbar_init(base + D_PREAD, 8);
+        mbar_init(base + D_DSFULL, 8);
+        mbar_init(base + D_DONE, 1);
+        mbar_init(base + D_DRAIN, 1);
+        *failed = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(base + D_TMEM, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + D_TMEM);
+    const uint32_t t_s = tmem, t_p = tmem + 128, t_ds = tmem + 256, t_dq = tmem + 320;
+
+    if (warp == 9) {
+        if (lane == 0 && steps > 0) {
+            const int tq = (int)s.q0 + row0;
+            mbar_arrive_expect_tx(base + D_QFULL, 3 * SLAB);
+            for (uint32_t c = 0; c < 3; ++c) tma_load_3d(base + D_Q + c * SLAB, &maps.q, 64 * c, h, tq, base + D_QFULL);
+            uint32_t ik = 0, iv = 0;
+            bool ok = true;
+            for (int j = 0; j < steps && ok; ++j) {
+                const int tok = (int)s.k0 + j * LAT_TILE;
+                for (int c = 0; c < 3 && ok; ++c) {
+                    const uint32_t slot = ik % KRING, bar = base + D_KFULL + 8 * slot;
+                    if (ik >= KRING) ok = wait_phase(base + D_KEMPTY + 8 * slot, (ik / KRING - 1) & 1, limit, failed);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(bar, SLAB);
+                    if (c < 2) tma_load_3d(base + D_K + slot * SLAB, &maps.kv, 64 * c, h, tok, bar);
+                    else tma_load_3d(base + D_K + slot * SLAB, &maps.pe, 0, 0, tok, bar);
+                    ++ik;
+                }
+                if (j == 0) {
+                    mbar_arrive_expect_tx(base + D_DOFULL, 2 * SLAB);
+                    for (uint32_t c = 0; c < 2; ++c)
+                        tma_load_3d(base + D_DO + c * SLAB, &maps.dout, 64 * c, h, tq, base + D_DOFULL);
+                }
+                for (int c = 0; c < 2 && ok; ++c) {
+                    const uint32_t slot = iv % VRING, bar = base + D_VFULL + 8 * slot;
+                    if (iv >= VRING) ok = wait_phase(base + D_VEMPTY + 8 * slot, (iv / VRING - 1) & 1, limit, failed);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(bar, SLAB);
+                    tma_load_3d(base + D_V + slot * SLAB, &maps.kv, LAT_N + 64 * c, h, tok, bar);
+                    ++iv;
+                }
+            }
+            // every copy issued here has landed before the CTA ends
+            mbar_wait(base + D_QFULL, 0, DRAIN_LIMIT);
+            mbar_wait(base + D_DOFULL, 0, DRAIN_LIMIT);
+            for (uint32_t k = ik > KRING ? ik - KRING : 0; k < ik; ++k)
+                mbar_wait(base + D_KFULL + 8 * (k % KRING), (k / KRING) & 1, DRAIN_LIMIT);
+            for (uint32_t k = iv > VRING ? iv - VRING : 0; k < iv; ++k)
+                mbar_wait(base + D_VFULL + 8 * (k % VRING), (k / VRING) & 1, DRAIN_LIMIT);
+        }
+    } else if (warp == 8) {
+        const MmaType ty = FP16 ? T_F16 : T_BF16;
+        const uint32_t id = idesc_f16(ty, 128, 128, false, false), id64 = idesc_f16(ty, 128, 64, false, true);
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            return ok;
+        };
+        auto score = [&](int j) {
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                const uint32_t i = 3 * j + c, b = base + D_K + (i % KRING) * SLAB;
+                if (!wait(D_KFULL + 8 * (i % KRING), (i / KRING) & 1)) return;
+                if ((j + 1) * LAT_TILE > s.lk) {
+                    // rows past the sequence's end hold whatever follows: dS is 0 there and has to meet zeros
+                    for (int r = s.lk - j * LAT_TILE + (lane >> 3); r < LAT_TILE; r += 4)
+                        *reinterpret_cast<uint4*>(smem + (b - base) + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f16_warp(t_s, desc_k(base + D_Q + c * SLAB, LAT_TILE, ks), desc_k(b, LAT_TILE, ks), id, c + ks > 0);
+            }
+            mma_commit_warp(base + D_SFULL);
+        };
+        auto grad_p = [&](int j) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t i = 2 * j + c;
+                if (!wait(D_VFULL + 8 * (i % VRING), (i / VRING) & 1)) return;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f16_warp(t_p, desc_k(base + D_DO + c * SLAB, LAT_TILE, ks),
+                                 desc_k(base + D_V + (i % VRING) * SLAB, LAT_TILE, ks), id, c + ks > 0);
+                mma_commit_warp(base + D_VEMPTY + 8 * (i % VRING));
+            }
+            mma_commit_warp(base + D_PFULL);
+        };
+        if (steps > 0) {
+            if (wait(D_QFULL, 0)) score(0);
+            if (ok && wait(D_DOFULL, 0)) grad_p(0);
+        }
+        for (int j = 0; j < steps && ok; ++j) {
+            if (j + 1 < steps && wait(D_SREAD, j & 1)) {
+                tc_fence_after();
+                score(j + 1);
+            }
+            if (!ok || !wait(D_DSFULL, j & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {              // dQ += dS K, 64 of its columns a K slab
+                const uint32_t i = (3 * j + c) % KRING;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_f16_ts_warp(t_dq + 64 * c, t_ds + 8 * ks, desc_mn(base + D_K + i * SLAB, LAT_TILE, ks), id64,
+                                    j + ks > 0);
+                mma_commit_warp(base + D_KEMPTY + 8 * i);
+            }
+            mma_commit_warp(base + D_DONE);
+            if (j + 1 < steps && wait(D_PREAD, j & 1)) {
+                tc_fence_after();
+                grad_p(j + 1);
+            }
+        }
+        // every product issued here is done before the tensor memory is freed
+        mma_commit_warp(base + D_DRAIN);
+        mbar_wait(base + D_DRAIN, 0, DRAIN_LIMIT);
+    } else {
+        const int g = warp >> 2, row = row0 + (warp & 3) * 32 + lane;   // columns 64 g .. of S and dP
+        const uint32_t quad = (uint32_t)(warp & 3) << 21;
+        const float c = p.scale * LOG2E;
+        const int kmax = p.causal ? min(s.lk, row + shift + 1) : s.lk;
+        const long long at = (s.q0 + row) * p.H + h;
+        const bool there = row < s.lq;
+        float lse2 = INFINITY, delta = 0.f;
+        if (there) {   // the key kernel's tables: tile slot of 64 queries
+            const int slot = p.cu_q == nullptr ? n * ((p.Tq + QT - 1) / QT) + row / QT : (int)(s.q0 / QT) + n + row / QT;
+            const float* aux = p.aux + ((long long)slot * p.H + h) * 2 * QT + row % QT;
+            lse2 = aux[0] + P_SHIFT<FP16>;
+            delta = aux[QT];
+        }
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            return ok;
+        };
+        for (int j = 0; j < steps; ++j) {
+            if (!wait(D_SFULL, j & 1)) break;
+            tc_fence_after();
+            float x[2][32];
+            tmem_ld32(t_s + 64 * g + quad, x[0]);
+            tmem_ld32(t_s + 64 * g + 32 + quad, x[1]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + D_SREAD);
+            const int lim = kmax - j * LAT_TILE - 64 * g;
+            const bool cut = __any_sync(0xffffffffu, lim < 64);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e >> 5][e & 31] = ex2(fmaf(x[e >> 5][e & 31], c, -lse2));
+            if (!wait(D_PFULL, j & 1)) break;
+            tc_fence_after();
+            float w[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float d[32];
+                tmem_ld32(t_p + 64 * g + 32 * b + quad, d);
+                tmem_ld_wait();
+                if (b == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(base + D_PREAD);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) d[e] = x[b][e] * (d[e] - delta);
+                if (cut) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) d[e] = 32 * b + e < lim ? d[e] : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) w[16 * b + (e >> 1)] = __uint_as_float(pack2<FP16>(d[e], d[e + 1]));
+            }
+            if (j > 0 && !wait(D_DONE, (j - 1) & 1)) break;   // dS is free
+            tc_fence_after();
+            tmem_st32(t_ds + 32 * g + quad, w);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + D_DSFULL);
+        }
+        if (steps > 0 && ok) wait(D_DONE, (steps - 1) & 1);
+        if (ok) {
+            tc_fence_after();
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dq) + at * LAT_QK) + 12 * g;
+#pragma unroll
+            for (int b = 0; b < 3; ++b) {
+                float d[32];
+                if (steps > 0) {
+                    tmem_ld32(t_dq + 96 * g + 32 * b + quad, d);
+                    tmem_ld_wait();
+                }
+                if (there) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            r[k] = steps > 0 ? pack2<FP16>(d[e + 2 * k] * p.scale, d[e + 2 * k + 1] * p.scale) : 0u;
+                        out[4 * b + (e >> 3)] = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------
+// dk, dv.  Shared memory: K and V (five slabs), three stages of a 64-query
+// tile (Q, dO and its aux rows).  Tensor memory: S^T 64 columns, dP^T 64,
+// P^T and dS^T 32 each (16-bit), dV 128, dK 192: all 512, which is what holds
+// the query tile at 64 (S^T and dP^T then read their first operand from
+// shared memory for 64 columns only and are bound by that: about 1600 cycles
+// a 128 x 64 tile beside 1280 of arithmetic).
+// ---------------------------------------------------------------------------
+constexpr uint32_t STAGES = 3;
+constexpr uint32_t STAGE = 5 * HSLAB;
+constexpr uint32_t K_K = 0, K_V = 3 * SLAB, K_ST = 5 * SLAB, K_AUX = K_ST + STAGES * STAGE,
+                   K_BAR = K_AUX + STAGES * 2 * QT * 4;
+constexpr uint32_t K_KVFULL = K_BAR, K_FULL = K_KVFULL + 8, K_EMPTY = K_FULL + 8 * STAGES, K_SFULL = K_EMPTY + 8 * STAGES,
+                   K_DPFULL = K_SFULL + 8, K_SREAD = K_DPFULL + 8, K_DPREAD = K_SREAD + 8, K_PFULL = K_DPREAD + 8,
+                   K_DSFULL = K_PFULL + 8, K_VDONE = K_DSFULL + 8, K_KDONE = K_VDONE + 8, K_DRAIN = K_KDONE + 8,
+                   K_TMEM = K_DRAIN + 8, K_FAILED = K_TMEM + 4;
+constexpr uint32_t K_SMEM = K_FAILED + 4 + 1024;
+static_assert(K_SMEM <= 232448, "shared memory of one CTA");
+
+template <bool FP16>
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+    latent_dkv_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ BwdMaps maps) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    volatile uint32_t* failed = reinterpret_cast<volatile uint32_t*>(smem + K_FAILED);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
+
+    int n, j0;   // the first keys of a sequence are seen by the most queries: they come first
+    LatentSeq s;
+    latent_slot(p.cu_k, p.Tk, p.N, blockIdx.x, LAT_TILE, n, j0);
+    if (!latent_seq(p, n, s)) return;
+    const int key0 = j0 * LAT_TILE, h = blockIdx.y;
+    if (key0 >= s.lk) return;
+    const int shift = s.lk - s.lq;
+    const int first = p.causal ? max(0, key0 - shift) / QT : 0;         // query tile
+    const int steps = max(0, (s.lq + QT - 1) / QT - first);
+    const int slot0 = p.cu_q == nullptr ? n * ((p.Tq + QT - 1) / QT) : (int)(s.q0 / QT) + n;
+
+    if (tid == 0) {
+        mbar_init(base + K_KVFULL, 1);
+        for (uint32_t i = 0; i < STAGES; ++i) mbar_init(base + K_FULL + 8 * i, 1), mbar_init(base + K_EMPTY + 8 * i, 1);
+        mbar_init(base + K_SFULL, 1);
+        mbar_init(base + K_DPFULL, 1);
+        mbar_init(base + K_SREAD, 8);
+        mbar_init(base + K_DPREAD, 8);
+        mbar_init(base + K_PFULL, 8);
+        mbar_init(base + K_DSFULL, 8);
+        mbar_init(base + K_VDONE, 1);
+        mbar_init(base + K_KDONE, 1);
+        mbar_init(base + K_DRAIN, 1);
+        *failed = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(base + K_TMEM, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + K_TMEM);
+    const uint32_t t_s = tmem, t_dp = tmem + 64, t_p = tmem + 128, t_ds = tmem + 160, t_dv = tmem + 192, t_dk = tmem + 320;
+
+    if (warp == 9) {
+        if (lane == 0 && steps > 0) {
+            const int tk = (int)s.k0 + key0;
+            mbar_arrive_expect_tx(base + K_KVFULL, 5 * SLAB);
+            for (uint32_t c = 0; c < 2; ++c) {
+                tma_load_3d(base + K_K + c * SLAB, &maps.kv, 64 * c, h, tk, base + K_KVFULL);
+                tma_load_3d(base + K_V + c * SLAB, &maps.kv, LAT_N + 64 * c, h, tk, base + K_KVFULL);
+            }
+            tma_load_3d(base + K_K + 2 * SLAB, &maps.pe, 0, 0, tk, base + K_KVFULL);
+            uint32_t i = 0;
+            for (; i < (uint32_t)steps; ++i) {
+                const uint32_t st = i % STAGES, bar = base + K_FULL + 8 * st, dst = base + K_ST + st * STAGE;
+                if (i >= STAGES && !wait_phase(base + K_EMPTY + 8 * st, (i / STAGES - 1) & 1, limit, failed)) break;
+                const int tile = first + (int)i, tq = (int)s.q0 + tile * QT;
+                mbar_arrive_expect_tx(bar, STAGE + 2 * QT * 4);
+                for (uint32_t c = 0; c < 3; ++c) tma_load_3d(dst + c * HSLAB, &maps.q64, 64 * c, h, tq, bar);
+                for (uint32_t c = 0; c < 2; ++c) tma_load_3d(dst + (3 + c) * HSLAB, &maps.dout64, 64 * c, h, tq, bar);
+                bulk_g2s(base + K_AUX + st * 2 * QT * 4, p.aux + ((long long)(slot0 + tile) * p.H + h) * 2 * QT, 2 * QT * 4,
+                         bar);
+            }
+            // every copy issued here has landed before the CTA ends
+            mbar_wait(base + K_KVFULL, 0, DRAIN_LIMIT);
+            for (uint32_t k = i > STAGES ? i - STAGES : 0; k < i; ++k)
+                mbar_wait(base + K_FULL + 8 * (k % STAGES), (k / STAGES) & 1, DRAIN_LIMIT);
+        }
+    } else if (warp == 8) {
+        const MmaType ty = FP16 ? T_F16 : T_BF16;
+        const uint32_t id_s = idesc_f16(ty, 128, QT, false, false), id_v = idesc_f16(ty, 128, 128, false, true),
+                       id_k = idesc_f16(ty, 128, 192, false, true);
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            return ok;
+        };
+        auto stage = [&](int i) { return base + K_ST + ((uint32_t)i % STAGES) * STAGE; };
+        auto score = [&](int i) {
+            if (!wait(K_FULL + 8 * (i % STAGES), (i / STAGES) & 1)) return;
+            const int past = s.lq - (first + i) * QT;
+            if (past < QT) {
+                // rows past the sequence's end hold whatever follows: zero weights have to meet zeros
+                for (int r = past + (lane >> 3); r < QT; r += 4)
+#pragma unroll
+                    for (int c = 0; c < 5; ++c)
+                        *reinterpret_cast<uint4*>(smem + (stage(i) - base) + c * HSLAB + r * 128 + (lane & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+#pragma unroll
+            for (int ks = 0; ks < 12; ++ks)
+                mma_f16_warp(t_s, desc_k(base + K_K, LAT_TILE, ks), desc_k(stage(i), QT, ks), id_s, ks > 0);
+            mma_commit_warp(base + K_SFULL);
+        };
+        auto grad_p = [&](int i) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                mma_f16_warp(t_dp, desc_k(base + K_V, LAT_TILE, ks), desc_k(stage(i) + 3 * HSLAB, QT, ks), id_s, ks > 0);
+            mma_commit_warp(base + K_DPFULL);
+        };
+        if (steps > 0 && wait(K_KVFULL, 0)) {
+            score(0);
+            if (ok) grad_p(0);
+        }
+        for (int i = 0; i < steps && ok; ++i) {
+            if (i + 1 < steps) {
+                if (!wait(K_SREAD, i & 1)) break;
+                tc_fence_after();
+                score(i + 1);
+                if (!ok || !wait(K_DPREAD, i & 1)) break;
+                tc_fence_after();
+                grad_p(i + 1);
+            }
+            if (!wait(K_PFULL, i & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                mma_f16_ts_warp(t_dv, t_p + 8 * ks, desc_mn(stage(i) + 3 * HSLAB, QT, ks), id_v, i + ks > 0);
+            mma_commit_warp(base + K_VDONE);
+            if (!wait(K_DSFULL, i & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                mma_f16_ts_warp(t_dk, t_ds + 8 * ks, desc_mn(stage(i), QT, ks), id_k, i + ks > 0);
+            mma_commit_warp(base + K_KDONE);
+            mma_commit_warp(base + K_EMPTY + 8 * (i % STAGES));
+        }
+        // every product issued here is done before the tensor memory is freed
+        mma_commit_warp(base + K_DRAIN);
+        mbar_wait(base + K_DRAIN, 0, DRAIN_LIMIT);
+    } else {
+        const int g = warp >> 2, key = key0 + (warp & 3) * 32 + lane;   // queries 32 g .. of a tile
+        const uint32_t quad = (uint32_t)(warp & 3) << 21;
+        const float c = p.scale * LOG2E;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            return ok;
+        };
+        for (int i = 0; i < steps; ++i) {
+            const uint32_t st = (uint32_t)i % STAGES;
+            if (!wait(K_FULL + 8 * st, (i / STAGES) & 1) || !wait(K_SFULL, i & 1)) break;
+            tc_fence_after();
+            const float4* aux = reinterpret_cast<const float4*>(smem + K_AUX + st * 2 * QT * 4) + 8 * g;
+            float x[32];
+            tmem_ld32(t_s + 32 * g + quad, x);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + K_SREAD);
+            // query e of these 32 sees this key iff e >= lo
+            const int lo = p.causal ? key - shift - (first + i) * QT - 32 * g : 0;
+            const bool cut = __any_sync(0xffffffffu, lo > 0);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4 l = aux[e >> 2];
+                x[e] = ex2(fmaf(x[e], c, -l.x));
+                x[e + 1] = ex2(fmaf(x[e + 1], c, -l.y));
+                x[e + 2] = ex2(fmaf(x[e + 2], c, -l.z));
+                x[e + 3] = ex2(fmaf(x[e + 3], c, -l.w));
+            }
+            if (cut) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = e >= lo ? x[e] : 0.f;
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) w[e >> 1] = pack2<FP16>(x[e], x[e + 1]);
+            if (i > 0 && !wait(K_VDONE, (i - 1) & 1)) break;   // P is free
+            tc_fence_after();
+            tmem_st16(t_p + 16 * g + quad, w);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + K_PFULL);
+            if (!wait(K_DPFULL, i & 1)) break;
+            tc_fence_after();
+            float d[32];
+            tmem_ld32(t_dp + 32 * g + quad, d);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + K_DPREAD);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4 l = aux[2 * QT / 8 + (e >> 2)];
+                d[e] = x[e] * (d[e] - l.x);
+                d[e + 1] = x[e + 1] * (d[e + 1] - l.y);
+                d[e + 2] = x[e + 2] * (d[e + 2] - l.z);
+                d[e + 3] = x[e + 3] * (d[e + 3] - l.w);
+            }
+            if constexpr (FP16) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) d[e] *= 0.00390625f;      // 2^-P_SHIFT
+            }
+            if (cut) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) d[e] = e >= lo ? d[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) w[e >> 1] = pack2<FP16>(d[e], d[e + 1]);
+            if (i > 0 && !wait(K_KDONE, (i - 1) & 1)) break;   // dS is free
+            tc_fence_after();
+            tmem_st16(t_ds + 16 * g + quad, w);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + K_DSFULL);
+        }
+        if (steps > 0 && ok) wait(K_KDONE, (steps - 1) & 1);
+        if (ok) {
+            tc_fence_after();
+            const long long rows = p.cu_k != nullptr ? p.Tk : (long long)p.N * p.Tk;
+            const bool there = key < s.lk;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dkv) + ((s.k0 + key) * p.H + h) * LAT_KV) +
+                         (g == 0 ? LAT_N / 8 : 0);
+            float4* part = reinterpret_cast<float4*>(p.dpe_part + (h * rows + s.k0 + key) * LAT_P);
+            const float f = g == 0 ? (FP16 ? 0.00390625f : 1.f) : p.scale;
+            const uint32_t src = (g == 0 ? t_dv : t_dk) + quad;
+#pragma unroll 1
+            for (int b = 0; b < (g == 0 ? 4 : 6); ++b) {
+                float d[32];
+                if (steps > 0) {
+                    tmem_ld32(src + 32 * b, d);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) d[e] = steps > 0 ? d[e] * f : 0.f;
+                if (there && b < 4) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        out[4 * b + (e >> 3)] =
+                            make_uint4(pack2<FP16>(d[e], d[e + 1]), pack2<FP16>(d[e + 2], d[e + 3]),
+                                       pack2<FP16>(d[e + 4], d[e + 5]), pack2<FP16>(d[e + 6], d[e + 7]));
+                } else if (there) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        part[8 * (b - 4) + (e >> 2)] = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
+}
+
+template <bool FP16>
+__global__ void __launch_bounds__(256) latent_dpe_kernel(const __grid_constant__ LatentParams p, long long quads) {
+    const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= quads) return;
+    const float4* part = reinterpret_cast<const float4*>(p.dpe_part) + e;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int h = 0; h < p.H; ++h) {
+        const float4 v = part[h * quads];
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+    }
+    static_cast<uint2*>(p.dk_pe)[e] = make_uint2(pack2<FP16>(sum.x, sum.y), pack2<FP16>(sum.z, sum.w));
+}
+
+template <bool FP16>
+cudaError_t launch(const LatentParams& p, const BwdMaps& maps, cudaStream_t stream) {
     const bool varlen = p.cu_q != nullptr;
-    const long long rows = varlen ? p.Tk : (long long)p.N * p.Tk;
-    if (const int slots = latent_slots(varlen, p.Tq, p.N, LAT_TILE))
-        latent_dq_kernel<T><<<dim3(slots, p.H), 256, 0, stream>>>(p);
-    if (const int slots = latent_slots(varlen, p.Tk, p.N, LAT_TILE))
-        latent_dkv_kernel<T><<<dim3(slots, p.H), 256, 0, stream>>>(p);
-    if (rows) latent_dpe_kernel<T><<<(unsigned)((rows * LAT_P + 255) / 256), 256, 0, stream>>>(p, rows);
+    cudaError_t e = cudaFuncSetAttribute(latent_dq_kernel<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)D_SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(latent_dkv_kernel<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K_SMEM);
+    if (e != cudaSuccess) return e;
+    if (p.Tq > 0) {
+        latent_aux_kernel<FP16><<<dim3(latent_slots(varlen, p.Tq, p.N, QT), p.H), 256, 0, stream>>>(p);
+        const int slots = latent_slots(varlen, p.Tq, p.N, LAT_TILE);
+        latent_dq_kernel<FP16><<<dim3(slots, p.H), BWD_THREADS, D_SMEM, stream>>>(p, maps, slots);
+    }
+    if (p.Tk > 0) {
+        latent_dkv_kernel<FP16><<<dim3(latent_slots(varlen, p.Tk, p.N, LAT_TILE), p.H), BWD_THREADS, K_SMEM, stream>>>(p, maps);
+        const long long quads = (varlen ? p.Tk : (long long)p.N * p.Tk) * (LAT_P / 4);
+        latent_dpe_kernel<FP16><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(p, quads);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
+// Floats of the tables that latent_aux_kernel writes.
+unsigned long long latent_aux_floats(int B, int Tq, int H, int N) {
+    const int varlen = latent_slots(true, Tq, N, QT), fixed = latent_slots(false, Tq, B, QT);
+    return (unsigned long long)(varlen > fixed ? varlen : fixed) * H * 2ull * QT;
+}
+
 cudaError_t launch_latent_bwd(const LatentParams& p, bool fp16, cudaStream_t stream) {
-    return fp16 ? launch<__half>(p, stream) : launch<__nv_bfloat16>(p, stream);
+    const bool varlen = p.cu_q != nullptr;
+    const long long rows_q = varlen ? p.Tq : (long long)p.N * p.Tq, rows_k = varlen ? p.Tk : (long long)p.N * p.Tk;
+    // without rows on one side nothing is loaded from it: any valid tensor does
+    const void* any = rows_q > 0 ? p.q : p.kv;
+    if (rows_q == 0 && rows_k == 0) return cudaSuccess;
+    const void* q = rows_q > 0 ? p.q : any;
+    const void* dout = rows_q > 0 ? p.dout : any;
+    const void* kv = rows_k > 0 ? p.kv : any;
+    const void* pe = rows_k > 0 ? p.k_pe : any;
+    const long long tq = rows_q > 0 ? rows_q : 1, tk = rows_k > 0 ? rows_k : 1;
+    BwdMaps maps;
+    if (!latent_row_map(&maps.q, q, LAT_QK, p.H, tq, (long long)p.H * LAT_QK, LAT_TILE) ||
+        !latent_row_map(&maps.dout, dout, LAT_V, p.H, tq, (long long)p.H * LAT_V, LAT_TILE) ||
+        !latent_row_map(&maps.kv, kv, LAT_KV, p.H, tk, (long long)p.H * LAT_KV, LAT_TILE) ||
+        !latent_row_map(&maps.pe, pe, LAT_P, 1, tk, p.k_pe_stride, LAT_TILE) ||
+        !latent_row_map(&maps.q64, q, LAT_QK, p.H, tq, (long long)p.H * LAT_QK, QT) ||
+        !latent_row_map(&maps.dout64, dout, LAT_V, p.H, tq, (long long)p.H * LAT_V, QT))
+        return cudaErrorInvalidValue;
+    return fp16 ? launch<true>(p, maps, stream) : launch<false>(p, maps, stream);
 }
 
 }  // namespace kda
