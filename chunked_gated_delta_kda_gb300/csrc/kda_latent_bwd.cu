@@ -85,10 +85,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 // S (j + 1) runs and the other two behind dP (j + 1).
 // Tensor memory: S 128 columns, dP 128, dS 64 (16-bit), dQ 192: all 512.
 // ---------------------------------------------------------------------------
-constexpr uint32_t KRING = 7, VRING = 2;
-constexpr uint32_t D_Q = 0, D_DO = 3 * SLAB, D_K = 5 * SLAB, D_V = D_K + KRING * SLAB, D_BAR = D_V + VRING * SLAB;
-constexpr uint32_t D_QFULL = D_BAR, D_DOFULL = D_QFULL + 8, D_KFULL = D_DOFULL + 8, D_KEMPTY = D_KFULL + 8 * KRING,
-                   D_VFULL = D_KEMPTY + 8 * KRING, D_VEMPTY = D_VFULL + 8 * VRING, D_SFULL = D_VEMPTY + 8 * VRING,
+constexpr uint32_t KRING = 7;
+constexpr uint32_t D_Q = 0, D_DO = 3 * SLAB, D_K = 5 * SLAB, D_V = D_K + KRING * SLAB, D_BAR = D_V + 2 * SLAB;
+constexpr uint32_t D_QFULL = D_BAR, D_DOFULL = D_QFULL + 8, D_KFULL = D_DOFULL + 8 /* [2]: first slab */,
+                   D_KREST = D_KFULL + 16 /* [2]: the other two */, D_VFULL = D_KREST + 16, D_SFULL = D_VFULL + 8,
                    D_PFULL = D_SFULL + 8, D_SREAD = D_PFULL + 8, D_PREAD = D_SREAD + 8, D_DSFULL = D_PREAD + 8,
                    D_DONE = D_DSFULL + 8, D_DRAIN = D_DONE + 8, D_TMEM = D_DRAIN + 8, D_FAILED = D_TMEM + 4;
 constexpr uint32_t D_SMEM = D_FAILED + 4 + 1024;
@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const int steps = most > 0 ? (most + LAT_TILE - 1) / LAT_TILE : 0;
 
     if (tid == 0) {
-        for (uint32_t i = 0; i < KRING; ++i) mbar_init(base + D_KFULL + 8 * i, 1), mbar_init(base + D_KEMPTY + 8 * i, 1);
-        for (uint32_t i = 0; i < VRING; ++i) mbar_init(base + D_VFULL + 8 * i, 1), mbar_init(base + D_VEMPTY + 8 * i, 1);
+        for (uint32_t i = 0; i < 2; ++i) mbar_init(base + D_KFULL + 8 * i, 1), mbar_init(base + D_KREST + 8 * i, 1);
+        mbar_init(base + D_VFULL, 1);
         mbar_init(base + D_QFULL, 1);
         mbar_init(base + D_DOFULL, 1);
         mbar_init(base + D_SFULL, 1);
@@ -144,54 +144,50 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             const int tq = (int)s.q0 + row0;
             mbar_arrive_expect_tx(base + D_QFULL, 3 * SLAB);
             for (uint32_t c = 0; c < 3; ++c) tma_load_3d(base + D_Q + c * SLAB, &maps.q, 64 * c, h, tq, base + D_QFULL);
-            uint32_t ik = 0, iv = 0;
-            bool ok = true;
-            for (int j = 0; j < steps && ok; ++j) {
-                const int tok = (int)s.k0 + j * LAT_TILE;
-                for (int c = 0; c < 3 && ok; ++c) {
-                    const uint32_t slot = ik % KRING, bar = base + D_KFULL + 8 * slot;
-                    if (ik >= KRING) ok = wait_phase(base + D_KEMPTY + 8 * slot, (ik / KRING - 1) & 1, limit, failed);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(bar, SLAB);
-                    if (c < 2) tma_load_3d(base + D_K + slot * SLAB, &maps.kv, 64 * c, h, tok, bar);
-                    else tma_load_3d(base + D_K + slot * SLAB, &maps.pe, 0, 0, tok, bar);
-                    ++ik;
-                }
-                if (j == 0) {
-                    mbar_arrive_expect_tx(base + D_DOFULL, 2 * SLAB);
+            mbar_arrive_expect_tx(base + D_DOFULL, 2 * SLAB);
+            // K slab i takes the place of slab i - 7: the first of step j that of K (j - 3)'s last, which was waited
+            // for in step j - 1, the others those of K (j - 2)'s first two, which dQ frees; dP (j - 1) frees V.
+            int a = 0, r = 0, v = 0;   // first slabs, other slabs and V tiles asked for
+            for (int j = 0; j < steps; ++j) {
+                const int tok = (int)s.k0 + j * LAT_TILE, st = j & 1;
+                auto k_slab = [&](int c) { return base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB; };
+                mbar_arrive_expect_tx(base + D_KFULL + 8 * st, SLAB);
+                tma_load_3d(k_slab(0), &maps.kv, 0, h, tok, base + D_KFULL + 8 * st);
+                ++a;
+                if (j >= 2 && !wait_phase(base + D_DONE, (j - 2) & 1, limit, failed)) break;
+                mbar_arrive_expect_tx(base + D_KREST + 8 * st, 2 * SLAB);
+                tma_load_3d(k_slab(1), &maps.kv, 64, h, tok, base + D_KREST + 8 * st);
+                tma_load_3d(k_slab(2), &maps.pe, 0, 0, tok, base + D_KREST + 8 * st);
+                ++r;
+                if (j == 0)
                     for (uint32_t c = 0; c < 2; ++c)
                         tma_load_3d(base + D_DO + c * SLAB, &maps.dout, 64 * c, h, tq, base + D_DOFULL);
-                }
-                for (int c = 0; c < 2 && ok; ++c) {
-                    const uint32_t slot = iv % VRING, bar = base + D_VFULL + 8 * slot;
-                    if (iv >= VRING) ok = wait_phase(base + D_VEMPTY + 8 * slot, (iv / VRING - 1) & 1, limit, failed);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(bar, SLAB);
-                    tma_load_3d(base + D_V + slot * SLAB, &maps.kv, LAT_N + 64 * c, h, tok, bar);
-                    ++iv;
-                }
+                if (j >= 1 && !wait_phase(base + D_PFULL, (j - 1) & 1, limit, failed)) break;
+                mbar_arrive_expect_tx(base + D_VFULL, 2 * SLAB);
+                for (uint32_t c = 0; c < 2; ++c)
+                    tma_load_3d(base + D_V + c * SLAB, &maps.kv, LAT_N + 64 * c, h, tok, base + D_VFULL);
+                ++v;
             }
             // every copy issued here has landed before the CTA ends
             mbar_wait(base + D_QFULL, 0, DRAIN_LIMIT);
             mbar_wait(base + D_DOFULL, 0, DRAIN_LIMIT);
-            for (uint32_t k = ik > KRING ? ik - KRING : 0; k < ik; ++k)
-                mbar_wait(base + D_KFULL + 8 * (k % KRING), (k / KRING) & 1, DRAIN_LIMIT);
-            for (uint32_t k = iv > VRING ? iv - VRING : 0; k < iv; ++k)
-                mbar_wait(base + D_VFULL + 8 * (k % VRING), (k / VRING) & 1, DRAIN_LIMIT);
+            for (int k = max(0, a - 2); k < a; ++k) mbar_wait(base + D_KFULL + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
+            for (int k = max(0, r - 2); k < r; ++k) mbar_wait(base + D_KREST + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
+            if (v > 0) mbar_wait(base + D_VFULL, (v - 1) & 1, DRAIN_LIMIT);
         }
     } else if (warp == 8) {
         const MmaType ty = FP16 ? T_F16 : T_BF16;
         const uint32_t id = idesc_f16(ty, 128, 128, false, false), id64 = idesc_f16(ty, 128, 64, false, true);
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            ok = ok && wait_warp(base + bar, parity, limit, failed);
             return ok;
         };
         auto score = [&](int j) {
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
-                const uint32_t i = 3 * j + c, b = base + D_K + (i % KRING) * SLAB;
-                if (!wait(D_KFULL + 8 * (i % KRING), (i / KRING) & 1)) return;
+                const uint32_t b = base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB;
+                if (c < 2 && !wait((c == 0 ? D_KFULL : D_KREST) + 8 * (j & 1), (j >> 1) & 1)) return;
                 if ((j + 1) * LAT_TILE > s.lk) {
                     // rows past the sequence's end hold whatever follows: dS is 0 there and has to meet zeros
                     for (int r = s.lk - j * LAT_TILE + (lane >> 3); r < LAT_TILE; r += 4)
@@ -199,22 +195,19 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     fence_async_smem();
                     __syncwarp();
                 }
+                const Desc da = desc_k(base + D_Q + c * SLAB), db = desc_k(b);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_warp(t_s, desc_k(base + D_Q + c * SLAB, LAT_TILE, ks), desc_k(b, LAT_TILE, ks), id, c + ks > 0);
+                for (int ks = 0; ks < 4; ++ks) mma_ss(t_s, da + 2 * ks, db + 2 * ks, id, c + ks > 0);
             }
             mma_commit_warp(base + D_SFULL);
         };
         auto grad_p = [&](int j) {
+            if (!wait(D_VFULL, j & 1)) return;
+            const Desc da = desc_k(base + D_DO), db = desc_k(base + D_V);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const uint32_t i = 2 * j + c;
-                if (!wait(D_VFULL + 8 * (i % VRING), (i / VRING) & 1)) return;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_warp(t_p, desc_k(base + D_DO + c * SLAB, LAT_TILE, ks),
-                                 desc_k(base + D_V + (i % VRING) * SLAB, LAT_TILE, ks), id, c + ks > 0);
-                mma_commit_warp(base + D_VEMPTY + 8 * (i % VRING));
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t at = (ks >> 2) * (SLAB / 16) + (ks & 3) * 2;
+                mma_ss(t_p, da + at, db + at, id, ks > 0);
             }
             mma_commit_warp(base + D_PFULL);
         };
@@ -231,12 +224,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 3; ++c) {              // dQ += dS K, 64 of its columns a K slab
-                const uint32_t i = (3 * j + c) % KRING;
+                const Desc db = desc_mn(base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB, LAT_TILE);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_f16_ts_warp(t_dq + 64 * c, t_ds + 8 * ks, desc_mn(base + D_K + i * SLAB, LAT_TILE, ks), id64,
-                                    j + ks > 0);
-                mma_commit_warp(base + D_KEMPTY + 8 * i);
+                for (int ks = 0; ks < 8; ++ks) mma_ts(t_dq + 64 * c, t_ds + 8 * ks, db + 128 * ks, id64, j + ks > 0);
             }
             mma_commit_warp(base + D_DONE);
             if (j + 1 < steps && wait(D_PREAD, j & 1)) {
@@ -263,7 +253,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         }
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            ok = ok && wait_warp(base + bar, parity, limit, failed);
             return ok;
         };
         for (int j = 0; j < steps; ++j) {
@@ -352,9 +342,9 @@ constexpr uint32_t STAGES = 3;
 constexpr uint32_t STAGE = 5 * HSLAB;
 constexpr uint32_t K_K = 0, K_V = 3 * SLAB, K_ST = 5 * SLAB, K_AUX = K_ST + STAGES * STAGE,
                    K_BAR = K_AUX + STAGES * 2 * QT * 4;
-constexpr uint32_t K_KVFULL = K_BAR, K_FULL = K_KVFULL + 8, K_EMPTY = K_FULL + 8 * STAGES, K_SFULL = K_EMPTY + 8 * STAGES,
+constexpr uint32_t K_KVFULL = K_BAR, K_FULL = K_KVFULL + 8, K_KDONE = K_FULL + 8 * STAGES, K_SFULL = K_KDONE + 8 * STAGES,
                    K_DPFULL = K_SFULL + 8, K_SREAD = K_DPFULL + 8, K_DPREAD = K_SREAD + 8, K_PFULL = K_DPREAD + 8,
-                   K_DSFULL = K_PFULL + 8, K_VDONE = K_DSFULL + 8, K_KDONE = K_VDONE + 8, K_DRAIN = K_KDONE + 8,
+                   K_DSFULL = K_PFULL + 8, K_DRAIN = K_DSFULL + 8,
                    K_TMEM = K_DRAIN + 8, K_FAILED = K_TMEM + 4;
 constexpr uint32_t K_SMEM = K_FAILED + 4 + 1024;
 static_assert(K_SMEM <= 232448, "shared memory of one CTA");
@@ -382,15 +372,13 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 
     if (tid == 0) {
         mbar_init(base + K_KVFULL, 1);
-        for (uint32_t i = 0; i < STAGES; ++i) mbar_init(base + K_FULL + 8 * i, 1), mbar_init(base + K_EMPTY + 8 * i, 1);
+        for (uint32_t i = 0; i < STAGES; ++i) mbar_init(base + K_FULL + 8 * i, 1), mbar_init(base + K_KDONE + 8 * i, 1);
         mbar_init(base + K_SFULL, 1);
         mbar_init(base + K_DPFULL, 1);
         mbar_init(base + K_SREAD, 8);
         mbar_init(base + K_DPREAD, 8);
         mbar_init(base + K_PFULL, 8);
         mbar_init(base + K_DSFULL, 8);
-        mbar_init(base + K_VDONE, 1);
-        mbar_init(base + K_KDONE, 1);
         mbar_init(base + K_DRAIN, 1);
         *failed = 0u;
         fence_mbar_init();
@@ -417,7 +405,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             uint32_t i = 0;
             for (; i < (uint32_t)steps; ++i) {
                 const uint32_t st = i % STAGES, bar = base + K_FULL + 8 * st, dst = base + K_ST + st * STAGE;
-                if (i >= STAGES && !wait_phase(base + K_EMPTY + 8 * st, (i / STAGES - 1) & 1, limit, failed)) break;
+                if (i >= STAGES && !wait_phase(base + K_KDONE + 8 * st, (i / STAGES - 1) & 1, limit, failed)) break;
                 const int tile = first + (int)i, tq = (int)s.q0 + tile * QT;
                 mbar_arrive_expect_tx(bar, STAGE + 2 * QT * 4);
                 for (uint32_t c = 0; c < 3; ++c) tma_load_3d(dst + c * HSLAB, &maps.q64, 64 * c, h, tq, bar);
@@ -436,7 +424,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                        id_k = idesc_f16(ty, 128, 192, false, true);
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            ok = ok && wait_warp(base + bar, parity, limit, failed);
             return ok;
         };
         auto stage = [&](int i) { return base + K_ST + ((uint32_t)i % STAGES) * STAGE; };
@@ -453,15 +441,19 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                 fence_async_smem();
                 __syncwarp();
             }
+            const Desc a = desc_k(base + K_K), b = desc_k(stage(i));
 #pragma unroll
             for (int ks = 0; ks < 12; ++ks)
-                mma_f16_warp(t_s, desc_k(base + K_K, LAT_TILE, ks), desc_k(stage(i), QT, ks), id_s, ks > 0);
+                mma_ss(t_s, a + ((ks >> 2) * (SLAB / 16) + (ks & 3) * 2), b + ((ks >> 2) * (HSLAB / 16) + (ks & 3) * 2), id_s,
+                       ks > 0);
             mma_commit_warp(base + K_SFULL);
         };
         auto grad_p = [&](int i) {
+            const Desc a = desc_k(base + K_V), b = desc_k(stage(i) + 3 * HSLAB);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-                mma_f16_warp(t_dp, desc_k(base + K_V, LAT_TILE, ks), desc_k(stage(i) + 3 * HSLAB, QT, ks), id_s, ks > 0);
+                mma_ss(t_dp, a + ((ks >> 2) * (SLAB / 16) + (ks & 3) * 2), b + ((ks >> 2) * (HSLAB / 16) + (ks & 3) * 2), id_s,
+                       ks > 0);
             mma_commit_warp(base + K_DPFULL);
         };
         if (steps > 0 && wait(K_KVFULL, 0)) {
@@ -469,27 +461,27 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             if (ok) grad_p(0);
         }
         for (int i = 0; i < steps && ok; ++i) {
-            if (i + 1 < steps) {
+            const bool more = i + 1 < steps;
+            if (more) {
                 if (!wait(K_SREAD, i & 1)) break;
                 tc_fence_after();
                 score(i + 1);
-                if (!ok || !wait(K_DPREAD, i & 1)) break;
+            }
+            if (!ok || !wait(K_PFULL, i & 1)) break;
+            tc_fence_after();
+            const Desc bv = desc_mn(stage(i) + 3 * HSLAB, QT), bk = desc_mn(stage(i), QT);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) mma_ts(t_dv, t_p + 8 * ks, bv + 128 * ks, id_v, i + ks > 0);
+            if (more) {
+                if (!wait(K_DPREAD, i & 1)) break;
                 tc_fence_after();
                 grad_p(i + 1);
             }
-            if (!wait(K_PFULL, i & 1)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_f16_ts_warp(t_dv, t_p + 8 * ks, desc_mn(stage(i) + 3 * HSLAB, QT, ks), id_v, i + ks > 0);
-            mma_commit_warp(base + K_VDONE);
             if (!wait(K_DSFULL, i & 1)) break;
             tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_f16_ts_warp(t_dk, t_ds + 8 * ks, desc_mn(stage(i), QT, ks), id_k, i + ks > 0);
-            mma_commit_warp(base + K_KDONE);
-            mma_commit_warp(base + K_EMPTY + 8 * (i % STAGES));
+            for (int ks = 0; ks < 4; ++ks) mma_ts(t_dk, t_ds + 8 * ks, bk + 128 * ks, id_k, i + ks > 0);
+            mma_commit_warp(base + K_KDONE + 8 * (i % STAGES));
         }
         // every product issued here is done before the tensor memory is freed
         mma_commit_warp(base + K_DRAIN);
@@ -500,7 +492,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         const float c = p.scale * LOG2E;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && wait_phase(base + bar, parity, limit, failed));
+            ok = ok && wait_warp(base + bar, parity, limit, failed);
             return ok;
         };
         for (int i = 0; i < steps; ++i) {
@@ -532,7 +524,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) w[e >> 1] = pack2<FP16>(x[e], x[e + 1]);
-            if (i > 0 && !wait(K_VDONE, (i - 1) & 1)) break;   // P is free
+            // P and dS are free once the step before is done
+            if (i > 0 && !wait(K_KDONE + 8 * ((i - 1) % STAGES), ((i - 1) / STAGES) & 1)) break;
             tc_fence_after();
             tmem_st16(t_p + 16 * g + quad, w);
             tmem_st_wait();
@@ -565,15 +558,13 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             }
 #pragma unroll
             for (int e = 0; e < 32; e += 2) w[e >> 1] = pack2<FP16>(d[e], d[e + 1]);
-            if (i > 0 && !wait(K_KDONE, (i - 1) & 1)) break;   // dS is free
-            tc_fence_after();
             tmem_st16(t_ds + 16 * g + quad, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(base + K_DSFULL);
         }
-        if (steps > 0 && ok) wait(K_KDONE, (steps - 1) & 1);
+        if (steps > 0 && ok) wait(K_KDONE + 8 * ((steps - 1) % STAGES), ((steps - 1) / STAGES) & 1);
         if (ok) {
             tc_fence_after();
             const long long rows = p.cu_k != nullptr ? p.Tk : (long long)p.N * p.Tk;

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
         uint32_t ip = 0, ie = 0, seg = 0;              // pairs, positional slabs and queries asked for
         bool ok = true;
         for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts)) {
-            if (seg > 0) ok = __all_sync(0xffffffffu, wait_phase(base + L::QEMPTY, (seg - 1) & 1, limit, failed));
+            if (seg > 0) ok = wait_warp(base + L::QEMPTY, (seg - 1) & 1, limit, failed);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(base + L::QFULL, 9 * R * 128);
             __syncwarp();
@@ -266,9 +266,8 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     const uint32_t i = c < 4 ? ip : ie, depth = c < 4 ? L::NP : L::NE;
                     const uint32_t full = base + (c < 4 ? L::PFULL : L::EFULL) + 8 * (i % depth);
                     if (i >= depth)
-                        ok = __all_sync(0xffffffffu,
-                                        wait_phase(base + (c < 4 ? L::PEMPTY : L::EEMPTY) + 8 * (i % depth),
-                                                   (i / depth - 1) & 1, limit, failed));
+                        ok = wait_warp(base + (c < 4 ? L::PEMPTY : L::EEMPTY) + 8 * (i % depth), (i / depth - 1) & 1, limit,
+                                       failed);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)box * (c < 4 ? 256u : 128u));
                     __syncwarp();
@@ -299,21 +298,21 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 5; ++c) {
                 const uint32_t i = c < 4 ? 4 * t + c : t, depth = c < 4 ? L::NP : L::NE;
-                ok = __all_sync(0xffffffffu, ok && wait_phase(base + (c < 4 ? L::PFULL : L::EFULL) + 8 * (i % depth),
-                                                              (i / depth) & 1, limit, failed));
+                ok = ok && wait_warp(base + (c < 4 ? L::PFULL : L::EFULL) + 8 * (i % depth), (i / depth) & 1, limit, failed);
                 if (!ok) return;
-                const uint32_t b = base + (c < 4 ? L::RP + (i % depth) * PAIR : L::RE + (i % depth) * PE);
+                const Desc a = desc_k(base + L::Q + 2 * c * R * 128);
+                const Desc b = desc_k(base + (c < 4 ? L::RP + (i % depth) * PAIR : L::RE + (i % depth) * PE));
 #pragma unroll
                 for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks)
-                    mma_f16_warp(t_s + 64 * (t & 1), desc_k(base + L::Q + 2 * c * R * 128, R, ks), desc_k(b, KEYS, ks), id_s,
-                                 c + ks > 0);
+                    mma_ss(t_s + 64 * (t & 1), a + ((ks >> 2) * (R * 8) + (ks & 3) * 2), b + ((ks >> 2) * (KEYS * 8) + (ks & 3) * 2),
+                           id_s, c + ks > 0);
             }
             mma_commit_warp(base + L::SFULL + 8 * (t & 1));
             mma_commit_warp(base + L::EEMPTY + 8 * (t % L::NE));
         };
         for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts), ++seg) {
             const bool gaps = bad_pages(p, w, lane);
-            ok = __all_sync(0xffffffffu, wait_phase(base + L::QFULL, seg & 1, limit, failed));
+            ok = wait_warp(base + L::QFULL, seg & 1, limit, failed);
             if (ok) score(g);
             if (ok && w.cnt == 1) mma_commit_warp(base + L::QEMPTY);
             for (int k = 0; k < w.cnt && ok; ++k, ++g) {
@@ -321,9 +320,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     score(g + 1);
                     if (ok && k + 2 == w.cnt) mma_commit_warp(base + L::QEMPTY);
                 }
-                ok = __all_sync(0xffffffffu, ok && wait_phase(base + L::WFULL, g & 1, limit, failed));
+                ok = ok && wait_warp(base + L::WFULL, g & 1, limit, failed);
                 if (ok && k == 0 && seg > 0)
-                    ok = __all_sync(0xffffffffu, wait_phase(base + L::OFREE, (seg - 1) & 1, limit, failed));
+                    ok = wait_warp(base + L::OFREE, (seg - 1) & 1, limit, failed);
                 if (!ok) break;
                 tc_fence_after();
                 const int tile = w.k0 + k;
@@ -342,10 +341,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {          // O^T: channels 128 c ..
                     const uint32_t i = (4 * g + c) % L::NP;
+                    const Desc a = desc_mn(base + L::RP + i * PAIR, KEYS), b = desc_k(base + L::P);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_warp(tmem + c * R, desc_mn(base + L::RP + i * PAIR, KEYS, ks),
-                                     desc_k(base + L::P, R, ks), id_o, k + ks > 0);
+                    for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + c * R, a + 128 * ks, b + 2 * ks, id_o, k + ks > 0);
                     mma_commit_warp(base + L::PEMPTY + 8 * i);
                 }
                 mma_commit_warp(base + L::VDONE);
@@ -368,7 +366,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             const int lim = w.len - p.S + 1 + min(gr, rows - 1) / p.H;   // keys [0, lim) are seen
             float m = -INFINITY, l = 0.f;
             for (int k = 0; k < w.cnt && ok; ++k, ++g) {
-                ok = bar_and_named(1, 128, wait_phase(base + L::SFULL + 8 * (g & 1), g >> 1 & 1, limit, failed));
+                ok = bar_and_named(1, 128, wait_warp(base + L::SFULL + 8 * (g & 1), g >> 1 & 1, limit, failed));
                 if (!ok) break;
                 tc_fence_after();
                 const int tile = w.k0 + k;
@@ -390,7 +388,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 bool grown = top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m);
                 grown = grown && r < R && lane < 16;
                 // P's buffer is free, and O stands still, once the tile before is done
-                if (k > 0) ok = wait_phase(base + L::VDONE, (g - 1) & 1, limit, failed);
+                if (k > 0) ok = wait_warp(base + L::VDONE, (g - 1) & 1, limit, failed);
                 if (!bar_and_named(1, 128, ok && !grown)) {
                     ok = bar_and_named(1, 128, ok);
                     if (!ok) break;
@@ -440,7 +438,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(base + L::WFULL);
             }
-            if (ok) ok = wait_phase(base + L::VDONE, (g - 1) & 1, limit, failed);
+            if (ok) ok = wait_warp(base + L::VDONE, (g - 1) & 1, limit, failed);
             ok = bar_and_named(1, 128, ok);
             if (!ok) break;
             tc_fence_after();

@@ -49,11 +49,12 @@ constexpr uint32_t RING = 8;
 constexpr uint32_t F_Q = 0;                             // [tile][3 slabs]
 constexpr uint32_t F_RING = 6 * SLAB;
 constexpr uint32_t F_BAR = F_RING + RING * SLAB;
-constexpr uint32_t F_FULL = F_BAR;                      // [RING]
-constexpr uint32_t F_EMPTY = F_FULL + 8 * RING;         // [RING]
-constexpr uint32_t F_QFULL = F_EMPTY + 8 * RING;        // [2]
-constexpr uint32_t F_SFULL = F_QFULL + 16;              // [2]
-constexpr uint32_t F_PFULL = F_SFULL + 16;              // [2]
+constexpr uint32_t F_KFULL = F_BAR;                     // [2] K of steps j & 1
+constexpr uint32_t F_VFULL = F_KFULL + 16;              // [2]
+constexpr uint32_t F_VEMPTY = F_VFULL + 16;             // [2]
+constexpr uint32_t F_QFULL = F_VEMPTY + 16;             // [2]
+constexpr uint32_t F_SFULL = F_QFULL + 16;              // [tile][step & 1]
+constexpr uint32_t F_PFULL = F_SFULL + 32;              // [2]
 constexpr uint32_t F_ODONE = F_PFULL + 16;              // [2]
 constexpr uint32_t F_DRAIN = F_ODONE + 16;
 constexpr uint32_t F_TMEM = F_DRAIN + 8;
@@ -96,13 +97,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     const int steps = max(nt[0], nt[1]);
 
     if (tid == 0) {
-        for (uint32_t i = 0; i < RING; ++i) {
-            mbar_init(base + F_FULL + 8 * i, 1);
-            mbar_init(base + F_EMPTY + 8 * i, 1);
-        }
         for (uint32_t t = 0; t < 2; ++t) {
+            mbar_init(base + F_KFULL + 8 * t, 1);
+            mbar_init(base + F_VFULL + 8 * t, 1);
+            mbar_init(base + F_VEMPTY + 8 * t, 1);
             mbar_init(base + F_QFULL + 8 * t, 1);
-            mbar_init(base + F_SFULL + 8 * t, 1);
+            mbar_init(base + F_SFULL + 16 * t, 1);
+            mbar_init(base + F_SFULL + 16 * t + 8, 1);
             mbar_init(base + F_PFULL + 8 * t, 4);
             mbar_init(base + F_ODONE + 8 * t, 1);
         }
@@ -132,57 +133,57 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     tma_load_3d(base + F_Q + (3 * t + c) * SLAB, &maps.q, 64 * c, h, (int)s.q0 + row0 + t * LAT_TILE,
                                 base + F_QFULL + 8 * t);
             }
-            uint32_t i = 0;
-            bool ok = true;
-            for (int j = 0; j < steps && ok; ++j) {
-                const int tok = (int)s.k0 + j * LAT_TILE;
-                for (uint32_t c = 0; c < 5; ++c, ++i) {
-                    if (i >= RING) ok = wait_phase(base + F_EMPTY + 8 * (i % RING), (i / RING - 1) & 1, limit, failed);
-                    if (!ok) break;
-                    const uint32_t bar = base + F_FULL + 8 * (i % RING);
-                    mbar_arrive_expect_tx(bar, SLAB);
-                    if (c == 2) tma_load_3d(slab(i), &maps.pe, 0, 0, tok, bar);
-                    else tma_load_3d(slab(i), &maps.kv, c < 2 ? 64 * c : 64 * (c - 1), h, tok, bar);
+            // Slab i takes the place of slab i - 8: K of step j that of K's last and V's slabs of step j - 2, V of
+            // step j that of K's first two of step j - 1, which the last product of S (j - 1) frees.
+            const uint32_t s_last = base + F_SFULL + (nt[1] > 0 ? 16 : 0);
+            int j = 0;
+            bool half = false;   // given up between a step's K and its V
+            for (; j < steps; ++j) {
+                const int tok = (int)s.k0 + j * LAT_TILE, st = j & 1;
+                if (j >= 2 && !wait_phase(base + F_VEMPTY + 8 * st, (j / 2 - 1) & 1, limit, failed)) break;
+                mbar_arrive_expect_tx(base + F_KFULL + 8 * st, 3 * SLAB);
+                for (int c = 0; c < 2; ++c) tma_load_3d(slab(5 * j + c), &maps.kv, 64 * c, h, tok, base + F_KFULL + 8 * st);
+                tma_load_3d(slab(5 * j + 2), &maps.pe, 0, 0, tok, base + F_KFULL + 8 * st);
+                if (j >= 1 && !wait_phase(s_last + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, limit, failed)) {
+                    half = true;
+                    break;
                 }
+                mbar_arrive_expect_tx(base + F_VFULL + 8 * st, 2 * SLAB);
+                for (int c = 0; c < 2; ++c)
+                    tma_load_3d(slab(5 * j + 3 + c), &maps.kv, LAT_N + 64 * c, h, tok, base + F_VFULL + 8 * st);
             }
             // every copy issued here has landed before the CTA ends
             for (int t = 0; t < 2; ++t)
                 if (nt[t] > 0) mbar_wait(base + F_QFULL + 8 * t, 0, DRAIN_LIMIT);
-            for (uint32_t k = i > RING ? i - RING : 0; k < i; ++k)
-                mbar_wait(base + F_FULL + 8 * (k % RING), (k / RING) & 1, DRAIN_LIMIT);
+            for (int k = max(0, j - 2); k < j; ++k) {
+                mbar_wait(base + F_KFULL + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
+                mbar_wait(base + F_VFULL + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
+            }
+            if (half) mbar_wait(base + F_KFULL + 8 * (j & 1), (j / 2) & 1, DRAIN_LIMIT);
         } else if (warp == 8) {
             const uint32_t id = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 128, false, false);
             const uint32_t idv = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 128, false, true);
             const uint32_t idv64 = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 64, false, true);
             bool ok = true;
-            auto full = [&](uint32_t i) {
-                ok = __all_sync(0xffffffffu,
-                                ok && wait_phase(base + F_FULL + 8 * (i % RING), (i / RING) & 1, limit, failed));
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && wait_warp(base + bar, parity, limit, failed);
+                return ok;
             };
-            auto qk = [&](int t, int j) {   // S_t = Q_t K_j^T
+            auto qk = [&](int t, int j, bool loaded) {   // S_t = Q_t K_j^T
+                if (!loaded && !wait(F_KFULL + 8 * (j & 1), (j >> 1) & 1)) return;
 #pragma unroll
                 for (int c = 0; c < 3; ++c) {
-                    if (t == 0 || nt[0] <= j) full(5 * j + c);
-                    if (!ok) return;
-                    const uint32_t a = base + F_Q + (3 * t + c) * SLAB, b = slab(5 * j + c);
+                    const Desc a = desc_k(base + F_Q + (3 * t + c) * SLAB), b = desc_k(slab(5 * j + c));
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_warp(tmem + 256 * t, desc_k(a, LAT_TILE, ks), desc_k(b, LAT_TILE, ks), id, c + ks > 0);
+                    for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + 256 * t, a + 2 * ks, b + 2 * ks, id, c + ks > 0);
                 }
-                mma_commit_warp(base + F_SFULL + 8 * t);
+                mma_commit_warp(base + F_SFULL + 16 * t + 8 * (j & 1));
             };
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (nt[t] == 0) continue;
-                ok = __all_sync(0xffffffffu, wait_phase(base + F_QFULL + 8 * t, 0, limit, failed));
-                if (ok) qk(t, 0);
-            }
-            if (steps > 0 && ok)
-                for (uint32_t c = 0; c < 3; ++c) mma_commit_warp(base + F_EMPTY + 8 * c);
+            for (int t = 0; t < 2 && ok; ++t)
+                if (nt[t] > 0 && wait(F_QFULL + 8 * t, 0)) qk(t, 0, t == 1 && nt[0] > 0);
             for (int j = 0; j < steps && ok; ++j) {
                 const uint32_t v = 5 * j + 3;
-                full(v);
-                full(v + 1);
-                if (!ok) break;
+                if (!wait(F_VFULL + 8 * (j & 1), (j >> 1) & 1)) break;
                 if ((j + 1) * LAT_TILE > s.lk) {
                     // rows past the sequence's end hold whatever follows: zero weights must meet zeros
                     for (int r = s.lk - j * LAT_TILE; r < LAT_TILE; ++r)
@@ -192,36 +193,35 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     fence_async_smem();
                     __syncwarp();
                 }
+                bool loaded = false;   // K of the next step
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (j < nt[t] && ok) {
-                        ok = __all_sync(0xffffffffu, wait_phase(base + F_PFULL + 8 * t, j & 1, limit, failed));
-                        if (!ok) break;
+                    if (j < nt[t]) {
+                        if (!wait(F_PFULL + 8 * t, j & 1)) break;
                         tc_fence_after();
                         // O_t += P_t V_j; where the ring wraps between V's two slabs, one product for each
                         const uint32_t d = tmem + 256 * t + 128, a = tmem + 256 * t;
+                        const Desc b = desc_mn(slab(v), LAT_TILE);
                         if ((v + 1) % RING != 0) {
 #pragma unroll
-                            for (int ks = 0; ks < 8; ++ks)
-                                mma_f16_ts_warp(d, a + 8 * ks, desc_mn(slab(v), LAT_TILE, ks), idv, j + ks > 0);
+                            for (int ks = 0; ks < 8; ++ks) mma_ts(d, a + 8 * ks, b + 128 * ks, idv, j + ks > 0);
                         } else {
+                            const Desc b1 = desc_mn(slab(v + 1), LAT_TILE);
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks) {
-                                mma_f16_ts_warp(d, a + 8 * ks, desc_mn(slab(v), LAT_TILE, ks), idv64, j + ks > 0);
-                                mma_f16_ts_warp(d + 64, a + 8 * ks, desc_mn(slab(v + 1), LAT_TILE, ks), idv64,
-                                                j + ks > 0);
+                                mma_ts(d, a + 8 * ks, b + 128 * ks, idv64, j + ks > 0);
+                                mma_ts(d + 64, a + 8 * ks, b1 + 128 * ks, idv64, j + ks > 0);
                             }
                         }
                         if (j == nt[t] - 1) mma_commit_warp(base + F_ODONE + 8 * t);
                     }
-                    if (t == 1) {
-                        mma_commit_warp(base + F_EMPTY + 8 * (v % RING));
-                        mma_commit_warp(base + F_EMPTY + 8 * ((v + 1) % RING));
+                    if (t == 1) mma_commit_warp(base + F_VEMPTY + 8 * (j & 1));
+                    if (j + 1 < nt[t]) {
+                        qk(t, j + 1, loaded);
+                        loaded = true;
                     }
-                    if (j + 1 < nt[t] && ok) qk(t, j + 1);
+                    if (!ok) break;
                 }
-                if (j + 1 < steps && ok)
-                    for (uint32_t c = 0; c < 3; ++c) mma_commit_warp(base + F_EMPTY + 8 * ((5 * (j + 1) + c) % RING));
             }
             // every product issued here is done before the tensor memory is freed
             mma_commit_warp(base + F_DRAIN);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = 0; j < nt[t]; ++j) {
-            ok = __all_sync(0xffffffffu, wait_phase(base + F_SFULL + 8 * t, j & 1, limit, failed));
+            ok = wait_warp(base + F_SFULL + 16 * t + 8 * (j & 1), (j >> 1) & 1, limit, failed);
             if (!ok) break;
             tc_fence_after();
             float x[4][32];
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(base + F_PFULL + 8 * t);
         }
-        if (nt[t] > 0 && ok) ok = wait_phase(base + F_ODONE + 8 * t, 0, limit, failed);
-        if (__all_sync(0xffffffffu, ok)) {
+        if (nt[t] > 0 && ok) ok = wait_warp(base + F_ODONE + 8 * t, 0, limit, failed);
+        if (ok) {
             tc_fence_after();
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long at = (s.q0 + row) * p.H + h;

@@ -10,29 +10,49 @@
 
 namespace kda {
 
-// D[tmem] (+)= A[tmem] B[smem]: rows of A in the lanes, two 16-bit elements
-// of a row in each 32-bit column, the even one in the low half.  Whole
-// converged warp, one elected lane issues.
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
-        "elect.sync r|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+// Shared-memory operand descriptor in two words (sm100_ptx.cuh: smem_desc).
+// A later k-step or slab of the same tile only adds to the address field of
+// `lo`: one addition a product.  With the descriptor built anew for each, the
+// issuing warp's dependent integer instructions took longer than the products
+// (forward, B=4 T=8192 H=16: 1087 us).
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ Desc operator+(uint32_t sixteenths) const { return {lo + sixteenths, hi}; }
+};
+// K-major operand of 128-byte swizzled slabs (64 columns each); the k-step
+// (16 columns) ks of a slab is + 2 ks.
+__device__ __forceinline__ Desc desc_k(uint32_t saddr) {
+    return {((saddr & 0x3FFFFu) >> 4) | (1u << 16), (1024u >> 4) | (1u << 14) | ((uint32_t)SW_128B << 29)};
+}
+// The same slabs as an MN-major operand (their rows are the k axis), `rows`
+// rows each; k-step ks, rows 16 ks .. 16 ks + 15, is + 128 ks.
+__device__ __forceinline__ Desc desc_mn(uint32_t saddr, uint32_t rows) {
+    return {((saddr & 0x3FFFFu) >> 4) | ((rows * 128u >> 4) << 16),
+            (1024u >> 4) | (1u << 14) | ((uint32_t)SW_128B << 29)};
 }
 
-// K-major operand of 128-byte swizzled slabs (`rows` rows of 64 columns
-// each): the descriptor of its k-step (16 columns) ks.
-__device__ __forceinline__ uint64_t desc_k(uint32_t base, uint32_t rows, int ks) {
-    return smem_desc(base + (uint32_t)(ks >> 2) * rows * 128u + (uint32_t)(ks & 3) * 32u, 16u, 1024u, SW_128B);
+// D[tmem] (+)= A[smem] B[smem]; whole converged warp, one elected lane issues.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
-// The same tile as an MN-major operand (its rows are the k axis): k-step ks
-// is rows 16 ks .. 16 ks + 15.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t base, uint32_t rows, int ks) {
-    return smem_desc(base + (uint32_t)ks * 2048u, rows * 128u, 1024u, SW_128B);
+// D[tmem] (+)= A[tmem] B[smem]: rows of A in the lanes, two 16-bit elements
+// of a row in each 32-bit column, the even one in the low half.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -68,6 +88,15 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32
     }
     *failed = 1u;
     return false;
+}
+
+// The same for a converged warp, every lane polling, joined by a vote: the
+// compiler knows a vote's result to be uniform and keeps the operands of the
+// products behind it in uniform registers.  (One lane polling in a branch of
+// its own loses that: forward at B=4 T=8192 H=16 5.3 ms instead of 1.02; one
+// elected lane polling, 1.06.)
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t limit, volatile uint32_t* failed) {
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, limit, failed));
 }
 
 // Tensor map over packed rows: [tokens][heads][width] 16-bit elements, rows
