@@ -22,7 +22,11 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr uint32_t SLAB = 64 * LAT_TILE * 2;            // 128 rows x 64 columns
-constexpr int BWD_THREADS = 320;                        // warps 0-7 elementwise, 8 products, 9 loads
+// Warps 0-7 elementwise (with sixteen, no faster: B=4 T=8192 H=16 3.55 ms
+// beside 3.48), 8 and 9 products, 10 loads.  Two warps issue so that
+// one's waits (about 90 cycles each even when they succeed at once) pass while
+// the other's products run: 8 the scores and dP, 9 the gradients.
+constexpr int BWD_THREADS = 352;
 constexpr int QT = 64;                                  // queries of a dkv step
 constexpr uint32_t HSLAB = 64 * QT * 2;                 // 64 rows x 64 columns
 
@@ -90,7 +94,7 @@ constexpr uint32_t D_Q = 0, D_DO = 3 * SLAB, D_K = 5 * SLAB, D_V = D_K + KRING *
 constexpr uint32_t D_QFULL = D_BAR, D_DOFULL = D_QFULL + 8, D_KFULL = D_DOFULL + 8 /* [2]: first slab */,
                    D_KREST = D_KFULL + 16 /* [2]: the other two */, D_VFULL = D_KREST + 16, D_SFULL = D_VFULL + 8,
                    D_PFULL = D_SFULL + 8, D_SREAD = D_PFULL + 8, D_PREAD = D_SREAD + 8, D_DSFULL = D_PREAD + 8,
-                   D_DONE = D_DSFULL + 8, D_DRAIN = D_DONE + 8, D_TMEM = D_DRAIN + 8, D_FAILED = D_TMEM + 4;
+                   D_DONE = D_DSFULL + 8, D_DRAIN = D_DONE + 8, D_TMEM = D_DRAIN + 16, D_FAILED = D_TMEM + 4;
 constexpr uint32_t D_SMEM = D_FAILED + 4 + 1024;
 static_assert(D_SMEM <= 232448, "shared memory of one CTA");
 
@@ -126,6 +130,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         mbar_init(base + D_DSFULL, 8);
         mbar_init(base + D_DONE, 1);
         mbar_init(base + D_DRAIN, 1);
+        mbar_init(base + D_DRAIN + 8, 1);
         *failed = 0u;
         fence_mbar_init();
     }
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + D_TMEM);
     const uint32_t t_s = tmem, t_p = tmem + 128, t_ds = tmem + 256, t_dq = tmem + 320;
 
-    if (warp == 9) {
+    if (warp == 10) {
         if (lane == 0 && steps > 0) {
             const int tq = (int)s.q0 + row0;
             mbar_arrive_expect_tx(base + D_QFULL, 3 * SLAB);
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             for (int k = max(0, r - 2); k < r; ++k) mbar_wait(base + D_KREST + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
             if (v > 0) mbar_wait(base + D_VFULL, (v - 1) & 1, DRAIN_LIMIT);
         }
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
         const MmaType ty = FP16 ? T_F16 : T_BF16;
         const uint32_t id = idesc_f16(ty, 128, 128, false, false), id64 = idesc_f16(ty, 128, 64, false, true);
         bool ok = true;
@@ -211,32 +216,34 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             }
             mma_commit_warp(base + D_PFULL);
         };
-        if (steps > 0) {
-            if (wait(D_QFULL, 0)) score(0);
-            if (ok && wait(D_DOFULL, 0)) grad_p(0);
-        }
-        for (int j = 0; j < steps && ok; ++j) {
-            if (j + 1 < steps && wait(D_SREAD, j & 1)) {
+        if (warp == 8) {
+            if (steps > 0) {
+                if (wait(D_QFULL, 0)) score(0);
+                if (ok && wait(D_DOFULL, 0)) grad_p(0);
+            }
+            for (int j = 0; j + 1 < steps && ok; ++j) {
+                if (!wait(D_SREAD, j & 1)) break;
                 tc_fence_after();
                 score(j + 1);
-            }
-            if (!ok || !wait(D_DSFULL, j & 1)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {              // dQ += dS K, 64 of its columns a K slab
-                const Desc db = desc_mn(base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB, LAT_TILE);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) mma_ts(t_dq + 64 * c, t_ds + 8 * ks, db + 128 * ks, id64, j + ks > 0);
-            }
-            mma_commit_warp(base + D_DONE);
-            if (j + 1 < steps && wait(D_PREAD, j & 1)) {
+                if (!ok || !wait(D_PREAD, j & 1)) break;
                 tc_fence_after();
                 grad_p(j + 1);
             }
+        } else {
+            for (int j = 0; j < steps && wait(D_DSFULL, j & 1); ++j) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {          // dQ += dS K, 64 of its columns a K slab
+                    const Desc db = desc_mn(base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB, LAT_TILE);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) mma_ts(t_dq + 64 * c, t_ds + 8 * ks, db + 128 * ks, id64, j + ks > 0);
+                }
+                mma_commit_warp(base + D_DONE);
+            }
         }
         // every product issued here is done before the tensor memory is freed
-        mma_commit_warp(base + D_DRAIN);
-        mbar_wait(base + D_DRAIN, 0, DRAIN_LIMIT);
+        mma_commit_warp(base + D_DRAIN + 8 * (warp & 1));
+        mbar_wait(base + D_DRAIN + 8 * (warp & 1), 0, DRAIN_LIMIT);
     } else {
         const int g = warp >> 2, row = row0 + (warp & 3) * 32 + lane;   // columns 64 g .. of S and dP
         const uint32_t quad = (uint32_t)(warp & 3) << 21;
@@ -345,7 +352,7 @@ constexpr uint32_t K_K = 0, K_V = 3 * SLAB, K_ST = 5 * SLAB, K_AUX = K_ST + STAG
 constexpr uint32_t K_KVFULL = K_BAR, K_FULL = K_KVFULL + 8, K_KDONE = K_FULL + 8 * STAGES, K_SFULL = K_KDONE + 8 * STAGES,
                    K_DPFULL = K_SFULL + 8, K_SREAD = K_DPFULL + 8, K_DPREAD = K_SREAD + 8, K_PFULL = K_DPREAD + 8,
                    K_DSFULL = K_PFULL + 8, K_DRAIN = K_DSFULL + 8,
-                   K_TMEM = K_DRAIN + 8, K_FAILED = K_TMEM + 4;
+                   K_TMEM = K_DRAIN + 16, K_FAILED = K_TMEM + 4;
 constexpr uint32_t K_SMEM = K_FAILED + 4 + 1024;
 static_assert(K_SMEM <= 232448, "shared memory of one CTA");
 
@@ -380,6 +387,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         mbar_init(base + K_PFULL, 8);
         mbar_init(base + K_DSFULL, 8);
         mbar_init(base + K_DRAIN, 1);
+        mbar_init(base + K_DRAIN + 8, 1);
         *failed = 0u;
         fence_mbar_init();
     }
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + K_TMEM);
     const uint32_t t_s = tmem, t_dp = tmem + 64, t_p = tmem + 128, t_ds = tmem + 160, t_dv = tmem + 192, t_dk = tmem + 320;
 
-    if (warp == 9) {
+    if (warp == 10) {
         if (lane == 0 && steps > 0) {
             const int tk = (int)s.k0 + key0;
             mbar_arrive_expect_tx(base + K_KVFULL, 5 * SLAB);
@@ -418,7 +426,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             for (uint32_t k = i > STAGES ? i - STAGES : 0; k < i; ++k)
                 mbar_wait(base + K_FULL + 8 * (k % STAGES), (k / STAGES) & 1, DRAIN_LIMIT);
         }
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
         const MmaType ty = FP16 ? T_F16 : T_BF16;
         const uint32_t id_s = idesc_f16(ty, 128, QT, false, false), id_v = idesc_f16(ty, 128, 128, false, true),
                        id_k = idesc_f16(ty, 128, 192, false, true);
@@ -456,36 +464,35 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                        ks > 0);
             mma_commit_warp(base + K_DPFULL);
         };
-        if (steps > 0 && wait(K_KVFULL, 0)) {
-            score(0);
-            if (ok) grad_p(0);
-        }
-        for (int i = 0; i < steps && ok; ++i) {
-            const bool more = i + 1 < steps;
-            if (more) {
+        if (warp == 8) {
+            if (steps > 0 && wait(K_KVFULL, 0)) {
+                score(0);
+                if (ok) grad_p(0);
+            }
+            for (int i = 0; i + 1 < steps && ok; ++i) {
                 if (!wait(K_SREAD, i & 1)) break;
                 tc_fence_after();
                 score(i + 1);
-            }
-            if (!ok || !wait(K_PFULL, i & 1)) break;
-            tc_fence_after();
-            const Desc bv = desc_mn(stage(i) + 3 * HSLAB, QT), bk = desc_mn(stage(i), QT);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) mma_ts(t_dv, t_p + 8 * ks, bv + 128 * ks, id_v, i + ks > 0);
-            if (more) {
-                if (!wait(K_DPREAD, i & 1)) break;
+                if (!ok || !wait(K_DPREAD, i & 1)) break;
                 tc_fence_after();
                 grad_p(i + 1);
             }
-            if (!wait(K_DSFULL, i & 1)) break;
-            tc_fence_after();
+        } else {
+            for (int i = 0; i < steps && wait(K_PFULL, i & 1); ++i) {
+                tc_fence_after();
+                const Desc bv = desc_mn(stage(i) + 3 * HSLAB, QT), bk = desc_mn(stage(i), QT);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) mma_ts(t_dk, t_ds + 8 * ks, bk + 128 * ks, id_k, i + ks > 0);
-            mma_commit_warp(base + K_KDONE + 8 * (i % STAGES));
+                for (int ks = 0; ks < 4; ++ks) mma_ts(t_dv, t_p + 8 * ks, bv + 128 * ks, id_v, i + ks > 0);
+                if (!wait(K_DSFULL, i & 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_ts(t_dk, t_ds + 8 * ks, bk + 128 * ks, id_k, i + ks > 0);
+                mma_commit_warp(base + K_KDONE + 8 * (i % STAGES));
+            }
         }
         // every product issued here is done before the tensor memory is freed
-        mma_commit_warp(base + K_DRAIN);
-        mbar_wait(base + K_DRAIN, 0, DRAIN_LIMIT);
+        mma_commit_warp(base + K_DRAIN + 8 * (warp & 1));
+        mbar_wait(base + K_DRAIN + 8 * (warp & 1), 0, DRAIN_LIMIT);
     } else {
         const int g = warp >> 2, key = key0 + (warp & 3) * 32 + lane;   // queries 32 g .. of a tile
         const uint32_t quad = (uint32_t)(warp & 3) << 21;
