@@ -382,9 +382,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     for (int e = 0; e < KEYS; ++e)
                         if (!(keys >> e & 1)) x[e >> 5][e & 31] = -INFINITY;
                 }
-                float top = x[0][0];
-#pragma unroll
-                for (int e = 1; e < KEYS; ++e) top = fmaxf(top, x[e >> 5][e & 31]);
+                const float top = fmaxf(max32(x[0]), max32(x[1]));
                 bool grown = top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m);
                 grown = grown && r < R && lane < 16;
                 // P's buffer is free, and O stands still, once the tile before is done
@@ -417,21 +415,25 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 }
                 if (r < R) {
                     const float mc = m == -INFINITY ? 0.f : m * c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int at = 8 * q + 2 * e;
-                            const float u = ex2(fmaf(x[at >> 5][at & 31], c, -mc));
-                            const float v = ex2(fmaf(x[at >> 5][(at & 31) + 1], c, -mc));
-                            l += u + v;
+                            float u = x[at >> 5][at & 31], v = x[at >> 5][(at & 31) + 1];
+                            fma2(u, v, c, -mc);
+                            u = ex2(u);
+                            v = ex2(v);
+                            add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], u, v);
                             o[e] = pack2<FP16>(u, v);
                         }
                         if (lane < 16)
                             *reinterpret_cast<uint4*>(smem + L::P + r * 128 + ((q ^ (r & 7)) * 16)) =
                                 make_uint4(o[0], o[1], o[2], o[3]);
                     }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
                 fence_async_smem();
                 tc_fence_before();

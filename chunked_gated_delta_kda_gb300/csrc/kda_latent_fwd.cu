@@ -251,11 +251,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[b][e] = 32 * b + e < lim ? x[b][e] : -INFINITY;
             }
-            float top = x[0][0];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, x[b][e]);
+            const float top = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3])));
             const bool grown = top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grown)) {
                 const float mn = grown ? top : m;
@@ -275,18 +271,22 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 m = mn;
             }
             const float mc = m == -INFINITY ? 0.f : m * c;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int b = 0; b < 4; b += 2) {
                 float w[32];
 #pragma unroll
                 for (int e = 0; e < 64; e += 2) {
-                    const float u = ex2(fmaf(x[b + (e >> 5)][e & 31], c, -mc));
-                    const float v = ex2(fmaf(x[b + (e >> 5)][(e & 31) + 1], c, -mc));
-                    l += u + v;
+                    float u = x[b + (e >> 5)][e & 31], v = x[b + (e >> 5)][(e & 31) + 1];
+                    fma2(u, v, c, -mc);
+                    u = ex2(u);
+                    v = ex2(v);
+                    add2(sum[e & 2], sum[(e & 2) + 1], u, v);
                     w[e >> 1] = __uint_as_float(pack2<FP16>(u, v));
                 }
                 tmem_st32(ts + 16 * b, w);
             }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();

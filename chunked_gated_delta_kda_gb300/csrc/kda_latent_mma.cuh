@@ -61,6 +61,37 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Two 32-bit operations in one instruction: (a, b) c + d, and (a, b) + (c, d).
+__device__ __forceinline__ void fma2(float& a, float& b, float c, float d) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
+}
+// Of three (NaN only from three NaN).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+// The largest of 32 values, in four independent chains.
+__device__ __forceinline__ float max32(const float (&x)[32]) {
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = fmaxf(x[i], x[i + 4]);
+#pragma unroll
+    for (int e = 8; e < 32; e += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = max3(m[i], x[e + i], x[e + i + 4]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 // a, b -> one 32-bit word of two rounded 16-bit floats, a in the low half.
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
