@@ -64,92 +64,114 @@ struct TableParams {
     int width, num_free, page_size, num_tokens, N;
 };
 
-constexpr int TAB_THREADS = 1024;
+// Tables of one step.  Every CTA takes the prefix sums of all sequences'
+// tokens and pages itself (a few microseconds of latency, in place of a second
+// launch), a chunk of sequences at a time; then the tokens, and the pages, are
+// spread over all threads of the grid, each finding its sequence by bisection
+// in shared memory.  So one long prompt is written as fast as many short ones.
+// A page taken in this step is read from the free list, not from the table
+// cell that another thread writes.  Bound by latency: 2048 sequences with
+// 525 thousand tokens (4.4 MB written) 296 us by one CTA.
+constexpr int TAB_THREADS = 512;
+constexpr int TAB_SEQS = 2048;                  // sequences of a chunk
+constexpr int TAB_PER = TAB_SEQS / TAB_THREADS;
 
-// Inclusive prefix sum over the CTA.
-__device__ long long cta_scan(long long x, long long* warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+// The last i in [0, n) with a[i] <= x (a[0] <= x).
+__device__ __forceinline__ int last_not_above(const long long* a, int n, long long x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid - 1;
     }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sums[w];
-    return x + before;
+    return lo;
 }
 
-__global__ void block_tables_kernel(TableParams p) {
-    __shared__ long long sums[32];
-    __shared__ int2 seq_at[TAB_THREADS];       // (first token, first free entry) of the chunk's sequences
-    __shared__ int2 seq_len[TAB_THREADS];      // (cached rows, new rows)
-    long long tok0 = 0, page0 = 0;
-    const long long head = p.free_head[0];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ps = p.page_size;
+__global__ void __launch_bounds__(TAB_THREADS) block_tables_kernel(const __grid_constant__ TableParams p) {
+    __shared__ long long tok_at[TAB_SEQS + 1], page_at[TAB_SEQS + 1];   // first token and page of each sequence
+    __shared__ int lens[TAB_SEQS];
+    __shared__ long long sums[2][TAB_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ps = p.page_size;
+    const int shift = 31 - __clz(ps);
+    const long long head = p.free_head[0], stride = (long long)gridDim.x * TAB_THREADS;
+    const long long me = (long long)blockIdx.x * TAB_THREADS + tid;
+    long long tok0 = 0, page0 = 0;              // of the chunk
     bool bad = false;
-    for (int base = 0; base < p.N; base += TAB_THREADS) {
-        const int n = base + threadIdx.x;
-        int a = 0, b = 0;
-        long long take = 0;
-        if (n < p.N) {
-            a = p.lens[n];
-            b = p.fresh[n];
-            if (a < 0 || b < 0 || (long long)a + b > INT32_MAX) {
+    auto held_of = [&](int len) { return (int)(((long long)len + ps - 1) >> shift); };
+    auto free_page = [&](long long at) {
+        at += head;
+        const bool ok = at >= 0 && at < p.num_free;
+        return ok ? p.free_pages[at] : -1;
+    };
+    for (int base = 0; base < p.N; base += TAB_SEQS) {
+        const int count = min(TAB_SEQS, p.N - base);
+        int a[TAB_PER], b[TAB_PER];
+        long long take[TAB_PER], toks = 0, pages = 0;
+#pragma unroll
+        for (int k = 0; k < TAB_PER; ++k) {
+            const int i = TAB_PER * tid + k;
+            a[k] = i < count ? p.lens[base + i] : 0;
+            b[k] = i < count ? p.fresh[base + i] : 0;
+            if (a[k] < 0 || b[k] < 0 || (long long)a[k] + b[k] > INT32_MAX) {
                 bad = true;
-                a = a < 0 ? 0 : a;
-                b = b < 0 || (long long)a + b > INT32_MAX ? 0 : b;
+                a[k] = max(a[k], 0);
+                if (b[k] < 0 || (long long)a[k] + b[k] > INT32_MAX) b[k] = 0;
             }
-            const long long held = ((long long)a + ps - 1) / ps, want = ((long long)a + b + ps - 1) / ps;
+            const int want = held_of(a[k] + (long long)b[k] > INT32_MAX ? a[k] : a[k] + b[k]);
             bad |= want > p.width;
-            take = max(0ll, min(want, (long long)p.width) - held);
+            take[k] = max(0, min(want, p.width) - held_of(a[k]));
+            toks += b[k];
+            pages += take[k];
         }
-        const long long tok = cta_scan(b, sums), pg = cta_scan(take, sums);
-        seq_at[threadIdx.x] = make_int2((int)min(tok0 + tok - b, (long long)INT32_MAX), (int)min(page0 + pg - take, (long long)INT32_MAX));
-        seq_len[threadIdx.x] = make_int2(a, b);
-        if (n < p.N) {
-            p.cu[n] = seq_at[threadIdx.x].x;
-            p.lens_out[n] = a + b;
+        long long x = toks, y = pages;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) x += u, y += v;
         }
+        __syncthreads();                        // the chunk before is done with shared memory
+        if (lane == 31) sums[0][warp] = x, sums[1][warp] = y;
         __syncthreads();
-        for (int i = warp; i < min(TAB_THREADS, p.N - base); i += TAB_THREADS / 32) {
-            const int la = seq_len[i].x, lb = seq_len[i].y;
-            const int held = (int)(((long long)la + ps - 1) / ps);
-            int32_t* row = p.table + (long long)(base + i) * p.width;
-            const int want = (int)min(((long long)la + lb + ps - 1) / ps, (long long)p.width);
-            for (int c = held + lane; c < want; c += 32) {
-                const long long at = head + seq_at[i].y + c - held;
-                const bool ok = at >= 0 && at < p.num_free;
-                bad |= !ok;
-                row[c] = ok ? p.free_pages[at] : -1;
+        x += tok0 - toks;
+        y += page0 - pages;
+        for (int w = 0; w < warp; ++w) x += sums[0][w], y += sums[1][w];
+#pragma unroll
+        for (int k = 0; k < TAB_PER; ++k) {
+            const int i = TAB_PER * tid + k;
+            tok_at[i] = x;
+            page_at[i] = y;
+            lens[i] = a[k];
+            if (blockIdx.x == 0 && i < count) {
+                p.cu[base + i] = (int)min(x, (long long)INT32_MAX);
+                p.lens_out[base + i] = a[k] + b[k];
             }
-            for (int k = lane; k < lb; k += 32) {
-                const long long t = (long long)seq_at[i].x + k;
-                if (t >= p.num_tokens) {
-                    bad = true;
-                    break;
-                }
-                const int pos = la + k, c = pos / ps;
-                int page = -1;
-                if (c < held) page = c < p.width ? row[c] : -1;
-                else if (c < p.width) {
-                    const long long at = head + seq_at[i].y + c - held;
-                    if (at >= 0 && at < p.num_free) page = p.free_pages[at];
-                }
-                bad |= page < 0;
-                p.slots[t] = page < 0 ? -1 : (int64_t)page * ps + pos % ps;
-            }
+            x += b[k];
+            y += take[k];
         }
+        if (tid == TAB_THREADS - 1) tok_at[TAB_SEQS] = x, page_at[TAB_SEQS] = y;
         __syncthreads();
-        if (threadIdx.x == TAB_THREADS - 1) sums[0] = tok, sums[1] = pg;
-        __syncthreads();
-        tok0 += sums[0];
-        page0 += sums[1];
-        __syncthreads();
+        const long long tok1 = tok_at[TAB_SEQS], page1 = page_at[TAB_SEQS];
+        for (long long q = page0 + me; q < page1; q += stride) {
+            const int i = last_not_above(page_at, count, q);
+            const int page = free_page(q);
+            bad |= page < 0;
+            p.table[(long long)(base + i) * p.width + held_of(lens[i]) + (q - page_at[i])] = page;
+        }
+        for (long long t = tok0 + me; t < min(tok1, (long long)p.num_tokens); t += stride) {
+            const int i = last_not_above(tok_at, count, t);
+            const int pos = lens[i] + (int)(t - tok_at[i]), cell = pos >> shift, held = held_of(lens[i]);
+            int page = -1;
+            if (cell < p.width)
+                page = cell < held ? p.table[(long long)(base + i) * p.width + cell] : free_page(page_at[i] + cell - held);
+            bad |= page < 0;
+            p.slots[t] = page < 0 ? -1 : ((int64_t)page << shift) + (pos & (ps - 1));
+        }
+        tok0 = tok1;
+        page0 = page1;
     }
-    for (long long t = tok0 + threadIdx.x; t < p.num_tokens; t += TAB_THREADS) p.slots[t] = -1;
-    if (threadIdx.x == 0) {
+    for (long long t = tok0 + me; t < p.num_tokens; t += stride) p.slots[t] = -1;
+    if (me == 0) {
+        bad |= tok0 > p.num_tokens;
         p.cu[p.N] = (int)min(tok0, (long long)INT32_MAX);
         p.head_out[0] = (int)max(min(head + page0, (long long)p.num_free), min(head, (long long)p.num_free));
     }
@@ -206,7 +228,9 @@ kda_status kda_block_tables(const int32_t* seq_lens, const int32_t* new_lens, in
     if (status && cudaMemsetAsync(status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
     TableParams p{seq_lens, new_lens,   block_table,  free_pages,    free_head,   slot_mapping, cu_seqlens,
                   seq_lens_out, free_head_out, status, table_width, num_free, page_size, num_tokens, N};
-    block_tables_kernel<<<1, TAB_THREADS, 0, stream>>>(p);
+    // eight tokens a thread before another CTA repeats the prefix sums
+    const int grid = (int)(((long long)num_tokens + 8ll * TAB_THREADS - 1) / (8ll * TAB_THREADS));
+    block_tables_kernel<<<grid < 1 ? 1 : grid > 152 ? 152 : grid, TAB_THREADS, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
