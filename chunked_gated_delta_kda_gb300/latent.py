@@ -17,12 +17,11 @@ library is missing, every call raises: there is no fallback path.
 
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple
 
 import torch
 
-from .binding import KDA_FLAG_CAUSAL, KDA_FLAG_FP16, KdaError, _ptr, _stream_handle, load_library
+from .binding import KDA_FLAG_CAUSAL, KDA_FLAG_FP16, KdaError, load_library
 
 LATENT_CHANNELS = 512
 PE_CHANNELS = 64
@@ -35,45 +34,64 @@ STATUS_BYTES = 256
 _FLOAT_FLAGS = {torch.bfloat16: 0, torch.float16: KDA_FLAG_FP16}
 
 
+# Decode steps are a few microseconds of GPU time, so the checks below run on
+# every call as plain comparisons and only a failed one builds its message.
 def _check(name: str, t, dtype, shape) -> None:
     """``shape``: the wanted sizes, None where any size goes."""
+    if type(t) is torch.Tensor or isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.is_cuda:
+            got = t.shape
+            if len(got) == len(shape):
+                for w, g in zip(shape, got):
+                    if w is not None and w != g:
+                        break
+                else:
+                    return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
-        want = ", ".join("*" if w is None else str(w) for w in shape)
-        raise ValueError(f"{name} must have shape [{want}], got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    want = ", ".join("*" if w is None else str(w) for w in shape)
+    raise ValueError(f"{name} must have shape [{want}], got {tuple(t.shape)}")
 
 
 def _float_flag(name: str, t) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _FLOAT_FLAGS:
+    flag = _FLOAT_FLAGS.get(t.dtype)
+    if flag is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-    return _FLOAT_FLAGS[t.dtype]
+    return flag
 
 
-def _same_device(dev, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _same_device(index: int, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on the same device: got cuda:{index} and {t.device}")
 
 
-def _status_workspace(workspace):
-    if workspace is not None and workspace.numel() * workspace.element_size() < STATUS_BYTES:
+def _status_workspace(workspace) -> Optional[int]:
+    if workspace is None:
+        return None
+    if workspace.numel() * workspace.element_size() < STATUS_BYTES:
         raise ValueError(f"workspace must have at least {STATUS_BYTES} bytes")
-    return workspace
+    return workspace.data_ptr()
 
 
-def _call(name: str, dev, *args) -> None:
-    if dev.index == torch.cuda.current_device():
-        rc = getattr(load_library(), name)(*args, _stream_handle(dev))
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _call(name: str, index: int, *args) -> None:
+    """The C entry point on torch's current stream of device ``index``."""
+    fn = getattr(load_library(), name)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            rc = getattr(load_library(), name)(*args, _stream_handle(dev))
+        with torch.cuda.device(index):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise KdaError(rc, name)
 
@@ -96,7 +114,7 @@ def _expanded(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k):
         if B != 1 or N < 1:
             raise ValueError("packed sequences need a leading size of 1 and at least one sequence")
         cu_seqlens_q, cu_seqlens_k = cu_seqlens_q.contiguous(), cu_seqlens_k.contiguous()
-    _same_device(q.device, kv=kv, k_pe=k_pe, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+    _same_device(q.get_device(), kv, k_pe, cu_seqlens_q, cu_seqlens_k)
     q, kv = _aligned(q.contiguous()), _aligned(kv.contiguous())
     # rows of a wider tensor are read in place where the kernels can
     stride = k_pe.stride(1) if Tk > 1 else k_pe.stride(0)
@@ -131,9 +149,9 @@ def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: Opt
     B, Tq, H, _ = q.shape
     o = torch.empty((B, Tq, H, VALUE_CHANNELS), dtype=q.dtype, device=q.device)
     lse = torch.empty((B, Tq, H), dtype=torch.float32, device=q.device)
-    _call("kda_latent_fwd", q.device, _ptr(q), _ptr(kv), _ptr(k_pe), stride, float(-1.0 if scale is None else scale),
+    _call("kda_latent_fwd", q.get_device(), _ptr(q), _ptr(kv), _ptr(k_pe), stride, float(-1.0 if scale is None else scale),
           _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(o), _ptr(lse), B, Tq, kv.shape[1], H, N,
-          flags | (KDA_FLAG_CAUSAL if causal else 0), _ptr(_status_workspace(workspace)))
+          flags | (KDA_FLAG_CAUSAL if causal else 0), _status_workspace(workspace))
     return o, lse
 
 
@@ -154,7 +172,7 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
     _check("o", o, q.dtype, (B, Tq, H, VALUE_CHANNELS))
     _check("do", do, q.dtype, (B, Tq, H, VALUE_CHANNELS))
     _check("lse", lse, torch.float32, (B, Tq, H))
-    _same_device(dev, o=o, lse=lse, do=do)
+    _same_device(q.get_device(), o, lse, do)
     o, do, lse = _aligned(o.contiguous()), _aligned(do.contiguous()), lse.contiguous()
     need = latent_bwd_workspace_bytes(B, Tq, Tk, H, N)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
@@ -162,7 +180,7 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
     dq = torch.empty_like(q)
     dkv = torch.empty_like(kv)
     dk_pe = torch.empty((B, Tk, PE_CHANNELS), dtype=q.dtype, device=dev)
-    _call("kda_latent_bwd", dev, _ptr(q), _ptr(kv), _ptr(k_pe), stride, _ptr(o), _ptr(lse), _ptr(do),
+    _call("kda_latent_bwd", q.get_device(), _ptr(q), _ptr(kv), _ptr(k_pe), stride, _ptr(o), _ptr(lse), _ptr(do),
           float(-1.0 if scale is None else scale), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(dq), _ptr(dkv),
           _ptr(dk_pe), B, Tq, Tk, H, N, flags | (KDA_FLAG_CAUSAL if causal else 0), _ptr(workspace),
           workspace.numel() * workspace.element_size())
@@ -192,7 +210,7 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     _check("block_table", block_table, torch.int32, (N, None))
     _check("seq_lens", seq_lens, torch.int32, (N,))
     dev = q.device
-    _same_device(dev, cache=cache, block_table=block_table, seq_lens=seq_lens)
+    _same_device(q.get_device(), cache, block_table, seq_lens)
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
     q, block_table, seq_lens = _aligned(q.contiguous()), block_table.contiguous(), seq_lens.contiguous()
@@ -201,7 +219,7 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         workspace = torch.empty(max(need, STATUS_BYTES), dtype=torch.uint8, device=dev)
     o = torch.empty((N, S, H, LATENT_CHANNELS), dtype=q.dtype, device=dev)
     lse = torch.empty((N, S, H), dtype=torch.float32, device=dev)
-    _call("kda_latent_decode", dev, _ptr(q), _ptr(cache), cache.shape[0], cache.shape[1], _ptr(block_table),
+    _call("kda_latent_decode", q.get_device(), _ptr(q), _ptr(cache), cache.shape[0], cache.shape[1], _ptr(block_table),
           block_table.shape[1], _ptr(seq_lens), float(-1.0 if scale is None else scale), _ptr(o), _ptr(lse), N, S, H,
           flags, _ptr(workspace), workspace.numel() * workspace.element_size())
     return o, lse
@@ -219,18 +237,18 @@ def latent_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     T = rows.shape[0]
     _check("slots", slots, torch.int64, (T,))
     _check("cache", cache, rows.dtype, (None, None, ROW_CHANNELS))
-    dev = rows.device
     if norm_weight is not None:
         _check("norm_weight", norm_weight, rows.dtype, (LATENT_CHANNELS,))
         norm_weight = _aligned(norm_weight.contiguous())
-    _same_device(dev, slots=slots, cache=cache, norm_weight=norm_weight)
+    _same_device(rows.get_device(), slots, cache, norm_weight)
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
     if rows.stride(1) != 1 or rows.stride(0) < ROW_CHANNELS or rows.stride(0) % 8 or rows.data_ptr() % 16:
         rows = _aligned(rows.contiguous())
-    _call("kda_latent_append", dev, _ptr(rows), max(rows.stride(0), ROW_CHANNELS), _ptr(slots.contiguous()),
+    slots = slots.contiguous()
+    _call("kda_latent_append", rows.get_device(), _ptr(rows), max(rows.stride(0), ROW_CHANNELS), _ptr(slots),
           _ptr(norm_weight), float(eps), _ptr(cache), cache.shape[0] * cache.shape[1], T, flags,
-          _ptr(_status_workspace(workspace)))
+          _status_workspace(workspace))
     return cache
 
 
@@ -253,14 +271,16 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
     _check("free_pages", free_pages, torch.int32, (None,))
     _check("free_head", free_head, torch.int32, (1,))
     dev = seq_lens.device
-    _same_device(dev, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_head=free_head)
+    _same_device(seq_lens.get_device(), new_lens, block_table, free_pages, free_head)
     if not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous")
     slots = torch.empty((num_tokens,), dtype=torch.int64, device=dev)
     out = torch.empty((2 * N + 2,), dtype=torch.int32, device=dev)
-    cu, lens_out, head_out = out[: N + 1], out[N + 1: 2 * N + 1], out[2 * N + 1:]
-    _call("kda_block_tables", dev, _ptr(seq_lens.contiguous()), _ptr(new_lens.contiguous()), _ptr(block_table),
-          block_table.shape[1], _ptr(free_pages.contiguous()), free_pages.shape[0], _ptr(free_head), int(page_size),
+    cu, lens_out, head_out = out.split((N + 1, N, 1))
+    # copies are held until the launch: a freed one's memory would go to the next
+    seq_lens, new_lens, free_pages = seq_lens.contiguous(), new_lens.contiguous(), free_pages.contiguous()
+    _call("kda_block_tables", seq_lens.get_device(), _ptr(seq_lens), _ptr(new_lens), _ptr(block_table),
+          block_table.shape[1], _ptr(free_pages), free_pages.shape[0], _ptr(free_head), int(page_size),
           _ptr(slots), int(num_tokens), _ptr(cu), _ptr(lens_out), _ptr(head_out), N,
-          _ptr(_status_workspace(workspace)))
+          _status_workspace(workspace))
     return slots, cu, lens_out, head_out
