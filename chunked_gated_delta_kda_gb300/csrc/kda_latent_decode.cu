@@ -20,7 +20,10 @@
 // which also writes the empty sequences.
 //   warps 0-3  softmax (row 16 w + l in lane l < 16 of warp w, as an M = 64
 //              product lays its rows out), rescaling and output of O
-//   warp 4     issues the products;  warp 5  loads
+//   warps 4, 5  issue the products, 4 the scores and 5 those with the values:
+//              the values' part of a tile must not wait for the next tile's
+//              loads, which its end makes room for
+//   warp 6     loads
 #include "kda_latent_decode.cuh"
 #include "kda_latent_mma.cuh"
 
@@ -28,33 +31,32 @@ namespace kda {
 
 namespace {
 
-constexpr int DEC_THREADS = 192;
+constexpr int DEC_THREADS = 224;
 constexpr int KEYS = 64;                                 // keys of a tile
-constexpr uint32_t PAIR = 2 * KEYS * 128;                // 128 channels of a tile: two 64-channel slabs
-constexpr uint32_t PE = KEYS * 128;                      // its 64 positional channels
+constexpr uint32_t KSLAB = KEYS * 128;                   // 64 channels of a tile
+constexpr uint32_t HALF = 4 * KSLAB;                     // 256 latent channels of a tile: the unit of the ring
 constexpr float RESCALE_LOG2 = 8.f;
 
 // Shared-memory layout for R rows of a unit: Q, P, then the two rings.
 template <int R>
 struct Lay {
-    static constexpr uint32_t NP = R == 64 ? 8 : 10, NE = R == 64 ? 2 : 3;   // 2 or 2.5 tiles in flight
+    static constexpr uint32_t NH = R == 64 ? 4 : 5, NE = R == 64 ? 2 : 3;   // 2 or 2.5 tiles in flight
     static constexpr uint32_t Q = 0;                     // 9 slabs of R rows
     static constexpr uint32_t P = Q + 9 * R * 128;
-    static constexpr uint32_t RP = P + R * 128;
-    static constexpr uint32_t RE = RP + NP * PAIR;
-    static constexpr uint32_t BAR = RE + NE * PE;
-    static constexpr uint32_t PFULL = BAR;               // ring: [NP] full, [NP] empty, [NE] full, [NE] empty
-    static constexpr uint32_t PEMPTY = PFULL + 8 * NP;
-    static constexpr uint32_t EFULL = PEMPTY + 8 * NP;
+    static constexpr uint32_t RH = P + R * 128;          // halves
+    static constexpr uint32_t RE = RH + NH * HALF;       // positional slabs
+    static constexpr uint32_t HFULL = RE + NE * KSLAB;
+    static constexpr uint32_t HEMPTY = HFULL + 8 * NH;
+    static constexpr uint32_t EFULL = HEMPTY + 8 * NH;
     static constexpr uint32_t EEMPTY = EFULL + 8 * NE;
     static constexpr uint32_t QFULL = EEMPTY + 8 * NE;
     static constexpr uint32_t QEMPTY = QFULL + 8;
     static constexpr uint32_t SFULL = QEMPTY + 8;        // [2]
-    static constexpr uint32_t WFULL = SFULL + 16;        // P written
-    static constexpr uint32_t VDONE = WFULL + 8;         // second product of a tile done
+    static constexpr uint32_t WFULL = SFULL + 16;        // [2] P written
+    static constexpr uint32_t VDONE = WFULL + 16;        // second product of a tile done
     static constexpr uint32_t OFREE = VDONE + 8;         // O read out
     static constexpr uint32_t DRAIN = OFREE + 8;
-    static constexpr uint32_t FACT = DRAIN + 8;          // [64] floats
+    static constexpr uint32_t FACT = DRAIN + 16;         // [64] floats
     static constexpr uint32_t PLAN = FACT + 256;
     static constexpr uint32_t BYTES = PLAN + 256;
     static constexpr uint32_t SMEM = BYTES + 1024;
@@ -156,9 +158,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     const int box = min(p.page_size, KEYS);
 
     if (tid == 0) {
-        for (uint32_t i = 0; i < L::NP; ++i) {
-            mbar_init(base + L::PFULL + 8 * i, 1);
-            mbar_init(base + L::PEMPTY + 8 * i, 1);
+        for (uint32_t i = 0; i < L::NH; ++i) {
+            mbar_init(base + L::HFULL + 8 * i, 1);
+            mbar_init(base + L::HEMPTY + 8 * i, 1);
         }
         for (uint32_t i = 0; i < L::NE; ++i) {
             mbar_init(base + L::EFULL + 8 * i, 1);
@@ -169,14 +171,17 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
         mbar_init(base + L::SFULL, 1);
         mbar_init(base + L::SFULL + 8, 1);
         mbar_init(base + L::WFULL, 4);
+        mbar_init(base + L::WFULL + 8, 4);
         mbar_init(base + L::VDONE, 1);
         mbar_init(base + L::OFREE, 4);
         mbar_init(base + L::DRAIN, 1);
+        mbar_init(base + L::DRAIN + 8, 1);
         plan.failed = 0u;
         plan.err = 0u;
         plan.count = 0;
         fence_mbar_init();
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 4) {
         tmem_alloc(base + L::PLAN + (uint32_t)offsetof(Plan, tmem), 512);
         tmem_relinquish();
@@ -240,10 +245,12 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&plan.tmem);
     const uint32_t t_s = tmem + 256;                   // S: two buffers of 64 columns; O: columns [0, 4 R)
 
-    if (warp == 5) {
+    if (warp == 6) {
         // ---- loads ----
-        uint32_t ip = 0, ie = 0, seg = 0;              // pairs, positional slabs and queries asked for
+        uint32_t ih = 0, ie = 0, seg = 0;              // halves, positional slabs and queries asked for
         bool ok = true;
+        const int nbox = KEYS / box;
+        const int b = lane % nbox, c = lane / nbox;    // this lane's box and slab (nbox <= 4: of 8 or more)
         for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts)) {
             if (seg > 0) ok = wait_warp(base + L::QEMPTY, (seg - 1) & 1, limit, failed);
             if (!ok) break;
@@ -252,106 +259,109 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             if (lane < 9)
                 tma_load_3d(base + L::Q + lane * R * 128, &maps.q, 64 * lane, 0, w.n * rows + w.mt * R, base + L::QFULL);
             ++seg;
-            const int nbox = KEYS / box;
             bool bad = false;
+            int row, page = box_page(p, w, w.k0, b, box, row);
             for (int k = 0; k < w.cnt && ok; ++k) {
                 const int tile = w.k0 + k;
-                int row;
-                const int page = lane < 2 * nbox ? box_page(p, w, tile, lane >> 1, box, row) : -1;
                 const bool have = page >= 0;
-                bad |= lane < 2 * nbox && !have && tile * KEYS + (lane >> 1) * box < w.len;
+                bad |= !have && tile * KEYS + b * box < w.len;
                 const int at = page * p.page_size + row;
-                const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) / 2u;
-                for (int c = 0; c < 5 && ok; ++c) {
-                    const uint32_t i = c < 4 ? ip : ie, depth = c < 4 ? L::NP : L::NE;
-                    const uint32_t full = base + (c < 4 ? L::PFULL : L::EFULL) + 8 * (i % depth);
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have && c == 0)) * (uint32_t)box * 128u;
+                if (k + 1 < w.cnt) page = box_page(p, w, tile + 1, b, box, row);
+#pragma unroll
+                for (int part = 0; part < 3 && ok; ++part) {   // two halves, then the positional slab
+                    const uint32_t i = part < 2 ? ih : ie, depth = part < 2 ? L::NH : L::NE;
+                    const uint32_t full = base + (part < 2 ? L::HFULL : L::EFULL) + 8 * (i % depth);
                     if (i >= depth)
-                        ok = wait_warp(base + (c < 4 ? L::PEMPTY : L::EEMPTY) + 8 * (i % depth), (i / depth - 1) & 1, limit,
+                        ok = wait_warp(base + (part < 2 ? L::HEMPTY : L::EEMPTY) + 8 * (i % depth), (i / depth - 1) & 1, limit,
                                        failed);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)box * (c < 4 ? 256u : 128u));
+                    if (lane == 0) mbar_arrive_expect_tx(full, bytes * (part < 2 ? 4u : 1u));
                     __syncwarp();
-                    const uint32_t dst = base + (c < 4 ? L::RP + (i % depth) * PAIR : L::RE + (i % depth) * PE) +
-                                         (uint32_t)(lane >> 1) * (uint32_t)box * 128u;
-                    if (have && (c < 4 || (lane & 1) == 0))
-                        tma_load_3d(dst + (uint32_t)(lane & 1) * (PAIR / 2), &maps.cache, 128 * c + 64 * (lane & 1), 0, at,
-                                    full);
-                    if (c < 4) ++ip;
+                    const uint32_t dst = base + (part < 2 ? L::RH + (i % depth) * HALF : L::RE + (i % depth) * KSLAB) +
+                                         (uint32_t)c * KSLAB + (uint32_t)(b * box) * 128u;
+                    if (have && c < (part < 2 ? 4 : 1)) tma_load_3d(dst, &maps.cache, 256 * part + 64 * c, 0, at, full);
+                    if (part < 2) ++ih;
                     else ++ie;
                 }
             }
             if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&plan.err, STATUS_BAD_PAGE);
         }
         // every copy issued here has landed before the CTA ends
-        for (uint32_t k = ip > L::NP ? ip - L::NP : 0; k < ip; ++k)
-            mbar_wait(base + L::PFULL + 8 * (k % L::NP), (k / L::NP) & 1, DRAIN_LIMIT);
+        for (uint32_t k = ih > L::NH ? ih - L::NH : 0; k < ih; ++k)
+            mbar_wait(base + L::HFULL + 8 * (k % L::NH), (k / L::NH) & 1, DRAIN_LIMIT);
         for (uint32_t k = ie > L::NE ? ie - L::NE : 0; k < ie; ++k)
             mbar_wait(base + L::EFULL + 8 * (k % L::NE), (k / L::NE) & 1, DRAIN_LIMIT);
         if (seg > 0) mbar_wait(base + L::QFULL, (seg - 1) & 1, DRAIN_LIMIT);
-    } else if (warp == 4) {
+    } else if (warp >= 4) {
         // ---- products ----
         const MmaType ty = FP16 ? T_F16 : T_BF16;
         const uint32_t id_s = idesc_f16(ty, 64, KEYS, false, false), id_o = idesc_f16(ty, 128, R, true, false);
         uint32_t g = 0, seg = 0;                       // tiles and segments so far
         bool ok = true;
-        auto score = [&](uint32_t t) {                 // S of tile t of the line
-#pragma unroll
-            for (int c = 0; c < 5; ++c) {
-                const uint32_t i = c < 4 ? 4 * t + c : t, depth = c < 4 ? L::NP : L::NE;
-                ok = ok && wait_warp(base + (c < 4 ? L::PFULL : L::EFULL) + 8 * (i % depth), (i / depth) & 1, limit, failed);
-                if (!ok) return;
-                const Desc a = desc_k(base + L::Q + 2 * c * R * 128);
-                const Desc b = desc_k(base + (c < 4 ? L::RP + (i % depth) * PAIR : L::RE + (i % depth) * PE));
-#pragma unroll
-                for (int ks = 0; ks < (c < 4 ? 8 : 4); ++ks)
-                    mma_ss(t_s + 64 * (t & 1), a + ((ks >> 2) * (R * 8) + (ks & 3) * 2), b + ((ks >> 2) * (KEYS * 8) + (ks & 3) * 2),
-                           id_s, c + ks > 0);
-            }
-            mma_commit_warp(base + L::SFULL + 8 * (t & 1));
-            mma_commit_warp(base + L::EEMPTY + 8 * (t % L::NE));
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && wait_warp(base + bar, parity, limit, failed);
+            return ok;
         };
-        for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts), ++seg) {
-            const bool gaps = bad_pages(p, w, lane);
-            ok = wait_warp(base + L::QFULL, seg & 1, limit, failed);
-            if (ok) score(g);
-            if (ok && w.cnt == 1) mma_commit_warp(base + L::QEMPTY);
-            for (int k = 0; k < w.cnt && ok; ++k, ++g) {
-                if (k + 1 < w.cnt) {
-                    score(g + 1);
-                    if (ok && k + 2 == w.cnt) mma_commit_warp(base + L::QEMPTY);
-                }
-                ok = ok && wait_warp(base + L::WFULL, g & 1, limit, failed);
-                if (ok && k == 0 && seg > 0)
-                    ok = wait_warp(base + L::OFREE, (seg - 1) & 1, limit, failed);
-                if (!ok) break;
-                tc_fence_after();
-                const int tile = w.k0 + k;
-                if (gaps || (tile + 1) * KEYS > w.len) {
-                    // rows that do not exist hold whatever was there: zero weights must meet zeros
-                    const unsigned long long keys = tile_keys(p, w, tile, box);
-                    for (int r = 0; r < KEYS; ++r)
-                        if (!(keys >> r & 1))
-                            for (uint32_t c = lane; c < 64; c += 32)
-                                *reinterpret_cast<uint4*>(smem + L::RP + ((4 * g + (c >> 4)) % L::NP) * PAIR +
-                                                          (c >> 3 & 1) * (PAIR / 2) + r * 128 + (c & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
-                    __syncwarp();
-                }
+        auto half = [&](uint32_t i) { return base + L::RH + (i % L::NH) * HALF; };
+        if (warp == 4) {
+            for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts), ++seg) {
+                if (!wait(L::QFULL, seg & 1)) break;
+                for (int k = 0; k < w.cnt && ok; ++k, ++g) {
+                    // S's buffer is free once the weights of the tile before the last are written
+                    if (g >= 2 && !wait(L::WFULL + 8 * (g & 1), ((g - 2) >> 1) & 1)) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {          // O^T: channels 128 c ..
-                    const uint32_t i = (4 * g + c) % L::NP;
-                    const Desc a = desc_mn(base + L::RP + i * PAIR, KEYS), b = desc_k(base + L::P);
+                    for (int part = 0; part < 3; ++part) {
+                        const uint32_t i = part < 2 ? 2 * g + part : g, depth = part < 2 ? L::NH : L::NE;
+                        if (!wait((part < 2 ? L::HFULL : L::EFULL) + 8 * (i % depth), (i / depth) & 1)) break;
+                        const Desc a = desc_k(base + L::Q + 4 * part * R * 128);
+                        const Desc b = desc_k(part < 2 ? half(i) : base + L::RE + (i % depth) * KSLAB);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + c * R, a + 128 * ks, b + 2 * ks, id_o, k + ks > 0);
-                    mma_commit_warp(base + L::PEMPTY + 8 * i);
+                        for (int ks = 0; ks < (part < 2 ? 16 : 4); ++ks)
+                            mma_ss(t_s + 64 * (g & 1), a + ((ks >> 2) * (R * 8) + (ks & 3) * 2),
+                                   b + ((ks >> 2) * (KSLAB / 16) + (ks & 3) * 2), id_s, part + ks > 0);
+                    }
+                    if (!ok) break;
+                    mma_commit_warp(base + L::SFULL + 8 * (g & 1));
+                    mma_commit_warp(base + L::EEMPTY + 8 * (g % L::NE));
+                    if (k + 1 == w.cnt) mma_commit_warp(base + L::QEMPTY);
                 }
-                mma_commit_warp(base + L::VDONE);
+            }
+        } else {
+            for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts), ++seg) {
+                const bool gaps = bad_pages(p, w, lane);
+                for (int k = 0; k < w.cnt; ++k, ++g) {
+                    if (!wait(L::WFULL + 8 * (g & 1), (g >> 1) & 1)) break;
+                    if (k == 0 && seg > 0 && !wait(L::OFREE, (seg - 1) & 1)) break;
+                    tc_fence_after();
+                    const int tile = w.k0 + k;
+                    if (gaps || (tile + 1) * KEYS > w.len) {
+                        // rows that do not exist hold whatever was there: zero weights must meet zeros
+                        const unsigned long long keys = tile_keys(p, w, tile, box);
+                        for (int r = 0; r < KEYS; ++r)
+                            if (!(keys >> r & 1))
+                                for (uint32_t c = lane; c < 64; c += 32)
+                                    *reinterpret_cast<uint4*>(smem + (half(2 * g + (c >> 5)) - base) + (c >> 3 & 3) * KSLAB +
+                                                              r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    const Desc b = desc_k(base + L::P);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {      // O^T: channels 128 c ..
+                        const Desc a = desc_mn(half(2 * g + (c >> 1)) + (c & 1) * 2 * KSLAB, KEYS);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + c * R, a + 128 * ks, b + 2 * ks, id_o, k + ks > 0);
+                        if (c & 1) mma_commit_warp(base + L::HEMPTY + 8 * ((2 * g + (c >> 1)) % L::NH));
+                    }
+                    mma_commit_warp(base + L::VDONE);
+                }
             }
         }
         // every product issued here is done before the tensor memory is freed
-        mma_commit_warp(base + L::DRAIN);
-        mbar_wait(base + L::DRAIN, 0, DRAIN_LIMIT);
+        mma_commit_warp(base + L::DRAIN + 8 * (warp & 1));
+        mbar_wait(base + L::DRAIN + 8 * (warp & 1), 0, DRAIN_LIMIT);
     } else {
         // ---- softmax and output ----
         const float c = p.scale * 1.4426950408889634f;
@@ -438,7 +448,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(base + L::WFULL);
+                if (lane == 0) mbar_arrive(base + L::WFULL + 8 * (g & 1));
             }
             if (ok) ok = wait_warp(base + L::VDONE, (g - 1) & 1, limit, failed);
             ok = bar_and_named(1, 128, ok);
@@ -459,27 +469,20 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             bar_and_named(1, 128, true);
             const int have = min(R, rows - w.mt * R);
 #pragma unroll 1
-            for (int b = 0; b < 4 * R; b += 16) {
-                float o[16];
-                tmem_ld16(tmem + quad + b, o);
+            for (int b = 0; b < 4 * R; b += 32) {
+                float o[32];
+                tmem_ld32(tmem + quad + b, o);
                 tmem_ld_wait();
-                const int ch = b / R * 128 + 32 * warp + lane;
-                if (whole) {
-                    uint16_t* out = static_cast<uint16_t*>(p.o) + ((long long)w.n * rows + w.mt * R) * LAT_C + ch;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int rr = b % R + e;
-                        const float f = fact[rr];
-                        if (rr < have) out[(long long)rr * LAT_C] = (uint16_t)pack2<FP16>(f == 0.f ? 0.f : o[e] * f, 0.f);
-                    }
-                } else {
-                    float* out = sc.o + (long long)slot * R * LAT_C + ch;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int rr = b % R + e;
-                        const float f = fact[rr];
-                        if (rr < have) out[rr * LAT_C] = f == 0.f ? 0.f : o[e] * f;
-                    }
+                for (int e = 0; e < 32; ++e) {
+                    const int rr = (b + e) % R, ch = (b + e) / R * 128 + 32 * warp + lane;
+                    const float f = fact[rr], v = f == 0.f ? 0.f : o[e] * f;
+                    if (rr >= have) continue;
+                    if (whole)
+                        static_cast<uint16_t*>(p.o)[((long long)w.n * rows + w.mt * R + rr) * LAT_C + ch] =
+                            (uint16_t)pack2<FP16>(v, 0.f);
+                    else
+                        sc.o[((long long)slot * R + rr) * LAT_C + ch] = v;
                 }
             }
             tc_fence_before();
@@ -493,17 +496,20 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     if (tid == 0) sc.err[cta] = plan.err | (plan.failed ? STATUS_TIMEOUT : 0u);
 }
 
-// Joins the parts of the units that were cut, one row a group of warps:
-// lse = log sum exp(lse_i), o = sum exp(lse_i - lse) o_i, in the order of the
-// parts; writes zeros for empty sequences.
-template <bool FP16>
+// Joins the parts of the units that were cut: lse = log sum exp(lse_i),
+// o = sum exp(lse_i - lse) o_i, in a fixed order; writes zeros for empty
+// sequences.  Many units: a warp a row (WARPS = 1), 512 channels.  Few, with
+// many parts each: WARPS = 8 warps share the parts of 128 channels of a row
+// (one sequence of 65536, 152 parts of 32 rows: 26 us by 32 CTAs).
+template <int WARPS, bool FP16>
 __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ DecodeParams p,
-                                                          const __grid_constant__ DecodeScratch sc, int R, int mts,
-                                                          int rows_cta, int ctas) {
-    __shared__ float acc[8][LAT_C];
+                                                          const __grid_constant__ DecodeScratch sc, int R, int mts, int ctas) {
+    constexpr int V = WARPS == 1 ? 4 : 1;              // groups of 128 channels a warp
+    __shared__ float4 acc[WARPS == 1 ? 1 : 8][32];
     __shared__ float stat[8][2];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = p.S * p.H;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) {
         uint32_t err = 0;
         for (int c = lane; c < ctas; c += 32) err |= sc.err[c];
         err = __reduce_or_sync(0xffffffffu, err);
@@ -518,61 +524,58 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
         c1 = (int)(((w0 + tiles) * g - 1) / total);
         if (c0 == c1) return;
     }
-    const int group = 8 / rows_cta;                    // warps of a row
-    const int r = blockIdx.y * rows_cta + warp / group, part = warp % group;
-    const bool there = r < R && mt * R + r < rows;
-    float m = -INFINITY, l = 0.f, o[16];
+    const int r = WARPS == 1 ? blockIdx.y * 8 + warp : blockIdx.y, part = WARPS == 1 ? 0 : warp;
+    if (r >= R || mt * R + r >= rows) return;          // a whole CTA where warps work together
+    // the first part of c0's unit is its last segment, unless the unit starts the range
+    const int slot0 = 2 * c0 + (tiles > 0 && c0 * total / g != w0 ? 1 : 0);
+    auto slot_of = [&](int c) { return c == c0 ? slot0 : 2 * c; };
+    float m = -INFINITY, l = 0.f;
+    float4 o[V];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = 0.f;
-    if (there) {
-        auto slot_of = [&](int c) { return 2 * c + (c > c0 || c * total / g == w0 ? 0 : 1); };
-        for (int c = c0 + part; c <= c1; c += group) m = fmaxf(m, sc.lse[slot_of(c) * R + r]);
-        for (int c = c0 + part; c <= c1; c += group) {
-            const int s = slot_of(c);
-            const float lse = sc.lse[s * R + r];
-            const float w = lse == -INFINITY ? 0.f : expf(lse - m);
-            const float4* src = reinterpret_cast<const float4*>(sc.o + ((long long)s * R + r) * LAT_C);
-            l += w;
+    for (int e = 0; e < V; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, sc.lse[slot_of(c) * R + r]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 v = src[lane + 32 * e];
-                o[4 * e] += w * v.x;
-                o[4 * e + 1] += w * v.y;
-                o[4 * e + 2] += w * v.z;
-                o[4 * e + 3] += w * v.w;
-            }
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll 4
+    for (int c = c0 + part; c <= c1; c += WARPS) {
+        const int s = slot_of(c);
+        const float lse = sc.lse[s * R + r];
+        const float w = lse == -INFINITY ? 0.f : expf(lse - m);
+        const float4* src = reinterpret_cast<const float4*>(sc.o + ((long long)s * R + r) * LAT_C) +
+                            (WARPS == 1 ? 0 : blockIdx.z * 32) + lane;
+        l += w;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float4 v = src[32 * e];
+            o[e].x += w * v.x;
+            o[e].y += w * v.y;
+            o[e].z += w * v.z;
+            o[e].w += w * v.w;
         }
     }
-    if (group > 1) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<float4*>(&acc[warp][4 * (lane + 32 * e)]) =
-                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        if (lane == 0) stat[warp][0] = m, stat[warp][1] = l;
+    if constexpr (WARPS > 1) {
+        acc[warp][lane] = o[0];
+        if (lane == 0) stat[warp][0] = l;
         __syncthreads();
-        if (part != 0) return;
-        float top = m;
-        for (int k = 1; k < group; ++k) top = fmaxf(top, stat[warp + k][0]);
+        if (warp != 0) return;
         l = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.f;
-        for (int k = 0; k < group; ++k) {
-            const float mk = stat[warp + k][0], f = mk == -INFINITY ? 0.f : expf(mk - top);
-            l += f * stat[warp + k][1];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] += f * acc[warp + k][4 * (lane + 32 * (e >> 2)) + (e & 3)];
+        o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < WARPS; ++k) {
+            const float4 v = acc[k][lane];
+            l += stat[k][0];
+            o[0].x += v.x;
+            o[0].y += v.y;
+            o[0].z += v.z;
+            o[0].w += v.w;
         }
-        m = top;
     }
-    if (!there) return;
     const long long at = (long long)n * rows + mt * R + r;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at * LAT_C);
+    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at * LAT_C) + (WARPS == 1 ? 0 : blockIdx.z * 32) + lane;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        out[lane + 32 * e] = make_uint2(pack2<FP16>(o[4 * e] * inv, o[4 * e + 1] * inv),
-                                        pack2<FP16>(o[4 * e + 2] * inv, o[4 * e + 3] * inv));
-    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
+    for (int e = 0; e < V; ++e)
+        out[32 * e] = make_uint2(pack2<FP16>(o[e].x * inv, o[e].y * inv), pack2<FP16>(o[e].z * inv, o[e].w * inv));
+    if (lane == 0 && blockIdx.z == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 int unit_rows(int S, int H) { return (long long)S * H <= 16 ? 16 : (long long)S * H <= 32 ? 32 : 64; }
@@ -588,11 +591,19 @@ cudaError_t launch(const DecodeParams& p, const DecMaps& maps, const DecodeScrat
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int mts = (p.S * p.H + R - 1) / R;
-    // few units: a CTA for each row, its warps sharing the parts; many: a warp a row
-    const int rows_cta = (long long)p.N * mts * R <= 1024 ? 1 : 8;
-    latent_join_kernel<FP16><<<dim3(p.N * mts, (R + rows_cta - 1) / rows_cta), 256, 0, stream>>>(p, sc, R, mts, rows_cta,
-                                                                                                DEC_CTAS);
-    return cudaGetLastError();
+    // The join may be set up while the last CTAs of the kernel before it run: it waits for them itself.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const bool few = (long long)p.N * mts * R <= 1024;
+    cfg.gridDim = few ? dim3(p.N * mts, R, 4) : dim3(p.N * mts, (R + 7) / 8);
+    return few ? cudaLaunchKernelEx(&cfg, latent_join_kernel<8, FP16>, p, sc, R, mts, DEC_CTAS)
+               : cudaLaunchKernelEx(&cfg, latent_join_kernel<1, FP16>, p, sc, R, mts, DEC_CTAS);
 }
 
 }  // namespace
