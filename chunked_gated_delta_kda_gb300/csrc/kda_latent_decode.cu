@@ -18,12 +18,14 @@
 // A unit inside one range is finished by its CTA; the parts of a cut one go
 // to the workspace with their log-sum-exp and are joined by a second kernel,
 // which also writes the empty sequences.
-//   warps 0-3  softmax (row 16 w + l in lane l < 16 of warp w, as an M = 64
-//              product lays its rows out), rescaling and output of O
+//   warps 0-3  softmax (row 16 w + l in lanes l and 16 + l of warp w, half of
+//              the keys each: an M = 64 product has its rows in 16 lanes of
+//              each quarter of tensor memory), rescaling and output of O
 //   warps 4, 5  issue the products, 4 the scores and 5 those with the values:
 //              the values' part of a tile must not wait for the next tile's
 //              loads, which its end makes room for
-//   warp 6     loads
+//   warp 6     loads (asking besides for pages a few tiles ahead to be brought
+//              into the L2 cost time: N=256 L=4096 255 us instead of 215)
 #include "kda_latent_decode.cuh"
 #include "kda_latent_mma.cuh"
 
@@ -36,6 +38,11 @@ constexpr int KEYS = 64;                                 // keys of a tile
 constexpr uint32_t KSLAB = KEYS * 128;                   // 64 channels of a tile
 constexpr uint32_t HALF = 4 * KSLAB;                     // 256 latent channels of a tile: the unit of the ring
 constexpr float RESCALE_LOG2 = 8.f;
+
+// 64-bit quotient of non-negative numbers that mostly fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // Shared-memory layout for R rows of a unit: Q, P, then the two rings.
 template <int R>
@@ -223,15 +230,15 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             if (tid == 0) sc.prefix[p.N] = total;
         }
         if (cta < g) {
-            const long long lo = cta * total / g, hi = (cta + 1) * total / g;
+            const long long lo = quotient(cta * total, g), hi = quotient((cta + 1) * total, g);
             if (lo >= at && lo < at + sum) {           // one thread: the range starts in its sequences
                 int n = a;
                 for (;; ++n) {
                     const int t = (clipped_len(p, n) + KEYS - 1) / KEYS;
                     if (lo < at + (long long)t * mts) {
                         plan.n = n;
-                        plan.mt = (int)((lo - at) / t);
-                        plan.k0 = (int)((lo - at) % t);
+                        plan.mt = (int)quotient(lo - at, t);
+                        plan.k0 = (int)(lo - at - (long long)plan.mt * t);
                         break;
                     }
                     at += (long long)t * mts;
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
         // ---- softmax and output ----
         const float c = p.scale * 1.4426950408889634f;
         const uint32_t quad = (uint32_t)warp << 21;    // this warp's lanes
-        const int r = 16 * warp + (lane & 15);         // its row; lanes 16-31 repeat it and store nothing
+        const int r = 16 * warp + (lane & 15);         // its row; lanes l and 16 + l have a half of the keys each
         float* fact = reinterpret_cast<float*>(smem + L::FACT);
         uint32_t g = 0;
         bool ok = true;
@@ -380,21 +387,21 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const int tile = w.k0 + k;
-                float x[2][32];
-                tmem_ld32(t_s + 64 * (g & 1) + quad, x[0]);
-                tmem_ld32(t_s + 64 * (g & 1) + 32 + quad, x[1]);
+                float x[32];
+                tmem_ld_half32(t_s + 64 * (g & 1) + quad, x);
                 tmem_ld_wait();
                 const int have = lim - tile * KEYS;
                 if (gaps || __any_sync(0xffffffffu, have < KEYS)) {
                     unsigned long long keys = gaps ? tile_keys(p, w, tile, box) : ~0ull;
                     keys &= have >= KEYS ? ~0ull : have > 0 ? (1ull << have) - 1 : 0ull;
+                    const uint32_t mine = (uint32_t)(keys >> (lane & 16) * 2);
 #pragma unroll
-                    for (int e = 0; e < KEYS; ++e)
-                        if (!(keys >> e & 1)) x[e >> 5][e & 31] = -INFINITY;
+                    for (int e = 0; e < 32; ++e)
+                        if (!(mine >> e & 1)) x[e] = -INFINITY;
                 }
-                const float top = fmaxf(max32(x[0]), max32(x[1]));
-                bool grown = top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m);
-                grown = grown && r < R && lane < 16;
+                float top = max32(x);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const bool grown = r < R && (top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m));
                 // P's buffer is free, and O stands still, once the tile before is done
                 if (k > 0) ok = wait_warp(base + L::VDONE, (g - 1) & 1, limit, failed);
                 if (!bar_and_named(1, 128, ok && !grown)) {
@@ -427,21 +434,19 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
+                    for (int q = 0; q < 4; ++q) {
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int at = 8 * q + 2 * e;
-                            float u = x[at >> 5][at & 31], v = x[at >> 5][(at & 31) + 1];
+                            float u = x[8 * q + 2 * e], v = x[8 * q + 2 * e + 1];
                             fma2(u, v, c, -mc);
                             u = ex2(u);
                             v = ex2(v);
                             add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], u, v);
                             o[e] = pack2<FP16>(u, v);
                         }
-                        if (lane < 16)
-                            *reinterpret_cast<uint4*>(smem + L::P + r * 128 + ((q ^ (r & 7)) * 16)) =
-                                make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(smem + L::P + r * 128 + (((q + (lane >> 4) * 4) ^ (r & 7)) * 16)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
@@ -455,6 +460,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             // ---- the segment's rows ----
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
             const bool whole = w.cnt == w.tiles;
             const int slot = 2 * cta + (w.first ? 0 : 1);
             if (r < R && lane < 16) {
@@ -468,21 +474,32 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             }
             bar_and_named(1, 128, true);
             const int have = min(R, rows - w.mt * R);
+            constexpr int RC = R < 32 ? R : 32;        // rows at a time
 #pragma unroll 1
-            for (int b = 0; b < 4 * R; b += 32) {
-                float o[32];
-                tmem_ld32(tmem + quad + b, o);
-                tmem_ld_wait();
+            for (int r0 = 0; r0 < R; r0 += RC) {
+                float f[RC];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int rr = (b + e) % R, ch = (b + e) / R * 128 + 32 * warp + lane;
-                    const float f = fact[rr], v = f == 0.f ? 0.f : o[e] * f;
-                    if (rr >= have) continue;
-                    if (whole)
-                        static_cast<uint16_t*>(p.o)[((long long)w.n * rows + w.mt * R + rr) * LAT_C + ch] =
-                            (uint16_t)pack2<FP16>(v, 0.f);
-                    else
-                        sc.o[((long long)slot * R + rr) * LAT_C + ch] = v;
+                for (int e = 0; e < RC; ++e) f[e] = fact[r0 + e];
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float o[32];
+                    if constexpr (R < 32) tmem_ld16(tmem + quad + b * R, reinterpret_cast<float(&)[16]>(o));
+                    else tmem_ld32(tmem + quad + b * R + r0, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < RC; ++e) o[e] = f[e] == 0.f ? 0.f : o[e] * f[e];
+                    const int ch = 128 * b + 32 * warp + lane, count = have - r0;
+                    if (whole) {
+                        uint16_t* out = static_cast<uint16_t*>(p.o) + ((long long)w.n * rows + w.mt * R + r0) * LAT_C + ch;
+#pragma unroll
+                        for (int e = 0; e < RC; ++e)
+                            if (e < count) out[e * LAT_C] = (uint16_t)pack2<FP16>(o[e], 0.f);
+                    } else {
+                        float* out = sc.o + ((long long)slot * R + r0) * LAT_C + ch;
+#pragma unroll
+                        for (int e = 0; e < RC; ++e)
+                            if (e < count) out[e * LAT_C] = o[e];
+                    }
                 }
             }
             tc_fence_before();
