@@ -164,6 +164,10 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     const int rows = p.S * p.H, mts = (rows + R - 1) / R;
     const int box = min(p.page_size, KEYS);
 
+    if (tid == 32) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.cache) : "memory");
+    }
     if (tid == 0) {
         for (uint32_t i = 0; i < L::NH; ++i) {
             mbar_init(base + L::HFULL + 8 * i, 1);
@@ -537,37 +541,56 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     const long long w0 = sc.prefix[n] + mt * tiles, g = min((long long)ctas, total);
     int c0 = 0, c1 = -1;
     if (tiles > 0) {
-        c0 = (int)(((w0 + 1) * g - 1) / total);
-        c1 = (int)(((w0 + tiles) * g - 1) / total);
+        c0 = (int)quotient((w0 + 1) * g - 1, total);
+        c1 = (int)quotient((w0 + tiles) * g - 1, total);
         if (c0 == c1) return;
     }
     const int r = WARPS == 1 ? blockIdx.y * 8 + warp : blockIdx.y, part = WARPS == 1 ? 0 : warp;
     if (r >= R || mt * R + r >= rows) return;          // a whole CTA where warps work together
     // the first part of c0's unit is its last segment, unless the unit starts the range
-    const int slot0 = 2 * c0 + (tiles > 0 && c0 * total / g != w0 ? 1 : 0);
+    const int slot0 = 2 * c0 + (tiles > 0 && quotient(c0 * total, g) != w0 ? 1 : 0);
     auto slot_of = [&](int c) { return c == c0 ? slot0 : 2 * c; };
     float m = -INFINITY, l = 0.f;
     float4 o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* src = reinterpret_cast<const float4*>(sc.o + (long long)r * LAT_C) + (WARPS == 1 ? 0 : blockIdx.z * 32) + lane;
+    auto part_of = [&](int c) { return src + (long long)slot_of(c) * R * (LAT_C / 4); };
+    // the parts' values do not depend on the weights: ask for them first
+    constexpr int BATCH = WARPS == 1 ? 2 : 10;
+    float4 v[BATCH][V];
+    auto fetch = [&](int first) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            if (first + k * WARPS <= c1) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[k][e] = part_of(first + k * WARPS)[32 * e];
+            }
+    };
+    fetch(c0 + part);
     for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, sc.lse[slot_of(c) * R + r]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-#pragma unroll 4
-    for (int c = c0 + part; c <= c1; c += WARPS) {
-        const int s = slot_of(c);
-        const float lse = sc.lse[s * R + r];
-        const float w = lse == -INFINITY ? 0.f : expf(lse - m);
-        const float4* src = reinterpret_cast<const float4*>(sc.o + ((long long)s * R + r) * LAT_C) +
-                            (WARPS == 1 ? 0 : blockIdx.z * 32) + lane;
-        l += w;
+    for (int c = c0 + part; c <= c1; c += BATCH * WARPS) {
+        if (c > c0 + part) fetch(c);
+        const int mine = c + lane * WARPS;             // lane k: the weight of the batch's part k
+        float w = 0.f;
+        if (lane < BATCH && mine <= c1) {
+            const float lse = sc.lse[slot_of(mine) * R + r];
+            w = lse == -INFINITY ? 0.f : expf(lse - m);
+        }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float4 v = src[32 * e];
-            o[e].x += w * v.x;
-            o[e].y += w * v.y;
-            o[e].z += w * v.z;
-            o[e].w += w * v.w;
+        for (int k = 0; k < BATCH; ++k) {
+            if (c + k * WARPS > c1) break;
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            l += wk;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                o[e].x += wk * v[k][e].x;
+                o[e].y += wk * v[k][e].y;
+                o[e].z += wk * v[k][e].z;
+                o[e].w += wk * v[k][e].w;
+            }
         }
     }
     if constexpr (WARPS > 1) {
