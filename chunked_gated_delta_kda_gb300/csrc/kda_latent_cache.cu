@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(TAB_THREADS) block_tables_kernel(const __grid_
     if (me == 0) {
         bad |= tok0 > p.num_tokens;
         p.cu[p.N] = (int)min(tok0, (long long)INT32_MAX);
-        p.head_out[0] = (int)max(min(head + page0, (long long)p.num_free), min(head, (long long)p.num_free));
+        p.head_out[0] = (int)min(head + page0, (long long)p.num_free);
     }
     if (bad) set_status(p.status, STATUS_BAD_PAGE);
 }

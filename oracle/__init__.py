@@ -20,6 +20,9 @@ Independent forms:
   * ``backward.kda_backward``: gradients of <do, o> + <dht, ht> by fp64
     torch autograd through the per-token recurrence (``backward.py``): the
     oracle of the backward entry point.
+  * ``latent``: latent attention (forward, backward, decode over the paged
+    cache), the cache append and the block tables from their definitions
+    (``latent.py``).
 
 Parity pins live in ``tests/test_oracle*.py``.
 """

@@ -1,0 +1,139 @@
+"""Host-side checks of the latent-attention entry points and wrappers: sizes
+and refusals, all before any CUDA call."""
+
+import ctypes
+
+import pytest
+import torch
+
+from chunked_gated_delta_kda_gb300 import binding, latent
+
+cpu_only = pytest.mark.skipif(torch.cuda.is_available(), reason="host-pointer validation cases run on CPU-only hosts")
+
+
+def host_block():
+    buf = (ctypes.c_uint8 * 4096)()
+    return buf, ctypes.addressof(buf) + (-ctypes.addressof(buf) % 256)
+
+
+def caller(fn, defaults):
+    def call(**kw):
+        assert set(kw) <= set(defaults), kw
+        return fn(*{**defaults, **kw}.values())
+    return call
+
+
+def test_workspace_sizes():
+    lib = binding.load_library()
+    r256 = lambda b: (b + 255) // 256 * 256  # noqa: E731
+
+    def bwd(slots, rows, H):   # header, two tables of 64 a tile slot and head, 64 floats a key and head
+        return 256 + r256(slots * H * 128 * 4) + rows * H * 64 * 4
+
+    assert lib.kda_latent_bwd_workspace_bytes(2, 2048, 2048, 8, 2) == bwd(64, 4096, 8)
+    assert lib.kda_latent_bwd_workspace_bytes(1, 9192, 9192, 32, 6) == bwd(9192 // 64 + 6, 9192, 32)
+    assert lib.kda_latent_bwd_workspace_bytes(1, 0, 0, 1, 1) > 0
+    for bad in ((0, 1, 1, 1, 1), (1, -1, 1, 1, 1), (1, 1, -1, 1, 1), (1, 1, 1, 0, 1), (1, 1, 1, 1, 0),
+                (1, 1, 1, 65536, 1), (1 << 16, 1 << 16, 1, 1, 1)):
+        assert lib.kda_latent_bwd_workspace_bytes(*bad) == 0
+
+    def dec(n, rows):          # header, 152 error words, offsets, two parts a CTA
+        return 256 + 768 + r256((n + 1) * 8) + r256(304 * rows * 4) + 304 * rows * 512 * 4
+
+    assert lib.kda_latent_decode_workspace_bytes(1, 1, 16) == dec(1, 16)
+    assert lib.kda_latent_decode_workspace_bytes(256, 1, 32) == dec(256, 32)
+    assert lib.kda_latent_decode_workspace_bytes(3, 4, 128) == dec(3, 64)
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (65536, 1, 1), (65535, 65535, 2)):
+        assert lib.kda_latent_decode_workspace_bytes(*bad) == 0
+
+
+def test_status_string():
+    assert b"page" in binding.load_library().kda_status_str(8)
+
+
+@cpu_only
+def test_fwd_refusals():
+    keep, p = host_block()
+    call = caller(binding.load_library().kda_latent_fwd, dict(
+        q=p, kv=p, pe=p, stride=64, scale=0.0, cu_q=None, cu_k=None, o=p, lse=p, B=1, Tq=8, Tk=8, H=1, N=1, flags=0,
+        ws=None, stream=None))
+    for kw in (dict(q=None), dict(kv=None), dict(pe=None), dict(o=None), dict(q=p + 8), dict(kv=p + 2), dict(pe=p + 4),
+               dict(o=p + 8), dict(lse=p + 2), dict(ws=p + 64), dict(stride=63), dict(stride=56), dict(stride=68),
+               dict(B=0), dict(Tq=-1), dict(Tk=-1), dict(H=0), dict(N=0), dict(N=2), dict(H=65536), dict(cu_q=p),
+               dict(cu_k=p), dict(cu_q=p, cu_k=p, B=2, N=2), dict(cu_q=p + 2, cu_k=p), dict(flags=1), dict(flags=512)):
+        assert call(**kw) == 1, kw
+
+
+@cpu_only
+def test_bwd_refusals():
+    keep, p = host_block()
+    lib = binding.load_library()
+    need = lib.kda_latent_bwd_workspace_bytes(1, 8, 8, 1, 1)
+    call = caller(lib.kda_latent_bwd, dict(
+        q=p, kv=p, pe=p, stride=64, o=p, lse=p, do=p, scale=0.0, cu_q=None, cu_k=None, dq=p, dkv=p, dpe=p, B=1, Tq=8,
+        Tk=8, H=1, N=1, flags=0, ws=p, wsb=need, stream=None))
+    for kw in (dict(q=None), dict(o=None), dict(lse=None), dict(do=None), dict(dq=None), dict(dkv=None), dict(dpe=None),
+               dict(ws=None), dict(wsb=need - 1), dict(ws=p + 16), dict(o=p + 8), dict(do=p + 8), dict(dq=p + 8),
+               dict(dkv=p + 8), dict(dpe=p + 8), dict(N=2), dict(stride=65), dict(flags=2)):
+        assert call(**kw) == 1, kw
+
+
+@cpu_only
+def test_decode_refusals():
+    keep, p = host_block()
+    lib = binding.load_library()
+    need = lib.kda_latent_decode_workspace_bytes(2, 1, 4)
+    call = caller(lib.kda_latent_decode, dict(
+        q=p, cache=p, pages=4, page=64, table=p, width=2, lens=p, scale=0.0, o=p, lse=p, N=2, S=1, H=4, flags=0, ws=p,
+        wsb=need, stream=None))
+    for kw in (dict(q=None), dict(cache=None), dict(table=None), dict(lens=None), dict(o=None), dict(ws=None),
+               dict(pages=0), dict(width=0), dict(page=0), dict(page=8), dict(page=48), dict(page=96), dict(page=-64),
+               dict(pages=1 << 26), dict(width=1 << 26), dict(N=0), dict(S=0), dict(H=0), dict(flags=256),
+               dict(wsb=need - 1), dict(q=p + 8), dict(cache=p + 8), dict(table=p + 2), dict(lens=p + 1), dict(o=p + 8),
+               dict(ws=p + 128)):
+        assert call(**kw) == 1, kw
+
+
+@cpu_only
+def test_append_refusals():
+    keep, p = host_block()
+    call = caller(binding.load_library().kda_latent_append, dict(
+        rows=p, stride=576, slots=p, weight=None, eps=1e-6, cache=p, num=64, T=1, flags=0, ws=None, stream=None))
+    for kw in (dict(rows=None), dict(slots=None), dict(cache=None), dict(stride=575), dict(stride=580), dict(T=-1),
+               dict(num=-1), dict(flags=256), dict(rows=p + 8), dict(slots=p + 4), dict(weight=p + 8), dict(cache=p + 2),
+               dict(weight=p, eps=-1.0), dict(weight=p, eps=float("nan")), dict(ws=p + 4)):
+        assert call(**kw) == 1, kw
+
+
+@cpu_only
+def test_tables_refusals():
+    keep, p = host_block()
+    call = caller(binding.load_library().kda_block_tables, dict(
+        lens=p, new=p, table=p, width=2, free=p, num_free=1, head=p, page=16, slots=p, tokens=1, cu=p, out=p, head_out=p,
+        N=1, ws=None, stream=None))
+    for kw in (dict(lens=None), dict(new=None), dict(table=None), dict(free=None), dict(head=None), dict(slots=None),
+               dict(cu=None), dict(out=None), dict(head_out=None), dict(N=0), dict(width=-1), dict(num_free=-1),
+               dict(tokens=-1), dict(page=0), dict(page=24), dict(slots=p + 4), dict(lens=p + 2), dict(ws=p + 32)):
+        assert call(**kw) == 1, kw
+
+
+def test_wrappers_refuse_what_the_kernels_do_not_take():
+    """CPU tensors, types, shapes: a clear error and no fallback."""
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d)  # noqa: E731
+    i32 = torch.int32
+    with pytest.raises(ValueError, match="CUDA"):
+        latent.latent_fwd(z(1, 4, 2, 192), z(1, 4, 2, 256), z(1, 4, 64))
+    with pytest.raises(TypeError, match="bfloat16 or"):
+        latent.latent_fwd(z(1, 4, 2, 192, d=torch.float32), z(1, 4, 2, 256), z(1, 4, 64))
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        latent.latent_decode([1], z(1, 16, 576), z(1, 1, d=i32), z(1, d=i32))
+    with pytest.raises(ValueError, match="CUDA"):
+        latent.latent_decode(z(1, 1, 1, 576), z(1, 16, 576), z(1, 1, d=i32), z(1, d=i32))
+    with pytest.raises(TypeError, match="rows must be"):
+        latent.latent_append(z(1, 576, d=i32), z(1, d=torch.int64), z(1, 16, 576))
+    with pytest.raises(ValueError, match="CUDA"):
+        latent.latent_append(z(1, 576), z(1, d=torch.int64), z(1, 16, 576))
+    with pytest.raises(ValueError, match="CUDA"):
+        latent.block_tables(z(1, d=i32), z(1, d=i32), z(1, 1, d=i32), z(1, d=i32), z(1, d=i32), 16, 1)
+    with pytest.raises(TypeError, match="seq_lens"):
+        latent.block_tables(z(1, d=torch.int64), z(1, d=i32), z(1, 1, d=i32), z(1, d=i32), z(1, d=i32), 16, 1)

@@ -1,0 +1,452 @@
+"""Latent attention, its cache and its tables on the GPU against the 64-bit
+oracle (``oracle.latent``), element by element within the oracle's bound of
+what the types' roundings and 32-bit sums may add."""
+
+import pytest
+import torch
+
+from oracle import latent as ol
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+U = {BF: 2.0 ** -8, FP: 2.0 ** -11}
+TINY = {BF: 0.0, FP: 2.0 ** -25}
+
+
+def api():
+    from chunked_gated_delta_kda_gb300 import latent
+    return latent
+
+
+def near(got, want, err, what=""):
+    got = got.double().cpu()
+    assert got.shape == want.shape, what
+    inf = torch.isinf(want)
+    assert torch.equal(inf, torch.isinf(got)) and torch.equal(want[inf], got[inf]), what
+    off = ((got - want).abs() - err)[~inf]
+    assert torch.isfinite(got[~inf]).all() and (off <= 0).all(), (what, off.max().item())
+
+
+def cu(lens):
+    return torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
+
+
+def expanded(lens_q, lens_k, H, dtype, seed=0, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    q, kv = (r(sum(lens_q), H, 192) * size).to(dtype), r(sum(lens_k), H, 256).to(dtype)
+    return q, kv, r(sum(lens_k), 64).to(dtype), r(sum(lens_q), H, 128).to(dtype)
+
+
+def run_fwd(q, kv, pe, lens_q, lens_k, causal=True, **kw):
+    o, lse = api().latent_fwd(q[None].cuda(), kv[None].cuda(), pe[None].cuda(), causal=causal, cu_seqlens_q=cu(lens_q),
+                              cu_seqlens_k=cu(lens_k), **kw)
+    return o[0], lse[0]
+
+
+CASES = [
+    # queries, keys, heads, type, causal
+    ([1], [1], 1, BF, True),
+    ([37], [37], 3, BF, True),
+    ([128], [128], 1, FP, False),
+    ([129], [129], 2, BF, True),
+    ([256, 257], [256, 257], 2, FP, True),
+    ([64, 65, 1], [127, 128, 300], 2, BF, True),          # prefixes; one token behind 299
+    ([1, 0, 3, 130], [2, 5, 0, 10], 2, BF, False),        # sequences without queries, without keys
+    ([300, 5], [100, 1], 2, BF, True),                    # more queries than keys: rows that see nothing
+    ([700], [900], 1, BF, True),
+    ([513], [1100], 1, FP, False),
+]
+
+
+@pytest.mark.parametrize("lens_q,lens_k,H,dtype,causal", CASES)
+def test_fwd(lens_q, lens_k, H, dtype, causal):
+    q, kv, pe, _ = expanded(lens_q, lens_k, H, dtype, seed=sum(lens_q))
+    o, lse = run_fwd(q, kv, pe, lens_q, lens_k, causal)
+    ro, rl, eo, el = ol.latent_fwd(q, kv, pe, lens_q, lens_k, causal, u=U[dtype], tiny=TINY[dtype])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+
+
+@pytest.mark.parametrize("lens_q,lens_k,H,dtype,causal", CASES)
+def test_bwd(lens_q, lens_k, H, dtype, causal):
+    q, kv, pe, do = expanded(lens_q, lens_k, H, dtype, seed=sum(lens_q))
+    o, lse = run_fwd(q, kv, pe, lens_q, lens_k, causal)
+    got = api().latent_bwd(q[None].cuda(), kv[None].cuda(), pe[None].cuda(), o[None], lse[None], do[None].cuda(),
+                           causal=causal, cu_seqlens_q=cu(lens_q), cu_seqlens_k=cu(lens_k))
+    want = ol.latent_bwd(q, kv, pe, do, lens_q, lens_k, causal, u=U[dtype], tiny=TINY[dtype])
+    for g, w, e, name in zip(got, want[:3], want[3:], ("dq", "dkv", "dk_pe")):
+        near(g[0], w, e, name)
+
+
+@pytest.mark.parametrize("size,scale", [(20.0, None), (1.0, 0.5), (0.01, None)])
+def test_fwd_peaked_and_flat_rows(size, scale):
+    """Scores far apart (the running maximum moves often) and all alike."""
+    lens = [300, 200]
+    q, kv, pe, _ = expanded(lens, lens, 2, BF, seed=7, size=size)
+    o, lse = run_fwd(q, kv, pe, lens, lens, scale=scale)
+    ro, rl, eo, el = ol.latent_fwd(q, kv, pe, lens, lens, scale=scale, u=U[BF])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+
+
+def test_fixed_length_is_the_packed_result():
+    q, kv, pe, do = expanded([200, 200], [200, 200], 3, BF, seed=8)
+    o, lse = run_fwd(q, kv, pe, [200, 200], [200, 200])
+    two = lambda t: t.view(2, 200, *t.shape[1:]).cuda()  # noqa: E731
+    of, lf = api().latent_fwd(two(q), two(kv), two(pe))
+    assert torch.equal(of.view_as(o), o) and torch.equal(lf.view_as(lse), lse)
+    a = api().latent_bwd(two(q), two(kv), two(pe), of, lf, two(do))
+    c = cu([200, 200])
+    b = api().latent_bwd(q[None].cuda(), kv[None].cuda(), pe[None].cuda(), o[None], lse[None], do[None].cuda(),
+                         cu_seqlens_q=c, cu_seqlens_k=c)
+    for x, y in zip(a, b):
+        assert torch.equal(x.reshape(y.shape), y)
+
+
+def test_views_and_strides():
+    """k_pe in place inside wider rows; views that start off a 16-byte boundary and transposed ones are copied."""
+    q, kv, pe, do = (t.cuda() for t in expanded([150], [150], 2, BF, seed=9))
+    o, lse = api().latent_fwd(q[None], kv[None], pe[None])
+    wide = torch.full((1, 150, 576), float("nan"), dtype=BF, device="cuda")
+    wide[..., 512:] = pe
+    off = torch.zeros(150 * 64 + 1, dtype=BF, device="cuda")
+    off[1:] = pe.flatten()
+    qt = q.transpose(0, 1).contiguous().transpose(0, 1)[None]
+    for q2, pe2 in ((q[None], wide[..., 512:]), (q[None], off[1:].view(1, 150, 64)), (qt, pe[None])):
+        o2, lse2 = api().latent_fwd(q2, kv[None], pe2)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        a, b = (api().latent_bwd(x, kv[None], y, o, lse, do[None]) for x, y in ((q[None], pe[None]), (q2, pe2)))
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_other_sequences_never_reach_a_result(bad):
+    lens_q, lens_k = [70, 90, 130], [70, 90, 130]
+    q, kv, pe, do = expanded(lens_q, lens_k, 2, BF, seed=10)
+    runs = []
+    for fill in (None, bad):
+        x = [t.clone() for t in (q, kv, pe, do)]
+        if fill is not None:
+            for t in x:
+                t[:70] = fill
+                t[160:] = fill
+        o, lse = run_fwd(*x[:3], lens_q, lens_k)
+        g = api().latent_bwd(*(t[None].cuda() for t in x[:3]), o[None], lse[None], x[3][None].cuda(),
+                             cu_seqlens_q=cu(lens_q), cu_seqlens_k=cu(lens_k))
+        runs.append([o[70:160], lse[70:160]] + [t[0, 70:160] for t in g])
+    for a, b in zip(*runs):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+def test_bwd_equal_inputs_give_equal_bits():
+    q, kv, pe, do = (t[None].cuda() for t in expanded([1000], [1000], 4, BF, seed=11))
+    o, lse = api().latent_fwd(q, kv, pe)
+    a, b = (api().latent_bwd(q, kv, pe, o, lse, do) for _ in range(2))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_empty_sides():
+    z = lambda *s: torch.zeros(s, dtype=BF, device="cuda")  # noqa: E731
+    o, lse = api().latent_fwd(z(2, 3, 2, 192), z(2, 0, 2, 256), z(2, 0, 64))
+    assert (o == 0).all() and torch.isinf(lse).all()
+    dq, dkv, dpe = api().latent_bwd(z(2, 3, 2, 192), z(2, 0, 2, 256), z(2, 0, 64), o, lse, o)
+    assert (dq == 0).all() and dkv.numel() == 0 and dpe.numel() == 0
+    o, lse = api().latent_fwd(z(2, 0, 2, 192), z(2, 3, 2, 256), z(2, 3, 64))
+    assert o.numel() == 0 and lse.numel() == 0
+    dq, dkv, dpe = api().latent_bwd(z(2, 0, 2, 192), z(2, 3, 2, 256), z(2, 3, 64), o, lse, o)
+    assert dq.numel() == 0 and (dkv == 0).all() and (dpe == 0).all()
+
+
+def test_bad_offsets_are_reported():
+    from chunked_gated_delta_kda_gb300 import binding
+    q, kv, pe, do = (t[None].cuda() for t in expanded([20], [20], 1, BF))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    good, short = cu([20]), torch.tensor([0, 19], dtype=torch.int32, device="cuda")
+    o, lse = api().latent_fwd(q, kv, pe, cu_seqlens_q=good, cu_seqlens_k=good, workspace=ws)
+    assert binding.get_status(ws) == 0
+    down = torch.tensor([0, 15, 12, 20], dtype=torch.int32, device="cuda")
+    for a, b in ((short, good), (good, short), (down, down)):
+        api().latent_fwd(q, kv, pe, cu_seqlens_q=a, cu_seqlens_k=b, workspace=ws)
+        assert binding.get_status(ws) == 4
+    wb = torch.zeros(api().latent_bwd_workspace_bytes(1, 20, 20, 1, 3), dtype=torch.uint8, device="cuda")
+    api().latent_bwd(q, kv, pe, o, lse, do, cu_seqlens_q=down, cu_seqlens_k=down, workspace=wb)
+    assert binding.get_status(wb) == 4
+
+
+# ---------------------------------------------------------------------------
+def paged(lens, page, dtype, seed=0, extra=2, fill=None):
+    """A cache with the sequences' rows on shuffled pages, its table, and (fill) every other row filled with it."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-max(l, 0) // page) for l in lens]
+    total, width = sum(need) + extra, max(1, max(need))
+    cache = torch.randn(total, page, 576, generator=g).to(dtype)
+    order = torch.randperm(total, generator=g).tolist()
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    used = torch.zeros(total, page, dtype=torch.bool)
+    for i, l in enumerate(lens):
+        for j in range(need[i]):
+            table[i, j] = order.pop()
+            used[table[i, j], :min(page, l - j * page)] = True
+    if fill is not None:
+        cache[~used] = fill
+    return cache, table
+
+
+DECODE = [
+    # lengths, tokens, heads, page, type
+    ([1], 1, 1, 16, BF),
+    ([64], 1, 16, 64, BF),
+    ([65, 0, 1, 63], 1, 17, 16, BF),
+    ([200, 129], 1, 32, 32, FP),
+    ([333, 3, 0, 1000], 4, 16, 64, BF),                   # more tokens than rows: some see nothing
+    ([500], 1, 64, 128, FP),
+    ([300, 77], 1, 65, 192, BF),                          # two blocks of rows, the second with one
+    ([130], 2, 64, 16, BF),
+    ([40] * 70, 1, 8, 16, BF),                            # short sequences, several a CTA
+    ([9000], 3, 5, 64, FP),                               # one long sequence over the whole GPU
+]
+
+
+@pytest.mark.parametrize("lens,S,H,page,dtype", DECODE)
+def test_decode(lens, S, H, page, dtype):
+    cache, table = paged(lens, page, dtype, seed=len(lens), fill=float("nan"))
+    q = torch.randn(len(lens), S, H, 576, generator=torch.Generator().manual_seed(1)).to(dtype)
+    n = torch.tensor(lens, dtype=torch.int32)
+    o, lse = api().latent_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda())
+    ro, rl, eo, el = ol.latent_decode(q, cache, table, n, u=U[dtype], tiny=TINY[dtype])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+
+
+def test_decode_peaked_scores():
+    cache, table = paged([700, 90], 64, BF, seed=3)
+    q = (torch.randn(2, 1, 32, 576, generator=torch.Generator().manual_seed(2)) * 12).to(BF)
+    n = torch.tensor([700, 90], dtype=torch.int32)
+    o, lse = api().latent_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), scale=0.2)
+    ro, rl, eo, el = ol.latent_decode(q, cache, table, n, scale=0.2, u=U[BF])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_missing_pages_and_bad_lengths(page):
+    from chunked_gated_delta_kda_gb300 import binding
+    lens = [300, 100, 200]
+    cache, table = paged(lens, page, BF, seed=5)
+    cache[:, 3] = float("nan") if page == 16 else cache[:, 3]
+    cache = torch.nan_to_num(cache, nan=0.5)
+    table[0, 1], table[2, 0], table[2, 2] = -7, cache.shape[0], 1 << 30
+    n = torch.tensor([300, -5, 10 ** 6], dtype=torch.int32)
+    q = torch.randn(3, 2, 8, 576, generator=torch.Generator().manual_seed(4)).to(BF)
+    ws = torch.full((api().latent_decode_workspace_bytes(3, 2, 8),), 0xFF, dtype=torch.uint8, device="cuda")
+    o, lse = api().latent_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), workspace=ws)
+    assert binding.get_status(ws) == 8
+    ro, rl, eo, el = ol.latent_decode(q, cache, table, n, u=U[BF])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+    good = torch.tensor([1, 1, 1], dtype=torch.int32)
+    table[2, 0] = 0
+    api().latent_decode(q.cuda(), cache.cuda(), table.cuda(), good.cuda(), workspace=ws)
+    assert binding.get_status(ws) == 0
+
+
+def test_decode_and_append_past_32_bit_offsets():
+    """A cache of more than 2^31 elements: its last pages."""
+    page, pages = 64, (1 << 31) // (576 * 64) + 60
+    cache = torch.empty(pages, page, 576, dtype=BF, device="cuda")
+    lens, width = [150], 3
+    table = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32)
+    rows = torch.randn(150, 576, generator=torch.Generator().manual_seed(6)).to(BF)
+    at = torch.arange(150)
+    slots = table[0][at // page].long() * page + at % page
+    api().latent_append(rows.cuda(), slots.cuda(), cache)
+    assert torch.equal(cache.view(-1, 576)[slots.cuda()].cpu(), rows)
+    q = torch.randn(1, 1, 16, 576, generator=torch.Generator().manual_seed(7)).to(BF)
+    n = torch.tensor(lens, dtype=torch.int32)
+    o, lse = api().latent_decode(q.cuda(), cache, table.cuda(), n.cuda())
+    small = torch.zeros(width, page, 576, dtype=BF)
+    small.view(-1, 576)[:150] = rows
+    ro, rl, eo, el = ol.latent_decode(q, small, torch.arange(width)[None], n, u=U[BF])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+
+
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,page,dtype,norm", [(1, 16, BF, True), (5, 64, FP, True), (333, 16, BF, False), (1000, 48, FP, True)])
+def test_append(T, page, dtype, norm):
+    from chunked_gated_delta_kda_gb300 import binding
+    g = torch.Generator().manual_seed(T)
+    pages = T // page + 3
+    wide = (torch.randn(T, 640, generator=g) * 3).to(dtype)
+    rows = wide[:, 8:584]                                 # rows of a wider tensor, 16-byte aligned
+    cache = torch.randn(pages, page, 576, generator=g).to(dtype)
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    slots[::7] = -1
+    weight = (1 + 0.1 * torch.randn(512, generator=g)).to(dtype) if norm else None
+    want = ol.latent_append(rows, slots, cache, weight, 1e-5)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    args = (slots.cuda(),), dict(norm_weight=None if weight is None else weight.cuda(), eps=1e-5, workspace=ws)
+    got = api().latent_append(wide.cuda()[:, 8:584], *args[0], cache.cuda(), **args[1])
+    # 512 squares in 32 bits, a reciprocal square root and two products, then the type
+    near(got, want, (U[dtype] + 520 * 2.0 ** -24) * want.abs() + TINY[dtype] if norm else torch.zeros_like(want), "cache")
+    assert binding.get_status(ws) == 0
+    got2 = api().latent_append(wide.cuda()[:, 3:579], *args[0], cache.cuda(), **args[1])   # off the boundary: copied
+    want2 = ol.latent_append(wide[:, 3:579], slots, cache, weight, 1e-5)
+    near(got2, want2, (U[dtype] + 520 * 2.0 ** -24) * want2.abs() + TINY[dtype] if norm else torch.zeros_like(want2), "cache")
+
+
+def test_append_refuses_slots_past_the_cache():
+    from chunked_gated_delta_kda_gb300 import binding
+    cache = torch.zeros(2, 16, 576, dtype=BF, device="cuda")
+    rows = torch.ones(3, 576, dtype=BF, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    api().latent_append(rows, torch.tensor([0, 32, 1 << 40], device="cuda"), cache, workspace=ws)
+    assert binding.get_status(ws) == 8
+    assert (cache[0, 0] == 1).all() and cache.view(-1, 576)[1:].abs().sum() == 0
+    api().latent_append(rows[:0], torch.zeros(0, dtype=torch.int64, device="cuda"), cache, workspace=ws)
+    assert binding.get_status(ws) == 0
+
+
+# ---------------------------------------------------------------------------
+def run_tables(lens, new, table, free, head, page, tokens):
+    from chunked_gated_delta_kda_gb300 import binding
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    t = i(table).reshape(len(lens), -1)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    slots, c, out, h = api().block_tables(i(lens), i(new), t, i(free), i([head]), page, tokens, workspace=ws)
+    return (slots.tolist(), c.tolist(), out.tolist(), h.item(), t.tolist()), binding.get_status(ws)
+
+
+@pytest.mark.parametrize("n,page,longest,most,head,pad", [
+    (1, 16, 0, 1, 0, 0), (7, 16, 100, 60, 3, 5), (300, 64, 500, 1, 0, 0), (2500, 16, 64, 20, 11, 3), (3, 128, 5, 20000, 0, 0),
+    (5000, 1, 3, 2, 2, 0)])
+def test_tables(n, page, longest, most, head, pad):
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, longest + 1, (n,), generator=g).tolist()
+    new = torch.randint(0, most + 1, (n,), generator=g).tolist()
+    held = [-(-l // page) for l in lens]
+    width = max(-(-(l + b) // page) for l, b in zip(lens, new)) + 1
+    order = torch.randperm(sum(held) + sum(-(-(l + b) // page) for l, b in zip(lens, new)) + head, generator=g).tolist()
+    table = [[order.pop() for _ in range(k)] + [-1] * (width - k) for k in held]
+    want = ol.block_tables(lens, new, table, order, head, page, sum(new) + pad)
+    got, status = run_tables(lens, new, table, order, head, page, sum(new) + pad)
+    assert status == 0 and got == tuple(want)
+
+
+@pytest.mark.parametrize("case", [
+    dict(lens=[3, 0, 9], new=[5, 40, 2], width=3, free=[9, 8], head=0, page=4, tokens=47),        # too few pages, too narrow
+    dict(lens=[-2, 5], new=[3, -1], width=4, free=[1, 2, 3], head=0, page=4, tokens=3),           # negative lengths
+    dict(lens=[0, 0], new=[6, 6], width=4, free=[1, 2, 3, 4, 5, 6], head=1, page=4, tokens=7),    # more tokens than the map
+    dict(lens=[0], new=[2], width=1, free=[4], head=-1, page=4, tokens=2),                        # a head outside the list
+    dict(lens=[2], new=[1], width=1, free=[], head=0, page=4, tokens=1),                          # a held cell without a page
+])
+def test_tables_faults_are_reported_and_contained(case):
+    width = case.pop("width")
+    table = [[-1] * width if len(case["lens"]) == 1 else [20 + 4 * i + j if j * case["page"] < l else -1 for j in range(width)]
+             for i, l in enumerate(case["lens"])]
+    want = ol.block_tables(case["lens"], case["new"], table, case["free"], case["head"], case["page"], case["tokens"])
+    got, status = run_tables(case["lens"], case["new"], table, case["free"], case["head"], case["page"], case["tokens"])
+    assert status == 8 and got == tuple(want)
+
+
+# ---------------------------------------------------------------------------
+def test_other_streams_and_graphs():
+    """Every operator on a stream of its own and captured into a graph that is replayed on new contents."""
+    q, kv, pe, do = (t[None].cuda() for t in expanded([200], [200], 2, BF, seed=12))
+    cache, table = (t.cuda() for t in paged([130, 40], 64, BF, seed=13))
+    lens = torch.tensor([130, 40], dtype=torch.int32, device="cuda")
+    qd = torch.randn(2, 1, 16, 576, generator=torch.Generator().manual_seed(14)).to(BF).cuda()
+    rows, slots = torch.ones(2, 576, dtype=BF, device="cuda"), torch.tensor([1, 70], device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    new, free, head, tab = torch.ones(2, **i32), torch.arange(9, **i32), torch.zeros(1, **i32), torch.zeros(2, 8, **i32)
+
+    def everything():
+        o, lse = api().latent_fwd(q, kv, pe)
+        g = api().latent_bwd(q, kv, pe, o, lse, do)
+        c = api().latent_append(rows, slots, cache)
+        d = api().latent_decode(qd, c, table, lens)
+        t = api().block_tables(lens, new, tab, free, head, 16, 4)
+        return (o, lse) + g + d + t
+
+    want = [t.clone() for t in everything()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = everything()
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = everything()
+        q.mul_(0.5)
+        qd.mul_(0.5)
+        graph.replay()
+        side.synchronize()
+    want = everything()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_waits_that_run_out_are_reported():
+    """With one poll a wait every role gives up: the calls end by themselves with KDA_ERR_TIMEOUT, and the next
+    ones are right."""
+    from chunked_gated_delta_kda_gb300 import binding
+    q, kv, pe, do = (t[None].cuda() for t in expanded([600], [600], 2, BF, seed=15))
+    cache, table = (t.cuda() for t in paged([900], 64, BF, seed=16))
+    lens = torch.tensor([900], dtype=torch.int32, device="cuda")
+    qd = torch.randn(1, 1, 16, 576, generator=torch.Generator().manual_seed(17)).to(BF).cuda()
+    ws = torch.zeros(api().latent_bwd_workspace_bytes(1, 600, 600, 2, 1), dtype=torch.uint8, device="cuda")
+    wd = torch.zeros(api().latent_decode_workspace_bytes(1, 1, 16), dtype=torch.uint8, device="cuda")
+
+    def calls():
+        o, lse = api().latent_fwd(q, kv, pe, workspace=ws)
+        status = [binding.get_status(ws)]
+        g = api().latent_bwd(q, kv, pe, o, lse, do, workspace=ws)
+        status.append(binding.get_status(ws))
+        d = api().latent_decode(qd, cache, table, lens, workspace=wd)
+        status.append(binding.get_status(wd))
+        return (o, lse) + g + d, status
+
+    want, status = calls()
+    assert status == [0, 0, 0]
+    binding.debug_set(binding.KDA_DEBUG_WAIT_LIMIT, 1)
+    try:
+        assert calls()[1] == [5, 5, 5]
+    finally:
+        binding.debug_set(binding.KDA_DEBUG_WAIT_LIMIT, 0)
+    got, status = calls()
+    assert status == [0, 0, 0] and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_serving_layer():
+    """Prefill, tables, cache and absorbed decode agree with the expanded form over whole sequences.  Query and
+    output of the absorbed form, the expanded keys, values and output are each rounded to bf16 (2^-8 of themselves),
+    and the two forms' weights besides: six roundings, against the norm."""
+    from chunked_gated_delta_kda_gb300 import latent_serving
+    assert latent_serving.main() < 6 * 2.0 ** -8
+
+
+def test_training_layer():
+    """The gradient of the layer's input against a difference quotient along a direction, in 64 bits."""
+    from chunked_gated_delta_kda_gb300.latent_serving import LatentLayer
+    g = torch.Generator(device="cuda").manual_seed(2)
+    layer = LatentLayer(256, 2, 1, pages=1)
+    x = torch.randn(1, 96, 256, generator=g, device="cuda").to(BF)
+    grad = torch.randn(1, 96, 2, 128, generator=g, device="cuda").to(BF)
+    o, dx = layer.train(x, grad)
+    step = torch.randn(1, 96, 256, generator=g, device="cuda", dtype=torch.float64)
+
+    def loss(x):
+        q = (x @ layer.w_q.double().T).view(96, 2, 192)
+        rows = x @ layer.w_row.double().T
+        kv = torch.einsum("tc,hdc->thd", rows[0, :, :512], layer.w_up.double())
+        out = ol.latent_fwd(q.cpu(), kv.cpu(), rows[0, :, 512:].cpu(), [96], [96])[0]
+        return (out * grad[0].double().cpu()).sum()
+
+    e = 2.0 ** -8
+    diff = (loss(x.double() + e * step) - loss(x.double() - e * step)) / (2 * e)
+    got = (dx.double() * step).sum().cpu()
+    # sums of 96 * 256 terms with independent signs: a few bf16 roundings of dx's norm times the step's rms (1)
+    assert (diff - got).abs() <= 8 * 2.0 ** -8 * dx.double().norm().cpu(), (diff, got)
