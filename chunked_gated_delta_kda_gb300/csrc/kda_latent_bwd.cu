@@ -118,6 +118,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const int most = p.causal ? min(s.lk, min(row0 + LAT_TILE, s.lq) + shift) : s.lk;
     const int steps = most > 0 ? (most + LAT_TILE - 1) / LAT_TILE : 0;
 
+    if (tid == 32) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.kv);
+        prefetch_map(&maps.pe);
+        prefetch_map(&maps.dout);
+    }
     if (tid == 0) {
         for (uint32_t i = 0; i < 2; ++i) mbar_init(base + D_KFULL + 8 * i, 1), mbar_init(base + D_KREST + 8 * i, 1);
         mbar_init(base + D_VFULL, 1);
@@ -249,7 +255,6 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         const uint32_t quad = (uint32_t)(warp & 3) << 21;
         const float c = p.scale * LOG2E;
         const int kmax = p.causal ? min(s.lk, row + shift + 1) : s.lk;
-        const long long at = (s.q0 + row) * p.H + h;
         const bool there = row < s.lq;
         float lse2 = INFINITY, delta = 0.f;
         if (there) {   // the key kernel's tables: tile slot of 64 queries
@@ -308,9 +313,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             if (lane == 0) mbar_arrive(base + D_DSFULL);
         }
         if (steps > 0 && ok) wait(D_DONE, (steps - 1) & 1);
-        if (ok) {
+        if (bar_and_named(1, 256, ok)) {
+            // every product is done: Q's slabs take the result
             tc_fence_after();
-            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dq) + at * LAT_QK) + 12 * g;
+            const int r = row - row0;
 #pragma unroll
             for (int b = 0; b < 3; ++b) {
                 float d[32];
@@ -318,17 +324,19 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     tmem_ld32(t_dq + 96 * g + 32 * b + quad, d);
                     tmem_ld_wait();
                 }
-                if (there) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t r[4];
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            r[k] = steps > 0 ? pack2<FP16>(d[e + 2 * k] * p.scale, d[e + 2 * k + 1] * p.scale) : 0u;
-                        out[4 * b + (e >> 3)] = make_uint4(r[0], r[1], r[2], r[3]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = steps > 0 ? pack2<FP16>(d[e + 2 * k] * p.scale, d[e + 2 * k + 1] * p.scale) : 0u;
+                    *reinterpret_cast<uint4*>(staged(smem + D_Q, r, 12 * g + 4 * b + (e >> 3))) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            bar_and_named(1, 256, true);
+            copy_rows<LAT_QK / 8>(smem + D_Q, static_cast<uint16_t*>(p.dq) + ((s.q0 + row0) * p.H + h) * LAT_QK,
+                                  (long long)p.H * LAT_QK * 2, min(LAT_TILE, s.lq - row0), tid, 256);
         }
     }
     tc_fence_before();
@@ -377,6 +385,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const int steps = max(0, (s.lq + QT - 1) / QT - first);
     const int slot0 = p.cu_q == nullptr ? n * ((p.Tq + QT - 1) / QT) : (int)(s.q0 / QT) + n;
 
+    if (tid == 32) {
+        prefetch_map(&maps.kv);
+        prefetch_map(&maps.pe);
+        prefetch_map(&maps.q64);
+        prefetch_map(&maps.dout64);
+    }
     if (tid == 0) {
         mbar_init(base + K_KVFULL, 1);
         for (uint32_t i = 0; i < STAGES; ++i) mbar_init(base + K_FULL + 8 * i, 1), mbar_init(base + K_KDONE + 8 * i, 1);
@@ -572,13 +586,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             if (lane == 0) mbar_arrive(base + K_DSFULL);
         }
         if (steps > 0 && ok) wait(K_KDONE + 8 * ((steps - 1) % STAGES), ((steps - 1) / STAGES) & 1);
-        if (ok) {
+        if (bar_and_named(1, 256, ok)) {
+            // every product is done: K's and V's slabs take dk and dv, the stages the shared key's part in 32 bits
             tc_fence_after();
-            const long long rows = p.cu_k != nullptr ? p.Tk : (long long)p.N * p.Tk;
-            const bool there = key < s.lk;
-            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dkv) + ((s.k0 + key) * p.H + h) * LAT_KV) +
-                         (g == 0 ? LAT_N / 8 : 0);
-            float4* part = reinterpret_cast<float4*>(p.dpe_part + (h * rows + s.k0 + key) * LAT_P);
+            const int r = key - key0;
             const float f = g == 0 ? (FP16 ? 0.00390625f : 1.f) : p.scale;
             const uint32_t src = (g == 0 ? t_dv : t_dk) + quad;
 #pragma unroll 1
@@ -590,18 +601,25 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) d[e] = steps > 0 ? d[e] * f : 0.f;
-                if (there && b < 4) {
+                if (b < 4) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
-                        out[4 * b + (e >> 3)] =
+                        *reinterpret_cast<uint4*>(staged(smem + K_K, r, (g == 0 ? 16 : 0) + 4 * b + (e >> 3))) =
                             make_uint4(pack2<FP16>(d[e], d[e + 1]), pack2<FP16>(d[e + 2], d[e + 3]),
                                        pack2<FP16>(d[e + 4], d[e + 5]), pack2<FP16>(d[e + 6], d[e + 7]));
-                } else if (there) {
+                } else {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        part[8 * (b - 4) + (e >> 2)] = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
+                        *reinterpret_cast<float4*>(staged(smem + K_ST, r, 8 * (b - 4) + (e >> 2))) =
+                            make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
                 }
             }
+            bar_and_named(1, 256, true);
+            const long long rows = p.cu_k != nullptr ? p.Tk : (long long)p.N * p.Tk;
+            const int count = min(LAT_TILE, s.lk - key0);
+            copy_rows<LAT_KV / 8>(smem + K_K, static_cast<uint16_t*>(p.dkv) + ((s.k0 + key0) * p.H + h) * LAT_KV,
+                                  (long long)p.H * LAT_KV * 2, count, tid, 256);
+            copy_rows<LAT_P / 4>(smem + K_ST, p.dpe_part + (h * rows + s.k0 + key0) * LAT_P, LAT_P * 4, count, tid, 256);
         }
     }
     tc_fence_before();

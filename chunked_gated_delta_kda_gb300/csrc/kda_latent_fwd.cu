@@ -19,6 +19,11 @@
 // products of one tile are issued in the order P V (j), Q K^T (j + 1); the
 // tensor pipe keeps that order, so S may overwrite P, and a full S means that
 // the P V before it is done.
+//
+// B=4 T=8192 H=16 causal: 0.88 ms, 1560 TFLOP/s of the mask's pairs, which is
+// the rate that the GPU's power leaves a long run of products (0.91 of a
+// library product's sustained 1719).  Short sequences are bound by a CTA's
+// first loads and last stores, which only other CTAs' work could cover.
 #include "kda_latent_mma.cuh"
 
 #include <cudaTypedefs.h>
@@ -69,7 +74,15 @@ struct FwdMaps {
     CUtensorMap q, kv, pe;
 };
 
-template <bool FP16>
+// Where a part's row keeps its 16-byte piece: swizzled, so that a thread a row
+// (written) and a warp a row (read) both spread over the banks.
+__device__ __forceinline__ uint32_t part_at(uint32_t row, uint32_t piece) {
+    return F_RING + row * 512u + ((piece ^ (row & 31u)) * 16u);
+}
+
+// SPLIT: the CTAs of a cluster share the keys of a tile pair, each with its
+// own m, l and O, and join them through the cluster's shared memory.
+template <bool FP16, bool SPLIT>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
     latent_fwd_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ FwdMaps maps, int slots) {
     extern __shared__ uint8_t smem_raw[];
@@ -82,7 +95,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     // the last rows of a sequence see the most keys: largest work first
     int n, j0;
     LatentSeq s;
-    latent_slot(p.cu_q, p.Tq, p.N, slots - 1 - (int)blockIdx.x, FWD_ROWS, n, j0);
+    latent_slot(p.cu_q, p.Tq, p.N, slots - 1 - (int)(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x), FWD_ROWS, n, j0);
     if (!latent_seq(p, n, s)) return;
     const int row0 = j0 * FWD_ROWS, h = blockIdx.y;
     if (row0 >= s.lq) return;
@@ -94,8 +107,19 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         const int kmax = first >= s.lq ? 0 : p.causal ? min(s.lk, last + shift + 1) : s.lk;
         nt[t] = kmax > 0 ? (kmax + LAT_TILE - 1) / LAT_TILE : 0;
     }
+    int j_first = 0;   // first key tile of this CTA
+    if constexpr (SPLIT) {
+        const int all = max(nt[0], nt[1]), each = (all + (int)cluster_size() - 1) / (int)cluster_size();
+        j_first = min(all, (int)cluster_rank() * each);
+        for (int t = 0; t < 2; ++t) nt[t] = max(0, min(nt[t] - j_first, each));
+    }
     const int steps = max(nt[0], nt[1]);
 
+    if (tid == 32) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.kv);
+        prefetch_map(&maps.pe);
+    }
     if (tid == 0) {
         for (uint32_t t = 0; t < 2; ++t) {
             mbar_init(base + F_KFULL + 8 * t, 1);
@@ -139,7 +163,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             int j = 0;
             bool half = false;   // given up between a step's K and its V
             for (; j < steps; ++j) {
-                const int tok = (int)s.k0 + j * LAT_TILE, st = j & 1;
+                const int tok = (int)s.k0 + (j_first + j) * LAT_TILE, st = j & 1;
                 if (j >= 2 && !wait_phase(base + F_VEMPTY + 8 * st, (j / 2 - 1) & 1, limit, failed)) break;
                 mbar_arrive_expect_tx(base + F_KFULL + 8 * st, 3 * SLAB);
                 for (int c = 0; c < 2; ++c) tma_load_3d(slab(5 * j + c), &maps.kv, 64 * c, h, tok, base + F_KFULL + 8 * st);
@@ -184,9 +208,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             for (int j = 0; j < steps && ok; ++j) {
                 const uint32_t v = 5 * j + 3;
                 if (!wait(F_VFULL + 8 * (j & 1), (j >> 1) & 1)) break;
-                if ((j + 1) * LAT_TILE > s.lk) {
+                if ((j_first + j + 1) * LAT_TILE > s.lk) {
                     // rows past the sequence's end hold whatever follows: zero weights must meet zeros
-                    for (int r = s.lk - j * LAT_TILE; r < LAT_TILE; ++r)
+                    for (int r = s.lk - (j_first + j) * LAT_TILE; r < LAT_TILE; ++r)
                         if (lane < 16)
                             *reinterpret_cast<uint4*>(smem + (slab(v + (lane >> 3)) - base) + r * 128 + (lane & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
@@ -244,7 +268,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, x[b]);
             tmem_ld_wait();
-            const int lim = kmax - j * LAT_TILE;
+            const int lim = kmax - (j_first + j) * LAT_TILE;
             if (__any_sync(0xffffffffu, lim < LAT_TILE)) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
@@ -292,32 +316,88 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(base + F_PFULL + 8 * t);
         }
-        if (nt[t] > 0 && ok) ok = wait_warp(base + F_ODONE + 8 * t, 0, limit, failed);
-        if (ok) {
-            tc_fence_after();
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long at = (s.q0 + row) * p.H + h;
-            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o_out) + at * LAT_V);
+        if constexpr (!SPLIT) {
+            if (nt[t] > 0 && ok) ok = wait_warp(base + F_ODONE + 8 * t, 0, limit, failed);
+            if (ok) {
+                tc_fence_after();
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const long long at = (s.q0 + row) * p.H + h;
+                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o_out) + at * LAT_V);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float o[32];
-                if (nt[t] > 0) {
-                    tmem_ld32(ts + 128 + 32 * b, o);
-                    tmem_ld_wait();
-                }
-                if (row < s.lq) {
+                for (int b = 0; b < 4; ++b) {
+                    float o[32];
+                    if (nt[t] > 0) {
+                        tmem_ld32(ts + 128 + 32 * b, o);
+                        tmem_ld_wait();
+                    }
+                    if (row < s.lq) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t r[4];
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t r[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            r[k] = l == 0.f ? 0u : pack2<FP16>(o[e + 2 * k] * inv, o[e + 2 * k + 1] * inv);
-                        out[4 * b + (e >> 3)] = make_uint4(r[0], r[1], r[2], r[3]);
+                            for (int k = 0; k < 4; ++k)
+                                r[k] = l == 0.f ? 0u : pack2<FP16>(o[e + 2 * k] * inv, o[e + 2 * k + 1] * inv);
+                            out[4 * b + (e >> 3)] = make_uint4(r[0], r[1], r[2], r[3]);
+                        }
                     }
                 }
+                if (row < s.lq && p.lse_out) p.lse_out[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
             }
-            if (row < s.lq && p.lse_out) p.lse_out[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+        } else {
+            // the ring is free once both tiles' products are done; it takes this CTA's part of all 256 rows
+            for (int k = 0; k < 2; ++k)
+                if (nt[k] > 0 && ok) ok = wait_warp(base + F_ODONE + 8 * k, 0, limit, failed);
+            if (ok) {
+                tc_fence_after();
+                const int r = t * LAT_TILE + (warp & 3) * 32 + lane;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float o[32];
+                    if (nt[t] > 0) {
+                        tmem_ld32(ts + 128 + 32 * b, o);
+                        tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(smem + part_at(r, 8 * b + (e >> 2))) =
+                            nt[t] > 0 ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                reinterpret_cast<float2*>(smem + F_Q)[r] = make_float2(m, l);
+            }
         }
+    }
+    if constexpr (SPLIT) {
+        // every CTA of the cluster, failed or not, passes both barriers: the parts are written; they are read
+        __syncwarp();
+        cluster_barrier();
+        if (warp < 8) {
+            const uint32_t ranks = cluster_size(), share = FWD_ROWS / ranks;
+            const float c = p.scale * 1.4426950408889634f;
+            for (uint32_t r = cluster_rank() * share + warp; r < (cluster_rank() + 1) * share; r += 8) {
+                const int row = row0 + (int)r;
+                if (row >= s.lq) break;
+                float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+                for (uint32_t k = 0; k < ranks; ++k)
+                    m = fmaxf(m, ld_cluster2(cluster_addr(base + F_Q + 8 * r, k)).x);
+                for (uint32_t k = 0; k < ranks; ++k) {
+                    const float2 st = ld_cluster2(cluster_addr(base + F_Q + 8 * r, k));
+                    const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
+                    const float4 v = ld_cluster4(cluster_addr(base + part_at(r, lane), k));
+                    l += f * st.y;
+                    o[0] += f * v.x;
+                    o[1] += f * v.y;
+                    o[2] += f * v.z;
+                    o[3] += f * v.w;
+                }
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const long long at = (s.q0 + row) * p.H + h;
+                reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o_out) + at * LAT_V)[lane] =
+                    make_uint2(pack2<FP16>(o[0] * inv, o[1] * inv), pack2<FP16>(o[2] * inv, o[3] * inv));
+                if (lane == 0 && p.lse_out) p.lse_out[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+            }
+        }
+        __syncwarp();
+        cluster_barrier();
     }
     tc_fence_before();
     __syncthreads();
@@ -325,13 +405,24 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
 }
 
-template <bool FP16>
-cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, cudaStream_t stream) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(latent_fwd_kernel<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
+template <bool FP16, bool SPLIT>
+cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, int ranks, cudaStream_t stream) {
+    const auto kernel = latent_fwd_kernel<FP16, SPLIT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
     if (e != cudaSuccess) return e;
-    latent_fwd_kernel<FP16><<<dim3(slots, p.H), FWD_THREADS, F_SMEM, stream>>>(p, maps, slots);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(slots * ranks), (unsigned)p.H);
+    cfg.blockDim = dim3(FWD_THREADS);
+    cfg.dynamicSmemBytes = F_SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, maps, slots);
 }
 
 }  // namespace
@@ -348,7 +439,16 @@ cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t str
         !latent_row_map(&maps.pe, pe, LAT_P, 1, rows_k > 0 ? rows_k : 1, p.k_pe_stride, LAT_TILE))
         return cudaErrorInvalidValue;
     const int slots = latent_slots(varlen, p.Tq, p.N, FWD_ROWS);
-    return fp16 ? launch<true>(p, maps, slots, stream) : launch<false>(p, maps, slots, stream);
+    // Few query tiles on long keys: a cluster for each tile pair, as large as leaves every CTA of every cluster an SM
+    // (measured with some pairs missing or short, hence the third above 152).  Without / by two / by four, in us:
+    // 512 queries on 8192 keys, 16 heads (48 pairs) 115 / 72 / 43, 32 heads 118 / 76 / 84; 256 on 2048, 8 heads
+    // 35 / 31 / 22; one on 4096, 32 heads 49 / 31 / 23.  More pairs, or fewer keys, lose: 2 x 2048 on themselves,
+    // 8 heads (144 pairs) 37 / 56 / 70; 4 x 1024, 4 heads (80) 22 / 26 / 34.
+    const long long pairs = (long long)slots * p.H;
+    const int ranks = rows_k / p.N < 2048 ? 1 : pairs * 4 <= 200 ? 4 : pairs * 2 <= 200 ? 2 : 1;
+    if (ranks > 1)
+        return fp16 ? launch<true, true>(p, maps, slots, ranks, stream) : launch<false, true>(p, maps, slots, ranks, stream);
+    return fp16 ? launch<true, false>(p, maps, slots, 1, stream) : launch<false, false>(p, maps, slots, 1, stream);
 }
 
 }  // namespace kda

@@ -127,6 +127,23 @@ __device__ __forceinline__ void tmem_ld_half32(uint32_t taddr, float (&r)[32]) {
         : "memory");
 }
 
+// Result tiles go through shared memory (slabs of 64 16-bit columns x 128
+// rows, 16-byte pieces swizzled by the row): a thread has a whole row, and
+// rows written straight to global memory are 32 lines an instruction (a
+// 128 x 192 tile 6000 cycles beside about 1500).
+__device__ __forceinline__ uint8_t* staged(uint8_t* slabs, int row, int piece) {
+    return slabs + (piece >> 3) * (LAT_TILE * 128) + row * 128 + (((piece & 7) ^ (row & 7)) * 16);
+}
+// Rows [0, rows) of PIECES 16-byte pieces to out, `stride` bytes apart.
+template <int PIECES>
+__device__ __forceinline__ void copy_rows(uint8_t* slabs, void* out, long long stride, int rows, int tid, int threads) {
+    for (int i = tid; i < rows * PIECES; i += threads) {
+        const int r = i / PIECES, c = i % PIECES;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + r * stride + c * 16) =
+            *reinterpret_cast<const uint4*>(staged(slabs, r, c));
+    }
+}
+
 // Bounded wait on a barrier phase.  Runs out after `limit` polls, or soon
 // after another role of the CTA has set the failure flag; sets the flag.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32_t limit, volatile uint32_t* failed) {
@@ -145,6 +162,43 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32
 // elected lane polling, 1.06.)
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t limit, volatile uint32_t* failed) {
     return __all_sync(0xffffffffu, wait_phase(bar, parity, limit, failed));
+}
+
+// ---- clusters: the CTA's place, a barrier of all threads, another CTA's shared memory ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
 // Tensor map over packed rows: [tokens][heads][width] 16-bit elements, rows

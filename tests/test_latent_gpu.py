@@ -57,6 +57,9 @@ CASES = [
     ([300, 5], [100, 1], 2, BF, True),                    # more queries than keys: rows that see nothing
     ([700], [900], 1, BF, True),
     ([513], [1100], 1, FP, False),
+    ([300, 40], [4100, 3], 2, BF, True),                  # few queries on many keys: keys shared by four CTAs,
+    ([5], [2300], 1, FP, False),
+    ([300], [2100], 30, BF, True),                        # by two
 ]
 
 
