@@ -84,17 +84,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 // ---------------------------------------------------------------------------
 // dq.  Shared memory: Q and dO (five slabs), K through a ring of seven slabs,
-// V through one of two.  K of step j is needed by S (j) and dQ (j); with the
-// order S (j + 1), dQ (j), dP (j + 1) the first slab of K (j + 2) loads while
-// S (j + 1) runs and the other two behind dP (j + 1).
+// V through one of two.  K of step j is needed by S (j) and, most of a step
+// later, by dQ (j), which frees it slab by slab: the first slab of K (j + 2)
+// has a place of its own, the other two load behind the slabs of dQ (j).
 // Tensor memory: S 128 columns, dP 128, dS 64 (16-bit), dQ 192: all 512.
+// A step is 2050 cycles of products and takes about 2600 with its waits; a CTA
+// (packed T=9192 H=32: 12 steps, 382 us in all) begins with 6000 cycles of
+// setup and first loads.  Not better: three K stages by tiles of 96 keys (products of
+// 96 columns run little faster than of 128: packed T=9192 H=32 449 us beside
+// 390), or by dO in tensor memory with dS over dP (S (j + 1), dQ and dP then
+// run one after another and nothing is left beside the elementwise part: 414
+// us, with sixteen elementwise warps 432).
 // ---------------------------------------------------------------------------
 constexpr uint32_t KRING = 7;
 constexpr uint32_t D_Q = 0, D_DO = 3 * SLAB, D_K = 5 * SLAB, D_V = D_K + KRING * SLAB, D_BAR = D_V + 2 * SLAB;
 constexpr uint32_t D_QFULL = D_BAR, D_DOFULL = D_QFULL + 8, D_KFULL = D_DOFULL + 8 /* [2]: first slab */,
-                   D_KREST = D_KFULL + 16 /* [2]: the other two */, D_VFULL = D_KREST + 16, D_SFULL = D_VFULL + 8,
+                   D_KREST = D_KFULL + 16 /* [second, third slab][2] */, D_VFULL = D_KREST + 32, D_SFULL = D_VFULL + 8,
                    D_PFULL = D_SFULL + 8, D_SREAD = D_PFULL + 8, D_PREAD = D_SREAD + 8, D_DSFULL = D_PREAD + 8,
-                   D_DONE = D_DSFULL + 8, D_DRAIN = D_DONE + 8, D_TMEM = D_DRAIN + 16, D_FAILED = D_TMEM + 4;
+                   D_DONE = D_DSFULL + 8 /* [3]: by step % 3 */, D_KFREE = D_DONE + 24 /* [slab 0, 1][3] */,
+                   D_DRAIN = D_KFREE + 48, D_TMEM = D_DRAIN + 16, D_FAILED = D_TMEM + 4;
 constexpr uint32_t D_SMEM = D_FAILED + 4 + 1024;
 static_assert(D_SMEM <= 232448, "shared memory of one CTA");
 
@@ -125,7 +133,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         prefetch_map(&maps.dout);
     }
     if (tid == 0) {
-        for (uint32_t i = 0; i < 2; ++i) mbar_init(base + D_KFULL + 8 * i, 1), mbar_init(base + D_KREST + 8 * i, 1);
+        for (uint32_t i = 0; i < 6; ++i) mbar_init(base + D_KFULL + 8 * i, 1);
         mbar_init(base + D_VFULL, 1);
         mbar_init(base + D_QFULL, 1);
         mbar_init(base + D_DOFULL, 1);
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         mbar_init(base + D_SREAD, 8);
         mbar_init(base + D_PREAD, 8);
         mbar_init(base + D_DSFULL, 8);
-        mbar_init(base + D_DONE, 1);
+        for (uint32_t i = 0; i < 9; ++i) mbar_init(base + D_DONE + 8 * i, 1);
         mbar_init(base + D_DRAIN, 1);
         mbar_init(base + D_DRAIN + 8, 1);
         *failed = 0u;
@@ -156,24 +164,31 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             mbar_arrive_expect_tx(base + D_QFULL, 3 * SLAB);
             for (uint32_t c = 0; c < 3; ++c) tma_load_3d(base + D_Q + c * SLAB, &maps.q, 64 * c, h, tq, base + D_QFULL);
             mbar_arrive_expect_tx(base + D_DOFULL, 2 * SLAB);
-            // K slab i takes the place of slab i - 7: the first of step j that of K (j - 3)'s last, which was waited
-            // for in step j - 1, the others those of K (j - 2)'s first two, which dQ frees; dP (j - 1) frees V.
-            int a = 0, r = 0, v = 0;   // first slabs, other slabs and V tiles asked for
-            for (int j = 0; j < steps; ++j) {
+            // K slab i takes the place of slab i - 7: the first of step j that of K (j - 3)'s last, the others those of
+            // K (j - 2)'s first two; dP (j - 1) frees V.  (A barrier waited for late must not get a phase ahead: what
+            // dQ frees has three barriers in turn, the next use of one needs the K that is asked for here.)
+            int a[3] = {0, 0, 0}, v = 0;   // K slabs and V tiles asked for
+            bool ok = true;
+            for (int j = 0; j < steps && ok; ++j) {
                 const int tok = (int)s.k0 + j * LAT_TILE, st = j & 1;
-                auto k_slab = [&](int c) { return base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB; };
-                mbar_arrive_expect_tx(base + D_KFULL + 8 * st, SLAB);
-                tma_load_3d(k_slab(0), &maps.kv, 0, h, tok, base + D_KFULL + 8 * st);
-                ++a;
-                if (j >= 2 && !wait_phase(base + D_DONE, (j - 2) & 1, limit, failed)) break;
-                mbar_arrive_expect_tx(base + D_KREST + 8 * st, 2 * SLAB);
-                tma_load_3d(k_slab(1), &maps.kv, 64, h, tok, base + D_KREST + 8 * st);
-                tma_load_3d(k_slab(2), &maps.pe, 0, 0, tok, base + D_KREST + 8 * st);
-                ++r;
+                for (int c = 0; c < 3 && ok; ++c) {
+                    const int of = c == 0 ? j - 3 : j - 2;   // the step whose slab goes
+                    if (of >= 0)
+                        ok = wait_phase(base + (c == 0 ? D_DONE : D_KFREE + 24 * (c - 1)) + 8 * (of % 3), (of / 3) & 1, limit,
+                                        failed);
+                    if (!ok) break;
+                    const uint32_t bar = base + (c == 0 ? D_KFULL : D_KREST + 16 * (c - 1)) + 8 * st;
+                    const uint32_t dst = base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB;
+                    mbar_arrive_expect_tx(bar, SLAB);
+                    if (c < 2) tma_load_3d(dst, &maps.kv, 64 * c, h, tok, bar);
+                    else tma_load_3d(dst, &maps.pe, 0, 0, tok, bar);
+                    ++a[c];
+                }
                 if (j == 0)
                     for (uint32_t c = 0; c < 2; ++c)
                         tma_load_3d(base + D_DO + c * SLAB, &maps.dout, 64 * c, h, tq, base + D_DOFULL);
-                if (j >= 1 && !wait_phase(base + D_PFULL, (j - 1) & 1, limit, failed)) break;
+                if (ok && j >= 1) ok = wait_phase(base + D_PFULL, (j - 1) & 1, limit, failed);
+                if (!ok) break;
                 mbar_arrive_expect_tx(base + D_VFULL, 2 * SLAB);
                 for (uint32_t c = 0; c < 2; ++c)
                     tma_load_3d(base + D_V + c * SLAB, &maps.kv, LAT_N + 64 * c, h, tok, base + D_VFULL);
@@ -182,8 +197,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             // every copy issued here has landed before the CTA ends
             mbar_wait(base + D_QFULL, 0, DRAIN_LIMIT);
             mbar_wait(base + D_DOFULL, 0, DRAIN_LIMIT);
-            for (int k = max(0, a - 2); k < a; ++k) mbar_wait(base + D_KFULL + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
-            for (int k = max(0, r - 2); k < r; ++k) mbar_wait(base + D_KREST + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
+            for (int c = 0; c < 3; ++c)
+                for (int k = max(0, a[c] - 2); k < a[c]; ++k)
+                    mbar_wait(base + (c == 0 ? D_KFULL : D_KREST + 16 * (c - 1)) + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
             if (v > 0) mbar_wait(base + D_VFULL, (v - 1) & 1, DRAIN_LIMIT);
         }
     } else if (warp >= 8) {
@@ -198,7 +214,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
                 const uint32_t b = base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB;
-                if (c < 2 && !wait((c == 0 ? D_KFULL : D_KREST) + 8 * (j & 1), (j >> 1) & 1)) return;
+                if (!wait((c == 0 ? D_KFULL : D_KREST + 16 * (c - 1)) + 8 * (j & 1), (j >> 1) & 1)) return;
                 if ((j + 1) * LAT_TILE > s.lk) {
                     // rows past the sequence's end hold whatever follows: dS is 0 there and has to meet zeros
                     for (int r = s.lk - j * LAT_TILE + (lane >> 3); r < LAT_TILE; r += 4)
@@ -243,8 +259,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     const Desc db = desc_mn(base + D_K + (uint32_t)((3 * j + c) % KRING) * SLAB, LAT_TILE);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) mma_ts(t_dq + 64 * c, t_ds + 8 * ks, db + 128 * ks, id64, j + ks > 0);
+                    mma_commit_warp(base + (c < 2 ? D_KFREE + 24 * c : D_DONE) + 8 * (j % 3));
                 }
-                mma_commit_warp(base + D_DONE);
             }
         }
         // every product issued here is done before the tensor memory is freed
@@ -304,7 +320,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) w[16 * b + (e >> 1)] = __uint_as_float(pack2<FP16>(d[e], d[e + 1]));
             }
-            if (j > 0 && !wait(D_DONE, (j - 1) & 1)) break;   // dS is free
+            if (j > 0 && !wait(D_DONE + 8 * ((j - 1) % 3), ((j - 1) / 3) & 1)) break;   // dS is free
             tc_fence_after();
             tmem_st32(t_ds + 32 * g + quad, w);
             tmem_st_wait();
@@ -312,7 +328,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(base + D_DSFULL);
         }
-        if (steps > 0 && ok) wait(D_DONE, (steps - 1) & 1);
+        if (steps > 0 && ok) wait(D_DONE + 8 * ((steps - 1) % 3), ((steps - 1) / 3) & 1);
         if (bar_and_named(1, 256, ok)) {
             // every product is done: Q's slabs take the result
             tc_fence_after();
