@@ -101,6 +101,29 @@ __device__ __forceinline__ void latent_slot(const int32_t* cu, int T, int N, int
     j = slot - (cu[lo] / tile + lo);
 }
 
+// The sequence and tile of a slot, whole warp: the offsets of up to 31 packed
+// sequences in one round of loads (a bisection is a chain of them, 2000 cycles
+// at the start of a CTA).  The sequence comes out of a vote and its offsets
+// are loaded again from there: values from a vote or a uniform load stay
+// uniform for the compiler, those from a shuffle do not, and every product
+// that depends on one costs several times as much.  (For the same reason the
+// kernels search before their first inline assembly: behind it, forward and
+// backward took 6 % longer.)  `cu` is p.cu_q or p.cu_k.
+__device__ __forceinline__ bool latent_find(const LatentParams& p, const int32_t* cu, int T, int slot, int tile, int& n, int& j,
+                                            LatentSeq& s) {
+    if (cu == nullptr || p.N > 31) {
+        latent_slot(cu, T, p.N, slot, tile, n, j);
+        return latent_seq(p, n, s);
+    }
+    const int lane = threadIdx.x & 31;
+    const int first = lane < p.N ? cu[lane] : INT32_MAX / 2;
+    const uint32_t le = __ballot_sync(0xffffffffu, first / tile + lane <= slot);
+    n = le != 0u ? 31 - __clz(le) : 0;
+    if (!latent_seq(p, n, s)) return false;
+    j = slot - (int)((cu == p.cu_q ? s.q0 : s.k0) / tile + n);
+    return true;
+}
+
 // ---- 16-bit floats ----
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }

@@ -45,9 +45,8 @@ template <bool FP16>
 __global__ void __launch_bounds__(256) latent_aux_kernel(const __grid_constant__ LatentParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int n, j;
-    latent_slot(p.cu_q, p.Tq, p.N, blockIdx.x, QT, n, j);
     LatentSeq s;
-    if (!latent_seq(p, n, s) || j * QT >= s.lq) return;
+    if (!latent_find(p, p.cu_q, p.Tq, blockIdx.x, QT, n, j, s) || j * QT >= s.lq) return;
     const int h = blockIdx.y;
     float* aux = p.aux + ((long long)blockIdx.x * p.H + h) * 2 * QT;
 #pragma unroll
@@ -109,6 +108,8 @@ static_assert(D_SMEM <= 232448, "shared memory of one CTA");
 template <bool FP16>
 __global__ void __launch_bounds__(BWD_THREADS, 1)
     latent_dq_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ BwdMaps maps, int slots) {
+    // the tables are there; the key kernel, which needs nothing else of this launch, may start beside its end
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
@@ -118,10 +119,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 
     int n, j0;
     LatentSeq s;
-    latent_slot(p.cu_q, p.Tq, p.N, slots - 1 - (int)blockIdx.x, LAT_TILE, n, j0);
-    if (!latent_seq(p, n, s)) return;
-    const int row0 = j0 * LAT_TILE, h = blockIdx.y;
-    if (row0 >= s.lq) return;
+    const bool found = latent_find(p, p.cu_q, p.Tq, slots - 1 - (int)blockIdx.x, LAT_TILE, n, j0, s);
+    const int row0 = found ? j0 * LAT_TILE : 0, h = blockIdx.y;
+    if (!found || row0 >= s.lq) {
+        return;
+    }
     const int shift = s.lk - s.lq;
     const int most = p.causal ? min(s.lk, min(row0 + LAT_TILE, s.lq) + shift) : s.lk;
     const int steps = most > 0 ? (most + LAT_TILE - 1) / LAT_TILE : 0;
@@ -392,10 +394,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 
     int n, j0;   // the first keys of a sequence are seen by the most queries: they come first
     LatentSeq s;
-    latent_slot(p.cu_k, p.Tk, p.N, blockIdx.x, LAT_TILE, n, j0);
-    if (!latent_seq(p, n, s)) return;
-    const int key0 = j0 * LAT_TILE, h = blockIdx.y;
-    if (key0 >= s.lk) return;
+    const bool found = latent_find(p, p.cu_k, p.Tk, blockIdx.x, LAT_TILE, n, j0, s);
+    const int key0 = found ? j0 * LAT_TILE : 0, h = blockIdx.y;
+    if (!found || key0 >= s.lk) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int shift = s.lk - s.lq;
     const int first = p.causal ? max(0, key0 - shift) / QT : 0;         // query tile
     const int steps = max(0, (s.lq + QT - 1) / QT - first);
@@ -640,6 +644,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // what follows this launch also follows the dq kernel
     if (warp == 8) tmem_dealloc(tmem, 512);
     if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
 }
@@ -668,13 +673,29 @@ cudaError_t launch(const LatentParams& p, const BwdMaps& maps, cudaStream_t stre
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(latent_dkv_kernel<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K_SMEM);
     if (e != cudaSuccess) return e;
+    // The dq and key kernels may be set up, and begin, beside the end of the launch before them (see there).
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(BWD_THREADS);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (p.Tq > 0) {
         latent_aux_kernel<FP16><<<dim3(latent_slots(varlen, p.Tq, p.N, QT), p.H), 256, 0, stream>>>(p);
         const int slots = latent_slots(varlen, p.Tq, p.N, LAT_TILE);
-        latent_dq_kernel<FP16><<<dim3(slots, p.H), BWD_THREADS, D_SMEM, stream>>>(p, maps, slots);
+        cfg.gridDim = dim3(slots, p.H);
+        cfg.dynamicSmemBytes = D_SMEM;
+        e = cudaLaunchKernelEx(&cfg, latent_dq_kernel<FP16>, p, maps, slots);
+        if (e != cudaSuccess) return e;
     }
     if (p.Tk > 0) {
-        latent_dkv_kernel<FP16><<<dim3(latent_slots(varlen, p.Tk, p.N, LAT_TILE), p.H), BWD_THREADS, K_SMEM, stream>>>(p, maps);
+        cfg.gridDim = dim3(latent_slots(varlen, p.Tk, p.N, LAT_TILE), p.H);
+        cfg.dynamicSmemBytes = K_SMEM;
+        cfg.numAttrs = p.Tq > 0 ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, latent_dkv_kernel<FP16>, p, maps);
+        if (e != cudaSuccess) return e;
         const long long quads = (varlen ? p.Tk : (long long)p.N * p.Tk) * (LAT_P / 4);
         latent_dpe_kernel<FP16><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(p, quads);
     }

@@ -95,10 +95,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     // the last rows of a sequence see the most keys: largest work first
     int n, j0;
     LatentSeq s;
-    latent_slot(p.cu_q, p.Tq, p.N, slots - 1 - (int)(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x), FWD_ROWS, n, j0);
-    if (!latent_seq(p, n, s)) return;
-    const int row0 = j0 * FWD_ROWS, h = blockIdx.y;
-    if (row0 >= s.lq) return;
+    const bool found = latent_find(p, p.cu_q, p.Tq, slots - 1 - (int)(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x),
+                                   FWD_ROWS, n, j0, s);
+    const int row0 = found ? j0 * FWD_ROWS : 0, h = blockIdx.y;
+    if (!found || row0 >= s.lq) return;   // all CTAs of a cluster alike
     const int shift = s.lk - s.lq;
     int nt[2];   // key tiles that each query tile needs
 #pragma unroll
