@@ -34,27 +34,20 @@ STATUS_BYTES = 256
 _FLOAT_FLAGS = {torch.bfloat16: 0, torch.float16: KDA_FLAG_FP16}
 
 
-# Decode steps are a few microseconds of GPU time, so the checks below run on
-# every call as plain comparisons and only a failed one builds its message.
+# Decode steps are a few microseconds of GPU time: each function tests its
+# arguments in one plain condition, and only where that fails goes through the
+# checks below, which say what is wrong.
 def _check(name: str, t, dtype, shape) -> None:
     """``shape``: the wanted sizes, None where any size goes."""
-    if type(t) is torch.Tensor or isinstance(t, torch.Tensor):
-        if t.dtype is dtype and t.is_cuda:
-            got = t.shape
-            if len(got) == len(shape):
-                for w, g in zip(shape, got):
-                    if w is not None and w != g:
-                        break
-                else:
-                    return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    want = ", ".join("*" if w is None else str(w) for w in shape)
-    raise ValueError(f"{name} must have shape [{want}], got {tuple(t.shape)}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name} must have shape [{want}], got {tuple(t.shape)}")
 
 
 def _float_flag(name: str, t) -> int:
@@ -64,6 +57,14 @@ def _float_flag(name: str, t) -> int:
     if flag is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
     return flag
+
+
+def _together(index: int, *tensors) -> bool:
+    """Whether all of them (None aside) are on CUDA device ``index``."""
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            return False
+    return index >= 0
 
 
 def _same_device(index: int, *tensors) -> None:
@@ -84,14 +85,18 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _call(name: str, index: int, *args) -> None:
-    """The C entry point on torch's current stream of device ``index``."""
-    fn = getattr(load_library(), name)
-    if index == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+def _elsewhere(index: int, fn, *args):
+    """``fn`` again, with device ``index`` current."""
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raise(rc: int, name: str) -> None:
     if rc != 0:
         raise KdaError(rc, name)
 
@@ -99,27 +104,36 @@ def _call(name: str, index: int, *args) -> None:
 def _expanded(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k):
     """Checks what forward and backward share: (q, kv, k_pe, its row stride, N, flags)."""
     flags = _float_flag("q", q)
-    _check("q", q, q.dtype, (None, None, None, QUERY_CHANNELS))
-    B, _, H, _ = q.shape
-    _check("kv", kv, q.dtype, (B, None, H, KEY_CHANNELS + VALUE_CHANNELS))
-    Tk = kv.shape[1]
-    _check("k_pe", k_pe, q.dtype, (B, Tk, PE_CHANNELS))
-    if (cu_seqlens_q is None) != (cu_seqlens_k is None):
+    dtype, packed = q.dtype, cu_seqlens_q is not None
+    if packed != (cu_seqlens_k is not None):
         raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
+    if not (q.dim() == kv.dim() == 4 and k_pe.dim() == 3 and kv.dtype is k_pe.dtype is dtype
+            and q.shape[3] == QUERY_CHANNELS and kv.shape[3] == KEY_CHANNELS + VALUE_CHANNELS
+            and k_pe.shape[2] == PE_CHANNELS and q.shape[2] == kv.shape[2] and q.shape[0] == kv.shape[0]
+            and k_pe.shape[:2] == kv.shape[:2]
+            and (not packed or cu_seqlens_q.dtype is cu_seqlens_k.dtype is torch.int32 and cu_seqlens_q.dim() == 1
+                 and cu_seqlens_q.shape == cu_seqlens_k.shape)
+            and _together(q.get_device(), kv, k_pe, cu_seqlens_q, cu_seqlens_k)):
+        _check("q", q, dtype, (None, None, None, QUERY_CHANNELS))
+        _check("kv", kv, dtype, (q.shape[0], None, q.shape[2], KEY_CHANNELS + VALUE_CHANNELS))
+        _check("k_pe", k_pe, dtype, (q.shape[0], kv.shape[1], PE_CHANNELS))
+        if packed:
+            _check("cu_seqlens_q", cu_seqlens_q, torch.int32, (None,))
+            _check("cu_seqlens_k", cu_seqlens_k, torch.int32, cu_seqlens_q.shape)
+        _same_device(q.get_device(), kv, k_pe, cu_seqlens_q, cu_seqlens_k)
+    B, Tk = kv.shape[:2]
     N = B
-    if cu_seqlens_q is not None:
-        _check("cu_seqlens_q", cu_seqlens_q, torch.int32, (None,))
+    if packed:
         N = cu_seqlens_q.shape[0] - 1
-        _check("cu_seqlens_k", cu_seqlens_k, torch.int32, (N + 1,))
         if B != 1 or N < 1:
             raise ValueError("packed sequences need a leading size of 1 and at least one sequence")
         cu_seqlens_q, cu_seqlens_k = cu_seqlens_q.contiguous(), cu_seqlens_k.contiguous()
-    _same_device(q.get_device(), kv, k_pe, cu_seqlens_q, cu_seqlens_k)
     q, kv = _aligned(q.contiguous()), _aligned(kv.contiguous())
     # rows of a wider tensor are read in place where the kernels can
-    stride = k_pe.stride(1) if Tk > 1 else k_pe.stride(0)
-    if (k_pe.stride(2) != 1 or stride < PE_CHANNELS or stride % 8 or k_pe.data_ptr() % 16
-            or (B > 1 and k_pe.stride(0) != Tk * stride)):
+    steps = k_pe.stride()
+    stride = steps[1] if Tk > 1 else steps[0]
+    if (steps[2] != 1 or stride < PE_CHANNELS or stride % 8 or k_pe.data_ptr() % 16
+            or (B > 1 and steps[0] != Tk * stride)):
         k_pe = _aligned(k_pe.contiguous())
         stride = PE_CHANNELS
     return q, kv, k_pe, stride, N, flags, cu_seqlens_q, cu_seqlens_k
@@ -146,12 +160,16 @@ def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: Opt
     ``workspace`` (256 bytes, 256-byte aligned) records device-detected faults
     for ``binding.get_status``."""
     q, kv, k_pe, stride, N, flags, cu_seqlens_q, cu_seqlens_k = _expanded(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k)
+    index = q.get_device()
+    if index != _current_device():
+        return _elsewhere(index, latent_fwd, q, kv, k_pe, scale, causal, cu_seqlens_q, cu_seqlens_k, workspace)
     B, Tq, H, _ = q.shape
     o = torch.empty((B, Tq, H, VALUE_CHANNELS), dtype=q.dtype, device=q.device)
     lse = torch.empty((B, Tq, H), dtype=torch.float32, device=q.device)
-    _call("kda_latent_fwd", q.get_device(), _ptr(q), _ptr(kv), _ptr(k_pe), stride, float(-1.0 if scale is None else scale),
-          _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(o), _ptr(lse), B, Tq, kv.shape[1], H, N,
-          flags | (KDA_FLAG_CAUSAL if causal else 0), _status_workspace(workspace))
+    _raise(load_library().kda_latent_fwd(
+        q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), stride, -1.0 if scale is None else scale, _ptr(cu_seqlens_q),
+        _ptr(cu_seqlens_k), o.data_ptr(), lse.data_ptr(), B, Tq, kv.shape[1], H, N,
+        flags | KDA_FLAG_CAUSAL if causal else flags, _status_workspace(workspace), _stream(index)), "kda_latent_fwd")
     return o, lse
 
 
@@ -167,12 +185,15 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
     lse, and o's gradient ``do``: returns (dq, dkv, dk_pe) in q's type, dk_pe
     summed over the heads.  Deterministic."""
     q, kv, k_pe, stride, N, flags, cu_seqlens_q, cu_seqlens_k = _expanded(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k)
+    index = q.get_device()
     B, Tq, H, _ = q.shape
     Tk, dev = kv.shape[1], q.device
     _check("o", o, q.dtype, (B, Tq, H, VALUE_CHANNELS))
     _check("do", do, q.dtype, (B, Tq, H, VALUE_CHANNELS))
     _check("lse", lse, torch.float32, (B, Tq, H))
-    _same_device(q.get_device(), o, lse, do)
+    _same_device(index, o, lse, do)
+    if index != _current_device():
+        return _elsewhere(index, latent_bwd, q, kv, k_pe, o, lse, do, scale, causal, cu_seqlens_q, cu_seqlens_k, workspace)
     o, do, lse = _aligned(o.contiguous()), _aligned(do.contiguous()), lse.contiguous()
     need = latent_bwd_workspace_bytes(B, Tq, Tk, H, N)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
@@ -180,10 +201,11 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
     dq = torch.empty_like(q)
     dkv = torch.empty_like(kv)
     dk_pe = torch.empty((B, Tk, PE_CHANNELS), dtype=q.dtype, device=dev)
-    _call("kda_latent_bwd", q.get_device(), _ptr(q), _ptr(kv), _ptr(k_pe), stride, _ptr(o), _ptr(lse), _ptr(do),
-          float(-1.0 if scale is None else scale), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(dq), _ptr(dkv),
-          _ptr(dk_pe), B, Tq, Tk, H, N, flags | (KDA_FLAG_CAUSAL if causal else 0), _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+    _raise(load_library().kda_latent_bwd(
+        q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), stride, o.data_ptr(), lse.data_ptr(), do.data_ptr(),
+        -1.0 if scale is None else scale, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), dq.data_ptr(), dkv.data_ptr(),
+        dk_pe.data_ptr(), B, Tq, Tk, H, N, flags | KDA_FLAG_CAUSAL if causal else flags, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(index)), "kda_latent_bwd")
     return dq, dkv, dk_pe
 
 
@@ -204,13 +226,21 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     (o [N, S, H, 512], lse fp32 [N, S, H]); a token that sees no row gets 0
     and -inf."""
     flags = _float_flag("q", q)
-    _check("q", q, q.dtype, (None, None, None, ROW_CHANNELS))
+    dtype = q.dtype
+    if not (q.dim() == 4 and cache.dim() == 3 and block_table.dim() == 2 and cache.dtype is dtype
+            and block_table.dtype is torch.int32 and seq_lens.dtype is torch.int32
+            and q.shape[3] == cache.shape[2] == ROW_CHANNELS and seq_lens.shape == block_table.shape[:1] == q.shape[:1]
+            and _together(q.get_device(), cache, block_table, seq_lens)):
+        _check("q", q, dtype, (None, None, None, ROW_CHANNELS))
+        _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
+        _check("block_table", block_table, torch.int32, (q.shape[0], None))
+        _check("seq_lens", seq_lens, torch.int32, (q.shape[0],))
+        _same_device(q.get_device(), cache, block_table, seq_lens)
+    index = q.get_device()
+    if index != _current_device():
+        return _elsewhere(index, latent_decode, q, cache, block_table, seq_lens, scale, workspace)
     N, S, H, _ = q.shape
-    _check("cache", cache, q.dtype, (None, None, ROW_CHANNELS))
-    _check("block_table", block_table, torch.int32, (N, None))
-    _check("seq_lens", seq_lens, torch.int32, (N,))
     dev = q.device
-    _same_device(q.get_device(), cache, block_table, seq_lens)
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
     q, block_table, seq_lens = _aligned(q.contiguous()), block_table.contiguous(), seq_lens.contiguous()
@@ -219,9 +249,10 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         workspace = torch.empty(max(need, STATUS_BYTES), dtype=torch.uint8, device=dev)
     o = torch.empty((N, S, H, LATENT_CHANNELS), dtype=q.dtype, device=dev)
     lse = torch.empty((N, S, H), dtype=torch.float32, device=dev)
-    _call("kda_latent_decode", q.get_device(), _ptr(q), _ptr(cache), cache.shape[0], cache.shape[1], _ptr(block_table),
-          block_table.shape[1], _ptr(seq_lens), float(-1.0 if scale is None else scale), _ptr(o), _ptr(lse), N, S, H,
-          flags, _ptr(workspace), workspace.numel() * workspace.element_size())
+    _raise(load_library().kda_latent_decode(
+        q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), -1.0 if scale is None else scale, o.data_ptr(), lse.data_ptr(), N, S, H, flags,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(index)), "kda_latent_decode")
     return o, lse
 
 
@@ -233,22 +264,31 @@ def latent_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     With ``norm_weight`` [512] the latent channels are RMS-normalised on the
     way.  Returns ``cache``, updated in place."""
     flags = _float_flag("rows", rows)
-    _check("rows", rows, rows.dtype, (None, ROW_CHANNELS))
+    dtype = rows.dtype
+    if not (rows.dim() == 2 and cache.dim() == 3 and cache.dtype is dtype and slots.dtype is torch.int64
+            and rows.shape[1] == cache.shape[2] == ROW_CHANNELS and slots.shape == rows.shape[:1]
+            and (norm_weight is None or norm_weight.dtype is dtype and norm_weight.shape == (LATENT_CHANNELS,))
+            and _together(rows.get_device(), slots, cache, norm_weight)):
+        _check("rows", rows, dtype, (None, ROW_CHANNELS))
+        _check("slots", slots, torch.int64, (rows.shape[0],))
+        _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
+        if norm_weight is not None:
+            _check("norm_weight", norm_weight, dtype, (LATENT_CHANNELS,))
+        _same_device(rows.get_device(), slots, cache, norm_weight)
+    index = rows.get_device()
+    if index != _current_device():
+        return _elsewhere(index, latent_append, rows, slots, cache, norm_weight, eps, workspace)
     T = rows.shape[0]
-    _check("slots", slots, torch.int64, (T,))
-    _check("cache", cache, rows.dtype, (None, None, ROW_CHANNELS))
     if norm_weight is not None:
-        _check("norm_weight", norm_weight, rows.dtype, (LATENT_CHANNELS,))
         norm_weight = _aligned(norm_weight.contiguous())
-    _same_device(rows.get_device(), slots, cache, norm_weight)
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
     if rows.stride(1) != 1 or rows.stride(0) < ROW_CHANNELS or rows.stride(0) % 8 or rows.data_ptr() % 16:
         rows = _aligned(rows.contiguous())
     slots = slots.contiguous()
-    _call("kda_latent_append", rows.get_device(), _ptr(rows), max(rows.stride(0), ROW_CHANNELS), _ptr(slots),
-          _ptr(norm_weight), float(eps), _ptr(cache), cache.shape[0] * cache.shape[1], T, flags,
-          _status_workspace(workspace))
+    _raise(load_library().kda_latent_append(
+        rows.data_ptr(), max(rows.stride(0), ROW_CHANNELS), slots.data_ptr(), _ptr(norm_weight), eps, cache.data_ptr(),
+        cache.shape[0] * cache.shape[1], T, flags, _status_workspace(workspace), _stream(index)), "kda_latent_append")
     return cache
 
 
@@ -264,23 +304,32 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
     num_tokens: the size of the slot map.  Returns (slot_mapping int64
     [num_tokens], cu_seqlens int32 [N + 1], the new lengths int32 [N], the new
     free_head int32 [1]); the inputs stay as they are."""
-    _check("seq_lens", seq_lens, torch.int32, (None,))
+    if not (isinstance(seq_lens, torch.Tensor) and isinstance(block_table, torch.Tensor)
+            and seq_lens.dtype is new_lens.dtype is block_table.dtype is free_pages.dtype is free_head.dtype is torch.int32
+            and seq_lens.dim() == free_pages.dim() == 1 and block_table.dim() == 2 and free_head.shape == (1,)
+            and new_lens.shape == seq_lens.shape == block_table.shape[:1]
+            and _together(seq_lens.get_device(), new_lens, block_table, free_pages, free_head)):
+        _check("seq_lens", seq_lens, torch.int32, (None,))
+        _check("new_lens", new_lens, torch.int32, seq_lens.shape)
+        _check("block_table", block_table, torch.int32, (seq_lens.shape[0], None))
+        _check("free_pages", free_pages, torch.int32, (None,))
+        _check("free_head", free_head, torch.int32, (1,))
+        _same_device(seq_lens.get_device(), new_lens, block_table, free_pages, free_head)
+    index = seq_lens.get_device()
+    if index != _current_device():
+        return _elsewhere(index, block_tables, seq_lens, new_lens, block_table, free_pages, free_head, page_size, num_tokens,
+                          workspace)
     N = seq_lens.shape[0]
-    _check("new_lens", new_lens, torch.int32, (N,))
-    _check("block_table", block_table, torch.int32, (N, None))
-    _check("free_pages", free_pages, torch.int32, (None,))
-    _check("free_head", free_head, torch.int32, (1,))
     dev = seq_lens.device
-    _same_device(seq_lens.get_device(), new_lens, block_table, free_pages, free_head)
     if not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous")
-    slots = torch.empty((num_tokens,), dtype=torch.int64, device=dev)
-    out = torch.empty((2 * N + 2,), dtype=torch.int32, device=dev)
-    cu, lens_out, head_out = out.split((N + 1, N, 1))
     # copies are held until the launch: a freed one's memory would go to the next
     seq_lens, new_lens, free_pages = seq_lens.contiguous(), new_lens.contiguous(), free_pages.contiguous()
-    _call("kda_block_tables", seq_lens.get_device(), _ptr(seq_lens), _ptr(new_lens), _ptr(block_table),
-          block_table.shape[1], _ptr(free_pages), free_pages.shape[0], _ptr(free_head), int(page_size),
-          _ptr(slots), int(num_tokens), _ptr(cu), _ptr(lens_out), _ptr(head_out), N,
-          _status_workspace(workspace))
+    slots = torch.empty((num_tokens,), dtype=torch.int64, device=dev)
+    cu = torch.empty((N + 1,), dtype=torch.int32, device=dev)
+    lens_out, head_out = torch.empty_like(seq_lens), torch.empty_like(free_head)
+    _raise(load_library().kda_block_tables(
+        seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(),
+        free_pages.shape[0], free_head.data_ptr(), page_size, slots.data_ptr(), num_tokens, cu.data_ptr(),
+        lens_out.data_ptr(), head_out.data_ptr(), N, _status_workspace(workspace), _stream(index)), "kda_block_tables")
     return slots, cu, lens_out, head_out
