@@ -107,13 +107,17 @@ def _expanded(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k):
     dtype, packed = q.dtype, cu_seqlens_q is not None
     if packed != (cu_seqlens_k is not None):
         raise ValueError("cu_seqlens_q and cu_seqlens_k go together")
-    if not (q.dim() == kv.dim() == 4 and k_pe.dim() == 3 and kv.dtype is k_pe.dtype is dtype
-            and q.shape[3] == QUERY_CHANNELS and kv.shape[3] == KEY_CHANNELS + VALUE_CHANNELS
-            and k_pe.shape[2] == PE_CHANNELS and q.shape[2] == kv.shape[2] and q.shape[0] == kv.shape[0]
-            and k_pe.shape[:2] == kv.shape[:2]
-            and (not packed or cu_seqlens_q.dtype is cu_seqlens_k.dtype is torch.int32 and cu_seqlens_q.dim() == 1
-                 and cu_seqlens_q.shape == cu_seqlens_k.shape)
-            and _together(q.get_device(), kv, k_pe, cu_seqlens_q, cu_seqlens_k)):
+    try:
+        fine = (q.dim() == kv.dim() == 4 and k_pe.dim() == 3 and kv.dtype is k_pe.dtype is dtype
+                and q.shape[3] == QUERY_CHANNELS and kv.shape[3] == KEY_CHANNELS + VALUE_CHANNELS
+                and k_pe.shape[2] == PE_CHANNELS and q.shape[2] == kv.shape[2] and q.shape[0] == kv.shape[0]
+                and k_pe.shape[:2] == kv.shape[:2]
+                and (not packed or cu_seqlens_q.dtype is cu_seqlens_k.dtype is torch.int32 and cu_seqlens_q.dim() == 1
+                     and cu_seqlens_q.shape == cu_seqlens_k.shape)
+                and _together(q.get_device(), kv, k_pe, cu_seqlens_q, cu_seqlens_k))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
         _check("q", q, dtype, (None, None, None, QUERY_CHANNELS))
         _check("kv", kv, dtype, (q.shape[0], None, q.shape[2], KEY_CHANNELS + VALUE_CHANNELS))
         _check("k_pe", k_pe, dtype, (q.shape[0], kv.shape[1], PE_CHANNELS))
@@ -227,10 +231,14 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     and -inf."""
     flags = _float_flag("q", q)
     dtype = q.dtype
-    if not (q.dim() == 4 and cache.dim() == 3 and block_table.dim() == 2 and cache.dtype is dtype
-            and block_table.dtype is torch.int32 and seq_lens.dtype is torch.int32
-            and q.shape[3] == cache.shape[2] == ROW_CHANNELS and seq_lens.shape == block_table.shape[:1] == q.shape[:1]
-            and _together(q.get_device(), cache, block_table, seq_lens)):
+    try:
+        fine = (q.dim() == 4 and cache.dim() == 3 and block_table.dim() == 2 and cache.dtype is dtype
+                and block_table.dtype is torch.int32 and seq_lens.dtype is torch.int32
+                and q.shape[3] == cache.shape[2] == ROW_CHANNELS and seq_lens.shape == block_table.shape[:1] == q.shape[:1]
+                and _together(q.get_device(), cache, block_table, seq_lens))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
         _check("q", q, dtype, (None, None, None, ROW_CHANNELS))
         _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
         _check("block_table", block_table, torch.int32, (q.shape[0], None))
@@ -265,10 +273,14 @@ def latent_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     way.  Returns ``cache``, updated in place."""
     flags = _float_flag("rows", rows)
     dtype = rows.dtype
-    if not (rows.dim() == 2 and cache.dim() == 3 and cache.dtype is dtype and slots.dtype is torch.int64
-            and rows.shape[1] == cache.shape[2] == ROW_CHANNELS and slots.shape == rows.shape[:1]
-            and (norm_weight is None or norm_weight.dtype is dtype and norm_weight.shape == (LATENT_CHANNELS,))
-            and _together(rows.get_device(), slots, cache, norm_weight)):
+    try:
+        fine = (rows.dim() == 2 and cache.dim() == 3 and cache.dtype is dtype and slots.dtype is torch.int64
+                and rows.shape[1] == cache.shape[2] == ROW_CHANNELS and slots.shape == rows.shape[:1]
+                and (norm_weight is None or norm_weight.dtype is dtype and norm_weight.shape == (LATENT_CHANNELS,))
+                and _together(rows.get_device(), slots, cache, norm_weight))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
         _check("rows", rows, dtype, (None, ROW_CHANNELS))
         _check("slots", slots, torch.int64, (rows.shape[0],))
         _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
@@ -304,11 +316,14 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
     num_tokens: the size of the slot map.  Returns (slot_mapping int64
     [num_tokens], cu_seqlens int32 [N + 1], the new lengths int32 [N], the new
     free_head int32 [1]); the inputs stay as they are."""
-    if not (isinstance(seq_lens, torch.Tensor) and isinstance(block_table, torch.Tensor)
-            and seq_lens.dtype is new_lens.dtype is block_table.dtype is free_pages.dtype is free_head.dtype is torch.int32
-            and seq_lens.dim() == free_pages.dim() == 1 and block_table.dim() == 2 and free_head.shape == (1,)
-            and new_lens.shape == seq_lens.shape == block_table.shape[:1]
-            and _together(seq_lens.get_device(), new_lens, block_table, free_pages, free_head)):
+    try:
+        fine = (seq_lens.dtype is new_lens.dtype is block_table.dtype is free_pages.dtype is free_head.dtype is torch.int32
+                and seq_lens.dim() == free_pages.dim() == 1 and block_table.dim() == 2 and free_head.shape == (1,)
+                and new_lens.shape == seq_lens.shape == block_table.shape[:1]
+                and _together(seq_lens.get_device(), new_lens, block_table, free_pages, free_head))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
         _check("seq_lens", seq_lens, torch.int32, (None,))
         _check("new_lens", new_lens, torch.int32, seq_lens.shape)
         _check("block_table", block_table, torch.int32, (seq_lens.shape[0], None))

@@ -137,3 +137,16 @@ def test_wrappers_refuse_what_the_kernels_do_not_take():
         latent.block_tables(z(1, d=i32), z(1, d=i32), z(1, 1, d=i32), z(1, d=i32), z(1, d=i32), 16, 1)
     with pytest.raises(TypeError, match="seq_lens"):
         latent.block_tables(z(1, d=torch.int64), z(1, d=i32), z(1, 1, d=i32), z(1, d=i32), z(1, d=i32), 16, 1)
+
+
+def test_wrappers_name_what_is_not_a_tensor():
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d)  # noqa: E731
+    i32 = torch.int32
+    for args in ((z(1, 1, 1, 576), None, z(1, 1, d=i32), z(1, d=i32)), (z(1, 1, 1, 576), z(1, 16, 576), [[0]], z(1, d=i32))):
+        with pytest.raises((TypeError, ValueError), match="must be"):
+            latent.latent_decode(*args)
+    for bad in range(5):
+        args = [z(1, d=i32), z(1, d=i32), z(1, 1, d=i32), z(1, d=i32), z(1, d=i32)]
+        args[bad] = [0]
+        with pytest.raises((TypeError, ValueError), match="must be"):
+            latent.block_tables(*args, 16, 1)
