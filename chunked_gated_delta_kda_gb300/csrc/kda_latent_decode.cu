@@ -57,8 +57,7 @@ struct Lay {
     static constexpr uint32_t EFULL = HEMPTY + 8 * NH;
     static constexpr uint32_t EEMPTY = EFULL + 8 * NE;
     static constexpr uint32_t QFULL = EEMPTY + 8 * NE;
-    static constexpr uint32_t QEMPTY = QFULL + 8;
-    static constexpr uint32_t SFULL = QEMPTY + 8;        // [2]
+    static constexpr uint32_t SFULL = QFULL + 8;         // [2]
     static constexpr uint32_t WFULL = SFULL + 16;        // [2] P written
     static constexpr uint32_t VDONE = WFULL + 16;        // second product of a tile done
     static constexpr uint32_t OFREE = VDONE + 8;         // O read out
@@ -178,7 +177,6 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             mbar_init(base + L::EEMPTY + 8 * i, 1);
         }
         mbar_init(base + L::QFULL, 1);
-        mbar_init(base + L::QEMPTY, 1);
         mbar_init(base + L::SFULL, 1);
         mbar_init(base + L::SFULL + 8, 1);
         mbar_init(base + L::WFULL, 4);
@@ -258,18 +256,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
 
     if (warp == 6) {
         // ---- loads ----
-        uint32_t ih = 0, ie = 0, seg = 0;              // halves, positional slabs and queries asked for
+        uint32_t ih = 0, ie = 0;                       // halves and positional slabs asked for
         bool ok = true;
         const int nbox = KEYS / box;
         const int b = lane % nbox, c = lane / nbox;    // this lane's box and slab (nbox <= 4: of 8 or more)
         for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts)) {
-            if (seg > 0) ok = wait_warp(base + L::QEMPTY, (seg - 1) & 1, limit, failed);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(base + L::QFULL, 9 * R * 128);
-            __syncwarp();
-            if (lane < 9)
-                tma_load_3d(base + L::Q + lane * R * 128, &maps.q, 64 * lane, 0, w.n * rows + w.mt * R, base + L::QFULL);
-            ++seg;
             bool bad = false;
             int row, page = box_page(p, w, w.k0, b, box, row);
             for (int k = 0; k < w.cnt && ok; ++k) {
@@ -303,7 +294,6 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             mbar_wait(base + L::HFULL + 8 * (k % L::NH), (k / L::NH) & 1, DRAIN_LIMIT);
         for (uint32_t k = ie > L::NE ? ie - L::NE : 0; k < ie; ++k)
             mbar_wait(base + L::EFULL + 8 * (k % L::NE), (k / L::NE) & 1, DRAIN_LIMIT);
-        if (seg > 0) mbar_wait(base + L::QFULL, (seg - 1) & 1, DRAIN_LIMIT);
     } else if (warp >= 4) {
         // ---- products ----
         const MmaType ty = FP16 ? T_F16 : T_BF16;
@@ -336,7 +326,6 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     if (!ok) break;
                     mma_commit_warp(base + L::SFULL + 8 * (g & 1));
                     mma_commit_warp(base + L::EEMPTY + 8 * (g % L::NE));
-                    if (k + 1 == w.cnt) mma_commit_warp(base + L::QEMPTY);
                 }
             }
         } else {
@@ -379,8 +368,18 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
         const uint32_t quad = (uint32_t)warp << 21;    // this warp's lanes
         const int r = 16 * warp + (lane & 15);         // its row; lanes l and 16 + l have a half of the keys each
         float* fact = reinterpret_cast<float*>(smem + L::FACT);
-        uint32_t g = 0;
+        uint32_t g = 0, asked = 0;
         bool ok = true;
+        // warp 3 asks for the queries: of the next segment as soon as the scores of this one are complete (the loading
+        // warp would have to wait for that and could not run ahead into the next segment's rows)
+        auto ask = [&](const Walk& w) {
+            if (lane == 0) mbar_arrive_expect_tx(base + L::QFULL, 9 * R * 128);
+            __syncwarp();
+            if (lane < 9)
+                tma_load_3d(base + L::Q + lane * R * 128, &maps.q, 64 * lane, 0, w.n * rows + w.mt * R, base + L::QFULL);
+            ++asked;
+        };
+        if (warp == 3 && plan.count > 0) ask(Walk(p, plan));
         for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts)) {
             const bool gaps = bad_pages(p, w, lane);
             const int gr = w.mt * R + r;
@@ -390,6 +389,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 ok = bar_and_named(1, 128, wait_warp(base + L::SFULL + 8 * (g & 1), g >> 1 & 1, limit, failed));
                 if (!ok) break;
                 tc_fence_after();
+                if (warp == 3 && k + 1 == w.cnt && w.left > w.cnt) {
+                    Walk next = w;
+                    next.next(p, mts);
+                    ask(next);
+                }
                 const int tile = w.k0 + k;
                 float x[32];
                 tmem_ld_half32(t_s + 64 * (g & 1) + quad, x);
@@ -510,6 +514,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             bar_and_named(1, 128, true);               // fact is reused by the next segment
             if (lane == 0) mbar_arrive(base + L::OFREE);
         }
+        if (asked > 0) mbar_wait(base + L::QFULL, (asked - 1) & 1, DRAIN_LIMIT);   // landed before the CTA ends
     }
     tc_fence_before();
     __syncthreads();
