@@ -119,8 +119,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 
     int n, j0;
     LatentSeq s;
-    const bool found = latent_find(p, p.cu_q, p.Tq, slots - 1 - (int)blockIdx.x, LAT_TILE, n, j0, s);
-    const int row0 = found ? j0 * LAT_TILE : 0, h = blockIdx.y;
+    int slot, h;
+    latent_order(p, (int)blockIdx.x, slots, true, slot, h);
+    const bool found = latent_find(p, p.cu_q, p.Tq, slot, LAT_TILE, n, j0, s);
+    const int row0 = found ? j0 * LAT_TILE : 0;
     if (!found || row0 >= s.lq) {
         return;
     }
@@ -384,7 +386,7 @@ static_assert(K_SMEM <= 232448, "shared memory of one CTA");
 
 template <bool FP16>
 __global__ void __launch_bounds__(BWD_THREADS, 1)
-    latent_dkv_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ BwdMaps maps) {
+    latent_dkv_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ BwdMaps maps, int slots) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
@@ -392,10 +394,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
 
-    int n, j0;   // the first keys of a sequence are seen by the most queries: they come first
+    int n, j0;
     LatentSeq s;
-    const bool found = latent_find(p, p.cu_k, p.Tk, blockIdx.x, LAT_TILE, n, j0, s);
-    const int key0 = found ? j0 * LAT_TILE : 0, h = blockIdx.y;
+    int slot, h;
+    latent_order(p, (int)blockIdx.x, slots, false, slot, h);
+    const bool found = latent_find(p, p.cu_k, p.Tk, slot, LAT_TILE, n, j0, s);
+    const int key0 = found ? j0 * LAT_TILE : 0;
     if (!found || key0 >= s.lk) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
@@ -685,16 +689,17 @@ cudaError_t launch(const LatentParams& p, const BwdMaps& maps, cudaStream_t stre
     if (p.Tq > 0) {
         latent_aux_kernel<FP16><<<dim3(latent_slots(varlen, p.Tq, p.N, QT), p.H), 256, 0, stream>>>(p);
         const int slots = latent_slots(varlen, p.Tq, p.N, LAT_TILE);
-        cfg.gridDim = dim3(slots, p.H);
+        cfg.gridDim = dim3((unsigned)(slots * p.H));
         cfg.dynamicSmemBytes = D_SMEM;
         e = cudaLaunchKernelEx(&cfg, latent_dq_kernel<FP16>, p, maps, slots);
         if (e != cudaSuccess) return e;
     }
     if (p.Tk > 0) {
-        cfg.gridDim = dim3(latent_slots(varlen, p.Tk, p.N, LAT_TILE), p.H);
+        const int slots = latent_slots(varlen, p.Tk, p.N, LAT_TILE);
+        cfg.gridDim = dim3((unsigned)(slots * p.H));
         cfg.dynamicSmemBytes = K_SMEM;
         cfg.numAttrs = p.Tq > 0 ? 1 : 0;
-        e = cudaLaunchKernelEx(&cfg, latent_dkv_kernel<FP16>, p, maps);
+        e = cudaLaunchKernelEx(&cfg, latent_dkv_kernel<FP16>, p, maps, slots);
         if (e != cudaSuccess) return e;
         const long long quads = (varlen ? p.Tk : (long long)p.N * p.Tk) * (LAT_P / 4);
         latent_dpe_kernel<FP16><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(p, quads);

@@ -92,12 +92,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
 
-    // the last rows of a sequence see the most keys: largest work first
     int n, j0;
     LatentSeq s;
-    const bool found = latent_find(p, p.cu_q, p.Tq, slots - 1 - (int)(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x),
-                                   FWD_ROWS, n, j0, s);
-    const int row0 = found ? j0 * FWD_ROWS : 0, h = blockIdx.y;
+    int slot, h;
+    latent_order(p, (int)(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x), slots, true, slot, h);
+    const bool found = latent_find(p, p.cu_q, p.Tq, slot, FWD_ROWS, n, j0, s);
+    const int row0 = found ? j0 * FWD_ROWS : 0;
     if (!found || row0 >= s.lq) return;   // all CTAs of a cluster alike
     const int shift = s.lk - s.lq;
     int nt[2];   // key tiles that each query tile needs
@@ -416,7 +416,7 @@ cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, int ra
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(slots * ranks), (unsigned)p.H);
+    cfg.gridDim = dim3((unsigned)(slots * ranks * p.H));
     cfg.blockDim = dim3(FWD_THREADS);
     cfg.dynamicSmemBytes = F_SMEM;
     cfg.stream = stream;
