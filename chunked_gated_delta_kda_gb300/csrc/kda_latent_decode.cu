@@ -386,10 +386,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
             const int lim = w.len - p.S + 1 + min(gr, rows - 1) / p.H;   // keys [0, lim) are seen
             float m = -INFINITY, l = 0.f;
             for (int k = 0; k < w.cnt && ok; ++k, ++g) {
-                ok = bar_and_named(1, 128, wait_warp(base + L::SFULL + 8 * (g & 1), g >> 1 & 1, limit, failed));
-                if (!ok) break;
+                ok = wait_warp(base + L::SFULL + 8 * (g & 1), g >> 1 & 1, limit, failed);   // joined with the others' below
                 tc_fence_after();
-                if (warp == 3 && k + 1 == w.cnt && w.left > w.cnt) {
+                if (warp == 3 && ok && k + 1 == w.cnt && w.left > w.cnt) {
                     Walk next = w;
                     next.next(p, mts);
                     ask(next);
@@ -411,7 +410,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 const bool grown = r < R && (top * c > m * c + RESCALE_LOG2 || (m == -INFINITY && top > m));
                 // P's buffer is free, and O stands still, once the tile before is done
-                if (k > 0) ok = wait_warp(base + L::VDONE, (g - 1) & 1, limit, failed);
+                if (k > 0 && ok) ok = wait_warp(base + L::VDONE, (g - 1) & 1, limit, failed);
                 if (!bar_and_named(1, 128, ok && !grown)) {
                     ok = bar_and_named(1, 128, ok);
                     if (!ok) break;
