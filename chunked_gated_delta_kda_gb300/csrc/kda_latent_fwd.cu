@@ -20,10 +20,15 @@
 // tensor pipe keeps that order, so S may overwrite P, and a full S means that
 // the P V before it is done.
 //
-// B=4 T=8192 H=16 causal: 0.88 ms, 1560 TFLOP/s of the mask's pairs, which is
-// the rate that the GPU's power leaves a long run of products (0.91 of a
-// library product's sustained 1719).  Short sequences are bound by a CTA's
-// first loads and last stores, which only other CTAs' work could cover.
+// B=4 T=8192 H=16 causal: 0.83 ms, 1660 TFLOP/s of the mask's pairs (0.97 of
+// a library product's sustained 1719, which the GPU's power sets); T=8192 H=8
+// 0.115 ms, 1490.  A step of both tiles is 2560 cycles of products and takes
+// 3460: a tile's softmax (1500 cycles from its scores to its weights) and its
+// two products follow each other, and the other tile fills the gap but for
+// that.  Short sequences are bound by a CTA's first loads and last stores,
+// which only other CTAs' work could cover.  Not better: the weights handed over
+// in two halves (T=8192 H=8 127 us), a warp of its own for each tile's products
+// (140), the output staged in shared memory as the backward's is (no change).
 #include "kda_latent_mma.cuh"
 
 #include <cudaTypedefs.h>

@@ -482,7 +482,10 @@ size_t kda_latent_decode_workspace_bytes(int N, int S, int H);
  *               aligned, contents need not be initialised
  * A negative length, or one past table_width pages, is clipped to that range,
  * and rows on a page outside [0, num_pages) count as masked; both set
- * KDA_ERR_BAD_PAGE in the status word.
+ * KDA_ERR_BAD_PAGE in the status word.  Precision as for kda_latent_fwd.  A
+ * row that a later token of the sequence sees and an earlier one does not has
+ * weight zero for the earlier one; an infinite or NaN value in it is not
+ * suppressed.
  */
 kda_status kda_latent_decode(const void* q, const void* cache, int num_pages, int page_size,
                              const int32_t* block_table, int table_width, const int32_t* seq_lens, float scale,
