@@ -76,7 +76,7 @@ struct Lay {
 
 struct Plan {
     long long scan[DEC_THREADS / 32];
-    long long first, count;     // this CTA's range
+    long long count;            // tiles of this CTA's range
     int n, mt, k0;              // where it starts
     uint32_t tmem, failed, err;
 };
@@ -110,9 +110,15 @@ struct Walk {
         if (left <= 0) return;
         k0 = 0;
         if (++mt == mts) {
+            // the next sequence that has rows (there is one), 32 looked at together: whole warp
             mt = 0;
-            do ++n;
-            while (n < p.N - 1 && clipped_len(p, n) == 0);
+            uint32_t there = 0;
+            for (++n; n < p.N; n += 32) {
+                const int at = n + (int)(threadIdx.x & 31);
+                there = __ballot_sync(0xffffffffu, at < p.N && clipped_len(p, at) > 0);
+                if (there != 0u) break;
+            }
+            n += __ffs(there) - 1;
         }
         set(p);
     }
@@ -250,7 +256,6 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     }
                     at += (long long)t * mts;
                 }
-                plan.first = lo;
                 plan.count = hi - lo;
             }
         }

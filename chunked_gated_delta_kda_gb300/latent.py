@@ -345,6 +345,6 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
     lens_out, head_out = torch.empty_like(seq_lens), torch.empty_like(free_head)
     _raise(load_library().kda_block_tables(
         seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(),
-        free_pages.shape[0], free_head.data_ptr(), page_size, slots.data_ptr(), num_tokens, cu.data_ptr(),
+        free_pages.shape[0], free_head.data_ptr(), int(page_size), slots.data_ptr(), int(num_tokens), cu.data_ptr(),
         lens_out.data_ptr(), head_out.data_ptr(), N, _status_workspace(workspace), _stream(index)), "kda_block_tables")
     return slots, cu, lens_out, head_out

@@ -209,6 +209,8 @@ DECODE = [
     ([130], 2, 64, 16, BF),
     ([40] * 70, 1, 8, 16, BF),                            # short sequences, several a CTA
     ([9000], 3, 5, 64, FP),                               # one long sequence over the whole GPU
+    ([70] + [0] * 100 + [1000, 0, 5] + [0] * 33 + [64] + [0] * 40, 1, 20, 64, BF),   # padded entries between and behind
+    ([0, 0, 0], 2, 3, 16, FP),
 ]
 
 
