@@ -30,6 +30,7 @@ KEY_CHANNELS = 128
 VALUE_CHANNELS = 128
 QUERY_CHANNELS = KEY_CHANNELS + PE_CHANNELS
 STATUS_BYTES = 256
+FP32 = torch.finfo(torch.float32)
 
 _FLOAT_FLAGS = {torch.bfloat16: 0, torch.float16: KDA_FLAG_FP16}
 
@@ -73,12 +74,39 @@ def _same_device(index: int, *tensors) -> None:
             raise ValueError(f"all tensors must be on the same device: got cuda:{index} and {t.device}")
 
 
-def _status_workspace(workspace) -> Optional[int]:
+def _check_workspace(workspace, index: int) -> None:
+    """The kernels write through its pointer, so it has to be the GPU's own memory in one piece."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}, got one on {workspace.device}")
+
+
+def _status_workspace(workspace, index: int) -> Optional[int]:
     if workspace is None:
         return None
+    _check_workspace(workspace, index)
     if workspace.numel() * workspace.element_size() < STATUS_BYTES:
         raise ValueError(f"workspace must have at least {STATUS_BYTES} bytes")
     return workspace.data_ptr()
+
+
+def _scratch(workspace, need: int, index: int, device) -> torch.Tensor:
+    """The caller's workspace, or a fresh one where there is none or it is too small."""
+    if workspace is not None:
+        _check_workspace(workspace, index)
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace
+    return torch.empty(max(need, STATUS_BYTES), dtype=torch.uint8, device=device)
+
+
+def _scale(scale) -> float:
+    """The C entries take what is not above zero for the default."""
+    if scale is None:
+        return -1.0
+    if not FP32.tiny <= scale <= FP32.max:
+        raise ValueError(f"scale must be a positive finite fp32 number or None, got {scale}")
+    return float(scale)
 
 
 def _ptr(t) -> Optional[int]:
@@ -171,9 +199,9 @@ def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: Opt
     o = torch.empty((B, Tq, H, VALUE_CHANNELS), dtype=q.dtype, device=q.device)
     lse = torch.empty((B, Tq, H), dtype=torch.float32, device=q.device)
     _raise(load_library().kda_latent_fwd(
-        q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), stride, -1.0 if scale is None else scale, _ptr(cu_seqlens_q),
+        q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), stride, _scale(scale), _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), o.data_ptr(), lse.data_ptr(), B, Tq, kv.shape[1], H, N,
-        flags | KDA_FLAG_CAUSAL if causal else flags, _status_workspace(workspace), _stream(index)), "kda_latent_fwd")
+        flags | KDA_FLAG_CAUSAL if causal else flags, _status_workspace(workspace, index), _stream(index)), "kda_latent_fwd")
     return o, lse
 
 
@@ -200,14 +228,13 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
         return _elsewhere(index, latent_bwd, q, kv, k_pe, o, lse, do, scale, causal, cu_seqlens_q, cu_seqlens_k, workspace)
     o, do, lse = _aligned(o.contiguous()), _aligned(do.contiguous()), lse.contiguous()
     need = latent_bwd_workspace_bytes(B, Tq, Tk, H, N)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(max(need, STATUS_BYTES), dtype=torch.uint8, device=dev)
+    workspace = _scratch(workspace, need, index, dev)
     dq = torch.empty_like(q)
     dkv = torch.empty_like(kv)
     dk_pe = torch.empty((B, Tk, PE_CHANNELS), dtype=q.dtype, device=dev)
     _raise(load_library().kda_latent_bwd(
         q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), stride, o.data_ptr(), lse.data_ptr(), do.data_ptr(),
-        -1.0 if scale is None else scale, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), dq.data_ptr(), dkv.data_ptr(),
+        _scale(scale), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), dq.data_ptr(), dkv.data_ptr(),
         dk_pe.data_ptr(), B, Tq, Tk, H, N, flags | KDA_FLAG_CAUSAL if causal else flags, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(index)), "kda_latent_bwd")
     return dq, dkv, dk_pe
@@ -253,13 +280,12 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         raise ValueError("cache must be contiguous")
     q, block_table, seq_lens = _aligned(q.contiguous()), block_table.contiguous(), seq_lens.contiguous()
     need = latent_decode_workspace_bytes(N, S, H)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(max(need, STATUS_BYTES), dtype=torch.uint8, device=dev)
+    workspace = _scratch(workspace, need, index, dev)
     o = torch.empty((N, S, H, LATENT_CHANNELS), dtype=q.dtype, device=dev)
     lse = torch.empty((N, S, H), dtype=torch.float32, device=dev)
     _raise(load_library().kda_latent_decode(
         q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), -1.0 if scale is None else scale, o.data_ptr(), lse.data_ptr(), N, S, H, flags,
+        seq_lens.data_ptr(), _scale(scale), o.data_ptr(), lse.data_ptr(), N, S, H, flags,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(index)), "kda_latent_decode")
     return o, lse
 
@@ -295,12 +321,14 @@ def latent_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
         norm_weight = _aligned(norm_weight.contiguous())
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
-    if rows.stride(1) != 1 or rows.stride(0) < ROW_CHANNELS or rows.stride(0) % 8 or rows.data_ptr() % 16:
+    stride = rows.stride(0) if T > 1 else ROW_CHANNELS   # a single row's is whatever it was cut from
+    if rows.stride(1) != 1 or stride < ROW_CHANNELS or stride % 8 or rows.data_ptr() % 16:
         rows = _aligned(rows.contiguous())
+        stride = ROW_CHANNELS
     slots = slots.contiguous()
     _raise(load_library().kda_latent_append(
-        rows.data_ptr(), max(rows.stride(0), ROW_CHANNELS), slots.data_ptr(), _ptr(norm_weight), eps, cache.data_ptr(),
-        cache.shape[0] * cache.shape[1], T, flags, _status_workspace(workspace), _stream(index)), "kda_latent_append")
+        rows.data_ptr(), stride, slots.data_ptr(), _ptr(norm_weight), eps, cache.data_ptr(),
+        cache.shape[0] * cache.shape[1], T, flags, _status_workspace(workspace, index), _stream(index)), "kda_latent_append")
     return cache
 
 
@@ -346,5 +374,5 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
     _raise(load_library().kda_block_tables(
         seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(),
         free_pages.shape[0], free_head.data_ptr(), int(page_size), slots.data_ptr(), int(num_tokens), cu.data_ptr(),
-        lens_out.data_ptr(), head_out.data_ptr(), N, _status_workspace(workspace), _stream(index)), "kda_block_tables")
+        lens_out.data_ptr(), head_out.data_ptr(), N, _status_workspace(workspace, index), _stream(index)), "kda_block_tables")
     return slots, cu, lens_out, head_out

@@ -150,3 +150,20 @@ def test_wrappers_name_what_is_not_a_tensor():
         args[bad] = [0]
         with pytest.raises((TypeError, ValueError), match="must be"):
             latent.block_tables(*args, 16, 1)
+
+
+def test_workspaces_and_scales_are_checked_before_the_launch():
+    """A workspace elsewhere would be written through a host pointer; a scale that is not above zero would be taken
+    for the default."""
+    host = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="on cuda:0"):
+        latent._status_workspace(host, 0)
+    with pytest.raises(ValueError, match="on cuda:1"):
+        latent._scratch(host, 256, 1, host.device)
+    with pytest.raises(TypeError, match="workspace"):
+        latent._scratch(4096, 256, 0, host.device)
+    assert latent._status_workspace(None, 0) is None
+    assert latent._scale(None) == -1.0 and latent._scale(0.25) == 0.25 and latent._scale(1) == 1.0
+    for bad in (0.0, -0.5, float("nan"), float("inf"), 1e-50):
+        with pytest.raises(ValueError, match="scale"):
+            latent._scale(bad)

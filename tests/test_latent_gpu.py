@@ -302,6 +302,32 @@ def test_append(T, page, dtype, norm):
     near(got2, want2, (U[dtype] + 520 * 2.0 ** -24) * want2.abs() + TINY[dtype] if norm else torch.zeros_like(want2), "cache")
 
 
+def test_append_of_one_row_takes_any_row_step():
+    """The step between rows means nothing where there is one row."""
+    for wide in (577, 580, 584, 1152):
+        rows = torch.randn(1, wide, generator=torch.Generator().manual_seed(wide)).to(BF).cuda()[:, :576]
+        cache = torch.zeros(1, 16, 576, dtype=BF, device="cuda")
+        api().latent_append(rows, torch.tensor([3], device="cuda"), cache)
+        assert torch.equal(cache[0, 3], rows[0]) and int(cache.count_nonzero()) == int(rows.count_nonzero())
+
+
+def test_workspaces_elsewhere_are_refused():
+    q, kv, pe, do = (t[None].cuda() for t in expanded([3], [3], 1, BF, seed=18))
+    cache, table = (t.cuda() for t in paged([3], 16, BF, seed=19))
+    lens, host = torch.tensor([3], dtype=torch.int32, device="cuda"), torch.zeros(1 << 22, dtype=torch.uint8)
+    o, lse = api().latent_fwd(q, kv, pe)
+    slot = torch.tensor([0], device="cuda")
+    one = torch.tensor([1], dtype=torch.int32, device="cuda")
+    for call in (lambda w: api().latent_fwd(q, kv, pe, workspace=w),
+                 lambda w: api().latent_bwd(q, kv, pe, o, lse, do, workspace=w),
+                 lambda w: api().latent_decode(cache[:1, None, :1], cache, table, lens, workspace=w),
+                 lambda w: api().latent_append(cache[0, :1], slot, cache, workspace=w),
+                 lambda w: api().block_tables(lens, one, table, one, one, 16, 1, workspace=w)):
+        for bad in (host, host.cuda()[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)
+
+
 def test_append_refuses_slots_past_the_cache():
     from chunked_gated_delta_kda_gb300 import binding
     cache = torch.zeros(2, 16, 576, dtype=BF, device="cuda")
