@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             // every copy issued here has landed before the CTA ends
             for (int t = 0; t < 2; ++t)
                 if (nt[t] > 0) mbar_wait(base + F_QFULL + 8 * t, 0, DRAIN_LIMIT);
-            for (int k = max(0, j - 2); k < j; ++k) {
+            // (given up halfway, step j - 2's have, and its barrier counts step j's)
+            for (int k = max(0, half ? j - 1 : j - 2); k < j; ++k) {
                 mbar_wait(base + F_KFULL + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
                 mbar_wait(base + F_VFULL + 8 * (k & 1), (k / 2) & 1, DRAIN_LIMIT);
             }
