@@ -20,7 +20,7 @@
 // which also writes the empty sequences.
 // One token of 256 sequences of 4096, H=32: 208 us, 5.8 TB/s (a tile every 3270
 // cycles, 6.5 TB/s, and some 15 us of plan, first loads, parts and join); of
-// lengths 1 to 8192 238 us, 5.2 TB/s; of one sequence of 65536, 25 us.  64 rows
+// lengths 1 to 8192 223 us, 5.5 TB/s; of one sequence of 65536, 25 us.  64 rows
 // (a unit's queries then leave room for two tiles) 64 x 8192 rows of cache 125
 // us, 4.8 TB/s; there, four tiles of 32 keys were slower (145).
 //   warps 0-3  softmax (row 16 w + l in lanes l and 16 + l of warp w, half of
@@ -317,7 +317,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
         auto half = [&](uint32_t i) { return base + L::RH + (i % L::NH) * HALF; };
         if (warp == 4) {
             for (Walk w(p, plan); w.left > 0 && ok; w.next(p, mts), ++seg) {
-                if (!wait(L::QFULL, seg & 1)) break;
+                // A lowered limit runs out here one poll early, and a limit of one at once: what it is lowered for is seen
+                // however long the hardware suspends a poll.  (Everywhere, a loop that may not run at all costs 1% here,
+                // 3% in the forward.)
+                ok = wait_warp(base + L::QFULL, seg & 1, p.wait_limit != 0u ? limit - 1u : limit, failed);
+                if (!ok) break;
                 for (int k = 0; k < w.cnt && ok; ++k, ++g) {
                     // S's buffer is free once the weights of the tile before the last are written
                     if (g >= 2 && !wait(L::WFULL + 8 * (g & 1), ((g - 2) >> 1) & 1)) break;
@@ -348,12 +352,20 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     const int tile = w.k0 + k;
                     if (gaps || (tile + 1) * KEYS > w.len) {
                         // rows that do not exist hold whatever was there: zero weights must meet zeros
-                        const unsigned long long keys = tile_keys(p, w, tile, box);
-                        for (int r = 0; r < KEYS; ++r)
-                            if (!(keys >> r & 1))
-                                for (uint32_t c = lane; c < 64; c += 32)
-                                    *reinterpret_cast<uint4*>(smem + (half(2 * g + (c >> 5)) - base) + (c >> 3 & 3) * KSLAB +
-                                                              r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        uint8_t* at = smem + (half(2 * g) - base) + (lane >> 3) * KSLAB + (lane & 7) * 16;
+                        const int other = (int)(half(2 * g + 1) - half(2 * g));
+                        // (one sequence of 200, H=16: 10.6 us; 15.4 with a test of each of the 64 rows)
+                        auto clear = [&](int r) {
+                            *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(at + r * 128 + other) = make_uint4(0, 0, 0, 0);
+                        };
+                        if (gaps) {
+                            for (unsigned long long none = ~tile_keys(p, w, tile, box); none != 0ull; none &= none - 1)
+                                clear(__ffsll(none) - 1);
+                        } else {
+#pragma unroll 8
+                            for (int r = w.len - tile * KEYS; r < KEYS; ++r) clear(r);
+                        }
                         fence_async_smem();
                         __syncwarp();
                     }
@@ -654,7 +666,9 @@ cudaError_t launch(const DecodeParams& p, const DecMaps& maps, const DecodeScrat
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool few = (long long)p.N * mts * R <= 1024;
+    // Eight warps for a row, or one (us a call): R = 16, sequences of 2048: 4 of them 12.5 / 19.6, 12 18.1 / 18.6, 24
+    // 25.8 / 20.9, 64 40 / 23; R = 32: 4 15.3 / 20.8, 8 18.2 / 18.6, 12 24.0 / 20.5; R = 64: 4 19.6 / 22.6, 8 25.0 / 20.3.
+    const bool few = (long long)p.N * mts * R <= 256;
     cfg.gridDim = few ? dim3(p.N * mts, R, 4) : dim3(p.N * mts, (R + 7) / 8);
     return few ? cudaLaunchKernelEx(&cfg, latent_join_kernel<8, FP16>, p, sc, R, mts, DEC_CTAS)
                : cudaLaunchKernelEx(&cfg, latent_join_kernel<1, FP16>, p, sc, R, mts, DEC_CTAS);
