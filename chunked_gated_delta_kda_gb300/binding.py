@@ -89,6 +89,10 @@ def load_library(path: Optional[str] = None):
     ll = ctypes.c_longlong
     lib.kda_latent_fwd.restype = ctypes.c_int
     lib.kda_latent_fwd.argtypes = [vp, vp, vp, ll, f, vp, vp, vp, vp, i, i, i, i, i, u, vp, vp]
+    lib.kda_latent_fwd_workspace_bytes.restype = sz
+    lib.kda_latent_fwd_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.kda_latent_fwd_ws.restype = ctypes.c_int
+    lib.kda_latent_fwd_ws.argtypes = [vp, vp, vp, ll, f, vp, vp, vp, vp, i, i, i, i, i, u, vp, sz, vp]
     lib.kda_latent_bwd_workspace_bytes.restype = sz
     lib.kda_latent_bwd_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.kda_latent_bwd.restype = ctypes.c_int

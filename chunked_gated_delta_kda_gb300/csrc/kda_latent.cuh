@@ -19,6 +19,8 @@ constexpr int LAT_QK = LAT_N + LAT_P;       // expanded query
 constexpr int LAT_KV = LAT_N + LAT_V;       // expanded key and value of one token and head
 constexpr int LAT_TILE = 128;               // rows of a query or key tile
 
+constexpr int LATENT_SHARE_ITEMS = 896;     // records of shared key ranges in the forward's workspace
+
 struct LatentParams {
     const void* q;          // [B*Tq, H, 192]
     const void* kv;         // [B*Tk, H, 256]
@@ -33,6 +35,8 @@ struct LatentParams {
     void* dkv;
     void* dk_pe;
     float* aux;             // backward workspace: per (64-query tile slot, head) 64 log2 lse, 64 dout . o
+    int4* share_items;      // forward's workspace for shared key ranges (see there), or null
+    float* share_parts;
     float* dpe_part;        // backward workspace: [H][B*Tk][64] per-head gradients of k_pe
     const int32_t* cu_q;    // int32 [N+1] or null
     const int32_t* cu_k;

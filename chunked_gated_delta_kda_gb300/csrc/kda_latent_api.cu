@@ -13,6 +13,7 @@ cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t str
 cudaError_t launch_latent_bwd(const LatentParams& p, bool fp16, cudaStream_t stream);
 cudaError_t launch_latent_decode(const DecodeParams& p, bool fp16, cudaStream_t stream);
 unsigned long long latent_decode_scratch(int N, int S, int H);
+unsigned long long latent_share_bytes(int B, int Tq, int Tk, int H, int N);
 unsigned long long latent_aux_floats(int B, int Tq, int H, int N);
 }  // namespace kda
 
@@ -47,14 +48,33 @@ kda_status check_common(const void* q, const void* kv, const void* k_pe, long lo
 
 extern "C" {
 
+size_t kda_latent_fwd_workspace_bytes(int B, int Tq, int Tk, int H, int N) {
+    return sizes_ok(B, Tq, Tk, H, N) ? (size_t)(kda::WS_HEADER + kda::latent_share_bytes(B, Tq, Tk, H, N)) : 0;
+}
+
 kda_status kda_latent_fwd(const void* q, const void* kv, const void* k_pe, long long k_pe_stride, float scale,
                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, void* o, float* lse, int B,
                           int Tq, int Tk, int H, int N, unsigned flags, void* workspace, cudaStream_t stream) {
+    return kda_latent_fwd_ws(q, kv, k_pe, k_pe_stride, scale, cu_seqlens_q, cu_seqlens_k, o, lse, B, Tq, Tk, H, N, flags,
+                             workspace, workspace ? kda::WS_HEADER : 0, stream);
+}
+
+kda_status kda_latent_fwd_ws(const void* q, const void* kv, const void* k_pe, long long k_pe_stride, float scale,
+                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, void* o, float* lse, int B,
+                             int Tq, int Tk, int H, int N, unsigned flags, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
     const kda_status st = check_common(q, kv, k_pe, k_pe_stride, cu_seqlens_q, cu_seqlens_k, B, Tq, Tk, H, N, flags,
                                        workspace);
     if (st != KDA_OK) return st;
     if ((Tq > 0 && !o) || off16(o) || off4(lse)) return KDA_ERR_INVALID_ARG;
+    if (workspace && workspace_bytes < kda::WS_HEADER) return KDA_ERR_INVALID_ARG;
     kda::LatentParams p{};
+    const unsigned long long share = workspace && cu_seqlens_q ? kda::latent_share_bytes(B, Tq, Tk, H, N) : 0;
+    if (share > 0 && workspace_bytes >= kda::WS_HEADER + share) {
+        uint8_t* at = static_cast<uint8_t*>(workspace) + kda::WS_HEADER;
+        p.share_items = reinterpret_cast<int4*>(at);
+        p.share_parts = reinterpret_cast<float*>(at + kda::LATENT_SHARE_ITEMS * 16ull);
+    }
     p.q = q;
     p.kv = kv;
     p.k_pe = k_pe;
@@ -71,7 +91,9 @@ kda_status kda_latent_fwd(const void* q, const void* kv, const void* k_pe, long 
     p.N = N;
     p.causal = (flags & KDA_FLAG_CAUSAL) != 0u;
     p.wait_limit = kda::debug_wait_limit();
-    if (workspace && cudaMemsetAsync(workspace, 0, kda::WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    // (with shared key ranges the first kernel clears it)
+    if (workspace && (Tq == 0 || !p.share_items) && cudaMemsetAsync(workspace, 0, kda::WS_CLEAR, stream) != cudaSuccess)
+        return KDA_ERR_CUDA;
     if (Tq == 0) return KDA_OK;
     return kda::launch_latent_fwd(p, (flags & KDA_FLAG_FP16) != 0u, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -85,9 +85,142 @@ __device__ __forceinline__ uint32_t part_at(uint32_t row, uint32_t piece) {
     return F_RING + row * 512u + ((piece ^ (row & 31u)) * 16u);
 }
 
-// SPLIT: the CTAs of a cluster share the keys of a tile pair, each with its
-// own m, l and O, and join them through the cluster's shared memory.
-template <bool FP16, bool SPLIT>
+// ---- tile pairs whose keys several CTAs share, chosen on the device ----
+// A pair's keys are walked by one CTA, so where one sequence has many more
+// keys than the others (a chunk behind a long prefix beside short prompts) its
+// pairs end last by far.  A first kernel counts each pair's key tiles, gives
+// those that are long against an SM's share of all of them up to 16 CTAs, and
+// sorts the work; the parts (O, m and l in 32 bits) are joined by a third.  The
+// two cost some 5 us where nothing is shared.  Without / with, in us, H=16:
+// queries 512, 129, 1, 1000 on 8192, 4039, 3000, 1000 keys 121 / 67; 64, 64, 2048
+// on 512, 16384, 2048 191 / 64; H=8: 14 x 1, 1, 1 on 14 x 500, 9000, 30000 338 /
+// 59; 6 x 300 on 500 to 8000 114 / 48; 4 x 2048 on themselves 54 / 48 (from the
+// order); H=4: 30 x 1 on 3000 each 47 / 53.  Clusters with ranks that leave where
+// a pair is short hold their SMs to the end of the cluster: 2 x 4096, 8 heads
+// 116 -> 298.
+constexpr int SHARE_SLOTS = 512;       // tile pairs of a head, at most
+constexpr int SHARE_PARTS = 256;       // parts of 256 rows, over all heads
+constexpr int SHARE_RANKS = 16;        // CTAs of a pair, at most
+constexpr int SHARE_STEPS = 16;        // key tiles below which a pair is not shared
+constexpr float SHARE_LEAST = 8.f;     // key tiles that are worth a part
+constexpr long long SHARE_FLOATS = FWD_ROWS * (LAT_V + 2);   // of a part: O as [32][256 rows][4], m and l of each row
+// Records: an item a CTA and head (x: slot or -1, y: rank, z: ranks, w: first part); behind the items an entry a shared
+// pair (x: first row, y: rows or -1, z, w as before).
+__host__ __device__ __forceinline__ int share_items(int slots, int H) { return slots + SHARE_PARTS / H; }
+static_assert(SHARE_SLOTS + SHARE_PARTS + SHARE_PARTS / 2 <= LATENT_SHARE_ITEMS, "records");
+__host__ __device__ __forceinline__ int share_pairs(int H) { return SHARE_PARTS / (2 * H); }
+
+// Key tiles of a tile pair's two query tiles.
+__device__ __forceinline__ void pair_tiles(const LatentParams& p, const LatentSeq& s, int row0, int (&nt)[2]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = row0 + t * LAT_TILE, last = min(first + LAT_TILE, s.lq) - 1;
+        const int kmax = first >= s.lq ? 0 : p.causal ? min(s.lk, last + s.lk - s.lq + 1) : s.lk;
+        nt[t] = kmax > 0 ? (kmax + LAT_TILE - 1) / LAT_TILE : 0;
+    }
+}
+
+__global__ void __launch_bounds__(SHARE_SLOTS) latent_share_kernel(const __grid_constant__ LatentParams p, int slots) {
+    __shared__ int keys[SHARE_SLOTS], counts[SHARE_SLOTS], sums[SHARE_SLOTS / 32], cu[SHARE_SLOTS + 1];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int items = share_items(slots, p.H), pairs = share_pairs(p.H);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (t < WS_CLEAR / 4) p.status[t] = 0u;
+    for (int i = t; i < items + pairs; i += SHARE_SLOTS) p.share_items[i] = make_int4(-1, -1, 0, 0);
+    for (int i = t; i <= p.N; i += SHARE_SLOTS) cu[i] = p.cu_q[i];
+    __syncthreads();
+    int n, j, steps = -1;              // -1: no such pair
+    LatentSeq s;
+    if (t < slots) {
+        latent_slot(cu, p.Tq, p.N, t, FWD_ROWS, n, j);
+        if (latent_seq(p, n, s) && (long long)j * FWD_ROWS < s.lq) {
+            int nt[2];
+            pair_tiles(p, s, j * FWD_ROWS, nt);
+            steps = max(nt[0], nt[1]);
+        }
+    }
+    const int mine = __reduce_add_sync(0xffffffffu, max(steps, 0));
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < SHARE_SLOTS / 32; ++w) total += sums[w];
+    // an SM's share of the key tiles of all heads, and the CTAs that bring a pair's nearest to it
+    const float share = fmaxf((float)total * (float)p.H * (1.f / 152.f), SHARE_LEAST);
+    int ranks = steps < SHARE_STEPS ? 1 : max(1, min(SHARE_RANKS, (int)((float)steps / share + 0.5f)));
+    // where a shared pair's parts and its entry go
+    int parts = ranks > 1 ? ranks : 0, x = parts | (parts > 0 ? 1 << 16 : 0);
+    const int own = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += sums[w];
+    x -= own;
+    const int base = x & 0xffff, entry = x >> 16;
+    if (parts > 0 && ((base + parts) * p.H > SHARE_PARTS || entry >= pairs)) ranks = 1, parts = 0;
+    const int each = steps < 0 ? -1 : (steps + ranks - 1) / ranks;   // what orders the work: the longest first
+    keys[t] = each;
+    counts[t] = steps < 0 ? 0 : ranks;
+    __syncthreads();
+    if (steps < 0) return;
+    int at = 0;
+    for (int u = 0; u < slots; ++u)
+        if (keys[u] > each || (keys[u] == each && u < t)) at += counts[u];
+    for (int k = 0; k < ranks; ++k) p.share_items[at + k] = make_int4(t, k, ranks, base);
+    if (parts > 0)
+        p.share_items[items + entry] = make_int4((int)s.q0 + j * FWD_ROWS, min(FWD_ROWS, s.lq - j * FWD_ROWS), ranks, base);
+}
+
+// Eight CTAs a shared pair and head, 16 channels each, a thread a row.
+template <bool FP16>
+__global__ void __launch_bounds__(FWD_ROWS) latent_share_join_kernel(const __grid_constant__ LatentParams p, int slots) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int h = blockIdx.x % p.H, r = threadIdx.x;
+    const int4 it = p.share_items[share_items(slots, p.H) + blockIdx.x / p.H];
+    if (r >= it.y) return;
+    const float c = p.scale * 1.4426950408889634f;
+    auto part = [&](int k) { return p.share_parts + ((long long)(it.w + k) * p.H + h) * SHARE_FLOATS; };
+    float m = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+    auto stat = [&](int k) { return reinterpret_cast<const float2*>(part(k) + FWD_ROWS * LAT_V)[r]; };
+#pragma unroll 4
+    for (int k = 0; k < it.z; ++k) m = fmaxf(m, stat(k).x);
+#pragma unroll 4
+    for (int k = 0; k < it.z; ++k) {
+        const float2 st = stat(k);
+        const float f = st.x == -INFINITY ? 0.f : ex2((st.x - m) * c);
+        l += f * st.y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 v = reinterpret_cast<const float4*>(part(k))[(4 * blockIdx.y + e) * FWD_ROWS + r];
+            o[4 * e] += f * v.x;
+            o[4 * e + 1] += f * v.y;
+            o[4 * e + 2] += f * v.z;
+            o[4 * e + 3] += f * v.w;
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long at = ((long long)it.x + r) * p.H + h;
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = pack2<FP16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o_out) + at * LAT_V + 16 * blockIdx.y);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (blockIdx.y == 0 && p.lse_out) p.lse_out[at] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+}
+
+enum Split { WHOLE, CLUSTER, SHARED };
+
+// CLUSTER: the CTAs of a cluster share the keys of a tile pair, each with its
+// own m, l and O, and join them through the cluster's shared memory.  SHARED:
+// see above.
+template <bool FP16, int SPLIT>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
     latent_fwd_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ FwdMaps maps, int slots) {
     extern __shared__ uint8_t smem_raw[];
@@ -100,22 +233,29 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     int n, j0;
     LatentSeq s;
     int slot, h;
-    latent_order(p, (int)(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x), slots, true, slot, h);
+    int4 item = make_int4(0, 0, 1, 0);
+    if constexpr (SPLIT == SHARED) {
+        // only the records are waited for: the tensors were there before the kernel that writes them began
+        asm volatile("griddepcontrol.wait;");
+        const volatile int* at = reinterpret_cast<const volatile int*>(p.share_items + blockIdx.x / p.H);
+        item = make_int4(at[0], at[1], at[2], at[3]);
+        slot = item.x;
+        h = blockIdx.x % p.H;
+        if (slot < 0) return;
+    } else {
+        latent_order(p, (int)(SPLIT == CLUSTER ? blockIdx.x / cluster_size() : blockIdx.x), slots, true, slot, h);
+    }
     const bool found = latent_find(p, p.cu_q, p.Tq, slot, FWD_ROWS, n, j0, s);
     const int row0 = found ? j0 * FWD_ROWS : 0;
     if (!found || row0 >= s.lq) return;   // all CTAs of a cluster alike
     const int shift = s.lk - s.lq;
     int nt[2];   // key tiles that each query tile needs
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int first = row0 + t * LAT_TILE, last = min(first + LAT_TILE, s.lq) - 1;
-        const int kmax = first >= s.lq ? 0 : p.causal ? min(s.lk, last + shift + 1) : s.lk;
-        nt[t] = kmax > 0 ? (kmax + LAT_TILE - 1) / LAT_TILE : 0;
-    }
+    pair_tiles(p, s, row0, nt);
     int j_first = 0;   // first key tile of this CTA
-    if constexpr (SPLIT) {
-        const int all = max(nt[0], nt[1]), each = (all + (int)cluster_size() - 1) / (int)cluster_size();
-        j_first = min(all, (int)cluster_rank() * each);
+    if constexpr (SPLIT != WHOLE) {
+        const int ranks = SPLIT == CLUSTER ? (int)cluster_size() : item.z, rank = SPLIT == CLUSTER ? (int)cluster_rank() : item.y;
+        const int all = max(nt[0], nt[1]), each = (all + ranks - 1) / ranks;
+        j_first = min(all, rank * each);
         for (int t = 0; t < 2; ++t) nt[t] = max(0, min(nt[t] - j_first, each));
     }
     const int steps = max(nt[0], nt[1]);
@@ -322,7 +462,27 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(base + F_PFULL + 8 * t);
         }
-        if constexpr (!SPLIT) {
+        if (SPLIT == SHARED && item.z > 1) {
+            if (nt[t] > 0 && ok) ok = wait_warp(base + F_ODONE + 8 * t, 0, limit, failed);
+            if (ok) {
+                tc_fence_after();
+                float* part = p.share_parts + ((long long)(item.w + item.y) * p.H + h) * SHARE_FLOATS;
+                const int r = t * LAT_TILE + (warp & 3) * 32 + lane;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float o[32];
+                    if (nt[t] > 0) {
+                        tmem_ld32(ts + 128 + 32 * b, o);
+                        tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        reinterpret_cast<float4*>(part)[(8 * b + (e >> 2)) * FWD_ROWS + r] =
+                            nt[t] > 0 ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                reinterpret_cast<float2*>(part + FWD_ROWS * LAT_V)[r] = make_float2(m, l);
+            }
+        } else if constexpr (SPLIT != CLUSTER) {
             if (nt[t] > 0 && ok) ok = wait_warp(base + F_ODONE + 8 * t, 0, limit, failed);
             if (ok) {
                 tc_fence_after();
@@ -372,7 +532,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             }
         }
     }
-    if constexpr (SPLIT) {
+    if constexpr (SPLIT == CLUSTER) {
         // every CTA of the cluster, failed or not, passes both barriers: the parts are written; they are read
         __syncwarp();
         cluster_barrier();
@@ -411,27 +571,63 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
 }
 
-template <bool FP16, bool SPLIT>
+template <bool FP16, int SPLIT>
 cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, int ranks, cudaStream_t stream) {
     const auto kernel = latent_fwd_kernel<FP16, SPLIT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
     if (e != cudaSuccess) return e;
+    if (SPLIT == SHARED) latent_share_kernel<<<1, SHARE_SLOTS, 0, stream>>>(p, slots);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    if (SPLIT == CLUSTER) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ranks;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(slots * ranks * p.H));
+    cfg.gridDim = dim3((unsigned)((SPLIT == SHARED ? share_items(slots, p.H) : slots * ranks) * p.H));
     cfg.blockDim = dim3(FWD_THREADS);
     cfg.dynamicSmemBytes = F_SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = SPLIT ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p, maps, slots);
+    cfg.numAttrs = SPLIT == WHOLE ? 0 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, p, maps, slots);
+    if (e != cudaSuccess || SPLIT != SHARED) return e;
+    cfg.gridDim = dim3((unsigned)(share_pairs(p.H) * p.H), LAT_V / 16);
+    cfg.blockDim = dim3(FWD_ROWS);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, latent_share_join_kernel<FP16>, p, slots);
+}
+
+// Few query tiles on long keys: a cluster for each tile pair, as large as leaves every CTA of every cluster an SM
+// (measured with some pairs missing or short, hence the third above 152).  Without / by two / by four, in us:
+// 512 queries on 8192 keys, 16 heads (48 pairs) 115 / 72 / 43, 32 heads 118 / 76 / 84; 256 on 2048, 8 heads
+// 35 / 31 / 22; one on 4096, 32 heads 49 / 31 / 23.  More pairs, or fewer keys, lose: 2 x 2048 on themselves,
+// 8 heads (144 pairs) 37 / 56 / 70; 4 x 1024, 4 heads (80) 22 / 26 / 34.
+int cluster_of(long long rows_k, int N, int slots, int H) {
+    const long long pairs = (long long)slots * H;
+    return rows_k / N < 2048 ? 1 : pairs * 4 <= 200 ? 4 : pairs * 2 <= 200 ? 2 : 1;
+}
+
+// Whether tile pairs of packed sequences may be shared by the device's choice: two pairs an SM at most (more fill the
+// gaps themselves: 4 x 2048 on themselves, 16 heads, 576 pairs 80 us without and 87 with; 2 x 4096 125 / 130; 512, 129,
+// 1, 1000 on 8192, 4039, 3000, 1000 at 32 heads, 320 pairs 137 / 131), and keys for a pair of 64 steps, 120 us, beside
+// which the 5 us are little (2 x 2048 on themselves, 8 heads 35 / 41).
+bool shares(int Tk, int slots, int H, int N) {
+    return N > 1 && Tk >= 64 * LAT_TILE && (long long)slots * H <= 304 && slots <= SHARE_SLOTS && H <= SHARE_PARTS / 2 &&
+           cluster_of(Tk, N, slots, H) == 1;
 }
 
 }  // namespace
+
+// Bytes behind the status header that let the forward share key ranges: items, entries, parts; 0 where it would not.
+unsigned long long latent_share_bytes(int B, int Tq, int Tk, int H, int N) {
+    if (B != 1 || !shares(Tk, latent_slots(true, Tq, N, FWD_ROWS), H, N)) return 0;
+    return LATENT_SHARE_ITEMS * 16ull + SHARE_PARTS * SHARE_FLOATS * 4ull;
+}
 
 cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t stream) {
     const bool varlen = p.cu_q != nullptr;
@@ -445,16 +641,12 @@ cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t str
         !latent_row_map(&maps.pe, pe, LAT_P, 1, rows_k > 0 ? rows_k : 1, p.k_pe_stride, LAT_TILE))
         return cudaErrorInvalidValue;
     const int slots = latent_slots(varlen, p.Tq, p.N, FWD_ROWS);
-    // Few query tiles on long keys: a cluster for each tile pair, as large as leaves every CTA of every cluster an SM
-    // (measured with some pairs missing or short, hence the third above 152).  Without / by two / by four, in us:
-    // 512 queries on 8192 keys, 16 heads (48 pairs) 115 / 72 / 43, 32 heads 118 / 76 / 84; 256 on 2048, 8 heads
-    // 35 / 31 / 22; one on 4096, 32 heads 49 / 31 / 23.  More pairs, or fewer keys, lose: 2 x 2048 on themselves,
-    // 8 heads (144 pairs) 37 / 56 / 70; 4 x 1024, 4 heads (80) 22 / 26 / 34.
-    const long long pairs = (long long)slots * p.H;
-    const int ranks = rows_k / p.N < 2048 ? 1 : pairs * 4 <= 200 ? 4 : pairs * 2 <= 200 ? 2 : 1;
+    const int ranks = cluster_of(rows_k, p.N, slots, p.H);
     if (ranks > 1)
-        return fp16 ? launch<true, true>(p, maps, slots, ranks, stream) : launch<false, true>(p, maps, slots, ranks, stream);
-    return fp16 ? launch<true, false>(p, maps, slots, 1, stream) : launch<false, false>(p, maps, slots, 1, stream);
+        return fp16 ? launch<true, CLUSTER>(p, maps, slots, ranks, stream) : launch<false, CLUSTER>(p, maps, slots, ranks, stream);
+    if (p.share_items != nullptr)
+        return fp16 ? launch<true, SHARED>(p, maps, slots, 1, stream) : launch<false, SHARED>(p, maps, slots, 1, stream);
+    return fp16 ? launch<true, WHOLE>(p, maps, slots, 1, stream) : launch<false, WHOLE>(p, maps, slots, 1, stream);
 }
 
 }  // namespace kda

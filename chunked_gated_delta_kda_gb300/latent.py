@@ -31,6 +31,7 @@ VALUE_CHANNELS = 128
 QUERY_CHANNELS = KEY_CHANNELS + PE_CHANNELS
 STATUS_BYTES = 256
 FP32 = torch.finfo(torch.float32)
+SHARED_KEYS = 8192   # packed keys below which latent_fwd has no use for a workspace
 
 _FLOAT_FLAGS = {torch.bfloat16: 0, torch.float16: KDA_FLAG_FP16}
 
@@ -176,6 +177,10 @@ def _aligned(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def latent_fwd_workspace_bytes(B: int, Tq: int, Tk: int, H: int, N: int) -> int:
+    return int(load_library().kda_latent_fwd_workspace_bytes(B, Tq, Tk, H, N))
+
+
 def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: Optional[float] = None,
                causal: bool = True, cu_seqlens_q: Optional[torch.Tensor] = None,
                cu_seqlens_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
@@ -189,19 +194,27 @@ def latent_fwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, scale: Opt
     both None.  With ``causal`` query i of a sequence sees the keys up to
     i + Lk - Lq.  ``scale`` None means 192**-0.5.  Returns (o [B, Tq, H, 128],
     lse fp32 [B, Tq, H]); a query that sees no key gets 0 and -inf.
-    ``workspace`` (256 bytes, 256-byte aligned) records device-detected faults
-    for ``binding.get_status``."""
+    ``workspace`` (256-byte aligned) records device-detected faults for
+    ``binding.get_status``; with ``latent_fwd_workspace_bytes`` bytes, 256 at
+    least, it also serves packed sequences some of which have many more keys
+    than the others, for which one is allocated otherwise."""
     q, kv, k_pe, stride, N, flags, cu_seqlens_q, cu_seqlens_k = _expanded(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k)
     index = q.get_device()
     if index != _current_device():
         return _elsewhere(index, latent_fwd, q, kv, k_pe, scale, causal, cu_seqlens_q, cu_seqlens_k, workspace)
     B, Tq, H, _ = q.shape
+    Tk = kv.shape[1]
     o = torch.empty((B, Tq, H, VALUE_CHANNELS), dtype=q.dtype, device=q.device)
     lse = torch.empty((B, Tq, H), dtype=torch.float32, device=q.device)
-    _raise(load_library().kda_latent_fwd(
+    if workspace is None and cu_seqlens_q is not None and Tk >= SHARED_KEYS:
+        need = latent_fwd_workspace_bytes(B, Tq, Tk, H, N)
+        if need > STATUS_BYTES:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _raise(load_library().kda_latent_fwd_ws(
         q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), stride, _scale(scale), _ptr(cu_seqlens_q),
-        _ptr(cu_seqlens_k), o.data_ptr(), lse.data_ptr(), B, Tq, kv.shape[1], H, N,
-        flags | KDA_FLAG_CAUSAL if causal else flags, _status_workspace(workspace, index), _stream(index)), "kda_latent_fwd")
+        _ptr(cu_seqlens_k), o.data_ptr(), lse.data_ptr(), B, Tq, Tk, H, N, flags | KDA_FLAG_CAUSAL if causal else flags,
+        _status_workspace(workspace, index), size, _stream(index)), "kda_latent_fwd")
     return o, lse
 
 

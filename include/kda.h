@@ -435,6 +435,19 @@ kda_status kda_latent_fwd(const void* q, const void* kv, const void* k_pe, long 
                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, void* o, float* lse, int B,
                           int Tq, int Tk, int H, int N, unsigned flags, void* workspace, cudaStream_t stream);
 
+/*
+ * The same with a workspace of kda_latent_fwd_workspace_bytes (256-byte
+ * aligned): where some sequences have many more keys than others, several
+ * CTAs share those, and their parts (32 bits) go through the workspace.  The
+ * lengths are on the device, and so is the choice.  A smaller workspace (256
+ * bytes at least, or NULL) serves as kda_latent_fwd's.
+ */
+size_t kda_latent_fwd_workspace_bytes(int B, int Tq, int Tk, int H, int N);
+kda_status kda_latent_fwd_ws(const void* q, const void* kv, const void* k_pe, long long k_pe_stride, float scale,
+                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, void* o, float* lse, int B,
+                             int Tq, int Tk, int H, int N, unsigned flags, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
 /* Bytes of device workspace kda_latent_bwd needs (0 on invalid sizes). */
 size_t kda_latent_bwd_workspace_bytes(int B, int Tq, int Tk, int H, int N);
 

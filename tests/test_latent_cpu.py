@@ -167,3 +167,25 @@ def test_workspaces_and_scales_are_checked_before_the_launch():
     for bad in (0.0, -0.5, float("nan"), float("inf"), 1e-50):
         with pytest.raises(ValueError, match="scale"):
             latent._scale(bad)
+
+
+def test_fwd_workspace_sizes():
+    """Records and 256 parts of 256 rows where packed sequences have 8192 keys or more; the status header elsewhere."""
+    lib = binding.load_library()
+    shared = 256 + 896 * 16 + 256 * 256 * 130 * 4
+    assert lib.kda_latent_fwd_workspace_bytes(1, 1642, 16231, 16, 4) == shared
+    assert lib.kda_latent_fwd_workspace_bytes(1, 64, 8192, 1, 30) == shared
+    for sizes in ((1, 1642, 8191, 16, 4), (1, 9000, 9000, 8, 1), (2, 9000, 9000, 8, 2), (1, 1642, 16231, 129, 4),
+                  (1, 8, 16384, 8, 2), (1, 200000, 200000, 8, 9), (1, 600, 600000, 1, 600), (1, 0, 0, 1, 1)):
+        assert lib.kda_latent_fwd_workspace_bytes(*sizes) == 256, sizes
+    assert lib.kda_latent_fwd_workspace_bytes(0, 1, 1, 1, 1) == 0
+
+
+@cpu_only
+def test_fwd_with_a_workspace_refusals():
+    keep, p = host_block()
+    call = caller(binding.load_library().kda_latent_fwd_ws, dict(
+        q=p, kv=p, pe=p, stride=64, scale=0.0, cu_q=None, cu_k=None, o=p, lse=p, B=1, Tq=8, Tk=8, H=1, N=1, flags=0,
+        ws=p, wsb=256, stream=None))
+    for kw in (dict(q=None), dict(o=None), dict(wsb=255), dict(wsb=0), dict(ws=p + 64), dict(N=2), dict(flags=1)):
+        assert call(**kw) == 1, kw

@@ -83,6 +83,74 @@ def test_bwd(lens_q, lens_k, H, dtype, causal):
         near(g[0], w, e, name)
 
 
+SHARED = [
+    # one sequence with many more keys than the others: CTAs chosen on the device share its pairs
+    ([300, 1, 0, 40, 5], [9000, 10, 7, 64, 1], 2, BF, True),
+    ([1, 20, 600, 3, 3], [2, 8300, 500, 0, 3], 3, FP, False),
+    ([700, 130, 1, 1, 9], [5000, 3200, 40, 1, 4], 5, BF, True),   # two of them, several pairs
+    ([9000, 1, 1, 1, 1], [8500, 1, 1, 1, 1], 1, BF, True),        # more queries than keys; 36 pairs
+    ([2, 2, 2, 2, 2], [1700] * 5, 30, FP, True),                  # none stands out: nothing is shared
+]
+
+
+@pytest.mark.parametrize("lens_q,lens_k,H,dtype,causal", SHARED)
+def test_fwd_shared_keys(lens_q, lens_k, H, dtype, causal):
+    assert api().latent_fwd_workspace_bytes(1, sum(lens_q), sum(lens_k), H, len(lens_q)) > 256
+    q, kv, pe, _ = expanded(lens_q, lens_k, H, dtype, seed=sum(lens_q))
+    o, lse = run_fwd(q, kv, pe, lens_q, lens_k, causal)
+    ro, rl, eo, el = ol.latent_fwd(q, kv, pe, lens_q, lens_k, causal, u=U[dtype], tiny=TINY[dtype])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")      # too small to share anything
+    o, lse = run_fwd(q, kv, pe, lens_q, lens_k, causal, workspace=ws)
+    near(o, ro, eo, "o, not shared")
+    near(lse, rl, el, "lse, not shared")
+
+
+def test_fwd_shared_keys_are_contained_and_reported():
+    """Bad rows of other sequences, peaked scores, a used workspace, equal bits, graphs, bad offsets, waits."""
+    from chunked_gated_delta_kda_gb300 import binding
+    lens_q, lens_k, H = [260, 30, 1, 70, 4], [8200, 100, 50, 70, 300], 2
+    q, kv, pe, _ = expanded(lens_q, lens_k, H, BF, seed=20, size=8.0)
+    want = ol.latent_fwd(q, kv, pe, lens_q, lens_k, u=U[BF])
+    size = api().latent_fwd_workspace_bytes(1, sum(lens_q), sum(lens_k), H, 5)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")     # NaN wherever a part is not written
+    o, lse = run_fwd(q, kv, pe, lens_q, lens_k, workspace=ws)
+    assert binding.get_status(ws) == 0
+    near(o, want[0], want[2], "o")
+    near(lse, want[1], want[3], "lse")
+    bad = kv.clone()
+    bad[8200:8300] = float("nan")                                       # the second sequence's
+    again = run_fwd(q, bad, pe, lens_q, lens_k, workspace=ws)
+    rest = torch.tensor([i for i in range(sum(lens_q)) if not 260 <= i < 290], device="cuda")
+    assert torch.equal(again[0][rest], o[rest]) and torch.equal(again[1][rest], lse[rest])
+
+    dev = [t[None].cuda() for t in (q, kv, pe)]
+    cq, ck, graph = cu(lens_q), cu(lens_k), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go, gl = api().latent_fwd(*dev, cu_seqlens_q=cq, cu_seqlens_k=ck, workspace=ws)
+    ws.fill_(255)
+    graph.replay()
+    assert torch.equal(go[0], o) and torch.equal(gl[0], lse)
+    ck.copy_(cu([100, 8200, 50, 70, 300]))                              # another sequence is the long one
+    graph.replay()
+    ro, rl, eo, el = ol.latent_fwd(q, kv, pe, lens_q, [100, 8200, 50, 70, 300], u=U[BF])
+    near(go[0], ro, eo, "o, other lengths")
+    near(gl[0], rl, el, "lse, other lengths")
+
+    api().latent_fwd(*dev, cu_seqlens_q=cq, cu_seqlens_k=ck + 1, workspace=ws)
+    assert binding.get_status(ws) == 4
+    binding.debug_set(binding.KDA_DEBUG_WAIT_LIMIT, 1)
+    try:
+        api().latent_fwd(*dev, cu_seqlens_q=cq, cu_seqlens_k=ck, workspace=ws)
+        assert binding.get_status(ws) == 5
+    finally:
+        binding.debug_set(binding.KDA_DEBUG_WAIT_LIMIT, 0)
+    graph.replay()
+    assert binding.get_status(ws) == 0
+    near(go[0], ro, eo, "o, after a timeout")
+
+
 @pytest.mark.parametrize("size,scale", [(20.0, None), (1.0, 0.5), (0.01, None)])
 def test_fwd_peaked_and_flat_rows(size, scale):
     """Scores far apart (the running maximum moves often) and all alike."""
