@@ -233,10 +233,16 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
     index = q.get_device()
     B, Tq, H, _ = q.shape
     Tk, dev = kv.shape[1], q.device
-    _check("o", o, q.dtype, (B, Tq, H, VALUE_CHANNELS))
-    _check("do", do, q.dtype, (B, Tq, H, VALUE_CHANNELS))
-    _check("lse", lse, torch.float32, (B, Tq, H))
-    _same_device(index, o, lse, do)
+    try:
+        fine = (o.dtype is do.dtype is q.dtype and lse.dtype is torch.float32 and lse.shape == (B, Tq, H)
+                and o.shape == do.shape == (B, Tq, H, VALUE_CHANNELS) and _together(index, o, lse, do))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
+        _check("o", o, q.dtype, (B, Tq, H, VALUE_CHANNELS))
+        _check("do", do, q.dtype, (B, Tq, H, VALUE_CHANNELS))
+        _check("lse", lse, torch.float32, (B, Tq, H))
+        _same_device(index, o, lse, do)
     if index != _current_device():
         return _elsewhere(index, latent_bwd, q, kv, k_pe, o, lse, do, scale, causal, cu_seqlens_q, cu_seqlens_k, workspace)
     o, do, lse = _aligned(o.contiguous()), _aligned(do.contiguous()), lse.contiguous()
