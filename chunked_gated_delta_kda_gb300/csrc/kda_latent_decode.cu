@@ -20,7 +20,7 @@
 // which also writes the empty sequences.
 // One token of 256 sequences of 4096, H=32: 208 us, 5.8 TB/s (a tile every 3270
 // cycles, 6.5 TB/s, and some 15 us of plan, first loads, parts and join); of
-// lengths 1 to 8192 223 us, 5.5 TB/s; of one sequence of 65536, 25 us.  64 rows
+// lengths 1 to 8192 223 us, 5.5 TB/s; of one sequence of 65536, 23 us.  64 rows
 // (a unit's queries then leave room for two tiles) 64 x 8192 rows of cache 125
 // us, 4.8 TB/s; there, four tiles of 32 keys were slower (145).
 //   warps 0-3  softmax (row 16 w + l in lanes l and 16 + l of warp w, half of
@@ -545,15 +545,14 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
 
 // Joins the parts of the units that were cut: lse = log sum exp(lse_i),
 // o = sum exp(lse_i - lse) o_i, in a fixed order; writes zeros for empty
-// sequences.  Many units: a warp a row (WARPS = 1), 512 channels.  Few, with
-// many parts each: WARPS = 8 warps share the parts of 128 channels of a row
-// (one sequence of 65536, 152 parts of 32 rows: 26 us by 32 CTAs).
-template <int WARPS, bool FP16>
+// sequences.  WARPS warps share the parts of V groups of 128 channels of a row,
+// 8 / WARPS rows a CTA: few units have many parts each, many have few.
+template <int WARPS, int V, bool FP16>
 __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ DecodeParams p,
                                                           const __grid_constant__ DecodeScratch sc, int R, int mts, int ctas) {
-    constexpr int V = WARPS == 1 ? 4 : 1;              // groups of 128 channels a warp
+    constexpr int ROWS = 8 / WARPS;                    // of a CTA
     __shared__ float4 acc[WARPS == 1 ? 1 : 8][32];
-    __shared__ float stat[8][2];
+    __shared__ float stat[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = p.S * p.H;
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) {
@@ -571,8 +570,9 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
         c1 = (int)quotient((w0 + tiles) * g - 1, total);
         if (c0 == c1) return;
     }
-    const int r = WARPS == 1 ? blockIdx.y * 8 + warp : blockIdx.y, part = WARPS == 1 ? 0 : warp;
-    if (r >= R || mt * R + r >= rows) return;          // a whole CTA where warps work together
+    const int r = blockIdx.y * ROWS + warp / WARPS, part = warp % WARPS;   // r < R
+    const bool there = mt * R + r < rows;
+    if (WARPS == 1 && !there) return;                  // (warps that work together stay; such rows' parts are not used)
     // the first part of c0's unit is its last segment, unless the unit starts the range
     const int slot0 = 2 * c0 + (tiles > 0 && quotient(c0 * total, g) != w0 ? 1 : 0);
     auto slot_of = [&](int c) { return c == c0 ? slot0 : 2 * c; };
@@ -580,10 +580,10 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     float4 o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* src = reinterpret_cast<const float4*>(sc.o + (long long)r * LAT_C) + (WARPS == 1 ? 0 : blockIdx.z * 32) + lane;
+    const float4* src = reinterpret_cast<const float4*>(sc.o + (long long)r * LAT_C) + blockIdx.z * (32 * V) + lane;
     auto part_of = [&](int c) { return src + (long long)slot_of(c) * R * (LAT_C / 4); };
     // the parts' values do not depend on the weights: ask for them first
-    constexpr int BATCH = WARPS == 1 ? 2 : 10;
+    constexpr int BATCH = V == 4 ? 2 : WARPS == 8 ? 20 : 10;   // at once (152 parts of a unit: 20 beside 10 1.3 us less)
     float4 v[BATCH][V];
     auto fetch = [&](int first) {
 #pragma unroll
@@ -621,14 +621,14 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     }
     if constexpr (WARPS > 1) {
         acc[warp][lane] = o[0];
-        if (lane == 0) stat[warp][0] = l;
+        if (lane == 0) stat[warp] = l;
         __syncthreads();
-        if (warp != 0) return;
+        if (part != 0 || !there) return;
         l = 0.f;
         o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < WARPS; ++k) {
-            const float4 v = acc[k][lane];
-            l += stat[k][0];
+            const float4 v = acc[warp + k][lane];
+            l += stat[warp + k];
             o[0].x += v.x;
             o[0].y += v.y;
             o[0].z += v.z;
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
     }
     const long long at = (long long)n * rows + mt * R + r;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at * LAT_C) + (WARPS == 1 ? 0 : blockIdx.z * 32) + lane;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at * LAT_C) + blockIdx.z * (32 * V) + lane;
 #pragma unroll
     for (int e = 0; e < V; ++e)
         out[32 * e] = make_uint2(pack2<FP16>(o[e].x * inv, o[e].y * inv), pack2<FP16>(o[e].z * inv, o[e].w * inv));
@@ -666,12 +666,20 @@ cudaError_t launch(const DecodeParams& p, const DecMaps& maps, const DecodeScrat
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // Eight warps for a row, or one (us a call): R = 16, sequences of 2048: 4 of them 12.5 / 19.6, 12 18.1 / 18.6, 24
-    // 25.8 / 20.9, 64 40 / 23; R = 32: 4 15.3 / 20.8, 8 18.2 / 18.6, 12 24.0 / 20.5; R = 64: 4 19.6 / 22.6, 8 25.0 / 20.3.
-    const bool few = (long long)p.N * mts * R <= 256;
-    cfg.gridDim = few ? dim3(p.N * mts, R, 4) : dim3(p.N * mts, (R + 7) / 8);
-    return few ? cudaLaunchKernelEx(&cfg, latent_join_kernel<8, FP16>, p, sc, R, mts, DEC_CTAS)
-               : cudaLaunchKernelEx(&cfg, latent_join_kernel<1, FP16>, p, sc, R, mts, DEC_CTAS);
+    // By the rows of all units (us a call; 8, 4, 2, 1 warps for 128 channels of a row, 1 for 512).  R = 16, sequences of
+    // 2048: 4 of them 12.5 / 12.4 / 13.1 / 14.5 / 19.7, 8 15.0 / 13.5 / 13.4 / 14.1 / 17.5, 24 25.5 / 21.8 / 19.9 / 20.0 /
+    // 20.8, 48 45 / 38 / 34.7 / 32.7 / 33.0; R = 64: 1 14.4 / 14.8 / 16.0 / 16.4 / 21.3, 3 17.4 / 15.6 / 17.2 / 17.2 /
+    // 22.5, 6 22.6 / 18.8 / 17.5 / 19.4 / 21.7, 12 34.7 / 27.9 / 24.1 / 22.9 / 23.8, 48 96 / 68 / 54 / 47 / 42.
+    const int units = p.N * mts;
+    const long long of_all = (long long)units * R;
+    auto join = [&](auto kernel, int warps, int groups) {
+        cfg.gridDim = dim3(units, R / (8 / warps), 4 / groups);
+        return cudaLaunchKernelEx(&cfg, kernel, p, sc, R, mts, DEC_CTAS);
+    };
+    if (of_all <= 64) return join(latent_join_kernel<8, 1, FP16>, 8, 1);
+    if (of_all <= 192) return join(latent_join_kernel<4, 1, FP16>, 4, 1);
+    if (of_all <= 384) return join(latent_join_kernel<2, 1, FP16>, 2, 1);
+    return of_all < 1024 ? join(latent_join_kernel<1, 1, FP16>, 1, 1) : join(latent_join_kernel<1, 4, FP16>, 1, 4);
 }
 
 }  // namespace
