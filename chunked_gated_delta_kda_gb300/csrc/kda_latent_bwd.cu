@@ -1,6 +1,6 @@
 // Expanded latent attention, backward, in four launches:
 //   aux   D_i = dout_i . o_i and log2(e) lse_i of every query and head, laid
-//         out as the key kernel reads them
+//         out as the key kernel reads them; in fp16 the sizes of dout and v
 //   dq    one CTA for 128 queries of a head, over the keys:
 //           S = Q K^T, dP = dO V^T, dS = P (dP - D), dQ += dS K
 //   dkv   one CTA for 128 keys of a head, over the queries:
@@ -45,22 +45,84 @@ struct BwdMaps {
 // themselves would fall into fp16's subnormal range (below 6e-5).
 template <bool FP16> constexpr float P_SHIFT = FP16 ? 8.f : 0.f;
 
+// dS = P (dP - D) is as small as dout times the weights, which fp16 alone
+// cannot hold: with unit keys and queries, 2048 keys and dout of 1e-4 most of
+// it is below 6e-5 (dk off by 1.5e-2 of its norm), and large dout can put it
+// past 65504.  So fp16 dS carries a factor 2^k until dq and dk are scaled in
+// 32 bits, from 2 max |dout_i| max |v_j| >= |dP - D| of the sequence and head
+// (o is a mean of values): 2^k times that bound is in [2^13, 2^14), four times
+// below fp16's end, and the typical dS of L keys near 2^9 / L.  (bf16 has
+// fp32's range and k = 0.)  The two maxima (of squared norms, as bits; rows
+// that are not finite and queries without keys do not count) wait in the
+// sequence's rows of dk_pe, which the last launch writes and none reads: 16 lk
+// pairs, so heads share one only where they are more than 16 times the keys.
+__device__ __forceinline__ uint32_t* grad_sizes(const LatentParams& p, const LatentSeq& s, int h) {
+    return static_cast<uint32_t*>(p.dk_pe) + s.k0 * (LAT_P / 2) + 2 * (h % min((long long)p.H, s.lk * (LAT_P / 4ll)));
+}
+template <bool FP16>
+__device__ __forceinline__ int grad_shift(const LatentParams& p, const LatentSeq& s, int h) {
+    if (!FP16 || s.lq == 0 || s.lk == 0) return 0;
+    const uint2 w = __ldcg(reinterpret_cast<const uint2*>(grad_sizes(p, s, h)));
+    const float bound = 2.f * sqrtf(__uint_as_float(w.x)) * sqrtf(__uint_as_float(w.y));   // 0, or 2^-47 to 2^41
+    return bound > 0.f ? 13 - ((int)(__float_as_uint(bound) >> 23) - 127) : 0;
+}
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// The largest of the block's non-negative values into *to.
+__device__ __forceinline__ void block_max(float x, float (&part)[8], uint32_t* to) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) x = fmaxf(x, part[w]);
+        atomicMax(to, __float_as_uint(x));   // (its operands' order does not change a maximum)
+    }
+}
+
 // Per 64-query tile slot and head: 64 of log2(e) lse - P_SHIFT (+infinity for
 // rows past the end and rows without keys: their weights become 0), 64 of D.
+// In fp16 the blocks from `slots` on take the norms of a 64-key tile's values.
 template <bool FP16>
-__global__ void __launch_bounds__(256) latent_aux_kernel(const __grid_constant__ LatentParams p) {
+__global__ void __launch_bounds__(256) latent_aux_kernel(const __grid_constant__ LatentParams p, int slots) {
+    __shared__ float part[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h = blockIdx.y;
     int n, j;
     LatentSeq s;
+    if (FP16 && (int)blockIdx.x >= slots) {
+        if (!latent_find(p, p.cu_k, p.Tk, (int)blockIdx.x - slots, QT, n, j, s) || j * QT >= s.lk) return;
+        float most = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = j * QT + 2 * (8 * k + warp) + (lane >> 4);
+            float sq = 0.f;
+            if (i < s.lk) {
+                const uint4 a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.kv) +
+                                                               ((s.k0 + i) * p.H + h) * LAT_KV + LAT_N)[lane & 15];
+                const uint32_t* x = &a.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = unpack2<FP16>(x[e]);
+                    sq += u.x * u.x + u.y * u.y;
+                }
+            }
+#pragma unroll
+            for (int m = 8; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
+            if (sq < INFINITY) most = fmaxf(most, sq);
+        }
+        block_max(most, part, grad_sizes(p, s, h) + 1);
+        return;
+    }
     if (!latent_find(p, p.cu_q, p.Tq, blockIdx.x, QT, n, j, s) || j * QT >= s.lq) return;
-    const int h = blockIdx.y;
     float* aux = p.aux + ((long long)blockIdx.x * p.H + h) * 2 * QT;
+    float most = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {                       // two rows a warp at a time, 16 bytes a lane
         const int r = 2 * (8 * k + warp) + (lane >> 4);
         const int i = j * QT + r;
         const long long row = (s.q0 + i) * p.H + h;
-        float d = 0.f;
+        float d = 0.f, sq = 0.f;
         if (i < s.lq) {
             const uint4 a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + row * LAT_V)[lane & 15];
             const uint4 b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.o) + row * LAT_V)[lane & 15];
@@ -69,16 +131,22 @@ __global__ void __launch_bounds__(256) latent_aux_kernel(const __grid_constant__
             for (int e = 0; e < 4; ++e) {
                 const float2 u = unpack2<FP16>(x[e]), v = unpack2<FP16>(y[e]);
                 d += u.x * v.x + u.y * v.y;
+                if constexpr (FP16) sq += u.x * u.x + u.y * u.y;
             }
         }
 #pragma unroll
-        for (int m = 8; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+        for (int m = 8; m > 0; m >>= 1) {
+            d += __shfl_xor_sync(0xffffffffu, d, m);
+            if constexpr (FP16) sq += __shfl_xor_sync(0xffffffffu, sq, m);
+        }
         if ((lane & 15) == 0) {
             const float lse = i < s.lq ? p.lse[row] : -INFINITY;
             aux[r] = lse == -INFINITY ? INFINITY : lse * LOG2E - P_SHIFT<FP16>;
             aux[QT + r] = d;
+            if (FP16 && lse != -INFINITY && sq < INFINITY) most = fmaxf(most, sq);
         }
     }
+    if (FP16 && s.lk > 0) block_max(most, part, grad_sizes(p, s, h));
 }
 
 // Sixteen registers -> columns col .. col + 15 of this thread's lane.
@@ -283,10 +351,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         const int kmax = p.causal ? min(s.lk, row + shift + 1) : s.lk;
         const bool there = row < s.lq;
         float lse2 = INFINITY, delta = 0.f;
+        const int gs = grad_shift<FP16>(p, s, h);       // P here only makes dS: its factor is in lse2
         if (there) {   // the key kernel's tables: tile slot of 64 queries
             const int slot = p.cu_q == nullptr ? n * ((p.Tq + QT - 1) / QT) + row / QT : (int)(s.q0 / QT) + n + row / QT;
             const float* aux = p.aux + ((long long)slot * p.H + h) * 2 * QT + row % QT;
-            lse2 = aux[0] + P_SHIFT<FP16>;
+            lse2 = aux[0] + (P_SHIFT<FP16> - (float)gs);
             delta = aux[QT];
         }
         bool ok = true;
@@ -343,12 +412,17 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             // every product is done: Q's slabs take the result
             tc_fence_after();
             const int r = row - row0;
+            const float undo = pow2(-gs);
 #pragma unroll
             for (int b = 0; b < 3; ++b) {
                 float d[32];
                 if (steps > 0) {
                     tmem_ld32(t_dq + 96 * g + 32 * b + quad, d);
                     tmem_ld_wait();
+                    if constexpr (FP16) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) d[e] *= undo;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
@@ -541,6 +615,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         const int g = warp >> 2, key = key0 + (warp & 3) * 32 + lane;   // queries 32 g .. of a tile
         const uint32_t quad = (uint32_t)(warp & 3) << 21;
         const float c = p.scale * LOG2E;
+        const int gs = grad_shift<FP16>(p, s, h);
+        const float to_ds = pow2(gs - (int)P_SHIFT<FP16>);
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = ok && wait_warp(base + bar, parity, limit, failed);
@@ -601,7 +677,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             }
             if constexpr (FP16) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) d[e] *= 0.00390625f;      // 2^-P_SHIFT
+                for (int e = 0; e < 32; ++e) d[e] *= to_ds;            // P's factor off, dS's on
             }
             if (cut) {
 #pragma unroll
@@ -620,7 +696,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             // every product is done: K's and V's slabs take dk and dv, the stages the shared key's part in 32 bits
             tc_fence_after();
             const int r = key - key0;
-            const float f = g == 0 ? (FP16 ? 0.00390625f : 1.f) : p.scale;
+            const float f = g == 0 ? 1.f : p.scale, undo = pow2(g == 0 ? -(int)P_SHIFT<FP16> : -gs);
             const uint32_t src = (g == 0 ? t_dv : t_dk) + quad;
 #pragma unroll 1
             for (int b = 0; b < (g == 0 ? 4 : 6); ++b) {
@@ -630,7 +706,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     tmem_ld_wait();
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) d[e] = steps > 0 ? d[e] * f : 0.f;
+                for (int e = 0; e < 32; ++e) d[e] = steps > 0 ? (FP16 ? d[e] * undo : d[e]) * f : 0.f;
                 if (b < 4) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -693,7 +769,15 @@ cudaError_t launch(const LatentParams& p, const BwdMaps& maps, cudaStream_t stre
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (p.Tq > 0) {
-        latent_aux_kernel<FP16><<<dim3(latent_slots(varlen, p.Tq, p.N, QT), p.H), 256, 0, stream>>>(p);
+        const int aux_slots = latent_slots(varlen, p.Tq, p.N, QT);
+        const bool sizes = FP16 && p.Tk > 0;
+        if (sizes) {   // the maxima of grad_sizes begin at zero
+            const size_t rows = varlen ? p.Tk : (size_t)p.N * p.Tk;
+            e = cudaMemsetAsync(p.dk_pe, 0, rows * LAT_P * 2, stream);
+            if (e != cudaSuccess) return e;
+        }
+        latent_aux_kernel<FP16><<<dim3(aux_slots + (sizes ? latent_slots(varlen, p.Tk, p.N, QT) : 0), p.H), 256, 0, stream>>>(
+            p, aux_slots);
         const int slots = latent_slots(varlen, p.Tq, p.N, LAT_TILE);
         cfg.gridDim = dim3((unsigned)(slots * p.H));
         cfg.dynamicSmemBytes = D_SMEM;

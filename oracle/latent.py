@@ -111,6 +111,56 @@ def latent_bwd(q, kv, k_pe, do, lens_q: Sequence[int], lens_k: Sequence[int], ca
     return dq, dkv, dpe, eq, ekv, epe + u * dpe.abs() + tiny
 
 
+def latent_bwd_norms(q, kv, k_pe, do, lens_q: Sequence[int], lens_k: Sequence[int], scale: Optional[float] = None,
+                     u: float = 0.0, tiny: float = 0.0):
+    """Causal gradients whose errors are bounded in the Frobenius norm, a sequence and head at a time (the elementwise
+    bounds of latent_bwd add up absolute values and are some sqrt(L) wider, and they admit half a smallest step in
+    every weight).  o, lse: the exact ones, o rounded to the tensors' type, are what the backward is given.  Returns
+    (o, lse, [per sequence and head: dict of name -> (rows, head, channels, exact gradient, bound)]) with the names dq,
+    dk, dv; the shared key's gradient is summed over the heads, name dpe, head None.
+
+    dS = p (dP - D) is off by twice the scores' error and by one rounding of itself (u; its smallest step must not
+    count), by the 32-bit sums of dP, and by D's change with o's rounding.  A product with a matrix M then is off by at
+    most |error|_F |M|_2, by its own 32-bit sums (at most L steps of partial sums of that size) and by the result's
+    rounding."""
+    scale = SCALE if scale is None else scale
+    typed = q.dtype
+    q, kv, k_pe, do = q.double(), kv.double(), k_pe.double(), do.double()
+    o, lse, _, _ = latent_fwd(q, kv, k_pe, lens_q, lens_k, True, scale)
+    given = o.to(typed).double()
+    norm = lambda x: float(torch.linalg.matrix_norm(x)) if x.numel() else 0.0  # noqa: E731
+    spectral = lambda x: float(torch.linalg.matrix_norm(x, 2)) if x.numel() else 0.0  # noqa: E731
+    rounded = lambda x: norm((u * x.abs()).clamp(min=tiny))  # noqa: E731
+    out, a, b = [], 0, 0
+    for lq, lk in zip(lens_q, lens_k):
+        sees, dpe, epe = _sees(lq, lk, True), torch.zeros(lk, PE, dtype=torch.float64), 0.0
+        for h in range(q.shape[1]):
+            rq, rk = slice(a, a + lq), slice(b, b + lk)
+            qi, di, v = q[rq, h], do[rq, h], kv[rk, h, KEY:]
+            k = torch.cat([kv[rk, h, :KEY], k_pe[rk]], -1)
+            p, _ = _softmax(scale * (qi @ k.T), sees)
+            ds = p * (di @ v.T - (di * o[rq, h]).sum(-1, keepdim=True))
+            big = torch.where(sees, qi.abs() @ k.abs().T, torch.zeros_like(p)).amax(-1)
+            dx = 192 * F32 * scale * big + 2.0 ** -20 + F32 * lse[rq, h].abs().nan_to_num(posinf=0.0)
+            d_d = (di.abs() * (given[rq, h] - o[rq, h]).abs()).sum(-1, keepdim=True)
+            sums = 128 * F32 * (di.abs() @ v.abs().T + (di * o[rq, h]).abs().sum(-1, keepdim=True))
+            e_ds = norm((u + 2 * dx[:, None]) * ds.abs() + p * sums)
+            steps = F32 * max(lq, lk) * norm(ds)
+            dq, dk, dv = scale * (ds @ k), scale * (ds.T @ qi), p.T @ di
+            e_q = scale * ((e_ds + steps) * spectral(k) + norm(d_d * (p @ k)))
+            e_k = scale * ((e_ds + steps) * spectral(qi) + norm(p.T @ (d_d * qi.abs())))
+            # (a weight carries 2^8 in the tensors' type: half of its smallest step is tiny 2^-8)
+            e_v = (norm((u + 2 * dx[:, None]) * p) + F32 * lq * norm(p) + tiny * 2.0 ** -8 * float(sees.sum()) ** 0.5) * spectral(di)
+            out.append(dict(dq=(rq, h, slice(0, 192), dq, e_q + rounded(dq)),
+                            dk=(rk, h, slice(0, KEY), dk[:, :KEY], e_k + rounded(dk[:, :KEY])),
+                            dv=(rk, h, slice(KEY, KEY + VAL), dv, e_v + rounded(dv))))
+            dpe += dk[:, KEY:]
+            epe += e_k
+        out.append(dict(dpe=(slice(b, b + lk), None, slice(0, PE), dpe, epe + rounded(dpe))))
+        a, b = a + lq, b + lk
+    return o, lse, out
+
+
 def latent_decode(q, cache, table, lens, scale: Optional[float] = None, u: float = 0.0, tiny: float = 0.0):
     """q [N, S, H, 576], cache [pages, page_size, 576], table [N, W], lens [N].  Rows on a page that does not
     exist are masked, lengths are clipped to the table.  Returns (o, lse, err_o, err_lse)."""

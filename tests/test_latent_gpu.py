@@ -549,3 +549,62 @@ def test_training_layer():
     got = (dx.double() * step).sum().cpu()
     # sums of 96 * 256 terms with independent signs: a few bf16 roundings of dx's norm times the step's rms (1)
     assert (diff - got).abs() <= 8 * 2.0 ** -8 * dx.double().norm().cpu(), (diff, got)
+
+
+# ---------------------------------------------------------------------------
+# fp16 gradients: dS = P (dP - D) is as small as dout times the weights, or larger than fp16 holds.  A small scale of
+# the queries and keys (and a large one of the scores) makes dq and dk large beside dS, so that their own rounding to
+# fp16 does not hide dS's.
+HALF_GRADS = [
+    # lengths, size of dout of each (sequence, head), of the values, of queries and keys, scale
+    ([2048], [[2.0 ** -16]], 1.0, 2.0 ** -6, 2.0 ** 12 * 192 ** -0.5),
+    ([2048], [[2.0 ** -20]], 1.0, 2.0 ** -7, 2.0 ** 14 * 192 ** -0.5),
+    ([600, 2048, 1], [[2.0 ** 8] * 2, [2.0 ** -16] * 2, [1.0] * 2], 1.0, 2.0 ** -6, 2.0 ** 12 * 192 ** -0.5),   # sequences apart
+    ([700], [[2.0 ** 6, 2.0 ** -17]], 1.0, 2.0 ** -6, 2.0 ** 12 * 192 ** -0.5),                                 # heads apart
+    ([1, 2, 3], [[2.0 ** -10] * 40] * 3, 1.0, 2.0 ** -3, 2.0 ** 6 * 192 ** -0.5),     # more heads than a row's pairs
+    ([300], [[2.0 ** 12]], 2.0 ** 4, 2.0 ** -6, None),                                # dS beyond 65504
+    ([300], [[2.0 ** -12]], 2.0 ** 11, 1.0, None),                                    # large values
+]
+
+
+@pytest.mark.parametrize("lens,sizes,size_v,size_x,scale", HALF_GRADS)
+def test_bwd_fp16_gradients_of_any_size(lens, sizes, size_v, size_x, scale):
+    H = len(sizes[0])
+    q, kv, pe, do = (t.float() for t in expanded(lens, lens, H, torch.float32, seed=21))
+    for i, row in enumerate(sizes):
+        for h, size in enumerate(row):
+            do[sum(lens[:i]):sum(lens[:i + 1]), h] *= size
+    kv[..., :128] *= size_x
+    kv[..., 128:] *= size_v
+    q, kv, pe, do = (q * size_x).to(FP), kv.to(FP), (pe * size_x).to(FP), do.to(FP)
+    o, lse, parts = ol.latent_bwd_norms(q, kv, pe, do, lens, lens, scale, u=U[FP], tiny=TINY[FP])
+    dq, dkv, dpe = (t[0].double().cpu() for t in api().latent_bwd(
+        q[None].cuda(), kv[None].cuda(), pe[None].cuda(), o.to(FP)[None].cuda(), lse.float()[None].cuda(), do[None].cuda(),
+        scale=scale, cu_seqlens_q=cu(lens), cu_seqlens_k=cu(lens)))
+    for part in parts:
+        for name, (rows, h, channels, want, bound) in part.items():
+            got = {"dq": dq, "dk": dkv, "dv": dkv, "dpe": dpe}[name]
+            got = got[rows, channels] if h is None else got[rows, h, channels]
+            off = torch.linalg.matrix_norm(got - want).item()
+            assert off <= bound, (name, rows, h, off, bound)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 6e4])
+def test_other_sequences_never_reach_an_fp16_gradient(bad):
+    """Nor through the factor that dS carries; and rows that see no key, whatever their dout, do not choose it."""
+    lens_q, lens_k, runs = [70, 90, 130], [70, 60, 130], []
+    q, kv, pe, do = expanded(lens_q, lens_k, 2, FP, seed=22)
+    do = do * 2.0 ** -10
+    for fill in (None, bad):
+        x = [t.clone() for t in (q, kv, pe, do)]
+        if fill is not None:
+            for t, keys in zip(x, (False, True, True, False)):
+                t[:70] = fill
+                t[130 if keys else 160:] = fill
+            x[3][70:100] = 6e4
+        o, lse = run_fwd(*x[:3], lens_q, lens_k)
+        g = api().latent_bwd(*(t[None].cuda() for t in x[:3]), o[None], lse[None], x[3][None].cuda(),
+                             cu_seqlens_q=cu(lens_q), cu_seqlens_k=cu(lens_k))
+        runs.append([g[0][0, 70:160], g[1][0, 70:130], g[2][0, 70:130]])
+    for a, b in zip(*runs):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
