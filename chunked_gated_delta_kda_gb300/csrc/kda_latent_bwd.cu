@@ -778,6 +778,8 @@ cudaError_t launch(const LatentParams& p, const BwdMaps& maps, cudaStream_t stre
         }
         latent_aux_kernel<FP16><<<dim3(aux_slots + (sizes ? latent_slots(varlen, p.Tk, p.N, QT) : 0), p.H), 256, 0, stream>>>(
             p, aux_slots);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
         const int slots = latent_slots(varlen, p.Tq, p.N, LAT_TILE);
         cfg.gridDim = dim3((unsigned)(slots * p.H));
         cfg.dynamicSmemBytes = D_SMEM;

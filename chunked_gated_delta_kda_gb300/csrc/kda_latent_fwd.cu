@@ -576,7 +576,11 @@ cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, int ra
     const auto kernel = latent_fwd_kernel<FP16, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
     if (e != cudaSuccess) return e;
-    if (SPLIT == SHARED) latent_share_kernel<<<1, SHARE_SLOTS, 0, stream>>>(p, slots);
+    if (SPLIT == SHARED) {   // (the kernel behind it takes its records as they are)
+        latent_share_kernel<<<1, SHARE_SLOTS, 0, stream>>>(p, slots);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute attr[1];
     if (SPLIT == CLUSTER) {
         attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -2,6 +2,10 @@
 and refusals, all before any CUDA call."""
 
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -189,3 +193,69 @@ def test_fwd_with_a_workspace_refusals():
         ws=p, wsb=256, stream=None))
     for kw in (dict(q=None), dict(o=None), dict(wsb=255), dict(wsb=0), dict(ws=p + 64), dict(N=2), dict(flags=1)):
         assert call(**kw) == 1, kw
+
+
+# A runtime whose n-th launch fails, in front of the real one: no GPU is needed, nothing runs.
+FAKE_RUNTIME = r"""
+static int count = 0, last = 0, fail_at = 0;
+void fake_begin(int at) { count = last = 0; fail_at = at; }
+int fake_launches(void) { return count; }
+static int launched(void) { return ++count == fail_at ? (last = 719) : 0; }
+int __cudaLaunchKernel(void) { return launched(); }
+int cudaLaunchKernel(void) { return launched(); }
+int cudaLaunchKernelExC(void) { return launched(); }
+int __cudaGetKernel(void) { return 0; }
+int cudaFuncSetAttribute(void) { return 0; }
+int cudaMemsetAsync(void) { return 0; }
+int cudaGetLastError(void) { int e = last; last = 0; return e; }
+static int encode(void) { return 0; }
+int cudaGetDriverEntryPointByVersion(const char* name, void** f, unsigned version, unsigned long long flags, int* found) {
+    *f = (void*)encode; *found = 0; return 0;
+}
+"""
+FAKE_CALLS = r"""
+import ctypes
+from chunked_gated_delta_kda_gb300 import binding
+lib = binding.load_library()
+buf = (ctypes.c_uint8 * 4096)()
+p = ctypes.addressof(buf) + (-ctypes.addressof(buf) % 256)
+big = 1 << 40
+calls = dict(
+    fwd=lambda: lib.kda_latent_fwd(p, p, p, 64, 0.0, None, None, p, p, 1, 64, 64, 2, 1, 0, None, None),
+    fwd_shared=lambda: lib.kda_latent_fwd_ws(p, p, p, 64, 0.0, p, p, p, p, 1, 64, 8192, 1, 30, 0, p, big, None),
+    bwd=lambda: lib.kda_latent_bwd(p, p, p, 64, p, p, p, 0.0, None, None, p, p, p, 1, 64, 64, 2, 1, 0, p, big, None),
+    bwd_fp16=lambda: lib.kda_latent_bwd(p, p, p, 64, p, p, p, 0.0, None, None, p, p, p, 1, 64, 64, 2, 1, 128, p, big, None),
+    decode=lambda: lib.kda_latent_decode(p, p, 4, 64, p, 2, p, 0.0, p, p, 2, 1, 16, 0, p, big, None),
+    append=lambda: lib.kda_latent_append(p, 576, p, None, 1e-6, p, 64, 5, 0, None, None),
+    tables=lambda: lib.kda_block_tables(p, p, p, 2, p, 1, p, 16, p, 1, p, p, p, 1, None, None))
+fake = ctypes.CDLL(None)
+for name, call in calls.items():
+    for at in range(5):
+        fake.fake_begin(at)
+        print(name, at, call(), fake.fake_launches())
+"""
+
+
+@pytest.fixture(scope="module")
+def fake_launches(tmp_path_factory):
+    """{(call, launch that fails): (status, launches tried)}"""
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    at = tmp_path_factory.mktemp("fake")
+    (at / "fake.c").write_text(FAKE_RUNTIME)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(at / "fake.so"), str(at / "fake.c")], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FAKE_CALLS], env=dict(os.environ, LD_PRELOAD=str(at / "fake.so"), PYTHONPATH=root),
+                         cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr[-1000:]
+    return {(name, int(at)): (int(rc), int(n)) for name, at, rc, n in (line.split() for line in out.stdout.splitlines())}
+
+
+@pytest.mark.parametrize("call,launches", [("fwd", 1), ("fwd_shared", 3), ("bwd", 4), ("bwd_fp16", 4), ("decode", 2),
+                                           ("append", 1), ("tables", 1)])
+def test_a_failed_launch_ends_the_call(fake_launches, call, launches):
+    """What follows reads what the failed one would have written (work items among it): it is not launched, and the
+    call says so."""
+    assert fake_launches[call, 0] == (0, launches)
+    for at in range(1, launches + 1):
+        assert fake_launches[call, at] == (3, at), at
