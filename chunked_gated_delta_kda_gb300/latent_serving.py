@@ -20,7 +20,7 @@ from __future__ import annotations
 
 import torch
 
-from . import latent
+from . import binding, latent
 from .latent import KEY_CHANNELS, LATENT_CHANNELS, PE_CHANNELS, ROW_CHANNELS, VALUE_CHANNELS
 
 
@@ -44,14 +44,23 @@ class LatentLayer:
         self.lens = torch.zeros(requests, **i32)
         self.free = torch.randperm(pages, generator=gen, device=device).to(torch.int32)
         self.head = torch.zeros(1, **i32)
+        self.status = torch.zeros(latent.STATUS_BYTES, dtype=torch.uint8, device=device)
 
     def _query(self, x):
         return (x @ self.w_q.T).view(*x.shape[:-1], self.heads, KEY_CHANNELS + PE_CHANNELS)
 
     def _advance(self, rows, new_lens):
-        """Pages for new_lens [N] tokens, and their rows [T, 576] (latent channels normalised) into the cache."""
-        slots, cu, self.lens, self.head = latent.block_tables(self.lens, new_lens, self.table, self.free, self.head,
-                                                              self.page_size, rows.shape[0])
+        """Pages for new_lens [N] tokens, and their rows [T, 576] (latent channels normalised) into the cache.  Where
+        a token gets no page (slot -1, which must not be looked up) or there is not one row a token, raises and leaves
+        lengths and cache as they were."""
+        slots, cu, lens, head = latent.block_tables(self.lens, new_lens, self.table, self.free, self.head, self.page_size,
+                                                    rows.shape[0], workspace=self.status)
+        status = binding.get_status(self.status)
+        if status != 0:
+            raise binding.KdaError(status, "LatentLayer")
+        if int(cu[-1]) != rows.shape[0]:
+            raise ValueError(f"{rows.shape[0]} rows for {int(cu[-1])} new tokens")
+        self.lens, self.head = lens, head
         latent.latent_append(rows, slots, self.cache, norm_weight=self.norm)
         return slots, cu
 

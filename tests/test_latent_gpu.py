@@ -608,3 +608,26 @@ def test_other_sequences_never_reach_an_fp16_gradient(bad):
         runs.append([g[0][0, 70:160], g[1][0, 70:130], g[2][0, 70:130]])
     for a, b in zip(*runs):
         assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+def test_serving_layer_without_room_says_so():
+    """A token without a page, in the free list or in the table, or rows that do not match the lengths: an error in
+    place of another row's keys, and the layer goes on as if the step had not been."""
+    from chunked_gated_delta_kda_gb300 import binding
+    from chunked_gated_delta_kda_gb300.latent_serving import LatentLayer
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(200, 128, generator=g, device="cuda").to(BF)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for room in (dict(pages=3, width=8), dict(pages=8, width=1)):
+        layer, fresh = (LatentLayer(128, 2, 2, page_size=64, **room) for _ in range(2))
+        with pytest.raises(binding.KdaError) as e:
+            layer.prefill(x, i32(150, 50))
+        assert e.value.code == 8
+        with pytest.raises(ValueError, match="rows"):
+            layer.prefill(x[:70], i32(40, 20))
+        assert layer.lens.tolist() == [0, 0] and layer.head.item() == 0 and layer.cache.count_nonzero() == 0
+        assert torch.equal(layer.prefill(x[:127], i32(64, 63)), fresh.prefill(x[:127], i32(64, 63)))
+        with pytest.raises(binding.KdaError):
+            for _ in range(80):
+                layer.decode(x[:2])
+        assert layer.lens.tolist() == ([64, 63] if room["width"] == 1 else [65, 64])
