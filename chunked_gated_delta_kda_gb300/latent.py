@@ -93,12 +93,20 @@ def _status_workspace(workspace, index: int) -> Optional[int]:
 
 
 def _scratch(workspace, need: int, index: int, device) -> torch.Tensor:
-    """The caller's workspace, or a fresh one where there is none or it is too small."""
+    """The caller's workspace, or a fresh one where there is none or it is too small (see ``_hand_back``)."""
     if workspace is not None:
         _check_workspace(workspace, index)
         if workspace.numel() * workspace.element_size() >= need:
             return workspace
     return torch.empty(max(need, STATUS_BYTES), dtype=torch.uint8, device=device)
+
+
+def _hand_back(scratch, workspace) -> None:
+    """After the launch: what the call recorded goes to the caller's workspace where a larger one stood in for it."""
+    if workspace is not None and workspace is not scratch:
+        own = workspace.view(-1).view(torch.uint8)
+        count = min(STATUS_BYTES, own.numel())
+        own[:count].copy_(scratch[:count])
 
 
 def _scale(scale) -> float:
@@ -228,7 +236,9 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
                workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Backward of ``latent_fwd`` with the same arguments, its results o and
     lse, and o's gradient ``do``: returns (dq, dkv, dk_pe) in q's type, dk_pe
-    summed over the heads.  Deterministic."""
+    summed over the heads.  Deterministic.  ``workspace`` (256-byte aligned)
+    has ``latent_bwd_workspace_bytes`` bytes; beside a smaller one another is
+    allocated, and the status still goes to it."""
     q, kv, k_pe, stride, N, flags, cu_seqlens_q, cu_seqlens_k = _expanded(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k)
     index = q.get_device()
     B, Tq, H, _ = q.shape
@@ -247,15 +257,16 @@ def latent_bwd(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, o: torch.T
         return _elsewhere(index, latent_bwd, q, kv, k_pe, o, lse, do, scale, causal, cu_seqlens_q, cu_seqlens_k, workspace)
     o, do, lse = _aligned(o.contiguous()), _aligned(do.contiguous()), lse.contiguous()
     need = latent_bwd_workspace_bytes(B, Tq, Tk, H, N)
-    workspace = _scratch(workspace, need, index, dev)
+    scratch = _scratch(workspace, need, index, dev)
     dq = torch.empty_like(q)
     dkv = torch.empty_like(kv)
     dk_pe = torch.empty((B, Tk, PE_CHANNELS), dtype=q.dtype, device=dev)
     _raise(load_library().kda_latent_bwd(
         q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), stride, o.data_ptr(), lse.data_ptr(), do.data_ptr(),
         _scale(scale), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), dq.data_ptr(), dkv.data_ptr(),
-        dk_pe.data_ptr(), B, Tq, Tk, H, N, flags | KDA_FLAG_CAUSAL if causal else flags, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(index)), "kda_latent_bwd")
+        dk_pe.data_ptr(), B, Tq, Tk, H, N, flags | KDA_FLAG_CAUSAL if causal else flags, scratch.data_ptr(),
+        scratch.numel() * scratch.element_size(), _stream(index)), "kda_latent_bwd")
+    _hand_back(scratch, workspace)
     return dq, dkv, dk_pe
 
 
@@ -274,7 +285,8 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     seq_lens: int32 [N], the S tokens included: token s sees the first
     seq_lens - S + 1 + s rows.  ``scale`` None means 192**-0.5.  Returns
     (o [N, S, H, 512], lse fp32 [N, S, H]); a token that sees no row gets 0
-    and -inf."""
+    and -inf.  ``workspace`` as for ``latent_bwd``, with
+    ``latent_decode_workspace_bytes`` bytes."""
     flags = _float_flag("q", q)
     dtype = q.dtype
     try:
@@ -299,13 +311,14 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         raise ValueError("cache must be contiguous")
     q, block_table, seq_lens = _aligned(q.contiguous()), block_table.contiguous(), seq_lens.contiguous()
     need = latent_decode_workspace_bytes(N, S, H)
-    workspace = _scratch(workspace, need, index, dev)
+    scratch = _scratch(workspace, need, index, dev)
     o = torch.empty((N, S, H, LATENT_CHANNELS), dtype=q.dtype, device=dev)
     lse = torch.empty((N, S, H), dtype=torch.float32, device=dev)
     _raise(load_library().kda_latent_decode(
         q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
         seq_lens.data_ptr(), _scale(scale), o.data_ptr(), lse.data_ptr(), N, S, H, flags,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(index)), "kda_latent_decode")
+        scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(index)), "kda_latent_decode")
+    _hand_back(scratch, workspace)
     return o, lse
 
 

@@ -631,3 +631,24 @@ def test_serving_layer_without_room_says_so():
             for _ in range(80):
                 layer.decode(x[:2])
         assert layer.lens.tolist() == ([64, 63] if room["width"] == 1 else [65, 64])
+
+
+@pytest.mark.parametrize("size,dtype", [(256, torch.uint8), (1000, torch.uint8), (64, torch.float32)])
+def test_a_workspace_that_is_too_small_still_gets_the_status(size, dtype):
+    """The calls use another one beside it; what they record must not stay there."""
+    from chunked_gated_delta_kda_gb300 import binding
+    ws = torch.zeros(size, dtype=dtype, device="cuda")
+    cache, table = (t.cuda() for t in paged([40], 16, BF, seed=23))
+    n = torch.tensor([40], dtype=torch.int32, device="cuda")
+    qd = torch.randn(1, 1, 4, 576, generator=torch.Generator().manual_seed(24)).to(BF).cuda()
+    want = api().latent_decode(qd, cache, table, n)
+    for lens, status in ((n, 0), (n + 9, 8), (n, 0)):   # a fault, and none again
+        got = api().latent_decode(qd, cache, table, lens, workspace=ws)
+        assert binding.get_status(ws) == status
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    q, kv, pe, do = (t[None].cuda() for t in expanded([20], [20], 1, BF, seed=25))
+    o, lse = api().latent_fwd(q, kv, pe)
+    down = torch.tensor([0, 15, 12, 20], dtype=torch.int32, device="cuda")
+    for c, status in ((cu([20]), 0), (down, 4), (cu([20]), 0)):
+        api().latent_bwd(q, kv, pe, o, lse, do, cu_seqlens_q=c, cu_seqlens_k=c, workspace=ws)
+        assert binding.get_status(ws) == status
