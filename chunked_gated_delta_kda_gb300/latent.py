@@ -31,6 +31,7 @@ VALUE_CHANNELS = 128
 QUERY_CHANNELS = KEY_CHANNELS + PE_CHANNELS
 STATUS_BYTES = 256
 FP32 = torch.finfo(torch.float32)
+INT_MAX = 2 ** 31 - 1
 SHARED_KEYS = 8192   # packed keys below which latent_fwd has no use for a workspace
 
 _FLOAT_FLAGS = {torch.bfloat16: 0, torch.float16: KDA_FLAG_FP16}
@@ -50,6 +51,12 @@ def _check(name: str, t, dtype, shape) -> None:
     if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
         want = ", ".join("*" if w is None else str(w) for w in shape)
         raise ValueError(f"{name} must have shape [{want}], got {tuple(t.shape)}")
+
+
+def _check_int(name: str, value) -> None:
+    """The C entries take 32 bits, and ctypes drops the others."""
+    if not -INT_MAX <= value <= INT_MAX or value != int(value):
+        raise ValueError(f"{name} must be a whole number of 32 bits, got {value}")
 
 
 def _float_flag(name: str, t) -> int:
@@ -293,6 +300,7 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         fine = (q.dim() == 4 and cache.dim() == 3 and block_table.dim() == 2 and cache.dtype is dtype
                 and block_table.dtype is torch.int32 and seq_lens.dtype is torch.int32
                 and q.shape[3] == cache.shape[2] == ROW_CHANNELS and seq_lens.shape == block_table.shape[:1] == q.shape[:1]
+                and block_table.size(1) <= INT_MAX
                 and _together(q.get_device(), cache, block_table, seq_lens))
     except AttributeError:   # not a tensor
         fine = False
@@ -301,6 +309,7 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
         _check("block_table", block_table, torch.int32, (q.shape[0], None))
         _check("seq_lens", seq_lens, torch.int32, (q.shape[0],))
+        _check_int("block_table's width", block_table.shape[1])
         _same_device(q.get_device(), cache, block_table, seq_lens)
     index = q.get_device()
     if index != _current_device():
@@ -380,10 +389,17 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
         fine = (seq_lens.dtype is new_lens.dtype is block_table.dtype is free_pages.dtype is free_head.dtype is torch.int32
                 and seq_lens.dim() == free_pages.dim() == 1 and block_table.dim() == 2 and free_head.shape == (1,)
                 and new_lens.shape == seq_lens.shape == block_table.shape[:1]
+                and 0 < page_size <= INT_MAX and num_tokens <= INT_MAX and page_size % 1 == num_tokens % 1 == 0
+                and seq_lens.numel() <= INT_MAX and block_table.size(1) <= INT_MAX and free_pages.numel() <= INT_MAX
                 and _together(seq_lens.get_device(), new_lens, block_table, free_pages, free_head))
     except AttributeError:   # not a tensor
         fine = False
     if not fine:
+        _check_int("page_size", page_size)
+        _check_int("num_tokens", num_tokens)
+        for name, t in (("seq_lens", seq_lens), ("block_table", block_table), ("free_pages", free_pages)):
+            for size in getattr(t, "shape", ()):
+                _check_int(f"a size of {name}", size)
         _check("seq_lens", seq_lens, torch.int32, (None,))
         _check("new_lens", new_lens, torch.int32, seq_lens.shape)
         _check("block_table", block_table, torch.int32, (seq_lens.shape[0], None))

@@ -259,3 +259,21 @@ def test_a_failed_launch_ends_the_call(fake_launches, call, launches):
     assert fake_launches[call, 0] == (0, launches)
     for at in range(1, launches + 1):
         assert fake_launches[call, at] == (3, at), at
+
+
+def test_sizes_that_do_not_fit_the_c_entries_are_refused():
+    """2^32 + 16 would arrive as 16."""
+    z = lambda *s, d=torch.int32: torch.zeros(1, dtype=d).expand(s)  # noqa: E731
+    big = 2 ** 32 + 16
+    good = dict(seq_lens=z(1), new_lens=z(1), block_table=z(1, 1), free_pages=z(1), free_head=z(1), page_size=16, num_tokens=1)
+    for name, value in (("page_size", big), ("page_size", 16 - 2 ** 32), ("page_size", 16.5), ("num_tokens", big), ("num_tokens", 2 ** 31),
+                        ("block_table", z(1, big)), ("free_pages", z(big))):
+        with pytest.raises(ValueError, match=name):
+            latent.block_tables(**{**good, name: value})
+    with pytest.raises(ValueError, match="seq_lens"):
+        latent.block_tables(**{**good, "seq_lens": z(big), "new_lens": z(big), "block_table": z(big, 1)})
+    with pytest.raises(ValueError, match="CUDA"):
+        latent.block_tables(**good)
+    latent._check_int("width", 2 ** 31 - 1)
+    with pytest.raises(ValueError, match="width"):
+        latent._check_int("width", 2 ** 31)
