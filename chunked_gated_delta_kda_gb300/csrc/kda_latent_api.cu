@@ -27,9 +27,11 @@ unsigned long long round256(unsigned long long b) { return (b + 255ull) / 256ull
 
 float scale_of(float s) { return s > 0.f && !std::isnan(s) ? s : 1.0f / std::sqrt((float)kda::LAT_QK); }
 
+// (the last line: a CTA a tile slot and head, in one dimension of a grid)
 bool sizes_ok(int B, int Tq, int Tk, int H, int N) {
     return B >= 1 && Tq >= 0 && Tk >= 0 && H >= 1 && N >= 1 && H <= 65535 && N <= 65535 &&
-           (long long)B * Tq < (1ll << 31) && (long long)B * Tk < (1ll << 31);
+           (long long)B * Tq < (1ll << 31) && (long long)B * Tk < (1ll << 31) &&
+           ((long long)B * (Tq > Tk ? Tq : Tk) / kda::LAT_TILE + N) * H < (1ll << 31);
 }
 
 // The checks that forward and backward share.

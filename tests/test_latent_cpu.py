@@ -227,6 +227,8 @@ calls = dict(
     bwd_fp16=lambda: lib.kda_latent_bwd(p, p, p, 64, p, p, p, 0.0, None, None, p, p, p, 1, 64, 64, 2, 1, 128, p, big, None),
     decode=lambda: lib.kda_latent_decode(p, p, 4, 64, p, 2, p, 0.0, p, p, 2, 1, 16, 0, p, big, None),
     append=lambda: lib.kda_latent_append(p, 576, p, None, 1e-6, p, 64, 5, 0, None, None),
+    fwd_huge=lambda: lib.kda_latent_fwd(p, p, p, 64, 0.0, p, p, p, p, 1, 512, 512, 65535, 65535, 0, None, None),
+    bwd_huge=lambda: lib.kda_latent_bwd(p, p, p, 64, p, p, p, 0.0, p, p, p, p, p, 1, 512, 512, 65535, 65535, 0, p, 1 << 50, None),
     tables=lambda: lib.kda_block_tables(p, p, p, 2, p, 1, p, 16, p, 1, p, p, p, 1, None, None))
 fake = ctypes.CDLL(None)
 for name, call in calls.items():
@@ -277,3 +279,13 @@ def test_sizes_that_do_not_fit_the_c_entries_are_refused():
     latent._check_int("width", 2 ** 31 - 1)
     with pytest.raises(ValueError, match="width"):
         latent._check_int("width", 2 ** 31)
+
+
+@pytest.mark.parametrize("Tq,Tk,N", [(1, 1, 65535), (512, 1, 65535), (1, 512, 65535), (512, 512, 32768)])
+def test_more_tiles_and_heads_than_a_grid_are_refused(fake_launches, Tq, Tk, N):
+    """512 rows in 65535 sequences with 65535 heads came out as a grid of 2^32 and some CTAs, cut to the some."""
+    lib = binding.load_library()
+    assert lib.kda_latent_fwd_workspace_bytes(1, Tq, Tk, 65535, N) == 0
+    assert lib.kda_latent_bwd_workspace_bytes(1, Tq, Tk, 65535, N) == 0
+    assert lib.kda_latent_bwd_workspace_bytes(1, 1, 1, 65535, 32767) > 0
+    assert fake_launches["fwd_huge", 0] == fake_launches["bwd_huge", 0] == (1, 0)
