@@ -652,3 +652,90 @@ def test_a_workspace_that_is_too_small_still_gets_the_status(size, dtype):
     for c, status in ((cu([20]), 0), (down, 4), (cu([20]), 0)):
         api().latent_bwd(q, kv, pe, o, lse, do, cu_seqlens_q=c, cu_seqlens_k=c, workspace=ws)
         assert binding.get_status(ws) == status
+
+
+# ---------------------------------------------------------------------------
+def mixed(n, seed, empty=()):
+    """n lengths around the tiles' borders, many of none or one, `empty` (a range) of none."""
+    g = torch.Generator().manual_seed(seed)
+    some = [0, 0, 1, 1, 2, 5, 63, 64, 65, 127, 128, 129, 130, 257]
+    lens = [some[i] for i in torch.randint(0, len(some), (n,), generator=g).tolist()]
+    return [0 if i in empty else l for i, l in enumerate(lens)]
+
+
+def fwd_and_bwd(lens_q, lens_k, H, dtype, causal, seed):
+    q, kv, pe, do = expanded(lens_q, lens_k, H, dtype, seed=seed)
+    o, lse = run_fwd(q, kv, pe, lens_q, lens_k, causal)
+    ro, rl, eo, el = ol.latent_fwd(q, kv, pe, lens_q, lens_k, causal, u=U[dtype], tiny=TINY[dtype])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
+    got = api().latent_bwd(q[None].cuda(), kv[None].cuda(), pe[None].cuda(), o[None], lse[None], do[None].cuda(),
+                           causal=causal, cu_seqlens_q=cu(lens_q), cu_seqlens_k=cu(lens_k))
+    want = ol.latent_bwd(q, kv, pe, do, lens_q, lens_k, causal, u=U[dtype], tiny=TINY[dtype])
+    for g, w, e, name in zip(got, want[:3], want[3:], ("dq", "dkv", "dk_pe")):
+        near(g[0], w, e, name)
+
+
+@pytest.mark.parametrize("n,H,dtype,causal,empty", [
+    (30, 2, BF, True, range(0)), (31, 2, FP, True, range(0, 4)), (32, 2, BF, False, range(28, 32)),
+    (33, 1, FP, True, range(30, 33)), (70, 3, BF, True, range(27, 40)), (70, 2, FP, False, range(0, 33)),
+    (257, 1, BF, True, range(100, 180))])
+def test_many_packed_sequences(n, H, dtype, causal, empty):
+    """Up to 31 sequences a tile finds its own by one vote, from 32 on by bisection."""
+    fwd_and_bwd(mixed(n, n, empty), mixed(n, n + 1000, range(5, 8)), H, dtype, causal, n)
+
+
+@pytest.mark.parametrize("n,long,dtype", [(31, 20, BF), (32, 0, FP), (70, 69, BF)])
+def test_many_packed_sequences_that_share_keys(n, long, dtype):
+    lens_q, lens_k = mixed(n, n, range(10, 14)), mixed(n, n + 1)
+    lens_q[long], lens_k[long] = 300, 8300
+    assert api().latent_fwd_workspace_bytes(1, sum(lens_q), sum(lens_k), 2, n) > 256
+    fwd_and_bwd(lens_q, lens_k, 2, dtype, True, n)
+
+
+@pytest.mark.parametrize("n,dtype", [(31, FP), (34, BF)])
+def test_many_packed_sequences_in_clusters(n, dtype):
+    """2048 keys a sequence on average, few queries: clusters."""
+    lens_q = [l % 30 for l in mixed(n, n, range(6, 9))]
+    lens_k = [0 if i % 7 == 3 else 2900 + 131 * (i % 5) for i in range(n)]
+    assert sum(lens_k) >= 2048 * n and api().latent_fwd_workspace_bytes(1, sum(lens_q), sum(lens_k), 1, n) == 256
+    fwd_and_bwd(lens_q, lens_k, 1, dtype, True, n)
+
+
+@pytest.mark.parametrize("B,Tq,Tk,H,dtype,causal", [
+    (3, 70, 200, 2, BF, True), (2, 300, 129, 2, FP, True), (4, 1, 65, 3, FP, False), (40, 33, 33, 1, FP, True),
+    (1, 20, 4100, 2, BF, True), (2, 5, 2100, 3, FP, False)])             # the last two: clusters
+def test_fixed_length(B, Tq, Tk, H, dtype, causal):
+    q, kv, pe, do = expanded([Tq] * B, [Tk] * B, H, dtype, seed=B * Tk)
+    lead = lambda t: t.view(B, -1, *t.shape[1:]).cuda()  # noqa: E731
+    flat = lambda t: t.flatten(0, 1)  # noqa: E731
+    o, lse = api().latent_fwd(lead(q), lead(kv), lead(pe), causal=causal)
+    ro, rl, eo, el = ol.latent_fwd(q, kv, pe, [Tq] * B, [Tk] * B, causal, u=U[dtype], tiny=TINY[dtype])
+    near(flat(o), ro, eo, "o")
+    near(flat(lse), rl, el, "lse")
+    got = api().latent_bwd(lead(q), lead(kv), lead(pe), o, lse, lead(do), causal=causal)
+    want = ol.latent_bwd(q, kv, pe, do, [Tq] * B, [Tk] * B, causal, u=U[dtype], tiny=TINY[dtype])
+    for g, w, e, name in zip(got, want[:3], want[3:], ("dq", "dkv", "dk_pe")):
+        near(flat(g), w, e, name)
+
+
+@pytest.mark.parametrize("page,S,H,dtype", [(16, 1, 4, BF), (32, 2, 16, FP), (64, 1, 64, BF), (128, 3, 5, FP)])
+def test_decode_missing_pages_meet_what_the_tiles_before_left(page, S, H, dtype):
+    """Rows that no token sees are NaN, each CTA walks some ten tiles, so the ring slots of rows on missing pages hold
+    NaN of sequences before."""
+    from chunked_gated_delta_kda_gb300 import binding
+    g = torch.Generator().manual_seed(page)
+    lens = torch.randint(1, 260, (600,), generator=g).tolist()
+    cache, table = paged(lens, page, dtype, seed=page, fill=float("nan"))
+    for i in range(0, 600, 2):                            # every other sequence misses pages, its first or last ones too
+        cells = -(-lens[i] // page)
+        for j in torch.randint(0, cells, (1 + i % 3,), generator=g).tolist():
+            table[i, j] = (-1, cache.shape[0], 1 << 30)[i % 3]
+    q = torch.randn(600, S, H, 576, generator=g).to(dtype)
+    n = torch.tensor(lens, dtype=torch.int32)
+    ws = torch.zeros(api().latent_decode_workspace_bytes(600, S, H), dtype=torch.uint8, device="cuda")
+    o, lse = api().latent_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), workspace=ws)
+    assert binding.get_status(ws) == 8
+    ro, rl, eo, el = ol.latent_decode(q, cache, table, n, u=U[dtype], tiny=TINY[dtype])
+    near(o, ro, eo, "o")
+    near(lse, rl, el, "lse")
