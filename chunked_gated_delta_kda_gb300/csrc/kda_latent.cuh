@@ -81,6 +81,16 @@ __device__ __forceinline__ bool latent_seq(const LatentParams& p, int n, LatentS
     return true;
 }
 
+// A decreasing step in either list, looked for by `threads` threads: the tile
+// slots of a list that is not sorted can pass over a sequence (0, 600, 300, 900
+// with tiles of 256: its second), whose offsets latent_seq then never sees.
+__device__ __forceinline__ void check_offsets(const LatentParams& p, int t, int threads) {
+    if (p.cu_q == nullptr || p.status == nullptr) return;
+    bool bad = false;
+    for (int n = t; n < p.N; n += threads) bad |= p.cu_q[n + 1] < p.cu_q[n] || p.cu_k[n + 1] < p.cu_k[n];
+    if (bad) set_status(p.status, STATUS_BAD_CU);
+}
+
 // Tile slots over packed rows with offsets cu (null: N sequences of T rows),
 // `tile` rows each: slot floor(cu[n] / tile) + n + j holds tile j of sequence
 // n, so floor(T / tile) + N slots hold every tile and some hold none.

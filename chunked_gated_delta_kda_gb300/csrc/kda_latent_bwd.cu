@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(256) latent_aux_kernel(const __grid_constant__
     __shared__ float part[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int h = blockIdx.y;
+    if (blockIdx.x == 0 && h == 0) check_offsets(p, threadIdx.x, 256);
     int n, j;
     LatentSeq s;
     if (FP16 && (int)blockIdx.x >= slots) {
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     latent_order(p, (int)blockIdx.x, slots, false, slot, h);
     const bool found = latent_find(p, p.cu_k, p.Tk, slot, LAT_TILE, n, j0, s);
     const int key0 = found ? j0 * LAT_TILE : 0;
+    if (p.Tq == 0 && blockIdx.x == 0) check_offsets(p, tid, BWD_THREADS);   // (elsewhere with the tables)
     if (!found || key0 >= s.lk) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;

@@ -53,7 +53,7 @@ bool latent_row_map(CUtensorMap* m, const void* base, int width, int heads, long
 namespace {
 
 constexpr int FWD_ROWS = 2 * LAT_TILE;
-constexpr int FWD_THREADS = 384;                        // warps 10 and 11 only hold registers for the softmax
+constexpr int FWD_THREADS = 384;                        // warps 10 and 11 hold registers for the softmax (and check offsets)
 constexpr uint32_t SLAB = 64 * LAT_TILE * 2;            // 16 KiB
 constexpr uint32_t RING = 8;
 constexpr uint32_t F_Q = 0;                             // [tile][3 slabs]
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(SHARE_SLOTS) latent_share_kernel(const __grid_
     for (int i = t; i < items + pairs; i += SHARE_SLOTS) p.share_items[i] = make_int4(-1, -1, 0, 0);
     for (int i = t; i <= p.N; i += SHARE_SLOTS) cu[i] = p.cu_q[i];
     __syncthreads();
+    check_offsets(p, t, SHARE_SLOTS);
     int n, j, steps = -1;              // -1: no such pair
     LatentSeq s;
     if (t < slots) {
@@ -247,7 +248,11 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     }
     const bool found = latent_find(p, p.cu_q, p.Tq, slot, FWD_ROWS, n, j0, s);
     const int row0 = found ? j0 * FWD_ROWS : 0;
-    if (!found || row0 >= s.lq) return;   // all CTAs of a cluster alike
+    const bool checks = SPLIT != SHARED && blockIdx.x == 0;
+    if (!found || row0 >= s.lq) {         // all CTAs of a cluster alike
+        if (checks) check_offsets(p, tid, FWD_THREADS);
+        return;
+    }
     const int shift = s.lk - s.lq;
     int nt[2];   // key tiles that each query tile needs
     pair_tiles(p, s, row0, nt);
@@ -396,6 +401,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             // every product issued here is done before the tensor memory is freed
             mma_commit_warp(base + F_DRAIN);
             mbar_wait(base + F_DRAIN, 0, DRAIN_LIMIT);
+        } else if (warp >= 10 && checks) {
+            check_offsets(p, tid - 320, FWD_THREADS - 320);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");

@@ -739,3 +739,31 @@ def test_decode_missing_pages_meet_what_the_tiles_before_left(page, S, H, dtype)
     ro, rl, eo, el = ol.latent_decode(q, cache, table, n, u=U[dtype], tiny=TINY[dtype])
     near(o, ro, eo, "o")
     near(lse, rl, el, "lse")
+
+
+@pytest.mark.parametrize("H,more", [(2, 0), (60, 0), (2, 40), (1, 2 ** 17), (2, 9000)])
+def test_offsets_that_step_back_are_reported(H, more):
+    """Also where no tile of the sequence that steps back is looked up.  Few sequences and 40 more, few heads and many;
+    2^17 more keys: clusters; 9000: CTAs that share keys."""
+    from chunked_gated_delta_kda_gb300 import binding
+    step, extra = [0, 600, 300, 900], [1] * {40: 40, 9000: 8}.get(more, 1)
+    at_q = torch.tensor(step + [900 + i + 1 for i in range(len(extra))], dtype=torch.int32, device="cuda")
+    tq, many = 900 + len(extra), more if more > 40 else 0
+    at_k = at_q.clone()
+    at_k[-1] += many
+    z = lambda *s: torch.zeros(s, dtype=BF, device="cuda")  # noqa: E731
+    args = z(1, tq, H, 192), z(1, tq + many, H, 256), z(1, tq + many, 64)
+    good_q, good_k = at_q.clone(), at_k.clone()
+    good_q[1:3] = good_k[1:3] = 450
+    ws = torch.zeros(max(256, api().latent_fwd_workspace_bytes(1, tq, tq + many, H, len(at_q) - 1)), dtype=torch.uint8, device="cuda")
+    assert (ws.numel() > 256) == (more == 9000)
+    wb = torch.zeros(api().latent_bwd_workspace_bytes(1, tq, tq + many, H, len(at_q) - 1), dtype=torch.uint8, device="cuda")
+    for a, b, status in ((good_q, good_k, 0), (at_q, at_k, 4), (at_q, good_k, 4), (good_q, at_k, 4)):
+        o, lse = api().latent_fwd(*args, cu_seqlens_q=a, cu_seqlens_k=b, workspace=ws)
+        assert binding.get_status(ws) == status
+        api().latent_bwd(*args, o, lse, o, cu_seqlens_q=a, cu_seqlens_k=b, workspace=wb)
+        assert binding.get_status(wb) == status
+    none = torch.zeros_like(at_q)
+    o = z(1, 0, H, 128)
+    api().latent_bwd(z(1, 0, H, 192), *args[1:], o, o[..., 0].float(), o, cu_seqlens_q=none, cu_seqlens_k=at_k, workspace=wb)
+    assert binding.get_status(wb) == 4
