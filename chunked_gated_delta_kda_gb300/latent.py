@@ -389,9 +389,11 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
         fine = (seq_lens.dtype is new_lens.dtype is block_table.dtype is free_pages.dtype is free_head.dtype is torch.int32
                 and seq_lens.dim() == free_pages.dim() == 1 and block_table.dim() == 2 and free_head.shape == (1,)
                 and new_lens.shape == seq_lens.shape == block_table.shape[:1]
-                and 0 < page_size <= INT_MAX and num_tokens <= INT_MAX and page_size % 1 == num_tokens % 1 == 0
-                and seq_lens.numel() <= INT_MAX and block_table.size(1) <= INT_MAX and free_pages.numel() <= INT_MAX
                 and _together(seq_lens.get_device(), new_lens, block_table, free_pages, free_head))
+        if fine:
+            (N, width), (pages,) = block_table.shape, free_pages.shape
+            fine = (0 < page_size <= INT_MAX and page_size % 1 == num_tokens % 1 == 0
+                    and num_tokens <= INT_MAX and N <= INT_MAX and width <= INT_MAX and pages <= INT_MAX)
     except AttributeError:   # not a tensor
         fine = False
     if not fine:
@@ -406,11 +408,11 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
         _check("free_pages", free_pages, torch.int32, (None,))
         _check("free_head", free_head, torch.int32, (1,))
         _same_device(seq_lens.get_device(), new_lens, block_table, free_pages, free_head)
+        (N, width), (pages,) = block_table.shape, free_pages.shape
     index = seq_lens.get_device()
     if index != _current_device():
         return _elsewhere(index, block_tables, seq_lens, new_lens, block_table, free_pages, free_head, page_size, num_tokens,
                           workspace)
-    N = seq_lens.shape[0]
     dev = seq_lens.device
     if not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous")
@@ -420,7 +422,7 @@ def block_tables(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
     cu = torch.empty((N + 1,), dtype=torch.int32, device=dev)
     lens_out, head_out = torch.empty_like(seq_lens), torch.empty_like(free_head)
     _raise(load_library().kda_block_tables(
-        seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(),
-        free_pages.shape[0], free_head.data_ptr(), int(page_size), slots.data_ptr(), int(num_tokens), cu.data_ptr(),
-        lens_out.data_ptr(), head_out.data_ptr(), N, _status_workspace(workspace, index), _stream(index)), "kda_block_tables")
+        seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), width, free_pages.data_ptr(), pages,
+        free_head.data_ptr(), int(page_size), slots.data_ptr(), int(num_tokens), cu.data_ptr(), lens_out.data_ptr(),
+        head_out.data_ptr(), N, _status_workspace(workspace, index), _stream(index)), "kda_block_tables")
     return slots, cu, lens_out, head_out
