@@ -767,3 +767,21 @@ def test_offsets_that_step_back_are_reported(H, more):
     o = z(1, 0, H, 128)
     api().latent_bwd(z(1, 0, H, 192), *args[1:], o, o[..., 0].float(), o, cu_seqlens_q=none, cu_seqlens_k=at_k, workspace=wb)
     assert binding.get_status(wb) == 4
+
+
+def test_expanded_form_past_32_bit_offsets():
+    """Packed tensors of more than 2^31 elements: the last sequences get the bits that they get alone."""
+    lens, H = [200] * 660 + [129, 1, 270], 128
+    T, last = sum(lens), 400
+    assert T * H * 128 > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(26)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF)  # noqa: E731
+    q, kv, pe, do = r(1, T, H, 192), r(1, T, H, 256), r(1, T, 64), r(1, T, H, 128)
+    c, alone = cu(lens), cu(lens[-3:])
+    o, lse = api().latent_fwd(q, kv, pe, cu_seqlens_q=c, cu_seqlens_k=c)
+    grads = api().latent_bwd(q, kv, pe, o, lse, do, cu_seqlens_q=c, cu_seqlens_k=c)
+    tail = [t[:, T - last:].contiguous() for t in (q, kv, pe, do)]
+    o2, lse2 = api().latent_fwd(*tail[:3], cu_seqlens_q=alone, cu_seqlens_k=alone)
+    assert torch.equal(o[:, T - last:], o2) and torch.equal(lse[:, T - last:], lse2)
+    for x, y in zip(grads, api().latent_bwd(*tail[:3], o2, lse2, tail[3], cu_seqlens_q=alone, cu_seqlens_k=alone)):
+        assert torch.equal(x[:, T - last:], y)
