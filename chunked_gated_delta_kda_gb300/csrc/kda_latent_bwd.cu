@@ -481,8 +481,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     latent_order(p, (int)blockIdx.x, slots, false, slot, h);
     const bool found = latent_find(p, p.cu_k, p.Tk, slot, LAT_TILE, n, j0, s);
     const int key0 = found ? j0 * LAT_TILE : 0;
-    if (p.Tq == 0 && blockIdx.x == 0) check_offsets(p, tid, BWD_THREADS);   // (elsewhere with the tables)
+    const bool checks = p.Tq == 0 && blockIdx.x == 0;                   // (elsewhere the launch of the tables does)
     if (!found || key0 >= s.lk) {
+        if (checks) check_offsets(p, tid, BWD_THREADS);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
@@ -734,6 +735,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");   // what follows this launch also follows the dq kernel
     if (warp == 8) tmem_dealloc(tmem, 512);
+    if (checks) check_offsets(p, tid, BWD_THREADS);
     if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
 }
 
