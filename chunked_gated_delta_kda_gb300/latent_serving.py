@@ -69,7 +69,10 @@ class LatentLayer:
         return torch.einsum("...c,hdc->...hd", rows[..., :LATENT_CHANNELS], self.w_up)
 
     def prefill(self, x, new_lens):
-        """Packed prompts x [T, D], new_lens int32 [N]; the requests' cache is empty.  Returns [T, H, 128]."""
+        """Packed prompts x [T, D], new_lens int32 [N], of requests that have nothing cached (0 tokens go to the
+        others).  Returns [T, H, 128]."""
+        if bool(((self.lens > 0) & (new_lens > 0)).any()):
+            raise ValueError("prefill sees the new tokens alone: a request with cached ones goes on with decode")
         slots, cu = self._advance(x @ self.w_row.T, new_lens)
         rows = self.cache.view(-1, ROW_CHANNELS)[slots]                 # as the cache holds them
         o, _ = latent.latent_fwd(self._query(x)[None], self._expand(rows)[None], rows[None, :, LATENT_CHANNELS:],

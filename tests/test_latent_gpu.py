@@ -785,3 +785,19 @@ def test_expanded_form_past_32_bit_offsets():
     assert torch.equal(o[:, T - last:], o2) and torch.equal(lse[:, T - last:], lse2)
     for x, y in zip(grads, api().latent_bwd(*tail[:3], o2, lse2, tail[3], cu_seqlens_q=alone, cu_seqlens_k=alone)):
         assert torch.equal(x[:, T - last:], y)
+
+
+def test_serving_layer_prefills_new_requests_only():
+    """A second prompt of a request would not see the first; other requests may be prefilled beside cached ones."""
+    from chunked_gated_delta_kda_gb300.latent_serving import LatentLayer
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(90, 128, generator=g, device="cuda").to(BF)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    layer, fresh = (LatentLayer(128, 2, 2, pages=8, width=2) for _ in range(2))
+    layer.prefill(x[:50], i32(50, 0))
+    with pytest.raises(ValueError, match="cached"):
+        layer.prefill(x[50:], i32(40, 0))
+    assert layer.lens.tolist() == [50, 0]
+    a, b = layer.prefill(x[50:], i32(0, 40)).float(), fresh.prefill(x, i32(50, 40))[50:].float()
+    # the projections of 40 and of 90 rows may sum in another order: a rounding of rows, keys, values and output each
+    assert (a - b).norm() <= 4 * 2.0 ** -8 * b.norm()
