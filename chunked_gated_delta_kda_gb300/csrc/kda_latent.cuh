@@ -142,11 +142,11 @@ __device__ __forceinline__ bool latent_find(const LatentParams& p, const int32_t
 // a sequence's largest tiles come first (its last ones where `last`), all heads
 // of a tile next to each other.  Heads after one another, which keeps fewer
 // keys in use at a time, was slower wherever the last head's large tiles came
-// late (forward / backward, us: T=8192 H=8 170 / 492 -> 117 / 422, packed T=9192
-// H=32 258 / 939 -> 228 / 888, B=4 T=8192 H=16 880 / 3408 -> 828 / 3391; 32
-// packed sequences of 2048, H=16, 622 / 2372 -> 600 / 2419); the tiles of all
-// sequences of equal length by size was slower as well (B=8 T=2048 H=16 171 /
-// 650 beside 150 / 588).
+// late (forward / backward, us, a few calls at a time: T=8192 H=8 170 / 492 ->
+// 117 / 422, packed T=9192 H=32 258 / 939 -> 228 / 888, B=4 T=8192 H=16 880 /
+// 3408 -> 828 / 3391; 32 packed sequences of 2048, H=16, 622 / 2372 -> 600 /
+// 2419); the tiles of all sequences of equal length by size was slower as well
+// (B=8 T=2048 H=16 171 / 650 beside 150 / 588).
 __device__ __forceinline__ void latent_order(const LatentParams& p, int index, int slots, bool last, int& slot, int& h) {
     const int at = index / p.H;
     h = index - at * p.H;

@@ -15,9 +15,14 @@
 // 16 bits as first operands.  dS is kept without the factor `scale`, which
 // the final dq and dk get in 32 bits.
 //
-// Packed T=9192 H=32 (six lengths, causal), alone: aux 29 us, dq 360, dkv 464, dpe 15;
-// 879 us in all, 814 TFLOP/s of the 832 multiply-adds a pair, 1127 of those
-// done.  B=4 T=8192 H=16 3.38 ms: 1460 done.  What is left is the first loads
+// Both roundings make operands of the tensor cores (32-bit ones run at half the
+// rate and twice the columns): bf16 gradients are off by 0.0024 of their norm,
+// 0.0018 of that their own rounding and o's; what is summed is in 32 bits.
+//
+// Packed T=9192 H=32 (six lengths, causal), alone: aux 29 us, dq 360, dkv 466, dpe 15
+// (fp16 46, 366, 475, 15); in all 860 us in a graph, 832 TFLOP/s of the 832
+// multiply-adds a pair, 1152 of those done.  B=4 T=8192 H=16 3.26 ms in a few
+// calls after a pause, 1520 done, and 3.49, 1420, at the power limit.  What is left is the first loads
 // and last stores of CTAs with some twelve steps each, and in dq the waits for
 // K.  Not better: dq with its own dout . o beside aux (944 us).
 #include "kda_latent_mma.cuh"

@@ -1,8 +1,9 @@
 // Absorbed latent attention over the paged cache (kda_latent_decode).
 //
-// The cached rows serve all rows (token, head) of a sequence, as keys with
-// their 576 channels and as values with the first 512, so each is read once
-// and used from shared memory by both products:
+// The cached rows serve up to 64 rows (token, head) of a sequence, as keys with
+// their 576 channels and as values with the first 512, so each is read once for
+// them and used from shared memory by both products; S H rows of a sequence
+// walk its cache ceil(S H / 64) times:
 //   S = Q R^T            [rows, 64 keys]       M = 64, K = 576
 //   O^T += R_v^T P^T     [512 channels, rows]  four M = 128 blocks, K = 64 keys
 // O is kept transposed: its channels fill the lanes of tensor memory whatever
@@ -20,9 +21,16 @@
 // which also writes the empty sequences.
 // One token of 256 sequences of 4096, H=32: 208 us, 5.8 TB/s (a tile every 3270
 // cycles, 6.5 TB/s, and some 15 us of plan, first loads, parts and join); of
-// lengths 1 to 8192 223 us, 5.5 TB/s; of one sequence of 65536, 23 us.  64 rows
-// (a unit's queries then leave room for two tiles) 64 x 8192 rows of cache 125
-// us, 4.8 TB/s; there, four tiles of 32 keys were slower (145).
+// lengths 1 to 8192 222 us, 5.5 TB/s; of one sequence of 65536, 29 us (23 where
+// the same 75 MB are read each time and partly stay in the L2).  64 rows (a
+// unit's queries then leave room for two tiles) 64 x 8192 rows of cache 123 us,
+// 4.9 TB/s; there, four tiles of 32 keys were slower (145).  128 rows of the
+// same 224 us, 2.7 TB/s of the cache and 5.4 of its two walks; 16 sequences of
+// 8192 with 7 tokens of 128 heads, 14 walks, 321 us, 6.6 TB/s of all of them.
+// P is rounded to the cache's type as an operand of the second product (32-bit
+// operands run at half the rate and take twice the room): bf16 o is off by
+// 0.0021 of its norm, 0.0017 of that its own rounding; the sums, the maximum and
+// the parts are in 32 bits.
 //   warps 0-3  softmax (row 16 w + l in lanes l and 16 + l of warp w, half of
 //              the keys each: an M = 64 product has its rows in 16 lanes of
 //              each quarter of tensor memory), rescaling and output of O

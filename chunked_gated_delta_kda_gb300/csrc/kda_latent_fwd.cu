@@ -20,9 +20,14 @@
 // tensor pipe keeps that order, so S may overwrite P, and a full S means that
 // the P V before it is done.
 //
-// B=4 T=8192 H=16 causal: 0.83 ms, 1660 TFLOP/s of the mask's pairs (0.97 of
-// a library product's sustained 1719, which the GPU's power sets); T=8192 H=8
-// 0.115 ms, 1490.  A step of both tiles is 2560 cycles of products and takes
+// P is rounded to the tensors' type as an operand of the second product (32-bit
+// operands run at half the rate and twice the columns): bf16 o is off by 0.0020
+// of its norm, 0.0015 of that its own rounding (B=4 T=8192).
+//
+// B=4 T=8192 H=16 causal: 0.82 ms in a few calls after a pause, 1670 TFLOP/s of
+// the mask's pairs, and 0.90, 1530, once calls back to back have brought the GPU
+// to its power limit (a library product then runs at 1710); T=8192 H=8 0.116 ms
+// in either state, 1480.  A step of both tiles is 2560 cycles of products and takes
 // 3460: a tile's softmax (1500 cycles from its scores to its weights) and its
 // two products follow each other, and the other tile fills the gap but for
 // that.  Short sequences are bound by a CTA's first loads and last stores,

@@ -469,7 +469,8 @@ size_t kda_latent_bwd_workspace_bytes(int B, int Tq, int Tk, int H, int N);
  * products.  In fp16 both carry powers of two, dx that of a bound on the
  * sequence's and head's dout . v, so that neither small dout nor large values
  * of either leave fp16's range on the way; the gradients themselves have it.
- * (dk_pe holds the bounds' parts until its own values are written.)
+ * (dk_pe holds the bounds' parts until its own values are written; no gradient
+ * may overlap an input.)
  */
 kda_status kda_latent_bwd(const void* q, const void* kv, const void* k_pe, long long k_pe_stride, const void* o,
                           const float* lse, const void* dout, float scale, const int32_t* cu_seqlens_q,
