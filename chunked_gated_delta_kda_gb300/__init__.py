@@ -5,17 +5,19 @@ The compute path is the C-ABI library ``libkda.so`` built from ``csrc/``
 marshals torch tensors into that C call; importing it loads the library and
 fails loudly when it is missing.  ``inputs`` (synthetic workloads) is
 importable without the library.  ``latent`` has the latent attention, its
-paged cache and its tables, for the full-attention layers beside KDA layers.
+paged cache and its tables, for the full-attention layers beside KDA layers,
+``pages`` what shares, frees and moves the cache's pages, ``drafts`` the
+verification of drafted tokens.
 """
 
-__all__ = ["fwd", "kda_fwd", "load_library", "latent"]
+__all__ = ["fwd", "kda_fwd", "load_library", "latent", "pages", "drafts"]
 
 
 def __getattr__(name):
     if name in ("fwd", "kda_fwd", "load_library", "workspace_bytes", "KdaError"):
         from . import binding
         return getattr(binding, name)
-    if name == "latent":
+    if name in ("latent", "pages", "drafts"):
         import importlib
-        return importlib.import_module(".latent", __name__)
+        return importlib.import_module("." + name, __name__)
     raise AttributeError(name)

@@ -31,6 +31,7 @@ KDA_FLAG_BWD_UMMA = 32
 KDA_FLAG_FWD_TOKEN_EXACT = 64
 KDA_FLAG_FP16 = 128
 KDA_FLAG_CAUSAL = 256
+KDA_FLAG_FP32 = 512
 
 KDA_DEBUG_WAIT_LIMIT = 1
 KDA_DEBUG_DROP_SCAN_LOAD = 2
@@ -40,6 +41,7 @@ _STATUS = {
     4: "invalid cu_seqlens", 5: "device wait timed out", 6: "too large for the no-alloc scratch",
     7: "state slot index or accepted-token count out of range",
     8: "page, slot or length out of range, or too few free pages",
+    9: "drafted token past the vocabulary, or nothing to draw from",
 }
 
 RECURRENT_WORKSPACE_BYTES = 256
@@ -105,6 +107,21 @@ def load_library(path: Optional[str] = None):
     lib.kda_latent_append.argtypes = [vp, ll, vp, vp, f, vp, ll, i, u, vp, vp]
     lib.kda_block_tables.restype = ctypes.c_int
     lib.kda_block_tables.argtypes = [vp, vp, vp, i, vp, i, vp, i, vp, i, vp, vp, vp, i, vp, vp]
+    lib.kda_latent_chunk_workspace_bytes.restype = sz
+    lib.kda_latent_chunk_workspace_bytes.argtypes = [i, i, i, i]
+    lib.kda_latent_chunk.restype = ctypes.c_int
+    lib.kda_latent_chunk.argtypes = [vp, vp, i, i, vp, i, vp, vp, f, vp, i, vp, vp, i, i, i, u, vp, sz, vp]
+    for name in ("kda_page_fork", "kda_page_free", "kda_page_compact"):
+        getattr(lib, name + "_workspace_bytes").restype = sz
+        getattr(lib, name + "_workspace_bytes").argtypes = [i]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.kda_page_fork.argtypes = [vp, i, vp, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, i, i, vp, sz, vp]
+    lib.kda_page_copy.restype = ctypes.c_int
+    lib.kda_page_copy.argtypes = [vp, i, i, ll, vp, vp, i, vp, vp]
+    lib.kda_page_free.argtypes = [vp, i, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, i, vp, sz, vp]
+    lib.kda_page_compact.argtypes = [vp, i, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, vp, vp, i, vp, sz, vp]
+    lib.kda_verify_drafts.restype = ctypes.c_int
+    lib.kda_verify_drafts.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, u, vp, vp]
     lib.kda_debug_set.restype = ctypes.c_int
     lib.kda_debug_set.argtypes = [i, u]
     lib.kda_status_str.restype = ctypes.c_char_p

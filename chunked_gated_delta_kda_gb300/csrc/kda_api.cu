@@ -161,6 +161,7 @@ kda_status kda_get_status(const void* workspace, cudaStream_t stream) {
     if (word & kda::STATUS_TIMEOUT) return KDA_ERR_TIMEOUT;
     if (word & kda::STATUS_BAD_INDEX) return KDA_ERR_BAD_STATE_INDEX;
     if (word & kda::STATUS_BAD_PAGE) return KDA_ERR_BAD_PAGE;
+    if (word & kda::STATUS_BAD_TOKEN) return KDA_ERR_BAD_TOKEN;
     return KDA_OK;
 }
 
@@ -186,6 +187,7 @@ const char* kda_status_str(kda_status status) {
         case KDA_ERR_TOO_LARGE: return "problem too large for the static no-alloc scratch";
         case KDA_ERR_BAD_STATE_INDEX: return "device found a state slot index or accepted-token count out of range";
         case KDA_ERR_BAD_PAGE: return "device found a page, slot or length out of range, or too few free pages";
+        case KDA_ERR_BAD_TOKEN: return "device found a drafted token past the vocabulary, or nothing to draw from";
     }
     return "unknown status";
 }

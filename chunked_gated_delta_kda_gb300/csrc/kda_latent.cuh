@@ -45,6 +45,7 @@ struct LatentParams {
     int Tq, Tk;             // per sequence (fixed) or packed (varlen)
     int H, N;
     int causal;
+    int chunk;              // of kda_latent_chunk: offsets may end before the rows, the status word is clear already
     uint32_t wait_limit;
 };
 
@@ -69,8 +70,9 @@ __device__ __forceinline__ bool latent_seq(const LatentParams& p, int n, LatentS
         return true;
     }
     const int a = p.cu_q[n], b = p.cu_q[n + 1], c = p.cu_k[n], d = p.cu_k[n + 1];
-    if (a < 0 || b < a || b > p.Tq || (n == 0 && a != 0) || (n == p.N - 1 && b != p.Tq) || c < 0 || d < c ||
-        d > p.Tk || (n == 0 && c != 0) || (n == p.N - 1 && d != p.Tk)) {
+    const bool whole = n == p.N - 1 && !p.chunk;   // the last sequence ends with the rows
+    if (a < 0 || b < a || b > p.Tq || (n == 0 && a != 0) || (whole && b != p.Tq) || c < 0 || d < c ||
+        d > p.Tk || (n == 0 && c != 0) || (whole && d != p.Tk)) {
         set_status(p.status, STATUS_BAD_CU);
         return false;
     }

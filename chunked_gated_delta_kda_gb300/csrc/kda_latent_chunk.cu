@@ -1,0 +1,415 @@
+// Attention of a chunk of new tokens over the paged latent cache
+// (kda_latent_chunk), with its C entry point.  See include/kda.h for the
+// contract.
+//
+// Keys and values are expanded from the cached rows, for all heads, into the
+// workspace, and the expanded forward runs on them.  A pair of a query and a
+// key then costs 640 operations a head beside 2176 in the absorbed form, and
+// the expansion 262144 for each key and head, so it is cheaper from some 170
+// new tokens a sequence on (where fewer are usual, kda_latent_decode serves).
+//
+// The expansion is a matrix product whose first operand is gathered page by
+// page:  [k_jh | v_jh] = W_h c_j,  128 rows j a tile, 256 columns a head, 512
+// channels.  All (tile, head) items form one line, heads inside a tile, cut
+// into equal ranges, one a CTA; a tile's rows stay in shared memory for all
+// heads of it that the CTA has.
+//   warps 0-3  the product's rows out of tensor memory, rounded, to the
+//              workspace (two accumulators of 256 columns take turns)
+//   warp 4     issues the products
+//   warp 5     loads: a tile's rows (eight slabs of 64 channels), and W_h in
+//              slabs of 64 channels through a ring
+#include <cmath>
+#include <cstdint>
+
+#include "kda.h"
+#include "kda_latent_mma.cuh"
+
+namespace kda {
+
+uint32_t debug_wait_limit();
+cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t stream);
+unsigned long long latent_share_bytes(int B, int Tq, int Tk, int H, int N);
+
+namespace {
+
+struct ChunkParams {
+    const void* cache;          // [num_pages * page_size, 576]
+    const int32_t* table;       // [N, width]
+    const int32_t* lens;        // [N]
+    const int32_t* cu_q;        // [N + 1]
+    int32_t* cu_k;              // [N + 1] expanded rows before each sequence
+    int32_t* tiles;             // [N + 1] tiles before each sequence
+    void* kv;                   // [num_keys, H, 256]
+    void* pe;                   // [num_keys, 64]
+    uint32_t* status;
+    int num_pages, page_size, width, num_keys, T, H, N;
+    uint32_t wait_limit;
+};
+
+struct ChunkMaps {
+    CUtensorMap cache, w;
+};
+
+// ---- where each sequence's expanded rows and tiles start: one CTA ----
+constexpr int PLAN_THREADS = 1024;
+
+__global__ void __launch_bounds__(PLAN_THREADS) latent_chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
+    __shared__ long long sums[2][PLAN_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long most = (long long)p.width * p.page_size;
+    long long rows0 = 0, tiles0 = 0;
+    bool bad = false, bad_cu = false;
+    if (tid < WS_CLEAR / 4) p.status[tid] = 0u;
+    for (int base = 0; base < p.N; base += PLAN_THREADS) {
+        const int n = base + tid;
+        long long rows = 0;
+        if (n < p.N) {
+            const int a = p.cu_q[n], b = p.cu_q[n + 1], len = p.lens[n];
+            bad_cu |= a < 0 || b < a || b > p.T || (n == 0 && a != 0);
+            if (b > a) {
+                bad |= len < 0 || len > most;
+                rows = max(0ll, min((long long)len, most));
+            }
+        }
+        long long x = rows;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sums[0][warp] = x;
+        __syncthreads();
+        long long all = 0, before = rows0 + x - rows;
+        for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+            if (w < warp) before += sums[0][w];
+            all += sums[0][w];
+        }
+        const long long first = min(before, (long long)p.num_keys), last = min(before + rows, (long long)p.num_keys);
+        bad |= last - first < rows;
+        const long long own = (last - first + LAT_TILE - 1) / LAT_TILE;
+        x = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) sums[1][warp] = x;
+        __syncthreads();
+        long long tiles = 0, ahead = tiles0 + x - own;
+        for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+            if (w < warp) ahead += sums[1][w];
+            tiles += sums[1][w];
+        }
+        if (n < p.N) {
+            p.cu_k[n] = (int)first;
+            p.tiles[n] = (int)ahead;
+        }
+        rows0 += all;
+        tiles0 += tiles;
+    }
+    if (tid == 0) {
+        p.cu_k[p.N] = (int)min(rows0, (long long)p.num_keys);
+        p.tiles[p.N] = (int)tiles0;
+    }
+    __syncthreads();                             // the status word is clear
+    if (bad) set_status(p.status, STATUS_BAD_PAGE);
+    if (bad_cu) set_status(p.status, STATUS_BAD_CU);
+}
+
+// ---- the expansion ----
+constexpr int EX_THREADS = 192;
+constexpr uint32_t A_SLAB = LAT_TILE * 128;              // 128 rows x 64 channels
+constexpr uint32_t B_SLAB = LAT_KV * 128;                // 256 columns x 64 channels
+constexpr uint32_t SLABS = LAT_C / 64;
+constexpr uint32_t EX_RING = 3;
+constexpr uint32_t X_A = 0;
+constexpr uint32_t X_B = X_A + SLABS * A_SLAB;
+constexpr uint32_t X_AFULL = X_B + EX_RING * B_SLAB;     // [8]
+constexpr uint32_t X_AEMPTY = X_AFULL + 8 * SLABS;
+constexpr uint32_t X_BFULL = X_AEMPTY + 8;               // [3]
+constexpr uint32_t X_BEMPTY = X_BFULL + 8 * EX_RING;     // [3]
+constexpr uint32_t X_DFULL = X_BEMPTY + 8 * EX_RING;     // [2]
+constexpr uint32_t X_DEMPTY = X_DFULL + 16;              // [2]
+constexpr uint32_t X_DRAIN = X_DEMPTY + 16;
+constexpr uint32_t X_TMEM = X_DRAIN + 8;
+constexpr uint32_t X_FAILED = X_TMEM + 4;
+constexpr uint32_t X_BYTES = X_FAILED + 4;
+constexpr uint32_t X_SMEM = X_BYTES + 1024;
+static_assert(X_SMEM <= 232448, "shared memory of one CTA");
+
+// A tile of the line: sequence, first row of the tile in it, its rows there.
+struct ChunkTile {
+    int n, row0, rows, out0;
+    __device__ __forceinline__ void find(const ChunkParams& p, int tile) {
+        int lo = 0, hi = p.N - 1;                // the last sequence whose tiles start at or before this one
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.tiles[mid] <= tile) lo = mid;
+            else hi = mid - 1;
+        }
+        n = lo;
+        row0 = (tile - p.tiles[lo]) * LAT_TILE;
+        out0 = p.cu_k[lo] + row0;
+        rows = min(LAT_TILE, p.cu_k[lo + 1] - out0);
+    }
+};
+
+__device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+template <bool FP16>
+__global__ void __launch_bounds__(EX_THREADS, 1)
+    latent_expand_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkMaps maps) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    volatile uint32_t* failed = reinterpret_cast<volatile uint32_t*>(smem + X_FAILED);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
+    const long long total = (long long)p.tiles[p.N] * p.H;
+    const long long first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
+    if (first >= last) return;
+
+    if (tid == 32) {
+        prefetch_map(&maps.cache);
+        prefetch_map(&maps.w);
+    }
+    if (tid == 0) {
+        for (uint32_t i = 0; i < SLABS; ++i) mbar_init(base + X_AFULL + 8 * i, 1);
+        mbar_init(base + X_AEMPTY, 1);
+        for (uint32_t i = 0; i < EX_RING; ++i) {
+            mbar_init(base + X_BFULL + 8 * i, 1);
+            mbar_init(base + X_BEMPTY + 8 * i, 1);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(base + X_DFULL + 8 * i, 1);
+            mbar_init(base + X_DEMPTY + 8 * i, 4);
+        }
+        mbar_init(base + X_DRAIN, 1);
+        *failed = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(base + X_TMEM, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + X_TMEM);
+    const int tile0 = (int)(first / p.H), h0 = (int)(first - (long long)tile0 * p.H);
+
+    if (warp == 5) {
+        const int box = min(p.page_size, 64), boxes = LAT_TILE / box;
+        const int nowhere = p.num_pages * p.page_size;   // rows from here on read as zeros
+        uint32_t loads = 0, tiles = 0;
+        int tile = tile0, h = h0;
+        bool ok = true, bad = false;
+        for (long long i = first; i < last && ok; ++i) {
+            if (i == first || h == 0) {
+                ChunkTile t;
+                t.find(p, tile);
+                int row = nowhere;
+                if (lane < boxes && lane * box < t.rows) {
+                    const int key = t.row0 + lane * box, page = p.table[(long long)t.n * p.width + key / p.page_size];
+                    if (page >= 0 && page < p.num_pages) row = page * p.page_size + key % p.page_size;
+                    else bad = true;
+                }
+                if (tiles > 0 && !wait_warp(base + X_AEMPTY, (tiles - 1) & 1, limit, failed)) break;
+                if (lane < (int)SLABS) mbar_arrive_expect_tx(base + X_AFULL + 8 * lane, A_SLAB);
+                __syncwarp();
+                if (lane < boxes)
+                    for (uint32_t c = 0; c < SLABS; ++c)
+                        tma_load_3d(base + X_A + c * A_SLAB + lane * box * 128, &maps.cache, 64 * c, 0, row, base + X_AFULL + 8 * c);
+                __syncwarp();
+                ++tiles;
+            }
+            for (uint32_t c = 0; c < SLABS; ++c, ++loads) {
+                const uint32_t slot = loads % EX_RING;
+                if (loads >= EX_RING && !wait_warp(base + X_BEMPTY + 8 * slot, (loads / EX_RING - 1) & 1, limit, failed)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(base + X_BFULL + 8 * slot, B_SLAB);
+                    tma_load_3d(base + X_B + slot * B_SLAB, &maps.w, 64 * c, 0, h * LAT_KV, base + X_BFULL + 8 * slot);
+                }
+                __syncwarp();
+            }
+            if (++h == p.H) h = 0, ++tile;
+        }
+        // every copy issued here has landed before the CTA ends
+        for (uint32_t k = loads > EX_RING ? loads - EX_RING : 0; k < loads; ++k)
+            mbar_wait(base + X_BFULL + 8 * (k % EX_RING), (k / EX_RING) & 1, DRAIN_LIMIT);
+        if (tiles > 0)
+            for (uint32_t c = 0; c < SLABS; ++c) mbar_wait(base + X_AFULL + 8 * c, (tiles - 1) & 1, DRAIN_LIMIT);
+        if (bad) set_status(p.status, STATUS_BAD_PAGE);
+    } else if (warp == 4) {
+        const uint32_t id = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 256, false, false);
+        uint32_t loads = 0, tiles = 0, item = 0;
+        int h = h0;
+        bool ok = true;
+        for (long long i = first; i < last && ok; ++i, ++item) {
+            const bool fresh = i == first || h == 0;
+            const uint32_t buf = item & 1;
+            if (fresh) ++tiles;
+            if (item >= 2 && !wait_warp(base + X_DEMPTY + 8 * buf, (item / 2 - 1) & 1, limit, failed)) break;
+            tc_fence_after();
+            for (uint32_t c = 0; c < SLABS; ++c, ++loads) {
+                const uint32_t slot = loads % EX_RING;
+                if (fresh && !wait_warp(base + X_AFULL + 8 * c, (tiles - 1) & 1, limit, failed)) ok = false;
+                if (ok && !wait_warp(base + X_BFULL + 8 * slot, (loads / EX_RING) & 1, limit, failed)) ok = false;
+                if (!ok) break;
+                const Desc a = desc_k(base + X_A + c * A_SLAB), b = desc_k(base + X_B + slot * B_SLAB);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + 256 * buf, a + 2 * ks, b + 2 * ks, id, c + ks > 0);
+                mma_commit_warp(base + X_BEMPTY + 8 * slot);
+            }
+            if (!ok) break;
+            mma_commit_warp(base + X_DFULL + 8 * buf);
+            if (++h == p.H) {
+                h = 0;
+                mma_commit_warp(base + X_AEMPTY);
+            }
+        }
+        // every product issued here is done before the tensor memory is freed
+        mma_commit_warp(base + X_DRAIN);
+        mbar_wait(base + X_DRAIN, 0, DRAIN_LIMIT);
+    } else {
+        const uint32_t at = tmem + ((uint32_t)warp << 21);   // this warp's lanes
+        const int r = warp * 32 + lane;
+        ChunkTile t;
+        int tile = tile0, h = h0;
+        uint32_t item = 0;
+        for (long long i = first; i < last; ++i, ++item) {
+            if (i == first || h == 0) t.find(p, tile);
+            if (h == 0 && r < t.rows) {                      // the positional channels, once for all heads
+                const int key = t.row0 + r, page = p.table[(long long)t.n * p.width + key / p.page_size];
+                const bool there = page >= 0 && page < p.num_pages;
+                const uint4* from = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.cache) + ((long long)(there ? page : 0) * p.page_size + key % p.page_size) * LAT_ROW + LAT_C);
+                uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.pe) + (long long)(t.out0 + r) * LAT_P);
+#pragma unroll
+                for (int k = 0; k < LAT_P / 8; ++k) to[k] = there ? __ldg(from + k) : make_uint4(0, 0, 0, 0);
+            }
+            const uint32_t buf = item & 1;
+            if (!wait_warp(base + X_DFULL + 8 * buf, (item / 2) & 1, limit, failed)) break;
+            tc_fence_after();
+            uint8_t* out = static_cast<uint8_t*>(p.kv) + (((long long)t.out0 + r) * p.H + h) * (LAT_KV * 2);
+#pragma unroll
+            for (int b = 0; b < LAT_KV / 32; ++b) {
+                float x[32];
+                tmem_ld32(at + 256 * buf + 32 * b, x);
+                tmem_ld_wait();
+                if (b == LAT_KV / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(base + X_DEMPTY + 8 * buf);
+                }
+                if (r < t.rows) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = pack2<FP16>(x[e + 2 * k], x[e + 2 * k + 1]);
+                        store32(out + 64 * b + 2 * e, w);
+                    }
+                }
+            }
+            if (++h == p.H) h = 0, ++tile;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) tmem_dealloc(tmem, 512);
+    if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
+}
+
+unsigned long long up256(unsigned long long b) { return (b + 255ull) / 256ull * 256ull; }
+
+struct ChunkLayout {
+    unsigned long long cu, tiles, kv, pe, bytes;
+    ChunkLayout(int T, int num_keys, int H, int N) {
+        cu = WS_HEADER + up256(latent_share_bytes(1, T, num_keys, H, N));
+        tiles = cu + up256((N + 1ull) * 4ull);
+        kv = tiles + up256((N + 1ull) * 4ull);
+        pe = kv + (unsigned long long)num_keys * H * LAT_KV * 2ull;
+        bytes = pe + (unsigned long long)num_keys * LAT_P * 2ull;
+    }
+};
+
+// (the last line: as kda_latent_fwd, a CTA a tile slot and head, in one dimension of a grid)
+bool sizes_ok(int T, int num_keys, int H, int N) {
+    return T >= 0 && num_keys >= 0 && H >= 1 && N >= 1 && H <= 65535 && N <= 65535 &&
+           ((long long)(T > num_keys ? T : num_keys) / LAT_TILE + N) * H < (1ll << 31);
+}
+
+bool off(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+}  // namespace
+
+}  // namespace kda
+
+extern "C" {
+
+size_t kda_latent_chunk_workspace_bytes(int T, int num_keys, int H, int N) {
+    return kda::sizes_ok(T, num_keys, H, N) ? (size_t)kda::ChunkLayout(T, num_keys, H, N).bytes : 0;
+}
+
+kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int page_size,
+                            const int32_t* block_table, int table_width, const int32_t* seq_lens, const void* w_up,
+                            float scale, const int32_t* cu_seqlens_q, int num_keys, void* o, float* lse, int T, int H,
+                            int N, unsigned flags, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    using namespace kda;
+    if (!sizes_ok(T, num_keys, H, N) || (flags & ~KDA_FLAG_FP16) != 0u) return KDA_ERR_INVALID_ARG;
+    if (num_pages < 1 || table_width < 1) return KDA_ERR_INVALID_ARG;
+    if (page_size != 16 && page_size != 32 && (page_size < 64 || page_size % 64 != 0)) return KDA_ERR_INVALID_ARG;
+    if ((long long)num_pages * page_size >= (1ll << 31) || (long long)table_width * page_size >= (1ll << 31))
+        return KDA_ERR_INVALID_ARG;
+    if ((T > 0 && (!q || !o)) || !cache || !block_table || !seq_lens || !w_up || !cu_seqlens_q || !workspace)
+        return KDA_ERR_INVALID_ARG;
+    if (off(q, 16) || off(cache, 16) || off(block_table, 4) || off(seq_lens, 4) || off(w_up, 16) || off(cu_seqlens_q, 4) ||
+        off(o, 16) || off(lse, 4) || off(workspace, 256))
+        return KDA_ERR_INVALID_ARG;
+    const ChunkLayout at(T, num_keys, H, N);
+    if (workspace_bytes < at.bytes) return KDA_ERR_INVALID_ARG;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    ChunkParams c{};
+    c.cache = cache, c.table = block_table, c.lens = seq_lens, c.cu_q = cu_seqlens_q;
+    c.cu_k = reinterpret_cast<int32_t*>(ws + at.cu), c.tiles = reinterpret_cast<int32_t*>(ws + at.tiles);
+    c.kv = ws + at.kv, c.pe = ws + at.pe, c.status = reinterpret_cast<uint32_t*>(ws);
+    c.num_pages = num_pages, c.page_size = page_size, c.width = table_width, c.num_keys = num_keys;
+    c.T = T, c.H = H, c.N = N, c.wait_limit = debug_wait_limit();
+    LatentParams p{};
+    if (latent_share_bytes(1, T, num_keys, H, N) > 0) {
+        p.share_items = reinterpret_cast<int4*>(ws + WS_HEADER);
+        p.share_parts = reinterpret_cast<float*>(ws + WS_HEADER + LATENT_SHARE_ITEMS * 16ull);
+    }
+    p.q = q, p.kv = c.kv, p.k_pe = c.pe, p.k_pe_stride = LAT_P, p.o_out = o, p.lse_out = lse;
+    p.cu_q = cu_seqlens_q, p.cu_k = c.cu_k, p.status = c.status;
+    p.scale = scale > 0.f && !std::isnan(scale) ? scale : 1.0f / std::sqrt((float)LAT_QK);
+    p.Tq = T, p.Tk = num_keys, p.H = H, p.N = N, p.causal = 1, p.chunk = 1, p.wait_limit = debug_wait_limit();
+
+    latent_chunk_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(c);
+    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    if (T == 0) return KDA_OK;
+    const bool fp16 = (flags & KDA_FLAG_FP16) != 0u;
+    if (num_keys > 0) {
+        ChunkMaps maps;
+        if (!latent_row_map(&maps.cache, cache, LAT_ROW, 1, (long long)num_pages * page_size, LAT_ROW, page_size < 64 ? page_size : 64) ||
+            !latent_row_map(&maps.w, w_up, LAT_C, 1, (long long)H * LAT_KV, LAT_C, LAT_KV))
+            return KDA_ERR_CUDA;
+        const auto kernel = fp16 ? latent_expand_kernel<true> : latent_expand_kernel<false>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X_SMEM) != cudaSuccess) return KDA_ERR_CUDA;
+        const long long items = ((long long)num_keys / LAT_TILE + N) * H;
+        kernel<<<(unsigned)(items < 152 ? items : 152), EX_THREADS, X_SMEM, stream>>>(c, maps);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return launch_latent_fwd(p, fp16, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(SHARE_SLOTS) latent_share_kernel(const __grid_
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int items = share_items(slots, p.H), pairs = share_pairs(p.H);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (t < WS_CLEAR / 4) p.status[t] = 0u;
+    if (t < WS_CLEAR / 4 && !p.chunk) p.status[t] = 0u;
     for (int i = t; i < items + pairs; i += SHARE_SLOTS) p.share_items[i] = make_int4(-1, -1, 0, 0);
     for (int i = t; i <= p.N; i += SHARE_SLOTS) cu[i] = p.cu_q[i];
     __syncthreads();

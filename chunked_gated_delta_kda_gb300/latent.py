@@ -6,6 +6,7 @@ decoder that are interleaved with KDA layers:
 
 ``latent_fwd`` / ``latent_bwd``  expanded form (prefill and training),
 ``latent_decode``                absorbed form over the paged cache,
+``latent_chunk``                 expanded form of new tokens over the paged cache,
 ``latent_append``                new tokens' rows into their cache slots,
 ``block_tables``                 block tables and slot map of a step.
 
@@ -327,6 +328,73 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
         seq_lens.data_ptr(), _scale(scale), o.data_ptr(), lse.data_ptr(), N, S, H, flags,
         scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(index)), "kda_latent_decode")
+    _hand_back(scratch, workspace)
+    return o, lse
+
+
+def latent_chunk_workspace_bytes(T: int, num_keys: int, H: int, N: int) -> int:
+    return int(load_library().kda_latent_chunk_workspace_bytes(T, num_keys, H, N))
+
+
+def latent_chunk(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 w_up: torch.Tensor, cu_seqlens_q: torch.Tensor, num_keys: int, scale: Optional[float] = None,
+                 workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Latent attention of a chunk of new tokens a sequence over all its cached
+    rows, its own included, in the expanded form (chunked prefill; from some
+    170 new tokens a sequence on it costs less than ``latent_decode``).
+
+    q: bf16 or fp16 [T, H, 128 + 64], packed; cache: [pages, page_size, 576]
+    (page_size 16, 32, or a multiple of 64), the new tokens' rows appended
+    already; block_table: int32 [N, width]; seq_lens: int32 [N], the new tokens
+    included; w_up: [H, 128 + 128, 512], what expands a row's latent channels
+    to a head's key and value; cu_seqlens_q: int32 [N + 1] on the device (rows
+    of q behind its last entry are padding, their results are not written);
+    num_keys: at least the sum of seq_lens over the sequences with new tokens
+    (what the expanded keys and values are given room for).  Query i of a
+    sequence sees the rows up to i + seq_len - new tokens.  ``scale`` None
+    means 192**-0.5.  Returns (o [T, H, 128], lse fp32 [T, H]); a query that
+    sees no row gets 0 and -inf.  ``workspace`` as for ``latent_bwd``, with
+    ``latent_chunk_workspace_bytes`` bytes."""
+    flags = _float_flag("q", q)
+    dtype = q.dtype
+    try:
+        fine = (q.dim() == cache.dim() == w_up.dim() == 3 and block_table.dim() == 2 and cache.dtype is w_up.dtype is dtype
+                and block_table.dtype is seq_lens.dtype is cu_seqlens_q.dtype is torch.int32
+                and q.shape[2] == QUERY_CHANNELS and cache.shape[2] == ROW_CHANNELS
+                and w_up.shape == (q.shape[1], KEY_CHANNELS + VALUE_CHANNELS, LATENT_CHANNELS)
+                and seq_lens.shape == block_table.shape[:1] and cu_seqlens_q.shape == (seq_lens.shape[0] + 1,)
+                and block_table.size(1) <= INT_MAX and 0 <= num_keys <= INT_MAX and num_keys % 1 == 0
+                and _together(q.get_device(), cache, block_table, seq_lens, w_up, cu_seqlens_q))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
+        _check("q", q, dtype, (None, None, QUERY_CHANNELS))
+        _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
+        _check("w_up", w_up, dtype, (q.shape[1], KEY_CHANNELS + VALUE_CHANNELS, LATENT_CHANNELS))
+        _check("block_table", block_table, torch.int32, (None, None))
+        _check("seq_lens", seq_lens, torch.int32, (block_table.shape[0],))
+        _check("cu_seqlens_q", cu_seqlens_q, torch.int32, (block_table.shape[0] + 1,))
+        _check_int("block_table's width", block_table.shape[1])
+        _check_int("num_keys", num_keys)
+        if num_keys < 0:
+            raise ValueError(f"num_keys must not be negative, got {num_keys}")
+        _same_device(q.get_device(), cache, block_table, seq_lens, w_up, cu_seqlens_q)
+    index = q.get_device()
+    if index != _current_device():
+        return _elsewhere(index, latent_chunk, q, cache, block_table, seq_lens, w_up, cu_seqlens_q, num_keys, scale, workspace)
+    T, H, _ = q.shape
+    N, dev, num_keys = seq_lens.shape[0], q.device, int(num_keys)
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    q, w_up = _aligned(q.contiguous()), _aligned(w_up.contiguous())
+    block_table, seq_lens, cu_seqlens_q = block_table.contiguous(), seq_lens.contiguous(), cu_seqlens_q.contiguous()
+    scratch = _scratch(workspace, latent_chunk_workspace_bytes(T, num_keys, H, N), index, dev)
+    o = torch.empty((T, H, VALUE_CHANNELS), dtype=dtype, device=dev)
+    lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    _raise(load_library().kda_latent_chunk(
+        q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), w_up.data_ptr(), _scale(scale), cu_seqlens_q.data_ptr(), num_keys, o.data_ptr(), lse.data_ptr(),
+        T, H, N, flags, scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(index)), "kda_latent_chunk")
     _hand_back(scratch, workspace)
     return o, lse
 

@@ -50,9 +50,11 @@ typedef enum {
                                     the library's static scratch holds */
     KDA_ERR_BAD_STATE_INDEX = 7, /* kda_fused_recurrent: device found a state slot index or an
                                     accepted-token count out of range (via kda_get_status) */
-    KDA_ERR_BAD_PAGE = 8         /* kda_latent_decode, kda_latent_append, kda_block_tables: device found
-                                    a page, slot or length out of range, or too few free pages (via
-                                    kda_get_status) */
+    KDA_ERR_BAD_PAGE = 8,        /* kda_latent_decode, kda_latent_append, kda_block_tables, kda_latent_chunk,
+                                    kda_page_*: device found a page, slot, row or length out of range, or too
+                                    few free pages (via kda_get_status) */
+    KDA_ERR_BAD_TOKEN = 9        /* kda_verify_drafts: device found a drafted token past the vocabulary, or a
+                                    row of probabilities to draw from without weight (via kda_get_status) */
 } kda_status;
 
 /* Apply the per-token L2 normalisation x / sqrt(sum(x^2) + 1e-6) to q and k
@@ -168,7 +170,7 @@ kda_status kda_fwd_timed(const void* q, const void* k, const void* v, const floa
  * Synchronise `stream`, then read the device status word that the last
  * kda_fwd, kda_bwd, kda_fused_recurrent, kda_latent_* or kda_block_tables on
  * this workspace wrote.  Returns KDA_OK, KDA_ERR_BAD_CU_SEQLENS,
- * KDA_ERR_TIMEOUT, KDA_ERR_BAD_STATE_INDEX, KDA_ERR_BAD_PAGE (in that order of
+ * KDA_ERR_TIMEOUT, KDA_ERR_BAD_STATE_INDEX, KDA_ERR_BAD_PAGE, KDA_ERR_BAD_TOKEN (in that order of
  * precedence), or KDA_ERR_CUDA if synchronising or reading failed.
  */
 kda_status kda_get_status(const void* workspace, cudaStream_t stream);
@@ -554,6 +556,190 @@ kda_status kda_block_tables(const int32_t* seq_lens, const int32_t* new_lens, in
                             const int32_t* free_pages, int num_free, const int32_t* free_head, int page_size,
                             int64_t* slot_mapping, int num_tokens, int32_t* cu_seqlens, int32_t* seq_lens_out,
                             int32_t* free_head_out, int N, void* workspace, cudaStream_t stream);
+
+/* Bytes of device workspace kda_latent_chunk needs (0 on invalid sizes). */
+size_t kda_latent_chunk_workspace_bytes(int T, int num_keys, int H, int N);
+
+/*
+ * Attention of a chunk of new tokens a sequence over all its cached rows, its
+ * own included: causal kda_latent_fwd of the packed queries on keys and values
+ * that are expanded from the paged rows, [k_jh | v_jh] = W_h c_j.
+ *   q           [T, H, 192], packed
+ *   cache, num_pages, page_size, block_table, table_width
+ *               as for kda_latent_decode; the new tokens' rows are cached
+ *               already
+ *   seq_lens    int32 [N], device: cached rows of each sequence, its new
+ *               tokens included
+ *   w_up        [H, 256, 512]: for each head 128 rows that make the key and
+ *               128 that make the value from the 512 latent channels
+ *   cu_seqlens_q  int32 [N+1], device: where each sequence's new tokens
+ *               start; its last entry may be below T (the rows behind it, of
+ *               q as of o and lse, are not used)
+ *   num_keys    room for expanded rows: at least the sum of seq_lens over the
+ *               sequences that have new tokens
+ *   o           [T, H, 128];   lse  fp32 [T, H] or NULL
+ *   flags       KDA_FLAG_FP16
+ *   workspace   kda_latent_chunk_workspace_bytes(...) bytes, 256-byte
+ *               aligned, contents need not be initialised
+ * Query i of a sequence with Lq new tokens and Lk cached rows sees the rows
+ * j <= i + Lk - Lq; one that sees none gets o = 0 and lse = -infinity.  A
+ * sequence without new tokens costs nothing.  A negative length, or one past
+ * table_width pages, is clipped to that range, one that finds no room within
+ * num_keys to what is left of it; rows on a page outside [0, num_pages) count
+ * as zeros; each sets KDA_ERR_BAD_PAGE.  Rows past a sequence's length are
+ * not used, whatever they hold.
+ *
+ * Precision: expanded keys and values are summed in 32 bits and rounded to
+ * the tensors' type, as a prefill's are; the rest as for kda_latent_fwd.
+ */
+kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int page_size,
+                            const int32_t* block_table, int table_width, const int32_t* seq_lens, const void* w_up,
+                            float scale, const int32_t* cu_seqlens_q, int num_keys, void* o, float* lse, int T, int H,
+                            int N, unsigned flags, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages that several requests own.  refs int32 [num_pages] holds how many
+ * owners a page has beside its first: 0 for one owner, and for a free page,
+ * so that pages taken by kda_block_tables need no entry.  Free pages are the
+ * entries free_head .. num_free of the free list.  Tables, lengths and
+ * workspaces as above; a row of the table has ceil(seq_lens / page_size)
+ * pages.  refs, lengths and free_head are not written: the functions give
+ * them anew, and outputs may not overlap inputs.  page_size is any positive
+ * number here.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of device workspace kda_page_fork needs (0 on invalid sizes). */
+size_t kda_page_fork_workspace_bytes(int N);
+
+/*
+ * Rows children[i] of the table go on from the tokens of rows parents[i]: full
+ * pages are shared (refs + 1), a last page that is not full gets a free page
+ * of its own, in the order of i, and a pair (page, own page) to be copied by
+ * kda_page_copy.
+ *   parents, children  int32 [F], device; a negative child is a padding entry
+ *               and is skipped.  Children are distinct rows of length 0, a
+ *               parent may occur any number of times
+ *   block_table int32 [N, table_width]: the children's first cells are
+ *               written in place, others left alone
+ *   seq_lens_out  int32 [N];  refs_out int32 [num_pages];  free_head_out
+ *               int32 [1]
+ *   pairs       int32 [F, 2]: source and target page of entry i, or -1, -1
+ * A row outside [0, N), a child that has tokens, or one that an earlier entry
+ * has: the entry is skipped.  A page outside [0, num_pages) becomes -1 in the
+ * child's table, and so does an own page where the free list ends.  Each sets
+ * KDA_ERR_BAD_PAGE; lengths outside the table are clipped and set it too.
+ *   workspace   kda_page_fork_workspace_bytes(...) bytes
+ */
+kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* parents,
+                         const int32_t* children, const int32_t* refs, int num_pages, const int32_t* free_pages,
+                         int num_free, const int32_t* free_head, int page_size, int32_t* seq_lens_out,
+                         int32_t* refs_out, int32_t* free_head_out, int32_t* pairs, int N, int F, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Copy pages within each of num_pools pools (the caches of a model's layers,
+ * or pools of states): page pairs[i][1] becomes page pairs[i][0].
+ *   pools       host array of num_pools device pointers, 16-byte aligned, to
+ *               num_pages pages of page_bytes bytes (a multiple of 16)
+ *   pairs       int32 [F, 2], device; a pair with a negative entry is
+ *               skipped.  Targets are distinct, and no pair's source
+ *   count       int32 [1], device: only the first `count` pairs are looked
+ *               at; or NULL for all F
+ * A pair past num_pages is skipped and sets KDA_ERR_BAD_PAGE.
+ *   workspace   NULL, or the 256-byte status header
+ */
+kda_status kda_page_copy(void* const* pools, int num_pools, int num_pages, long long page_bytes, const int32_t* pairs,
+                         const int32_t* count, int F, void* workspace, cudaStream_t stream);
+
+/* Bytes of device workspace kda_page_free needs (0 on invalid sizes). */
+size_t kda_page_free_workspace_bytes(int num_pages);
+
+/*
+ * Row n of the table keeps its first keep_lens[n] tokens (0: it ends; fewer
+ * than it has: rejected drafts): each page behind them loses an owner, and
+ * those that had no other become free.  They come in front of the free list,
+ * in increasing order of their numbers.
+ *   keep_lens   int32 [N], device, at most seq_lens
+ *   free_pages  int32 [num_free]: the entries in front of free_head that the
+ *               pages take are written in place, others left alone
+ *   seq_lens_out  int32 [N]: keep_lens;  refs_out int32 [num_pages];
+ *   free_head_out int32 [1]: free_head less the pages that became free
+ * The table is only read: cells behind a row's length have no meaning.  A
+ * page outside [0, num_pages), one that loses more owners than it has, a
+ * length out of range (clipped), or a page that finds no room in front of
+ * free_head (not listed): KDA_ERR_BAD_PAGE.
+ *   workspace   kda_page_free_workspace_bytes(...) bytes
+ */
+kda_status kda_page_free(const int32_t* block_table, int table_width, const int32_t* seq_lens,
+                         const int32_t* keep_lens, const int32_t* refs, int num_pages, int32_t* free_pages,
+                         int num_free, const int32_t* free_head, int page_size, int32_t* seq_lens_out,
+                         int32_t* refs_out, int32_t* free_head_out, int N, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+
+/* Bytes of device workspace kda_page_compact needs (0 on invalid sizes). */
+size_t kda_page_compact_workspace_bytes(int num_pages);
+
+/*
+ * The U pages that are not in the free list onto the numbers 0 .. U - 1: the
+ * ones at U and above move, in increasing order, to the free pages below U.
+ *   block_table int32 [N, table_width], seq_lens int32 [N], refs, free_pages,
+ *               free_head  as above, not written
+ *   table_out   int32 [N, table_width]: the new numbers; -1 behind a row's pages
+ *   refs_out    int32 [num_pages]
+ *   free_out    int32 [num_free]: U, U + 1, ... from free_head on, the entries
+ *               in front of it as before; free_head stays
+ *   pairs       int32 [num_pages / 2, 2]: source and target of each page that
+ *               moves, for kda_page_copy; -1, -1 behind them
+ *   count       int32 [1]: how many move
+ *   moved       int32 [num_pages]: each page's new number, -1 for a free one
+ *               (for holders of pages besides the table)
+ * A page outside [0, num_pages) in a row's cells or in the free list, one that
+ * is listed twice, a row's page that is free, or a length out of range
+ * (clipped): KDA_ERR_BAD_PAGE.
+ *   workspace   kda_page_compact_workspace_bytes(...) bytes
+ */
+kda_status kda_page_compact(const int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* refs,
+                            int num_pages, const int32_t* free_pages, int num_free, const int32_t* free_head,
+                            int page_size, int32_t* table_out, int32_t* refs_out, int32_t* free_out, int32_t* pairs,
+                            int32_t* count, int32_t* moved, int N, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/* kda_verify_drafts: probabilities are fp32 instead of bf16 or fp16. */
+#define KDA_FLAG_FP32 512u
+
+/*
+ * Which of S drafted tokens a sequence are accepted, and the token behind
+ * them, so that the tokens are distributed as the target's.  With the target's
+ * probabilities p_s of the position that draft s stands at (p_S: the position
+ * behind the last one), the proposer's q_s and uniform numbers u: draft s with
+ * token d is accepted where u_s q_s(d) < p_s(d), as long as all before it are;
+ * a is their number.  The token behind them is the first i with
+ *   sum_{j <= i} r_j > u_S sum_j r_j,   r = max(p_a - q_a, 0),
+ * or r = p_a where a is the number of drafts, or where all of max(p_a - q_a, 0)
+ * is 0; and the last i with r_i > 0 where no i is above.
+ *   draft_tokens int64 [N, S]: a negative token ends a sequence's drafts
+ *   draft_probs [N, S, V], rows draft_strides[0] (n) and draft_strides[1] (s)
+ *               elements apart, or NULL: the proposer was sure of each draft
+ *               (q = 1 at its token and 0 elsewhere)
+ *   target_probs [N, S + 1, V], rows target_strides[0], [1] elements apart
+ *   uniform     fp32 [N, S + 1], in [0, 1)
+ *   tokens      int64 [N, S + 1]: the accepted drafts, the token behind them,
+ *               then -1
+ *   num_accepted int32 [N]: how many of `tokens` there are, a + 1 (what
+ *               kda_fused_recurrent takes as num_accepted_tokens)
+ *   flags       KDA_FLAG_FP32 or KDA_FLAG_FP16 (else bf16), of both
+ *               probabilities
+ *   workspace   NULL, or the 256-byte status header
+ * The comparisons are exact and the sums good to some 2^-46.  Probabilities
+ * need not sum to one; what is not above zero, NaN included, has no weight.  A
+ * token >= V ends the drafts as a negative one does, and r without weight, or
+ * with an infinite one, gives a token in [0, V) that means nothing; both set
+ * KDA_ERR_BAD_TOKEN.
+ */
+kda_status kda_verify_drafts(const int64_t* draft_tokens, const void* draft_probs, const long long* draft_strides,
+                             const void* target_probs, const long long* target_strides, const float* uniform,
+                             int64_t* tokens, int32_t* num_accepted, int N, int S, int V, unsigned flags,
+                             void* workspace, cudaStream_t stream);
 
 /* Static English description of a status code. */
 const char* kda_status_str(kda_status status);
