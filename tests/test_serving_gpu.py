@@ -648,7 +648,7 @@ def test_wrappers_name_what_they_refuse():
         pages().page_free(z(2, 3), z(2), z(3), z(4), z(4), z(1), 16)
     with pytest.raises(ValueError, match="parents"):
         pages().page_fork(z(2, 3), z(2), z(2), z(1), z(4), z(4), z(1), 16)
-    with pytest.raises(ValueError, match="same device"):
+    with pytest.raises(ValueError, match="free_pages"):
         pages().page_compact(z(2, 3), z(2), z(4), torch.zeros(4, dtype=torch.int32), z(1), 16)
     with pytest.raises(TypeError, match="target_probs"):
         verify(z(1, 1, d=torch.int64), z(1, 2, 4, d=torch.float64), z(1, 2, d=F32))
