@@ -46,6 +46,10 @@ struct LatentParams {
     int H, N;
     int causal;
     int chunk;              // of kda_latent_chunk: offsets may end before the rows, the status word is clear already
+    const void* k_lo;       // there: [rows, H, 128] what the keys lost in rounding, sequence n's from cu_lo[n] on
+    const int32_t* cu_lo;   // [N + 1]
+    long long lo_rows;
+    int lo_tiles;           // used by query tiles whose keys are at most this many tiles
     uint32_t wait_limit;
 };
 

@@ -41,6 +41,9 @@ struct ChunkParams {
     int32_t* tiles;             // [N + 1] tiles before each sequence
     void* kv;                   // [num_keys, H, 256]
     void* pe;                   // [num_keys, 64]
+    void* k_lo;                 // [lo_rows, H, 128]
+    int32_t* cu_lo;             // [N + 1] rows of k_lo before each sequence's
+    int lo_tiles;
     uint32_t* status;
     int num_pages, page_size, width, num_keys, T, H, N;
     uint32_t wait_limit;
@@ -53,64 +56,67 @@ struct ChunkMaps {
 // ---- where each sequence's expanded rows and tiles start: one CTA ----
 constexpr int PLAN_THREADS = 1024;
 
+// Sum of `mine` over the threads before this one; the CTA's total in `total`.
+__device__ __forceinline__ long long threads_before(long long mine, long long& total, long long* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = x - mine;
+    total = 0;
+    for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    return before;
+}
+
 __global__ void __launch_bounds__(PLAN_THREADS) latent_chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
-    __shared__ long long sums[2][PLAN_THREADS / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ long long sums[PLAN_THREADS / 32];
+    const int tid = threadIdx.x;
     const long long most = (long long)p.width * p.page_size;
-    long long rows0 = 0, tiles0 = 0;
+    long long rows0 = 0, tiles0 = 0, lo0 = 0, all;
     bool bad = false, bad_cu = false;
     if (tid < WS_CLEAR / 4) p.status[tid] = 0u;
     for (int base = 0; base < p.N; base += PLAN_THREADS) {
         const int n = base + tid;
-        long long rows = 0;
+        long long rows = 0, lq = 0;
         if (n < p.N) {
             const int a = p.cu_q[n], b = p.cu_q[n + 1], len = p.lens[n];
             bad_cu |= a < 0 || b < a || b > p.T || (n == 0 && a != 0);
             if (b > a) {
                 bad |= len < 0 || len > most;
                 rows = max(0ll, min((long long)len, most));
+                lq = (long long)b - a;
             }
         }
-        long long x = rows;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) sums[0][warp] = x;
-        __syncthreads();
-        long long all = 0, before = rows0 + x - rows;
-        for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-            if (w < warp) before += sums[0][w];
-            all += sums[0][w];
-        }
-        const long long first = min(before, (long long)p.num_keys), last = min(before + rows, (long long)p.num_keys);
-        bad |= last - first < rows;
-        const long long own = (last - first + LAT_TILE - 1) / LAT_TILE;
-        x = own;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
-        if (lane == 31) sums[1][warp] = x;
-        __syncthreads();
-        long long tiles = 0, ahead = tiles0 + x - own;
-        for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-            if (w < warp) ahead += sums[1][w];
-            tiles += sums[1][w];
-        }
+        const long long before = rows0 + threads_before(rows, all, sums);
+        rows0 += all;
+        const long long first = min(before, (long long)p.num_keys), last = min(before + rows, (long long)p.num_keys), lk = last - first;
+        bad |= lk < rows;
+        // tiles; rows of k_lo: those that a sequence's first 256 queries see, or more, where they are few enough
+        const long long sees = lk - lq + min(lq, 256ll), limit = (long long)p.lo_tiles * LAT_TILE;
+        const long long tiles = (lk + LAT_TILE - 1) / LAT_TILE, lo = sees <= limit ? min(lk, limit) : 0;
+        const long long tiles_at = tiles0 + threads_before(tiles, all, sums);
+        tiles0 += all;
+        const long long lo_at = lo0 + threads_before(lo, all, sums);
+        lo0 += all;
         if (n < p.N) {
             p.cu_k[n] = (int)first;
-            p.tiles[n] = (int)ahead;
+            p.tiles[n] = (int)tiles_at;
+            p.cu_lo[n] = (int)lo_at;
         }
-        rows0 += all;
-        tiles0 += tiles;
     }
     if (tid == 0) {
         p.cu_k[p.N] = (int)min(rows0, (long long)p.num_keys);
         p.tiles[p.N] = (int)tiles0;
+        p.cu_lo[p.N] = (int)lo0;
     }
     __syncthreads();                             // the status word is clear
     if (bad) set_status(p.status, STATUS_BAD_PAGE);
@@ -141,6 +147,7 @@ static_assert(X_SMEM <= 232448, "shared memory of one CTA");
 // A tile of the line: sequence, first row of the tile in it, its rows there.
 struct ChunkTile {
     int n, row0, rows, out0;
+    int lo0, lo_rows;                            // the tile's first row in k_lo, how many of its rows are there
     __device__ __forceinline__ void find(const ChunkParams& p, int tile) {
         int lo = 0, hi = p.N - 1;                // the last sequence whose tiles start at or before this one
         while (lo < hi) {
@@ -152,6 +159,8 @@ struct ChunkTile {
         row0 = (tile - p.tiles[lo]) * LAT_TILE;
         out0 = p.cu_k[lo] + row0;
         rows = min(LAT_TILE, p.cu_k[lo + 1] - out0);
+        lo0 = p.cu_lo[lo] + row0;
+        lo_rows = min(rows, p.cu_lo[lo + 1] - lo0);
     }
 };
 
@@ -300,6 +309,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
             if (!wait_warp(base + X_DFULL + 8 * buf, (item / 2) & 1, limit, failed)) break;
             tc_fence_after();
             uint8_t* out = static_cast<uint8_t*>(p.kv) + (((long long)t.out0 + r) * p.H + h) * (LAT_KV * 2);
+            uint8_t* out_lo = static_cast<uint8_t*>(p.k_lo) + (((long long)t.lo0 + r) * p.H + h) * (LAT_N * 2);
 #pragma unroll
             for (int b = 0; b < LAT_KV / 32; ++b) {
                 float x[32];
@@ -317,6 +327,14 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = pack2<FP16>(x[e + 2 * k], x[e + 2 * k + 1]);
                         store32(out + 64 * b + 2 * e, w);
+                        if (b < LAT_N / 32 && r < t.lo_rows) {       // what the keys lose in rounding
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float2 hi = unpack2<FP16>(w[k]);
+                                w[k] = pack2<FP16>(x[e + 2 * k] - hi.x, x[e + 2 * k + 1] - hi.y);
+                            }
+                            store32(out_lo + 64 * b + 2 * e, w);
+                        }
                     }
                 }
             }
@@ -331,14 +349,27 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 
 unsigned long long up256(unsigned long long b) { return (b + 255ull) / 256ull * 256ull; }
 
+// Queries that see at most this many tiles of keys get them as two numbers a
+// channel.  A key's rounding (2^-9 of it in bf16) reaches the scores, and their
+// log-sum-exp averages it over the keys that count: a relative error of 1e-4 at
+// some ten keys and of 4e-6 at 2048 (scores of unit variance), so beyond that
+// the second numbers, which add 40 % to the products of a pair, are left out.
+// fp16 rounds eight times finer.
+int lo_tiles(bool fp16) { return fp16 ? 1 : 16; }
+
 struct ChunkLayout {
-    unsigned long long cu, tiles, kv, pe, bytes;
+    unsigned long long cu, tiles, cu_lo, kv, pe, lo, bytes;
+    long long lo_rows;
     ChunkLayout(int T, int num_keys, int H, int N) {
         cu = WS_HEADER + up256(latent_share_bytes(1, T, num_keys, H, N));
         tiles = cu + up256((N + 1ull) * 4ull);
-        kv = tiles + up256((N + 1ull) * 4ull);
+        cu_lo = tiles + up256((N + 1ull) * 4ull);
+        kv = cu_lo + up256((N + 1ull) * 4ull);
         pe = kv + (unsigned long long)num_keys * H * LAT_KV * 2ull;
-        bytes = pe + (unsigned long long)num_keys * LAT_P * 2ull;
+        lo = pe + up256((unsigned long long)num_keys * LAT_P * 2ull);
+        const long long most = (long long)N * lo_tiles(false) * LAT_TILE;
+        lo_rows = num_keys < most ? num_keys : most;
+        bytes = lo + (unsigned long long)lo_rows * H * LAT_N * 2ull;
     }
 };
 
@@ -381,6 +412,7 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
     ChunkParams c{};
     c.cache = cache, c.table = block_table, c.lens = seq_lens, c.cu_q = cu_seqlens_q;
     c.cu_k = reinterpret_cast<int32_t*>(ws + at.cu), c.tiles = reinterpret_cast<int32_t*>(ws + at.tiles);
+    c.cu_lo = reinterpret_cast<int32_t*>(ws + at.cu_lo), c.k_lo = ws + at.lo, c.lo_tiles = lo_tiles((flags & KDA_FLAG_FP16) != 0u);
     c.kv = ws + at.kv, c.pe = ws + at.pe, c.status = reinterpret_cast<uint32_t*>(ws);
     c.num_pages = num_pages, c.page_size = page_size, c.width = table_width, c.num_keys = num_keys;
     c.T = T, c.H = H, c.N = N, c.wait_limit = debug_wait_limit();
@@ -392,6 +424,7 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
     p.q = q, p.kv = c.kv, p.k_pe = c.pe, p.k_pe_stride = LAT_P, p.o_out = o, p.lse_out = lse;
     p.cu_q = cu_seqlens_q, p.cu_k = c.cu_k, p.status = c.status;
     p.scale = scale > 0.f && !std::isnan(scale) ? scale : 1.0f / std::sqrt((float)LAT_QK);
+    p.k_lo = c.k_lo, p.cu_lo = c.cu_lo, p.lo_rows = at.lo_rows, p.lo_tiles = c.lo_tiles;
     p.Tq = T, p.Tk = num_keys, p.H = H, p.N = N, p.causal = 1, p.chunk = 1, p.wait_limit = debug_wait_limit();
 
     latent_chunk_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(c);

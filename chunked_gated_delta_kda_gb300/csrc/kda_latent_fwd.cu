@@ -81,7 +81,7 @@ static_assert(F_SMEM <= 232448, "shared memory of one CTA");
 constexpr float RESCALE_LOG2 = 8.f;
 
 struct FwdMaps {
-    CUtensorMap q, kv, pe;
+    CUtensorMap q, kv, pe, lo;
 };
 
 // Where a part's row keeps its 16-byte piece: swizzled, so that a thread a row
@@ -226,7 +226,7 @@ enum Split { WHOLE, CLUSTER, SHARED };
 // CLUSTER: the CTAs of a cluster share the keys of a tile pair, each with its
 // own m, l and O, and join them through the cluster's shared memory.  SHARED:
 // see above.
-template <bool FP16, int SPLIT>
+template <bool FP16, int SPLIT, bool CHUNK>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
     latent_fwd_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ FwdMaps maps, int slots) {
     extern __shared__ uint8_t smem_raw[];
@@ -261,6 +261,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     const int shift = s.lk - s.lq;
     int nt[2];   // key tiles that each query tile needs
     pair_tiles(p, s, row0, nt);
+    // where the keys come as two numbers a channel: K takes five slabs a step, and the loads wait for all of the step before
+    const bool lo = CHUNK && max(nt[0], nt[1]) <= p.lo_tiles;
+    const int nk = lo ? 5 : 3, per = nk + 2;
+    const int lo0 = lo ? p.cu_lo[n] : 0;
     int j_first = 0;   // first key tile of this CTA
     if constexpr (SPLIT != WHOLE) {
         const int ranks = SPLIT == CLUSTER ? (int)cluster_size() : item.z, rank = SPLIT == CLUSTER ? (int)cluster_rank() : item.y;
@@ -274,6 +278,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         prefetch_map(&maps.q);
         prefetch_map(&maps.kv);
         prefetch_map(&maps.pe);
+        if (CHUNK) prefetch_map(&maps.lo);
     }
     if (tid == 0) {
         for (uint32_t t = 0; t < 2; ++t) {
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + F_TMEM);
-    // slab sequence: K of step j at 5 j .. 5 j + 2, its V at 5 j + 3, 5 j + 4
+    // slab sequence: K of step j at 5 j .. 5 j + 2, its V at 5 j + 3, 5 j + 4 (with two numbers a channel: 7 j .. 7 j + 4)
     auto slab = [&](uint32_t i) { return base + F_RING + (i % RING) * SLAB; };
 
     if (warp >= 8) {
@@ -319,17 +324,25 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             bool half = false;   // given up between a step's K and its V
             for (; j < steps; ++j) {
                 const int tok = (int)s.k0 + (j_first + j) * LAT_TILE, st = j & 1;
-                if (j >= 2 && !wait_phase(base + F_VEMPTY + 8 * st, (j / 2 - 1) & 1, limit, failed)) break;
-                mbar_arrive_expect_tx(base + F_KFULL + 8 * st, 3 * SLAB);
-                for (int c = 0; c < 2; ++c) tma_load_3d(slab(5 * j + c), &maps.kv, 64 * c, h, tok, base + F_KFULL + 8 * st);
-                tma_load_3d(slab(5 * j + 2), &maps.pe, 0, 0, tok, base + F_KFULL + 8 * st);
-                if (j >= 1 && !wait_phase(s_last + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, limit, failed)) {
+                const uint32_t s_before = s_last + 8 * ((j - 1) & 1), v_before = base + F_VEMPTY + 8 * ((j - 1) & 1);
+                // (the seven-slab steps: K takes the place of the last slab of V of step j - 2, which S (j - 1) comes
+                // behind, and of K of step j - 1; V that of K's last and V's first of step j - 1)
+                if (lo ? j >= 1 && !wait_phase(s_before, ((j - 1) >> 1) & 1, limit, failed)
+                       : j >= 2 && !wait_phase(base + F_VEMPTY + 8 * st, (j / 2 - 1) & 1, limit, failed))
+                    break;
+                mbar_arrive_expect_tx(base + F_KFULL + 8 * st, nk * SLAB);
+                for (int c = 0; c < 2; ++c) tma_load_3d(slab(per * j + c), &maps.kv, 64 * c, h, tok, base + F_KFULL + 8 * st);
+                tma_load_3d(slab(per * j + 2), &maps.pe, 0, 0, tok, base + F_KFULL + 8 * st);
+                if (lo)
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_3d(slab(per * j + 3 + c), &maps.lo, 64 * c, h, lo0 + (j_first + j) * LAT_TILE, base + F_KFULL + 8 * st);
+                if (j >= 1 && !wait_phase(lo ? v_before : s_before, ((j - 1) >> 1) & 1, limit, failed)) {
                     half = true;
                     break;
                 }
                 mbar_arrive_expect_tx(base + F_VFULL + 8 * st, 2 * SLAB);
                 for (int c = 0; c < 2; ++c)
-                    tma_load_3d(slab(5 * j + 3 + c), &maps.kv, LAT_N + 64 * c, h, tok, base + F_VFULL + 8 * st);
+                    tma_load_3d(slab(per * j + nk + c), &maps.kv, LAT_N + 64 * c, h, tok, base + F_VFULL + 8 * st);
             }
             // every copy issued here has landed before the CTA ends
             for (int t = 0; t < 2; ++t)
@@ -353,16 +366,24 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 if (!loaded && !wait(F_KFULL + 8 * (j & 1), (j >> 1) & 1)) return;
 #pragma unroll
                 for (int c = 0; c < 3; ++c) {
-                    const Desc a = desc_k(base + F_Q + (3 * t + c) * SLAB), b = desc_k(slab(5 * j + c));
+                    const Desc a = desc_k(base + F_Q + (3 * t + c) * SLAB), b = desc_k(slab(per * j + c));
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + 256 * t, a + 2 * ks, b + 2 * ks, id, c + ks > 0);
+                }
+                if (lo) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const Desc a = desc_k(base + F_Q + (3 * t + c) * SLAB), b = desc_k(slab(per * j + 3 + c));
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + 256 * t, a + 2 * ks, b + 2 * ks, id, 1);
+                    }
                 }
                 mma_commit_warp(base + F_SFULL + 16 * t + 8 * (j & 1));
             };
             for (int t = 0; t < 2 && ok; ++t)
                 if (nt[t] > 0 && wait(F_QFULL + 8 * t, 0)) qk(t, 0, t == 1 && nt[0] > 0);
             for (int j = 0; j < steps && ok; ++j) {
-                const uint32_t v = 5 * j + 3;
+                const uint32_t v = per * j + nk;
                 if (!wait(F_VFULL + 8 * (j & 1), (j >> 1) & 1)) break;
                 if ((j_first + j + 1) * LAT_TILE > s.lk) {
                     // rows past the sequence's end hold whatever follows: zero weights must meet zeros
@@ -583,9 +604,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
 }
 
-template <bool FP16, int SPLIT>
+template <bool FP16, int SPLIT, bool CHUNK>
 cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, int ranks, cudaStream_t stream) {
-    const auto kernel = latent_fwd_kernel<FP16, SPLIT>;
+    const auto kernel = latent_fwd_kernel<FP16, SPLIT, CHUNK>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
     if (e != cudaSuccess) return e;
     if (SPLIT == SHARED) {   // (the kernel behind it takes its records as they are)
@@ -616,6 +637,13 @@ cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, int ra
     cfg.blockDim = dim3(FWD_ROWS);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, latent_share_join_kernel<FP16>, p, slots);
+}
+
+template <bool FP16, bool CHUNK>
+cudaError_t launch_split(const LatentParams& p, const FwdMaps& maps, int slots, int ranks, cudaStream_t stream) {
+    if (ranks > 1) return launch<FP16, CLUSTER, CHUNK>(p, maps, slots, ranks, stream);
+    if (p.share_items != nullptr) return launch<FP16, SHARED, CHUNK>(p, maps, slots, 1, stream);
+    return launch<FP16, WHOLE, CHUNK>(p, maps, slots, 1, stream);
 }
 
 // Few query tiles on long keys: a cluster for each tile pair, as large as leaves every CTA of every cluster an SM
@@ -658,11 +686,11 @@ cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t str
         return cudaErrorInvalidValue;
     const int slots = latent_slots(varlen, p.Tq, p.N, FWD_ROWS);
     const int ranks = cluster_of(rows_k, p.N, slots, p.H);
-    if (ranks > 1)
-        return fp16 ? launch<true, CLUSTER>(p, maps, slots, ranks, stream) : launch<false, CLUSTER>(p, maps, slots, ranks, stream);
-    if (p.share_items != nullptr)
-        return fp16 ? launch<true, SHARED>(p, maps, slots, 1, stream) : launch<false, SHARED>(p, maps, slots, 1, stream);
-    return fp16 ? launch<true, WHOLE>(p, maps, slots, 1, stream) : launch<false, WHOLE>(p, maps, slots, 1, stream);
+    if (!p.chunk) return fp16 ? launch_split<true, false>(p, maps, slots, ranks, stream) : launch_split<false, false>(p, maps, slots, ranks, stream);
+    const bool some = p.lo_rows > 0;
+    if (!latent_row_map(&maps.lo, some ? p.k_lo : p.q, LAT_N, p.H, some ? p.lo_rows : 1, (long long)p.H * LAT_N, LAT_TILE))
+        return cudaErrorInvalidValue;
+    return fp16 ? launch_split<true, true>(p, maps, slots, ranks, stream) : launch_split<false, true>(p, maps, slots, ranks, stream);
 }
 
 }  // namespace kda

@@ -589,8 +589,10 @@ size_t kda_latent_chunk_workspace_bytes(int T, int num_keys, int H, int N);
  * as zeros; each sets KDA_ERR_BAD_PAGE.  Rows past a sequence's length are
  * not used, whatever they hold.
  *
- * Precision: expanded keys and values are summed in 32 bits and rounded to
- * the tensors' type, as a prefill's are; the rest as for kda_latent_fwd.
+ * Precision: expanded keys and values are summed in 32 bits; values are
+ * rounded to the tensors' type, as a prefill's are; keys come as a sum of two
+ * such numbers where queries see few of them (2048 in bf16, 128 in fp16), and
+ * are rounded where they see more.  The rest as for kda_latent_fwd.
  */
 kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int page_size,
                             const int32_t* block_table, int table_width, const int32_t* seq_lens, const void* w_up,

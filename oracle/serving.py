@@ -39,9 +39,15 @@ def _rounded(x, spread, dtype) -> Tuple[torch.Tensor, torch.Tensor]:
     return mid, torch.maximum(high - mid, mid - low)
 
 
+def _as_two(x, spread, u: float, tiny: float) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x, and how far a sum of two numbers of a type with unit u may be from it, which a 32-bit sum was split into."""
+    return x, 512 * F32 * spread + u * u * x.abs() + tiny
+
+
 def latent_chunk(q, cache, table, lens: Sequence[int], w_up, lens_q: Sequence[int], scale: Optional[float] = None,
-                 dtype=None, u: float = 0.0, tiny: float = 0.0):
-    """q [T, H, 192] (packed by lens_q).  With `dtype` the expanded keys and values are rounded to it.  Returns
+                 dtype=None, u: float = 0.0, tiny: float = 0.0, few: int = 0):
+    """q [T, H, 192] (packed by lens_q).  With `dtype` the expanded values are rounded to it, and the keys, but for
+    query pairs of tiles (256 rows) that see at most `few` keys, for which they are sums of two such numbers.  Returns
     (o, lse, err_o, err_lse), the errors' bounds as in ``latent.attention`` with what the expanded values may be off."""
     scale = SCALE if scale is None else scale
     q, w = q.double(), w_up.double()
@@ -51,23 +57,30 @@ def latent_chunk(q, cache, table, lens: Sequence[int], w_up, lens_q: Sequence[in
     eo, el = torch.zeros_like(o), torch.zeros_like(lse)
     a = 0
     for n, (lq, lk) in enumerate(zip(lens_q, lens)):
-        if lq == 0:
-            continue
-        rows = cached_rows(cache, table, n, lk)
-        c, pe = rows[:, :LATENT], rows[:, LATENT:]
-        sees = _sees(lq, lk, True)
-        for h in range(H):
-            kv, ekv = _rounded(c @ w[h].T, c.abs() @ w[h].abs().T, dtype)
-            k, v, ek, ev = kv[:, :KEY], kv[:, KEY:], ekv[:, :KEY], ekv[:, KEY:]
-            qi = q[a:a + lq, h]
-            ro, rl, e, x = attention(qi, torch.cat([k, pe], 1), v, sees, scale, u, tiny)
-            more = torch.zeros(lq, dtype=torch.float64)
-            if lk:
-                more = scale * torch.where(sees, qi[:, :KEY].abs() @ ek.T, torch.zeros(lq, lk, dtype=torch.float64)).amax(-1)
-                s = torch.where(sees, scale * (qi @ torch.cat([k, pe], 1).T), torch.full((lq, lk), -float("inf"), dtype=torch.float64))
-                p = torch.nan_to_num(torch.softmax(s, -1))
-                e = e + 2 * more[:, None] * (p @ v.abs()) + p @ ev
-            o[a:a + lq, h], lse[a:a + lq, h], eo[a:a + lq, h], el[a:a + lq, h] = ro, rl, e, x + more
+        rows = cached_rows(cache, table, n, lk) if lq else None
+        for first in range(0, lq, 256):
+            pair = slice(first, min(lq, first + 256))
+            at = slice(a + pair.start, a + pair.stop)
+            sees = _sees(lq, lk, True)[pair]
+            two = -(-max(0, min(lk, pair.stop + lk - lq)) // 128) * 128 <= few
+            c, pe = rows[:, :LATENT], rows[:, LATENT:]
+            for h in range(H):
+                wk, wv = w[h, :KEY], w[h, KEY:]
+                spread = c.abs() @ wk.abs().T
+                k, ek = _as_two(c @ wk.T, spread, u, tiny) if two else _rounded(c @ wk.T, spread, dtype)
+                v, ev = _rounded(c @ wv.T, c.abs() @ wv.abs().T, dtype)
+                qi, k = q[at, h], torch.cat([k, pe], 1)
+                # (the scores' sums are 128 products longer where the keys are two numbers)
+                ro, rl, e, x = attention(qi, k, v, sees, scale, u, tiny)
+                more = torch.zeros(len(qi), dtype=torch.float64)
+                if lk:
+                    none = torch.zeros(len(qi), lk, dtype=torch.float64)
+                    more = torch.where(sees, scale * (qi[:, :KEY].abs() @ ek.T), none).amax(-1)
+                    if two:
+                        more = more + 128 * F32 * scale * torch.where(sees, qi.abs() @ k.abs().T, none).amax(-1)
+                    p = torch.nan_to_num(torch.softmax(torch.where(sees, scale * (qi @ k.T), none - float("inf")), -1))
+                    e = e + 2 * more[:, None] * (p @ v.abs()) + p @ ev
+                o[at, h], lse[at, h], eo[at, h], el[at, h] = ro, rl, e, x + more
         a += lq
     return o, lse, eo, el
 

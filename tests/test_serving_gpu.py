@@ -12,6 +12,7 @@ pytestmark = pytest.mark.gpu
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
 U = {BF: 2.0 ** -8, FP: 2.0 ** -11}
 TINY = {BF: 0.0, FP: 2.0 ** -25}
+FEW = {BF: 2048, FP: 128}
 
 
 def latent():
@@ -95,6 +96,11 @@ CHUNKS = [
     ([256, 1, 2], [257, 385, 1000], 17, 192, FP),            # pages of one and a half tiles
     ([7, 300], [9000, 310], 2, 64, BF),                      # keys shared by CTAs of the device's choice
     ([20], [4100], 2, 32, FP),                               # and of the host's
+    ([700, 3], [2500, 2048], 2, 64, BF),                     # around the border of few keys: pairs of tiles on either side,
+    ([300, 260, 2], [2049, 2049, 2050], 1, 16, BF),
+    ([300, 200], [300, 129], 2, 64, FP),
+    ([600] * 8 + [40], [900] * 8 + [2000], 6, 64, BF),       # two numbers a key with CTAs that share keys,
+    ([2048], [2048], 1, 64, BF), ([40], [2047], 3, 32, BF),  # and in clusters
 ]
 
 
@@ -106,7 +112,7 @@ def test_chunk(lens_q, lens, H, page, dtype):
     ws = torch.full((latent().latent_chunk_workspace_bytes(sum(lens_q), keys, H, len(lens)),), 255, dtype=torch.uint8, device="cuda")
     o, lse = run_chunk(q, cache, table, lens, w, lens_q, keys, workspace=ws)
     assert status(ws) == 0
-    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, dtype=dtype, u=U[dtype], tiny=TINY[dtype])
+    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, dtype=dtype, u=U[dtype], tiny=TINY[dtype], few=FEW[dtype])
     near(o, ro, eo, "o")
     near(lse, rl, el, "lse")
     again = run_chunk(q, cache, table, lens, w, lens_q, keys)
@@ -121,7 +127,7 @@ def test_chunk_of_many_sequences(n, page, dtype):
     lens = [l + e for l, e in zip(lens_q, torch.randint(0, 40 if n > 100 else 150, (n,), generator=g).tolist())]
     q, cache, table, w = chunk_inputs(lens_q, lens, 2, page, dtype, seed=n, fill=float("nan"))
     o, lse = run_chunk(q, cache, table, lens, w, lens_q)
-    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, dtype=dtype, u=U[dtype], tiny=TINY[dtype])
+    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, dtype=dtype, u=U[dtype], tiny=TINY[dtype], few=FEW[dtype])
     near(o, ro, eo, "o")
     near(lse, rl, el, "lse")
 
@@ -138,7 +144,7 @@ def test_chunk_scale_and_strided_inputs():
     big[..., 4:516] = w.cuda()
     got = latent().latent_chunk(wide[:, 1:3, 3:195], cache.cuda(), tables.T, i32(lens), big[..., 4:516], cu(lens_q), 210, scale=0.03)
     assert all(torch.equal(a, b) for a, b in zip(want, got))
-    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, scale=0.03, dtype=BF, u=U[BF])
+    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, scale=0.03, dtype=BF, u=U[BF], few=FEW[BF])
     near(want[0], ro, eo, "o")
     near(want[1], rl, el, "lse")
 
@@ -151,7 +157,7 @@ def test_chunk_missing_pages_count_as_zeros(page):
     ws = torch.zeros(latent().latent_chunk_workspace_bytes(83, 630, 2, 3), dtype=torch.uint8, device="cuda")
     o, lse = run_chunk(q, cache, table, lens, w, lens_q, workspace=ws)
     assert status(ws) == 8
-    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, dtype=BF, u=U[BF])
+    ro, rl, eo, el = sv.latent_chunk(q, cache, table, lens, w, lens_q, dtype=BF, u=U[BF], few=FEW[BF])
     near(o, ro, eo, "o")
     near(lse, rl, el, "lse")
 
