@@ -112,14 +112,12 @@ def load_library(path: Optional[str] = None):
     lib.kda_latent_chunk.restype = ctypes.c_int
     lib.kda_latent_chunk.argtypes = [vp, vp, i, i, vp, i, vp, vp, f, vp, i, vp, vp, i, i, i, u, vp, sz, vp]
     for name in ("kda_page_fork", "kda_page_free", "kda_page_compact"):
-        getattr(lib, name + "_workspace_bytes").restype = sz
-        getattr(lib, name + "_workspace_bytes").argtypes = [i]
         getattr(lib, name).restype = ctypes.c_int
-    lib.kda_page_fork.argtypes = [vp, i, vp, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, i, i, vp, sz, vp]
+    lib.kda_page_fork.argtypes = [vp, i, vp, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, i, i, vp, vp]
     lib.kda_page_copy.restype = ctypes.c_int
     lib.kda_page_copy.argtypes = [vp, i, i, ll, vp, vp, i, vp, vp]
-    lib.kda_page_free.argtypes = [vp, i, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, i, vp, sz, vp]
-    lib.kda_page_compact.argtypes = [vp, i, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, vp, vp, i, vp, sz, vp]
+    lib.kda_page_free.argtypes = [vp, i, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, i, vp, vp]
+    lib.kda_page_compact.argtypes = [vp, i, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, vp, vp, i, vp, vp]
     lib.kda_verify_drafts.restype = ctypes.c_int
     lib.kda_verify_drafts.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, u, vp, vp]
     lib.kda_debug_set.restype = ctypes.c_int

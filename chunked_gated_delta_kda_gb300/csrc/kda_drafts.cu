@@ -339,8 +339,9 @@ extern "C" kda_status kda_verify_drafts(const int64_t* draft_tokens, const void*
     const long long pieces = 16 / size;
     const bool vec = !off(target_probs, 16) && !off(draft_probs, 16) && p.p_n % pieces == 0 && p.p_s % pieces == 0 &&
                      p.q_n % pieces == 0 && p.q_s % pieces == 0;
+    // as many CTAs a sequence as fit the GPU at once (two an SM), and have 512 elements a warp
     int ctas = 1;
-    while (ctas < DR_MOST && (long long)ctas * DR_WARPS * 512 < V) ctas *= 2;
+    while (ctas < DR_MOST && (long long)ctas * DR_WARPS * 512 < V && 2ll * ctas * N <= 304) ctas *= 2;
     p.seg = (int)(((long long)V + ctas * DR_WARPS * 512 - 1) / (ctas * DR_WARPS * 512) * 512);
     if (p.status && cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
     const cudaError_t e = (flags & KDA_FLAG_FP32) != 0u   ? launch<float>(p, vec, N, ctas, stream)

@@ -23,42 +23,28 @@ from typing import Optional, Sequence, Tuple, Union
 import torch
 
 from .binding import load_library
-from .latent import (INT_MAX, _check, _check_int, _current_device, _elsewhere, _hand_back, _raise, _same_device, _scratch,
-                     _status_workspace, _stream, _together)
+from .latent import INT_MAX, _check, _check_int, _current_device, _elsewhere, _raise, _same_device, _status_workspace, _stream, _together
+
+_I32 = torch.int32
 
 
-def _checked(block_table, seq_lens, refs, free_pages, free_head, page_size, rows=(), vectors=()):
-    """Checks what the three table functions share; ``rows``: more (name, tensor) pairs of seq_lens' shape, ``vectors``:
-    of any length."""
-    try:
-        fine = (block_table.dtype is seq_lens.dtype is refs.dtype is free_pages.dtype is free_head.dtype is torch.int32
-                and block_table.dim() == 2 and refs.dim() == free_pages.dim() == 1 and free_head.shape == (1,)
-                and seq_lens.shape == block_table.shape[:1] and 0 < page_size <= INT_MAX and page_size % 1 == 0
-                and all(t.dtype is torch.int32 and t.shape == seq_lens.shape for _, t in rows)
-                and all(t.dtype is torch.int32 and t.dim() == 1 for _, t in vectors)
-                and max(block_table.size(0), block_table.size(1), refs.size(0), free_pages.size(0)) <= INT_MAX
-                and _together(seq_lens.get_device(), block_table, refs, free_pages, free_head, *(t for _, t in rows),
-                              *(t for _, t in vectors)))
-    except AttributeError:   # not a tensor
-        fine = False
-    if not fine:
-        _check_int("page_size", page_size)
-        if page_size < 1:
-            raise ValueError(f"page_size must be positive, got {page_size}")
-        _check("block_table", block_table, torch.int32, (None, None))
-        _check("seq_lens", seq_lens, torch.int32, (block_table.shape[0],))
-        _check("refs", refs, torch.int32, (None,))
-        _check("free_pages", free_pages, torch.int32, (None,))
-        _check("free_head", free_head, torch.int32, (1,))
-        for name, t in rows:
-            _check(name, t, torch.int32, seq_lens.shape)
-        for name, t in vectors:
-            _check(name, t, torch.int32, (None,))
-        for name, t in (("block_table", block_table), ("refs", refs), ("free_pages", free_pages)):
-            for size in t.shape:
-                _check_int(f"a size of {name}", size)
-        _same_device(seq_lens.get_device(), block_table, refs, free_pages, free_head, *(t for _, t in rows),
-                     *(t for _, t in vectors))
+def _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, **more):
+    """Says what is wrong with the arguments of a table function (see ``latent``'s checks); ``more``: tensors of
+    seq_lens' length, or with a name that ends in ``s_`` of any."""
+    _check_int("page_size", page_size)
+    if page_size < 1:
+        raise ValueError(f"page_size must be positive, got {page_size}")
+    _check("block_table", block_table, _I32, (None, None))
+    _check("seq_lens", seq_lens, _I32, (block_table.shape[0],))
+    _check("refs", refs, _I32, (None,))
+    _check("free_pages", free_pages, _I32, (None,))
+    _check("free_head", free_head, _I32, (1,))
+    for name, t in more.items():
+        _check(name.rstrip("_"), t, _I32, (None,) if name[-1] == "_" else (block_table.shape[0],))
+    for name, t in (("block_table", block_table), ("refs", refs), ("free_pages", free_pages), *more.items()):
+        for size in t.shape:
+            _check_int(f"a size of {name.rstrip('_')}", size)
+    _same_device(seq_lens.get_device(), block_table, refs, free_pages, free_head, *more.values())
 
 
 def page_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor, children: torch.Tensor,
@@ -74,13 +60,21 @@ def page_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.
     Full pages are shared; a last page that is not full gets a page of its own.
     Returns (the new lengths, the new refs, the new free_head, pairs int32
     [F, 2] for ``page_copy``: the page to copy and the own page, or -1); the
-    other inputs stay as they are.  ``workspace`` (256-byte aligned,
-    ``page_fork_workspace_bytes``) records device-detected faults for
-    ``binding.get_status``; beside a smaller one another is allocated."""
-    _checked(block_table, seq_lens, refs, free_pages, free_head, page_size, vectors=(("parents", parents), ("children", children)))
-    if parents.shape != children.shape or parents.shape[0] > INT_MAX:
+    other inputs stay as they are.  ``workspace`` (256 bytes, 256-byte aligned)
+    records device-detected faults for ``binding.get_status``."""
+    try:
+        index = seq_lens.get_device()
+        N, width = block_table.shape
+        (pages,), (free,), (F,) = refs.shape, free_pages.shape, parents.shape
+        fine = (block_table.dtype is seq_lens.dtype is parents.dtype is children.dtype is refs.dtype is free_pages.dtype
+                is free_head.dtype is _I32 and seq_lens.shape == (N,) and children.shape == (F,) and free_head.shape == (1,)
+                and 0 < page_size <= INT_MAX and page_size % 1 == 0 and max(N, width, pages, free, F) <= INT_MAX
+                and _together(index, block_table, parents, children, refs, free_pages, free_head))
+    except (AttributeError, ValueError):   # not a tensor, or not of one dimension or two
+        fine = False
+    if not fine:
+        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, parents_=parents, children_=children)
         raise ValueError(f"parents and children must be of one length, got {parents.shape[0]} and {children.shape[0]}")
-    index = seq_lens.get_device()
     if index != _current_device():
         return _elsewhere(index, page_fork, block_table, seq_lens, parents, children, refs, free_pages, free_head, page_size,
                           workspace)
@@ -89,29 +83,13 @@ def page_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.
     # copies are held until the launch: a freed one's memory would go to the next
     seq_lens, refs, free_pages = seq_lens.contiguous(), refs.contiguous(), free_pages.contiguous()
     parents, children = parents.contiguous(), children.contiguous()
-    (N, width), F = block_table.shape, parents.shape[0]
-    scratch = _scratch(workspace, page_fork_workspace_bytes(N), index, seq_lens.device)
     lens_out, refs_out, head_out = torch.empty_like(seq_lens), torch.empty_like(refs), torch.empty_like(free_head)
-    pairs = torch.empty((F, 2), dtype=torch.int32, device=seq_lens.device)
+    pairs = torch.empty((F, 2), dtype=_I32, device=seq_lens.device)
     _raise(load_library().kda_page_fork(
-        block_table.data_ptr(), width, seq_lens.data_ptr(), parents.data_ptr(), children.data_ptr(), refs.data_ptr(),
-        refs.shape[0], free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(), int(page_size), lens_out.data_ptr(),
-        refs_out.data_ptr(), head_out.data_ptr(), pairs.data_ptr(), N, F, scratch.data_ptr(),
-        scratch.numel() * scratch.element_size(), _stream(index)), "kda_page_fork")
-    _hand_back(scratch, workspace)
+        block_table.data_ptr(), width, seq_lens.data_ptr(), parents.data_ptr(), children.data_ptr(), refs.data_ptr(), pages,
+        free_pages.data_ptr(), free, free_head.data_ptr(), int(page_size), lens_out.data_ptr(), refs_out.data_ptr(),
+        head_out.data_ptr(), pairs.data_ptr(), N, F, _status_workspace(workspace, index), _stream(index)), "kda_page_fork")
     return lens_out, refs_out, head_out, pairs
-
-
-def page_fork_workspace_bytes(N: int) -> int:
-    return int(load_library().kda_page_fork_workspace_bytes(N))
-
-
-def page_free_workspace_bytes(pages: int) -> int:
-    return int(load_library().kda_page_free_workspace_bytes(pages))
-
-
-def page_compact_workspace_bytes(pages: int) -> int:
-    return int(load_library().kda_page_compact_workspace_bytes(pages))
 
 
 def page_copy(pools: Union[torch.Tensor, Sequence[torch.Tensor]], pairs: torch.Tensor,
@@ -127,33 +105,44 @@ def page_copy(pools: Union[torch.Tensor, Sequence[torch.Tensor]], pairs: torch.T
     updated in place."""
     if not isinstance(pools, (torch.Tensor, list, tuple)):
         raise TypeError("pools must be a torch.Tensor or a list of them")
-    several = [pools] if isinstance(pools, torch.Tensor) else pools
+    several = (pools,) if isinstance(pools, torch.Tensor) else pools
     if not several:
         raise ValueError("pools must not be empty")
     first = several[0]
-    for t in several:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("pools must be torch.Tensors")
-        if not t.is_cuda or t.dim() < 1 or not t.is_contiguous():
-            raise ValueError(f"pools must be contiguous CUDA tensors [pages, ...], got {tuple(t.shape)} on {t.device}")
-        if t.shape != first.shape or t.dtype is not first.dtype:
-            raise ValueError("pools must have one shape and type")
-    _check("pairs", pairs, torch.int32, (None, 2))
-    if count is not None:
-        _check("count", count, torch.int32, (1,))
-    _check_int("a size of pairs", pairs.shape[0])
-    _check_int("a size of pools", first.shape[0])
-    index = first.get_device()
-    _same_device(index, pairs, count, *several)
+    try:
+        index, shape, dtype = first.get_device(), first.shape, first.dtype
+        fine = (pairs.dtype is _I32 and pairs.dim() == 2 and pairs.shape[1] == 2 and len(shape) > 0
+                and (count is None or count.dtype is _I32 and count.shape == (1,))
+                and max(pairs.shape[0], shape[0]) <= INT_MAX and _together(index, pairs, count))
+        at, low = [], 0
+        for t in several:
+            fine = fine and t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            at.append(t.data_ptr())
+            low |= at[-1]
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
+        for t in several:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("pools must be torch.Tensors")
+            if not t.is_cuda or t.dim() < 1 or not t.is_contiguous():
+                raise ValueError(f"pools must be contiguous CUDA tensors [pages, ...], got {tuple(t.shape)} on {t.device}")
+            if t.shape != first.shape or t.dtype is not first.dtype:
+                raise ValueError("pools must have one shape and type")
+        _check("pairs", pairs, _I32, (None, 2))
+        if count is not None:
+            _check("count", count, _I32, (1,))
+        _check_int("a size of pairs", pairs.shape[0])
+        _check_int("a size of pools", first.shape[0])
+        _same_device(first.get_device(), pairs, count, *several)
     if index != _current_device():
         return _elsewhere(index, page_copy, pools, pairs, count, workspace)
-    pages = first.shape[0]
+    pages = shape[0]
     page_bytes = first.numel() // max(pages, 1) * first.element_size()
-    if pages < 1 or page_bytes < 16 or page_bytes % 16 or any(t.data_ptr() % 16 for t in several):
-        raise ValueError(f"pools need pages of a multiple of 16 bytes that start on 16 bytes, got {pages} of {page_bytes}")
+    if pages < 1 or page_bytes < 16 or page_bytes % 16 or low % 16:
+        raise ValueError(f"pools must have pages of a multiple of 16 bytes that start on 16 bytes, got {pages} of {page_bytes}")
     pairs = pairs.contiguous()
-    at = (ctypes.c_void_p * len(several))(*[t.data_ptr() for t in several])
-    _raise(load_library().kda_page_copy(at, len(several), pages, page_bytes, pairs.data_ptr(),
+    _raise(load_library().kda_page_copy((ctypes.c_void_p * len(at))(*at), len(at), pages, page_bytes, pairs.data_ptr(),
                                         None if count is None else count.data_ptr(), pairs.shape[0],
                                         _status_workspace(workspace, index), _stream(index)), "kda_page_copy")
     return pools
@@ -169,24 +158,29 @@ def page_free(block_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torc
     int32 [1].  The pages that lose their last owner come in front of the free
     list, in increasing order: their entries of ``free_pages`` are written in
     place.  Returns (the new lengths, the new refs, the new free_head); the
-    other inputs stay as they are.  ``workspace`` as for ``page_fork``, with
-    ``page_free_workspace_bytes`` bytes."""
-    _checked(block_table, seq_lens, refs, free_pages, free_head, page_size, rows=(("keep_lens", keep_lens),))
-    index = seq_lens.get_device()
+    other inputs stay as they are.  ``workspace`` as for ``page_fork``."""
+    try:
+        index = seq_lens.get_device()
+        N, width = block_table.shape
+        (pages,), (free,) = refs.shape, free_pages.shape
+        fine = (block_table.dtype is seq_lens.dtype is keep_lens.dtype is refs.dtype is free_pages.dtype is free_head.dtype is _I32
+                and seq_lens.shape == keep_lens.shape == (N,) and free_head.shape == (1,)
+                and 0 < page_size <= INT_MAX and page_size % 1 == 0 and max(N, width, pages, free) <= INT_MAX
+                and _together(index, block_table, keep_lens, refs, free_pages, free_head))
+    except (AttributeError, ValueError):   # not a tensor, or not of one dimension or two
+        fine = False
+    if not fine:
+        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, keep_lens=keep_lens)
     if index != _current_device():
         return _elsewhere(index, page_free, block_table, seq_lens, keep_lens, refs, free_pages, free_head, page_size, workspace)
     if not free_pages.is_contiguous():
         raise ValueError("free_pages must be contiguous")
-    block_table, seq_lens, keep_lens, refs = (t.contiguous() for t in (block_table, seq_lens, keep_lens, refs))
-    (N, width), pages = block_table.shape, refs.shape[0]
-    scratch = _scratch(workspace, page_free_workspace_bytes(pages), index, seq_lens.device)
+    block_table, seq_lens, keep_lens, refs = block_table.contiguous(), seq_lens.contiguous(), keep_lens.contiguous(), refs.contiguous()
     lens_out, refs_out, head_out = torch.empty_like(seq_lens), torch.empty_like(refs), torch.empty_like(free_head)
     _raise(load_library().kda_page_free(
-        block_table.data_ptr(), width, seq_lens.data_ptr(), keep_lens.data_ptr(), refs.data_ptr(), pages,
-        free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(), int(page_size), lens_out.data_ptr(),
-        refs_out.data_ptr(), head_out.data_ptr(), N, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
-        _stream(index)), "kda_page_free")
-    _hand_back(scratch, workspace)
+        block_table.data_ptr(), width, seq_lens.data_ptr(), keep_lens.data_ptr(), refs.data_ptr(), pages, free_pages.data_ptr(),
+        free, free_head.data_ptr(), int(page_size), lens_out.data_ptr(), refs_out.data_ptr(), head_out.data_ptr(), N,
+        _status_workspace(workspace, index), _stream(index)), "kda_page_free")
     return lens_out, refs_out, head_out
 
 
@@ -201,22 +195,27 @@ def page_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.
     on, which stays; pairs int32 [pages // 2, 2] and count int32 [1] for
     ``page_copy``; moved int32 [pages], each page's new number, -1 for a free
     one).  The inputs stay as they are: copy the pages of every cache before
-    the new table is used.  ``workspace`` as for ``page_fork``, with
-    ``page_compact_workspace_bytes`` bytes."""
-    _checked(block_table, seq_lens, refs, free_pages, free_head, page_size)
-    index = seq_lens.get_device()
+    the new table is used.  ``workspace`` as for ``page_fork``."""
+    try:
+        index = seq_lens.get_device()
+        N, width = block_table.shape
+        (pages,), (free,) = refs.shape, free_pages.shape
+        fine = (block_table.dtype is seq_lens.dtype is refs.dtype is free_pages.dtype is free_head.dtype is _I32
+                and seq_lens.shape == (N,) and free_head.shape == (1,)
+                and 0 < page_size <= INT_MAX and page_size % 1 == 0 and max(N, width, pages, free) <= INT_MAX
+                and _together(index, block_table, refs, free_pages, free_head))
+    except (AttributeError, ValueError):   # not a tensor, or not of one dimension or two
+        fine = False
+    if not fine:
+        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size)
     if index != _current_device():
         return _elsewhere(index, page_compact, block_table, seq_lens, refs, free_pages, free_head, page_size, workspace)
-    block_table, seq_lens, refs, free_pages = (t.contiguous() for t in (block_table, seq_lens, refs, free_pages))
-    (N, width), pages = block_table.shape, refs.shape[0]
-    scratch = _scratch(workspace, page_compact_workspace_bytes(pages), index, seq_lens.device)
+    block_table, seq_lens, refs, free_pages = block_table.contiguous(), seq_lens.contiguous(), refs.contiguous(), free_pages.contiguous()
     table_out, refs_out, free_out = torch.empty_like(block_table), torch.empty_like(refs), torch.empty_like(free_pages)
-    pairs = torch.empty((pages // 2, 2), dtype=torch.int32, device=seq_lens.device)
+    pairs = torch.empty((pages // 2, 2), dtype=_I32, device=seq_lens.device)
     count, moved = torch.empty_like(free_head), torch.empty_like(refs)
     _raise(load_library().kda_page_compact(
-        block_table.data_ptr(), width, seq_lens.data_ptr(), refs.data_ptr(), pages, free_pages.data_ptr(),
-        free_pages.shape[0], free_head.data_ptr(), int(page_size), table_out.data_ptr(), refs_out.data_ptr(),
-        free_out.data_ptr(), pairs.data_ptr(), count.data_ptr(), moved.data_ptr(), N, scratch.data_ptr(),
-        scratch.numel() * scratch.element_size(), _stream(index)), "kda_page_compact")
-    _hand_back(scratch, workspace)
+        block_table.data_ptr(), width, seq_lens.data_ptr(), refs.data_ptr(), pages, free_pages.data_ptr(), free,
+        free_head.data_ptr(), int(page_size), table_out.data_ptr(), refs_out.data_ptr(), free_out.data_ptr(), pairs.data_ptr(),
+        count.data_ptr(), moved.data_ptr(), N, _status_workspace(workspace, index), _stream(index)), "kda_page_compact")
     return table_out, refs_out, free_out, pairs, count, moved

@@ -591,7 +591,7 @@ size_t kda_latent_chunk_workspace_bytes(int T, int num_keys, int H, int N);
  *
  * Precision: expanded keys and values are summed in 32 bits; values are
  * rounded to the tensors' type, as a prefill's are; keys come as a sum of two
- * such numbers where queries see few of them (2048 in bf16, 128 in fp16), and
+ * such numbers where queries see few of them (4096 in bf16, 512 in fp16), and
  * are rounded where they see more.  The rest as for kda_latent_fwd.
  */
 kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int page_size,
@@ -606,12 +606,9 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
  * entries free_head .. num_free of the free list.  Tables, lengths and
  * workspaces as above; a row of the table has ceil(seq_lens / page_size)
  * pages.  refs, lengths and free_head are not written: the functions give
- * them anew, and outputs may not overlap inputs.  page_size is any positive
- * number here.
+ * them anew, and outputs may not overlap inputs.  refs_out and moved are on 16
+ * bytes.  page_size is any positive number here.
  * ------------------------------------------------------------------------ */
-
-/* Bytes of device workspace kda_page_fork needs (0 on invalid sizes). */
-size_t kda_page_fork_workspace_bytes(int N);
 
 /*
  * Rows children[i] of the table go on from the tokens of rows parents[i]: full
@@ -630,13 +627,13 @@ size_t kda_page_fork_workspace_bytes(int N);
  * has: the entry is skipped.  A page outside [0, num_pages) becomes -1 in the
  * child's table, and so does an own page where the free list ends.  Each sets
  * KDA_ERR_BAD_PAGE; lengths outside the table are clipped and set it too.
- *   workspace   kda_page_fork_workspace_bytes(...) bytes
+ *   workspace   NULL, or the 256-byte status header
  */
 kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* parents,
                          const int32_t* children, const int32_t* refs, int num_pages, const int32_t* free_pages,
                          int num_free, const int32_t* free_head, int page_size, int32_t* seq_lens_out,
                          int32_t* refs_out, int32_t* free_head_out, int32_t* pairs, int N, int F, void* workspace,
-                         size_t workspace_bytes, cudaStream_t stream);
+                         cudaStream_t stream);
 
 /*
  * Copy pages within each of num_pools pools (the caches of a model's layers,
@@ -653,9 +650,6 @@ kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* s
 kda_status kda_page_copy(void* const* pools, int num_pools, int num_pages, long long page_bytes, const int32_t* pairs,
                          const int32_t* count, int F, void* workspace, cudaStream_t stream);
 
-/* Bytes of device workspace kda_page_free needs (0 on invalid sizes). */
-size_t kda_page_free_workspace_bytes(int num_pages);
-
 /*
  * Row n of the table keeps its first keep_lens[n] tokens (0: it ends; fewer
  * than it has: rejected drafts): each page behind them loses an owner, and
@@ -670,16 +664,12 @@ size_t kda_page_free_workspace_bytes(int num_pages);
  * page outside [0, num_pages), one that loses more owners than it has, a
  * length out of range (clipped), or a page that finds no room in front of
  * free_head (not listed): KDA_ERR_BAD_PAGE.
- *   workspace   kda_page_free_workspace_bytes(...) bytes
+ *   workspace   NULL, or the 256-byte status header
  */
 kda_status kda_page_free(const int32_t* block_table, int table_width, const int32_t* seq_lens,
                          const int32_t* keep_lens, const int32_t* refs, int num_pages, int32_t* free_pages,
                          int num_free, const int32_t* free_head, int page_size, int32_t* seq_lens_out,
-                         int32_t* refs_out, int32_t* free_head_out, int N, void* workspace, size_t workspace_bytes,
-                         cudaStream_t stream);
-
-/* Bytes of device workspace kda_page_compact needs (0 on invalid sizes). */
-size_t kda_page_compact_workspace_bytes(int num_pages);
+                         int32_t* refs_out, int32_t* free_head_out, int N, void* workspace, cudaStream_t stream);
 
 /*
  * The U pages that are not in the free list onto the numbers 0 .. U - 1: the
@@ -698,13 +688,12 @@ size_t kda_page_compact_workspace_bytes(int num_pages);
  * A page outside [0, num_pages) in a row's cells or in the free list, one that
  * is listed twice, a row's page that is free, or a length out of range
  * (clipped): KDA_ERR_BAD_PAGE.
- *   workspace   kda_page_compact_workspace_bytes(...) bytes
+ *   workspace   NULL, or the 256-byte status header
  */
 kda_status kda_page_compact(const int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* refs,
                             int num_pages, const int32_t* free_pages, int num_free, const int32_t* free_head,
                             int page_size, int32_t* table_out, int32_t* refs_out, int32_t* free_out, int32_t* pairs,
-                            int32_t* count, int32_t* moved, int N, void* workspace, size_t workspace_bytes,
-                            cudaStream_t stream);
+                            int32_t* count, int32_t* moved, int N, void* workspace, cudaStream_t stream);
 
 /* kda_verify_drafts: probabilities are fp32 instead of bf16 or fp16. */
 #define KDA_FLAG_FP32 512u

@@ -29,13 +29,12 @@ def test_workspace_sizes():
     shared = 896 * 16 + 256 * 256 * 130 * 4
     rows = lambda keys, H, low: keys * H * 512 + r256(keys * 128) + low * H * 256  # noqa: E731
     assert lib.kda_latent_chunk_workspace_bytes(37, 237, 8, 1) == 256 + 3 * 256 + rows(237, 8, 237)
-    assert lib.kda_latent_chunk_workspace_bytes(1642, 16231, 16, 4) == 256 + r256(shared) + 3 * 256 + rows(16231, 16, 8192)
+    assert lib.kda_latent_chunk_workspace_bytes(1642, 16231, 16, 4) == 256 + r256(shared) + 3 * 256 + rows(16231, 16, 16231)
     assert lib.kda_latent_chunk_workspace_bytes(0, 0, 1, 1) == 256 + 3 * 256
     for bad in ((-1, 1, 1, 1), (1, -1, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0), (1, 1, 65536, 1), (1, 1, 1, 65536),
                 (1 << 30, 1, 65535, 1), (1, 1, 65535, 65535)):
         assert lib.kda_latent_chunk_workspace_bytes(*bad) == 0, bad
-    for fn in (lib.kda_page_fork_workspace_bytes, lib.kda_page_free_workspace_bytes, lib.kda_page_compact_workspace_bytes):
-        assert [fn(n) for n in (-1, 0, 1, 8, 9, 100000)] == [0, 0, 288, 288, 320, 256 + 400000]
+    assert lib.kda_latent_chunk_workspace_bytes(8, 100000, 1, 2) == 256 + 3 * 256 + rows(100000, 1, 8192)
 
 
 def test_status_string():
@@ -64,26 +63,26 @@ def test_chunk_refusals():
 def test_page_refusals():
     keep, p = host_block()
     lib = binding.load_library()
-    shared = (dict(refs=None), dict(lens=None), dict(head=None), dict(table=None), dict(refs_out=None), dict(ws=None),
-              dict(wsb=287), dict(width=-1), dict(pages=0), dict(free_n=-1), dict(free=None), dict(page=0), dict(page=-16),
+    shared = (dict(refs=None), dict(lens=None), dict(head=None), dict(table=None), dict(refs_out=None), dict(refs_out=p + 8),
+              dict(width=-1), dict(pages=0), dict(free_n=-1), dict(free=None), dict(page=0), dict(page=-16),
               dict(N=0), dict(ws=p + 16), dict(table=p + 2), dict(lens=p + 1), dict(refs=p + 2), dict(free=p + 2),
               dict(head=p + 2), dict(refs_out=p + 2))
     fork = caller(lib.kda_page_fork, dict(
         table=p, width=2, lens=p, parents=p, children=p, refs=p, pages=4, free=p, free_n=4, head=p, page=16, lens_out=p,
-        refs_out=p, head_out=p, pairs=p, N=2, F=1, ws=p, wsb=4096, stream=None))
+        refs_out=p, head_out=p, pairs=p, N=2, F=1, ws=p, stream=None))
     for kw in shared + (dict(parents=None), dict(children=None), dict(pairs=None), dict(lens_out=None), dict(head_out=None),
                         dict(F=-1), dict(parents=p + 2), dict(pairs=p + 2)):
         assert fork(**kw) == 1, kw
     free = caller(lib.kda_page_free, dict(
         table=p, width=2, lens=p, keep=p, refs=p, pages=4, free=p, free_n=4, head=p, page=16, lens_out=p, refs_out=p,
-        head_out=p, N=2, ws=p, wsb=4096, stream=None))
+        head_out=p, N=2, ws=p, stream=None))
     for kw in shared + (dict(keep=None), dict(lens_out=None), dict(head_out=None), dict(keep=p + 2)):
         assert free(**kw) == 1, kw
     compact = caller(lib.kda_page_compact, dict(
         table=p, width=2, lens=p, refs=p, pages=4, free=p, free_n=4, head=p, page=16, table_out=p, refs_out=p, free_out=p,
-        pairs=p, count=p, moved=p, N=2, ws=p, wsb=4096, stream=None))
+        pairs=p, count=p, moved=p, N=2, ws=p, stream=None))
     for kw in shared + (dict(table_out=None), dict(free_out=None), dict(pairs=None), dict(count=None), dict(moved=None),
-                        dict(moved=p + 2), dict(table_out=p + 1)):
+                        dict(moved=p + 4), dict(table_out=p + 1)):
         assert compact(**kw) == 1, kw
     at = (ctypes.c_void_p * 2)(p, p)
     copy = caller(lib.kda_page_copy, dict(pools=at, n=2, pages=4, bytes=32, pairs=p, count=None, F=1, ws=None, stream=None))

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
 U = {BF: 2.0 ** -8, FP: 2.0 ** -11}
 TINY = {BF: 0.0, FP: 2.0 ** -25}
-FEW = {BF: 2048, FP: 128}
+FEW = {BF: 4096, FP: 512}
 
 
 def latent():
@@ -96,11 +96,11 @@ CHUNKS = [
     ([256, 1, 2], [257, 385, 1000], 17, 192, FP),            # pages of one and a half tiles
     ([7, 300], [9000, 310], 2, 64, BF),                      # keys shared by CTAs of the device's choice
     ([20], [4100], 2, 32, FP),                               # and of the host's
-    ([700, 3], [2500, 2048], 2, 64, BF),                     # around the border of few keys: pairs of tiles on either side,
-    ([300, 260, 2], [2049, 2049, 2050], 1, 16, BF),
-    ([300, 200], [300, 129], 2, 64, FP),
+    ([700, 3], [4500, 4096], 2, 64, BF),                     # around the border of few keys: pairs of tiles on either side,
+    ([300, 260, 2], [4097, 4097, 4098], 1, 16, BF),
+    ([700, 200], [1200, 513], 2, 64, FP),
     ([600] * 8 + [40], [900] * 8 + [2000], 6, 64, BF),       # two numbers a key with CTAs that share keys,
-    ([2048], [2048], 1, 64, BF), ([40], [2047], 3, 32, BF),  # and in clusters
+    ([2048], [2048], 1, 64, BF), ([40], [4000], 3, 32, BF),  # and in clusters
 ]
 
 
@@ -417,7 +417,7 @@ def test_page_free(longest, n, page, spare, group):
     table, refs, free, head = pool_state(lens, page, spare, n, group)
     keep = [0 if i % 3 == 0 else l if i % 3 == 1 else l * (i % 7) // 7 for i, l in enumerate(lens)]
     t, f = table.cuda(), i32(free)
-    ws = torch.full((pages().page_free_workspace_bytes(len(refs)),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
     for _ in range(2):                                   # the inputs but for the listed pages stay as they are
         got = pages().page_free(t, i32(lens), i32(keep), i32(refs), f, i32([head]), page, workspace=ws)
         wl, wr, wf, wh = sv.page_free(table, lens, keep, refs, free, head, page)
