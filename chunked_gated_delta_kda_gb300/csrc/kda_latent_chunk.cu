@@ -9,15 +9,18 @@
 // new tokens a sequence on (where fewer are usual, kda_latent_decode serves).
 //
 // The expansion is a matrix product whose first operand is gathered page by
-// page:  [k_jh | v_jh] = W_h c_j,  128 rows j a tile, 256 columns a head, 512
-// channels.  All (tile, head) items form one line, heads inside a tile, cut
-// into equal ranges, one a CTA; a tile's rows stay in shared memory for all
-// heads of it that the CTA has.
+// page:  [k_jh | v_jh] = W_h c_j,  512 channels.  A pair of SMs makes 256 rows
+// j of one head at a time, 128 rows each; all (pair of tiles, head) items form
+// one line, heads inside tiles, cut into equal ranges, one a pair.  The rows
+// stay in shared memory for all heads of the range, and of W_h each SM loads
+// and reads half: with a whole W_h in every SM its loads (32 KiB for 512 cycles
+// of products) took as long as the L2 let them, 206 us beside ** at 65536 rows
+// and 16 heads.
 //   warps 0-3  the product's rows out of tensor memory, rounded, to the
 //              workspace (two accumulators of 256 columns take turns)
-//   warp 4     issues the products
-//   warp 5     loads: a tile's rows (eight slabs of 64 channels), and W_h in
-//              slabs of 64 channels through a ring
+//   warp 4     the first SM's issues the products of both
+//   warp 5     loads: a tile's rows (eight slabs of 64 channels), and half of
+//              W_h in slabs of 64 channels through a ring
 #include <cmath>
 #include <cstdint>
 
@@ -125,18 +128,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_chunk_plan_kernel(const _
 
 // ---- the expansion ----
 constexpr int EX_THREADS = 192;
-constexpr uint32_t A_SLAB = LAT_TILE * 128;              // 128 rows x 64 channels
-constexpr uint32_t B_SLAB = LAT_KV * 128;                // 256 columns x 64 channels
+constexpr uint32_t EX_SLAB = LAT_TILE * 128;             // 128 rows or columns x 64 channels
 constexpr uint32_t SLABS = LAT_C / 64;
-constexpr uint32_t EX_RING = 3;
+constexpr uint32_t EX_RING = 5;
 constexpr uint32_t X_A = 0;
-constexpr uint32_t X_B = X_A + SLABS * A_SLAB;
-constexpr uint32_t X_AFULL = X_B + EX_RING * B_SLAB;     // [8]
+constexpr uint32_t X_B = X_A + SLABS * EX_SLAB;
+constexpr uint32_t X_AFULL = X_B + EX_RING * EX_SLAB;    // [8] both SMs' slabs have landed (in the first SM)
 constexpr uint32_t X_AEMPTY = X_AFULL + 8 * SLABS;
-constexpr uint32_t X_BFULL = X_AEMPTY + 8;               // [3]
-constexpr uint32_t X_BEMPTY = X_BFULL + 8 * EX_RING;     // [3]
+constexpr uint32_t X_BFULL = X_AEMPTY + 8;               // [5] (in the first SM)
+constexpr uint32_t X_BEMPTY = X_BFULL + 8 * EX_RING;     // [5]
 constexpr uint32_t X_DFULL = X_BEMPTY + 8 * EX_RING;     // [2]
-constexpr uint32_t X_DEMPTY = X_DFULL + 16;              // [2]
+constexpr uint32_t X_DEMPTY = X_DFULL + 16;              // [2] (in the first SM)
 constexpr uint32_t X_DRAIN = X_DEMPTY + 16;
 constexpr uint32_t X_TMEM = X_DRAIN + 8;
 constexpr uint32_t X_FAILED = X_TMEM + 4;
@@ -144,11 +146,45 @@ constexpr uint32_t X_BYTES = X_FAILED + 4;
 constexpr uint32_t X_SMEM = X_BYTES + 1024;
 static_assert(X_SMEM <= 232448, "shared memory of one CTA");
 
+// ---- the two SMs of a pair ----
+// One product of 256 rows and 256 columns; rows, columns of B and results are half in each SM's memory.
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier at this place in both SMs once the products issued before are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
+        : "memory");
+}
+// A load into this SM's memory that completes on a barrier of either (a cluster address).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // A tile of the line: sequence, first row of the tile in it, its rows there.
 struct ChunkTile {
     int n, row0, rows, out0;
     int lo0, lo_rows;                            // the tile's first row in k_lo, how many of its rows are there
-    __device__ __forceinline__ void find(const ChunkParams& p, int tile) {
+    __device__ __forceinline__ void find(const ChunkParams& p, int tile, int all) {
+        n = row0 = rows = out0 = lo0 = lo_rows = 0;
+        if (tile >= all) return;                 // the second of the last pair
         int lo = 0, hi = p.N - 1;                // the last sequence whose tiles start at or before this one
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -171,17 +207,20 @@ __device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
 }
 
 template <bool FP16>
-__global__ void __launch_bounds__(EX_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
     latent_expand_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkMaps maps) {
     extern __shared__ uint8_t smem_raw[];
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;   // at the same place in both SMs
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
     volatile uint32_t* failed = reinterpret_cast<volatile uint32_t*>(smem + X_FAILED);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
     const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
-    const long long total = (long long)p.tiles[p.N] * p.H;
-    const long long first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
-    if (first >= last) return;
+    const int all_tiles = p.tiles[p.N];
+    const long long total = (long long)((all_tiles + 1) / 2) * p.H;
+    const long long pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const long long first = total * pair / pairs, last = total * (pair + 1) / pairs;
+    if (first >= last) return;                                     // both SMs alike
 
     if (tid == 32) {
         prefetch_map(&maps.cache);
@@ -196,32 +235,34 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(base + X_DFULL + 8 * i, 1);
-            mbar_init(base + X_DEMPTY + 8 * i, 4);
+            mbar_init(base + X_DEMPTY + 8 * i, 8);
         }
         mbar_init(base + X_DRAIN, 1);
         *failed = 0u;
         fence_mbar_init();
     }
     if (warp == 4) {
-        tmem_alloc(base + X_TMEM, 512);
-        tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + X_TMEM) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_barrier();                                             // both SMs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + X_TMEM);
     const int tile0 = (int)(first / p.H), h0 = (int)(first - (long long)tile0 * p.H);
+    const uint32_t lead = cluster_addr(base, 0);                   // the first SM's memory
 
     if (warp == 5) {
         const int box = min(p.page_size, 64), boxes = LAT_TILE / box;
-        const int nowhere = p.num_pages * p.page_size;   // rows from here on read as zeros
+        const int nowhere = p.num_pages * p.page_size;             // rows from here on read as zeros
         uint32_t loads = 0, tiles = 0;
         int tile = tile0, h = h0;
         bool ok = true, bad = false;
         for (long long i = first; i < last && ok; ++i) {
             if (i == first || h == 0) {
                 ChunkTile t;
-                t.find(p, tile);
+                t.find(p, 2 * tile + (int)rank, all_tiles);
                 int row = nowhere;
                 if (lane < boxes && lane * box < t.rows) {
                     const int key = t.row0 + lane * box, page = p.table[(long long)t.n * p.width + key / p.page_size];
@@ -229,11 +270,11 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
                     else bad = true;
                 }
                 if (tiles > 0 && !wait_warp(base + X_AEMPTY, (tiles - 1) & 1, limit, failed)) break;
-                if (lane < (int)SLABS) mbar_arrive_expect_tx(base + X_AFULL + 8 * lane, A_SLAB);
+                if (rank == 0 && lane < (int)SLABS) mbar_arrive_expect_tx(base + X_AFULL + 8 * lane, 2 * EX_SLAB);
                 __syncwarp();
                 if (lane < boxes)
                     for (uint32_t c = 0; c < SLABS; ++c)
-                        tma_load_3d(base + X_A + c * A_SLAB + lane * box * 128, &maps.cache, 64 * c, 0, row, base + X_AFULL + 8 * c);
+                        tma_load_pair(base + X_A + c * EX_SLAB + lane * box * 128, &maps.cache, 64 * c, 0, row, lead + X_AFULL + 8 * c);
                 __syncwarp();
                 ++tiles;
             }
@@ -244,59 +285,57 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
                     break;
                 }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(base + X_BFULL + 8 * slot, B_SLAB);
-                    tma_load_3d(base + X_B + slot * B_SLAB, &maps.w, 64 * c, 0, h * LAT_KV, base + X_BFULL + 8 * slot);
+                    if (rank == 0) mbar_arrive_expect_tx(base + X_BFULL + 8 * slot, 2 * EX_SLAB);
+                    tma_load_pair(base + X_B + slot * EX_SLAB, &maps.w, 64 * c, 0, h * LAT_KV + (int)rank * LAT_TILE,
+                                  lead + X_BFULL + 8 * slot);
                 }
                 __syncwarp();
             }
             if (++h == p.H) h = 0, ++tile;
         }
-        // every copy issued here has landed before the CTA ends
-        for (uint32_t k = loads > EX_RING ? loads - EX_RING : 0; k < loads; ++k)
-            mbar_wait(base + X_BFULL + 8 * (k % EX_RING), (k / EX_RING) & 1, DRAIN_LIMIT);
-        if (tiles > 0)
-            for (uint32_t c = 0; c < SLABS; ++c) mbar_wait(base + X_AFULL + 8 * c, (tiles - 1) & 1, DRAIN_LIMIT);
         if (bad) set_status(p.status, STATUS_BAD_PAGE);
     } else if (warp == 4) {
-        const uint32_t id = idesc_f16(FP16 ? T_F16 : T_BF16, 128, 256, false, false);
-        uint32_t loads = 0, tiles = 0, item = 0;
-        int h = h0;
-        bool ok = true;
-        for (long long i = first; i < last && ok; ++i, ++item) {
-            const bool fresh = i == first || h == 0;
-            const uint32_t buf = item & 1;
-            if (fresh) ++tiles;
-            if (item >= 2 && !wait_warp(base + X_DEMPTY + 8 * buf, (item / 2 - 1) & 1, limit, failed)) break;
-            tc_fence_after();
-            for (uint32_t c = 0; c < SLABS; ++c, ++loads) {
-                const uint32_t slot = loads % EX_RING;
-                if (fresh && !wait_warp(base + X_AFULL + 8 * c, (tiles - 1) & 1, limit, failed)) ok = false;
-                if (ok && !wait_warp(base + X_BFULL + 8 * slot, (loads / EX_RING) & 1, limit, failed)) ok = false;
-                if (!ok) break;
-                const Desc a = desc_k(base + X_A + c * A_SLAB), b = desc_k(base + X_B + slot * B_SLAB);
+        if (rank == 0) {
+            const uint32_t id = idesc_f16(FP16 ? T_F16 : T_BF16, 256, 256, false, false);
+            uint32_t loads = 0, tiles = 0, item = 0;
+            int h = h0;
+            bool ok = true;
+            for (long long i = first; i < last && ok; ++i, ++item) {
+                const bool fresh = i == first || h == 0;
+                const uint32_t buf = item & 1;
+                if (fresh) ++tiles;
+                if (item >= 2 && !wait_warp(base + X_DEMPTY + 8 * buf, (item / 2 - 1) & 1, limit, failed)) break;
+                tc_fence_after();
+                for (uint32_t c = 0; c < SLABS; ++c, ++loads) {
+                    const uint32_t slot = loads % EX_RING;
+                    if (fresh && !wait_warp(base + X_AFULL + 8 * c, (tiles - 1) & 1, limit, failed)) ok = false;
+                    if (ok && !wait_warp(base + X_BFULL + 8 * slot, (loads / EX_RING) & 1, limit, failed)) ok = false;
+                    if (!ok) break;
+                    const Desc a = desc_k(base + X_A + c * EX_SLAB), b = desc_k(base + X_B + slot * EX_SLAB);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_ss(tmem + 256 * buf, a + 2 * ks, b + 2 * ks, id, c + ks > 0);
-                mma_commit_warp(base + X_BEMPTY + 8 * slot);
+                    for (int ks = 0; ks < 4; ++ks) mma_pair(tmem + 256 * buf, a + 2 * ks, b + 2 * ks, id, c + ks > 0);
+                    commit_pair(base + X_BEMPTY + 8 * slot);
+                }
+                if (!ok) break;
+                commit_pair(base + X_DFULL + 8 * buf);
+                if (++h == p.H) {
+                    h = 0;
+                    commit_pair(base + X_AEMPTY);
+                }
             }
-            if (!ok) break;
-            mma_commit_warp(base + X_DFULL + 8 * buf);
-            if (++h == p.H) {
-                h = 0;
-                mma_commit_warp(base + X_AEMPTY);
-            }
+            commit_pair(base + X_DRAIN);
         }
-        // every product issued here is done before the tensor memory is freed
-        mma_commit_warp(base + X_DRAIN);
+        // every product is done, and has been signalled, before the tensor and shared memory go
         mbar_wait(base + X_DRAIN, 0, DRAIN_LIMIT);
     } else {
-        const uint32_t at = tmem + ((uint32_t)warp << 21);   // this warp's lanes
+        const uint32_t at = tmem + ((uint32_t)warp << 21);         // this warp's lanes
         const int r = warp * 32 + lane;
         ChunkTile t;
         int tile = tile0, h = h0;
         uint32_t item = 0;
         for (long long i = first; i < last; ++i, ++item) {
-            if (i == first || h == 0) t.find(p, tile);
-            if (h == 0 && r < t.rows) {                      // the positional channels, once for all heads
+            if (i == first || h == 0) t.find(p, 2 * tile + (int)rank, all_tiles);
+            if (h == 0 && r < t.rows) {                            // the positional channels, once for all heads
                 const int key = t.row0 + r, page = p.table[(long long)t.n * p.width + key / p.page_size];
                 const bool there = page >= 0 && page < p.num_pages;
                 const uint4* from = reinterpret_cast<const uint4*>(
@@ -318,7 +357,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
                 if (b == LAT_KV / 32 - 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(base + X_DEMPTY + 8 * buf);
+                    if (lane == 0) arrive_cluster(lead + X_DEMPTY + 8 * buf);
                 }
                 if (r < t.rows) {
 #pragma unroll
@@ -327,7 +366,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = pack2<FP16>(x[e + 2 * k], x[e + 2 * k + 1]);
                         store32(out + 64 * b + 2 * e, w);
-                        if (b < LAT_N / 32 && r < t.lo_rows) {       // what the keys lose in rounding
+                        if (b < LAT_N / 32 && r < t.lo_rows) {     // what the keys lose in rounding
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 const float2 hi = unpack2<FP16>(w[k]);
@@ -343,7 +382,12 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) tmem_dealloc(tmem, 512);
+    // The products have waited for every copy, unless a role has given up: copies in flight then get 100 us to land.
+    if (*failed)
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
+    cluster_barrier();                                             // neither SM is used by the other any more
+    tc_fence_after();
+    if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
 }
 
@@ -434,12 +478,12 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
     if (num_keys > 0) {
         ChunkMaps maps;
         if (!latent_row_map(&maps.cache, cache, LAT_ROW, 1, (long long)num_pages * page_size, LAT_ROW, page_size < 64 ? page_size : 64) ||
-            !latent_row_map(&maps.w, w_up, LAT_C, 1, (long long)H * LAT_KV, LAT_C, LAT_KV))
+            !latent_row_map(&maps.w, w_up, LAT_C, 1, (long long)H * LAT_KV, LAT_C, LAT_TILE))
             return KDA_ERR_CUDA;
         const auto kernel = fp16 ? latent_expand_kernel<true> : latent_expand_kernel<false>;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X_SMEM) != cudaSuccess) return KDA_ERR_CUDA;
-        const long long items = ((long long)num_keys / LAT_TILE + N) * H;
-        kernel<<<(unsigned)(items < 152 ? items : 152), EX_THREADS, X_SMEM, stream>>>(c, maps);
+        const long long items = (((long long)num_keys / LAT_TILE + N + 1) / 2) * H;
+        kernel<<<2u * (unsigned)(items < 76 ? items : 76), EX_THREADS, X_SMEM, stream>>>(c, maps);
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
     return launch_latent_fwd(p, fp16, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
