@@ -16,10 +16,10 @@
 // and reads half: with a whole W_h in every SM its loads (32 KiB for 512 cycles
 // of products) took as long as the L2 let them, 206 us beside ** at 65536 rows
 // and 16 heads.
-//   warps 0-3  the product's rows out of tensor memory, rounded, to the
+//   warps 0-7  the product's rows out of tensor memory, rounded, to the
 //              workspace (two accumulators of 256 columns take turns)
-//   warp 4     the first SM's issues the products of both
-//   warp 5     loads: a tile's rows (eight slabs of 64 channels), and half of
+//   warp 8     the first SM's issues the products of both
+//   warp 9     loads: a tile's rows (eight slabs of 64 channels), and half of
 //              W_h in slabs of 64 channels through a ring
 #include <cmath>
 #include <cstdint>
@@ -127,16 +127,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_chunk_plan_kernel(const _
 }
 
 // ---- the expansion ----
-constexpr int EX_THREADS = 192;
+constexpr int EX_THREADS = 320;
 constexpr uint32_t EX_SLAB = LAT_TILE * 128;             // 128 rows or columns x 64 channels
 constexpr uint32_t SLABS = LAT_C / 64;
-constexpr uint32_t EX_RING = 5;
+constexpr uint32_t EX_RING = 4;
 constexpr uint32_t X_A = 0;
 constexpr uint32_t X_B = X_A + SLABS * EX_SLAB;
-constexpr uint32_t X_AFULL = X_B + EX_RING * EX_SLAB;    // [8] both SMs' slabs have landed (in the first SM)
+constexpr uint32_t X_STAGE = X_B + EX_RING * EX_SLAB;    // [8 warps] 32 rows x 64 columns
+constexpr uint32_t X_AFULL = X_STAGE + 8 * 4096;         // [8] both SMs' slabs have landed (in the first SM)
 constexpr uint32_t X_AEMPTY = X_AFULL + 8 * SLABS;
-constexpr uint32_t X_BFULL = X_AEMPTY + 8;               // [5] (in the first SM)
-constexpr uint32_t X_BEMPTY = X_BFULL + 8 * EX_RING;     // [5]
+constexpr uint32_t X_BFULL = X_AEMPTY + 8;               // [4] (in the first SM)
+constexpr uint32_t X_BEMPTY = X_BFULL + 8 * EX_RING;     // [4]
 constexpr uint32_t X_DFULL = X_BEMPTY + 8 * EX_RING;     // [2]
 constexpr uint32_t X_DEMPTY = X_DFULL + 16;              // [2] (in the first SM)
 constexpr uint32_t X_DRAIN = X_DEMPTY + 16;
@@ -200,10 +201,22 @@ struct ChunkTile {
     }
 };
 
-__device__ __forceinline__ void store32(void* to, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+// A warp's 32 rows of 64 16-bit columns (two in a word) to rows `stride` bytes
+// apart, the first `rows` of them.  A thread has a row, and rows written from
+// there are 32 lines an instruction: they go through 4 KiB of shared memory, a
+// row's 16-byte pieces swizzled by the row, and leave as whole 128-byte lines.
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&w)[32], uint8_t* out, long long stride, int rows, int lane) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + (lane >> 3), c = lane & 7;
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) * 16));
+        if (row < rows) *reinterpret_cast<uint4*>(out + row * stride + c * 16) = x;
+    }
+    __syncwarp();
 }
 
 template <bool FP16>
@@ -235,13 +248,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(base + X_DFULL + 8 * i, 1);
-            mbar_init(base + X_DEMPTY + 8 * i, 8);
+            mbar_init(base + X_DEMPTY + 8 * i, 16);
         }
         mbar_init(base + X_DRAIN, 1);
         *failed = 0u;
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + X_TMEM) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -253,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
     const int tile0 = (int)(first / p.H), h0 = (int)(first - (long long)tile0 * p.H);
     const uint32_t lead = cluster_addr(base, 0);                   // the first SM's memory
 
-    if (warp == 5) {
+    if (warp == 9) {
         const int box = min(p.page_size, 64), boxes = LAT_TILE / box;
         const int nowhere = p.num_pages * p.page_size;             // rows from here on read as zeros
         uint32_t loads = 0, tiles = 0;
@@ -294,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
             if (++h == p.H) h = 0, ++tile;
         }
         if (bad) set_status(p.status, STATUS_BAD_PAGE);
-    } else if (warp == 4) {
+    } else if (warp == 8) {
         if (rank == 0) {
             const uint32_t id = idesc_f16(FP16 ? T_F16 : T_BF16, 256, 256, false, false);
             uint32_t loads = 0, tiles = 0, item = 0;
@@ -328,14 +341,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
         // every product is done, and has been signalled, before the tensor and shared memory go
         mbar_wait(base + X_DRAIN, 0, DRAIN_LIMIT);
     } else {
-        const uint32_t at = tmem + ((uint32_t)warp << 21);         // this warp's lanes
-        const int r = warp * 32 + lane;
+        const int quarter = warp & 3, half = warp >> 2, r0 = quarter * 32, r = r0 + lane;
+        const uint32_t at = tmem + ((uint32_t)quarter << 21);      // this warp's lanes
+        uint8_t* stage = smem + X_STAGE + warp * 4096;
+        const long long stride = (long long)p.H * (LAT_KV * 2), stride_lo = (long long)p.H * (LAT_N * 2);
         ChunkTile t;
         int tile = tile0, h = h0;
         uint32_t item = 0;
         for (long long i = first; i < last; ++i, ++item) {
             if (i == first || h == 0) t.find(p, 2 * tile + (int)rank, all_tiles);
-            if (h == 0 && r < t.rows) {                            // the positional channels, once for all heads
+            if (h == 0 && half == 0 && r < t.rows) {               // the positional channels, once for all heads
                 const int key = t.row0 + r, page = p.table[(long long)t.n * p.width + key / p.page_size];
                 const bool there = page >= 0 && page < p.num_pages;
                 const uint4* from = reinterpret_cast<const uint4*>(
@@ -347,34 +362,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
             const uint32_t buf = item & 1;
             if (!wait_warp(base + X_DFULL + 8 * buf, (item / 2) & 1, limit, failed)) break;
             tc_fence_after();
-            uint8_t* out = static_cast<uint8_t*>(p.kv) + (((long long)t.out0 + r) * p.H + h) * (LAT_KV * 2);
-            uint8_t* out_lo = static_cast<uint8_t*>(p.k_lo) + (((long long)t.lo0 + r) * p.H + h) * (LAT_N * 2);
+            uint8_t* out = static_cast<uint8_t*>(p.kv) + (t.out0 + r0) * stride + h * (LAT_KV * 2);
+            uint8_t* out_lo = static_cast<uint8_t*>(p.k_lo) + (t.lo0 + r0) * stride_lo + h * (LAT_N * 2);
 #pragma unroll
-            for (int b = 0; b < LAT_KV / 32; ++b) {
-                float x[32];
-                tmem_ld32(at + 256 * buf + 32 * b, x);
+            for (int k = 0; k < 2; ++k) {                          // 64 columns of the key, 64 of the value
+                const int b = half + 2 * k;
+                float x[2][32];
+                uint32_t w[32];
+                tmem_ld32(at + 256 * buf + 64 * b, x[0]);
+                tmem_ld32(at + 256 * buf + 64 * b + 32, x[1]);
                 tmem_ld_wait();
-                if (b == LAT_KV / 32 - 1) {
+                if (k == 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_cluster(lead + X_DEMPTY + 8 * buf);
                 }
-                if (r < t.rows) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 16) {
-                        uint32_t w[8];
+                for (int e = 0; e < 32; ++e) w[e] = pack2<FP16>(x[e >> 4][2 * e & 31], x[e >> 4][(2 * e & 31) + 1]);
+                store_rows(stage, w, out + 128 * b, stride, t.rows - r0, lane);
+                if (k == 0 && t.lo_rows > r0) {                    // what the keys lose in rounding
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) w[k] = pack2<FP16>(x[e + 2 * k], x[e + 2 * k + 1]);
-                        store32(out + 64 * b + 2 * e, w);
-                        if (b < LAT_N / 32 && r < t.lo_rows) {     // what the keys lose in rounding
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float2 hi = unpack2<FP16>(w[k]);
-                                w[k] = pack2<FP16>(x[e + 2 * k] - hi.x, x[e + 2 * k + 1] - hi.y);
-                            }
-                            store32(out_lo + 64 * b + 2 * e, w);
-                        }
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 hi = unpack2<FP16>(w[e]);
+                        w[e] = pack2<FP16>(x[e >> 4][2 * e & 31] - hi.x, x[e >> 4][(2 * e & 31) + 1] - hi.y);
                     }
+                    store_rows(stage, w, out_lo + 128 * b, stride_lo, t.lo_rows - r0, lane);
                 }
             }
             if (++h == p.H) h = 0, ++tile;
@@ -387,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
         for (int i = 0; i < 100; ++i) __nanosleep(1000);
     cluster_barrier();                                             // neither SM is used by the other any more
     tc_fence_after();
-    if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     if (tid == 0 && *failed) set_status(p.status, STATUS_TIMEOUT);
 }
 
