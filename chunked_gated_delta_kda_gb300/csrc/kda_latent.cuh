@@ -23,7 +23,7 @@ constexpr int LATENT_SHARE_ITEMS = 896;     // records of shared key ranges in t
 
 struct LatentParams {
     const void* q;          // [B*Tq, H, 192]
-    const void* kv;         // [B*Tk, H, 256]
+    const void* kv;         // [B*Tk, H, 256]; of kda_latent_chunk [H, Tk, 256]
     const void* k_pe;       // [B*Tk, 64], k_pe_stride elements apart
     long long k_pe_stride;
     const void* o;          // backward: [B*Tq, H, 128]
@@ -46,7 +46,7 @@ struct LatentParams {
     int H, N;
     int causal;
     int chunk;              // of kda_latent_chunk: offsets may end before the rows, the status word is clear already
-    const void* k_lo;       // there: [rows, H, 128] what the keys lost in rounding, sequence n's from cu_lo[n] on
+    const void* k_lo;       // there: [H, lo_rows, 128] what the keys lost in rounding, sequence n's from cu_lo[n] on
     const int32_t* cu_lo;   // [N + 1]
     long long lo_rows;
     int lo_tiles;           // used by query tiles whose keys are at most this many tiles

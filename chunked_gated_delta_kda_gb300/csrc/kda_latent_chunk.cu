@@ -42,10 +42,11 @@ struct ChunkParams {
     const int32_t* cu_q;        // [N + 1]
     int32_t* cu_k;              // [N + 1] expanded rows before each sequence
     int32_t* tiles;             // [N + 1] tiles before each sequence
-    void* kv;                   // [num_keys, H, 256]
+    void* kv;                   // [H, num_keys, 256]: a tile of a head is 64 KiB in one piece
     void* pe;                   // [num_keys, 64]
-    void* k_lo;                 // [lo_rows, H, 128]
+    void* k_lo;                 // [H, lo_rows, 128]
     int32_t* cu_lo;             // [N + 1] rows of k_lo before each sequence's
+    long long lo_rows;
     int lo_tiles;
     uint32_t* status;
     int num_pages, page_size, width, num_keys, T, H, N;
@@ -205,7 +206,7 @@ struct ChunkTile {
 // apart, the first `rows` of them.  A thread has a row, and rows written from
 // there are 32 lines an instruction: they go through 4 KiB of shared memory, a
 // row's 16-byte pieces swizzled by the row, and leave as whole 128-byte lines.
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&w)[32], uint8_t* out, long long stride, int rows, int lane) {
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&w)[32], uint8_t* out, int stride, int rows, int lane) {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
@@ -344,7 +345,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
         const int quarter = warp & 3, half = warp >> 2, r0 = quarter * 32, r = r0 + lane;
         const uint32_t at = tmem + ((uint32_t)quarter << 21);      // this warp's lanes
         uint8_t* stage = smem + X_STAGE + warp * 4096;
-        const long long stride = (long long)p.H * (LAT_KV * 2), stride_lo = (long long)p.H * (LAT_N * 2);
         ChunkTile t;
         int tile = tile0, h = h0;
         uint32_t item = 0;
@@ -362,8 +362,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
             const uint32_t buf = item & 1;
             if (!wait_warp(base + X_DFULL + 8 * buf, (item / 2) & 1, limit, failed)) break;
             tc_fence_after();
-            uint8_t* out = static_cast<uint8_t*>(p.kv) + (t.out0 + r0) * stride + h * (LAT_KV * 2);
-            uint8_t* out_lo = static_cast<uint8_t*>(p.k_lo) + (t.lo0 + r0) * stride_lo + h * (LAT_N * 2);
+            uint8_t* out = static_cast<uint8_t*>(p.kv) + ((long long)h * p.num_keys + t.out0 + r0) * (LAT_KV * 2);
+            uint8_t* out_lo = static_cast<uint8_t*>(p.k_lo) + (h * p.lo_rows + t.lo0 + r0) * (LAT_N * 2);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {                          // 64 columns of the key, 64 of the value
                 const int b = half + 2 * k;
@@ -379,14 +379,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) w[e] = pack2<FP16>(x[e >> 4][2 * e & 31], x[e >> 4][(2 * e & 31) + 1]);
-                store_rows(stage, w, out + 128 * b, stride, t.rows - r0, lane);
+                store_rows(stage, w, out + 128 * b, LAT_KV * 2, t.rows - r0, lane);
                 if (k == 0 && t.lo_rows > r0) {                    // what the keys lose in rounding
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const float2 hi = unpack2<FP16>(w[e]);
                         w[e] = pack2<FP16>(x[e >> 4][2 * e & 31] - hi.x, x[e >> 4][(2 * e & 31) + 1] - hi.y);
                     }
-                    store_rows(stage, w, out_lo + 128 * b, stride_lo, t.lo_rows - r0, lane);
+                    store_rows(stage, w, out_lo + 128 * b, LAT_N * 2, t.lo_rows - r0, lane);
                 }
             }
             if (++h == p.H) h = 0, ++tile;
@@ -468,7 +468,7 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
     ChunkParams c{};
     c.cache = cache, c.table = block_table, c.lens = seq_lens, c.cu_q = cu_seqlens_q;
     c.cu_k = reinterpret_cast<int32_t*>(ws + at.cu), c.tiles = reinterpret_cast<int32_t*>(ws + at.tiles);
-    c.cu_lo = reinterpret_cast<int32_t*>(ws + at.cu_lo), c.k_lo = ws + at.lo, c.lo_tiles = lo_tiles((flags & KDA_FLAG_FP16) != 0u);
+    c.cu_lo = reinterpret_cast<int32_t*>(ws + at.cu_lo), c.k_lo = ws + at.lo, c.lo_rows = at.lo_rows, c.lo_tiles = lo_tiles((flags & KDA_FLAG_FP16) != 0u);
     c.kv = ws + at.kv, c.pe = ws + at.pe, c.status = reinterpret_cast<uint32_t*>(ws);
     c.num_pages = num_pages, c.page_size = page_size, c.width = table_width, c.num_keys = num_keys;
     c.T = T, c.H = H, c.N = N, c.wait_limit = debug_wait_limit();

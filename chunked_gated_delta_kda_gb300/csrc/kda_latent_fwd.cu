@@ -43,11 +43,11 @@ namespace kda {
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder();
 
 bool latent_row_map(CUtensorMap* m, const void* base, int width, int heads, long long tokens, long long row_stride,
-                    int box_rows) {
+                    int box_rows, long long head_stride) {
     const PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * 2u, (cuuint64_t)row_stride * 2u};
+    const cuuint64_t strides[2] = {(cuuint64_t)(head_stride > 0 ? head_stride : width) * 2u, (cuuint64_t)row_stride * 2u};
     const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)box_rows};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
@@ -680,15 +680,17 @@ cudaError_t launch_latent_fwd(const LatentParams& p, bool fp16, cudaStream_t str
     // without keys nothing is loaded: any valid tensor does
     const void* kv = rows_k > 0 ? p.kv : p.q;
     const void* pe = rows_k > 0 ? p.k_pe : p.q;
+    const bool by_head = p.chunk && rows_k > 0;   // latent_chunk's keys and values, head after head
     if (!latent_row_map(&maps.q, p.q, LAT_QK, p.H, rows_q, (long long)p.H * LAT_QK, LAT_TILE) ||
-        !latent_row_map(&maps.kv, kv, LAT_KV, p.H, rows_k > 0 ? rows_k : 1, (long long)p.H * LAT_KV, LAT_TILE) ||
+        !latent_row_map(&maps.kv, kv, LAT_KV, p.H, rows_k > 0 ? rows_k : 1, by_head ? LAT_KV : (long long)p.H * LAT_KV, LAT_TILE,
+                        by_head ? rows_k * LAT_KV : 0) ||
         !latent_row_map(&maps.pe, pe, LAT_P, 1, rows_k > 0 ? rows_k : 1, p.k_pe_stride, LAT_TILE))
         return cudaErrorInvalidValue;
     const int slots = latent_slots(varlen, p.Tq, p.N, FWD_ROWS);
     const int ranks = cluster_of(rows_k, p.N, slots, p.H);
     if (!p.chunk) return fp16 ? launch_split<true, false>(p, maps, slots, ranks, stream) : launch_split<false, false>(p, maps, slots, ranks, stream);
     const bool some = p.lo_rows > 0;
-    if (!latent_row_map(&maps.lo, some ? p.k_lo : p.q, LAT_N, p.H, some ? p.lo_rows : 1, (long long)p.H * LAT_N, LAT_TILE))
+    if (!latent_row_map(&maps.lo, some ? p.k_lo : p.q, LAT_N, p.H, some ? p.lo_rows : 1, LAT_N, LAT_TILE, p.lo_rows * LAT_N))
         return cudaErrorInvalidValue;
     return fp16 ? launch_split<true, true>(p, maps, slots, ranks, stream) : launch_split<false, true>(p, maps, slots, ranks, stream);
 }

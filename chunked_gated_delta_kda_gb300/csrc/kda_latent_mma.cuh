@@ -202,9 +202,10 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
 }
 
 // Tensor map over packed rows: [tokens][heads][width] 16-bit elements, rows
-// `row_stride` elements apart, boxes of 64 columns of one head and `box_rows`
-// rows, 128-byte swizzled; rows past the end read as zero.
+// `row_stride` elements apart (and heads `head_stride`, width where it is 0),
+// boxes of 64 columns of one head and `box_rows` rows, 128-byte swizzled; rows
+// past the end read as zero.
 bool latent_row_map(CUtensorMap* m, const void* base, int width, int heads, long long tokens, long long row_stride,
-                    int box_rows);
+                    int box_rows, long long head_stride = 0);
 
 }  // namespace kda
