@@ -74,7 +74,7 @@ __device__ __forceinline__ long long threads_before(long long mine, long long& t
     __syncthreads();
     long long before = x - mine;
     total = 0;
-    for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         if (w < warp) before += sums[w];
         total += sums[w];
     }
@@ -87,8 +87,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_chunk_plan_kernel(const _
     const long long most = (long long)p.width * p.page_size;
     long long rows0 = 0, tiles0 = 0, lo0 = 0, all;
     bool bad = false, bad_cu = false;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < WS_CLEAR / 4) p.status[tid] = 0u;
-    for (int base = 0; base < p.N; base += PLAN_THREADS) {
+    for (int base = 0; base < p.N; base += blockDim.x) {
         const int n = base + tid;
         long long rows = 0, lq = 0;
         if (n < p.N) {
@@ -230,12 +231,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const uint32_t limit = p.wait_limit != 0u ? p.wait_limit : WAIT_LIMIT;
-    const int all_tiles = p.tiles[p.N];
-    const long long total = (long long)((all_tiles + 1) / 2) * p.H;
-    const long long pairs = gridDim.x / 2, pair = blockIdx.x / 2;
-    const long long first = total * pair / pairs, last = total * (pair + 1) / pairs;
-    if (first >= last) return;                                     // both SMs alike
-
     if (tid == 32) {
         prefetch_map(&maps.cache);
         prefetch_map(&maps.w);
@@ -264,6 +259,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
     cluster_barrier();                                             // both SMs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + X_TMEM);
+    // the plan; what follows this kernel may set itself up
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+    const int all_tiles = p.tiles[p.N];
+    const long long total = (long long)((all_tiles + 1) / 2) * p.H;
+    const long long pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const long long first = total * pair / pairs, last = total * (pair + 1) / pairs;   // of both SMs alike, maybe none
     const int tile0 = (int)(first / p.H), h0 = (int)(first - (long long)tile0 * p.H);
     const uint32_t lead = cluster_addr(base, 0);                   // the first SM's memory
 
@@ -483,7 +484,7 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
     p.k_lo = c.k_lo, p.cu_lo = c.cu_lo, p.lo_rows = at.lo_rows, p.lo_tiles = c.lo_tiles;
     p.Tq = T, p.Tk = num_keys, p.H = H, p.N = N, p.causal = 1, p.chunk = 1, p.wait_limit = debug_wait_limit();
 
-    latent_chunk_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(c);
+    latent_chunk_plan_kernel<<<1, (unsigned)(N < PLAN_THREADS ? (N + 31) / 32 * 32 : PLAN_THREADS), 0, stream>>>(c);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     if (T == 0) return KDA_OK;
     const bool fp16 = (flags & KDA_FLAG_FP16) != 0u;
@@ -495,8 +496,17 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
         const auto kernel = fp16 ? latent_expand_kernel<true> : latent_expand_kernel<false>;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X_SMEM) != cudaSuccess) return KDA_ERR_CUDA;
         const long long items = (((long long)num_keys / LAT_TILE + N + 1) / 2) * H;
-        kernel<<<2u * (unsigned)(items < 76 ? items : 76), EX_THREADS, X_SMEM, stream>>>(c, maps);
-        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up beside the plan
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2u * (unsigned)(items < 76 ? items : 76));
+        cfg.blockDim = dim3(EX_THREADS);
+        cfg.dynamicSmemBytes = X_SMEM;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, kernel, c, maps) != cudaSuccess) return KDA_ERR_CUDA;
     }
     return launch_latent_fwd(p, fp16, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

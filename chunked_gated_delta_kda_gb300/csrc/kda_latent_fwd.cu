@@ -126,20 +126,24 @@ __device__ __forceinline__ void pair_tiles(const LatentParams& p, const LatentSe
 }
 
 __global__ void __launch_bounds__(SHARE_SLOTS) latent_share_kernel(const __grid_constant__ LatentParams p, int slots) {
-    __shared__ int keys[SHARE_SLOTS], counts[SHARE_SLOTS], sums[SHARE_SLOTS / 32], cu[SHARE_SLOTS + 1];
+    __shared__ int keys[SHARE_SLOTS], counts[SHARE_SLOTS], sums[SHARE_SLOTS / 32], cu[2][SHARE_SLOTS + 1];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int items = share_items(slots, p.H), pairs = share_pairs(p.H);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (t < WS_CLEAR / 4 && !p.chunk) p.status[t] = 0u;
     for (int i = t; i < items + pairs; i += SHARE_SLOTS) p.share_items[i] = make_int4(-1, -1, 0, 0);
-    for (int i = t; i <= p.N; i += SHARE_SLOTS) cu[i] = p.cu_q[i];
+    // (of kda_latent_chunk this runs beside the expansion, and cu_k is of the kernel before that: from the L2)
+    for (int i = t; i <= p.N; i += SHARE_SLOTS) cu[0][i] = __ldcg(p.cu_q + i), cu[1][i] = __ldcg(p.cu_k + i);
     __syncthreads();
-    check_offsets(p, t, SHARE_SLOTS);
+    LatentParams at_hand = p;
+    at_hand.cu_q = cu[0];
+    at_hand.cu_k = cu[1];
+    check_offsets(at_hand, t, SHARE_SLOTS);
     int n, j, steps = -1;              // -1: no such pair
     LatentSeq s;
     if (t < slots) {
-        latent_slot(cu, p.Tq, p.N, t, FWD_ROWS, n, j);
-        if (latent_seq(p, n, s) && (long long)j * FWD_ROWS < s.lq) {
+        latent_slot(cu[0], p.Tq, p.N, t, FWD_ROWS, n, j);
+        if (latent_seq(at_hand, n, s) && (long long)j * FWD_ROWS < s.lq) {
             int nt[2];
             pair_tiles(p, s, j * FWD_ROWS, nt);
             steps = max(nt[0], nt[1]);
@@ -172,13 +176,15 @@ __global__ void __launch_bounds__(SHARE_SLOTS) latent_share_kernel(const __grid_
     keys[t] = each;
     counts[t] = steps < 0 ? 0 : ranks;
     __syncthreads();
-    if (steps < 0) return;
-    int at = 0;
-    for (int u = 0; u < slots; ++u)
-        if (keys[u] > each || (keys[u] == each && u < t)) at += counts[u];
-    for (int k = 0; k < ranks; ++k) p.share_items[at + k] = make_int4(t, k, ranks, base);
-    if (parts > 0)
-        p.share_items[items + entry] = make_int4((int)s.q0 + j * FWD_ROWS, min(FWD_ROWS, s.lq - j * FWD_ROWS), ranks, base);
+    if (steps >= 0) {
+        int at = 0;
+        for (int u = 0; u < slots; ++u)
+            if (keys[u] > each || (keys[u] == each && u < t)) at += counts[u];
+        for (int k = 0; k < ranks; ++k) p.share_items[at + k] = make_int4(t, k, ranks, base);
+        if (parts > 0)
+            p.share_items[items + entry] = make_int4((int)s.q0 + j * FWD_ROWS, min(FWD_ROWS, s.lq - j * FWD_ROWS), ranks, base);
+    }
+    if (p.chunk) asm volatile("griddepcontrol.wait;" ::: "memory");   // what waits for this kernel waits for the expansion
 }
 
 // Eight CTAs a shared pair and head, 16 channels each, a thread a row.
@@ -240,6 +246,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     LatentSeq s;
     int slot, h;
     int4 item = make_int4(0, 0, 1, 0);
+    if constexpr (CHUNK && SPLIT != SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");   // the expanded keys
     if constexpr (SPLIT == SHARED) {
         // only the records are waited for: the tensors were there before the kernel that writes them began
         asm volatile("griddepcontrol.wait;");
@@ -609,28 +616,29 @@ cudaError_t launch(const LatentParams& p, const FwdMaps& maps, int slots, int ra
     const auto kernel = latent_fwd_kernel<FP16, SPLIT, CHUNK>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F_SMEM);
     if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
     if (SPLIT == SHARED) {   // (the kernel behind it takes its records as they are)
-        latent_share_kernel<<<1, SHARE_SLOTS, 0, stream>>>(p, slots);
-        e = cudaGetLastError();
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(SHARE_SLOTS);
+        cfg.numAttrs = CHUNK ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, latent_share_kernel, p, slots);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr[1];
-    if (SPLIT == CLUSTER) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)ranks;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-    } else {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-    }
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((SPLIT == SHARED ? share_items(slots, p.H) : slots * ranks) * p.H));
     cfg.blockDim = dim3(FWD_THREADS);
     cfg.dynamicSmemBytes = F_SMEM;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = SPLIT == WHOLE ? 0 : 1;
+    const bool early = CHUNK || SPLIT == SHARED;   // set up beside the kernel before
+    cfg.attrs = early ? attr : attr + 1;
+    cfg.numAttrs = (early ? 1 : 0) + (SPLIT == CLUSTER ? 1 : 0);
     e = cudaLaunchKernelEx(&cfg, kernel, p, maps, slots);
     if (e != cudaSuccess || SPLIT != SHARED) return e;
     cfg.gridDim = dim3((unsigned)(share_pairs(p.H) * p.H), LAT_V / 16);
