@@ -137,8 +137,8 @@ constexpr uint32_t X_A = 0;
 constexpr uint32_t X_B = X_A + SLABS * EX_SLAB;
 constexpr uint32_t X_STAGE = X_B + EX_RING * EX_SLAB;    // [8 warps] 32 rows x 64 columns
 constexpr uint32_t X_AFULL = X_STAGE + 8 * 4096;         // [8] both SMs' slabs have landed (in the first SM)
-constexpr uint32_t X_AEMPTY = X_AFULL + 8 * SLABS;
-constexpr uint32_t X_BFULL = X_AEMPTY + 8;               // [4] (in the first SM)
+constexpr uint32_t X_AEMPTY = X_AFULL + 8 * SLABS;       // [8]
+constexpr uint32_t X_BFULL = X_AEMPTY + 8 * SLABS;               // [4] (in the first SM)
 constexpr uint32_t X_BEMPTY = X_BFULL + 8 * EX_RING;     // [4]
 constexpr uint32_t X_DFULL = X_BEMPTY + 8 * EX_RING;     // [2]
 constexpr uint32_t X_DEMPTY = X_DFULL + 16;              // [2] (in the first SM)
@@ -236,8 +236,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
         prefetch_map(&maps.w);
     }
     if (tid == 0) {
-        for (uint32_t i = 0; i < SLABS; ++i) mbar_init(base + X_AFULL + 8 * i, 1);
-        mbar_init(base + X_AEMPTY, 1);
+        for (uint32_t i = 0; i < SLABS; ++i) {
+            mbar_init(base + X_AFULL + 8 * i, 1);
+            mbar_init(base + X_AEMPTY + 8 * i, 1);
+        }
         for (uint32_t i = 0; i < EX_RING; ++i) {
             mbar_init(base + X_BFULL + 8 * i, 1);
             mbar_init(base + X_BEMPTY + 8 * i, 1);
@@ -275,26 +277,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
         int tile = tile0, h = h0;
         bool ok = true, bad = false;
         for (long long i = first; i < last && ok; ++i) {
-            if (i == first || h == 0) {
+            const bool fresh = i == first || h == 0;
+            int row = nowhere;
+            if (fresh) {
                 ChunkTile t;
                 t.find(p, 2 * tile + (int)rank, all_tiles);
-                int row = nowhere;
                 if (lane < boxes && lane * box < t.rows) {
                     const int key = t.row0 + lane * box, page = p.table[(long long)t.n * p.width + key / p.page_size];
                     if (page >= 0 && page < p.num_pages) row = page * p.page_size + key % p.page_size;
                     else bad = true;
                 }
-                if (tiles > 0 && !wait_warp(base + X_AEMPTY, (tiles - 1) & 1, limit, failed)) break;
-                if (rank == 0 && lane < (int)SLABS) mbar_arrive_expect_tx(base + X_AFULL + 8 * lane, 2 * EX_SLAB);
-                __syncwarp();
-                if (lane < boxes)
-                    for (uint32_t c = 0; c < SLABS; ++c)
-                        tma_load_pair(base + X_A + c * EX_SLAB + lane * box * 128, &maps.cache, 64 * c, 0, row, lead + X_AFULL + 8 * c);
-                __syncwarp();
                 ++tiles;
             }
             for (uint32_t c = 0; c < SLABS; ++c, ++loads) {
                 const uint32_t slot = loads % EX_RING;
+                if (fresh) {                                       // a slab of the tile's rows as the last head of the tile before frees it
+                    if (tiles > 1 && !wait_warp(base + X_AEMPTY + 8 * c, tiles & 1, limit, failed)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0 && lane == 0) mbar_arrive_expect_tx(base + X_AFULL + 8 * c, 2 * EX_SLAB);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_pair(base + X_A + c * EX_SLAB + lane * box * 128, &maps.cache, 64 * c, 0, row, lead + X_AFULL + 8 * c);
+                }
                 if (loads >= EX_RING && !wait_warp(base + X_BEMPTY + 8 * slot, (loads / EX_RING - 1) & 1, limit, failed)) {
                     ok = false;
                     break;
@@ -330,13 +336,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) mma_pair(tmem + 256 * buf, a + 2 * ks, b + 2 * ks, id, c + ks > 0);
                     commit_pair(base + X_BEMPTY + 8 * slot);
+                    if (h == p.H - 1) commit_pair(base + X_AEMPTY + 8 * c);
                 }
                 if (!ok) break;
                 commit_pair(base + X_DFULL + 8 * buf);
-                if (++h == p.H) {
-                    h = 0;
-                    commit_pair(base + X_AEMPTY);
-                }
+                if (++h == p.H) h = 0;
             }
             commit_pair(base + X_DRAIN);
         }
