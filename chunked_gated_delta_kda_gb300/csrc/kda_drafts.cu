@@ -10,9 +10,9 @@
 //
 // Which token it is depends on the sums' last bits, and 64-bit arithmetic runs
 // at two operations a clock and SM here, less than the rows' bytes leave time
-// for.  So r and its sums are pairs of 32-bit numbers whose rounding errors are
-// kept (Knuth's and Dekker's exact sums): some 2^-46 of the sum, 16 operations
-// an element; the warps' sums are joined in 64 bits.
+// for.  So r, its sums and the border are pairs of 32-bit numbers whose
+// rounding errors are kept (Knuth's and Dekker's exact sums), 16 operations an
+// element; sums are good to some 2^-40.
 #include <cstdint>
 
 #include "kda.h"
@@ -44,6 +44,29 @@ __device__ __forceinline__ float val(float x) { return x; }
 __device__ __forceinline__ float val(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float val(__half x) { return __half2float(x); }
 
+// A number as h + l, l what h lost in rounding.
+struct Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair pair_of(float s, float c) {      // |s| not below |c|, or s = 0
+    const float h = s + c;
+    return {h, c - (h - s)};
+}
+__device__ __forceinline__ Pair operator+(Pair x, Pair y) {
+    const float s = x.h + y.h, b = s - x.h;
+    return pair_of(s, ((x.h - (s - b)) + (y.h - b)) + (x.l + y.l));
+}
+__device__ __forceinline__ Pair operator-(Pair x, Pair y) { return x + Pair{-y.h, -y.l}; }
+__device__ __forceinline__ Pair operator*(float u, Pair x) {
+    const float p = u * x.h;
+    return pair_of(p, fmaf(u, x.h, -p) + u * x.l);
+}
+__device__ __forceinline__ bool operator>(Pair x, Pair y) { return x.h > y.h || (x.h == y.h && x.l > y.l); }
+template <typename SHFL>
+__device__ __forceinline__ Pair moved(Pair x, SHFL f) {
+    return {f(x.h), f(x.l)};
+}
+
 // A sum of non-negative numbers as s + c.
 struct Sum {
     float s = 0.f, c = 0.f;
@@ -52,7 +75,12 @@ struct Sum {
         c += ((s - (t - b)) + (h - b)) + l;
         s = t;
     }
-    __device__ __forceinline__ double value() const { return (double)s + (double)c; }
+    __device__ __forceinline__ void add(float h) {
+        const float t = s + h, b = t - s;
+        c += (s - (t - b)) + (h - b);
+        s = t;
+    }
+    __device__ __forceinline__ Pair value() const { return pair_of(s, c); }
 };
 
 // max(p - q, 0) as h + l, exactly; 0 where it is no number.
@@ -71,82 +99,118 @@ struct Row {
     const T* p;
     const T* q;
     Kind kind;
-    int but;
-    __device__ __forceinline__ void weigh(int i, float x, float y, float& h, float& l) const {
-        rest(x, kind == P_LESS_Q ? y : 0.f, h, l);
-        if (kind == P_BUT_ONE && i == but) h = l = 0.f;
-    }
+    int but;                                     // -1 where no token is left out
     __device__ __forceinline__ void at(int i, float& h, float& l) const {
-        weigh(i, val(__ldg(p + i)), kind == P_LESS_Q ? val(__ldg(q + i)) : 0.f, h, l);
+        rest(val(__ldg(p + i)), kind == P_LESS_Q ? val(__ldg(q + i)) : 0.f, h, l);
+        if (i == but) h = l = 0.f;
     }
 };
 
-// The sum of [from, to), whole warp, in every lane.  VEC: the rows start on 16
-// bytes, and so does `from`.
-template <typename T, bool VEC>
-__device__ __forceinline__ double sum_range(const Row<T>& row, int from, int to) {
-    constexpr int W = VEC ? 16 / (int)sizeof(T) : 1, BATCH = VEC ? 16 / W : 8;   // (512 elements of a warp at a time)
+// 16 bytes of elements.
+template <typename T>
+union Piece {
+    uint4 u;
+    T t[16 / sizeof(T)];
+};
+
+// 16 bytes from any element on, a lane the next ones: the aligned words that
+// they lie in, whose second half the next lane has loaded as its first.
+template <typename T>
+__device__ __forceinline__ uint4 load_any(const T* at) {
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15u);
+    const uint4* words = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)15u);
+    const uint4 x = __ldg(words);
+    if (off == 0) return x;                      // all lanes alike
+    uint4 y = x;
+    if ((threadIdx.x & 31) == 31) y = __ldg(words + 1);
+    const int from = ((threadIdx.x & 31) + 1) & 31;
+    const uint4 z = make_uint4(__shfl_sync(0xffffffffu, x.x, from), __shfl_sync(0xffffffffu, x.y, from), __shfl_sync(0xffffffffu, x.z, from),
+                               __shfl_sync(0xffffffffu, x.w, from));
+    if ((threadIdx.x & 31) != 31) y = z;
+    uint32_t w[6] = {x.x, x.y, x.z, x.w, y.x, y.y};
+    if (off & 8u) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = y.z, w[5] = y.w;
+    if (off & 4u) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+    const uint32_t bits = 8u * (off & 3u);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+}
+
+// The sum of [from, to), whole warp, in every lane.  ALIGNED: the rows start on
+// 16 bytes, and so does `from`.  LESS: of p - q (256 x 50257 in bf16 without q
+// ** us; 28 with the operations that q needs).
+template <typename T, bool ALIGNED, bool LESS>
+__device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, int V) {
+    constexpr int W = 16 / (int)sizeof(T), BATCH = 16 / W;   // 512 elements of a warp at a time
     const int lane = threadIdx.x & 31;
     Sum sum;
-    int i = from + lane * W;
-    union Piece {
-        uint4 u;
-        T t[16 / sizeof(T)];
-    };
-    for (; i + (BATCH - 1) * 32 * W + W <= to; i += BATCH * 32 * W) {
-        Piece x[BATCH], y[BATCH];
+    if (!ALIGNED && from == 0) {                 // (no word in front of the rows is read)
+        const int first = min(W, to);
+        if (lane < first) {
+            float h, l;
+            row.at(lane, h, l);
+            sum.add(h, l);
+        }
+        from = first;
+    }
+    int i = from;
+    // (nor one behind the rows)
+    for (; i + 512 <= to && (ALIGNED || i + 512 + W <= V); i += 512) {
+        Piece<T> x[BATCH], y[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            if constexpr (VEC) x[k].u = __ldg(reinterpret_cast<const uint4*>(row.p + i + k * 32 * W));
-            else x[k].t[0] = row.p[i + k * 32];
+            const T* at = row.p + i + (k * 32 + lane) * W;
+            if constexpr (ALIGNED) x[k].u = __ldg(reinterpret_cast<const uint4*>(at));
+            else x[k].u = load_any(at);
         }
-        if (row.kind == P_LESS_Q) {
+        if constexpr (LESS) {
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
-                if constexpr (VEC) y[k].u = __ldg(reinterpret_cast<const uint4*>(row.q + i + k * 32 * W));
-                else y[k].t[0] = row.q[i + k * 32];
+                const T* at = row.q + i + (k * 32 + lane) * W;
+                if constexpr (ALIGNED) y[k].u = __ldg(reinterpret_cast<const uint4*>(at));
+                else y[k].u = load_any(at);
             }
         }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                float h, l;
-                row.weigh(i + k * 32 * W + e, val(x[k].t[e]), row.kind == P_LESS_Q ? val(y[k].t[e]) : 0.f, h, l);
-                sum.add(h, l);
+                const float p = val(x[k].t[e]);
+                if constexpr (LESS) {
+                    float h, l;
+                    rest(p, val(y[k].t[e]), h, l);
+                    sum.add(h, l);
+                } else {
+                    sum.add(p > 0.f && i + (k * 32 + lane) * W + e != row.but ? p : 0.f);
+                }
             }
     }
-    for (; i < to; i += 32 * W) {
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-            if (i + e < to) {
-                float h, l;
-                row.at(i + e, h, l);
-                sum.add(h, l);
-            }
+#pragma unroll 8
+    for (i += lane; i < to; i += 32) {
+        float h, l;
+        row.at(i, h, l);
+        sum.add(h, l);
     }
-    double d = sum.value();
+    Pair d = sum.value();
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+    for (int m = 16; m > 0; m >>= 1) d = d + moved(d, [&](float x) { return __shfl_xor_sync(0xffffffffu, x, m); });
     return d;
 }
 
 // Inclusive prefix sum over the lanes.
-__device__ __forceinline__ double lanes_upto(double x) {
+__device__ __forceinline__ Pair lanes_upto(Pair x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+        const Pair y = moved(x, [&](float z) { return __shfl_up_sync(0xffffffffu, z, d); });
+        if (lane >= d) x = y + x;
     }
     return x;
 }
 
-template <typename T, bool VEC>
+template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __grid_constant__ DraftParams p) {
-    __shared__ double sums[2][DR_SEGS], parts[DR_THREADS];
-    __shared__ double bound;
-    __shared__ int taken_s, drafted_s, seg_s, best_s;
+    __shared__ Pair sums[2][DR_SEGS], parts[DR_WARPS], bound_s, total_s;
+    __shared__ int taken_s, drafted_s, seg_s, firsts[DR_WARPS], lasts[DR_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank(), n = blockIdx.x / ctas;
     const int64_t* drafts = p.drafts + (long long)n * p.S;
@@ -191,58 +255,60 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
     row.q = draft ? draft + taken * p.q_s : nullptr;
     row.kind = !drafted_s ? P_ALONE : draft ? P_LESS_Q : P_BUT_ONE;
     row.but = row.kind == P_BUT_ONE ? (int)drafts[taken] : -1;
-    const double u = uniform[p.S];
+    const float u = uniform[p.S];
 
     const int segs = ctas * DR_WARPS, mine = rank * DR_WARPS + warp;
-    double total = 0.0;
-    int round = 0;
+    Pair total;
     cluster_barrier();                           // every CTA's shared memory is there
-    for (;; ++round) {
+    for (int round = 0;; ++round) {
         const int from = min((long long)p.V, (long long)mine * p.seg), to = min((long long)p.V, (long long)from + p.seg);
-        const double d = sum_range<T, VEC>(row, from, to);
+        const Pair d = row.kind == P_LESS_Q ? sum_range<T, ALIGNED, true>(row, from, to, p.V) : sum_range<T, ALIGNED, false>(row, from, to, p.V);
         if (lane < ctas) {
             const uint32_t at = cluster_addr(smem_u32(&sums[round][mine]), lane);
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(d) : "memory");
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(d.h), "f"(d.l) : "memory");
         }
         cluster_barrier();
         if (warp == 0) {
             // the range that holds the border: the first whose sums up to it are above, else the last with weight
-            double up[DR_SEGS / 32], x[DR_SEGS / 32], all = 0.0;
+            Pair up[DR_SEGS / 32], x[DR_SEGS / 32], all = {0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < DR_SEGS / 32; ++k) {
                 const int s = 32 * k + lane;
-                x[k] = s < segs ? sums[round][s] : 0.0;
-                up[k] = lanes_upto(x[k]) + all;
-                all = __shfl_sync(0xffffffffu, up[k], 31);
+                x[k] = s < segs ? sums[round][s] : Pair{0.f, 0.f};
+                up[k] = lanes_upto(x[k]);
             }
-            const double border = u * all;
-            int seg = -1, last = -1;
-            double before = 0.0;
 #pragma unroll
             for (int k = 0; k < DR_SEGS / 32; ++k) {
-                const uint32_t above = __ballot_sync(0xffffffffu, x[k] > 0.0 && up[k] > border);
-                const uint32_t some = __ballot_sync(0xffffffffu, x[k] > 0.0);
+                up[k] = all + up[k];
+                all = moved(up[k], [&](float z) { return __shfl_sync(0xffffffffu, z, 31); });
+            }
+            const Pair border = u * all;
+            int seg = -1, last = -1;
+            Pair before = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < DR_SEGS / 32; ++k) {
+                const uint32_t above = __ballot_sync(0xffffffffu, x[k].h > 0.f && up[k] > border);
+                const uint32_t some = __ballot_sync(0xffffffffu, x[k].h > 0.f);
                 if (some) last = 32 * k + 31 - __clz(some);
                 if (seg < 0 && above) {
                     seg = 32 * k + __ffs(above) - 1;
-                    before = __shfl_sync(0xffffffffu, up[k] - x[k], __ffs(above) - 1);
+                    before = moved(up[k] - x[k], [&](float z) { return __shfl_sync(0xffffffffu, z, __ffs(above) - 1); });
                 }
             }
             if (lane == 0) {
                 seg_s = seg >= 0 ? seg : last;
-                bound = seg >= 0 ? border - before : INFINITY;
-                parts[0] = all;
-                best_s = -1;
+                bound_s = seg >= 0 ? border - before : Pair{INFINITY, 0.f};
+                total_s = all;
             }
         }
         __syncthreads();
-        total = parts[0];
-        if (total > 0.0 || row.kind == P_ALONE || round == 1) break;
+        total = total_s;
+        if (total.h > 0.f || row.kind == P_ALONE || round == 1) break;
         row.kind = P_ALONE;                      // p = q everywhere: p itself
+        row.but = -1;
     }
     const int seg = seg_s;
-    const bool fine = total > 0.0 && total < INFINITY && seg >= 0;
-    if (!fine) {
+    if (!(total.h > 0.f && total.h < INFINITY && seg >= 0)) {
         if (rank == 0 && tid == 0) {
             p.tokens[(long long)n * (p.S + 1) + taken] = 0;
             set_status(p.status, STATUS_BAD_TOKEN);
@@ -250,45 +316,45 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
         return;
     }
     if (seg / DR_WARPS != rank) return;
-    // this CTA's range: a thread a run of elements, then the run that holds the border
+    // this CTA's range: a thread a run of elements, then the run that holds the border, a lane an element
+    const Pair bound = bound_s;
     const int from = seg * p.seg, to = min((long long)p.V, (long long)from + p.seg);
     const int each = p.seg / DR_THREADS, a = min(to, from + tid * each), b = min(to, a + each);
     Sum sum;
+#pragma unroll 8
     for (int i = a; i < b; ++i) {
         float h, l;
         row.at(i, h, l);
         sum.add(h, l);
     }
-    const double own = sum.value(), upto = lanes_upto(own);
-    __syncthreads();                             // parts[0] has been read
+    const Pair own = sum.value(), upto = lanes_upto(own);
     if (lane == 31) parts[warp] = upto;
     __syncthreads();
-    double before = 0.0;
-    for (int w = 0; w < warp; ++w) before += parts[w];
-    const bool some = own > 0.0, above = some && before + upto > bound;
+    Pair before = {0.f, 0.f};
+    for (int w = 0; w < warp; ++w) before = before + parts[w];
     // the first run above the border, else the last with weight
+    const bool some = own.h > 0.f, above = some && before + upto > bound;
     const int first_above = __reduce_min_sync(0xffffffffu, above ? tid : DR_THREADS);
     const int last_some = __reduce_max_sync(0xffffffffu, some ? tid : -1);
-    __shared__ int firsts[DR_WARPS], lasts[DR_WARPS];
     if (lane == 0) firsts[warp] = first_above, lasts[warp] = last_some;
     __syncthreads();
-    int run = DR_THREADS, last = -1;
-    for (int w = 0; w < DR_WARPS; ++w) run = min(run, firsts[w]), last = max(last, lasts[w]);
-    const bool found = run < DR_THREADS;
-    if (!found) run = last;
-    if (tid != run) return;
-    double c = before + (upto - own);
-    int token = a;
-    for (int i = a; i < b; ++i) {
-        float h, l;
-        row.at(i, h, l);
-        if (h > 0.f) {
-            token = i;
-            c += (double)h + (double)l;
-            if (found && c > bound) break;
-        }
+    int run = __reduce_min_sync(0xffffffffu, firsts[lane & (DR_WARPS - 1)]);
+    const int last = __reduce_max_sync(0xffffffffu, lasts[lane & (DR_WARPS - 1)]);
+    if (run == DR_THREADS) run = last;
+    if (warp != run / 32) return;
+    Pair c = moved(before + (upto - own), [&](float z) { return __shfl_sync(0xffffffffu, z, run & 31); });
+    const int a0 = min(to, from + run * each), b0 = min(to, a0 + each);
+    int token = -1, latest = a0;                 // (a sum's last bits may put the border behind its run: the last with weight then)
+    for (int base = a0; base < b0 && token < 0; base += 32) {
+        float h = 0.f, l = 0.f;
+        if (base + lane < b0) row.at(base + lane, h, l);
+        const Pair up = c + lanes_upto(pair_of(h, l));
+        const uint32_t weights = __ballot_sync(0xffffffffu, h > 0.f), over = __ballot_sync(0xffffffffu, h > 0.f && up > bound);
+        if (over) token = base + __ffs(over) - 1;
+        if (weights) latest = base + 31 - __clz(weights);
+        c = moved(up, [&](float z) { return __shfl_sync(0xffffffffu, z, 31); });
     }
-    p.tokens[(long long)n * (p.S + 1) + taken] = token;
+    if (lane == 0) p.tokens[(long long)n * (p.S + 1) + taken] = token >= 0 ? token : latest;
 }
 
 template <typename T>
