@@ -75,12 +75,49 @@ struct Sum {
         c += ((s - (t - b)) + (h - b)) + l;
         s = t;
     }
-    __device__ __forceinline__ void add(float h) {
-        const float t = s + h, b = t - s;
-        c += (s - (t - b)) + (h - b);
+    __device__ __forceinline__ Pair value() const { return pair_of(s, c); }
+};
+
+// Two 32-bit numbers an operation (the sums of even and of odd elements).
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+}
+__device__ __forceinline__ float2 halves(Two x) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(x));
+    return v;
+}
+__device__ __forceinline__ Two plus(Two a, Two b) {
+    Two x;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+    return x;
+}
+__device__ __forceinline__ Two minus(Two a, Two b) {
+    Two x;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(b), "l"(0xbf800000bf800000ull), "l"(a));
+    return x;
+}
+struct TwoSums {
+    Two s = 0, c = 0;
+    __device__ __forceinline__ void add(Two h) {
+        const Two t = plus(s, h), b = minus(t, s);
+        c = plus(c, plus(minus(s, minus(t, b)), minus(h, b)));
         s = t;
     }
-    __device__ __forceinline__ Pair value() const { return pair_of(s, c); }
+    // max(p - q, 0), as rest() below
+    __device__ __forceinline__ void add_rest(Two p, Two q) {
+        const Two d = minus(p, q), b = minus(p, d);
+        const float2 h = halves(d), l = halves(plus(minus(p, plus(d, b)), minus(b, q)));
+        add(two(h.x > 0.f ? h.x : 0.f, h.y > 0.f ? h.y : 0.f));
+        c = plus(c, two(h.x > 0.f ? l.x : 0.f, h.y > 0.f ? l.y : 0.f));
+    }
+    __device__ __forceinline__ Pair value() const {
+        const float2 x = halves(s), y = halves(c);
+        return pair_of(x.x, y.x) + pair_of(x.y, y.y);
+    }
 };
 
 // max(p - q, 0) as h + l, exactly; 0 where it is no number.
@@ -143,6 +180,7 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
     constexpr int W = 16 / (int)sizeof(T), BATCH = 16 / W;   // 512 elements of a warp at a time
     const int lane = threadIdx.x & 31;
     Sum sum;
+    TwoSums sums;
     if (!ALIGNED && from == 0) {                 // (no word in front of the rows is read)
         const int first = min(W, to);
         if (lane < first) {
@@ -162,7 +200,17 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
             if constexpr (ALIGNED) x[k].u = __ldg(reinterpret_cast<const uint4*>(at));
             else x[k].u = load_any(at);
         }
-        if constexpr (LESS) {
+        if constexpr (!LESS) {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int left_out = row.but - i - (k * 32 + lane) * W;
+                if (left_out >= 0 && left_out < W) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        if (e == left_out) x[k].t[e] = T(0.f);
+                }
+            }
+        } else {
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
                 const T* at = row.q + i + (k * 32 + lane) * W;
@@ -173,15 +221,10 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const float p = val(x[k].t[e]);
-                if constexpr (LESS) {
-                    float h, l;
-                    rest(p, val(y[k].t[e]), h, l);
-                    sum.add(h, l);
-                } else {
-                    sum.add(p > 0.f && i + (k * 32 + lane) * W + e != row.but ? p : 0.f);
-                }
+            for (int e = 0; e < W; e += 2) {
+                const float a = val(x[k].t[e]), b = val(x[k].t[e + 1]);
+                if constexpr (LESS) sums.add_rest(two(a, b), two(val(y[k].t[e]), val(y[k].t[e + 1])));
+                else sums.add(two(fmaxf(a, 0.f), fmaxf(b, 0.f)));   // (0 from what is no number)
             }
     }
 #pragma unroll 8
@@ -190,7 +233,7 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
         row.at(i, h, l);
         sum.add(h, l);
     }
-    Pair d = sum.value();
+    Pair d = sum.value() + sums.value();
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) d = d + moved(d, [&](float x) { return __shfl_xor_sync(0xffffffffu, x, m); });
     return d;
