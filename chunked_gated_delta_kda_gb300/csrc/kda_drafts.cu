@@ -150,16 +150,31 @@ union Piece {
     T t[16 / sizeof(T)];
 };
 
-// 16 bytes from any element on, a lane the next ones: the aligned words that
-// they lie in, whose second half the next lane has loaded as its first.
+// A whole 16-byte word of a row [begin, end), 0 where the row is not.
 template <typename T>
-__device__ __forceinline__ uint4 load_any(const T* at) {
+__device__ __forceinline__ uint4 load_word(const uint4* word, const T* begin, const T* end) {
+    const T* at = reinterpret_cast<const T*>(word);
+    constexpr int W = 16 / (int)sizeof(T);
+    if (at >= begin && end - at >= W) return __ldg(word);
+    Piece<T> x;
+    x.u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+        if (at + e >= begin && at + e < end) x.t[e] = at[e];
+    return x.u;
+}
+
+// 16 bytes of a row from any element on, a lane the next ones: the words that
+// they lie in, whose second the next lane has loaded as its first.  EDGE: they
+// may reach past the row, where they are 0.
+template <bool EDGE, typename T>
+__device__ __forceinline__ uint4 load_any(const T* at, const T* begin, const T* end) {
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15u);
     const uint4* words = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)15u);
-    const uint4 x = __ldg(words);
+    const uint4 x = EDGE ? load_word(words, begin, end) : __ldg(words);
     if (off == 0) return x;                      // all lanes alike
     uint4 y = x;
-    if ((threadIdx.x & 31) == 31) y = __ldg(words + 1);
+    if ((threadIdx.x & 31) == 31) y = EDGE ? load_word(words + 1, begin, end) : __ldg(words + 1);
     const int from = ((threadIdx.x & 31) + 1) & 31;
     const uint4 z = make_uint4(__shfl_sync(0xffffffffu, x.x, from), __shfl_sync(0xffffffffu, x.y, from), __shfl_sync(0xffffffffu, x.z, from),
                                __shfl_sync(0xffffffffu, x.w, from));
@@ -172,35 +187,37 @@ __device__ __forceinline__ uint4 load_any(const T* at) {
                       __funnelshift_r(w[3], w[4], bits));
 }
 
-// The sum of [from, to), whole warp, in every lane.  ALIGNED: the rows start on
-// 16 bytes, and so does `from`.  LESS: of p - q (256 x 50257 in bf16 without q
-// ** us; 28 with the operations that q needs).
+template <int N>
+struct Number {
+    static constexpr int value = N;
+};
+
+// The sum of [from, to), whole warp, in every lane; `to` is where the row ends
+// or `from` and a multiple of 512.  ALIGNED: the rows start on 16 bytes.  LESS:
+// of p - q (256 x 50257 in bf16 without q ** us; 28 with the operations that q
+// needs).
 template <typename T, bool ALIGNED, bool LESS>
 __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, int V) {
-    constexpr int W = 16 / (int)sizeof(T), BATCH = 16 / W;   // 512 elements of a warp at a time
+    constexpr int W = 16 / (int)sizeof(T);
     const int lane = threadIdx.x & 31;
-    Sum sum;
     TwoSums sums;
-    if (!ALIGNED && from == 0) {                 // (no word in front of the rows is read)
-        const int first = min(W, to);
-        if (lane < first) {
-            float h, l;
-            row.at(lane, h, l);
-            sum.add(h, l);
-        }
-        from = first;
-    }
-    int i = from;
-    // (nor one behind the rows)
-    for (; i + 512 <= to && (ALIGNED || i + 512 + W <= V); i += 512) {
+    // BATCH x 32 pieces of 16 bytes from element i on
+    auto chunk = [&](auto batch, auto edge, int i) {
+        constexpr int BATCH = decltype(batch)::value;
+        constexpr bool EDGE = decltype(edge)::value != 0;
         Piece<T> x[BATCH], y[BATCH];
+        auto fetch = [&](const T* r, Piece<T>(&z)[BATCH]) {
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const T* at = row.p + i + (k * 32 + lane) * W;
-            if constexpr (ALIGNED) x[k].u = __ldg(reinterpret_cast<const uint4*>(at));
-            else x[k].u = load_any(at);
-        }
-        if constexpr (!LESS) {
+            for (int k = 0; k < BATCH; ++k) {
+                const T* at = r + i + (k * 32 + lane) * W;
+                if constexpr (ALIGNED && !EDGE) z[k].u = __ldg(reinterpret_cast<const uint4*>(at));
+                else z[k].u = load_any<EDGE>(at, r, r + V);
+            }
+        };
+        fetch(row.p, x);
+        if constexpr (LESS) {
+            fetch(row.q, y);
+        } else {
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
                 const int left_out = row.but - i - (k * 32 + lane) * W;
@@ -209,13 +226,6 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
                     for (int e = 0; e < W; ++e)
                         if (e == left_out) x[k].t[e] = T(0.f);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const T* at = row.q + i + (k * 32 + lane) * W;
-                if constexpr (ALIGNED) y[k].u = __ldg(reinterpret_cast<const uint4*>(at));
-                else y[k].u = load_any(at);
             }
         }
 #pragma unroll
@@ -226,14 +236,16 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
                 if constexpr (LESS) sums.add_rest(two(a, b), two(val(y[k].t[e]), val(y[k].t[e + 1])));
                 else sums.add(two(fmaxf(a, 0.f), fmaxf(b, 0.f)));   // (0 from what is no number)
             }
+    };
+    constexpr int MOST = W == 8 ? 4 : LESS ? 4 : 8, STEP = 32 * W * MOST;
+    int i = from;
+    if (!ALIGNED && i == 0 && to > 0) {          // the first may begin inside a word
+        chunk(Number<1>(), Number<1>(), 0);
+        i = 32 * W;
     }
-#pragma unroll 8
-    for (i += lane; i < to; i += 32) {
-        float h, l;
-        row.at(i, h, l);
-        sum.add(h, l);
-    }
-    Pair d = sum.value() + sums.value();
+    for (; i + STEP <= to && (ALIGNED || i + STEP + W <= V); i += STEP) chunk(Number<MOST>(), Number<0>(), i);
+    for (; i < to; i += 32 * W) chunk(Number<1>(), Number<1>(), i);
+    Pair d = sums.value();
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) d = d + moved(d, [&](float x) { return __shfl_xor_sync(0xffffffffu, x, m); });
     return d;
