@@ -21,9 +21,8 @@ constexpr int PG_CTAS = 8;
 constexpr int PG_THREADS = 1024;
 constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_ALL = PG_CTAS * PG_THREADS;
-constexpr int PG_PER = 8;                        // pages of a thread, in a row
-constexpr int PG_CHUNK = PG_THREADS * PG_PER;
-constexpr int PG_KEEP = 4;                       // chunks whose masks stay in registers
+constexpr int PG_SHARES = PG_CTAS * PG_WARPS;    // the cluster's warps, each with a share of the pages
+constexpr long long FREE_ALONE = 1 << 17;        // cells that the cluster gives back by itself
 
 struct PageParams {
     const int32_t* table;
@@ -55,11 +54,11 @@ __device__ __forceinline__ int row_pages(const PageParams& p, int len, bool& bad
 }
 
 template <typename FUNC>
-__device__ __forceinline__ void copy_words(const int32_t* from, int32_t* to, int count, int me, FUNC f) {
+__device__ __forceinline__ void copy_words(const int32_t* from, int32_t* to, int count, int me, FUNC f, int all = PG_ALL) {
     if (((reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to)) & 15u) == 0) {
         const int quads = count >> 2;
 #pragma unroll 4
-        for (int i = me; i < quads; i += PG_ALL) {
+        for (int i = me; i < quads; i += all) {
             const int4 x = __ldg(reinterpret_cast<const int4*>(from) + i);
             __stcg(reinterpret_cast<int4*>(to) + i, make_int4(f(x.x), f(x.y), f(x.z), f(x.w)));
         }
@@ -67,7 +66,7 @@ __device__ __forceinline__ void copy_words(const int32_t* from, int32_t* to, int
         return;
     }
 #pragma unroll 4
-    for (int i = me; i < count; i += PG_ALL) __stcg(to + i, f(__ldg(from + i)));
+    for (int i = me; i < count; i += all) __stcg(to + i, f(__ldg(from + i)));
 }
 
 __device__ __forceinline__ void fill_words(int32_t* to, int value, int count, int me) {   // on 16 bytes
@@ -92,25 +91,6 @@ __device__ __forceinline__ int block_before(int mine, int& total, int* sums) {
     return x - mine + __reduce_add_sync(0xffffffffu, lane < warp ? s : 0);
 }
 static_assert(PG_WARPS == 32, "a lane a warp's sum");
-
-// `mine` of every CTA of the cluster: the sum of those of lower rank, and of
-// all.  Has a cluster barrier; `slots` serves one call.
-__device__ __forceinline__ int cluster_before(int mine, int& total, int* slots) {
-    const uint32_t rank = cluster_rank();
-    if (threadIdx.x < PG_CTAS) {
-        const uint32_t at = cluster_addr(smem_u32(slots + rank), threadIdx.x);
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(mine) : "memory");
-    }
-    cluster_barrier();
-    int before = 0;
-    total = 0;
-    for (uint32_t r = 0; r < PG_CTAS; ++r) {
-        const int s = slots[r];
-        if (r < rank) before += s;
-        total += s;
-    }
-    return before;
-}
 
 // ---- fork: a warp an entry ----
 // While entries claim their children, lens_out holds i - F at a child of
@@ -190,85 +170,82 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
     if (bad) set_status(p.status, STATUS_BAD_PAGE);
 }
 
-// ---- a CTA's share of the pages, PG_CHUNK at a time, in the order of their numbers ----
-struct PageWalk {
-    int first, last;                             // in whole eights
-    uint32_t masks[PG_KEEP];
-    int before[PG_KEEP];                         // pages in a mask before the thread's, among the CTA's
-    int kept;                                    // and before the chunks that are not kept
-
-    __device__ __forceinline__ explicit PageWalk(int num_pages) {
-        const int each = (int)((((long long)num_pages + PG_CTAS - 1) / PG_CTAS + PG_PER - 1) / PG_PER * PG_PER);
-        first = (int)min((long long)num_pages, (long long)cluster_rank() * each);
+// ---- the pages in the order of their numbers, a share a warp ----
+struct Share {
+    int first, last;                             // in whole lines of 128 pages
+    __device__ __forceinline__ Share(int num_pages, int index) {
+        const int each = (int)((((long long)num_pages + PG_SHARES - 1) / PG_SHARES + 127) / 128 * 128);
+        first = (int)min((long long)num_pages, (long long)index * each);
         last = (int)min((long long)num_pages, (long long)first + each);
-    }
-    // mask_of(first page, pages): their mask.  Returns how many of the CTA's pages are in one.
-    template <typename MASK>
-    __device__ __forceinline__ int scan(int* sums, MASK mask_of) {
-        int running = 0, total;
-#pragma unroll
-        for (int c = 0; c < PG_KEEP; ++c) {
-            const int at = first + c * PG_CHUNK + (int)threadIdx.x * PG_PER;
-            masks[c] = 0u;
-            if (first + c * PG_CHUNK < last) {
-                if (at < last) masks[c] = mask_of(at, min(PG_PER, last - at));
-                before[c] = running + block_before(__popc(masks[c]), total, sums);
-                running += total;
-            }
-        }
-        kept = running;
-        for (int base = first + PG_KEEP * PG_CHUNK; base < last; base += PG_CHUNK) {
-            const int at = base + (int)threadIdx.x * PG_PER;
-            block_before(at < last ? __popc(mask_of(at, min(PG_PER, last - at))) : 0, total, sums);
-            running += total;
-        }
-        return running;
-    }
-    // f(first page, pages, mask, pages in a mask before the first); mask_of has to give what it gave.
-    template <typename MASK, typename FUNC>
-    __device__ __forceinline__ void each(int* sums, MASK mask_of, FUNC f) const {
-#pragma unroll
-        for (int c = 0; c < PG_KEEP; ++c) {
-            const int at = first + c * PG_CHUNK + (int)threadIdx.x * PG_PER;
-            if (at < last) f(at, min(PG_PER, last - at), masks[c], before[c]);
-        }
-        int running = kept, total;
-        for (int base = first + PG_KEEP * PG_CHUNK; base < last; base += PG_CHUNK) {
-            const int at = base + (int)threadIdx.x * PG_PER;
-            const uint32_t mask = at < last ? mask_of(at, min(PG_PER, last - at)) : 0u;
-            const int ahead = running + block_before(__popc(mask), total, sums);
-            if (at < last) f(at, min(PG_PER, last - at), mask, ahead);
-            running += total;
-        }
     }
 };
 
-// n of PG_PER words from an array on 16 bytes, `at` in whole eights; the others 0.
-__device__ __forceinline__ void load_words(const int32_t* from, int at, int n, int (&x)[PG_PER]) {
-    if (n == PG_PER) {
-        const int4 a = __ldcg(reinterpret_cast<const int4*>(from + at)), b = __ldcg(reinterpret_cast<const int4*>(from + at) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
+// Whole warp: f(first page of the lane, its four words of `from` (on 16 bytes), how many of them there are), 128 pages a time.
+template <typename FUNC>
+__device__ __forceinline__ void walk(const int32_t* from, int first, int last, FUNC f) {
+    const int lane = threadIdx.x & 31;
+    for (int base = first; base < last; base += 4 * 128) {
+        int x[4][4];
 #pragma unroll
-        for (int k = 0; k < PG_PER; ++k) x[k] = k < n ? __ldcg(from + at + k) : 0;
+        for (int u = 0; u < 4; ++u) {
+            const int at = base + 128 * u + 4 * lane;
+            if (at + 4 <= last) {
+                const int4 v = __ldcg(reinterpret_cast<const int4*>(from + at));
+                x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[u][k] = at + k < last ? __ldcg(from + at + k) : 0;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (base + 128 * u < last) {
+                const int at = base + 128 * u + 4 * lane;
+                f(at, x[u], max(0, min(4, last - at)));
+            }
     }
+}
+
+// How many of the pages that are marked (mark(word)) come before the lane's, among the warp's 128 ones; all of them in `total`.
+template <typename MARK>
+__device__ __forceinline__ int lanes_before(const int (&x)[4], int n, MARK mark, int& total) {
+    const uint32_t lower = (1u << (threadIdx.x & 31)) - 1;
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t marked = __ballot_sync(0xffffffffu, k < n && mark(x[k]));
+        before += __popc(marked & lower);
+        total += __popc(marked);
+    }
+    return before;
+}
+
+// Every warp's number to all CTAs of the cluster, and back: the sum of those of the shares before `index`, and of all
+// where index is PG_SHARES.  Between the two, a cluster barrier.
+__device__ __forceinline__ void send_count(int mine, int index, int* counts) {
+    const int lane = threadIdx.x & 31;
+    if (lane < PG_CTAS) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(smem_u32(counts + index), lane)), "r"(mine) : "memory");
+}
+__device__ __forceinline__ int shares_before(int index, const int* counts) {
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < PG_SHARES; k += 32) {
+        const int i = k + (int)(threadIdx.x & 31);
+        if (i < index) sum += counts[i];
+    }
+    return __reduce_add_sync(0xffffffffu, sum);
 }
 
 // ---- free ----
 // refs_out starts as the owners beside the first and loses one for each row
 // that gives the page back, so it is negative where the last one has.
-__global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_free_kernel(const __grid_constant__ PageParams p) {
-    __shared__ int sums[PG_WARPS], slots[PG_CTAS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster_rank(), me = rank * PG_THREADS + tid;
-    const long long head = p.free_head[0];
-    bool bad = false;
-    if (me == 0 && p.status) __stcg(p.status, 0u);
-    copy_words(p.refs, p.refs_out, p.num_pages, me, [](int x) { return max(x, 0); });
-    cluster_barrier();
-    // A warp takes up to 32 rows, a lane looks a row's lengths up; then the cells of all of them, a lane a cell.
-    const int rows = min(32, max(1, (p.N + PG_ALL / 32 - 1) / (PG_ALL / 32)));
-    for (int n0 = (rank * PG_WARPS + warp) * rows; n0 < p.N; n0 += PG_ALL / 32 * rows) {
-        const int n = n0 + lane;
+
+// A warp takes `rows` rows at a time, a lane looks a row's lengths up; then the cells of all of them, a lane a cell.
+__device__ __forceinline__ void release_rows(const PageParams& p, int warp, int warps, int rows, bool& bad) {
+    const int lane = threadIdx.x & 31;
+    for (long long n0 = (long long)warp * rows; n0 < p.N; n0 += (long long)warps * rows) {
+        const int n = (int)n0 + lane;
         int from = 0, cells = 0;
         if (lane < rows && n < p.N) {
             const int len = p.lens[n], keep = p.keep[n], kept = max(0, min(keep, len));
@@ -307,28 +284,62 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
                 }
         }
     }
-    cluster_barrier();
-    PageWalk walk(p.num_pages);
-    auto freed = [&](int at, int n) {
-        int x[PG_PER];
-        load_words(p.refs_out, at, n, x);
-        uint32_t mask = 0;
+}
+
+__device__ __forceinline__ int owners(int refs) { return max(refs, 0); }
+
+// Where many cells may be given back, the whole GPU does that, in two kernels in front of the cluster.
+__global__ void __launch_bounds__(256) page_owners_kernel(const __grid_constant__ PageParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int me = blockIdx.x * 256 + threadIdx.x;
+    if (me == 0 && p.status) *p.status = 0u;
+    copy_words(p.refs, p.refs_out, p.num_pages, me, owners, gridDim.x * 256);
+}
+__global__ void __launch_bounds__(256) page_release_kernel(const __grid_constant__ PageParams p, int rows) {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    bool bad = false;
+    release_rows(p, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, rows, bad);
+    if (bad) set_status(p.status, STATUS_BAD_PAGE);
+}
+
+template <bool ALONE>
+__global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_free_kernel(const __grid_constant__ PageParams p) {
+    __shared__ int counts[PG_SHARES];
+    const int rank = (int)cluster_rank(), me = rank * PG_THREADS + (int)threadIdx.x, index = me >> 5;
+    const long long head = p.free_head[0];
+    bool bad = false;
+    if constexpr (ALONE) {
+        if (me == 0 && p.status) __stcg(p.status, 0u);
+        copy_words(p.refs, p.refs_out, p.num_pages, me, owners);
+        cluster_barrier();
+        release_rows(p, index, PG_SHARES, min(32, max(1, (p.N + PG_SHARES - 1) / PG_SHARES)), bad);
+        cluster_barrier();
+    } else {
+        cluster_barrier();                       // the other CTAs' shared memory is there
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+    const Share share(p.num_pages, index);
+    int mine = 0;
+    walk(p.refs_out, share.first, share.last, [&](int, const int(&x)[4], int) {
 #pragma unroll
-        for (int k = 0; k < PG_PER; ++k)
-            if (x[k] < 0) mask |= 1u << k, bad |= x[k] < -1;
-        return mask;
-    };
-    const int mine = walk.scan(sums, freed);
-    int all;
-    const int before = cluster_before(mine, all, slots);
-    walk.each(sums, freed, [&](int at, int, uint32_t mask, int ahead) {
-        long long to = head - all + before + ahead;
-        for (; mask != 0u; mask &= mask - 1, ++to) {
-            const int page = at + __ffs(mask) - 1;
-            p.refs_out[page] = 0;
-            if (to >= 0 && to < p.num_free) p.free_io[to] = page;
-            else bad = true;
-        }
+        for (int k = 0; k < 4; ++k) mine += x[k] < 0, bad |= x[k] < -1;
+    });
+    send_count(__reduce_add_sync(0xffffffffu, mine), index, counts);
+    cluster_barrier();
+    const int all = shares_before(PG_SHARES, counts);
+    long long to = head - all + shares_before(index, counts);
+    walk(p.refs_out, share.first, share.last, [&](int at, const int(&x)[4], int n) {
+        int total;
+        long long place = to + lanes_before(x, n, [](int v) { return v < 0; }, total);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (x[k] < 0) {
+                p.refs_out[at + k] = 0;
+                if (place >= 0 && place < p.num_free) p.free_io[place] = at + k;
+                else bad = true;
+                ++place;
+            }
+        to += total;
     });
     if (me == 0) p.head_out[0] = (int)max(0ll, head - all);
     if (bad) set_status(p.status, STATUS_BAD_PAGE);
@@ -337,68 +348,69 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
 // ---- compact ----
 // `moved` marks the free pages until it is written.
 __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_compact_kernel(const __grid_constant__ PageParams p) {
-    __shared__ int sums[PG_WARPS], slots[2][PG_CTAS];
-    const int rank = (int)cluster_rank(), me = rank * PG_THREADS + (int)threadIdx.x;
+    __shared__ int counts[PG_SHARES], sums[PG_WARPS];
+    const int rank = (int)cluster_rank(), me = rank * PG_THREADS + (int)threadIdx.x, index = me >> 5, warp = (int)threadIdx.x >> 5;
     const long long head = p.free_head[0];
     bool bad = false;
     if (me == 0 && p.status) __stcg(p.status, 0u);
     fill_words(p.moved, 0, p.num_pages, me);
     cluster_barrier();
+#pragma unroll 4
     for (long long i = max(head, 0ll) + me; i < p.num_free; i += PG_ALL) {
         const int page = p.free_pages[i];
         if (page < 0 || page >= p.num_pages || atomicExch(p.moved + page, 1) != 0) bad = true;
     }
     cluster_barrier();
-    PageWalk walk(p.num_pages);
-    auto is_free = [&](int at, int n) {
-        int x[PG_PER];
-        load_words(p.moved, at, n, x);
-        uint32_t mask = 0;
+    auto is_free = [](int v) { return v != 0; };
+    const Share share(p.num_pages, index);
+    auto count = [&](int first, int last) {
+        int mine = 0;
+        walk(p.moved, first, last, [&](int, const int(&x)[4], int) {
 #pragma unroll
-        for (int k = 0; k < PG_PER; ++k)
-            if (x[k] != 0) mask |= 1u << k;
-        return mask;
-    };
-    int all, holes, total;
-    const int mine = walk.scan(sums, is_free), before = cluster_before(mine, all, slots[0]), used = p.num_pages - all;
-    int below = 0;                               // free pages below `used`
-    walk.each(sums, is_free, [&](int at, int n, uint32_t mask, int) {
-        below += __popc(mask & (used - at >= PG_PER ? 0xffu : used > at ? (1u << (used - at)) - 1 : 0u));
-    });
-    block_before(below, total, sums);
-    cluster_before(total, holes, slots[1]);
-    // the k-th free page below `used` takes the k-th used one from there on
-    auto place = [&](auto f) {
-        walk.each(sums, is_free, [&](int at, int n, uint32_t mask, int ahead) {
-            int free_before = before + ahead;
-#pragma unroll
-            for (int k = 0; k < PG_PER; ++k)
-                if (k < n) {
-                    const int i = at + k;
-                    const bool hole = (mask >> k) & 1u;
-                    f(i, hole, hole ? free_before : (i - used) - (free_before - holes));
-                    free_before += hole;
-                }
+            for (int k = 0; k < 4; ++k) mine += x[k] != 0;
         });
+        return __reduce_add_sync(0xffffffffu, mine);
     };
-    place([&](int i, bool hole, int k) {
-        if (hole == (i < used)) __stcg(p.pairs + 2ll * k + (hole ? 1 : 0), i);
+    send_count(count(share.first, share.last), index, counts);
+    cluster_barrier();
+    const int used = p.num_pages - shares_before(PG_SHARES, counts);
+    // free pages below `used`: those of the shares before the one that it is in, and of that up to there (a part a warp)
+    const int each = max(128, Share(p.num_pages, 0).last), cut = min(PG_SHARES, used / each);
+    const int part = (each / 128 + PG_WARPS - 1) / PG_WARPS * 128, first = min(used, cut * each + warp * part);
+    const int some = count(first, min(used, first + part));
+    if ((threadIdx.x & 31) == 0) sums[warp] = some;
+    cluster_barrier();                           // (the marks are read for the last time but by their own share's warp)
+    const int holes = shares_before(cut, counts) + __reduce_add_sync(0xffffffffu, sums[threadIdx.x & 31]);
+    // The k-th free page below `used` takes the k-th used one from there on; `ahead`: free pages before the lane's.
+    int ahead = shares_before(index, counts);
+    walk(p.moved, share.first, share.last, [&](int at, const int(&x)[4], int n) {
+        int total, before = ahead + lanes_before(x, n, is_free, total);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < n) {
+                const int i = at + k;
+                const bool hole = x[k] != 0, below = i < used;
+                if (hole && below) p.pairs[2ll * before + 1] = i;
+                if (!hole && !below) p.pairs[2ll * ((i - used) - (before - holes))] = i;
+                if (hole || below) __stcg(p.moved + i, hole ? -1 : i);
+                if (!below) __stcg(p.refs_out + i, 0);
+                else if (!hole) p.refs_out[i] = __ldg(p.refs + i);
+                before += hole;
+            }
+        ahead += total;
     });
     for (int i = 2 * holes + me; i < p.num_pages / 2 * 2; i += PG_ALL) p.pairs[i] = -1;
-    cluster_barrier();
-    place([&](int i, bool hole, int k) {
-        int to = i;
-        if (hole) to = -1;
-        else if (i >= used) to = __ldcg(p.pairs + 2ll * k + 1);
-        p.moved[i] = to;
-        if (to >= 0) p.refs_out[to] = __ldg(p.refs + i);
-        if (i >= used) p.refs_out[i] = 0;
-    });
     for (int i = me; i < p.num_free; i += PG_ALL) {
         const long long to = used + (i - head);
         p.free_out[i] = i < head ? p.free_pages[i] : to < p.num_pages ? (int)to : -1;
     }
     if (me == 0) p.count[0] = holes;
+    cluster_barrier();
+    for (int k = me; k < holes; k += PG_ALL) {
+        const int src = __ldcg(p.pairs + 2ll * k), dst = __ldcg(p.pairs + 2ll * k + 1);
+        p.moved[src] = dst;
+        p.refs_out[dst] = __ldg(p.refs + src);
+    }
     if (bad) set_status(p.status, STATUS_BAD_PAGE);
 }
 
@@ -546,8 +558,29 @@ kda_status kda_page_free(const int32_t* block_table, int table_width, const int3
     if (!common_ok(p, block_table)) return KDA_ERR_INVALID_ARG;
     if (missing(keep_lens, seq_lens_out, free_head_out) || (num_free > 0 && !free_pages)) return KDA_ERR_INVALID_ARG;
     if (off4(keep_lens, free_pages, seq_lens_out, free_head_out)) return KDA_ERR_INVALID_ARG;
-    page_free_kernel<<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
-    return launched();
+    const long long cells = (long long)N * table_width;   // at most, as the lengths are on the device
+    if (cells <= FREE_ALONE) {
+        page_free_kernel<true><<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
+        return launched();
+    }
+    const long long blocks = ((long long)num_pages / 4 + 255) / 256 + 1;
+    page_owners_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up beside the kernel before
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int warps = 152 * 8 * 4, rows = N <= warps ? 1 : N / warps < 32 ? N / warps : 32;
+    const long long groups = ((long long)N + 8ll * rows - 1) / (8ll * rows);
+    cfg.gridDim = dim3((unsigned)(groups < 152 * 8 ? groups : 152 * 8));
+    cfg.blockDim = dim3(256);
+    if (cudaLaunchKernelEx(&cfg, page_release_kernel, p, rows) != cudaSuccess) return KDA_ERR_CUDA;
+    cfg.gridDim = dim3(PG_CTAS);
+    cfg.blockDim = dim3(PG_THREADS);
+    return cudaLaunchKernelEx(&cfg, page_free_kernel<false>, p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_page_compact(const int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* refs,
