@@ -113,7 +113,7 @@ def load_library(path: Optional[str] = None):
     lib.kda_latent_chunk.argtypes = [vp, vp, i, i, vp, i, vp, vp, f, vp, i, vp, vp, i, i, i, u, vp, sz, vp]
     for name in ("kda_page_fork", "kda_page_free", "kda_page_compact"):
         getattr(lib, name).restype = ctypes.c_int
-    lib.kda_page_fork.argtypes = [vp, i, vp, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, i, i, vp, vp]
+    lib.kda_page_fork.argtypes = [vp, i, vp, vp, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, vp, i, i, vp, vp]
     lib.kda_page_copy.restype = ctypes.c_int
     lib.kda_page_copy.argtypes = [vp, i, i, ll, vp, vp, i, vp, vp]
     lib.kda_page_free.argtypes = [vp, i, vp, vp, vp, i, vp, i, vp, i, vp, vp, vp, i, vp, vp]

@@ -31,6 +31,7 @@ struct PageParams {
     const int32_t* keep;
     const int32_t* parents;
     const int32_t* children;
+    const int32_t* fork_lens;
     const int32_t* refs;
     const int32_t* free_pages;
     int32_t* free_io;
@@ -120,9 +121,10 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
             if (c >= 0) {
                 if (c < p.N && a >= 0 && a < p.N && p.lens[c] == 0 && __ldcg(p.lens_out + c) == i - p.F) {
                     const long long most = (long long)p.width * p.page_size;
-                    const int len = p.lens[a];
-                    bad |= len < 0 || len > most;
-                    e = make_int4(a, c, (int)max(0ll, min((long long)len, most)), -1);
+                    const int len = p.lens[a], whole = (int)max(0ll, min((long long)len, most));
+                    const int taken_over = p.fork_lens ? p.fork_lens[i] : whole, some = max(0, min(taken_over, whole));
+                    bad |= len != whole || taken_over != some;
+                    e = make_int4(a, c, some, -1);
                 } else {
                     bad = true;
                 }
@@ -318,6 +320,14 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
         cluster_barrier();                       // the other CTAs' shared memory is there
         asm volatile("griddepcontrol.wait;" ::: "memory");
     }
+    // rows that go back into a page with another owner left
+    for (int n = me; n < p.N; n += PG_ALL) {
+        const int len = p.lens[n], kept = max(0, min(p.keep[n], len));
+        if (kept < len && kept % p.page_size != 0 && kept / p.page_size < p.width) {
+            const int page = p.table[(long long)n * p.width + kept / p.page_size];
+            bad |= page < 0 || page >= p.num_pages || __ldcg(p.refs_out + page) > 0;
+        }
+    }
     const Share share(p.num_pages, index);
     int mine = 0;
     walk(p.refs_out, share.first, share.last, [&](int, const int(&x)[4], int) {
@@ -500,21 +510,21 @@ extern "C" {
 
 
 kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* parents,
-                         const int32_t* children, const int32_t* refs, int num_pages, const int32_t* free_pages,
-                         int num_free, const int32_t* free_head, int page_size, int32_t* seq_lens_out,
-                         int32_t* refs_out, int32_t* free_head_out, int32_t* pairs, int N, int F, void* workspace,
-                         cudaStream_t stream) {
+                         const int32_t* children, const int32_t* fork_lens, const int32_t* refs, int num_pages,
+                         const int32_t* free_pages, int num_free, const int32_t* free_head, int page_size,
+                         int32_t* seq_lens_out, int32_t* refs_out, int32_t* free_head_out, int32_t* pairs, int N,
+                         int F, void* workspace, cudaStream_t stream) {
     using namespace kda;
     PageParams p{};
     p.status = static_cast<uint32_t*>(workspace);
-    p.table_io = block_table, p.lens = seq_lens, p.parents = parents, p.children = children, p.refs = refs;
+    p.table_io = block_table, p.lens = seq_lens, p.parents = parents, p.children = children, p.fork_lens = fork_lens, p.refs = refs;
     p.free_pages = free_pages, p.free_head = free_head, p.lens_out = seq_lens_out, p.refs_out = refs_out;
     p.head_out = free_head_out, p.pairs = pairs;
     p.width = table_width, p.num_pages = num_pages, p.num_free = num_free, p.page_size = page_size, p.N = N, p.F = F;
     if (!common_ok(p, block_table) || F < 0) return KDA_ERR_INVALID_ARG;
     if (missing(seq_lens_out, free_head_out) || (F > 0 && missing(parents, children, pairs)) || (num_free > 0 && !free_pages))
         return KDA_ERR_INVALID_ARG;
-    if (off4(parents, children, free_pages, seq_lens_out, free_head_out, pairs)) return KDA_ERR_INVALID_ARG;
+    if (off4(parents, children, fork_lens, free_pages, seq_lens_out, free_head_out, pairs)) return KDA_ERR_INVALID_ARG;
     page_fork_kernel<<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
     return launched();
 }

@@ -49,14 +49,15 @@ def _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, **mo
 
 def page_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor, children: torch.Tensor,
               refs: torch.Tensor, free_pages: torch.Tensor, free_head: torch.Tensor, page_size: int,
-              workspace: Optional[torch.Tensor] = None
+              fork_lens: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
               ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """Rows ``children[i]`` of the table go on from the tokens of rows ``parents[i]``.
 
     block_table: int32 [N, width], the children's cells are written in place;
     seq_lens: int32 [N]; parents, children: int32 [F] (a negative child is
     skipped), the children distinct rows of length 0; refs: int32 [pages];
-    free_pages: int32 [free] and free_head: int32 [1], as for ``block_tables``.
+    free_pages: int32 [free] and free_head: int32 [1], as for ``block_tables``;
+    fork_lens: int32 [F], how many of the parent's first tokens (None: all).
     Full pages are shared; a last page that is not full gets a page of its own.
     Returns (the new lengths, the new refs, the new free_head, pairs int32
     [F, 2] for ``page_copy``: the page to copy and the own page, or -1); the
@@ -68,25 +69,31 @@ def page_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.
         (pages,), (free,), (F,) = refs.shape, free_pages.shape, parents.shape
         fine = (block_table.dtype is seq_lens.dtype is parents.dtype is children.dtype is refs.dtype is free_pages.dtype
                 is free_head.dtype is _I32 and seq_lens.shape == (N,) and children.shape == (F,) and free_head.shape == (1,)
+                and (fork_lens is None or fork_lens.dtype is _I32 and fork_lens.shape == (F,))
                 and 0 < page_size <= INT_MAX and page_size % 1 == 0 and max(N, width, pages, free, F) <= INT_MAX
-                and _together(index, block_table, parents, children, refs, free_pages, free_head))
+                and _together(index, block_table, parents, children, fork_lens, refs, free_pages, free_head))
     except (AttributeError, ValueError):   # not a tensor, or not of one dimension or two
         fine = False
     if not fine:
-        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, parents_=parents, children_=children)
-        raise ValueError(f"parents and children must be of one length, got {parents.shape[0]} and {children.shape[0]}")
+        more = {} if fork_lens is None else dict(fork_lens_=fork_lens)
+        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, parents_=parents, children_=children, **more)
+        raise ValueError("parents, children and fork_lens must be of one length, got "
+                         f"{[t.shape[0] for t in (parents, children, *more.values())]}")
     if index != _current_device():
         return _elsewhere(index, page_fork, block_table, seq_lens, parents, children, refs, free_pages, free_head, page_size,
-                          workspace)
+                          fork_lens, workspace)
     if not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous")
     # copies are held until the launch: a freed one's memory would go to the next
     seq_lens, refs, free_pages = seq_lens.contiguous(), refs.contiguous(), free_pages.contiguous()
     parents, children = parents.contiguous(), children.contiguous()
+    if fork_lens is not None:
+        fork_lens = fork_lens.contiguous()
     lens_out, refs_out, head_out = torch.empty_like(seq_lens), torch.empty_like(refs), torch.empty_like(free_head)
     pairs = torch.empty((F, 2), dtype=_I32, device=seq_lens.device)
     _raise(load_library().kda_page_fork(
-        block_table.data_ptr(), width, seq_lens.data_ptr(), parents.data_ptr(), children.data_ptr(), refs.data_ptr(), pages,
+        block_table.data_ptr(), width, seq_lens.data_ptr(), parents.data_ptr(), children.data_ptr(),
+        None if fork_lens is None else fork_lens.data_ptr(), refs.data_ptr(), pages,
         free_pages.data_ptr(), free, free_head.data_ptr(), int(page_size), lens_out.data_ptr(), refs_out.data_ptr(),
         head_out.data_ptr(), pairs.data_ptr(), N, F, _status_workspace(workspace, index), _stream(index)), "kda_page_fork")
     return lens_out, refs_out, head_out, pairs
@@ -158,7 +165,10 @@ def page_free(block_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torc
     int32 [1].  The pages that lose their last owner come in front of the free
     list, in increasing order: their entries of ``free_pages`` are written in
     place.  Returns (the new lengths, the new refs, the new free_head); the
-    other inputs stay as they are.  ``workspace`` as for ``page_fork``."""
+    other inputs stay as they are.  A row that goes back into a page that has
+    another owner left is reported: tokens appended to it would overwrite that
+    one's (``page_fork`` its first tokens into another row instead).
+    ``workspace`` as for ``page_fork``."""
     try:
         index = seq_lens.get_device()
         N, width = block_table.shape

@@ -618,6 +618,8 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
  *   parents, children  int32 [F], device; a negative child is a padding entry
  *               and is skipped.  Children are distinct rows of length 0, a
  *               parent may occur any number of times
+ *   fork_lens   int32 [F], device: how many of the parent's first tokens entry
+ *               i takes over, or NULL for all
  *   block_table int32 [N, table_width]: the children's first cells are
  *               written in place, others left alone
  *   seq_lens_out  int32 [N];  refs_out int32 [num_pages];  free_head_out
@@ -626,14 +628,15 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
  * A row outside [0, N), a child that has tokens, or one that an earlier entry
  * has: the entry is skipped.  A page outside [0, num_pages) becomes -1 in the
  * child's table, and so does an own page where the free list ends.  Each sets
- * KDA_ERR_BAD_PAGE; lengths outside the table are clipped and set it too.
+ * KDA_ERR_BAD_PAGE; lengths outside the table, or fork_lens outside the
+ * parent's tokens, are clipped and set it too.
  *   workspace   NULL, or the 256-byte status header
  */
 kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* parents,
-                         const int32_t* children, const int32_t* refs, int num_pages, const int32_t* free_pages,
-                         int num_free, const int32_t* free_head, int page_size, int32_t* seq_lens_out,
-                         int32_t* refs_out, int32_t* free_head_out, int32_t* pairs, int N, int F, void* workspace,
-                         cudaStream_t stream);
+                         const int32_t* children, const int32_t* fork_lens, const int32_t* refs, int num_pages,
+                         const int32_t* free_pages, int num_free, const int32_t* free_head, int page_size,
+                         int32_t* seq_lens_out, int32_t* refs_out, int32_t* free_head_out, int32_t* pairs, int N,
+                         int F, void* workspace, cudaStream_t stream);
 
 /*
  * Copy pages within each of num_pools pools (the caches of a model's layers,
@@ -663,7 +666,9 @@ kda_status kda_page_copy(void* const* pools, int num_pools, int num_pages, long 
  * The table is only read: cells behind a row's length have no meaning.  A
  * page outside [0, num_pages), one that loses more owners than it has, a
  * length out of range (clipped), or a page that finds no room in front of
- * free_head (not listed): KDA_ERR_BAD_PAGE.
+ * free_head (not listed): KDA_ERR_BAD_PAGE.  So does a row that goes back into
+ * a page that has another owner left: tokens appended to it would overwrite
+ * that one's (fork its first tokens into a row of their own instead).
  *   workspace   NULL, or the 256-byte status header
  */
 kda_status kda_page_free(const int32_t* block_table, int table_width, const int32_t* seq_lens,

@@ -147,21 +147,22 @@ def _pages(length: int, size: int) -> int:
     return -(-length // size)
 
 
-def page_fork(table, lens, parents, children, refs, free, head: int, size: int):
+def page_fork(table, lens, parents, children, refs, free, head: int, size: int, fork_lens=None):
     """Returns (table, lens, refs, head, pairs) anew."""
     table, new, refs, pairs = table.clone(), list(lens), list(refs), []
-    for a, c in zip(parents, children):
+    for i, (a, c) in enumerate(zip(parents, children)):
         pair = (-1, -1)
         if c >= 0:
-            full = lens[a] // size
+            length = lens[a] if fork_lens is None else fork_lens[i]
+            full = length // size
             for j in range(full):
                 table[c, j] = table[a, j]
                 refs[int(table[a, j])] += 1
-            if lens[a] % size:
+            if length % size:
                 pair = (int(table[a, full]), int(free[head]))
                 table[c, full] = free[head]
                 head += 1
-            new[c] = lens[a]
+            new[c] = length
         pairs.append(pair)
     return table, new, refs, head, pairs
 

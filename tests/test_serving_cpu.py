@@ -68,10 +68,10 @@ def test_page_refusals():
               dict(N=0), dict(ws=p + 16), dict(table=p + 2), dict(lens=p + 1), dict(refs=p + 2), dict(free=p + 2),
               dict(head=p + 2), dict(refs_out=p + 2))
     fork = caller(lib.kda_page_fork, dict(
-        table=p, width=2, lens=p, parents=p, children=p, refs=p, pages=4, free=p, free_n=4, head=p, page=16, lens_out=p,
+        table=p, width=2, lens=p, parents=p, children=p, fork_lens=None, refs=p, pages=4, free=p, free_n=4, head=p, page=16, lens_out=p,
         refs_out=p, head_out=p, pairs=p, N=2, F=1, ws=p, stream=None))
     for kw in shared + (dict(parents=None), dict(children=None), dict(pairs=None), dict(lens_out=None), dict(head_out=None),
-                        dict(F=-1), dict(parents=p + 2), dict(pairs=p + 2)):
+                        dict(F=-1), dict(parents=p + 2), dict(fork_lens=p + 2), dict(pairs=p + 2)):
         assert fork(**kw) == 1, kw
     free = caller(lib.kda_page_free, dict(
         table=p, width=2, lens=p, keep=p, refs=p, pages=4, free=p, free_n=4, head=p, page=16, lens_out=p, refs_out=p,
@@ -134,7 +134,7 @@ def test_wrappers_refuse_what_the_kernels_do_not_take():
                                           ("num_keys", -1), ("num_keys", 2 ** 32 + 4), ("num_keys", 4.5), ("q", None), ("w_up", 3)]),
             (pages.page_fork, fork, [("parents", z(2)), ("children", z(1, d=i64)), ("refs", z(4, d=i64)), ("free_head", z(2)),
                                      ("page_size", 0), ("page_size", 2 ** 32 + 16), ("page_size", 16.5), ("block_table", z(3, 3)),
-                                     ("seq_lens", None), ("refs", big(2 ** 32 + 4)), ("parents", [0])]),
+                                     ("seq_lens", None), ("refs", big(2 ** 32 + 4)), ("parents", [0]), ("fork_lens", z(2)), ("fork_lens", z(1, d=i64))]),
             (pages.page_free, free, [("keep_lens", z(3)), ("keep_lens", None), ("free_pages", z(2, 2)), ("page_size", -1),
                                      ("block_table", big(2, 2 ** 32))]),
             (pages.page_compact, compact, [("refs", z(2, 2)), ("free_pages", z(4, d=f32)), ("page_size", 0), ("free_head", 0)]),

@@ -421,7 +421,8 @@ def test_page_free(longest, n, page, spare, group):
     for _ in range(2):                                   # the inputs but for the listed pages stay as they are
         got = pages().page_free(t, i32(lens), i32(keep), i32(refs), f, i32([head]), page, workspace=ws)
         wl, wr, wf, wh = sv.page_free(table, lens, keep, refs, free, head, page)
-        assert status(ws) == 0 and torch.equal(t.cpu(), table)
+        shared = any(k < l and k % page and wr[table[i, k // page]] > 0 for i, (k, l) in enumerate(zip(keep, lens)))
+        assert status(ws) == (8 if shared else 0) and torch.equal(t.cpu(), table)
         assert got[0].tolist() == wl and got[1].tolist() == wr and got[2].item() == wh and f.tolist() == wf
 
 
@@ -448,6 +449,15 @@ def test_page_fork(longest, n, page, spare, group):
         assert torch.equal(t.cpu(), wt)
         assert got[0].tolist() == wl and got[1].tolist() == wr and got[2].item() == wh
         assert [tuple(p) for p in got[3].tolist()] == wp
+    some = [lens[a] * (i % 5) // 4 for i, a in enumerate(parents)]
+    for i, (a, c) in enumerate(zip(parents, children)):
+        if some[i] % page and not lens[a] % page and c >= 0:   # (there are own pages for parents whose last page is not full)
+            some[i] -= some[i] % page
+    t = table.cuda()
+    got = pages().page_fork(t, i32(lens), i32(parents), i32(children), i32(refs), i32(free), i32([head]), page, fork_lens=i32(some))
+    wt, wl, wr, wh, wp = sv.page_fork(table, lens, parents, children, refs, free, head, page, some)
+    assert torch.equal(t.cpu(), wt) and got[0].tolist() == wl and got[1].tolist() == wr and got[2].item() == wh
+    assert [tuple(p) for p in got[3].tolist()] == wp
 
 
 @pytest.mark.parametrize("longest,n,page,spare,group", STATES)
@@ -506,6 +516,10 @@ def test_page_faults_are_reported():
     assert s == 8 and t[3] == [4, -1, -1] and l[3] == 8 and r[4] == 2 and pairs == [[-1, -1]]
     s, t, l, r, h, pairs = fork([0, 0], [2, 3], head=7)   # one page left
     assert s == 8 and t[2] == [4, 5, 7] and t[3] == [4, 5, -1] and h == [8] and pairs == [[6, 7], [-1, -1]]
+    for some, kept in ((11, 10), (-1, 0)):                # tokens that the parent has not
+        t = table.cuda()
+        got = p.page_fork(t, i32(lens), i32([0]), i32([2]), i32(refs), i32(free), i32([4]), 4, fork_lens=i32([some]), workspace=ws)
+        assert status(ws) == 8 and got[0].tolist()[2] == kept
     for n in (99, -4):
         s, t, l, r, h, pairs = fork([0, 4], [2, 3], lens=[10, 8, 0, 0, n])
         assert s == 8 and t[2] == [4, 5, 3] and l[2] == 10 and l[3] == (12 if n > 0 else 0)
@@ -521,6 +535,10 @@ def test_page_faults_are_reported():
     assert s == 0 and f == [4, 5, 5, 6, 3, 0, 1, 7] and h == [2] and l == [4, 8, 0, 0, 8]
     s, f, l, r, h = release([10, 8, 0, 0, 0])             # page 2 twice
     assert s == 8 and h == [3] and f[3] == 2 and r == refs
+    s, f, l, r, h = release([3, 5, 0, 0, 8])              # into page 4, which the other one owns too
+    assert s == 8 and l == [3, 5, 0, 0, 8] and r == [0, 0, 0, 0, 1, 0, 0, 0] and h == [2]
+    s, f, l, r, h = release([3, 0, 0, 0, 8], lens=[10, 4, 0, 0, 8])   # which ends
+    assert s == 0 and l == [3, 0, 0, 0, 8] and r == [0] * 8 and h == [2]
     s, f, l, r, h = release([11, -1, 0, 0, 8])
     assert s == 8 and l == [10, 0, 0, 0, 8] and r[4] == 0 and h == [4]
     s, f, l, r, h = release([0, 8, 0, 0, 8], head=1)      # no room in front
@@ -660,3 +678,120 @@ def test_wrappers_name_what_they_refuse():
         verify(z(1, 1, d=torch.int64), z(1, 2, 4, d=torch.float64), z(1, 2, d=F32))
     with pytest.raises(ValueError, match="uniform"):
         verify(z(1, 1, d=torch.int64), z(1, 2, 4, d=F32), z(1, 1, d=F32))
+
+
+# ---------------------------------------------------------------------------
+# together
+def layers(n, requests, pages=64, **kw):
+    from chunked_gated_delta_kda_gb300.latent_serving import LatentLayer
+    return [LatentLayer(128, 2, requests, pages=pages, width=16, page_size=16, **kw) for _ in range(n)]
+
+
+def test_layer_reads_a_prompt_in_chunks_forks_it_and_takes_tokens_back():
+    """Whatever the steps, pages and forks were, a request's rows are those of a layer that read its tokens at once."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    layer, = layers(1, 4)
+    x = torch.randn(4, 200, 128, generator=g, device="cuda").to(BF)
+    tokens = [x[0, :0]] * 4
+
+    def add(*counts):
+        new = [x[i, len(tokens[i]):len(tokens[i]) + n] for i, n in enumerate(counts)]
+        out = layer.chunk(torch.cat(new), i32(counts))
+        for i, n in enumerate(new):
+            tokens[i] = torch.cat([tokens[i], n])
+        return out, counts
+
+    def keep(*lens):
+        layer.keep(i32(lens))
+        for i, n in enumerate(lens):
+            tokens[i] = tokens[i][:n]
+
+    def check(out, counts):
+        fresh, = layers(1, 4)
+        want = fresh.prefill(torch.cat(tokens), i32([len(t) for t in tokens]))
+        at = 0
+        for i, n in enumerate(counts):
+            end = sum(len(t) for t in tokens[:i + 1])
+            a, b = out[at:at + n].float(), want[end - n:end].float()
+            # as many rows in another product: a rounding of rows, queries, keys, values and output each, and the weights'
+            assert (a - b).norm() <= 6 * 2.0 ** -8 * b.norm(), (i, n)
+            at += n
+        # every page has as many owners as the tables say, and the free list has the others
+        held = [layer.table[i, :-(-len(t) // 16)].tolist() for i, t in enumerate(tokens)]
+        owners = [sum(p in h for h in held) for p in range(64)]
+        free = layer.free[layer.head.item():].tolist()
+        assert layer.refs.tolist() == [max(o - 1, 0) for o in owners]
+        assert sorted(free) == [p for p in range(64) if owners[p] == 0] and layer.lens.tolist() == [len(t) for t in tokens]
+
+    check(*add(50, 20, 0, 0))
+    check(*add(40, 1, 0, 0))
+    layer.fork(i32([0, 0]), i32([2, 3]))
+    tokens[2] = tokens[3] = tokens[0]
+    x[2, :90] = x[3, :90] = x[0, :90]
+    check(*add(7, 0, 7, 33))                               # into each one's own last page
+    keep(97, 0, 92, 80)                                    # request 1 ends, 3 goes back into shared pages' tokens
+    check(*add(3, 60, 5, 0))
+    keep(0, 60, 97, 80)
+    moved = layer.compact()
+    assert moved > 0 and max(layer.table[i, :-(-n // 16)].max().item() for i, n in enumerate([0, 60, 97, 80]) if n) < 64 - len(
+        layer.free[layer.head.item():])
+    check(*add(10, 0, 1, 0))                               # into a page of a forked request: its own
+
+
+def test_layer_does_not_go_back_into_a_shared_page():
+    """A request that goes back into a page that others own too would write into their rows: refused; a fork of its first
+    tokens has a page of its own."""
+    layer, = layers(1, 2)
+    x = torch.randn(60, 128, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda").to(BF)
+    layer.chunk(x[:48], i32([48, 0]))
+    layer.fork(i32([0]), i32([1]))
+    from chunked_gated_delta_kda_gb300 import binding
+    with pytest.raises(binding.KdaError) as e:
+        layer.keep(i32([48, 40]))
+    assert e.value.code == 8
+    assert layer.lens.tolist() == [48, 48]
+    layer.keep(i32([48, 0]))
+    layer.fork(i32([0]), i32([1]), i32([40]))
+    assert layer.lens.tolist() == [48, 40] and layer.table[0, 2] != layer.table[1, 2]
+    rows = lambda i: layer.cache[layer.table[i, :3].long()].reshape(-1, 576)  # noqa: E731
+    assert torch.equal(rows(0)[:40], rows(1)[:40])
+    layer.chunk(x[48:60], i32([0, 12]))
+    layer.keep(i32([48, 32]))
+    layer.keep(i32([0, 32]))                               # the other owner ends
+    layer.keep(i32([0, 20]))
+
+
+def test_drafts_leave_greedy_decoding_as_it_is():
+    """Tokens of the largest probability, with drafts of every quality: the tokens are those without drafts."""
+    from chunked_gated_delta_kda_gb300.latent_serving import Decoder
+    g = torch.Generator(device="cuda").manual_seed(7)
+    prompt = torch.randint(0, 50, (70,), generator=g, device="cuda")
+    plain, quick = (Decoder(50, 256, 4, 2, pages=64, width=16, page_size=16, temper=1e4, seed=2) for _ in range(2))
+    n = i32([40, 30])
+    u = lambda s: torch.rand(2, s, generator=g, device="cuda")  # noqa: E731
+    first = plain.start(prompt, n, u(1)[:, 0])
+    assert torch.equal(first, quick.start(prompt, n, u(1)[:, 0]))
+    want = [first]
+    for _ in range(24):
+        want.append(plain.step(want[-1], first.new_empty(2, 0), u(1))[0][:, 0])
+    want = torch.stack(want, 1)
+    texts, steps = [[t] for t in first.tolist()], 0
+    while min(len(t) for t in texts) < 25:
+        guess = torch.full((2, 3), -1, dtype=torch.int64, device="cuda")
+        for i, t in enumerate(texts):
+            right = (want[i].tolist() + [0] * 99)[len(t):len(t) + 3]
+            wrong = [(r + 1) % 50 for r in right]
+            kind = (steps + i) % 4                          # none; wrong from the first, the second, none of them on
+            guess[i] = torch.tensor([[-1] * 3, wrong, right[:1] + wrong[1:], right][kind], device="cuda")
+        out, count = quick.step(torch.tensor([t[-1] for t in texts], device="cuda"), guess, u(4))
+        for t, row, c in zip(texts, out.tolist(), count.tolist()):
+            t += row[:c]
+        steps += 1
+    for i in range(2):
+        assert texts[i][:25] == want[i].tolist()
+    assert steps < 24
+
+
+def test_serving_example_runs():
+    from chunked_gated_delta_kda_gb300 import latent_serving
+    assert latent_serving.continue_forked() >= 1.0
