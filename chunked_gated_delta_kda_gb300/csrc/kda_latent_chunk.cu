@@ -413,10 +413,12 @@ unsigned long long up256(unsigned long long b) { return (b + 255ull) / 256ull * 
 // Queries that see at most this many tiles of keys get them as two numbers a
 // channel.  A key's rounding (2^-9 of it in bf16) reaches the scores, and their
 // log-sum-exp averages it over the keys that count (scores of unit variance: a
-// relative error of 8e-5 at 237 keys, 1e-5 at 2049, 3.5e-6 at 8192), so beyond
-// that the second numbers, which add 40 % to the products of a pair, are left
-// out.  fp16 rounds eight times finer (1e-5 at 129 keys, 6e-6 at 300).
-int lo_tiles(bool fp16) { return fp16 ? 4 : 32; }
+// relative error of 8e-5 at 237 keys, 6e-6 at 2100, 3.5e-6 at 8192), so beyond
+// that the second numbers are left out: they add 40 % to the products of a pair
+// and 20 % to the expansion (8 x 1024 tokens on 4096 rows, H=16: 456 us with
+// them, 331 without).  fp16 rounds eight times finer (1e-5 at 129 keys, 6e-6 at
+// 300).
+int lo_tiles(bool fp16) { return fp16 ? 2 : 16; }
 
 struct ChunkLayout {
     unsigned long long cu, tiles, cu_lo, kv, pe, lo, bytes;

@@ -29,12 +29,12 @@ def test_workspace_sizes():
     shared = 896 * 16 + 256 * 256 * 130 * 4
     rows = lambda keys, H, low: keys * H * 512 + r256(keys * 128) + low * H * 256  # noqa: E731
     assert lib.kda_latent_chunk_workspace_bytes(37, 237, 8, 1) == 256 + 3 * 256 + rows(237, 8, 237)
-    assert lib.kda_latent_chunk_workspace_bytes(1642, 16231, 16, 4) == 256 + r256(shared) + 3 * 256 + rows(16231, 16, 16231)
+    assert lib.kda_latent_chunk_workspace_bytes(1642, 16231, 16, 4) == 256 + r256(shared) + 3 * 256 + rows(16231, 16, 8192)
     assert lib.kda_latent_chunk_workspace_bytes(0, 0, 1, 1) == 256 + 3 * 256
     for bad in ((-1, 1, 1, 1), (1, -1, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0), (1, 1, 65536, 1), (1, 1, 1, 65536),
                 (1 << 30, 1, 65535, 1), (1, 1, 65535, 65535)):
         assert lib.kda_latent_chunk_workspace_bytes(*bad) == 0, bad
-    assert lib.kda_latent_chunk_workspace_bytes(8, 100000, 1, 2) == 256 + 3 * 256 + rows(100000, 1, 8192)
+    assert lib.kda_latent_chunk_workspace_bytes(8, 100000, 1, 2) == 256 + 3 * 256 + rows(100000, 1, 4096)
 
 
 def test_status_string():

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
 U = {BF: 2.0 ** -8, FP: 2.0 ** -11}
 TINY = {BF: 0.0, FP: 2.0 ** -25}
-FEW = {BF: 4096, FP: 512}
+FEW = {BF: 2048, FP: 256}
 
 
 def latent():
@@ -96,11 +96,11 @@ CHUNKS = [
     ([256, 1, 2], [257, 385, 1000], 17, 192, FP),            # pages of one and a half tiles
     ([7, 300], [9000, 310], 2, 64, BF),                      # keys shared by CTAs of the device's choice
     ([20], [4100], 2, 32, FP),                               # and of the host's
-    ([700, 3], [4500, 4096], 2, 64, BF),                     # around the border of few keys: pairs of tiles on either side,
-    ([300, 260, 2], [4097, 4097, 4098], 1, 16, BF),
-    ([700, 200], [1200, 513], 2, 64, FP),
+    ([700, 3], [2500, 2048], 2, 64, BF),                     # around the border of few keys: pairs of tiles on either side,
+    ([300, 260, 2], [2049, 2049, 2050], 1, 16, BF),
+    ([700, 200], [900, 257], 2, 64, FP),
     ([600] * 8 + [40], [900] * 8 + [2000], 6, 64, BF),       # two numbers a key with CTAs that share keys,
-    ([2048], [2048], 1, 64, BF), ([40], [4000], 3, 32, BF),  # and in clusters
+    ([2048], [2048], 1, 64, BF), ([40], [2040], 3, 32, BF),  # and in clusters
 ]
 
 
@@ -795,3 +795,40 @@ def test_drafts_leave_greedy_decoding_as_it_is():
 def test_serving_example_runs():
     from chunked_gated_delta_kda_gb300 import latent_serving
     assert latent_serving.continue_forked() >= 1.0
+
+
+def test_verified_drafts_and_forked_states_of_the_recurrence():
+    """A step of four tokens a request leaves a state behind each; the accepted number picks the one that the next step
+    starts from, and a copied slot is a fork of the request."""
+    from chunked_gated_delta_kda_gb300 import binding
+    from chunked_gated_delta_kda_gb300.inputs import make_decode_inputs
+    N, S, H, V = 5, 3, 2, 300
+    x = make_decode_inputs(N, H, S + 1 + 2, pool_slots=40, seed=31)
+    d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+    part = lambda a, b: [d[k][:, a:b].contiguous() for k in ("q", "k", "v", "g", "beta")]  # noqa: E731
+    base = torch.arange(N, dtype=torch.int32, device="cuda")[:, None] * (S + 1)
+    slots = base + torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    pool = d["pool"][:40].clone()
+    start = pool.clone()
+    binding.fused_recurrent(*part(0, S + 1), pool, slots, num_accepted_tokens=torch.ones(N, dtype=torch.int32, device="cuda"))
+    tokens, target, u, draft = draft_inputs(N, S, V, F32, seed=32)
+    u[0, :S] = 0.0                                       # all accepted
+    target[1, 0, tokens[1, 0]] = 0.0                     # none
+    _, accepted = verify(tokens.cuda(), target.cuda(), u.cuda(), draft.cuda())
+    assert accepted[0] == S + 1 and accepted[1] == 1
+    forks = torch.stack([slots.gather(1, accepted[:, None].long() - 1)[:, 0], 20 + torch.arange(N, dtype=torch.int32, device="cuda")], 1)
+    pages().page_copy(pool, forks)
+    ahead = lambda p, s, n: binding.fused_recurrent(*part(S + 1, S + 3), p, s, num_accepted_tokens=n)  # noqa: E731
+    of_forks = ahead(pool, torch.stack([forks[:, 1], forks[:, 1] + 10], 1), torch.ones_like(accepted))
+    of_requests = ahead(pool, slots, accepted)
+    assert torch.equal(of_forks, of_requests)
+    for n, count in enumerate(accepted.tolist()):
+        one = start.clone()
+        slot = torch.full((N, 1), -1, dtype=torch.int32, device="cuda")
+        slot[n] = slots[n, 0]
+        for t in [*range(count), S + 1, S + 2]:
+            o = binding.fused_recurrent(*part(t, t + 1), one, slot)
+            if t > S:
+                # (four tokens a window sum in another order than one: a rounding of o each)
+                a, b = of_requests[n, t - S - 1].float(), o[n, 0].float()
+                assert (a - b).abs().max() <= 2.0 ** -7 * b.abs().max()
