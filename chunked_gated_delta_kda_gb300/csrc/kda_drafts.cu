@@ -11,8 +11,16 @@
 // Which token it is depends on the sums' last bits, and 64-bit arithmetic runs
 // at two operations a clock and SM here, less than the rows' bytes leave time
 // for.  So r, its sums and the border are pairs of 32-bit numbers whose
-// rounding errors are kept (Knuth's and Dekker's exact sums), 16 operations an
-// element; sums are good to some 2^-40.
+// rounding errors are kept (Knuth's and Dekker's exact sums), two elements an
+// operation: ten for an element, four without q; sums are good to some 2^-40.
+//
+// 128 sequences of 131072 in fp32 (134 MB): 21.8 us, 6.2 TB/s; before, with
+// sums in 64 bits where warps join 31, one element an operation 23.  One
+// sequence of 32768: 7.7 us, of which the launch, the drafts' two rounds of
+// loads, the row's, the cluster's exchange and the last range's are some 1.3
+// each.  Rows of odd length, which start anywhere, are read in whole words that
+// are shifted together (256 x 50257 in bf16, one row each: 18.5 us, on 16 bytes
+// 14; element by element 28).
 #include <cstdint>
 
 #include "kda.h"
@@ -194,8 +202,7 @@ struct Number {
 
 // The sum of [from, to), whole warp, in every lane; `to` is where the row ends
 // or `from` and a multiple of 512.  ALIGNED: the rows start on 16 bytes.  LESS:
-// of p - q (256 x 50257 in bf16 without q ** us; 28 with the operations that q
-// needs).
+// of p - q.
 template <typename T, bool ALIGNED, bool LESS>
 __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, int V) {
     constexpr int W = 16 / (int)sizeof(T);
@@ -244,6 +251,8 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
         i = 32 * W;
     }
     for (; i + STEP <= to && (ALIGNED || i + STEP + W <= V); i += STEP) chunk(Number<MOST>(), Number<0>(), i);
+    constexpr int HALF = 512 / (32 * W);         // (a share is whole 512s but for the row's last)
+    for (; i + 512 <= to && (ALIGNED || i + 512 + W <= V); i += 512) chunk(Number<HALF>(), Number<0>(), i);
     for (; i < to; i += 32 * W) chunk(Number<1>(), Number<1>(), i);
     Pair d = sums.value();
 #pragma unroll
@@ -460,7 +469,9 @@ extern "C" kda_status kda_verify_drafts(const int64_t* draft_tokens, const void*
     const long long pieces = 16 / size;
     const bool vec = !off(target_probs, 16) && !off(draft_probs, 16) && p.p_n % pieces == 0 && p.p_s % pieces == 0 &&
                      p.q_n % pieces == 0 && p.q_s % pieces == 0;
-    // as many CTAs a sequence as fit the GPU at once (two an SM), and have 512 elements a warp
+    // As many CTAs a sequence as fit the GPU at once (two an SM) and have 512 elements a warp (128 sequences of 131072, us
+    // with 2 / 4 / 8: 22 / 27 / 37; 64 with 4 / 8: 14 / 19; 100 with 2 / 3: 21 / 23; 256 of 50257 in bf16 with 1 / 2 / 4:
+    // 19 / 28 / 38).
     int ctas = 1;
     while (ctas < DR_MOST && (long long)ctas * DR_WARPS * 512 < V && 2ll * ctas * N <= 304) ctas *= 2;
     p.seg = (int)(((long long)V + ctas * DR_WARPS * 512 - 1) / (ctas * DR_WARPS * 512) * 512);
