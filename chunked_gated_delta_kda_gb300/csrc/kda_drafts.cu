@@ -22,6 +22,7 @@
 // are shifted together (256 x 50257 in bf16, one row each: 18.5 us, on 16 bytes
 // 14; element by element 28).
 #include <cstdint>
+#include <type_traits>
 
 #include "kda.h"
 #include "kda_latent_mma.cuh"
@@ -158,6 +159,14 @@ union Piece {
     T t[16 / sizeof(T)];
 };
 
+// Elements 2 j and 2 j + 1 of them.
+template <typename T>
+__device__ __forceinline__ float2 pair_at(uint4 u, int j) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    else return unpack2<sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value>(w[j]);
+}
+
 // A whole 16-byte word of a row [begin, end), 0 where the row is not.
 template <typename T>
 __device__ __forceinline__ uint4 load_word(const uint4* word, const T* begin, const T* end) {
@@ -200,9 +209,10 @@ struct Number {
     static constexpr int value = N;
 };
 
-// The sum of [from, to), whole warp, in every lane; `to` is where the row ends
-// or `from` and a multiple of 512.  ALIGNED: the rows start on 16 bytes.  LESS:
-// of p - q.
+// The sum of [from, to) of a row of V, whole warp, in every lane; row.p + from
+// is on 16 bytes (`from` may be below 0: what is in front of the row counts
+// nothing), `to` is V or `from` and a multiple of 512.  LESS: of p - q, whose
+// rows start on 16 bytes where p's do if ALIGNED, and anywhere if not.
 template <typename T, bool ALIGNED, bool LESS>
 __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, int V) {
     constexpr int W = 16 / (int)sizeof(T);
@@ -212,19 +222,23 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
     auto chunk = [&](auto batch, auto edge, int i) {
         constexpr int BATCH = decltype(batch)::value;
         constexpr bool EDGE = decltype(edge)::value != 0;
-        Piece<T> x[BATCH], y[BATCH];
-        auto fetch = [&](const T* r, Piece<T>(&z)[BATCH]) {
+        Piece<T> x[BATCH];
+        [[maybe_unused]] Piece<T> y[LESS ? BATCH : 1];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const uint4* at = reinterpret_cast<const uint4*>(row.p + i + (k * 32 + lane) * W);
+            if constexpr (EDGE) x[k].u = load_word(at, row.p, row.p + V);
+            else x[k].u = __ldg(at);
+        }
+        if constexpr (LESS) {
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
-                const T* at = r + i + (k * 32 + lane) * W;
-                if constexpr (ALIGNED && !EDGE) z[k].u = __ldg(reinterpret_cast<const uint4*>(at));
-                else z[k].u = load_any<EDGE>(at, r, r + V);
+                const T* at = row.q + i + (k * 32 + lane) * W;
+                if constexpr (ALIGNED && !EDGE) y[k].u = __ldg(reinterpret_cast<const uint4*>(at));
+                else y[k].u = load_any<EDGE>(at, row.q, row.q + V);
             }
-        };
-        fetch(row.p, x);
-        if constexpr (LESS) {
-            fetch(row.q, y);
-        } else {
+        }
+        if constexpr (EDGE && !LESS) {
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
                 const int left_out = row.but - i - (k * 32 + lane) * W;
@@ -238,22 +252,29 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
 #pragma unroll
-            for (int e = 0; e < W; e += 2) {
-                const float a = val(x[k].t[e]), b = val(x[k].t[e + 1]);
-                if constexpr (LESS) sums.add_rest(two(a, b), two(val(y[k].t[e]), val(y[k].t[e + 1])));
-                else sums.add(two(fmaxf(a, 0.f), fmaxf(b, 0.f)));   // (0 from what is no number)
+            for (int j = 0; j < W / 2; ++j) {
+                const float2 a = pair_at<T>(x[k].u, j);
+                if constexpr (LESS) {
+                    const float2 b = pair_at<T>(y[k].u, j);
+                    sums.add_rest(two(a.x, a.y), two(b.x, b.y));
+                } else {
+                    sums.add(two(fmaxf(a.x, 0.f), fmaxf(a.y, 0.f)));   // (0 from what is no number)
+                }
             }
     };
-    constexpr int MOST = W == 8 ? 4 : LESS ? 4 : 8, STEP = 32 * W * MOST;
+    // whole steps, where they neither reach past the row nor hold the token that is left out
+    constexpr int MOST = W == 8 ? 4 : LESS ? 4 : 8, STEP = 32 * W * MOST, HALF = 512 / (32 * W);
+    auto plain = [&](int i, int count) {
+        if constexpr (LESS) return i >= (ALIGNED ? 0 : W) && i + count <= to && (ALIGNED || i + count + W <= V);
+        else return i >= 0 && i + count <= to && (row.but < i || row.but >= i + count);
+    };
     int i = from;
-    if (!ALIGNED && i == 0 && to > 0) {          // the first may begin inside a word
-        chunk(Number<1>(), Number<1>(), 0);
-        i = 32 * W;
+    while (i < to) {
+        for (; plain(i, STEP); i += STEP) chunk(Number<MOST>(), Number<0>(), i);
+        for (; plain(i, 512); i += 512) chunk(Number<HALF>(), Number<0>(), i);
+        if (i < to) chunk(Number<1>(), Number<1>(), i);
+        i += 32 * W;
     }
-    for (; i + STEP <= to && (ALIGNED || i + STEP + W <= V); i += STEP) chunk(Number<MOST>(), Number<0>(), i);
-    constexpr int HALF = 512 / (32 * W);         // (a share is whole 512s but for the row's last)
-    for (; i + 512 <= to && (ALIGNED || i + 512 + W <= V); i += 512) chunk(Number<HALF>(), Number<0>(), i);
-    for (; i < to; i += 32 * W) chunk(Number<1>(), Number<1>(), i);
     Pair d = sums.value();
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) d = d + moved(d, [&](float x) { return __shfl_xor_sync(0xffffffffu, x, m); });
@@ -274,7 +295,7 @@ __device__ __forceinline__ Pair lanes_upto(Pair x) {
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __grid_constant__ DraftParams p) {
     __shared__ Pair sums[2][DR_SEGS], parts[DR_WARPS], bound_s, total_s;
-    __shared__ int taken_s, drafted_s, seg_s, firsts[DR_WARPS], lasts[DR_WARPS];
+    __shared__ int taken_s, drafted_s, seg_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank(), n = blockIdx.x / ctas;
     const int64_t* drafts = p.drafts + (long long)n * p.S;
@@ -320,12 +341,13 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
     row.kind = !drafted_s ? P_ALONE : draft ? P_LESS_Q : P_BUT_ONE;
     row.but = row.kind == P_BUT_ONE ? (int)drafts[taken] : -1;
     const float u = uniform[p.S];
+    const int shift = (int)((reinterpret_cast<uintptr_t>(row.p) & 15u) / sizeof(T));   // ranges begin on 16 bytes
 
     const int segs = ctas * DR_WARPS, mine = rank * DR_WARPS + warp;
     Pair total;
     cluster_barrier();                           // every CTA's shared memory is there
     for (int round = 0;; ++round) {
-        const int from = min((long long)p.V, (long long)mine * p.seg), to = min((long long)p.V, (long long)from + p.seg);
+        const int from = (int)min((long long)p.V, (long long)mine * p.seg - shift), to = (int)min((long long)p.V, (long long)from + p.seg);
         const Pair d = row.kind == P_LESS_Q ? sum_range<T, ALIGNED, true>(row, from, to, p.V) : sum_range<T, ALIGNED, false>(row, from, to, p.V);
         if (lane < ctas) {
             const uint32_t at = cluster_addr(smem_u32(&sums[round][mine]), lane);
@@ -333,32 +355,34 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
         }
         cluster_barrier();
         if (warp == 0) {
-            // the range that holds the border: the first whose sums up to it are above, else the last with weight
-            Pair up[DR_SEGS / 32], x[DR_SEGS / 32], all = {0.f, 0.f};
+            // the range that holds the border: the first whose sums up to it are above, else the last with weight; a lane PER
+            // ranges in a row
+            constexpr int PER = DR_SEGS / 32;
+            Pair x[PER], up[PER];
 #pragma unroll
-            for (int k = 0; k < DR_SEGS / 32; ++k) {
-                const int s = 32 * k + lane;
-                x[k] = s < segs ? sums[round][s] : Pair{0.f, 0.f};
-                up[k] = lanes_upto(x[k]);
+            for (int k = 0; k < PER; ++k) {
+                x[k] = PER * lane + k < segs ? sums[round][PER * lane + k] : Pair{0.f, 0.f};
+                up[k] = k == 0 ? x[0] : up[k - 1] + x[k];
             }
-#pragma unroll
-            for (int k = 0; k < DR_SEGS / 32; ++k) {
-                up[k] = all + up[k];
-                all = moved(up[k], [&](float z) { return __shfl_sync(0xffffffffu, z, 31); });
-            }
+            const Pair lanes = lanes_upto(up[PER - 1]), all = moved(lanes, [&](float z) { return __shfl_sync(0xffffffffu, z, 31); });
+            Pair ahead = moved(lanes, [&](float z) { return __shfl_up_sync(0xffffffffu, z, 1); });
+            if (lane == 0) ahead = {0.f, 0.f};
             const Pair border = u * all;
-            int seg = -1, last = -1;
+            int first = -1, weight = -1;
             Pair before = {0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < DR_SEGS / 32; ++k) {
-                const uint32_t above = __ballot_sync(0xffffffffu, x[k].h > 0.f && up[k] > border);
-                const uint32_t some = __ballot_sync(0xffffffffu, x[k].h > 0.f);
-                if (some) last = 32 * k + 31 - __clz(some);
-                if (seg < 0 && above) {
-                    seg = 32 * k + __ffs(above) - 1;
-                    before = moved(up[k] - x[k], [&](float z) { return __shfl_sync(0xffffffffu, z, __ffs(above) - 1); });
+            for (int k = PER - 1; k >= 0; --k) {
+                if (!(x[k].h > 0.f)) continue;
+                if (weight < 0) weight = PER * lane + k;
+                if (ahead + up[k] > border) {
+                    first = PER * lane + k;
+                    before = k == 0 ? ahead : ahead + up[k - 1];
                 }
             }
+            const uint32_t above = __ballot_sync(0xffffffffu, first >= 0);
+            const int last = __reduce_max_sync(0xffffffffu, weight);
+            const int at = above ? __ffs(above) - 1 : 0, seg = __shfl_sync(0xffffffffu, first, at);
+            before = moved(before, [&](float z) { return __shfl_sync(0xffffffffu, z, at); });
             if (lane == 0) {
                 seg_s = seg >= 0 ? seg : last;
                 bound_s = seg >= 0 ? border - before : Pair{INFINITY, 0.f};
@@ -382,8 +406,8 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
     if (seg / DR_WARPS != rank) return;
     // this CTA's range: a thread a run of elements, then the run that holds the border, a lane an element
     const Pair bound = bound_s;
-    const int from = seg * p.seg, to = min((long long)p.V, (long long)from + p.seg);
-    const int each = p.seg / DR_THREADS, a = min(to, from + tid * each), b = min(to, a + each);
+    const int from = seg * p.seg - shift, to = (int)min((long long)p.V, (long long)from + p.seg);
+    const int each = p.seg / DR_THREADS, a = max(0, min(to, from + tid * each)), b = max(0, min(to, from + (tid + 1) * each));
     Sum sum;
 #pragma unroll 8
     for (int i = a; i < b; ++i) {
@@ -394,20 +418,16 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
     const Pair own = sum.value(), upto = lanes_upto(own);
     if (lane == 31) parts[warp] = upto;
     __syncthreads();
-    Pair before = {0.f, 0.f};
-    for (int w = 0; w < warp; ++w) before = before + parts[w];
-    // the first run above the border, else the last with weight
-    const bool some = own.h > 0.f, above = some && before + upto > bound;
-    const int first_above = __reduce_min_sync(0xffffffffu, above ? tid : DR_THREADS);
-    const int last_some = __reduce_max_sync(0xffffffffu, some ? tid : -1);
-    if (lane == 0) firsts[warp] = first_above, lasts[warp] = last_some;
-    __syncthreads();
-    int run = __reduce_min_sync(0xffffffffu, firsts[lane & (DR_WARPS - 1)]);
-    const int last = __reduce_max_sync(0xffffffffu, lasts[lane & (DR_WARPS - 1)]);
-    if (run == DR_THREADS) run = last;
-    if (warp != run / 32) return;
+    // the first warp whose runs reach above the border, else the last with weight; all others are done
+    const Pair part = lane < DR_WARPS ? parts[lane] : Pair{0.f, 0.f}, parts_upto = lanes_upto(part);
+    const uint32_t over_warps = __ballot_sync(0xffffffffu, part.h > 0.f && parts_upto > bound);
+    const uint32_t with_weight = __ballot_sync(0xffffffffu, part.h > 0.f);
+    if (warp != (over_warps ? __ffs(over_warps) - 1 : max(0, 31 - __clz(with_weight)))) return;
+    const Pair before = moved(parts_upto - part, [&](float z) { return __shfl_sync(0xffffffffu, z, warp); });
+    const uint32_t over_runs = __ballot_sync(0xffffffffu, own.h > 0.f && before + upto > bound), runs = __ballot_sync(0xffffffffu, own.h > 0.f);
+    const int run = warp * 32 + (over_runs ? __ffs(over_runs) - 1 : max(0, 31 - __clz(runs)));
     Pair c = moved(before + (upto - own), [&](float z) { return __shfl_sync(0xffffffffu, z, run & 31); });
-    const int a0 = min(to, from + run * each), b0 = min(to, a0 + each);
+    const int a0 = max(0, min(to, from + run * each)), b0 = max(0, min(to, from + (run + 1) * each));
     int token = -1, latest = a0;                 // (a sum's last bits may put the border behind its run: the last with weight then)
     for (int base = a0; base < b0 && token < 0; base += 32) {
         float h = 0.f, l = 0.f;
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
 }
 
 template <typename T>
-cudaError_t launch(const DraftParams& p, bool vec, int N, int ctas, cudaStream_t stream) {
+cudaError_t launch(const DraftParams& p, bool aligned, int N, int ctas, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)ctas;
@@ -434,7 +454,7 @@ cudaError_t launch(const DraftParams& p, bool vec, int N, int ctas, cudaStream_t
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return vec ? cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, true>, p) : cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, false>, p);
+    return aligned ? cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, true>, p) : cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, false>, p);
 }
 
 bool off(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
@@ -467,17 +487,19 @@ extern "C" kda_status kda_verify_drafts(const int64_t* draft_tokens, const void*
     for (const long long x : {p.p_n, p.p_s, p.q_n, p.q_s})
         if (x < 0 || x >= most) return KDA_ERR_INVALID_ARG;
     const long long pieces = 16 / size;
-    const bool vec = !off(target_probs, 16) && !off(draft_probs, 16) && p.p_n % pieces == 0 && p.p_s % pieces == 0 &&
+    const bool aligned = !off(target_probs, 16) && !off(draft_probs, 16) && p.p_n % pieces == 0 && p.p_s % pieces == 0 &&
                      p.q_n % pieces == 0 && p.q_s % pieces == 0;
     // As many CTAs a sequence as fit the GPU at once (two an SM) and have 512 elements a warp (128 sequences of 131072, us
     // with 2 / 4 / 8: 22 / 27 / 37; 64 with 4 / 8: 14 / 19; 100 with 2 / 3: 21 / 23; 256 of 50257 in bf16 with 1 / 2 / 4:
     // 19 / 28 / 38).
     int ctas = 1;
     while (ctas < DR_MOST && (long long)ctas * DR_WARPS * 512 < V && 2ll * ctas * N <= 304) ctas *= 2;
-    p.seg = (int)(((long long)V + ctas * DR_WARPS * 512 - 1) / (ctas * DR_WARPS * 512) * 512);
+    p.seg = (int)((V + (aligned ? 0 : pieces - 1) + ctas * DR_WARPS * 512 - 1) / (ctas * DR_WARPS * 512) * 512);   // with room for the shift
+    // ranges a power of two apart meet in the same parts of the memory (256 x 131072 in fp32 44 us, so 41; 160 of them 37, 34)
+    if (p.seg * size >= 32768u && p.seg * size % 8192u == 0) p.seg += 512;
     if (p.status && cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    const cudaError_t e = (flags & KDA_FLAG_FP32) != 0u   ? launch<float>(p, vec, N, ctas, stream)
-                          : (flags & KDA_FLAG_FP16) != 0u ? launch<__half>(p, vec, N, ctas, stream)
-                                                          : launch<__nv_bfloat16>(p, vec, N, ctas, stream);
+    const cudaError_t e = (flags & KDA_FLAG_FP32) != 0u   ? launch<float>(p, aligned, N, ctas, stream)
+                          : (flags & KDA_FLAG_FP16) != 0u ? launch<__half>(p, aligned, N, ctas, stream)
+                                                          : launch<__nv_bfloat16>(p, aligned, N, ctas, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
