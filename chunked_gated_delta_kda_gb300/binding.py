@@ -47,6 +47,7 @@ _STATUS = {
 RECURRENT_WORKSPACE_BYTES = 256
 
 _lib = None
+_marshal = None
 
 
 class KdaError(RuntimeError):
@@ -126,6 +127,20 @@ def load_library(path: Optional[str] = None):
     lib.kda_status_str.argtypes = [i]
     _lib = lib
     return lib
+
+
+def load_marshal():
+    """The module that marshals the serving entry points' tensors (built beside the library)."""
+    global _marshal
+    if _marshal is None:
+        load_library()
+        from importlib import machinery, util
+        spec = util.spec_from_file_location("kda_marshal", _build.MARSHAL,
+                                            loader=machinery.ExtensionFileLoader("kda_marshal", _build.MARSHAL))
+        module = util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _marshal = module
+    return _marshal
 
 
 def _ptr(t: Optional[torch.Tensor]):

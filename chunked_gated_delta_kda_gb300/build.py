@@ -1,8 +1,10 @@
-"""Build ``libkda.so`` (the C-ABI KDA forward library) in-tree with nvcc.
+"""Build ``libkda.so`` (the C-ABI KDA forward library) in-tree with nvcc, and
+``kda_marshal.so``, a Python module between torch and some of its entry points.
 
 Each ``csrc/*.cu`` is compiled for sm_103a in parallel, then linked into
 ``chunked_gated_delta_kda_gb300/_build/libkda.so`` against the shared CUDA
-runtime.  Rebuilds only when a source or header is newer than the library.
+runtime; beside them ``csrc/kda_marshal.cpp`` by the host compiler against the
+installed torch.  Rebuilds only when a source or header is newer.
 """
 
 from __future__ import annotations
@@ -12,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libkda.so")
+MARSHAL = os.path.join(OUT, "kda_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -35,14 +39,31 @@ def sources():
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "kda.h"),
-                                                                  os.path.abspath(__file__)]
+                                                                  os.path.join(CSRC, "kda_marshal.cpp"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _marshal_commands():
+    """Compiling the Python module, and linking it beside ``libkda.so``."""
+    import torch
+    at = os.path.dirname(torch.__file__)
+    include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include"),
+               os.path.join(ROOT, "include")]
+    obj = os.path.join(OUT, "kda_marshal.o")
+    host = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    compile_ = [host, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *(f"-I{p}" for p in include), "-c", os.path.join(CSRC, "kda_marshal.cpp"), "-o", obj]
+    libs = os.path.join(at, "lib")
+    link = [host, "-shared", "-o", MARSHAL + f".tmp{os.getpid()}", obj, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-ltorch_cuda", "-lc10", "-lc10_cuda", LIB, "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    return compile_, link
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -61,6 +82,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    compile_, link = _marshal_commands()
+    procs.append(("kda_marshal.cpp", subprocess.Popen(compile_, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -71,11 +94,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(text, file=sys.stderr)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compiling failed:\n{msg}")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
+    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, "-Xlinker", "-soname=libkda.so", *objs]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    subprocess.run(link, check=True)
+    os.replace(link[3], MARSHAL)
     return LIB
 
 

@@ -4,22 +4,21 @@
 and draws the token behind them; the accepted number is what
 ``binding.fused_recurrent`` takes as ``num_accepted_tokens``, and what a
 request keeps of the step's cached rows (``pages.page_free``).  It runs in a
-kernel of ``libkda.so`` (``include/kda.h`` has the contract).  If the library
-is missing, the call raises: there is no fallback path.
+kernel of ``libkda.so`` (``include/kda.h`` has the contract);
+``csrc/kda_marshal.cpp`` calls it, and what that refuses is explained here.  If
+the library is missing, the call raises: there is no fallback path.
 """
 
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple
 
 import torch
 
-from .binding import KDA_FLAG_FP16, KDA_FLAG_FP32, load_library
-from .latent import INT_MAX, _check, _check_int, _current_device, _elsewhere, _raise, _same_device, _status_workspace, _stream, _together
+from .binding import KdaError, load_marshal
+from .latent import _check, _check_int, _same_device, _status_workspace
 
-_FLAGS = {torch.float32: KDA_FLAG_FP32, torch.float16: KDA_FLAG_FP16, torch.bfloat16: 0}
-_PAIR = ctypes.c_longlong * 2
+_TYPES = (torch.float32, torch.bfloat16, torch.float16)
 
 
 def verify_drafts(draft_tokens: torch.Tensor, target_probs: torch.Tensor, uniform: torch.Tensor,
@@ -40,46 +39,23 @@ def verify_drafts(draft_tokens: torch.Tensor, target_probs: torch.Tensor, unifor
     -1; num_accepted int32 [N], how many those are, 1 to S + 1).
     ``workspace`` (256 bytes, 256-byte aligned) records device-detected faults
     for ``binding.get_status``."""
-    try:
-        flags = _FLAGS.get(target_probs.dtype)
-        N, S = draft_tokens.shape
-        V = target_probs.shape[2]
-        fine = (flags is not None and draft_tokens.dtype is torch.int64 and target_probs.shape == (N, S + 1, V)
-                and uniform.dtype is torch.float32 and uniform.shape == (N, S + 1)
-                and (draft_probs is None or draft_probs.dtype is target_probs.dtype and draft_probs.shape == (N, S, V))
-                and max(N, S, V) < INT_MAX and _together(target_probs.get_device(), draft_tokens, uniform, draft_probs))
-    except (AttributeError, ValueError, IndexError):   # not a tensor, or not of two or three dimensions
-        fine = False
-    if not fine:
-        _check("draft_tokens", draft_tokens, torch.int64, (None, None))
-        N, S = draft_tokens.shape
-        if not isinstance(target_probs, torch.Tensor):
-            raise TypeError("target_probs must be a torch.Tensor")
-        if target_probs.dtype not in _FLAGS:
-            raise TypeError(f"target_probs must be torch.float32, torch.bfloat16 or torch.float16, got {target_probs.dtype}")
-        _check("target_probs", target_probs, target_probs.dtype, (N, S + 1, None))
-        _check("uniform", uniform, torch.float32, (N, S + 1))
-        if draft_probs is not None:
-            _check("draft_probs", draft_probs, target_probs.dtype, (N, S, target_probs.shape[2]))
-        for size in target_probs.shape:
-            _check_int("a size of target_probs", size)
-        _same_device(target_probs.get_device(), draft_tokens, uniform, draft_probs)
-    index = target_probs.get_device()
-    if index != _current_device():
-        return _elsewhere(index, verify_drafts, draft_tokens, target_probs, uniform, draft_probs, workspace)
-    if target_probs.stride(2) != 1 and V > 1:
-        target_probs = target_probs.contiguous()
-    strides = _PAIR(target_probs.stride(0), target_probs.stride(1))
-    draft_strides = None
+    out = load_marshal().verify_drafts(draft_tokens, target_probs, uniform, draft_probs, workspace)
+    if type(out) is tuple:
+        return out
+    if out is not None:
+        raise KdaError(out, "kda_verify_drafts")
+    _check("draft_tokens", draft_tokens, torch.int64, (None, None))
+    N, S = draft_tokens.shape
+    if not isinstance(target_probs, torch.Tensor):
+        raise TypeError("target_probs must be a torch.Tensor")
+    if target_probs.dtype not in _TYPES:
+        raise TypeError(f"target_probs must be torch.float32, torch.bfloat16 or torch.float16, got {target_probs.dtype}")
+    _check("target_probs", target_probs, target_probs.dtype, (N, S + 1, None))
+    _check("uniform", uniform, torch.float32, (N, S + 1))
     if draft_probs is not None:
-        if draft_probs.stride(2) != 1 and V > 1:
-            draft_probs = draft_probs.contiguous()
-        draft_strides = _PAIR(draft_probs.stride(0), draft_probs.stride(1))
-    draft_tokens, uniform = draft_tokens.contiguous(), uniform.contiguous()
-    tokens = torch.empty((N, S + 1), dtype=torch.int64, device=uniform.device)
-    accepted = torch.empty((N,), dtype=torch.int32, device=uniform.device)
-    _raise(load_library().kda_verify_drafts(
-        draft_tokens.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), draft_strides,
-        target_probs.data_ptr(), strides, uniform.data_ptr(), tokens.data_ptr(), accepted.data_ptr(), N, S, V, flags,
-        _status_workspace(workspace, index), _stream(index)), "kda_verify_drafts")
-    return tokens, accepted
+        _check("draft_probs", draft_probs, target_probs.dtype, (N, S, target_probs.shape[2]))
+    for size in target_probs.shape:
+        _check_int("a size of target_probs", size)
+    _same_device(target_probs.get_device(), draft_tokens, uniform, draft_probs)
+    _status_workspace(workspace, target_probs.get_device())
+    raise ValueError("verify_drafts: an argument must be of another kind")

@@ -11,9 +11,10 @@ decoder that are interleaved with KDA layers:
 ``block_tables``                 block tables and slot map of a step.
 
 Every step runs in the kernels of ``libkda.so`` (``include/kda.h`` has the
-contract); this module checks torch tensors, allocates outputs and workspaces
-on the tensors' device and passes pointers and torch's current stream.  If the
-library is missing, every call raises: there is no fallback path.
+contract); this module (for ``latent_chunk`` ``csrc/kda_marshal.cpp``) checks
+torch tensors, allocates outputs and workspaces on the tensors' device and
+passes pointers and torch's current stream.  If the library is missing, every
+call raises: there is no fallback path.
 """
 
 from __future__ import annotations
@@ -22,7 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .binding import KDA_FLAG_CAUSAL, KDA_FLAG_FP16, KdaError, load_library
+from .binding import KDA_FLAG_CAUSAL, KDA_FLAG_FP16, KdaError, load_library, load_marshal
 
 LATENT_CHANNELS = 512
 PE_CHANNELS = 64
@@ -355,48 +356,30 @@ def latent_chunk(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor
     means 192**-0.5.  Returns (o [T, H, 128], lse fp32 [T, H]); a query that
     sees no row gets 0 and -inf.  ``workspace`` as for ``latent_bwd``, with
     ``latent_chunk_workspace_bytes`` bytes."""
-    flags = _float_flag("q", q)
+    out = load_marshal().latent_chunk(q, cache, block_table, seq_lens, w_up, cu_seqlens_q, num_keys, _scale(scale), workspace)
+    if type(out) is tuple:
+        return out
+    _raise(out or 0, "kda_latent_chunk")
+    _float_flag("q", q)
     dtype = q.dtype
-    try:
-        fine = (q.dim() == cache.dim() == w_up.dim() == 3 and block_table.dim() == 2 and cache.dtype is w_up.dtype is dtype
-                and block_table.dtype is seq_lens.dtype is cu_seqlens_q.dtype is torch.int32
-                and q.shape[2] == QUERY_CHANNELS and cache.shape[2] == ROW_CHANNELS
-                and w_up.shape == (q.shape[1], KEY_CHANNELS + VALUE_CHANNELS, LATENT_CHANNELS)
-                and seq_lens.shape == block_table.shape[:1] and cu_seqlens_q.shape == (seq_lens.shape[0] + 1,)
-                and block_table.size(1) <= INT_MAX and 0 <= num_keys <= INT_MAX and num_keys % 1 == 0
-                and _together(q.get_device(), cache, block_table, seq_lens, w_up, cu_seqlens_q))
-    except AttributeError:   # not a tensor
-        fine = False
-    if not fine:
-        _check("q", q, dtype, (None, None, QUERY_CHANNELS))
-        _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
-        _check("w_up", w_up, dtype, (q.shape[1], KEY_CHANNELS + VALUE_CHANNELS, LATENT_CHANNELS))
-        _check("block_table", block_table, torch.int32, (None, None))
-        _check("seq_lens", seq_lens, torch.int32, (block_table.shape[0],))
-        _check("cu_seqlens_q", cu_seqlens_q, torch.int32, (block_table.shape[0] + 1,))
-        _check_int("block_table's width", block_table.shape[1])
-        _check_int("num_keys", num_keys)
-        if num_keys < 0:
-            raise ValueError(f"num_keys must not be negative, got {num_keys}")
-        _same_device(q.get_device(), cache, block_table, seq_lens, w_up, cu_seqlens_q)
-    index = q.get_device()
-    if index != _current_device():
-        return _elsewhere(index, latent_chunk, q, cache, block_table, seq_lens, w_up, cu_seqlens_q, num_keys, scale, workspace)
-    T, H, _ = q.shape
-    N, dev, num_keys = seq_lens.shape[0], q.device, int(num_keys)
+    _check("q", q, dtype, (None, None, QUERY_CHANNELS))
+    _check("cache", cache, dtype, (None, None, ROW_CHANNELS))
+    _check("w_up", w_up, dtype, (q.shape[1], KEY_CHANNELS + VALUE_CHANNELS, LATENT_CHANNELS))
+    _check("block_table", block_table, torch.int32, (None, None))
+    _check("seq_lens", seq_lens, torch.int32, (block_table.shape[0],))
+    _check("cu_seqlens_q", cu_seqlens_q, torch.int32, (block_table.shape[0] + 1,))
+    for name, t in (("q", q), ("block_table", block_table), ("cache", cache)):
+        for size in t.shape:
+            _check_int(f"a size of {name}", size)
+    _check_int("num_keys", num_keys)
+    if num_keys < 0:
+        raise ValueError(f"num_keys must not be negative, got {num_keys}")
+    _same_device(q.get_device(), cache, block_table, seq_lens, w_up, cu_seqlens_q)
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
-    q, w_up = _aligned(q.contiguous()), _aligned(w_up.contiguous())
-    block_table, seq_lens, cu_seqlens_q = block_table.contiguous(), seq_lens.contiguous(), cu_seqlens_q.contiguous()
-    scratch = _scratch(workspace, latent_chunk_workspace_bytes(T, num_keys, H, N), index, dev)
-    o = torch.empty((T, H, VALUE_CHANNELS), dtype=dtype, device=dev)
-    lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    _raise(load_library().kda_latent_chunk(
-        q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), w_up.data_ptr(), _scale(scale), cu_seqlens_q.data_ptr(), num_keys, o.data_ptr(), lse.data_ptr(),
-        T, H, N, flags, scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(index)), "kda_latent_chunk")
-    _hand_back(scratch, workspace)
-    return o, lse
+    if workspace is not None:
+        _check_workspace(workspace, q.get_device())
+    raise ValueError(f"num_keys must be a whole number, got {num_keys!r}")
 
 
 def latent_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,

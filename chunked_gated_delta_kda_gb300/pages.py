@@ -9,28 +9,29 @@ Beside ``latent.block_tables``, which takes pages from the free list:
 
 ``refs`` (int32, a number for each page) is how many owners a page has beside
 its first, so pages that ``block_tables`` takes need no entry.  Every step runs
-in the kernels of ``libkda.so`` (``include/kda.h`` has the contract); this
-module checks torch tensors, allocates outputs on the tensors' device and
-passes pointers and torch's current stream.  If the library is missing, every
-call raises: there is no fallback path.
+in the kernels of ``libkda.so`` (``include/kda.h`` has the contract);
+``csrc/kda_marshal.cpp`` checks the tensors, allocates outputs on their device
+and calls it on torch's current stream, and what it refuses is explained here.
+If the library is missing, every call raises: there is no fallback path.
 """
 
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
-from .binding import load_library
-from .latent import INT_MAX, _check, _check_int, _current_device, _elsewhere, _raise, _same_device, _status_workspace, _stream, _together
+from .binding import KdaError, load_marshal
+from .latent import _check, _check_int, _same_device, _status_workspace
 
 _I32 = torch.int32
 
 
-def _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, **more):
-    """Says what is wrong with the arguments of a table function (see ``latent``'s checks); ``more``: tensors of
-    seq_lens' length, or with a name that ends in ``s_`` of any."""
+def _explain(name, status, block_table, seq_lens, refs, free_pages, free_head, page_size, in_place, workspace, **more):
+    """Raises what a table function did not go through for: the C entry's status, or what is wrong with an argument.
+    ``more``: tensors of seq_lens' length, or with a name that ends in ``s_`` of one length of their own."""
+    if status is not None:
+        raise KdaError(status, name)
     _check_int("page_size", page_size)
     if page_size < 1:
         raise ValueError(f"page_size must be positive, got {page_size}")
@@ -39,12 +40,20 @@ def _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, **mo
     _check("refs", refs, _I32, (None,))
     _check("free_pages", free_pages, _I32, (None,))
     _check("free_head", free_head, _I32, (1,))
-    for name, t in more.items():
-        _check(name.rstrip("_"), t, _I32, (None,) if name[-1] == "_" else (block_table.shape[0],))
-    for name, t in (("block_table", block_table), ("refs", refs), ("free_pages", free_pages), *more.items()):
+    others = {key: t for key, t in more.items() if key[-1] == "_"}
+    for key, t in more.items():
+        _check(key.rstrip("_"), t, _I32, (None,) if key in others else (block_table.shape[0],))
+    if len({t.shape for t in others.values()}) > 1:
+        raise ValueError(f"{', '.join(k.rstrip('_') for k in others)} must be of one length, got "
+                         f"{[t.shape[0] for t in others.values()]}")
+    for key, t in (("block_table", block_table), ("refs", refs), ("free_pages", free_pages), *more.items()):
         for size in t.shape:
-            _check_int(f"a size of {name.rstrip('_')}", size)
+            _check_int(f"a size of {key.rstrip('_')}", size)
     _same_device(seq_lens.get_device(), block_table, refs, free_pages, free_head, *more.values())
+    if not dict(block_table=block_table, free_pages=free_pages).get(in_place, seq_lens[:0]).is_contiguous():
+        raise ValueError(f"{in_place} must be contiguous")
+    _status_workspace(workspace, seq_lens.get_device())
+    raise ValueError(f"{name}: page_size must be a whole number, got {page_size!r}")
 
 
 def page_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor, children: torch.Tensor,
@@ -63,40 +72,12 @@ def page_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.
     [F, 2] for ``page_copy``: the page to copy and the own page, or -1); the
     other inputs stay as they are.  ``workspace`` (256 bytes, 256-byte aligned)
     records device-detected faults for ``binding.get_status``."""
-    try:
-        index = seq_lens.get_device()
-        N, width = block_table.shape
-        (pages,), (free,), (F,) = refs.shape, free_pages.shape, parents.shape
-        fine = (block_table.dtype is seq_lens.dtype is parents.dtype is children.dtype is refs.dtype is free_pages.dtype
-                is free_head.dtype is _I32 and seq_lens.shape == (N,) and children.shape == (F,) and free_head.shape == (1,)
-                and (fork_lens is None or fork_lens.dtype is _I32 and fork_lens.shape == (F,))
-                and 0 < page_size <= INT_MAX and page_size % 1 == 0 and max(N, width, pages, free, F) <= INT_MAX
-                and _together(index, block_table, parents, children, fork_lens, refs, free_pages, free_head))
-    except (AttributeError, ValueError):   # not a tensor, or not of one dimension or two
-        fine = False
-    if not fine:
-        more = {} if fork_lens is None else dict(fork_lens_=fork_lens)
-        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, parents_=parents, children_=children, **more)
-        raise ValueError("parents, children and fork_lens must be of one length, got "
-                         f"{[t.shape[0] for t in (parents, children, *more.values())]}")
-    if index != _current_device():
-        return _elsewhere(index, page_fork, block_table, seq_lens, parents, children, refs, free_pages, free_head, page_size,
-                          fork_lens, workspace)
-    if not block_table.is_contiguous():
-        raise ValueError("block_table must be contiguous")
-    # copies are held until the launch: a freed one's memory would go to the next
-    seq_lens, refs, free_pages = seq_lens.contiguous(), refs.contiguous(), free_pages.contiguous()
-    parents, children = parents.contiguous(), children.contiguous()
-    if fork_lens is not None:
-        fork_lens = fork_lens.contiguous()
-    lens_out, refs_out, head_out = torch.empty_like(seq_lens), torch.empty_like(refs), torch.empty_like(free_head)
-    pairs = torch.empty((F, 2), dtype=_I32, device=seq_lens.device)
-    _raise(load_library().kda_page_fork(
-        block_table.data_ptr(), width, seq_lens.data_ptr(), parents.data_ptr(), children.data_ptr(),
-        None if fork_lens is None else fork_lens.data_ptr(), refs.data_ptr(), pages,
-        free_pages.data_ptr(), free, free_head.data_ptr(), int(page_size), lens_out.data_ptr(), refs_out.data_ptr(),
-        head_out.data_ptr(), pairs.data_ptr(), N, F, _status_workspace(workspace, index), _stream(index)), "kda_page_fork")
-    return lens_out, refs_out, head_out, pairs
+    out = load_marshal().page_fork(block_table, seq_lens, parents, children, refs, free_pages, free_head, page_size, fork_lens,
+                                   workspace)
+    if type(out) is not tuple:
+        _explain("kda_page_fork", out, block_table, seq_lens, refs, free_pages, free_head, page_size, "block_table", workspace,
+                 parents_=parents, children_=children, **({} if fork_lens is None else dict(fork_lens_=fork_lens)))
+    return out
 
 
 def page_copy(pools: Union[torch.Tensor, Sequence[torch.Tensor]], pairs: torch.Tensor,
@@ -110,49 +91,33 @@ def page_copy(pools: Union[torch.Tensor, Sequence[torch.Tensor]], pairs: torch.T
     device, how many pairs count (None: all).  ``workspace`` (256 bytes,
     256-byte aligned) records device-detected faults.  Returns ``pools``,
     updated in place."""
+    out = load_marshal().page_copy(pools, pairs, count, workspace)
+    if type(out) is tuple:
+        return pools
+    if out is not None:
+        raise KdaError(out, "kda_page_copy")
     if not isinstance(pools, (torch.Tensor, list, tuple)):
         raise TypeError("pools must be a torch.Tensor or a list of them")
     several = (pools,) if isinstance(pools, torch.Tensor) else pools
     if not several:
         raise ValueError("pools must not be empty")
     first = several[0]
-    try:
-        index, shape, dtype = first.get_device(), first.shape, first.dtype
-        fine = (pairs.dtype is _I32 and pairs.dim() == 2 and pairs.shape[1] == 2 and len(shape) > 0
-                and (count is None or count.dtype is _I32 and count.shape == (1,))
-                and max(pairs.shape[0], shape[0]) <= INT_MAX and _together(index, pairs, count))
-        at, low = [], 0
-        for t in several:
-            fine = fine and t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            at.append(t.data_ptr())
-            low |= at[-1]
-    except AttributeError:   # not a tensor
-        fine = False
-    if not fine:
-        for t in several:
-            if not isinstance(t, torch.Tensor):
-                raise TypeError("pools must be torch.Tensors")
-            if not t.is_cuda or t.dim() < 1 or not t.is_contiguous():
-                raise ValueError(f"pools must be contiguous CUDA tensors [pages, ...], got {tuple(t.shape)} on {t.device}")
-            if t.shape != first.shape or t.dtype is not first.dtype:
-                raise ValueError("pools must have one shape and type")
-        _check("pairs", pairs, _I32, (None, 2))
-        if count is not None:
-            _check("count", count, _I32, (1,))
-        _check_int("a size of pairs", pairs.shape[0])
-        _check_int("a size of pools", first.shape[0])
-        _same_device(first.get_device(), pairs, count, *several)
-    if index != _current_device():
-        return _elsewhere(index, page_copy, pools, pairs, count, workspace)
-    pages = shape[0]
-    page_bytes = first.numel() // max(pages, 1) * first.element_size()
-    if pages < 1 or page_bytes < 16 or page_bytes % 16 or low % 16:
-        raise ValueError(f"pools must have pages of a multiple of 16 bytes that start on 16 bytes, got {pages} of {page_bytes}")
-    pairs = pairs.contiguous()
-    _raise(load_library().kda_page_copy((ctypes.c_void_p * len(at))(*at), len(at), pages, page_bytes, pairs.data_ptr(),
-                                        None if count is None else count.data_ptr(), pairs.shape[0],
-                                        _status_workspace(workspace, index), _stream(index)), "kda_page_copy")
-    return pools
+    for t in several:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("pools must be torch.Tensors")
+        if not t.is_cuda or t.dim() < 1 or not t.is_contiguous():
+            raise ValueError(f"pools must be contiguous CUDA tensors [pages, ...], got {tuple(t.shape)} on {t.device}")
+        if t.shape != first.shape or t.dtype is not first.dtype:
+            raise ValueError("pools must have one shape and type")
+    _check("pairs", pairs, _I32, (None, 2))
+    if count is not None:
+        _check("count", count, _I32, (1,))
+    _check_int("a size of pairs", pairs.shape[0])
+    _check_int("a size of pools", first.shape[0])
+    _same_device(first.get_device(), pairs, count, *several)
+    _status_workspace(workspace, first.get_device())
+    raise ValueError("pools must have pages of a multiple of 16 bytes that start on 16 bytes, got "
+                     f"{first.shape[0]} in {first.numel() * first.element_size()} bytes")
 
 
 def page_free(block_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor, refs: torch.Tensor,
@@ -169,29 +134,11 @@ def page_free(block_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torc
     another owner left is reported: tokens appended to it would overwrite that
     one's (``page_fork`` its first tokens into another row instead).
     ``workspace`` as for ``page_fork``."""
-    try:
-        index = seq_lens.get_device()
-        N, width = block_table.shape
-        (pages,), (free,) = refs.shape, free_pages.shape
-        fine = (block_table.dtype is seq_lens.dtype is keep_lens.dtype is refs.dtype is free_pages.dtype is free_head.dtype is _I32
-                and seq_lens.shape == keep_lens.shape == (N,) and free_head.shape == (1,)
-                and 0 < page_size <= INT_MAX and page_size % 1 == 0 and max(N, width, pages, free) <= INT_MAX
-                and _together(index, block_table, keep_lens, refs, free_pages, free_head))
-    except (AttributeError, ValueError):   # not a tensor, or not of one dimension or two
-        fine = False
-    if not fine:
-        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size, keep_lens=keep_lens)
-    if index != _current_device():
-        return _elsewhere(index, page_free, block_table, seq_lens, keep_lens, refs, free_pages, free_head, page_size, workspace)
-    if not free_pages.is_contiguous():
-        raise ValueError("free_pages must be contiguous")
-    block_table, seq_lens, keep_lens, refs = block_table.contiguous(), seq_lens.contiguous(), keep_lens.contiguous(), refs.contiguous()
-    lens_out, refs_out, head_out = torch.empty_like(seq_lens), torch.empty_like(refs), torch.empty_like(free_head)
-    _raise(load_library().kda_page_free(
-        block_table.data_ptr(), width, seq_lens.data_ptr(), keep_lens.data_ptr(), refs.data_ptr(), pages, free_pages.data_ptr(),
-        free, free_head.data_ptr(), int(page_size), lens_out.data_ptr(), refs_out.data_ptr(), head_out.data_ptr(), N,
-        _status_workspace(workspace, index), _stream(index)), "kda_page_free")
-    return lens_out, refs_out, head_out
+    out = load_marshal().page_free(block_table, seq_lens, keep_lens, refs, free_pages, free_head, page_size, workspace)
+    if type(out) is not tuple:
+        _explain("kda_page_free", out, block_table, seq_lens, refs, free_pages, free_head, page_size, "free_pages", workspace,
+                 keep_lens=keep_lens)
+    return out
 
 
 def page_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor, free_pages: torch.Tensor,
@@ -206,26 +153,7 @@ def page_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.
     ``page_copy``; moved int32 [pages], each page's new number, -1 for a free
     one).  The inputs stay as they are: copy the pages of every cache before
     the new table is used.  ``workspace`` as for ``page_fork``."""
-    try:
-        index = seq_lens.get_device()
-        N, width = block_table.shape
-        (pages,), (free,) = refs.shape, free_pages.shape
-        fine = (block_table.dtype is seq_lens.dtype is refs.dtype is free_pages.dtype is free_head.dtype is _I32
-                and seq_lens.shape == (N,) and free_head.shape == (1,)
-                and 0 < page_size <= INT_MAX and page_size % 1 == 0 and max(N, width, pages, free) <= INT_MAX
-                and _together(index, block_table, refs, free_pages, free_head))
-    except (AttributeError, ValueError):   # not a tensor, or not of one dimension or two
-        fine = False
-    if not fine:
-        _explain(block_table, seq_lens, refs, free_pages, free_head, page_size)
-    if index != _current_device():
-        return _elsewhere(index, page_compact, block_table, seq_lens, refs, free_pages, free_head, page_size, workspace)
-    block_table, seq_lens, refs, free_pages = block_table.contiguous(), seq_lens.contiguous(), refs.contiguous(), free_pages.contiguous()
-    table_out, refs_out, free_out = torch.empty_like(block_table), torch.empty_like(refs), torch.empty_like(free_pages)
-    pairs = torch.empty((pages // 2, 2), dtype=_I32, device=seq_lens.device)
-    count, moved = torch.empty_like(free_head), torch.empty_like(refs)
-    _raise(load_library().kda_page_compact(
-        block_table.data_ptr(), width, seq_lens.data_ptr(), refs.data_ptr(), pages, free_pages.data_ptr(), free,
-        free_head.data_ptr(), int(page_size), table_out.data_ptr(), refs_out.data_ptr(), free_out.data_ptr(), pairs.data_ptr(),
-        count.data_ptr(), moved.data_ptr(), N, _status_workspace(workspace, index), _stream(index)), "kda_page_compact")
-    return table_out, refs_out, free_out, pairs, count, moved
+    out = load_marshal().page_compact(block_table, seq_lens, refs, free_pages, free_head, page_size, workspace)
+    if type(out) is not tuple:
+        _explain("kda_page_compact", out, block_table, seq_lens, refs, free_pages, free_head, page_size, None, workspace)
+    return out
