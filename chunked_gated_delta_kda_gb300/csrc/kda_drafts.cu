@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
     const T* draft = p.q ? static_cast<const T*>(p.q) + n * p.q_n : nullptr;
     const float* uniform = p.uniform + (long long)n * (p.S + 1);
 
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
         int taken = 0, drafted = 0;              // accepted; whether the one behind them is a draft
         bool bad = false;
@@ -443,17 +444,19 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
 
 template <typename T>
 cudaError_t launch(const DraftParams& p, bool aligned, int N, int ctas, cudaStream_t stream) {
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up beside the kernel before, which it waits for
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(N * ctas));
     cfg.blockDim = dim3(DR_THREADS);
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return aligned ? cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, true>, p) : cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T, false>, p);
 }
 

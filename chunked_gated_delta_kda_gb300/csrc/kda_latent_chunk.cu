@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_chunk_plan_kernel(const _
     const long long most = (long long)p.width * p.page_size;
     long long rows0 = 0, tiles0 = 0, lo0 = 0, all;
     bool bad = false, bad_cu = false;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     if (tid < WS_CLEAR / 4) p.status[tid] = 0u;
     for (int base = 0; base < p.N; base += blockDim.x) {
         const int n = base + tid;
@@ -490,8 +490,17 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
     p.k_lo = c.k_lo, p.cu_lo = c.cu_lo, p.lo_rows = at.lo_rows, p.lo_tiles = c.lo_tiles;
     p.Tq = T, p.Tk = num_keys, p.H = H, p.N = N, p.causal = 1, p.chunk = 1, p.wait_limit = debug_wait_limit();
 
-    latent_chunk_plan_kernel<<<1, (unsigned)(N < PLAN_THREADS ? (N + 31) / 32 * 32 : PLAN_THREADS), 0, stream>>>(c);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    // each kernel may be set up while the one before it runs, which it waits for
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3((unsigned)(N < PLAN_THREADS ? (N + 31) / 32 * 32 : PLAN_THREADS));
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, latent_chunk_plan_kernel, c) != cudaSuccess) return KDA_ERR_CUDA;
     if (T == 0) return KDA_OK;
     const bool fp16 = (flags & KDA_FLAG_FP16) != 0u;
     if (num_keys > 0) {
@@ -502,16 +511,9 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
         const auto kernel = fp16 ? latent_expand_kernel<true> : latent_expand_kernel<false>;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X_SMEM) != cudaSuccess) return KDA_ERR_CUDA;
         const long long items = (((long long)num_keys / LAT_TILE + N + 1) / 2) * H;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up beside the plan
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2u * (unsigned)(items < 76 ? items : 76));
         cfg.blockDim = dim3(EX_THREADS);
         cfg.dynamicSmemBytes = X_SMEM;
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, kernel, c, maps) != cudaSuccess) return KDA_ERR_CUDA;
     }
     return launch_latent_fwd(p, fp16, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

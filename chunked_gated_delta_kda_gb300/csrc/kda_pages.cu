@@ -99,6 +99,7 @@ static_assert(PG_WARPS == 32, "a lane a warp's sum");
 __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_fork_kernel(const __grid_constant__ PageParams p) {
     __shared__ int sums[PG_WARPS];
     __shared__ int4 entries[PG_THREADS];         // parent (-1: skipped), child, tokens, place among the own pages (-1: none)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster_rank(), me = rank * PG_THREADS + tid;
     const int head = p.free_head[0];
     bool bad = false;
@@ -292,7 +293,7 @@ __device__ __forceinline__ int owners(int refs) { return max(refs, 0); }
 
 // Where many cells may be given back, the whole GPU does that, in two kernels in front of the cluster.
 __global__ void __launch_bounds__(256) page_owners_kernel(const __grid_constant__ PageParams p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     const int me = blockIdx.x * 256 + threadIdx.x;
     if (me == 0 && p.status) *p.status = 0u;
     copy_words(p.refs, p.refs_out, p.num_pages, me, owners, gridDim.x * 256);
@@ -308,7 +309,8 @@ template <bool ALONE>
 __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_free_kernel(const __grid_constant__ PageParams p) {
     __shared__ int counts[PG_SHARES];
     const int rank = (int)cluster_rank(), me = rank * PG_THREADS + (int)threadIdx.x, index = me >> 5;
-    const long long head = p.free_head[0];
+    if constexpr (ALONE) asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool bad = false;
     if constexpr (ALONE) {
         if (me == 0 && p.status) __stcg(p.status, 0u);
@@ -320,6 +322,7 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
         cluster_barrier();                       // the other CTAs' shared memory is there
         asm volatile("griddepcontrol.wait;" ::: "memory");
     }
+    const long long head = p.free_head[0];
     // rows that go back into a page with another owner left
     for (int n = me; n < p.N; n += PG_ALL) {
         const int len = p.lens[n], kept = max(0, min(p.keep[n], len));
@@ -356,13 +359,115 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
 }
 
 // ---- compact ----
-// `moved` marks the free pages until it is written.
-__global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_compact_kernel(const __grid_constant__ PageParams p) {
+// Every CTA marks the free pages as bits in its shared memory, all of them, and
+// counts them group by group.  So it knows each page's new number by itself
+// (the k-th used page from `used` on, the number of used ones, goes to the k-th
+// free one below, found by bisection) and takes its share of the pages, of the
+// free list and of the table, with no step between the CTAs.
+constexpr int CP_GROUP = 256;                    // pages of a count
+constexpr int CP_MOST = 1 << 20;                 // pages; as bits 128 KiB
+
+struct FreePages {
+    const uint32_t* bits;
+    const int* counts;                           // free pages before each group
+    int groups, used, holes;                     // holes: free pages below `used`
+    __device__ __forceinline__ bool is_free(int page) const { return (bits[page >> 5] >> (page & 31)) & 1u; }
+    __device__ __forceinline__ int before(int page) const {
+        int n = counts[page / CP_GROUP];
+        for (int w = page / CP_GROUP * (CP_GROUP / 32); w < page >> 5; ++w) n += __popc(bits[w]);
+        return n + __popc(bits[page >> 5] & ((1u << (page & 31)) - 1));
+    }
+    __device__ __forceinline__ int select(int k) const {
+        int lo = 0, hi = groups - 1;             // the last group with at most k before it
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (counts[mid] <= k) lo = mid;
+            else hi = mid - 1;
+        }
+        k -= counts[lo];
+        int w = lo * (CP_GROUP / 32);
+        for (int c; (c = __popc(bits[w])) <= k; ++w) k -= c;
+        uint32_t word = bits[w];
+        for (; k > 0; --k) word &= word - 1;
+        return 32 * w + __ffs(word) - 1;
+    }
+    // The page's new number, -1 for a free one; k: its place among those that move, or -1.
+    __device__ __forceinline__ int moved(int page, int& k) const {
+        k = -1;
+        if (is_free(page)) return -1;
+        if (page < used) return page;
+        k = (page - used) - (before(page) - holes);
+        return select(k);
+    }
+};
+
+__global__ void __launch_bounds__(PG_THREADS, 1) page_compact_kernel(const __grid_constant__ PageParams p, int32_t* table_out) {
+    extern __shared__ uint32_t bits[];           // of whole groups, then the counts
+    __shared__ int sums[PG_WARPS];
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, groups = (p.num_pages + CP_GROUP - 1) / CP_GROUP, words = groups * (CP_GROUP / 32);
+    int* counts = reinterpret_cast<int*>(bits + words);
+    const long long head = p.free_head[0];
+    bool bad = false;
+    for (int i = tid; i < words; i += PG_THREADS) bits[i] = 0u;
+    __syncthreads();
+#pragma unroll 8
+    for (long long i = max(head, 0ll) + tid; i < p.num_free; i += PG_THREADS) {
+        const int page = __ldg(p.free_pages + i);
+        if (page < 0 || page >= p.num_pages || ((atomicOr(bits + (page >> 5), 1u << (page & 31)) >> (page & 31)) & 1u) != 0u) bad = true;
+    }
+    __syncthreads();
+    int all = 0;
+    for (int base = 0; base < groups; base += PG_THREADS) {
+        const int g = base + tid;
+        int mine = 0, total;
+        if (g < groups)
+#pragma unroll
+            for (int w = 0; w < CP_GROUP / 32; ++w) mine += __popc(bits[g * (CP_GROUP / 32) + w]);
+        const int before = block_before(mine, total, sums);
+        if (g < groups) counts[g] = all + before;
+        all += total;
+    }
+    __syncthreads();
+    FreePages f{bits, counts, groups, p.num_pages - all, all};
+    if (f.used < p.num_pages) f.holes = f.before(f.used);
+
+    const int me = blockIdx.x * PG_THREADS + tid, threads = gridDim.x * PG_THREADS;
+    int k;
+    for (int i = me; i < p.num_pages; i += threads) {
+        const int to = f.moved(i, k);
+        p.moved[i] = to;
+        if (to >= 0) p.refs_out[to] = __ldg(p.refs + i);
+        if (i >= f.used) p.refs_out[i] = 0;
+        if (k >= 0) p.pairs[2ll * k] = i, p.pairs[2ll * k + 1] = to;
+    }
+    for (int i = 2 * f.holes + me; i < p.num_pages / 2 * 2; i += threads) p.pairs[i] = -1;
+    for (int i = me; i < p.num_free; i += threads) {
+        const long long to = f.used + (i - head);
+        p.free_out[i] = i < head ? __ldg(p.free_pages + i) : to < p.num_pages ? (int)to : -1;
+    }
+    const long long cells = (long long)p.N * p.width;
+    for (long long i = me; i < cells; i += threads) {
+        const int n = (int)(i / p.width), col = (int)(i - (long long)n * p.width);
+        int to = -1;
+        if (col < row_pages(p, p.lens[n], bad)) {
+            const int page = __ldg(p.table + i);
+            if (page >= 0 && page < p.num_pages) to = f.moved(page, k);
+            bad |= to < 0;
+        }
+        table_out[i] = to;
+    }
+    if (me == 0) p.count[0] = f.holes;
+    if (bad) set_status(p.status, STATUS_BAD_PAGE);
+}
+
+// More pages than fit as bits: through memory, in steps of one cluster, and the table behind it.  `moved` marks the free
+// pages until it is written.
+__global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_compact_large_kernel(const __grid_constant__ PageParams p) {
     __shared__ int counts[PG_SHARES], sums[PG_WARPS];
     const int rank = (int)cluster_rank(), me = rank * PG_THREADS + (int)threadIdx.x, index = me >> 5, warp = (int)threadIdx.x >> 5;
     const long long head = p.free_head[0];
     bool bad = false;
-    if (me == 0 && p.status) __stcg(p.status, 0u);
     fill_words(p.moved, 0, p.num_pages, me);
     cluster_barrier();
 #pragma unroll 4
@@ -458,6 +563,7 @@ struct CopyParams {
 };
 
 __global__ void __launch_bounds__(COPY_THREADS) page_copy_kernel(const __grid_constant__ CopyParams p) {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     const int pairs = p.count ? max(0, min(p.F, p.count[0])) : p.F;
     const long long each = p.pieces * p.num_pools, items = each * pairs;
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
@@ -500,6 +606,22 @@ bool common_ok(const PageParams& p, const void* table) {
     return !off4(table, p.lens, p.refs, p.free_head) && !off(p.refs_out, 16) && !off(p.status, 256);
 }
 
+// A kernel that may be set up while the one before it runs; it waits for that one itself.
+template <typename... A, typename... B>
+kda_status launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t stream, const B&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
 kda_status launched() { return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 }  // namespace
@@ -525,6 +647,7 @@ kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* s
     if (missing(seq_lens_out, free_head_out) || (F > 0 && missing(parents, children, pairs)) || (num_free > 0 && !free_pages))
         return KDA_ERR_INVALID_ARG;
     if (off4(parents, children, fork_lens, free_pages, seq_lens_out, free_head_out, pairs)) return KDA_ERR_INVALID_ARG;
+    // (an early launch is 1.2 us dearer on the host, which is what a fork of a few requests waits for)
     page_fork_kernel<<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
     return launched();
 }
@@ -549,8 +672,8 @@ kda_status kda_page_copy(void* const* pools, int num_pools, int num_pages, long 
         p.num_pools = num_pools - first < COPY_POOLS ? num_pools - first : COPY_POOLS;
         for (int i = 0; i < p.num_pools; ++i) p.pools[i] = static_cast<uint4*>(pools[first + i]);
         const long long items = p.pieces * p.num_pools * F, most = 152ll * 8;
-        page_copy_kernel<<<(unsigned)(items < most ? items : most), COPY_THREADS, 0, stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+        const kda_status st = launch_early(page_copy_kernel, dim3((unsigned)(items < most ? items : most)), COPY_THREADS, 0, stream, p);
+        if (st != KDA_OK) return st;
     }
     return KDA_OK;
 }
@@ -569,28 +692,15 @@ kda_status kda_page_free(const int32_t* block_table, int table_width, const int3
     if (missing(keep_lens, seq_lens_out, free_head_out) || (num_free > 0 && !free_pages)) return KDA_ERR_INVALID_ARG;
     if (off4(keep_lens, free_pages, seq_lens_out, free_head_out)) return KDA_ERR_INVALID_ARG;
     const long long cells = (long long)N * table_width;   // at most, as the lengths are on the device
-    if (cells <= FREE_ALONE) {
-        page_free_kernel<true><<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
-        return launched();
-    }
+    if (cells <= FREE_ALONE) return launch_early(page_free_kernel<true>, dim3(PG_CTAS), PG_THREADS, 0, stream, p);
     const long long blocks = ((long long)num_pages / 4 + 255) / 256 + 1;
-    page_owners_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up beside the kernel before
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    kda_status st = launch_early(page_owners_kernel, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), 256, 0, stream, p);
+    if (st != KDA_OK) return st;
     const int warps = 152 * 8 * 4, rows = N <= warps ? 1 : N / warps < 32 ? N / warps : 32;
     const long long groups = ((long long)N + 8ll * rows - 1) / (8ll * rows);
-    cfg.gridDim = dim3((unsigned)(groups < 152 * 8 ? groups : 152 * 8));
-    cfg.blockDim = dim3(256);
-    if (cudaLaunchKernelEx(&cfg, page_release_kernel, p, rows) != cudaSuccess) return KDA_ERR_CUDA;
-    cfg.gridDim = dim3(PG_CTAS);
-    cfg.blockDim = dim3(PG_THREADS);
-    return cudaLaunchKernelEx(&cfg, page_free_kernel<false>, p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    st = launch_early(page_release_kernel, dim3((unsigned)(groups < 152 * 8 ? groups : 152 * 8)), 256, 0, stream, p, rows);
+    if (st != KDA_OK) return st;
+    return launch_early(page_free_kernel<false>, dim3(PG_CTAS), PG_THREADS, 0, stream, p);
 }
 
 kda_status kda_page_compact(const int32_t* block_table, int table_width, const int32_t* seq_lens, const int32_t* refs,
@@ -608,9 +718,18 @@ kda_status kda_page_compact(const int32_t* block_table, int table_width, const i
         (table_width > 0 && !table_out))
         return KDA_ERR_INVALID_ARG;
     if (off4(free_pages, free_out, pairs, count, table_out) || off(moved, 16)) return KDA_ERR_INVALID_ARG;
-    page_compact_kernel<<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
+    if (p.status && cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    const long long cells = (long long)N * table_width;
+    if (num_pages <= CP_MOST) {
+        const int groups = (num_pages + CP_GROUP - 1) / CP_GROUP, bytes = groups * (CP_GROUP / 8 + 4);
+        if (cudaFuncSetAttribute(page_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return KDA_ERR_CUDA;
+        // (each CTA reads the whole free list; four items a thread before there is another)
+        const long long items = cells > num_pages ? cells : num_pages, ctas = (items + 4 * PG_THREADS - 1) / (4 * PG_THREADS);
+        return launch_early(page_compact_kernel, dim3((unsigned)(ctas < 152 ? ctas : 152)), PG_THREADS, bytes, stream, p, table_out);
+    }
+    page_compact_large_kernel<<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-    const long long blocks = ((long long)N * table_width + 255) / 256, most = 152ll * 8;
+    const long long blocks = (cells + 255) / 256, most = 152ll * 8;
     if (blocks == 0) return KDA_OK;
     page_remap_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(p, table_out);
     return launched();

@@ -2,9 +2,15 @@
 sizes and refusals, all before any CUDA call."""
 
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 import torch
+
+from test_latent_cpu import FAKE_RUNTIME
 
 from chunked_gated_delta_kda_gb300 import binding, drafts, latent, pages
 
@@ -149,3 +155,59 @@ def test_wrappers_refuse_what_the_kernels_do_not_take():
             with pytest.raises((TypeError, ValueError)) as e:
                 fn(**{**good, name: value})
             assert "must" in str(e.value), (fn.__name__, name, e.value)
+
+
+FAKE_CALLS = r"""
+import ctypes
+from chunked_gated_delta_kda_gb300 import binding
+lib = binding.load_library()
+buf = (ctypes.c_uint8 * 4096)()
+p = ctypes.addressof(buf) + (-ctypes.addressof(buf) % 256)
+big = 1 << 50
+pair, pools = (ctypes.c_longlong * 2)(64, 16), (ctypes.c_void_p * 70)(*[p] * 70)
+chunk = lambda T, keys, H, N: lib.kda_latent_chunk(p, p, 4, 64, p, 2, p, p, 0.0, p, keys, p, p, T, H, N, 0, p, big, None)
+compact = lambda pages: lib.kda_page_compact(p, 2, p, p, pages, p, 4, p, 16, p, p, p, p, p, p, 2, None, None)
+calls = dict(
+    chunk=lambda: chunk(64, 300, 2, 1),
+    chunk_shared=lambda: chunk(64, 8192, 1, 30),
+    chunk_no_rows=lambda: chunk(64, 0, 2, 1),
+    chunk_nothing=lambda: chunk(0, 300, 2, 1),
+    fork=lambda: lib.kda_page_fork(p, 2, p, p, p, None, p, 4, p, 4, p, 16, p, p, p, p, 2, 1, None, None),
+    copy=lambda: lib.kda_page_copy(pools, 70, 4, 32, p, None, 1, None, None),
+    free=lambda: lib.kda_page_free(p, 2, p, p, p, 4, p, 4, p, 16, p, p, p, 2, None, None),
+    free_many=lambda: lib.kda_page_free(p, 1000, p, p, p, 4, p, 4, p, 16, p, p, p, 2000, None, None),
+    compact=lambda: compact(4),
+    compact_large=lambda: compact(1 << 21),
+    verify=lambda: lib.kda_verify_drafts(p, p, pair, p, pair, p, p, p, 2, 3, 16, 512, None, None))
+fake = ctypes.CDLL(None)
+for name, call in calls.items():
+    for at in range(7):
+        fake.fake_begin(at)
+        print(name, at, call(), fake.fake_launches())
+"""
+
+
+@pytest.fixture(scope="module")
+def fake_launches(tmp_path_factory):
+    """{(call, launch that fails): (status, launches tried)}, with a runtime whose n-th launch fails in front of the real
+    one: no GPU is needed, nothing runs."""
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    at = tmp_path_factory.mktemp("fake")
+    (at / "fake.c").write_text(FAKE_RUNTIME)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(at / "fake.so"), str(at / "fake.c")], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FAKE_CALLS], env=dict(os.environ, LD_PRELOAD=str(at / "fake.so"), PYTHONPATH=root),
+                         cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr[-1000:]
+    return {(name, int(at)): (int(rc), int(n)) for name, at, rc, n in (line.split() for line in out.stdout.splitlines())}
+
+
+@pytest.mark.parametrize("call,launches", [("chunk", 3), ("chunk_shared", 5), ("chunk_no_rows", 2), ("chunk_nothing", 1), ("fork", 1),
+                                           ("copy", 2), ("free", 1), ("free_many", 3), ("compact", 1), ("compact_large", 2),
+                                           ("verify", 1)])
+def test_a_failed_launch_ends_the_call(fake_launches, call, launches):
+    """What follows reads what the failed one would have written: it is not launched, and the call says so."""
+    assert fake_launches[call, 0] == (0, launches)
+    for at in range(1, launches + 1):
+        assert fake_launches[call, at] == (3, at), at

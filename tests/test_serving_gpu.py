@@ -470,7 +470,7 @@ def test_page_compact(longest, n, page, spare, group):
     assert [tuple(p) for p in got[3].tolist()] == wp and got[4].item() == wc and got[5].tolist() == wm
 
 
-@pytest.mark.parametrize("P", [1, 2, 7, 9, 4096, 32769, 300001])
+@pytest.mark.parametrize("P", [1, 2, 7, 9, 255, 256, 257, 4096, 32769, 300001, 2 ** 20, 2 ** 20 + 1])
 def test_pages_of_any_number(P):
     """One request on every second page; all of it freed again; none in use, and all."""
     for held in {0, P // 2, P}:
