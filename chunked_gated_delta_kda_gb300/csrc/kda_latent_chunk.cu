@@ -13,9 +13,16 @@
 // j of one head at a time, 128 rows each; all (pair of tiles, head) items form
 // one line, heads inside tiles, cut into equal ranges, one a pair.  The rows
 // stay in shared memory for all heads of the range, and of W_h each SM loads
-// and reads half: with a whole W_h in every SM its loads (32 KiB for 512 cycles
-// of products) took as long as the L2 let them, 206 us beside ** at 65536 rows
-// and 16 heads.
+// and reads half.
+//
+// 65536 rows, 16 heads: 170 us, 1620 TFLOP/s, as fast as the 537 MB that it
+// writes (a fill alone takes 135 us) and the power limit allow: without the
+// stores 140, without the loads 159.  16231 rows of four sequences on pages of
+// 16: 53 us, tensor cores 65 % busy while SMs have work.  On the way there:
+// 206 us with a whole W_h in every SM, 193 with pairs, 187 with rows leaving as
+// whole lines by way of shared memory (a thread a row before), 170 with a
+// tile of a head in one piece ([H, rows, 256]; [rows, H, 256] before).
+// The attention behind it takes 447 us, 1440 TFLOP/s of the mask's pairs.
 //   warps 0-7  the product's rows out of tensor memory, rounded, to the
 //              workspace (two accumulators of 256 columns take turns)
 //   warp 8     the first SM's issues the products of both
