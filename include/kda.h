@@ -592,7 +592,8 @@ size_t kda_latent_chunk_workspace_bytes(int T, int num_keys, int H, int N);
  * Precision: expanded keys and values are summed in 32 bits; values are
  * rounded to the tensors' type, as a prefill's are; keys come as a sum of two
  * such numbers where queries see few of them (2048 in bf16, 256 in fp16), and
- * are rounded where they see more.  The rest as for kda_latent_fwd.
+ * are rounded where they see more.  In fp16 a key or value past 65504 is
+ * infinite.  The rest as for kda_latent_fwd.
  */
 kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int page_size,
                             const int32_t* block_table, int table_width, const int32_t* seq_lens, const void* w_up,
