@@ -111,6 +111,15 @@ PyObject* result(kda_status status, std::initializer_list<Tensor> outputs) {
     return tuple;
 }
 
+// A launch may have to wait for room in the stream's queue: other threads go on meanwhile.
+template <typename F>
+kda_status launch(F f) {
+    PyThreadState* state = PyEval_SaveThread();
+    const kda_status status = f();
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 cudaStream_t stream_of(int64_t device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
 #define MARSHAL(name, count)                                                             \
@@ -140,9 +149,10 @@ MARSHAL(page_fork, 10)
     const Tensor s = some ? some->contiguous() : Tensor();
     Tensor lens_out = fresh({N}, l, at::kInt), refs_out = fresh({r.size(0)}, l, at::kInt), head_out = fresh({1}, l, at::kInt);
     Tensor pairs = fresh({F, 2}, l, at::kInt);
-    return result(kda_page_fork(i32_out(*table), (int)table->size(1), i32(l), i32(p), i32(k), some ? i32(s) : nullptr, i32(r), (int)r.size(0),
+    const cudaStream_t stream = stream_of(c.device);
+    return result(launch([&] { return kda_page_fork(i32_out(*table), (int)table->size(1), i32(l), i32(p), i32(k), some ? i32(s) : nullptr, i32(r), (int)r.size(0),
                                 i32(f), (int)f.size(0), i32(*head), (int)page, i32_out(lens_out), i32_out(refs_out), i32_out(head_out),
-                                i32_out(pairs), (int)N, (int)F, status, stream_of(c.device)),
+                                i32_out(pairs), (int)N, (int)F, status, stream); }),
                   {lens_out, refs_out, head_out, pairs});
     END_HANDLE_TH_ERRORS
 }
@@ -175,8 +185,9 @@ MARSHAL(page_copy, 4)
     if (!c.fine || bytes < 16 || bytes % 16 != 0) Py_RETURN_NONE;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
     const Tensor p = pairs->contiguous();
-    return result(kda_page_copy(at.data(), (int)several, (int)pages, bytes, i32(p), count ? i32(*count) : nullptr, (int)p.size(0), status,
-                                stream_of(c.device)),
+    const cudaStream_t stream = stream_of(c.device);
+    return result(launch([&] { return kda_page_copy(at.data(), (int)several, (int)pages, bytes, i32(p), count ? i32(*count) : nullptr, (int)p.size(0), status,
+                                stream); }),
                   {});
     END_HANDLE_TH_ERRORS
 }
@@ -197,8 +208,9 @@ MARSHAL(page_free, 8)
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
     const Tensor t = table->contiguous(), l = lens->contiguous(), k = keep->contiguous(), r = refs->contiguous();
     Tensor lens_out = fresh({N}, l, at::kInt), refs_out = fresh({r.size(0)}, l, at::kInt), head_out = fresh({1}, l, at::kInt);
-    return result(kda_page_free(i32(t), (int)t.size(1), i32(l), i32(k), i32(r), (int)r.size(0), i32_out(*list), (int)list->size(0), i32(*head),
-                                (int)page, i32_out(lens_out), i32_out(refs_out), i32_out(head_out), (int)N, status, stream_of(c.device)),
+    const cudaStream_t stream = stream_of(c.device);
+    return result(launch([&] { return kda_page_free(i32(t), (int)t.size(1), i32(l), i32(k), i32(r), (int)r.size(0), i32_out(*list), (int)list->size(0), i32(*head),
+                                (int)page, i32_out(lens_out), i32_out(refs_out), i32_out(head_out), (int)N, status, stream); }),
                   {lens_out, refs_out, head_out});
     END_HANDLE_TH_ERRORS
 }
@@ -217,9 +229,10 @@ MARSHAL(page_compact, 7)
     const Tensor t = table->contiguous(), l = lens->contiguous(), r = refs->contiguous(), f = list->contiguous();
     Tensor table_out = fresh({N, t.size(1)}, l, at::kInt), refs_out = fresh({pages}, l, at::kInt), free_out = fresh({f.size(0)}, l, at::kInt);
     Tensor pairs = fresh({pages / 2, 2}, l, at::kInt), count = fresh({1}, l, at::kInt), moved = fresh({pages}, l, at::kInt);
-    return result(kda_page_compact(i32(t), (int)t.size(1), i32(l), i32(r), (int)pages, i32(f), (int)f.size(0), i32(*head), (int)page,
+    const cudaStream_t stream = stream_of(c.device);
+    return result(launch([&] { return kda_page_compact(i32(t), (int)t.size(1), i32(l), i32(r), (int)pages, i32(f), (int)f.size(0), i32(*head), (int)page,
                                    i32_out(table_out), i32_out(refs_out), i32_out(free_out), i32_out(pairs), i32_out(count), i32_out(moved), (int)N,
-                                   status, stream_of(c.device)),
+                                   status, stream); }),
                   {table_out, refs_out, free_out, pairs, count, moved});
     END_HANDLE_TH_ERRORS
 }
@@ -247,9 +260,10 @@ MARSHAL(verify_drafts, 5)
     const long long p_strides[2] = {p.stride(0), p.stride(1)}, q_strides[2] = {draft ? q.stride(0) : 0, draft ? q.stride(1) : 0};
     Tensor tokens = fresh({N, S + 1}, d, at::kLong), accepted = fresh({N}, d, at::kInt);
     const unsigned flags = type == at::kFloat ? KDA_FLAG_FP32 : type == at::kHalf ? KDA_FLAG_FP16 : 0u;
-    return result(kda_verify_drafts(static_cast<const int64_t*>(d.data_ptr()), draft ? q.data_ptr() : nullptr, q_strides, p.data_ptr(), p_strides,
+    const cudaStream_t stream = stream_of(c.device);
+    return result(launch([&] { return kda_verify_drafts(static_cast<const int64_t*>(d.data_ptr()), draft ? q.data_ptr() : nullptr, q_strides, p.data_ptr(), p_strides,
                                     static_cast<const float*>(u.data_ptr()), static_cast<int64_t*>(tokens.data_ptr()), i32_out(accepted), (int)N,
-                                    (int)S, (int)V, flags, status, stream_of(c.device)),
+                                    (int)S, (int)V, flags, status, stream); }),
                   {tokens, accepted});
     END_HANDLE_TH_ERRORS
 }
@@ -279,10 +293,11 @@ MARSHAL(latent_chunk, 9)
     const Tensor scratch = enough ? *given : fresh({(int64_t)(need > (size_t)STATUS_BYTES ? need : (size_t)STATUS_BYTES)}, l, at::kByte);
     Tensor out = fresh({T, H, VALUE}, q, type), lse = fresh({T, H}, q, at::kFloat);
     const cudaStream_t stream = stream_of(c.device);
-    kda_status status = kda_latent_chunk(
+    const float scale = (float)PyFloat_AsDouble(a[7]);
+    kda_status status = launch([&] { return kda_latent_chunk(
         q.data_ptr(), cache->data_ptr(), (int)cache->size(0), (int)cache->size(1), i32(t), (int)t.size(1), i32(l), w.data_ptr(),
-        (float)PyFloat_AsDouble(a[7]), i32(o), (int)keys, out.data_ptr(), static_cast<float*>(lse.data_ptr()), (int)T, (int)H, (int)N,
-        type == at::kHalf ? KDA_FLAG_FP16 : 0u, scratch.data_ptr(), scratch.nbytes(), stream);
+        scale, i32(o), (int)keys, out.data_ptr(), static_cast<float*>(lse.data_ptr()), (int)T, (int)H, (int)N,
+        type == at::kHalf ? KDA_FLAG_FP16 : 0u, scratch.data_ptr(), scratch.nbytes(), stream); });
     if (status == KDA_OK && given != nullptr && !enough) {
         const size_t bytes = given->nbytes() < (size_t)STATUS_BYTES ? given->nbytes() : (size_t)STATUS_BYTES;
         if (cudaMemcpyAsync(given->data_ptr(), scratch.data_ptr(), bytes, cudaMemcpyDeviceToDevice, stream) != cudaSuccess) status = KDA_ERR_CUDA;
