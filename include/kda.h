@@ -168,10 +168,11 @@ kda_status kda_fwd_timed(const void* q, const void* k, const void* v, const floa
 
 /*
  * Synchronise `stream`, then read the device status word that the last
- * kda_fwd, kda_bwd, kda_fused_recurrent, kda_latent_* or kda_block_tables on
- * this workspace wrote.  Returns KDA_OK, KDA_ERR_BAD_CU_SEQLENS,
- * KDA_ERR_TIMEOUT, KDA_ERR_BAD_STATE_INDEX, KDA_ERR_BAD_PAGE, KDA_ERR_BAD_TOKEN (in that order of
- * precedence), or KDA_ERR_CUDA if synchronising or reading failed.
+ * kda_fwd, kda_bwd, kda_fused_recurrent, kda_latent_*, kda_block_tables,
+ * kda_page_* or kda_verify_drafts on this workspace wrote.  Returns KDA_OK,
+ * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_TIMEOUT, KDA_ERR_BAD_STATE_INDEX,
+ * KDA_ERR_BAD_PAGE, KDA_ERR_BAD_TOKEN (in that order of precedence), or
+ * KDA_ERR_CUDA if synchronising or reading failed.
  */
 kda_status kda_get_status(const void* workspace, cudaStream_t stream);
 
