@@ -9,7 +9,7 @@
 // launch and no scratch memory, the outputs hold what the steps pass on, and
 // what one CTA writes and another reads goes through the L2 (atomics, __stcg,
 // __ldcg).  Compacting needs no steps (see there).  Measured, in a graph: 256
-// forks of up to 128 pages 8 us, 8 forks 5.5; 256 requests that go back by up
+// forks of up to 128 pages 8 us, 8 forks 5; 256 requests that go back by up
 // to seven tokens 8.6; 2048 that end or stay, 100 thousand cells, 17.5; 512
 // pages compacted in 4.3, 8192 in 6.0, a million in 121.  Copying pages is
 // bound by HBM: 150 MB each way 86 us, 93 % of what a plain copy reaches.
@@ -99,10 +99,18 @@ __device__ __forceinline__ int block_before(int mine, int& total, int* sums) {
 static_assert(PG_WARPS == 32, "a lane a warp's sum");
 
 // ---- fork: a warp an entry ----
-// While entries claim their children, lens_out holds i - F at a child of
-// length 0 that entry i is the first to have.
+// Up to 256 entries (FEW) every CTA looks for earlier entries with the same
+// child in its shared memory; beyond, entries claim their children: lens_out
+// holds i - F at a child of length 0 that entry i is the first to have. That
+// takes two barriers more, the search a time that grows with the entries:
+// forks of a page 4.1 us by search and 5.1 by claims for 8, 5.3 and 6.0 for
+// 256, 7.7 and 7.0 for 512, 14.7 and 8.7 for 1024.
+constexpr int PG_FEW = 256;
+
+template <bool FEW>
 __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1) page_fork_kernel(const __grid_constant__ PageParams p) {
     __shared__ int sums[PG_WARPS];
+    __shared__ int4 wanted[FEW ? PG_FEW / 4 : 1];   // the children of entries that may have them, else -1
     __shared__ int4 entries[PG_THREADS];         // parent (-1: skipped), child, tokens, place among the own pages (-1: none)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster_rank(), me = rank * PG_THREADS + tid;
@@ -112,12 +120,18 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
     auto same = [](int x) { return x; };
     copy_words(p.refs, p.refs_out, p.num_pages, me, same);
     copy_words(p.lens, p.lens_out, p.N, me, same);
-    cluster_barrier();
-    for (int i = me; i < p.F; i += PG_ALL) {
-        const int a = p.parents[i], c = p.children[i];
-        if (c >= 0 && c < p.N && a >= 0 && a < p.N && p.lens[c] == 0) atomicMin(p.lens_out + c, i - p.F);
+    auto may_have = [&](int a, int c) { return c >= 0 && c < p.N && a >= 0 && a < p.N && p.lens[c] == 0; };
+    if constexpr (FEW) {
+        if (tid < PG_FEW) reinterpret_cast<int*>(wanted)[tid] = tid < p.F && may_have(p.parents[tid], p.children[tid]) ? p.children[tid] : -1;
+        __syncthreads();
+    } else {
+        cluster_barrier();
+        for (int i = me; i < p.F; i += PG_ALL) {
+            const int a = p.parents[i], c = p.children[i];
+            if (may_have(a, c)) atomicMin(p.lens_out + c, i - p.F);
+        }
+        cluster_barrier();
     }
-    cluster_barrier();
     int taken = 0;
     for (int base = 0; base < p.F; base += PG_THREADS) {
         const int i = base + tid;
@@ -125,7 +139,18 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
         if (i < p.F) {
             const int a = p.parents[i], c = p.children[i];
             if (c >= 0) {
-                if (c < p.N && a >= 0 && a < p.N && p.lens[c] == 0 && __ldcg(p.lens_out + c) == i - p.F) {
+                bool first = may_have(a, c);
+                if constexpr (FEW) {
+                    for (int k = 0; k < tid / 4; ++k) {
+                        const int4 w = wanted[k];
+                        if (w.x == c || w.y == c || w.z == c || w.w == c) first = false;
+                    }
+                    for (int k = tid / 4 * 4; k < tid; ++k)
+                        if (reinterpret_cast<const int*>(wanted)[k] == c) first = false;
+                } else if (first) {
+                    first = __ldcg(p.lens_out + c) == i - p.F;
+                }
+                if (first) {
                     const long long most = (long long)p.width * p.page_size;
                     const int len = p.lens[a], whole = (int)max(0ll, min((long long)len, most));
                     const int taken_over = p.fork_lens ? p.fork_lens[i] : whole, some = max(0, min(taken_over, whole));
@@ -141,7 +166,7 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
         const int before = block_before(part ? 1 : 0, total, sums);
         if (part) e.w = taken + before;
         entries[tid] = e;
-        cluster_barrier();                       // every CTA has looked its entries up before lens_out changes
+        cluster_barrier();                       // the copies are there, and every CTA has looked its entries up
         for (int k = rank * PG_WARPS + warp; k < min(PG_THREADS, p.F - base); k += PG_ALL / 32) {
             const int4 f = entries[k];
             int2 pair = make_int2(-1, -1);
@@ -655,7 +680,8 @@ kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* s
         return KDA_ERR_INVALID_ARG;
     if (off4(parents, children, fork_lens, free_pages, seq_lens_out, free_head_out, pairs)) return KDA_ERR_INVALID_ARG;
     // (an early launch is 1.2 us dearer on the host, which is what a fork of a few requests waits for)
-    page_fork_kernel<<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
+    if (F <= PG_FEW) page_fork_kernel<true><<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
+    else page_fork_kernel<false><<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
     return launched();
 }
 

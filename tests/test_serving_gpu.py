@@ -559,6 +559,27 @@ def test_page_faults_are_reported():
     assert compact(table=table[:, :0], lens=[0] * 5)[0] == 0
 
 
+@pytest.mark.parametrize("F", [255, 256, 257, 1024, 1025, 2500])
+def test_many_forks_with_children_twice(F):
+    """Every third entry wants a child that an earlier one has, some far before it."""
+    rows = F + 5
+    lens = [33, 16] + [0] * (rows - 2)
+    table = torch.full((rows, 4), -1, dtype=torch.int32)
+    table[0, :3], table[1, 0] = torch.tensor([0, 1, 2]), 3
+    refs, free = [0] * (F + 10), list(range(F + 10))
+    order = torch.randperm(rows - 2, generator=torch.Generator().manual_seed(F)).tolist()
+    children = [order[i] + 2 if i % 3 or i < 9 else order[i // 3 if i % 2 else i - 1] + 2 for i in range(F)]
+    parents = [i % 2 for i in range(F)]
+    twice = [c in children[:i] for i, c in enumerate(children)]
+    assert sum(twice) > F // 4
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    t = table.cuda()
+    got = pages().page_fork(t, i32(lens), i32(parents), i32(children), i32(refs), i32(free), i32([4]), 16, workspace=ws)
+    wt, wl, wr, wh, wp = sv.page_fork(table, lens, parents, [-1 if d else c for c, d in zip(children, twice)], refs, free, 4, 16)
+    assert status(ws) == 8 and torch.equal(t.cpu(), wt) and got[0].tolist() == wl and got[1].tolist() == wr and got[2].item() == wh
+    assert [tuple(p) for p in got[3].tolist()] == wp
+
+
 def test_page_tensors_that_start_anywhere():
     """Views whose first element is not on 16 bytes, and a table that is a slice."""
     lens = lengths(30, 200, 3)
