@@ -392,11 +392,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) w[e] = pack2<FP16>(x[e >> 4][2 * e & 31], x[e >> 4][(2 * e & 31) + 1]);
                 store_rows(stage, w, out + 128 * b, LAT_KV * 2, t.rows - r0, lane);
-                if (k == 0 && t.lo_rows > r0) {                    // what the keys lose in rounding
+                if (k == 0 && t.lo_rows > r0) {                    // what the keys lose in rounding, nothing where they are infinite
+                    auto lost = [](float x, float hi) { return fabsf(hi) < INFINITY ? x - hi : 0.f; };
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const float2 hi = unpack2<FP16>(w[e]);
-                        w[e] = pack2<FP16>(x[e >> 4][2 * e & 31] - hi.x, x[e >> 4][(2 * e & 31) + 1] - hi.y);
+                        w[e] = pack2<FP16>(lost(x[e >> 4][2 * e & 31], hi.x), lost(x[e >> 4][(2 * e & 31) + 1], hi.y));
                     }
                     store_rows(stage, w, out_lo + 128 * b, LAT_N * 2, t.lo_rows - r0, lane);
                 }
