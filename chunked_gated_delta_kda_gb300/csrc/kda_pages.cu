@@ -397,6 +397,7 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
 // free one below, found by bisection) and takes its share of the pages, of the
 // free list and of the table, with no step between the CTAs.
 constexpr int CP_GROUP = 256;                    // pages of a count
+constexpr int CP_GROUP_BYTES = CP_GROUP / 8 + 4; // bits and count
 constexpr int CP_MOST = 1 << 20;                 // pages; as bits 128 KiB
 
 struct FreePages {
@@ -754,8 +755,10 @@ kda_status kda_page_compact(const int32_t* block_table, int table_width, const i
     if (p.status && cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
     const long long cells = (long long)N * table_width;
     if (num_pages <= CP_MOST) {
-        const int groups = (num_pages + CP_GROUP - 1) / CP_GROUP, bytes = groups * (CP_GROUP / 8 + 4);
-        if (cudaFuncSetAttribute(page_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return KDA_ERR_CUDA;
+        const int groups = (num_pages + CP_GROUP - 1) / CP_GROUP, bytes = groups * CP_GROUP_BYTES;
+        // (the limit is the kernel's, for all threads that call it: the same for every pool)
+        if (cudaFuncSetAttribute(page_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CP_MOST / CP_GROUP * CP_GROUP_BYTES) != cudaSuccess)
+            return KDA_ERR_CUDA;
         // an item a thread, though each CTA reads the whole free list (8192 pages, 256 rows of 32: 6 us, with four 11)
         const long long items = cells > num_pages ? cells : num_pages, ctas = (items + PG_THREADS - 1) / PG_THREADS;
         return launch_early(page_compact_kernel, dim3((unsigned)(ctas < 152 ? ctas : 152)), PG_THREADS, bytes, stream, p, table_out);

@@ -1,0 +1,83 @@
+"""Serving entry points on the host, without a GPU: what a call sets and leaves
+behind in the runtime."""
+
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+# A runtime whose n-th launch fails, in front of the real one; like the real one it keeps the last error until that is read.
+RUNTIME = r"""
+static int count = 0, last = 0, fail_at = 0, smem = 0;
+void fake_begin(int at, int before) { count = smem = 0; fail_at = at; last = before; }
+int fake_last(void) { return last; }
+int fake_smem(void) { return smem; }
+static int launched(void) { return ++count == fail_at ? (last = 719) : 0; }
+int __cudaLaunchKernel(void) { return launched(); }
+int cudaLaunchKernel(void) { return launched(); }
+int cudaLaunchKernelExC(void) { return launched(); }
+int __cudaGetKernel(void) { return 0; }
+int cudaFuncSetAttribute(const void* f, int attr, int value) { smem = value; return 0; }
+int cudaMemsetAsync(void) { return 0; }
+int cudaGetLastError(void) { int e = last; last = 0; return e; }
+static int encode(void) { return 0; }
+int cudaGetDriverEntryPointByVersion(const char* name, void** f, unsigned version, unsigned long long flags, int* found) {
+    *f = (void*)encode; *found = 0; return 0;
+}
+"""
+CALLS = r"""
+import ctypes
+from chunked_gated_delta_kda_gb300 import binding
+lib = binding.load_library()
+buf = (ctypes.c_uint8 * 4096)()
+p = ctypes.addressof(buf) + (-ctypes.addressof(buf) % 256)
+big = 1 << 50
+pair, pools = (ctypes.c_longlong * 2)(64, 16), (ctypes.c_void_p * 70)(*[p] * 70)
+chunk = lambda T, keys, H, N: lib.kda_latent_chunk(p, p, 4, 64, p, 2, p, p, 0.0, p, keys, p, p, T, H, N, 0, p, big, None)
+compact = lambda pages: lib.kda_page_compact(p, 2, p, p, pages, p, 4, p, 16, p, p, p, p, p, p, 2, None, None)
+calls = dict(
+    chunk=lambda: chunk(64, 300, 2, 1),
+    chunk_shared=lambda: chunk(64, 8192, 1, 30),
+    fork=lambda: lib.kda_page_fork(p, 2, p, p, p, None, p, 4, p, 4, p, 16, p, p, p, p, 2, 1, None, None),
+    fork_many=lambda: lib.kda_page_fork(p, 2, p, p, p, None, p, 4, p, 4, p, 16, p, p, p, p, 2, 300, None, None),
+    copy=lambda: lib.kda_page_copy(pools, 70, 4, 32, p, None, 1, None, None),
+    free=lambda: lib.kda_page_free(p, 2, p, p, p, 4, p, 4, p, 16, p, p, p, 2, None, None),
+    free_many=lambda: lib.kda_page_free(p, 1000, p, p, p, 4, p, 4, p, 16, p, p, p, 2000, None, None),
+    compact=lambda: compact(4),
+    compact_large=lambda: compact(1 << 21),
+    verify=lambda: lib.kda_verify_drafts(p, p, pair, p, pair, p, p, p, 2, 3, 16, 512, None, None))
+fake = ctypes.CDLL(None)
+for name, call in calls.items():
+    for at, before in ((0, 0), (0, 700), (1, 0), (2, 0), (3, 0)):
+        fake.fake_begin(at, before)
+        print(name, at, before, call(), fake.fake_last())
+for pages in (1, 512, 8192, 1 << 20):
+    fake.fake_begin(0, 0)
+    compact(pages)
+    print("smem", pages, 0, 0, fake.fake_smem())
+"""
+
+
+@pytest.fixture(scope="module")
+def left_behind(tmp_path_factory):
+    """{(call, launch that fails, error there before): (status, error there afterwards)}"""
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    at = tmp_path_factory.mktemp("fake")
+    (at / "fake.c").write_text(RUNTIME)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(at / "fake.so"), str(at / "fake.c")], check=True)
+    out = subprocess.run([sys.executable, "-c", CALLS], env=dict(os.environ, LD_PRELOAD=str(at / "fake.so"), PYTHONPATH=ROOT),
+                         cwd=ROOT, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr[-1000:]
+    return {(name, int(at), int(b)): (int(rc), int(e)) for name, at, b, rc, e in (line.split() for line in out.stdout.splitlines())}
+
+
+def test_compaction_sets_its_kernels_shared_memory_alike_for_every_pool(left_behind):
+    """The limit is the function's, not the call's: another thread's smaller pool must not lower it between the setting
+    and the launch."""
+    set_to = {left_behind["smem", pages, 0][1] for pages in (1, 512, 8192, 1 << 20)}
+    assert len(set_to) == 1 and set_to.pop() >= (1 << 20) // 8

@@ -1,9 +1,11 @@
 """Serving over the paged cache at the edges of its types, sizes and threads."""
 
+import threading
+
 import pytest
 import torch
 
-from test_serving_gpu import BF, FEW, FP, chunk_inputs, run_chunk
+from test_serving_gpu import BF, FEW, FP, chunk_inputs, i32, run_chunk
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,37 @@ def test_chunk_keys_past_the_largest_number_are_infinite(dtype, row, ups):
     q[::2, :, 5] *= -1                                   # rows of either sign in one tile
     o, lse = run_chunk(q, cache, table, lens, w, lens_q)
     assert torch.equal(o[::2], got[1][0][::2]) and torch.equal(lse[::2], got[1][1][::2]) and torch.isnan(o[1::2][meets[1::2]]).all()
+
+
+# ---------------------------------------------------------------------------
+# threads
+def test_pools_of_different_size_are_compacted_by_two_threads():
+    from chunked_gated_delta_kda_gb300 import pages
+    sizes, failed, got = (512, 1 << 20), [], {}
+
+    def work(size):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                held = size // 2
+                order = torch.arange(size, dtype=torch.int32, device="cuda").flip(0)
+                args = order[None, :held].contiguous(), i32([held]), torch.zeros_like(order), order, i32([held]), 1
+                torch.cuda.current_stream().synchronize()
+                for _ in range(3000):
+                    out = pages.page_compact(*args)
+                torch.cuda.current_stream().synchronize()
+                got[size] = [x.cpu() for x in out]
+        except Exception as e:                           # (of a thread: told below)
+            failed.append((size, e))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(size,)) for size in sizes]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for size in sizes:
+        table, _, free, pairs, count, moved = got[size]
+        held = size // 2
+        assert count.item() == held and torch.equal(table[0].sort().values, torch.arange(held, dtype=torch.int32))
+        assert torch.equal(free[held:], torch.arange(held, size, dtype=torch.int32)) and torch.equal(moved[pairs[:, 0].long()], pairs[:, 1])
