@@ -59,6 +59,14 @@ constexpr uint32_t STATUS_BAD_TOKEN = 16u;   // drafts: a token past the vocabul
 constexpr uint32_t WS_HEADER = 256;
 constexpr uint32_t WS_CLEAR = 16;
 
+// Whether a call of the runtime succeeded.  The error of one that did not is
+// told by the entry point's status: it does not stay behind as the last error,
+// where the thread's next launch, of this library or another, would find it.
+inline bool succeeded(cudaError_t e) {
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e == cudaSuccess;
+}
+
 // ---- warp helpers of the token-by-token kernels ----
 
 __device__ __forceinline__ float warp_sum(float x) {

@@ -501,9 +501,9 @@ extern "C" kda_status kda_verify_drafts(const int64_t* draft_tokens, const void*
     p.seg = (int)((V + (aligned ? 0 : pieces - 1) + ctas * DR_WARPS * 512 - 1) / (ctas * DR_WARPS * 512) * 512);   // with room for the shift
     // ranges a power of two apart meet in the same parts of the memory (256 x 131072 in fp32 44 us, so 41; 160 of them 37, 34)
     if (p.seg * size >= 32768u && p.seg * size % 8192u == 0) p.seg += 512;
-    if (p.status && cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    if (p.status && !succeeded(cudaMemsetAsync(p.status, 0, WS_CLEAR, stream))) return KDA_ERR_CUDA;
     const cudaError_t e = (flags & KDA_FLAG_FP32) != 0u   ? launch<float>(p, aligned, N, ctas, stream)
                           : (flags & KDA_FLAG_FP16) != 0u ? launch<__half>(p, aligned, N, ctas, stream)
                                                           : launch<__nv_bfloat16>(p, aligned, N, ctas, stream);
-    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return succeeded(e) ? KDA_OK : KDA_ERR_CUDA;
 }

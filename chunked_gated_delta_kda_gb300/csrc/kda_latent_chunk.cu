@@ -508,7 +508,7 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, latent_chunk_plan_kernel, c) != cudaSuccess) return KDA_ERR_CUDA;
+    if (!succeeded(cudaLaunchKernelEx(&cfg, latent_chunk_plan_kernel, c))) return KDA_ERR_CUDA;
     if (T == 0) return KDA_OK;
     const bool fp16 = (flags & KDA_FLAG_FP16) != 0u;
     if (num_keys > 0) {
@@ -517,14 +517,14 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
             !latent_row_map(&maps.w, w_up, LAT_C, 1, (long long)H * LAT_KV, LAT_C, LAT_TILE))
             return KDA_ERR_CUDA;
         const auto kernel = fp16 ? latent_expand_kernel<true> : latent_expand_kernel<false>;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X_SMEM) != cudaSuccess) return KDA_ERR_CUDA;
+        if (!succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)X_SMEM))) return KDA_ERR_CUDA;
         const long long items = (((long long)num_keys / LAT_TILE + N + 1) / 2) * H;
         cfg.gridDim = dim3(2u * (unsigned)(items < 76 ? items : 76));
         cfg.blockDim = dim3(EX_THREADS);
         cfg.dynamicSmemBytes = X_SMEM;
-        if (cudaLaunchKernelEx(&cfg, kernel, c, maps) != cudaSuccess) return KDA_ERR_CUDA;
+        if (!succeeded(cudaLaunchKernelEx(&cfg, kernel, c, maps))) return KDA_ERR_CUDA;
     }
-    return launch_latent_fwd(p, fp16, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return succeeded(launch_latent_fwd(p, fp16, stream)) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -300,7 +300,10 @@ MARSHAL(latent_chunk, 9)
         type == at::kHalf ? KDA_FLAG_FP16 : 0u, scratch.data_ptr(), scratch.nbytes(), stream); });
     if (status == KDA_OK && given != nullptr && !enough) {
         const size_t bytes = given->nbytes() < (size_t)STATUS_BYTES ? given->nbytes() : (size_t)STATUS_BYTES;
-        if (cudaMemcpyAsync(given->data_ptr(), scratch.data_ptr(), bytes, cudaMemcpyDeviceToDevice, stream) != cudaSuccess) status = KDA_ERR_CUDA;
+        if (cudaMemcpyAsync(given->data_ptr(), scratch.data_ptr(), bytes, cudaMemcpyDeviceToDevice, stream) != cudaSuccess) {
+            (void)cudaGetLastError();
+            status = KDA_ERR_CUDA;
+        }
     }
     return result(status, {out, lse});
     END_HANDLE_TH_ERRORS

@@ -652,10 +652,15 @@ kda_status launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return succeeded(cudaLaunchKernelEx(&cfg, kernel, args...)) ? KDA_OK : KDA_ERR_CUDA;
 }
 
-kda_status launched() { return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+// One that begins behind it.
+template <typename... A>
+kda_status launch(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    void* at[] = {&args...};
+    return succeeded(cudaLaunchKernel(kernel, grid, dim3((unsigned)threads), at, 0, stream)) ? KDA_OK : KDA_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -681,9 +686,7 @@ kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* s
         return KDA_ERR_INVALID_ARG;
     if (off4(parents, children, fork_lens, free_pages, seq_lens_out, free_head_out, pairs)) return KDA_ERR_INVALID_ARG;
     // (an early launch is 1.2 us dearer on the host, which is what a fork of a few requests waits for)
-    if (F <= PG_FEW) page_fork_kernel<true><<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
-    else page_fork_kernel<false><<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
-    return launched();
+    return launch(F <= PG_FEW ? page_fork_kernel<true> : page_fork_kernel<false>, dim3(PG_CTAS), PG_THREADS, stream, p);
 }
 
 kda_status kda_page_copy(void* const* pools, int num_pools, int num_pages, long long page_bytes, const int32_t* pairs,
@@ -700,7 +703,7 @@ kda_status kda_page_copy(void* const* pools, int num_pools, int num_pages, long 
     const long long most_words = COPY_THREADS * COPY_PER;
     p.pieces = (p.words + most_words - 1) / most_words;   // equal ones
     p.piece = (int)((p.words + p.pieces - 1) / p.pieces);
-    if (p.status && cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    if (p.status && !succeeded(cudaMemsetAsync(p.status, 0, WS_CLEAR, stream))) return KDA_ERR_CUDA;
     if (F == 0) return KDA_OK;
     for (int first = 0; first < num_pools; first += COPY_POOLS) {
         p.num_pools = num_pools - first < COPY_POOLS ? num_pools - first : COPY_POOLS;
@@ -752,23 +755,21 @@ kda_status kda_page_compact(const int32_t* block_table, int table_width, const i
         (table_width > 0 && !table_out))
         return KDA_ERR_INVALID_ARG;
     if (off4(free_pages, free_out, pairs, count, table_out) || off(moved, 16)) return KDA_ERR_INVALID_ARG;
-    if (p.status && cudaMemsetAsync(p.status, 0, WS_CLEAR, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    if (p.status && !succeeded(cudaMemsetAsync(p.status, 0, WS_CLEAR, stream))) return KDA_ERR_CUDA;
     const long long cells = (long long)N * table_width;
     if (num_pages <= CP_MOST) {
         const int groups = (num_pages + CP_GROUP - 1) / CP_GROUP, bytes = groups * CP_GROUP_BYTES;
         // (the limit is the kernel's, for all threads that call it: the same for every pool)
-        if (cudaFuncSetAttribute(page_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CP_MOST / CP_GROUP * CP_GROUP_BYTES) != cudaSuccess)
+        if (!succeeded(cudaFuncSetAttribute(page_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CP_MOST / CP_GROUP * CP_GROUP_BYTES)))
             return KDA_ERR_CUDA;
         // an item a thread, though each CTA reads the whole free list (8192 pages, 256 rows of 32: 6 us, with four 11)
         const long long items = cells > num_pages ? cells : num_pages, ctas = (items + PG_THREADS - 1) / PG_THREADS;
         return launch_early(page_compact_kernel, dim3((unsigned)(ctas < 152 ? ctas : 152)), PG_THREADS, bytes, stream, p, table_out);
     }
-    page_compact_large_kernel<<<PG_CTAS, PG_THREADS, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    const kda_status st = launch(page_compact_large_kernel, dim3(PG_CTAS), PG_THREADS, stream, p);
     const long long blocks = (cells + 255) / 256, most = 152ll * 8;
-    if (blocks == 0) return KDA_OK;
-    page_remap_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(p, table_out);
-    return launched();
+    if (st != KDA_OK || blocks == 0) return st;
+    return launch(page_remap_kernel, dim3((unsigned)(blocks < most ? blocks : most)), 256, stream, p, table_out);
 }
 
 }  // extern "C"

@@ -81,3 +81,13 @@ def test_compaction_sets_its_kernels_shared_memory_alike_for_every_pool(left_beh
     and the launch."""
     set_to = {left_behind["smem", pages, 0][1] for pages in (1, 512, 8192, 1 << 20)}
     assert len(set_to) == 1 and set_to.pop() >= (1 << 20) // 8
+
+
+@pytest.mark.parametrize("call,launches", [("chunk", 3), ("chunk_shared", 3), ("fork", 1), ("fork_many", 1), ("copy", 2), ("free", 1),
+                                           ("free_many", 3), ("compact", 1), ("compact_large", 2), ("verify", 1)])
+def test_a_failed_launch_is_told_once(left_behind, call, launches):
+    """A call does not report an error that was there before it, nor leave its own for the thread's next call."""
+    assert left_behind[call, 0, 0] == (0, 0)
+    assert left_behind[call, 0, 700][0] == 0
+    for at in range(1, launches + 1):
+        assert left_behind[call, at, 0] == (3, 0), at
