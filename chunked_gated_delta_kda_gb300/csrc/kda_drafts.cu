@@ -12,7 +12,14 @@
 // at two operations a clock and SM here, less than the rows' bytes leave time
 // for.  So r, its sums and the border are pairs of 32-bit numbers whose
 // rounding errors are kept (Knuth's and Dekker's exact sums), two elements an
-// operation: ten for an element, four without q; sums are good to some 2^-40.
+// operation: ten for an element, four without q.  The errors' own sum has 32
+// bits too, so after 128 additions in a thread (a vocabulary of 2^17 and more)
+// it all goes into a pair in shared memory, which takes no registers from the
+// loads (kept in registers: 128 x 131072 4 % slower).  n additions are off by
+// n^2 2^-48 of their sum at most, a chain of m pairs by 3 m 2^-48, the border
+// by 2^-31 of the total at V = 2^30: less than u can tell apart.  (A replay of
+// 2^18 additions: exponentials of uniform numbers 2^-43, one number again and
+// again 0; without the pairs 2^-29 and 2^-18.)
 //
 // 128 sequences of 131072 in fp32 (134 MB): 21.5 us, 6.2 TB/s, 256 of them
 // 41, 6.6 (with sums in 64 bits where warps join 31, one element an operation
@@ -214,8 +221,9 @@ struct Number {
 // is on 16 bytes (`from` may be below 0: what is in front of the row counts
 // nothing), `to` is V or `from` and a multiple of 512.  LESS: of p - q, whose
 // rows start on 16 bytes where p's do if ALIGNED, and anywhere if not.
+// `carried` is the thread's own.
 template <typename T, bool ALIGNED, bool LESS>
-__device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, int V) {
+__device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, int V, Pair* carried) {
     constexpr int W = 16 / (int)sizeof(T);
     const int lane = threadIdx.x & 31;
     TwoSums sums;
@@ -264,19 +272,26 @@ __device__ __forceinline__ Pair sum_range(const Row<T>& row, int from, int to, i
             }
     };
     // whole steps, where they neither reach past the row nor hold the token that is left out
-    constexpr int MOST = W == 8 ? 4 : LESS ? 4 : 8, STEP = 32 * W * MOST, HALF = 512 / (32 * W);
+    constexpr int MOST = W == 8 ? 4 : LESS ? 4 : 8, STEP = 32 * W * MOST, HALF = 512 / (32 * W), CARRY = 8;
     auto plain = [&](int i, int count) {
         if constexpr (LESS) return i >= (ALIGNED ? 0 : W) && i + count <= to && (ALIGNED || i + count + W <= V);
         else return i >= 0 && i + count <= to && (row.but < i || row.but >= i + count);
     };
-    int i = from;
+    int i = from, steps = 0;
     while (i < to) {
-        for (; plain(i, STEP); i += STEP) chunk(Number<MOST>(), Number<0>(), i);
+        for (; plain(i, STEP); i += STEP) {
+            chunk(Number<MOST>(), Number<0>(), i);
+            if (++steps % CARRY == 0) {
+                *carried = steps == CARRY ? sums.value() : *carried + sums.value();
+                sums = TwoSums();
+            }
+        }
         for (; plain(i, 512); i += 512) chunk(Number<HALF>(), Number<0>(), i);
         if (i < to) chunk(Number<1>(), Number<1>(), i);
         i += 32 * W;
     }
     Pair d = sums.value();
+    if (steps >= CARRY) d = *carried + d;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) d = d + moved(d, [&](float x) { return __shfl_xor_sync(0xffffffffu, x, m); });
     return d;
@@ -296,6 +311,7 @@ __device__ __forceinline__ Pair lanes_upto(Pair x) {
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __grid_constant__ DraftParams p) {
     __shared__ Pair sums[2][DR_SEGS], parts[DR_WARPS], bound_s, total_s;
+    __shared__ Pair carried[DR_THREADS];
     __shared__ int taken_s, drafted_s, seg_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = (int)cluster_size(), rank = (int)cluster_rank(), n = blockIdx.x / ctas;
@@ -350,7 +366,8 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
     cluster_barrier();                           // every CTA's shared memory is there
     for (int round = 0;; ++round) {
         const int from = (int)min((long long)p.V, (long long)mine * p.seg - shift), to = (int)min((long long)p.V, (long long)from + p.seg);
-        const Pair d = row.kind == P_LESS_Q ? sum_range<T, ALIGNED, true>(row, from, to, p.V) : sum_range<T, ALIGNED, false>(row, from, to, p.V);
+        const Pair d = row.kind == P_LESS_Q ? sum_range<T, ALIGNED, true>(row, from, to, p.V, carried + tid)
+                                            : sum_range<T, ALIGNED, false>(row, from, to, p.V, carried + tid);
         if (lane < ctas) {
             const uint32_t at = cluster_addr(smem_u32(&sums[round][mine]), lane);
             asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(d.h), "f"(d.l) : "memory");
@@ -410,14 +427,19 @@ __global__ void __launch_bounds__(DR_THREADS, 2) verify_drafts_kernel(const __gr
     const Pair bound = bound_s;
     const int from = seg * p.seg - shift, to = (int)min((long long)p.V, (long long)from + p.seg);
     const int each = p.seg / DR_THREADS, a = max(0, min(to, from + tid * each)), b = max(0, min(to, from + (tid + 1) * each));
-    Sum sum;
+    auto some = [&](int first, int last) {
+        Sum sum;
 #pragma unroll 8
-    for (int i = a; i < b; ++i) {
-        float h, l;
-        row.at(i, h, l);
-        sum.add(h, l);
-    }
-    const Pair own = sum.value(), upto = lanes_upto(own);
+        for (int i = first; i < last; ++i) {
+            float h, l;
+            row.at(i, h, l);
+            sum.add(h, l);
+        }
+        return sum.value();
+    };
+    Pair own = some(a, min(b, a + 64));
+    for (int i = a + 64; i < b; i += 64) own = own + some(i, min(b, i + 64));
+    const Pair upto = lanes_upto(own);
     if (lane == 31) parts[warp] = upto;
     __syncthreads();
     // the first warp whose runs reach above the border, else the last with weight; all others are done

@@ -730,11 +730,11 @@ kda_status kda_page_compact(const int32_t* block_table, int table_width, const i
  *   flags       KDA_FLAG_FP32 or KDA_FLAG_FP16 (else bf16), of both
  *               probabilities
  *   workspace   NULL, or the 256-byte status header
- * The comparisons are exact and the sums good to some 2^-46.  Probabilities
- * need not sum to one; what is not above zero, NaN included, has no weight.  A
- * token >= V ends the drafts as a negative one does, and r without weight, or
- * with an infinite one, gives a token in [0, V) that means nothing; both set
- * KDA_ERR_BAD_TOKEN.
+ * The comparisons are exact; the sums and the border are good to 2^-31 of the
+ * total for any V (u tells 2^-24 apart).  Probabilities need not sum to one;
+ * what is not above zero, NaN included, has no weight.  A token >= V ends the
+ * drafts as a negative one does, and r without weight, or with an infinite
+ * one, gives a token in [0, V) that means nothing; both set KDA_ERR_BAD_TOKEN.
  */
 kda_status kda_verify_drafts(const int64_t* draft_tokens, const void* draft_probs, const long long* draft_strides,
                              const void* target_probs, const long long* target_strides, const float* uniform,

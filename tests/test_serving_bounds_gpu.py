@@ -1,11 +1,12 @@
 """Serving over the paged cache at the edges of its types, sizes and threads."""
 
 import threading
+from fractions import Fraction
 
 import pytest
 import torch
 
-from test_serving_gpu import BF, FEW, FP, chunk_inputs, i32, run_chunk
+from test_serving_gpu import BF, F32, FEW, FP, check_drafts, chunk_inputs, draft_inputs, i32, run_chunk, verify
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,60 @@ def test_pools_of_different_size_are_compacted_by_two_threads():
         held = size // 2
         assert count.item() == held and torch.equal(table[0].sort().values, torch.arange(held, dtype=torch.int32))
         assert torch.equal(free[held:], torch.arange(held, size, dtype=torch.int32)) and torch.equal(moved[pairs[:, 0].long()], pairs[:, 1])
+
+
+# ---------------------------------------------------------------------------
+# long rows of probabilities
+def halves_row(V, numbers, dtype):
+    """[1, 1, V], the first half of it one number, the second half another."""
+    row = torch.full((1, 1, V), numbers[0], dtype=dtype, device="cuda")
+    row[..., V // 2:] = numbers[1]
+    return row
+
+
+def check_halves(tokens, u, V, ends, weights, slack):
+    """Drawn tokens of a row whose weights are 0, then weights[0] from ends[0] on and weights[1] from V / 2 on: each
+    one's sums, exact, enclose its border within slack of the total."""
+    a, b = (Fraction(w) for w in weights)
+    upto = lambda i: a * (min(i, V // 2) - ends) + b * max(0, i - V // 2)  # noqa: E731  (weight of the tokens before i)
+    total = upto(V)
+    for token, x in zip(tokens.tolist(), u.tolist()):
+        assert ends <= token < V
+        border, off = Fraction(x) * total, Fraction(slack) * total
+        assert upto(token) <= border + off and upto(token + 1) > border - off, (token, float((upto(token + 1) - border) / total))
+
+
+ROWS = 153   # as many as leave a sequence one CTA, whose sums are the longest
+
+
+@pytest.mark.parametrize("V,slack", [(1 << 18, 2.0 ** -40), (1 << 22, 2.0 ** -33), (1 << 28, 2.0 ** -31)])
+def test_drafts_of_long_rows(V, slack):
+    """A number whose sums round the same way for many steps, beside one that is summed exactly; all sequences read one
+    row."""
+    weights = 1.0, torch.tensor(1.74220228).item()
+    target = halves_row(V, weights, F32).expand(ROWS, 1, V)
+    u = torch.rand(ROWS, 1, generator=torch.Generator().manual_seed(V))
+    out, n = verify(torch.zeros(ROWS, 0, dtype=torch.int64, device="cuda"), target, u.cuda())
+    assert (n == 1).all()
+    check_halves(out[:, 0].cpu(), u[:, 0], V, 0, weights, slack)
+    one = halves_row(V, weights, F32)          # and by eight
+    out, _ = verify(torch.zeros(1, 0, dtype=torch.int64, device="cuda"), one, u[:1].cuda())
+    check_halves(out[:, 0].cpu(), u[:1, 0], V, 0, weights, slack)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_drafts_of_long_rows_with_a_proposers(dtype):
+    """max(p - q, 0) of two rows; the draft has no probability and is rejected."""
+    V, S = 1 << 26, 1
+    p, q = halves_row(V, (1.5, 1.7421875), dtype), halves_row(V, (0.5, 0.0145111083984375), dtype)
+    weights = [float(p[0, 0, i].double() - q[0, 0, i].double()) for i in (0, V - 1)]
+    p[..., 0] = 0
+    u = torch.rand(ROWS, 2, generator=torch.Generator().manual_seed(5))
+    out, n = verify(torch.zeros(ROWS, S, dtype=torch.int64, device="cuda"), p.expand(ROWS, 2, V), u.cuda(), q.expand(ROWS, 1, V))
+    assert (n == 1).all() and (out[:, 1] == -1).all()
+    check_halves(out[:, 0].cpu(), u[:, 1], V, 1, weights, 2.0 ** -31)
+
+
+@pytest.mark.parametrize("V,dtype", [(262144, F32), (262147, BF), (1000003, FP)])
+def test_drafts_of_large_vocabularies(V, dtype):
+    check_drafts(*draft_inputs(2, 1, V, dtype, seed=V))
