@@ -268,7 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EX_THREADS, 1)
     cluster_barrier();                                             // both SMs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + X_TMEM);
-    // the plan; what follows this kernel may set itself up
+    // The plan; then what follows may begin.  In this order: latent_share_kernel runs beside this kernel, reads the plan's
+    // cu_k and writes its records over those that the call before has read, with no wait of its own in front.
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const int all_tiles = p.tiles[p.N];
     const long long total = (long long)((all_tiles + 1) / 2) * p.H;

@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     int4 item = make_int4(0, 0, 1, 0);
     if constexpr (CHUNK && SPLIT != SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");   // the expanded keys
     if constexpr (SPLIT == SHARED) {
-        // only the records are waited for: the tensors were there before the kernel that writes them began
-        asm volatile("griddepcontrol.wait;");
+        // The records are waited for.  The tensors were there before the kernel that writes them began; expanded keys come
+        // beside it, and it ends behind them.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         const volatile int* at = reinterpret_cast<const volatile int*>(p.share_items + blockIdx.x / p.H);
         item = make_int4(at[0], at[1], at[2], at[3]);
         slot = item.x;

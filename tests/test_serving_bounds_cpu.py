@@ -1,7 +1,9 @@
 """Serving entry points on the host, without a GPU: what a call sets and leaves
-behind in the runtime."""
+behind in the runtime, and what the sources have to say for it."""
 
+import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -91,3 +93,29 @@ def test_a_failed_launch_is_told_once(left_behind, call, launches):
     assert left_behind[call, 0, 700][0] == 0
     for at in range(1, launches + 1):
         assert left_behind[call, at, 0] == (3, 0), at
+
+
+def source(name):
+    with open(os.path.join(ROOT, "chunked_gated_delta_kda_gb300", "csrc", name)) as f:
+        return f.read()
+
+
+def test_memory_is_read_behind_the_wait_for_the_kernel_before():
+    """A wait that the compiler may move loads over is none."""
+    waits = 0
+    for path in glob.glob(os.path.join(ROOT, "chunked_gated_delta_kda_gb300", "csrc", "*.cu*")):
+        for line in source(os.path.basename(path)).splitlines():
+            if "griddepcontrol.wait" in line:
+                waits += 1
+                assert re.search(r'asm volatile\(".*griddepcontrol\.wait;.*" ::: "memory"\)', line), (path, line)
+    assert waits > 10
+
+
+def test_the_expansion_lets_the_next_kernel_begin_behind_its_own_wait():
+    """latent_share_kernel, launched behind the expansion, reads the plan that the expansion waits for, without a wait."""
+    text = source("kda_latent_chunk.cu")
+    kernel = text[text.index("latent_expand_kernel("):]
+    assert kernel.index("griddepcontrol.wait") < kernel.index("griddepcontrol.launch_dependents")
+    share = source("kda_latent_fwd.cu")
+    share = share[share.index("latent_share_kernel("):]
+    assert share.index("p.cu_k") < share.index("griddepcontrol.wait")
