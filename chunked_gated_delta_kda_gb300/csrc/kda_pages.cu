@@ -28,6 +28,7 @@ constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_ALL = PG_CTAS * PG_THREADS;
 constexpr int PG_SHARES = PG_CTAS * PG_WARPS;    // the cluster's warps, each with a share of the pages
 constexpr long long FREE_ALONE = 1 << 17;        // cells that the cluster gives back by itself
+constexpr int PG_MOST = 1 << 30;                 // rows, columns, pages, entries: an index that steps past them stays in 32 bits
 
 struct PageParams {
     const int32_t* table;
@@ -635,6 +636,7 @@ bool off4(const P*... p) { return (off(p, 4) || ...); }
 // What the three share: sizes, the table, the free list, the status header.
 bool common_ok(const PageParams& p, const void* table) {
     if (p.N < 1 || p.width < 0 || p.num_pages < 1 || p.num_free < 0 || p.page_size < 1) return false;
+    if (p.N > PG_MOST || p.width > PG_MOST || p.num_pages > PG_MOST || p.num_free > PG_MOST) return false;
     if ((p.width > 0 && !table) || missing(p.lens, p.refs, p.refs_out, p.free_head)) return false;
     return !off4(table, p.lens, p.refs, p.free_head) && !off(p.refs_out, 16) && !off(p.status, 256);
 }
@@ -681,7 +683,7 @@ kda_status kda_page_fork(int32_t* block_table, int table_width, const int32_t* s
     p.free_pages = free_pages, p.free_head = free_head, p.lens_out = seq_lens_out, p.refs_out = refs_out;
     p.head_out = free_head_out, p.pairs = pairs;
     p.width = table_width, p.num_pages = num_pages, p.num_free = num_free, p.page_size = page_size, p.N = N, p.F = F;
-    if (!common_ok(p, block_table) || F < 0) return KDA_ERR_INVALID_ARG;
+    if (!common_ok(p, block_table) || F < 0 || F > PG_MOST) return KDA_ERR_INVALID_ARG;
     if (missing(seq_lens_out, free_head_out) || (F > 0 && missing(parents, children, pairs)) || (num_free > 0 && !free_pages))
         return KDA_ERR_INVALID_ARG;
     if (off4(parents, children, fork_lens, free_pages, seq_lens_out, free_head_out, pairs)) return KDA_ERR_INVALID_ARG;
@@ -733,7 +735,9 @@ kda_status kda_page_free(const int32_t* block_table, int table_width, const int3
     const long long blocks = ((long long)num_pages / 4 + 255) / 256 + 1;
     kda_status st = launch_early(page_owners_kernel, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), 256, 0, stream, p);
     if (st != KDA_OK) return st;
-    const int warps = 152 * 8 * 4, rows = N <= warps ? 1 : N / warps < 32 ? N / warps : 32;
+    const int warps = 152 * 8 * 4, fit = PG_MOST / table_width;   // (a warp counts its rows' cells in 32 bits)
+    int rows = N <= warps ? 1 : N / warps < 32 ? N / warps : 32;
+    rows = rows < fit ? rows : fit;
     const long long groups = ((long long)N + 8ll * rows - 1) / (8ll * rows);
     st = launch_early(page_release_kernel, dim3((unsigned)(groups < 152 * 8 ? groups : 152 * 8)), 256, 0, stream, p, rows);
     if (st != KDA_OK) return st;

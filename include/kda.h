@@ -611,7 +611,8 @@ kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int
  * workspaces as above; a row of the table has ceil(seq_lens / page_size)
  * pages.  refs, lengths and free_head are not written: the functions give
  * them anew, and outputs may not overlap inputs.  refs_out and moved are on 16
- * bytes.  page_size is any positive number here.
+ * bytes.  page_size is any positive number here; rows, columns, pages, entries
+ * of the free list and forks are 2^30 at most.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -10,6 +10,10 @@ import sys
 
 import pytest
 
+from test_serving_cpu import caller, cpu_only, host_block
+
+from chunked_gated_delta_kda_gb300 import binding
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 # A runtime whose n-th launch fails, in front of the real one; like the real one it keeps the last error until that is read.
@@ -119,3 +123,24 @@ def test_the_expansion_lets_the_next_kernel_begin_behind_its_own_wait():
     share = source("kda_latent_fwd.cu")
     share = share[share.index("latent_share_kernel("):]
     assert share.index("p.cu_k") < share.index("griddepcontrol.wait")
+
+
+@cpu_only
+def test_sizes_that_an_index_could_step_out_of_are_refused():
+    """The pages' kernels walk rows, columns and pages in steps of up to 155648 with 32-bit numbers."""
+    keep, p = host_block()
+    lib = binding.load_library()
+    shared = dict(table=p, width=2, lens=p, refs=p, pages=4, free=p, free_n=4, head=p, page=16)
+    last = dict(N=2, ws=p, stream=None)
+    fork = caller(lib.kda_page_fork, dict(
+        table=p, width=2, lens=p, parents=p, children=p, fork_lens=None, refs=p, pages=4, free=p, free_n=4, head=p, page=16, lens_out=p,
+        refs_out=p, head_out=p, pairs=p, N=2, F=1, ws=p, stream=None))
+    free = caller(lib.kda_page_free, dict(
+        table=p, width=2, lens=p, keep=p, refs=p, pages=4, free=p, free_n=4, head=p, page=16, lens_out=p, refs_out=p, head_out=p, **last))
+    compact = caller(lib.kda_page_compact, dict(
+        **shared, table_out=p, refs_out=p, free_out=p, pairs=p, count=p, moved=p, **last))
+    for big in (2 ** 30 + 1, 2 ** 31 - 1):
+        for call in (fork, free, compact):
+            for name in ("N", "width", "pages", "free_n"):
+                assert call(**{name: big}) == 1, (name, big)
+        assert fork(F=big) == 1

@@ -6,7 +6,9 @@ from fractions import Fraction
 import pytest
 import torch
 
-from test_serving_gpu import BF, F32, FEW, FP, check_drafts, chunk_inputs, draft_inputs, i32, run_chunk, verify
+from oracle import serving as sv
+from test_serving_gpu import (BF, F32, FEW, FP, check_drafts, chunk_inputs, draft_inputs, i32, lengths, pages, pool_state, run_chunk,
+                              status, verify)
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +131,18 @@ def test_drafts_of_long_rows_with_a_proposers(dtype):
 @pytest.mark.parametrize("V,dtype", [(262144, F32), (262147, BF), (1000003, FP)])
 def test_drafts_of_large_vocabularies(V, dtype):
     check_drafts(*draft_inputs(2, 1, V, dtype, seed=V))
+
+
+# ---------------------------------------------------------------------------
+# pages
+@pytest.mark.parametrize("n,width", [(255, 512), (256, 512), (257, 512), (4, 40000)])
+def test_rejected_drafts_in_tables_around_the_border(n, width):
+    """Up to seven tokens back, in tables of as many cells as one cluster gives back, and of more."""
+    lens = lengths(n, 16 * width, n)
+    table, refs, free, head = pool_state(lens, 16, 64, n, 1, width)
+    keep = [max(0, l - (i * 5) % 8) for i, l in enumerate(lens)]
+    f = i32(free)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    got = pages().page_free(table.cuda(), i32(lens), i32(keep), i32(refs), f, i32([head]), 16, workspace=ws)
+    wl, wr, wf, wh = sv.page_free(table, lens, keep, refs, free, head, 16)
+    assert status(ws) == 0 and got[0].tolist() == wl and got[1].tolist() == wr and got[2].item() == wh and f.tolist() == wf
