@@ -62,7 +62,7 @@ def load_library(path: Optional[str] = None):
     if _lib is not None:
         return _lib
     if path is None:
-        path = _build.LIB if _build.up_to_date() else _build.build()
+        path = _build.build_library()
     lib = ctypes.CDLL(path)
     vp, i, f, sz, u = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint
     lib.kda_fwd.restype = ctypes.c_int
@@ -135,8 +135,10 @@ def load_marshal():
     if _marshal is None:
         load_library()
         from importlib import machinery, util
-        spec = util.spec_from_file_location("kda_marshal", _build.MARSHAL,
-                                            loader=machinery.ExtensionFileLoader("kda_marshal", _build.MARSHAL))
+        path = _build.marshal()
+        if not _build.marshal_up_to_date():
+            _build.build()
+        spec = util.spec_from_file_location("kda_marshal", path, loader=machinery.ExtensionFileLoader("kda_marshal", path))
         module = util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _marshal = module

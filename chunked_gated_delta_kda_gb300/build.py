@@ -1,10 +1,12 @@
 """Build ``libkda.so`` (the C-ABI KDA forward library) in-tree with nvcc, and
-``kda_marshal.so``, a Python module between torch and some of its entry points.
+``kda_marshal.*.so``, a Python module between torch and some of its entry points.
 
 Each ``csrc/*.cu`` is compiled for sm_103a in parallel, then linked into
 ``chunked_gated_delta_kda_gb300/_build/libkda.so`` against the shared CUDA
 runtime; beside them ``csrc/kda_marshal.cpp`` by the host compiler against the
-installed torch.  Rebuilds only when a source or header is newer.
+installed torch, whose version is part of the module's file name.  The library
+needs neither torch nor its headers.  Rebuilds only when a source or header is
+newer.
 """
 
 from __future__ import annotations
@@ -21,7 +23,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libkda.so")
-MARSHAL = os.path.join(OUT, "kda_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "kda_marshal.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -37,16 +39,24 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "kda.h"),
-                                                                  os.path.join(CSRC, "kda_marshal.cpp"), os.path.abspath(__file__)]
+def marshal() -> str:
+    """Path of the Python module for this torch and Python, whose C++ and C interfaces it is compiled against."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(OUT, f"kda_marshal.torch-{torch.__version__}-{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+def _newer(path, deps) -> bool:
+    deps = [*deps, os.path.join(ROOT, "include", "kda.h"), os.path.abspath(__file__)]
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+def marshal_up_to_date() -> bool:
+    return _newer(marshal(), [MARSHAL_SOURCE])
 
 
 def _marshal_commands():
@@ -59,48 +69,68 @@ def _marshal_commands():
     obj = os.path.join(OUT, "kda_marshal.o")
     host = os.environ.get("CXX") or shutil.which("g++") or "c++"
     compile_ = [host, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                *(f"-I{p}" for p in include), "-c", os.path.join(CSRC, "kda_marshal.cpp"), "-o", obj]
+                *(f"-I{p}" for p in include), "-c", MARSHAL_SOURCE, "-o", obj]
     libs = os.path.join(at, "lib")
-    link = [host, "-shared", "-o", MARSHAL + f".tmp{os.getpid()}", obj, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+    link = [host, "-shared", "-o", marshal() + f".tmp{os.getpid()}", obj, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
             "-ltorch_cuda", "-lc10", "-lc10_cuda", LIB, "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
     return compile_, link
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and up_to_date():
+def _start(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(procs, show) -> None:
+    """Wait for the compilers [(source, process)]; raises what failed."""
+    failed = []
+    for src, pr in procs:
+        text = pr.communicate()[0].decode(errors="replace")
+        if pr.returncode != 0:
+            failed.append(f"--- {src}\n{text}")
+        elif show:
+            print(text, file=sys.stderr)
+    if failed:
+        raise RuntimeError("compiling failed:\n" + "\n".join(failed))
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """``libkda.so``, which needs nvcc alone."""
+    if not force and library_up_to_date():
         return LIB
     nvcc = _nvcc()
     os.makedirs(OUT, exist_ok=True)
-    procs = []
-    objs = []
+    procs, objs = [], []
     for src in sources():
-        obj = os.path.join(OUT, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
+        objs.append(os.path.join(OUT, os.path.basename(src)[:-3] + ".o"))
+        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", objs[-1]]
         if ptxas_info:
             cmd.insert(1, "-Xptxas=-v")
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-        objs.append(obj)
-    compile_, link = _marshal_commands()
-    procs.append(("kda_marshal.cpp", subprocess.Popen(compile_, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
-    for src, pr in procs:
-        out, _ = pr.communicate()
-        text = out.decode(errors="replace")
-        if pr.returncode != 0:
-            failed.append((src, text))
-        elif verbose or ptxas_info:
-            print(text, file=sys.stderr)
-    if failed:
-        msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"compiling failed:\n{msg}")
+        procs.append((src, _start(cmd, verbose)))
+    _finish(procs, verbose or ptxas_info)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, "-Xlinker", "-soname=libkda.so", *objs]
-    subprocess.run(cmd, check=True)
+    subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, "-Xlinker", "-soname=libkda.so", *objs], check=True)
     os.replace(tmp, LIB)
-    subprocess.run(link, check=True)
-    os.replace(link[3], MARSHAL)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """The library and the Python module, compiled beside each other.  A module that does not compile raises when the
+    library is there."""
+    beside = None
+    if force or not marshal_up_to_date():
+        os.makedirs(OUT, exist_ok=True)
+        compile_, link = _marshal_commands()
+        beside = _start(compile_, verbose)
+    try:
+        build_library(force, verbose, ptxas_info)
+    finally:
+        if beside:
+            _finish([("kda_marshal.cpp", beside)], verbose)
+    if beside:
+        subprocess.run(link, check=True)
+        os.replace(link[3], marshal())
     return LIB
 
 

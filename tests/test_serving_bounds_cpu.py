@@ -1,6 +1,7 @@
 """Serving entry points on the host, without a GPU: what a call sets and leaves
 behind in the runtime, and what the sources have to say for it."""
 
+import ctypes
 import glob
 import os
 import re
@@ -9,10 +10,11 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from test_serving_cpu import caller, cpu_only, host_block
 
-from chunked_gated_delta_kda_gb300 import binding
+from chunked_gated_delta_kda_gb300 import binding, build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -37,7 +39,7 @@ int cudaGetDriverEntryPointByVersion(const char* name, void** f, unsigned versio
 """
 CALLS = r"""
 import ctypes
-from chunked_gated_delta_kda_gb300 import binding
+from chunked_gated_delta_kda_gb300 import binding, build
 lib = binding.load_library()
 buf = (ctypes.c_uint8 * 4096)()
 p = ctypes.addressof(buf) + (-ctypes.addressof(buf) % 256)
@@ -144,3 +146,31 @@ def test_sizes_that_an_index_could_step_out_of_are_refused():
             for name in ("N", "width", "pages", "free_n"):
                 assert call(**{name: big}) == 1, (name, big)
         assert fork(F=big) == 1
+
+
+def test_the_library_is_built_without_torchs_headers(tmp_path, monkeypatch):
+    """A module that does not compile says so, and the library it would have called is there all the same."""
+    tiny = tmp_path / "tiny.cu"
+    tiny.write_text('extern "C" int tiny() { return 5; }\n')
+    monkeypatch.setattr(build, "OUT", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libkda.so"))
+    monkeypatch.setattr(build, "sources", lambda: [str(tiny)])
+    monkeypatch.setattr(build, "_marshal_commands", lambda: (["false"], ["false", "-shared", "-o", str(tmp_path / "x")]))
+    with pytest.raises(RuntimeError, match="kda_marshal"):
+        build.build()
+    assert ctypes.CDLL(str(tmp_path / "libkda.so")).tiny() == 5
+
+
+def test_the_module_of_another_torch_is_not_taken(tmp_path, monkeypatch):
+    """It is compiled against torch's C++ and Python's C interfaces."""
+    monkeypatch.setattr(build, "OUT", str(tmp_path))
+    here = build.marshal()
+    open(here, "w").close()
+    assert build.marshal_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0")
+        assert build.marshal() != here and not build.marshal_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(build.sysconfig, "get_config_var", lambda name: ".cpython-0.so")
+        assert not build.marshal_up_to_date()
+    assert build.marshal_up_to_date()
