@@ -146,3 +146,79 @@ def test_rejected_drafts_in_tables_around_the_border(n, width):
     got = pages().page_free(table.cuda(), i32(lens), i32(keep), i32(refs), f, i32([head]), 16, workspace=ws)
     wl, wr, wf, wh = sv.page_free(table, lens, keep, refs, free, head, 16)
     assert status(ws) == 0 and got[0].tolist() == wl and got[1].tolist() == wr and got[2].item() == wh and f.tolist() == wf
+
+
+def test_lengths_past_the_table_are_clipped_when_pages_go_back():
+    """A row of 1000 tokens in a table of three pages of four gives back three."""
+    table = torch.tensor([[4, 5, 6], [7, -1, -1]], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    shared = [0, 0, 0, 0, 1, 0, 0, 0]
+    for keep, listed, head, refs in ((0, [9, 4, 5, 6], 1, [0] * 8), (5, [9, 0, 4, 6], 3, shared), (12, [9, 0, 4, 5], 4, shared)):
+        free = i32([9, 0, 4, 5, 0, 1, 2, 3])
+        lens, r, h = pages().page_free(table, i32([1000, 4]), i32([keep, 4]), i32(refs), free, i32([4]), 4, workspace=ws)
+        assert status(ws) == 8 and lens.tolist() == [keep, 4] and r.tolist() == refs and h.tolist() == [head]
+        assert free.tolist() == listed + [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("P", [2 ** 20, 2 ** 20 + 1, 2 ** 20 + 300])
+def test_owners_and_tables_move_with_their_pages(P):
+    """Several rows, some shorter than the table, that share pages: owners, tables and numbers as the definition gives
+    them, in pools on either side of what fits as bits."""
+    g = torch.Generator().manual_seed(P)
+    lens = [0, 3, 5000, 4999, 1, 700, 5000 - 64, 16]
+    need = [-(-n // 2) for n in lens]
+    width, used = max(need) + 2, sum(need)
+    order = torch.randperm(P, generator=g).to(torch.int32)
+    table = torch.randint(-3, P + 3, (len(lens), width), generator=g).to(torch.int32)
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = order[at:at + n]
+        at += n
+    refs = torch.zeros(P, dtype=torch.int32)
+    refs[order[:used].long()] = torch.randint(0, 1000, (used,), generator=g).to(torch.int32)
+    got = [x.cpu() for x in pages().page_compact(table.cuda(), i32(lens), refs.cuda(), order.cuda(), i32([used]), 2)]
+    free = torch.zeros(P, dtype=torch.bool)
+    free[order[used:].long()] = True
+    holes, movers = free[:used].nonzero()[:, 0], (~free[used:]).nonzero()[:, 0] + used
+    moved = torch.where(free, -1, torch.arange(P)).to(torch.int32)
+    moved[movers] = holes.to(torch.int32)
+    new = torch.zeros(P, dtype=torch.int32)
+    new[moved[~free].long()] = refs[~free]
+    out = torch.full_like(table, -1)
+    for i, n in enumerate(need):
+        out[i, :n] = moved[table[i, :n].long()]
+    assert torch.equal(got[0], out) and torch.equal(got[1], new) and torch.equal(got[5], moved)
+    assert torch.equal(got[2], torch.cat([order[:used], torch.arange(used, P, dtype=torch.int32)]))
+    k = len(holes)
+    assert got[4].item() == k and (got[3][k:] == -1).all() and torch.equal(got[3][:k], torch.stack([movers, holes], 1).to(torch.int32))
+
+
+# ---------------------------------------------------------------------------
+# together
+def test_drafts_leave_greedy_decoding_as_it_is_past_the_border_of_few_keys():
+    """A prompt that ends in front of 2048 rows, where keys are two numbers, and goes on behind them; and a longer one."""
+    from chunked_gated_delta_kda_gb300.latent_serving import Decoder
+    g = torch.Generator(device="cuda").manual_seed(9)
+    lens = [2040, 2300]
+    prompt = torch.randint(0, 50, (sum(lens),), generator=g, device="cuda")
+    plain, quick = (Decoder(50, 256, 4, 2, pages=320, width=160, page_size=16, temper=1e4, seed=2) for _ in range(2))
+    u = lambda s: torch.rand(2, s, generator=g, device="cuda")  # noqa: E731
+    first = plain.start(prompt, i32(lens), u(1)[:, 0])
+    assert torch.equal(first, quick.start(prompt, i32(lens), u(1)[:, 0]))
+    want = [first]
+    for _ in range(20):
+        want.append(plain.step(want[-1], first.new_empty(2, 0), u(1))[0][:, 0])
+    want = torch.stack(want, 1).tolist()
+    texts, steps = [[t] for t in first.tolist()], 0
+    while min(len(t) for t in texts) < 21:
+        guess = []
+        for i, t in enumerate(texts):                    # right up to a place that moves from step to step
+            right = (want[i] + [0] * 9)[len(t):len(t) + 3]
+            guess.append([r if k < (steps + i) % 4 else (r + 1) % 50 for k, r in enumerate(right)])
+        out, count = quick.step(torch.tensor([t[-1] for t in texts], device="cuda"), torch.tensor(guess, device="cuda"), u(4))
+        for t, row, c in zip(texts, out.tolist(), count.tolist()):
+            t += row[:c]
+        steps += 1
+    for i in range(2):
+        assert texts[i][:21] == want[i]
+    assert steps < 20 and quick.layer.lens[0] > 2048
