@@ -185,7 +185,7 @@ __global__ void __cluster_dims__(PG_CTAS, 1, 1) __launch_bounds__(PG_THREADS, 1)
                 if (f.w >= 0) {
                     const long long at = (long long)head + f.w;
                     int own = at >= 0 && at < p.num_free ? p.free_pages[at] : -1;
-                    if (own >= p.num_pages) own = -1;
+                    if (own < 0 || own >= p.num_pages) own = -1;
                     const int old = from[full];
                     if (own < 0 || old < 0 || old >= p.num_pages) bad = true;
                     else pair = make_int2(old, own);

@@ -160,6 +160,16 @@ def test_lengths_past_the_table_are_clipped_when_pages_go_back():
         assert free.tolist() == listed + [0, 1, 2, 3]
 
 
+@pytest.mark.parametrize("listed", [-7, -1, 8, 1 << 30])
+def test_a_listed_page_that_is_none_becomes_none_in_a_forks_table(listed):
+    table = torch.tensor([[4, 5, 6], [-1, -1, -1], [-1, -1, -1]], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    lens, refs, head, pairs = pages().page_fork(table, i32([10, 0, 0]), i32([0, 0]), i32([1, 2]), i32([0] * 8), i32([4, 5, 6, listed, 3]),
+                                                i32([3]), 4, workspace=ws)
+    assert status(ws) == 8 and table.tolist() == [[4, 5, 6], [4, 5, -1], [4, 5, 3]] and pairs.tolist() == [[-1, -1], [6, 3]]
+    assert lens.tolist() == [10, 10, 10] and refs.tolist() == [0, 0, 0, 0, 2, 2, 0, 0] and head.tolist() == [5]
+
+
 @pytest.mark.parametrize("P", [2 ** 20, 2 ** 20 + 1, 2 ** 20 + 300])
 def test_owners_and_tables_move_with_their_pages(P):
     """Several rows, some shorter than the table, that share pages: owners, tables and numbers as the definition gives
