@@ -21,14 +21,14 @@
 // 2^18 additions: exponentials of uniform numbers 2^-43, one number again and
 // again 0; without the pairs 2^-29 and 2^-18.)
 //
-// 128 sequences of 131072 in fp32 (134 MB): 21.5 us, 6.2 TB/s, 256 of them
-// 41, 6.6 (with sums in 64 bits where warps join 31, one element an operation
-// 23).  One sequence of 32768: 6.6 us: the launch, the drafts' two rounds of
-// loads, the row's, the cluster's exchange and the last range's, about one each.
-// Rows of odd length start anywhere: the warps' ranges begin on 16 bytes of p,
-// and q's words are shifted together (256 x 50257 in bf16 without q 12.5 us;
-// element by element 28).  16-bit rows with q are bound by their operations
-// (256 x 65536: 19 us, 3.6 TB/s).
+// In a graph: 128 sequences of 131072 in fp32 (134 MB) 21.7 us, 6.2 TB/s (26.5
+// called one by one), 256 of them 41, 6.6 (with sums in 64 bits where warps join
+// 31, one element an operation 23).  One sequence of 32768: 6.6 us: the launch,
+// the drafts' two rounds of loads, the row's, the cluster's exchange and the last
+// range's, about one each.  Rows of odd length start anywhere: the warps' ranges
+// begin on 16 bytes of p, and q's words are shifted together (256 x 50257 in bf16
+// without q 12.5 us; element by element 28).  16-bit rows with q are bound by
+// their operations (256 x 65536: 18.5 us, 3.6 TB/s).
 #include <cstdint>
 #include <type_traits>
 

@@ -11,8 +11,9 @@
 // __ldcg).  Compacting needs no steps (see there).  Measured, in a graph: 256
 // forks of up to 128 pages 8 us, 8 forks 5; 256 requests that go back by up
 // to seven tokens 8.6; 2048 that end or stay, 100 thousand cells, 17.5; 512
-// pages compacted in 4.3, 8192 in 6.0, a million in 121.  Copying pages is
-// bound by HBM: 150 MB each way 86 us, 93 % of what a plain copy reaches.
+// pages compacted in 4.3, 8192 in 6.0, a million in 121 (each CTA reads the
+// whole free list, through the L2).  Copying pages is bound by HBM: 297 MB each
+// way 91 us, 6.5 TB/s, 96 % of what a plain copy reaches.
 #include <cstdint>
 
 #include "kda.h"
@@ -323,8 +324,11 @@ __device__ __forceinline__ void release_rows(const PageParams& p, int warp, int 
 __device__ __forceinline__ int owners(int refs) { return max(refs, 0); }
 
 // Where many cells may be given back, the whole GPU does that, in two kernels in front of the cluster, whose eight SMs
-// take about a cell a clock each (rows of 256 cells, two in three given back, by the cluster alone / so: 512 18 / 12 us,
-// 1024 28 / 17, 2048 47 / 27; 256 12 / 9, but two more launches are 5 us on the host).
+// take about a cell a clock each.  How many are given back only the device knows.  The limit, of the table's cells, is
+// where a step of drafts breaks even, which gives back few; where requests end it would be lower.  Rows of 512 cells, us
+// a call, by the cluster alone / so: a step that takes back up to seven tokens 64 rows 7.1 / 10, 128 7.8 / 10, 256
+// 9.9 / 9.9, 512 13.3 / 11.8, 2048 32.5 / 24.8; two in three rows ended 64 16.6 / 12.2, 128 18.5 / 13.8, 256 23.3 / 18.7,
+// 512 38.7 / 26.4, 2048 126 / 77 (two more launches are 5 us on the host).
 __global__ void __launch_bounds__(256) page_owners_kernel(const __grid_constant__ PageParams p) {
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     const int me = blockIdx.x * 256 + threadIdx.x;
