@@ -59,6 +59,10 @@ def marshal_up_to_date() -> bool:
     return _newer(marshal(), [MARSHAL_SOURCE])
 
 
+def up_to_date() -> bool:
+    return library_up_to_date() and marshal_up_to_date()
+
+
 def _marshal_commands():
     """Compiling the Python module, and linking it beside ``libkda.so``."""
     import torch
