@@ -595,7 +595,7 @@ size_t kda_latent_chunk_workspace_bytes(int T, int num_keys, int H, int N);
  * such numbers where queries see few of them (2048 in bf16, 256 in fp16), and
  * are rounded where they see more.  In fp16 a key or value past 65504 is
  * infinite (the second number of such a key is 0): where its channel meets a
- * query's of the other sign the row has weight 0, and with its own sign the
+ * query's of the other sign the row has weight 0; with its own sign, or 0, the
  * query's results are NaN.  The rest as for kda_latent_fwd.
  */
 kda_status kda_latent_chunk(const void* q, const void* cache, int num_pages, int page_size,
