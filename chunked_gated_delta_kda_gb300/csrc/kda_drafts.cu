@@ -494,7 +494,7 @@ extern "C" kda_status kda_verify_drafts(const int64_t* draft_tokens, const void*
                                         int64_t* tokens, int32_t* num_accepted, int N, int S, int V, unsigned flags,
                                         void* workspace, cudaStream_t stream) {
     using namespace kda;
-    if (N < 1 || S < 0 || V < 1 || N > (1 << 24) || V > (1 << 30) || S == INT32_MAX) return KDA_ERR_INVALID_ARG;
+    if (N < 1 || S < 0 || V < 1 || N > (1 << 24) || V > (1 << 30) || S > (1 << 30)) return KDA_ERR_INVALID_ARG;   // (steps of 512 in 32 bits)
     if ((flags & ~(KDA_FLAG_FP16 | KDA_FLAG_FP32)) != 0u || flags == (KDA_FLAG_FP16 | KDA_FLAG_FP32)) return KDA_ERR_INVALID_ARG;
     if ((S > 0 && !draft_tokens) || !target_probs || !target_strides || !uniform || !tokens || !num_accepted ||
         (draft_probs && !draft_strides))

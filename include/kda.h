@@ -731,6 +731,7 @@ kda_status kda_page_compact(const int32_t* block_table, int table_width, const i
  *   flags       KDA_FLAG_FP32 or KDA_FLAG_FP16 (else bf16), of both
  *               probabilities
  *   workspace   NULL, or the 256-byte status header
+ * N is 2^24 at most, S and V 2^30.
  * The comparisons are exact; the sums and the border are good to 2^-31 of the
  * total for any V (u tells 2^-24 apart).  Probabilities need not sum to one;
  * what is not above zero, NaN included, has no weight.  A token >= V ends the

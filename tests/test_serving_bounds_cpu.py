@@ -148,6 +148,16 @@ def test_sizes_that_an_index_could_step_out_of_are_refused():
         assert fork(F=big) == 1
 
 
+@cpu_only
+def test_more_drafts_than_an_index_could_step_over_are_refused():
+    keep, p = host_block()
+    pair = (ctypes.c_longlong * 2)(64, 16)
+    call = caller(binding.load_library().kda_verify_drafts, dict(
+        tokens=p, draft=p, ds=pair, target=p, ts=pair, uniform=p, out=p, accepted=p, N=2, S=3, V=16, flags=512, ws=None, stream=None))
+    for S in (2 ** 30 + 1, 2 ** 31 - 2):
+        assert call(S=S) == 1
+
+
 def test_the_library_is_built_without_torchs_headers(tmp_path, monkeypatch):
     """A module that does not compile says so, and the library it would have called is there all the same."""
     tiny = tmp_path / "tiny.cu"
